@@ -18,6 +18,12 @@
  *                            GPU-resident window of recently critical pages)
  *   kv_dense_decode_attn  -> the same over every page (Dual-Blade, "Background
  *                            and key observations": decode reads all prior KV)
+ *   kv_chunk_attn         -> attention of a chunk of new tokens per sequence (a
+ *                            prefill step, proposed tokens to check) over the
+ *                            cache that holds them
+ *   kv_q8_append, kv_q8_chunk_attn, kv_q8_read -> the cache held in 8 bits:
+ *                            quantised as it is written, attended in place,
+ *                            read back into the shape's own type
  * K/V pages live in device memory (HBM) or in pinned host memory that the GPU
  * reads in place, with no staging copy (DirectKV -- No Buffer, No Bottleneck:
  * Efficient Zero-Copy KV Cache Offloading for Long-Context LLMs, core method 1
@@ -410,6 +416,109 @@ int kv_sparse_decode_attn_window(const kv_shape *shape, const void *q, const voi
                                  const float *scores, float scale, float *out,
                                  const kv_window *win, void *workspace, size_t workspace_bytes,
                                  void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Chunks of new tokens.  A call takes a ragged batch: sequence b brings
+ * n_b = q_start[b + 1] - q_start[b] >= 0 new tokens, rows q_start[b] ..
+ * q_start[b + 1] - 1 of the call's [total_q] arrays.  n_b may differ from
+ * sequence to sequence and be 0; one token each is a decode step.
+ *   q_start   [B + 1] int32, device memory, 0 <= q_start[b] <= q_start[b + 1]
+ *             <= total_q
+ *   total_q   rows of the [total_q] arrays (>= 1); rows no sequence owns are
+ *             neither used nor written
+ *   max_q_len upper bound of every n_b (>= 1): the launch is sized by it
+ *   window    attention only: 0, or the number of tokens a row sees, itself
+ *             included (a sliding window)
+ * A sequence whose q_start entries are out of order or out of range, whose
+ * n_b exceeds max_q_len, or whose length is out of range is skipped whole and
+ * recorded as KV_ERR_BOUNDS. */
+typedef struct {
+  const int32_t *q_start;
+  int32_t total_q;
+  int32_t max_q_len;
+  int32_t window;
+  int32_t reserved; /* 0 */
+} kv_chunk;
+
+/* Chunk attention.  context_lens[b] counts the cached tokens WITH the chunk's
+ * own, whose K and V are in the cache already (0 <= context_lens[b] <= maxP *
+ * ps): row i of the chunk is token t = context_lens[b] - n_b + i and
+ *   out[q_start[b] + i][h] = sum_j softmax_j(scale * q . k_j) v_j
+ * over the tokens max(0, t - window + 1) <= j <= t (window 0: 0 <= j <= t).
+ * A row that sees no token (t < 0: fewer tokens cached than the chunk has)
+ * is 0.
+ *   q   [total_q][Hq][d] dtype        out [total_q][Hq][d] dtype
+ * out has the type of q (what the next projection takes), rounded once;
+ * scores, the softmax and the sums are fp32, and the softmax weights enter
+ * the value product in dtype.  What unseen tokens and unused slots of a page
+ * hold, infinities and NaN among it, does not reach a row.  A page whose
+ * block-table entry is out of range is skipped and recorded as
+ * KV_ERR_BOUNDS.  With K/V in pinned host memory and 16-bit data the pages
+ * the call needs cross the link once, into the workspace.  Results do not
+ * depend on what ran before and repeat bit for bit on the same device.
+ * kv_chunk_workspace_bytes: the workspace for this shape and chunk on the
+ * current device (0 for an invalid one); q_start itself is not read.  Calls
+ * that may run at the same time need workspaces of their own. */
+size_t kv_chunk_workspace_bytes(const kv_shape *shape, const kv_chunk *chunk);
+int kv_chunk_attn(const kv_shape *shape, const kv_chunk *chunk, const void *q,
+                  const void *k_cache, const void *v_cache, const int32_t *block_table,
+                  const int32_t *context_lens, float scale, void *out, void *workspace,
+                  size_t workspace_bytes, void *stream);
+
+/* The cache in 8 bits (half the bytes that offloading moves and attention
+ * reads).  Every key and value vector x of a token and kv head is held as d
+ * e4m3 codes c and one power of two:
+ *   e = the smallest integer with max |x| <= 448 * 2^e, kept in [-15, 7] for
+ *       KV_F16 and in [-110, 7] for KV_BF16 and KV_F32
+ *   c = e4m3(x * 2^-e), ties to even, beyond +-448 (|x| > 57344) limited to it
+ * and stands for c * 2^e, which is exact in every dtype.  A power of two
+ * makes the scaling itself exact, so the codes do not depend on how it is
+ * computed.  The scale is kept as the byte e + 127.  A vector with an infinity
+ * or a NaN is kept as NaN (scale byte 255, codes 0x7f).
+ *   k_codes, v_codes  [N][Hkv][ps][d] bytes  (where kv_loc says)
+ *   k_scale, v_scale  [N][Hkv][ps]    bytes  (where kv_loc says)
+ * All 16-byte aligned.  A cache is read with the dtype it was written with. */
+typedef struct {
+  uint8_t *k_codes;
+  uint8_t *v_codes;
+  uint8_t *k_scale;
+  uint8_t *v_scale;
+} kv_q8_cache;
+
+/* Quantising append: token i of sequence b's chunk is stored at position
+ * context_lens[b] + i, context_lens being the lengths BEFORE the append (as
+ * kv_append_token; context_lens[b] + n_b <= maxP * ps).
+ *   k_new, v_new [total_q][Hkv][d] dtype, device memory.
+ * context_lens_out (may be NULL, may equal context_lens): receives
+ * context_lens[b] + n_b.  A token whose block-table entry is out of range is
+ * dropped; its sequence keeps its length, and KV_ERR_BOUNDS is recorded (the
+ * same for a sequence that is skipped whole).  The pages written must not be
+ * shared with another row. */
+int kv_q8_append(const kv_shape *shape, const kv_chunk *chunk, const void *k_new,
+                 const void *v_new, const kv_q8_cache *cache, const int32_t *block_table,
+                 const int32_t *context_lens, int32_t *context_lens_out, void *stream);
+
+/* Reading back: every token p of sequence b's pages, as c * 2^e rounded to
+ * dtype, from page block_table[b][p / ps] of the 8-bit cache into page
+ * out_table[b][p / ps] of a cache of the shape's dtype:
+ *   k_out, v_out [out_pages][Hkv][ps][d] dtype, device memory.
+ * The result is a cache every other call takes (with num_phys_pages =
+ * out_pages and KV_LOC_HBM).  A negative out_table entry skips its page, so
+ * that some pages only can be brought back; out_table may be block_table
+ * itself.  Slots past the last token keep what they held.  0 <=
+ * context_lens[b] <= maxP * ps; an entry of either table out of range skips
+ * the page and records KV_ERR_BOUNDS. */
+int kv_q8_read(const kv_shape *shape, const kv_q8_cache *cache, const int32_t *block_table,
+               const int32_t *context_lens, const int32_t *out_table, int64_t out_pages,
+               void *k_out, void *v_out, void *stream);
+
+/* Chunk attention over the 8-bit cache: kv_chunk_attn on the values it stands
+ * for (a NaN vector makes the rows that see it NaN). */
+size_t kv_q8_chunk_workspace_bytes(const kv_shape *shape, const kv_chunk *chunk);
+int kv_q8_chunk_attn(const kv_shape *shape, const kv_chunk *chunk, const void *q,
+                     const kv_q8_cache *cache, const int32_t *block_table,
+                     const int32_t *context_lens, float scale, void *out, void *workspace,
+                     size_t workspace_bytes, void *stream);
 
 /* Synchronises `stream`, then returns and clears the device status word of
  * the current device: KV_OK, KV_ERR_DEVICE_TIMEOUT or KV_ERR_BOUNDS (the

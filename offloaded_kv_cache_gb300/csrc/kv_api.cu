@@ -9,6 +9,7 @@
 #include <cstdint>
 #include <mutex>
 
+#include "kv_host.h"
 #include "kv_internal.cuh"
 #include "kv_launch.h"
 
@@ -27,6 +28,14 @@ std::atomic<int> g_sm_count[kMaxDevices];
 std::atomic<int> g_debug_skip_page{-1};
 std::atomic<int> g_split_mode{-1};
 std::atomic<unsigned long long> g_wait_limit_ns{2000000000ull};
+
+}  // namespace
+
+// declared in kv_host.h: the chunk operators' entry points use these too
+namespace kvs {
+
+int debug_skip_page() { return g_debug_skip_page.load(std::memory_order_relaxed); }
+unsigned long long wait_limit_ns() { return g_wait_limit_ns.load(std::memory_order_relaxed); }
 
 int current_device() {
   int dev = -1;
@@ -60,9 +69,6 @@ int sm_count(int dev) {
   return n;
 }
 
-bool al16(const void *p) { return p && ((uintptr_t)p & 15u) == 0; }
-bool al4(const void *p) { return p && ((uintptr_t)p & 3u) == 0; }
-int elem_bytes(int dtype) { return dtype == KV_F32 ? 4 : 2; }
 
 int check_shape(const kv_shape *s) {
   if (!s) return KV_ERR_INVALID_ARG;
@@ -104,6 +110,10 @@ int resolve_kv(const kv_shape *s, const void *p, const void **dev_ptr) {
   return KV_OK;
 }
 
+}  // namespace kvs
+
+namespace {
+
 // ---------------------------------------------------------------------------
 // attention launch plan: head chunking, split count, pipeline depth, workspace
 // ---------------------------------------------------------------------------
@@ -121,8 +131,6 @@ struct Plan {
   size_t off_spa_o = 0, off_spa_ml = 0, off_gmeta = 0;
   size_t total = 0;
 };
-
-size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // CTA shapes the planner chooses between (consumer warps, stages):
 //  * wide: small CTAs, many resident per SM, for many short (b, head) units
@@ -363,7 +371,9 @@ Plan cached_plan(const kv_shape *s, int k, bool win = false) {
   return pl;
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+}  // namespace
+
+PFN_cuTensorMapEncodeTiled_v12000 kvs::encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -378,6 +388,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   });
   return fn;
 }
+
+namespace {
 
 // 3-D view [slab][rows = N * Hkv * ps][128 bytes]: a 128-element row is
 // `elem` slabs of 128 bytes (strides: a row, 128 bytes), so one box of every

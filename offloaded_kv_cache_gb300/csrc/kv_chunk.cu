@@ -1,0 +1,299 @@
+// kv_chunk.cu -- chunk attention on the CUDA cores in fp32, and the combine
+// of partial results.  kv_chunk.cuh has the formula and how the work is cut.
+#include <algorithm>
+#include <type_traits>
+
+#include "kv_chunk.cuh"
+#include "kv_launch.h"
+#include "kv_q8.cuh"
+
+namespace kvs {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTile = 64;             // tokens per KV tile
+constexpr int kQStr = kHeadDim + 4;   // padded rows: 16-byte reads of 16 rows meet distinct banks
+constexpr int kPStr = kTile + 4;
+
+// Rows of a unit = 16 * MR.  256 threads as 16 x 16: thread (ty, tx) holds
+// rows ty * MR .. + MR - 1; of the scores the columns tx + 16 j, of the output
+// the channels 4 tx .. + 3 and 64 + 4 tx .. + 3.  Per tile: scores = Q K^T
+// (a 4 x MR register block per thread), one streaming-softmax step (row
+// maximum and sum over the 16 tx lanes), output += P V.  The weights P take
+// K's place in shared memory once the scores are done, so that two CTAs fit an
+// SM.  FP32 multiply-adds bound it for many rows, the K/V stream for few.
+template <int MR> struct Shape {
+  static constexpr int kRows = 16 * MR;
+  static constexpr int kKBytes = kTile * kQStr * 4;
+  static constexpr int kSmem = kRows * kQStr * 4 + kKBytes + kTile * kHeadDim * 4;
+  static_assert(kRows * kPStr * 4 <= kKBytes, "P takes K's place");
+};
+
+// 8 channels of one cached vector in fp32
+template <class T, bool Q8>
+__device__ __forceinline__ void cached8(const void *base, const uint8_t *scale, long long vec,
+                                        int c, float (&x)[8]) {
+  if constexpr (Q8) {
+    const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(base) +
+                                                     vec * kHeadDim + c);
+    float lo[4], hi[4];
+    q8_unpack4(w.x, lo);
+    q8_unpack4(w.y, hi);
+    const float s = q8_scale(scale[vec]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = lo[i] * s;
+      x[4 + i] = hi[i] * s;
+    }
+  } else {
+    load8(static_cast<const T *>(base) + vec * kHeadDim + c, x);
+  }
+}
+
+template <class T, int MR, bool Q8>
+__global__ void __launch_bounds__(kThreads) chunk_core_kernel(const ChunkArgs a) {
+  using Sh = Shape<MR>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ ChunkShare share;
+  __shared__ long long red[33];
+  __shared__ int tok_ok[kTile];
+  float *Qs = reinterpret_cast<float *>(smem);
+  float *Ks = Qs + Sh::kRows * kQStr;
+  float *Vs = Ks + kTile * kQStr;
+  float *Ps = Ks;
+  pdl_wait();
+  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  if (tid == 0) a.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
+  share_init(a, Sh::kRows, kTile, &share, red);
+  for (;;) {
+    __syncthreads();
+    if (tid == 0) share_next(a, Sh::kRows, kTile, &share);
+    __syncthreads();
+    if (share.nseg == 0) break;
+    for (int sg = 0; sg < share.nseg; ++sg) {
+      const ChunkSeg g = share.seg[sg];
+      __syncthreads();  // the previous segment's Q is read
+      for (int i = tid; i < Sh::kRows * 16; i += kThreads) {
+        const int r = i >> 4, c = (i & 15) * 8;
+        float x[8] = {};
+        if (r < g.nrows) {
+          const int pr = g.r0 + r, row = g.q0 + pr / a.G, head = g.kvh * a.G + pr % a.G;
+          load8(static_cast<const T *>(a.q) + ((long long)row * a.Hq + head) * kHeadDim + c, x);
+        }
+        store8(Qs + r * kQStr + c, x);
+      }
+      int t[MR];
+      float m[MR], l[MR], o[MR][8];
+#pragma unroll
+      for (int r = 0; r < MR; ++r) {
+        t[r] = g.len - g.n + (g.r0 + min(ty * MR + r, g.nrows - 1)) / a.G;
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) o[r][c] = 0.f;
+      }
+      const int t_first = g.len - g.n + g.r0 / a.G;
+      for (int tile = g.tile_lo; tile < g.tile_hi; ++tile) {
+        const int tok0 = tile * kTile;
+        // K and V of the tile; tokens past the end or of a bad page are zero
+        for (int i = tid; i < kTile * 16; i += kThreads) {
+          const int tok = i >> 4, c = (i & 15) * 8, pos = tok0 + tok;
+          float kx[8] = {}, vx[8] = {};
+          bool ok = pos < g.len;
+          if (ok) {
+            const int ph = a.bt[(long long)g.b * a.maxP + pos / a.ps];
+            ok = ph >= 0 && ph < a.nphys;
+            if (!ok && c == 0) flag_error(a.status, KV_ERR_BOUNDS);
+            if (ok) {
+              const long long vec = ((long long)ph * a.Hkv + g.kvh) * a.ps + pos % a.ps;
+              cached8<T, Q8>(a.k, a.k_scale, vec, c, kx);
+              cached8<T, Q8>(a.v, a.v_scale, vec, c, vx);
+            }
+          }
+          if (c == 0) tok_ok[tok] = ok;
+          store8(Ks + tok * kQStr + c, kx);
+          store8(Vs + tok * kHeadDim + c, vx);
+        }
+        __syncthreads();
+        float s[MR][4] = {};
+#pragma unroll 4
+        for (int d = 0; d < kHeadDim; d += 4) {
+          float4 qv[MR], kv[4];
+#pragma unroll
+          for (int r = 0; r < MR; ++r)
+            qv[r] = *reinterpret_cast<const float4 *>(Qs + (ty * MR + r) * kQStr + d);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            kv[j] = *reinterpret_cast<const float4 *>(Ks + (tx + 16 * j) * kQStr + d);
+#pragma unroll
+          for (int r = 0; r < MR; ++r)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              s[r][j] += qv[r].x * kv[j].x + qv[r].y * kv[j].y + qv[r].z * kv[j].z +
+                         qv[r].w * kv[j].w;
+        }
+        bool ok[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) ok[j] = tok_ok[tx + 16 * j];
+        __syncthreads();  // every thread is done with K: P takes its place
+#pragma unroll
+        for (int r = 0; r < MR; ++r) {
+          const int hi = vis_hi(t[r], tok0), lo = vis_lo(t[r], tok0, a.window);
+          float mx = m[r];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int c = tx + 16 * j;
+            s[r][j] = ok[j] && c <= hi && c >= lo ? s[r][j] * a.scale_log2 : -INFINITY;
+            mx = fmaxf(mx, s[r][j]);
+          }
+#pragma unroll
+          for (int off = 8; off > 0; off >>= 1)
+            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off, 16));
+          const float base = mx == -INFINITY ? 0.f : mx;
+          const float alpha = ex2(m[r] - base);
+          m[r] = mx;
+          float sum = 0.f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float p = ex2(s[r][j] - base);
+            sum += p;
+            Ps[(ty * MR + r) * kPStr + tx + 16 * j] = p;
+          }
+          l[r] = l[r] * alpha + sum;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) o[r][c] *= alpha;
+        }
+        __syncthreads();
+        // where some row does not see some token, a weight of 0 must not meet
+        // an infinity or NaN of V
+        const bool edge = tok0 + kTile - 1 > t_first || a.window > 0;
+#pragma unroll 4
+        for (int j = 0; j < kTile; ++j) {
+          const float4 v0 = *reinterpret_cast<const float4 *>(Vs + j * kHeadDim + tx * 4);
+          const float4 v1 = *reinterpret_cast<const float4 *>(Vs + j * kHeadDim + 64 + tx * 4);
+          const float vv[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+          for (int r = 0; r < MR; ++r) {
+            const float p = Ps[(ty * MR + r) * kPStr + j];
+            if (edge && p == 0.f) continue;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) o[r][c] += p * vv[c];
+          }
+        }
+        __syncthreads();
+      }
+      const bool whole = g.first && g.last;
+      const int slot = part_slot(g);
+#pragma unroll
+      for (int r = 0; r < MR; ++r) {
+        float sum = l[r];
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off, 16);
+        const int rr = ty * MR + r;
+        if (rr >= g.nrows) continue;
+        if (whole) {
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          const int pr = g.r0 + rr, row = g.q0 + pr / a.G, head = g.kvh * a.G + pr % a.G;
+          T *dst = static_cast<T *>(a.out) + ((long long)row * a.Hq + head) * kHeadDim + tx * 4;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float y[4] = {o[r][4 * h] * inv, o[r][4 * h + 1] * inv, o[r][4 * h + 2] * inv,
+                                o[r][4 * h + 3] * inv};
+            if constexpr (std::is_same_v<T, float>)
+              *reinterpret_cast<float4 *>(dst + 64 * h) = make_float4(y[0], y[1], y[2], y[3]);
+            else
+              *reinterpret_cast<uint2 *>(dst + 64 * h) =
+                  make_uint2(pack2(y[0], y[1], T{}), pack2(y[2], y[3], T{}));
+          }
+        } else {
+          const long long pr = (long long)slot * a.slot_rows + rr;
+          float *dst = a.part_o + pr * kHeadDim + tx * 4;
+          *reinterpret_cast<float4 *>(dst) = make_float4(o[r][0], o[r][1], o[r][2], o[r][3]);
+          *reinterpret_cast<float4 *>(dst + 64) = make_float4(o[r][4], o[r][5], o[r][6], o[r][7]);
+          if (tx == 0) {
+            a.part_ml[2 * pr] = m[r];
+            a.part_ml[2 * pr + 1] = sum;
+          }
+        }
+      }
+    }
+  }
+  pdl_trigger();
+}
+
+// Joins the parts of every unit that several CTAs share: CTA i of the
+// attention left part 2 i + 1, the CTAs i + 1 .. j parts 2 (i + 1) .. 2 j.  A
+// warp takes a row, a lane four channels.
+template <class T>
+__global__ void __launch_bounds__(256) chunk_combine_kernel(const ChunkArgs a) {
+  pdl_wait();
+  const int4 u = a.meta[2 * blockIdx.x];
+  if (u.x < 0) return;
+  const int4 w = a.meta[2 * blockIdx.x + 1];
+  const int first = blockIdx.x, last = w.y, lane = threadIdx.x & 31;
+  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < u.w; r += gridDim.y * 8) {
+    float M = -INFINITY;
+    for (int j = first + lane; j <= last; j += 32) {
+      const int slot = j == first ? 2 * j + 1 : 2 * j;
+      M = fmaxf(M, a.part_ml[2 * ((long long)slot * a.slot_rows + r)]);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, off));
+    const float base = M == -INFINITY ? 0.f : M;
+    float L = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int j = first; j <= last; ++j) {
+      const long long row = (long long)(j == first ? 2 * j + 1 : 2 * j) * a.slot_rows + r;
+      const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + 2 * row);
+      const float4 x = *reinterpret_cast<const float4 *>(a.part_o + row * kHeadDim + lane * 4);
+      const float f = ex2(ml.x - base);
+      L += ml.y * f;
+      o.x += x.x * f;
+      o.y += x.y * f;
+      o.z += x.z * f;
+      o.w += x.w * f;
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const int pr = u.z + r, row = w.x + pr / a.G, head = u.y * a.G + pr % a.G;
+    T *dst = static_cast<T *>(a.out) + ((long long)row * a.Hq + head) * kHeadDim + lane * 4;
+    if constexpr (std::is_same_v<T, float>)
+      *reinterpret_cast<float4 *>(dst) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    else
+      *reinterpret_cast<uint2 *>(dst) =
+          make_uint2(pack2(o.x * inv, o.y * inv, T{}), pack2(o.z * inv, o.w * inv, T{}));
+  }
+}
+
+template <class T, int MR, bool Q8>
+cudaError_t core_go(const ChunkArgs &a, int ctas, cudaStream_t st) {
+  const cudaError_t e = cudaFuncSetAttribute(
+      chunk_core_kernel<T, MR, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<MR>::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(chunk_core_kernel<T, MR, Q8>, dim3(ctas), dim3(kThreads), Shape<MR>::kSmem, st,
+                    a);
+}
+template <class T>
+cudaError_t core_type(const ChunkArgs &a, bool q8, int rows, int ctas, cudaStream_t st) {
+  if (rows == 16)
+    return q8 ? core_go<T, 1, true>(a, ctas, st) : core_go<T, 1, false>(a, ctas, st);
+  return q8 ? core_go<T, 4, true>(a, ctas, st) : core_go<T, 4, false>(a, ctas, st);
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_core(int dtype, const ChunkArgs &a, bool q8, int rows, int ctas,
+                              cudaStream_t st) {
+  return dtype == KV_F32   ? core_type<float>(a, q8, rows, ctas, st)
+         : dtype == KV_F16 ? core_type<__half>(a, q8, rows, ctas, st)
+                           : core_type<__nv_bfloat16>(a, q8, rows, ctas, st);
+}
+
+cudaError_t launch_chunk_combine(int dtype, const ChunkArgs &a, int ctas, cudaStream_t st) {
+  const dim3 grid(ctas, std::min(32, (a.slot_rows + 7) / 8)), block(256);
+  return dtype == KV_F32   ? launch_pdl(chunk_combine_kernel<float>, grid, block, 0, st, a)
+         : dtype == KV_F16 ? launch_pdl(chunk_combine_kernel<__half>, grid, block, 0, st, a)
+                           : launch_pdl(chunk_combine_kernel<__nv_bfloat16>, grid, block, 0, st, a);
+}
+
+}  // namespace kvs

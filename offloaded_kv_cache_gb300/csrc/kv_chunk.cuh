@@ -1,0 +1,248 @@
+// kv_chunk.cuh -- attention of a chunk of new tokens over a paged cache: what
+// its kernels share, above all how the work is cut.
+//
+// What it computes, for row i of sequence b's n_b new tokens (token t = len_b
+// - n_b + i) and query head h:
+//   out = sum_j softmax_j(scale * q . k_j) v_j,   max(0, t - window + 1) <= j <= t
+//
+// Work.  The G query heads of a kv head read the same K and V, so their rows
+// are packed: packed row r = i * G + g is token i, head kvh * G + g.  A unit
+// is `rows` consecutive packed rows of one (sequence, kv head); it meets the
+// KV tiles [tile_lo, tile_hi) its rows can see, one at least.  All units' tiles laid end to end
+// (sequence, kv head, row block; lengths differ, so the total is known on the
+// device only) are cut into equal shares, one per CTA, one CTA per SM.  A
+// share is a list of segments: the end of one unit, whole units, the start of
+// another.  A unit within one share is written to out; the others leave
+// partial results (at most two per CTA, so the workspace does not grow with
+// the batch) that the combine kernel joins.  Ragged batches, one long
+// sequence and many short ones are balanced by the same rule to one tile.
+#pragma once
+
+#include "kv_internal.cuh"
+
+namespace kvs {
+
+struct ChunkArgs {
+  const void *q;
+  const void *k, *v;                // K and V (8-bit: the codes)
+  const uint8_t *k_scale, *v_scale; // 8-bit only
+  const int32_t *q_start, *bt, *ctx;
+  void *out;
+  float *part_o;    // [2 * ctas][slot_rows][d]
+  float *part_ml;   // [2 * ctas][slot_rows][2]: log2-domain maximum, sum
+  int4 *meta;       // [ctas][2]: the unit whose first tile lies in the CTA's share and whose last does not
+  int *status;
+  long long nphys;
+  int B, Hq, Hkv, G, ps, maxP, total_q, max_q_len, window;
+  int slot_rows;
+  float scale_log2;  // scale * log2(e)
+  unsigned long long wait_limit_ns;
+  int debug_skip_tile;  // >= 0: the producer never fills that tile of a share (timeout test)
+};
+
+// One sequence of the call; n = 0 when it has no rows or is skipped.
+struct ChunkSeq {
+  int q0, n, len;
+};
+__device__ __forceinline__ ChunkSeq chunk_seq(const ChunkArgs &a, int b, bool flag) {
+  const int q0 = a.q_start[b], q1 = a.q_start[b + 1], len = a.ctx[b];
+  const bool ok = q0 >= 0 && q1 >= q0 && q1 <= a.total_q && q1 - q0 <= a.max_q_len && len >= 0 &&
+                  (long long)len <= (long long)a.maxP * a.ps;
+  if (!ok && flag) flag_error(a.status, KV_ERR_BOUNDS);
+  return ChunkSeq{q0, ok ? q1 - q0 : 0, len};
+}
+
+// KV tiles [lo, hi) of the unit of packed rows [r0, r0 + nrows): what its
+// rows can see, and one tile where they see nothing (it writes the zeros).
+struct TileRange {
+  int lo, hi;
+};
+__device__ __forceinline__ TileRange unit_tiles(const ChunkArgs &a, const ChunkSeq &s, int r0,
+                                                int nrows, int tile) {
+  const int t_first = s.len - s.n + r0 / a.G;
+  const int t_last = s.len - s.n + (r0 + nrows - 1) / a.G;
+  if (t_last < 0) return TileRange{0, 1};
+  const int lo = a.window > 0 ? max(0, t_first - a.window + 1) : 0;
+  return TileRange{lo / tile, t_last / tile + 1};
+}
+
+// One segment of a CTA's share.
+struct ChunkSeg {
+  int b, kvh, r0, nrows;  // unit: packed rows [r0, r0 + nrows) of (b, kvh)
+  int q0, n, len;         // its sequence
+  int tile_lo, tile_hi;   // the KV tiles of this segment
+  int first, last;        // it holds the unit's first / last tile
+  int pad;
+};
+
+constexpr int kMaxSegs = 32;  // segments listed at a time
+
+struct ChunkShare {
+  long long work, lo, hi;  // all tiles; this CTA's share
+  int b, kvh, r0, off;     // walk: the next unit, and its tiles already passed
+  long long left;          // tiles of the share not listed yet
+  int nseg;
+  int ctas;                // CTAs with a share: no more than there are tiles
+  ChunkSeg seg[kMaxSegs];
+};
+
+__device__ __forceinline__ int packed_rows(const ChunkArgs &a, const ChunkSeq &s) {
+  return s.n * a.G;  // checked on the host against int32 (max_q_len * G)
+}
+// tiles of all row blocks of one kv head of sequence s
+__device__ __forceinline__ long long head_tiles(const ChunkArgs &a, const ChunkSeq &s, int rows,
+                                                int tile) {
+  const int R = packed_rows(a, s);
+  long long w = 0;
+  for (int r0 = 0; r0 < R; r0 += rows) {
+    const TileRange t = unit_tiles(a, s, r0, min(rows, R - r0), tile);
+    w += t.hi - t.lo;
+  }
+  return w;
+}
+
+__device__ __forceinline__ long long warp_sum(long long x) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, off);
+  return x;
+}
+
+// Every thread of the CTA: the total work, this CTA's share and where it
+// starts.  red: 33 long longs of shared scratch.
+__device__ __forceinline__ void share_init(const ChunkArgs &a, int rows, int tile, ChunkShare *sh,
+                                           long long *red) {
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, nw = blockDim.x >> 5;
+  long long mine = 0;
+  for (int b = t; b < a.B; b += blockDim.x)
+    mine += head_tiles(a, chunk_seq(a, b, blockIdx.x == 0), rows, tile);
+  mine = warp_sum(mine);
+  if (lane == 0) red[warp] = mine;
+  __syncthreads();
+  if (t == 0) {
+    long long w = 0;
+    for (int i = 0; i < nw; ++i) w += red[i];
+    w *= a.Hkv;
+    const long long n = min((long long)gridDim.x, w), i = min((long long)blockIdx.x, n);
+    sh->work = w;
+    sh->ctas = (int)n;
+    sh->lo = n > 0 ? w * i / n : 0;
+    sh->hi = i < n ? w * (i + 1) / n : sh->lo;
+    sh->left = sh->hi - sh->lo;
+    sh->b = -1;
+    sh->nseg = 0;
+  }
+  __syncthreads();
+  if (sh->left == 0) return;
+  // the sequence holding tile lo: one warp walks the sequences 32 at a time
+  if (warp == 0) {
+    long long base = 0;
+    const long long want = sh->lo;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      const int b = b0 + lane;
+      ChunkSeq s{0, 0, 0};
+      if (b < a.B) s = chunk_seq(a, b, false);
+      const long long hw = head_tiles(a, s, rows, tile), w = hw * a.Hkv;
+      long long inc = w;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const long long x = __shfl_up_sync(0xFFFFFFFFu, inc, off);
+        if (lane >= off) inc += x;
+      }
+      const long long first = base + inc - w;
+      const bool here = want >= first && want < first + w;
+      if (here) {
+        long long rem = want - first;
+        sh->b = b;
+        sh->kvh = (int)(rem / hw);
+        rem %= hw;
+        int r0 = 0;
+        const int R = packed_rows(a, s);
+        for (;; r0 += rows) {
+          const TileRange t2 = unit_tiles(a, s, r0, min(rows, R - r0), tile);
+          if (rem < t2.hi - t2.lo || r0 + rows >= R) break;
+          rem -= t2.hi - t2.lo;
+        }
+        sh->r0 = r0;
+        sh->off = (int)rem;
+      }
+      if (__any_sync(0xFFFFFFFFu, here)) break;
+      base += __shfl_sync(0xFFFFFFFFu, inc, 31);
+    }
+  }
+  __syncthreads();
+}
+
+// One thread: the next segments of the share (nseg = 0 when it is used up).
+// The CTA that holds a unit's first tile but not its last records where the
+// combine finds the rest: slot 2 i + 1 of CTA i (a share's last segment) for
+// the first part, slot 2 j (a share's first segment) for each further part.
+__device__ __forceinline__ void share_next(const ChunkArgs &a, int rows, int tile,
+                                           ChunkShare *sh) {
+  int n = 0;
+  if (sh->left > 0) {
+    int b = sh->b, kvh = sh->kvh, r0 = sh->r0, off = sh->off;
+    long long left = sh->left;
+    ChunkSeq s = chunk_seq(a, b, false);
+    int R = packed_rows(a, s);
+    while (n < kMaxSegs && left > 0) {
+      const int nrows = min(rows, R - r0);
+      const TileRange t = unit_tiles(a, s, r0, nrows, tile);
+      const int have = t.hi - t.lo - off;
+      const int take = (int)min((long long)have, left);
+      ChunkSeg &g = sh->seg[n++];
+      g.b = b;
+      g.kvh = kvh;
+      g.r0 = r0;
+      g.nrows = nrows;
+      g.q0 = s.q0;
+      g.n = s.n;
+      g.len = s.len;
+      g.tile_lo = t.lo + off;
+      g.tile_hi = t.lo + off + take;
+      g.first = off == 0;
+      g.last = take == have;
+      if (g.first && !g.last) {
+        // the CTA whose share holds the unit's last tile
+        const long long end = sh->hi - left + (t.hi - t.lo) - 1;
+        const int j = (int)(((end + 1) * sh->ctas - 1) / sh->work);
+        a.meta[2 * blockIdx.x] = make_int4(b, kvh, r0, nrows);
+        a.meta[2 * blockIdx.x + 1] = make_int4(s.q0, j, 0, 0);
+      }
+      left -= take;
+      off = 0;
+      r0 += rows;
+      if (r0 >= R) {
+        r0 = 0;
+        if (++kvh == a.Hkv) {
+          kvh = 0;
+          s.n = 0;
+          while (left > 0 && ++b < a.B) {
+            s = chunk_seq(a, b, false);
+            if (s.n > 0) break;
+          }
+          R = packed_rows(a, s);
+          if (R == 0) break;
+        }
+      }
+    }
+    sh->b = b;
+    sh->kvh = kvh;
+    sh->r0 = r0;
+    sh->off = 0;
+    sh->left = n > 0 && R == 0 ? 0 : left;
+  }
+  sh->nseg = n;
+}
+
+// partial-result slot of a segment that is not a whole unit
+__device__ __forceinline__ int part_slot(const ChunkSeg &g) {
+  return 2 * (int)blockIdx.x + (g.first ? 1 : 0);
+}
+
+// visible columns [lo, hi] of a tile starting at token tile0, for token t
+__device__ __forceinline__ int vis_hi(int t, int tile0) { return t - tile0; }
+__device__ __forceinline__ int vis_lo(int t, int tile0, int window) {
+  return window > 0 ? t - window + 1 - tile0 : 0;
+}
+
+}  // namespace kvs

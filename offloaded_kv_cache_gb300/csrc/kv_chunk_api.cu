@@ -1,0 +1,223 @@
+// kv_chunk_api.cu -- the extern "C" boundary of the chunk operators: argument
+// checks, launch plans and launches.  Contracts are in include/kvsparse.h.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstring>
+
+#include "kv_chunk.cuh"
+#include "kv_host.h"
+#include "kv_launch.h"
+
+namespace {
+
+using namespace kvs;
+
+int check_chunk(const kv_shape *s, const kv_chunk *c) {
+  if (!c || !al4(c->q_start) || c->total_q < 1 || c->max_q_len < 1 || c->window < 0 ||
+      c->reserved != 0)
+    return KV_ERR_INVALID_ARG;
+  // packed rows (token, head of the group) and output rows fit in int32
+  if ((long long)c->total_q * s->num_q_heads > INT_MAX) return KV_ERR_UNSUPPORTED;
+  return KV_OK;
+}
+
+// The four arrays of an 8-bit cache, as the device sees them.
+int resolve_q8(const kv_shape *s, const kv_q8_cache *c, kv_q8_cache *dev) {
+  if (!c) return KV_ERR_INVALID_ARG;
+  const uint8_t *const in[4] = {c->k_codes, c->v_codes, c->k_scale, c->v_scale};
+  const void *out[4];
+  for (int i = 0; i < 4; ++i) {
+    const int rc = resolve_kv(s, in[i], &out[i]);
+    if (rc != KV_OK) return rc;
+  }
+  dev->k_codes = static_cast<uint8_t *>(const_cast<void *>(out[0]));
+  dev->v_codes = static_cast<uint8_t *>(const_cast<void *>(out[1]));
+  dev->k_scale = static_cast<uint8_t *>(const_cast<void *>(out[2]));
+  dev->v_scale = static_cast<uint8_t *>(const_cast<void *>(out[3]));
+  return KV_OK;
+}
+
+struct ChunkPlan {
+  int rows = 64;      // packed rows per unit
+  int ctas = 1;
+  int slot_rows = 1;  // rows of a partial result
+  size_t off_meta = 0, off_ml = 0, off_o = 0;
+  size_t total = 0;
+};
+
+// Everything here follows from the shape and the host's bounds; the lengths
+// are known on the device only.
+ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, bool q8) {
+  (void)q8;
+  ChunkPlan pl;
+  const int dev = current_device();
+  const int sms = dev >= 0 ? sm_count(dev) : 152;
+  const int G = s->num_q_heads / s->num_kv_heads;
+  const long long packed = (long long)std::min(c->max_q_len, c->total_q) * G;
+  int tile = 64;
+  pl.rows = packed <= 16 ? 16 : 64;
+  const long long blocks = (packed + pl.rows - 1) / pl.rows;
+  const long long tiles = ((long long)s->max_pages_per_seq * s->page_size + tile - 1) / tile;
+  // two CTAs share an SM; no more CTAs than there can be tiles
+  const double most = (double)s->batch * s->num_kv_heads * blocks * tiles;
+  pl.ctas = (int)std::min<double>(2.0 * sms, std::max(1.0, most));
+  pl.slot_rows = (int)std::min<long long>(pl.rows, packed);
+  size_t off = align256((size_t)pl.ctas * 32);
+  pl.off_ml = off;
+  off = align256(off + (size_t)2 * pl.ctas * pl.slot_rows * 8);
+  pl.off_o = off;
+  off = align256(off + (size_t)2 * pl.ctas * pl.slot_rows * kHeadDim * 4);
+  pl.total = off;
+  return pl;
+}
+
+size_t chunk_bytes(const kv_shape *s, const kv_chunk *c, bool q8) {
+  if (check_shape(s) != KV_OK || check_chunk(s, c) != KV_OK) return 0;
+  return make_chunk_plan(s, c, q8).total;
+}
+
+int chunk_common(const kv_shape *s, const kv_chunk *c, const void *q, const void *k_cache,
+                 const void *v_cache, const kv_q8_cache *q8, bool is_q8, const int32_t *bt,
+                 const int32_t *ctx, float scale, void *out, void *workspace, size_t ws_bytes,
+                 void *stream) {
+  int rc = check_shape(s);
+  if (rc) return rc;
+  if ((rc = check_chunk(s, c)) != KV_OK) return rc;
+  if (!al16(q) || !al16(out) || !al4(bt) || !al4(ctx) || !std::isfinite(scale))
+    return KV_ERR_INVALID_ARG;
+  const int dev = current_device();
+  if (dev < 0) return KV_ERR_CUDA;
+  ChunkArgs a = {};
+  if (is_q8) {
+    kv_q8_cache d;
+    if ((rc = resolve_q8(s, q8, &d)) != KV_OK) return rc;
+    a.k = d.k_codes;
+    a.v = d.v_codes;
+    a.k_scale = d.k_scale;
+    a.v_scale = d.v_scale;
+  } else {
+    if ((rc = resolve_kv(s, k_cache, &a.k)) != KV_OK) return rc;
+    if ((rc = resolve_kv(s, v_cache, &a.v)) != KV_OK) return rc;
+  }
+  const ChunkPlan pl = make_chunk_plan(s, c, is_q8);
+  if (!al16(workspace) || ws_bytes < pl.total) return KV_ERR_WORKSPACE;
+  int *status = status_ptr(dev);
+  if (!status) return KV_ERR_CUDA;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  a.q = q;
+  a.q_start = c->q_start;
+  a.bt = bt;
+  a.ctx = ctx;
+  a.out = out;
+  a.part_o = reinterpret_cast<float *>(ws + pl.off_o);
+  a.part_ml = reinterpret_cast<float *>(ws + pl.off_ml);
+  a.meta = reinterpret_cast<int4 *>(ws + pl.off_meta);
+  a.status = status;
+  a.nphys = s->num_phys_pages;
+  a.B = s->batch;
+  a.Hq = s->num_q_heads;
+  a.Hkv = s->num_kv_heads;
+  a.G = s->num_q_heads / s->num_kv_heads;
+  a.ps = s->page_size;
+  a.maxP = s->max_pages_per_seq;
+  a.total_q = c->total_q;
+  a.max_q_len = c->max_q_len;
+  // a window as wide as the longest row is no window
+  a.window = c->window >= (long long)a.maxP * a.ps ? 0 : c->window;
+  a.slot_rows = pl.slot_rows;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.wait_limit_ns = wait_limit_ns();
+  a.debug_skip_tile = debug_skip_page();
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_chunk_core(s->dtype, a, is_q8, pl.rows, pl.ctas, st);
+  if (e == cudaSuccess) e = launch_chunk_combine(s->dtype, a, pl.ctas, st);
+  return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t kv_chunk_workspace_bytes(const kv_shape *shape, const kv_chunk *chunk) {
+  return chunk_bytes(shape, chunk, false);
+}
+
+size_t kv_q8_chunk_workspace_bytes(const kv_shape *shape, const kv_chunk *chunk) {
+  return chunk_bytes(shape, chunk, true);
+}
+
+int kv_chunk_attn(const kv_shape *shape, const kv_chunk *chunk, const void *q,
+                  const void *k_cache, const void *v_cache, const int32_t *block_table,
+                  const int32_t *context_lens, float scale, void *out, void *workspace,
+                  size_t workspace_bytes, void *stream) {
+  KV_API_RANGE();
+  return chunk_common(shape, chunk, q, k_cache, v_cache, nullptr, false, block_table,
+                      context_lens, scale, out, workspace, workspace_bytes, stream);
+}
+
+int kv_q8_chunk_attn(const kv_shape *shape, const kv_chunk *chunk, const void *q,
+                     const kv_q8_cache *cache, const int32_t *block_table,
+                     const int32_t *context_lens, float scale, void *out, void *workspace,
+                     size_t workspace_bytes, void *stream) {
+  KV_API_RANGE();
+  return chunk_common(shape, chunk, q, nullptr, nullptr, cache, true, block_table, context_lens,
+                      scale, out, workspace, workspace_bytes, stream);
+}
+
+int kv_q8_append(const kv_shape *shape, const kv_chunk *chunk, const void *k_new,
+                 const void *v_new, const kv_q8_cache *cache, const int32_t *block_table,
+                 const int32_t *context_lens, int32_t *context_lens_out, void *stream) {
+  KV_API_RANGE();
+  int rc = check_shape(shape);
+  if (rc) return rc;
+  if ((rc = check_chunk(shape, chunk)) != KV_OK) return rc;
+  if (!al16(k_new) || !al16(v_new) || !al4(block_table) || !al4(context_lens) ||
+      (context_lens_out && !al4(context_lens_out)))
+    return KV_ERR_INVALID_ARG;
+  const int dev = current_device();
+  if (dev < 0) return KV_ERR_CUDA;
+  kv_q8_cache d;
+  if ((rc = resolve_q8(shape, cache, &d)) != KV_OK) return rc;
+  int *status = status_ptr(dev);
+  if (!status) return KV_ERR_CUDA;
+  const cudaError_t e = launch_q8_append(
+      shape->dtype, k_new, v_new, d, chunk->q_start, block_table, context_lens, context_lens_out,
+      shape->batch, shape->num_kv_heads, shape->page_size, shape->max_pages_per_seq,
+      shape->num_phys_pages, chunk->total_q, chunk->max_q_len, status,
+      static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+}
+
+int kv_q8_read(const kv_shape *shape, const kv_q8_cache *cache, const int32_t *block_table,
+               const int32_t *context_lens, const int32_t *out_table, int64_t out_pages,
+               void *k_out, void *v_out, void *stream) {
+  KV_API_RANGE();
+  int rc = check_shape(shape);
+  if (rc) return rc;
+  if (!al16(k_out) || !al16(v_out) || !al4(block_table) || !al4(context_lens) ||
+      !al4(out_table) || out_pages < 1)
+    return KV_ERR_INVALID_ARG;
+  if (out_pages > INT_MAX / ((long long)shape->num_kv_heads * shape->page_size))
+    return KV_ERR_UNSUPPORTED;
+  const int dev = current_device();
+  if (dev < 0) return KV_ERR_CUDA;
+  kv_q8_cache d;
+  if ((rc = resolve_q8(shape, cache, &d)) != KV_OK) return rc;
+  // the pages read back are in device memory whatever kv_loc says
+  kv_shape hbm = *shape;
+  hbm.kv_loc = KV_LOC_HBM;
+  const void *ko = nullptr, *vo = nullptr;
+  if ((rc = resolve_kv(&hbm, k_out, &ko)) != KV_OK) return rc;
+  if ((rc = resolve_kv(&hbm, v_out, &vo)) != KV_OK) return rc;
+  int *status = status_ptr(dev);
+  if (!status) return KV_ERR_CUDA;
+  const cudaError_t e = launch_q8_read(
+      shape->dtype, d, block_table, context_lens, out_table, out_pages, const_cast<void *>(ko),
+      const_cast<void *>(vo), shape->batch, shape->num_kv_heads, shape->page_size,
+      shape->max_pages_per_seq, shape->num_phys_pages, status,
+      static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+}
+
+}  // extern "C"

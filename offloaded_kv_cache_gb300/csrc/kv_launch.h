@@ -77,4 +77,21 @@ cudaError_t launch_combine_lists(const float *part_o, const float *part_ml, cons
                                  const float *spa_ml, const int32_t *gmeta, float *out, int S,
                                  int B, int Hq, int Hkv, int nw, int *status, cudaStream_t st);
 
+// the chunk operators (kv_chunk.cuh): rows = packed rows per unit, ctas = the
+// shares the work is cut into
+struct ChunkArgs;
+cudaError_t launch_chunk_core(int dtype, const ChunkArgs &a, bool q8, int rows, int ctas,
+                              cudaStream_t st);
+cudaError_t launch_chunk_combine(int dtype, const ChunkArgs &a, int ctas, cudaStream_t st);
+// the 8-bit cache (device-visible addresses)
+cudaError_t launch_q8_append(int dtype, const void *k_new, const void *v_new,
+                             const kv_q8_cache &c, const int32_t *q_start, const int32_t *bt,
+                             const int32_t *ctx, int32_t *ctx_out, int B, int Hkv, int ps,
+                             int maxP, long long nphys, int total_q, int max_q_len, int *status,
+                             cudaStream_t st);
+cudaError_t launch_q8_read(int dtype, const kv_q8_cache &c, const int32_t *bt, const int32_t *ctx,
+                           const int32_t *out_table, long long out_pages, void *k_out,
+                           void *v_out, int B, int Hkv, int ps, int maxP, long long nphys,
+                           int *status, cudaStream_t st);
+
 }  // namespace kvs

@@ -56,6 +56,17 @@ class kv_step_io(ctypes.Structure):
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
 
+class kv_chunk(ctypes.Structure):
+    _fields_ = [("q_start", ctypes.c_void_p), ("total_q", ctypes.c_int32),
+                ("max_q_len", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class kv_q8_cache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
 class KvError(RuntimeError):
     def __init__(self, code: int, where: str):
         super().__init__(f"{where}: {status_string(code)} ({code})")
@@ -107,6 +118,15 @@ def load(path: str = LIB_PATH):
         "kv_stream_read_probe": (ctypes.c_int, [P, sz, P, i32, P]),
         "kv_stream_read_probe_shape": (ctypes.c_int, [P, sz, P, i32, i32, i32, P]),
     }
+    C, Q = ctypes.POINTER(kv_chunk), ctypes.POINTER(kv_q8_cache)
+    sig.update({
+        "kv_chunk_workspace_bytes": (sz, [S, C]),
+        "kv_chunk_attn": (ctypes.c_int, [S, C, P, P, P, P, P, f32, P, P, sz, P]),
+        "kv_q8_append": (ctypes.c_int, [S, C, P, P, Q, P, P, P, P]),
+        "kv_q8_read": (ctypes.c_int, [S, Q, P, P, P, ctypes.c_int64, P, P, P]),
+        "kv_q8_chunk_workspace_bytes": (sz, [S, C]),
+        "kv_q8_chunk_attn": (ctypes.c_int, [S, C, P, Q, P, P, f32, P, P, sz, P]),
+    })
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
         fn.restype = res
@@ -289,6 +309,60 @@ def kv_dense_decode_attn(shape, q, k_cache, v_cache, block_table, context_lens, 
                                      _ptr(out), _ptr(workspace), int(workspace_bytes),
                                      _stream(stream))
     return _ret(rc, "kv_dense_decode_attn", check)
+
+
+def make_chunk(q_start, total_q, max_q_len, window=0) -> kv_chunk:
+    """The ragged batch of new tokens of a call; q_start is a device int32
+    tensor [B + 1], which must outlive the calls."""
+    return kv_chunk(_ptr(q_start), int(total_q), int(max_q_len), int(window), 0)
+
+
+def make_q8_cache(k_codes, v_codes, k_scale, v_scale) -> kv_q8_cache:
+    return kv_q8_cache(_ptr(k_codes), _ptr(v_codes), _ptr(k_scale), _ptr(v_scale))
+
+
+def _ref(x):
+    return None if x is None else ctypes.byref(x)
+
+
+def kv_chunk_workspace_bytes(shape, chunk) -> int:
+    return int(load().kv_chunk_workspace_bytes(ctypes.byref(shape), _ref(chunk)))
+
+
+def kv_chunk_attn(shape, chunk, q, k_cache, v_cache, block_table, context_lens, scale, out,
+                  workspace, workspace_bytes, stream=None, check=True):
+    rc = load().kv_chunk_attn(ctypes.byref(shape), _ref(chunk), _ptr(q), _ptr(k_cache),
+                              _ptr(v_cache), _ptr(block_table), _ptr(context_lens), float(scale),
+                              _ptr(out), _ptr(workspace), int(workspace_bytes), _stream(stream))
+    return _ret(rc, "kv_chunk_attn", check)
+
+
+def kv_q8_append(shape, chunk, k_new, v_new, cache, block_table, context_lens,
+                 context_lens_out=None, stream=None, check=True):
+    rc = load().kv_q8_append(ctypes.byref(shape), _ref(chunk), _ptr(k_new), _ptr(v_new),
+                             _ref(cache), _ptr(block_table), _ptr(context_lens),
+                             _ptr(context_lens_out), _stream(stream))
+    return _ret(rc, "kv_q8_append", check)
+
+
+def kv_q8_read(shape, cache, block_table, context_lens, out_table, out_pages, k_out, v_out,
+               stream=None, check=True):
+    rc = load().kv_q8_read(ctypes.byref(shape), _ref(cache), _ptr(block_table),
+                           _ptr(context_lens), _ptr(out_table), int(out_pages), _ptr(k_out),
+                           _ptr(v_out), _stream(stream))
+    return _ret(rc, "kv_q8_read", check)
+
+
+def kv_q8_chunk_workspace_bytes(shape, chunk) -> int:
+    return int(load().kv_q8_chunk_workspace_bytes(ctypes.byref(shape), _ref(chunk)))
+
+
+def kv_q8_chunk_attn(shape, chunk, q, cache, block_table, context_lens, scale, out, workspace,
+                     workspace_bytes, stream=None, check=True):
+    rc = load().kv_q8_chunk_attn(ctypes.byref(shape), _ref(chunk), _ptr(q), _ref(cache),
+                                 _ptr(block_table), _ptr(context_lens), float(scale), _ptr(out),
+                                 _ptr(workspace), int(workspace_bytes), _stream(stream))
+    return _ret(rc, "kv_q8_chunk_attn", check)
 
 
 def kv_device_status(stream=None) -> int:
