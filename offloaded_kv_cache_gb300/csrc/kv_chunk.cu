@@ -30,7 +30,7 @@ template <int MR> struct Shape {
 };
 
 // 8 channels of one cached vector in fp32
-template <class T, bool Q8>
+template <bool Q8>
 __device__ __forceinline__ void cached8(const void *base, const uint8_t *scale, long long vec,
                                         int c, float (&x)[8]) {
   if constexpr (Q8) {
@@ -46,15 +46,15 @@ __device__ __forceinline__ void cached8(const void *base, const uint8_t *scale, 
       x[4 + i] = hi[i] * s;
     }
   } else {
-    load8(static_cast<const T *>(base) + vec * kHeadDim + c, x);
+    load8(static_cast<const float *>(base) + vec * kHeadDim + c, x);
   }
 }
 
-template <class T, int MR, bool Q8>
+template <int MR, bool Q8>
 __global__ void __launch_bounds__(kThreads) chunk_core_kernel(const ChunkArgs a) {
   using Sh = Shape<MR>;
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ ChunkShare share;
+  __shared__ ChunkShare<16> share;
   __shared__ long long red[33];
   __shared__ int tok_ok[kTile];
   float *Qs = reinterpret_cast<float *>(smem);
@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kThreads) chunk_core_kernel(const ChunkArgs a)
         float x[8] = {};
         if (r < g.nrows) {
           const int pr = g.r0 + r, row = g.q0 + pr / a.G, head = g.kvh * a.G + pr % a.G;
-          load8(static_cast<const T *>(a.q) + ((long long)row * a.Hq + head) * kHeadDim + c, x);
+          load8(static_cast<const float *>(a.q) + ((long long)row * a.Hq + head) * kHeadDim + c, x);
         }
         store8(Qs + r * kQStr + c, x);
       }
@@ -92,7 +92,6 @@ __global__ void __launch_bounds__(kThreads) chunk_core_kernel(const ChunkArgs a)
 #pragma unroll
         for (int c = 0; c < 8; ++c) o[r][c] = 0.f;
       }
-      const int t_first = g.len - g.n + g.r0 / a.G;
       for (int tile = g.tile_lo; tile < g.tile_hi; ++tile) {
         const int tok0 = tile * kTile;
         // K and V of the tile; tokens past the end or of a bad page are zero
@@ -106,8 +105,8 @@ __global__ void __launch_bounds__(kThreads) chunk_core_kernel(const ChunkArgs a)
             if (!ok && c == 0) flag_error(a.status, KV_ERR_BOUNDS);
             if (ok) {
               const long long vec = ((long long)ph * a.Hkv + g.kvh) * a.ps + pos % a.ps;
-              cached8<T, Q8>(a.k, a.k_scale, vec, c, kx);
-              cached8<T, Q8>(a.v, a.v_scale, vec, c, vx);
+              cached8<Q8>(a.k, a.k_scale, vec, c, kx);
+              cached8<Q8>(a.v, a.v_scale, vec, c, vx);
             }
           }
           if (c == 0) tok_ok[tok] = ok;
@@ -166,7 +165,7 @@ __global__ void __launch_bounds__(kThreads) chunk_core_kernel(const ChunkArgs a)
         __syncthreads();
         // where some row does not see some token, a weight of 0 must not meet
         // an infinity or NaN of V
-        const bool edge = tok0 + kTile - 1 > t_first || a.window > 0;
+        const bool edge = tok0 + kTile - 1 > g.t_first || a.window > 0;
 #pragma unroll 4
         for (int j = 0; j < kTile; ++j) {
           const float4 v0 = *reinterpret_cast<const float4 *>(Vs + j * kHeadDim + tx * 4);
@@ -182,7 +181,7 @@ __global__ void __launch_bounds__(kThreads) chunk_core_kernel(const ChunkArgs a)
         }
         __syncthreads();
       }
-      const bool whole = g.first && g.last;
+      const bool whole = g.whole();
       const int slot = part_slot(g);
 #pragma unroll
       for (int r = 0; r < MR; ++r) {
@@ -194,17 +193,12 @@ __global__ void __launch_bounds__(kThreads) chunk_core_kernel(const ChunkArgs a)
         if (whole) {
           const float inv = sum == 0.f ? 0.f : 1.f / sum;
           const int pr = g.r0 + rr, row = g.q0 + pr / a.G, head = g.kvh * a.G + pr % a.G;
-          T *dst = static_cast<T *>(a.out) + ((long long)row * a.Hq + head) * kHeadDim + tx * 4;
+          float *dst = static_cast<float *>(a.out) + ((long long)row * a.Hq + head) * kHeadDim;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float y[4] = {o[r][4 * h] * inv, o[r][4 * h + 1] * inv, o[r][4 * h + 2] * inv,
-                                o[r][4 * h + 3] * inv};
-            if constexpr (std::is_same_v<T, float>)
-              *reinterpret_cast<float4 *>(dst + 64 * h) = make_float4(y[0], y[1], y[2], y[3]);
-            else
-              *reinterpret_cast<uint2 *>(dst + 64 * h) =
-                  make_uint2(pack2(y[0], y[1], T{}), pack2(y[2], y[3], T{}));
-          }
+          for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<float4 *>(dst + 64 * h + tx * 4) =
+                make_float4(o[r][4 * h] * inv, o[r][4 * h + 1] * inv, o[r][4 * h + 2] * inv,
+                            o[r][4 * h + 3] * inv);
         } else {
           const long long pr = (long long)slot * a.slot_rows + rr;
           float *dst = a.part_o + pr * kHeadDim + tx * 4;
@@ -265,28 +259,19 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const ChunkArgs a) {
   }
 }
 
-template <class T, int MR, bool Q8>
+template <int MR, bool Q8>
 cudaError_t core_go(const ChunkArgs &a, int ctas, cudaStream_t st) {
   const cudaError_t e = cudaFuncSetAttribute(
-      chunk_core_kernel<T, MR, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<MR>::kSmem);
+      chunk_core_kernel<MR, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<MR>::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(chunk_core_kernel<T, MR, Q8>, dim3(ctas), dim3(kThreads), Shape<MR>::kSmem, st,
-                    a);
-}
-template <class T>
-cudaError_t core_type(const ChunkArgs &a, bool q8, int rows, int ctas, cudaStream_t st) {
-  if (rows == 16)
-    return q8 ? core_go<T, 1, true>(a, ctas, st) : core_go<T, 1, false>(a, ctas, st);
-  return q8 ? core_go<T, 4, true>(a, ctas, st) : core_go<T, 4, false>(a, ctas, st);
+  return launch_pdl(chunk_core_kernel<MR, Q8>, dim3(ctas), dim3(kThreads), Shape<MR>::kSmem, st, a);
 }
 
 }  // namespace
 
-cudaError_t launch_chunk_core(int dtype, const ChunkArgs &a, bool q8, int rows, int ctas,
-                              cudaStream_t st) {
-  return dtype == KV_F32   ? core_type<float>(a, q8, rows, ctas, st)
-         : dtype == KV_F16 ? core_type<__half>(a, q8, rows, ctas, st)
-                           : core_type<__nv_bfloat16>(a, q8, rows, ctas, st);
+cudaError_t launch_chunk_core(const ChunkArgs &a, bool q8, int rows, int ctas, cudaStream_t st) {
+  if (rows == 16) return q8 ? core_go<1, true>(a, ctas, st) : core_go<1, false>(a, ctas, st);
+  return q8 ? core_go<4, true>(a, ctas, st) : core_go<4, false>(a, ctas, st);
 }
 
 cudaError_t launch_chunk_combine(int dtype, const ChunkArgs &a, int ctas, cudaStream_t st) {

@@ -22,6 +22,8 @@
 
 namespace kvs {
 
+constexpr int kChunkTile = 128;  // tokens per KV tile of the tensor-core kernels
+
 struct ChunkArgs {
   const void *q;
   const void *k, *v;                // K and V (8-bit: the codes)
@@ -71,19 +73,20 @@ struct ChunkSeg {
   int b, kvh, r0, nrows;  // unit: packed rows [r0, r0 + nrows) of (b, kvh)
   int q0, n, len;         // its sequence
   int tile_lo, tile_hi;   // the KV tiles of this segment
-  int first, last;        // it holds the unit's first / last tile
-  int pad;
+  int parts;              // bit 0: it holds the unit's first tile, bit 1: its last
+  int t_first, t_last;    // tokens of the unit's first and last row
+  __device__ __forceinline__ bool first() const { return parts & 1; }
+  __device__ __forceinline__ bool whole() const { return parts == 3; }
 };
 
-constexpr int kMaxSegs = 32;  // segments listed at a time
-
-struct ChunkShare {
+// A CTA's share, kSegs segments of it listed at a time.
+template <int kSegs> struct ChunkShare {
   long long work, lo, hi;  // all tiles; this CTA's share
   int b, kvh, r0, off;     // walk: the next unit, and its tiles already passed
   long long left;          // tiles of the share not listed yet
   int nseg;
   int ctas;                // CTAs with a share: no more than there are tiles
-  ChunkSeg seg[kMaxSegs];
+  ChunkSeg seg[kSegs];
 };
 
 __device__ __forceinline__ int packed_rows(const ChunkArgs &a, const ChunkSeq &s) {
@@ -109,8 +112,9 @@ __device__ __forceinline__ long long warp_sum(long long x) {
 
 // Every thread of the CTA: the total work, this CTA's share and where it
 // starts.  red: 33 long longs of shared scratch.
-__device__ __forceinline__ void share_init(const ChunkArgs &a, int rows, int tile, ChunkShare *sh,
-                                           long long *red) {
+template <int kSegs>
+__device__ __forceinline__ void share_init(const ChunkArgs &a, int rows, int tile,
+                                           ChunkShare<kSegs> *sh, long long *red) {
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, nw = blockDim.x >> 5;
   long long mine = 0;
   for (int b = t; b < a.B; b += blockDim.x)
@@ -176,15 +180,16 @@ __device__ __forceinline__ void share_init(const ChunkArgs &a, int rows, int til
 // The CTA that holds a unit's first tile but not its last records where the
 // combine finds the rest: slot 2 i + 1 of CTA i (a share's last segment) for
 // the first part, slot 2 j (a share's first segment) for each further part.
+template <int kSegs>
 __device__ __forceinline__ void share_next(const ChunkArgs &a, int rows, int tile,
-                                           ChunkShare *sh) {
+                                           ChunkShare<kSegs> *sh) {
   int n = 0;
   if (sh->left > 0) {
     int b = sh->b, kvh = sh->kvh, r0 = sh->r0, off = sh->off;
     long long left = sh->left;
     ChunkSeq s = chunk_seq(a, b, false);
     int R = packed_rows(a, s);
-    while (n < kMaxSegs && left > 0) {
+    while (n < kSegs && left > 0) {
       const int nrows = min(rows, R - r0);
       const TileRange t = unit_tiles(a, s, r0, nrows, tile);
       const int have = t.hi - t.lo - off;
@@ -199,9 +204,10 @@ __device__ __forceinline__ void share_next(const ChunkArgs &a, int rows, int til
       g.len = s.len;
       g.tile_lo = t.lo + off;
       g.tile_hi = t.lo + off + take;
-      g.first = off == 0;
-      g.last = take == have;
-      if (g.first && !g.last) {
+      g.parts = (off == 0 ? 1 : 0) | (take == have ? 2 : 0);
+      g.t_first = s.len - s.n + r0 / a.G;
+      g.t_last = s.len - s.n + (r0 + nrows - 1) / a.G;
+      if (g.parts == 1) {
         // the CTA whose share holds the unit's last tile
         const long long end = sh->hi - left + (t.hi - t.lo) - 1;
         const int j = (int)(((end + 1) * sh->ctas - 1) / sh->work);
@@ -236,7 +242,7 @@ __device__ __forceinline__ void share_next(const ChunkArgs &a, int rows, int til
 
 // partial-result slot of a segment that is not a whole unit
 __device__ __forceinline__ int part_slot(const ChunkSeg &g) {
-  return 2 * (int)blockIdx.x + (g.first ? 1 : 0);
+  return 2 * (int)blockIdx.x + (g.first() ? 1 : 0);
 }
 
 // visible columns [lo, hi] of a tile starting at token tile0, for token t

@@ -3,7 +3,7 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
-#include <cstring>
+#include <mutex>
 
 #include "kv_chunk.cuh"
 #include "kv_host.h"
@@ -39,37 +39,107 @@ int resolve_q8(const kv_shape *s, const kv_q8_cache *c, kv_q8_cache *dev) {
 }
 
 struct ChunkPlan {
+  bool mma = false;   // tensor cores (16-bit data)
+  bool pair = false;  // units of at most 128 rows
+  bool stage = false; // K/V pass through the workspace in 16 bits
+  bool renumber = false;  // the staged pages have a block table of their own
+  long long stage_pages = 0;
   int rows = 64;      // packed rows per unit
   int ctas = 1;
   int slot_rows = 1;  // rows of a partial result
-  size_t off_meta = 0, off_ml = 0, off_o = 0;
+  size_t off_meta = 0, off_ml = 0, off_o = 0, off_table = 0, off_k = 0, off_v = 0;
   size_t total = 0;
 };
 
 // Everything here follows from the shape and the host's bounds; the lengths
 // are known on the device only.
 ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, bool q8) {
-  (void)q8;
   ChunkPlan pl;
   const int dev = current_device();
   const int sms = dev >= 0 ? sm_count(dev) : 152;
   const int G = s->num_q_heads / s->num_kv_heads;
   const long long packed = (long long)std::min(c->max_q_len, c->total_q) * G;
-  int tile = 64;
-  pl.rows = packed <= 16 ? 16 : 64;
+  pl.mma = s->dtype != KV_F32;
+  int tile = 64, per_sm = 2;
+  if (pl.mma) {
+    tile = kChunkTile;
+    per_sm = 1;
+    pl.pair = packed <= 128;
+    pl.rows = pl.pair ? 128 : 256;
+    pl.stage = q8 || s->kv_loc == KV_LOC_HOST_PINNED;
+  } else {
+    pl.rows = packed <= 16 ? 16 : 64;
+  }
   const long long blocks = (packed + pl.rows - 1) / pl.rows;
   const long long tiles = ((long long)s->max_pages_per_seq * s->page_size + tile - 1) / tile;
-  // two CTAs share an SM; no more CTAs than there can be tiles
+  // no more CTAs than there can be tiles
   const double most = (double)s->batch * s->num_kv_heads * blocks * tiles;
-  pl.ctas = (int)std::min<double>(2.0 * sms, std::max(1.0, most));
+  pl.ctas = (int)std::min<double>((double)per_sm * sms, std::max(1.0, most));
   pl.slot_rows = (int)std::min<long long>(pl.rows, packed);
   size_t off = align256((size_t)pl.ctas * 32);
   pl.off_ml = off;
   off = align256(off + (size_t)2 * pl.ctas * pl.slot_rows * 8);
   pl.off_o = off;
   off = align256(off + (size_t)2 * pl.ctas * pl.slot_rows * kHeadDim * 4);
+  if (pl.stage) {
+    // staged under the cache's own page numbers, or, where that takes less,
+    // under the rows of the block table
+    const long long rows = (long long)s->batch * s->max_pages_per_seq;
+    pl.renumber = rows < s->num_phys_pages;
+    pl.stage_pages = pl.renumber ? rows : s->num_phys_pages;
+    const size_t page = (size_t)s->num_kv_heads * s->page_size * kHeadDim * 2;
+    pl.off_table = off;
+    if (pl.renumber) off = align256(off + (size_t)rows * 4);
+    pl.off_k = off;
+    off = align256(off + (size_t)pl.stage_pages * page);
+    pl.off_v = off;
+    off = align256(off + (size_t)pl.stage_pages * page);
+  }
   pl.total = off;
   return pl;
+}
+
+// 2-D view [rows = pages * Hkv * ps][128 elements] of 16-bit pages; a box is
+// 64 channels (128 bytes, swizzled) of one page.  Encoding takes host time on
+// every call, so the last ones are kept; an entry depends on its key alone.
+struct MapEntry {
+  int dev, dtype, ps;
+  const void *base;
+  long long rows;
+  CUtensorMap map;
+};
+std::mutex g_map_mutex;
+MapEntry g_maps[16];
+unsigned g_map_n = 0;
+
+int page_map(const kv_shape *s, const void *base, long long pages, int dev, CUtensorMap *map) {
+  const long long rows = pages * s->num_kv_heads * s->page_size;
+  std::lock_guard<std::mutex> lock(g_map_mutex);
+  for (unsigned i = 0; i < std::min(g_map_n, 16u); ++i) {
+    const MapEntry &e = g_maps[i];
+    if (e.dev == dev && e.base == base && e.rows == rows && e.dtype == s->dtype &&
+        e.ps == s->page_size) {
+      *map = e.map;
+      return KV_OK;
+    }
+  }
+  auto fn = encode_fn();
+  if (!fn) return KV_ERR_CUDA;
+  cuuint64_t dims[2] = {(cuuint64_t)kHeadDim, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)kHeadDim * 2};
+  cuuint32_t box[2] = {64, (cuuint32_t)s->page_size};
+  cuuint32_t estr[2] = {1, 1};
+  const CUresult r =
+      fn(map, s->dtype == KV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+         2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return KV_ERR_CUDA;
+  MapEntry &e = g_maps[g_map_n % 16];
+  e = MapEntry{dev, s->dtype, s->page_size, base, rows, *map};
+  ++g_map_n;
+  if (g_map_n >= 32) g_map_n -= 16;
+  return KV_OK;
 }
 
 size_t chunk_bytes(const kv_shape *s, const kv_chunk *c, bool q8) {
@@ -101,6 +171,9 @@ int chunk_common(const kv_shape *s, const kv_chunk *c, const void *q, const void
     if ((rc = resolve_kv(s, v_cache, &a.v)) != KV_OK) return rc;
   }
   const ChunkPlan pl = make_chunk_plan(s, c, is_q8);
+  // the staged cache's rows are indexed as a cache's own
+  if (pl.stage_pages > INT_MAX / ((long long)s->num_kv_heads * s->page_size))
+    return KV_ERR_UNSUPPORTED;
   if (!al16(workspace) || ws_bytes < pl.total) return KV_ERR_WORKSPACE;
   int *status = status_ptr(dev);
   if (!status) return KV_ERR_CUDA;
@@ -128,9 +201,28 @@ int chunk_common(const kv_shape *s, const kv_chunk *c, const void *q, const void
   a.slot_rows = pl.slot_rows;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.wait_limit_ns = wait_limit_ns();
-  a.debug_skip_tile = debug_skip_page();
+  a.debug_skip_tile = debug_skip_page() < 0 ? -1 : debug_skip_page() / (kChunkTile / kTileTokens);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_chunk_core(s->dtype, a, is_q8, pl.rows, pl.ctas, st);
+  cudaError_t e;
+  if (pl.mma) {
+    long long pages = s->num_phys_pages;
+    if (pl.stage) {
+      int32_t *table = pl.renumber ? reinterpret_cast<int32_t *>(ws + pl.off_table) : nullptr;
+      if (launch_chunk_stage(s->dtype, is_q8, a, ws + pl.off_k, ws + pl.off_v, table, st) !=
+          cudaSuccess)
+        return KV_ERR_CUDA;
+      a.k = ws + pl.off_k;
+      a.v = ws + pl.off_v;
+      if (table) a.bt = table;
+      a.nphys = pages = pl.stage_pages;
+    }
+    CUtensorMap tk, tv;
+    if ((rc = page_map(s, a.k, pages, dev, &tk)) != KV_OK) return rc;
+    if ((rc = page_map(s, a.v, pages, dev, &tv)) != KV_OK) return rc;
+    e = launch_chunk_mma(s->dtype, pl.pair, a, tk, tv, pl.ctas, st);
+  } else {
+    e = launch_chunk_core(a, is_q8, pl.rows, pl.ctas, st);
+  }
   if (e == cudaSuccess) e = launch_chunk_combine(s->dtype, a, pl.ctas, st);
   return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
 }

@@ -1,0 +1,729 @@
+// kv_chunk_mma.cu -- chunk attention for 16-bit data on the tensor cores
+// (tcgen05, accumulators in TMEM).  kv_chunk.cuh has the formula and how the
+// work is cut into shares of segments.
+//
+// One CTA per SM, twelve warps:
+//   warps 0-3, 4-7  two softmax groups, a thread per packed row
+//   warp 8          loads K and V tiles (TMA, one box per page and 64 channels)
+//   warp 9          issues the matrix products (one lane)
+//   warp 10         mends V at the edges (below)
+//   warp 11         loads Q
+// Per KV tile of 128 tokens and softmax group: S = Q K^T (128 x 128 x 128)
+// into TMEM; the group takes its maximum and exponentials and writes the
+// weights P in 16 bits over S; O += P V.  While one group computes, the tensor
+// cores work for the other.  TMEM: S and P of the groups at columns 0 and 128,
+// O at 256 and 384.
+//   * kPair = false: a unit is 256 packed rows, 128 per group; both groups use
+//     each K/V tile, which halves the reads of K and V per product.
+//   * kPair = true: a unit is up to 128 rows; the groups take its KV tiles in
+//     turn (even, odd) and join their results at the end.  For few rows per
+//     sequence, where the K/V stream is the bound and each tile's chain of
+//     product, softmax and product would otherwise be exposed.
+//
+// The running maximum is moved only when a row's new maximum exceeds it by
+// more than 2^8 in the weights: until then the weights may be as large as 2^8,
+// which neither 16-bit type nor the fp32 sums mind, and O need not be
+// rescaled.  f16 weights are kept 2^7 larger, so that weights down to 2^-21
+// of the maximum keep all their bits.
+//
+// What a row does not see must not reach it through 0 * infinity: K needs no
+// care (its scores are replaced), V does.  Slots past the sequence's end in its
+// last page are zeroed in shared memory before the product.  In tiles where
+// some row does not see some token, infinities and NaN of V are zeroed as
+// well, and the rows that do see them get their NaN when they are written
+// (a slow path that only such data takes).  Pages past the end or out of range
+// are filled with zeros by the TMA unit.
+#include <type_traits>
+
+#include "kv_chunk.cuh"
+#include "kv_launch.h"
+#include "kv_q8.cuh"
+#include "kv_umma.cuh"
+
+namespace kvs {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kTile = kChunkTile;
+constexpr int kTileBytes = kTile * kHeadDim * 2;  // 32 KB
+constexpr int kSlab = kTile * 128;                // 64 channels of a tile
+constexpr uint32_t kTmemCols = 512;
+constexpr float kMoveAt = 8.f;  // log2 of the largest weight before the maximum moves
+
+template <bool kPair> struct Shape {
+  static constexpr int kRows = kPair ? 128 : 256;
+  static constexpr int kQTiles = kPair ? 1 : 2;
+  static constexpr int kStages = kPair ? 6 : 5;  // K and V tiles in the ring
+  static constexpr int kTileArea = (kQTiles + kStages) * kTileBytes;
+};
+
+template <bool kPair> struct Control {
+  uint64_t full[6], empty[6];
+  uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_done[2], mend[2], mended[2];
+  uint64_t joined, read, drain;
+  uint32_t tmem;
+  int abort;      // a wait ran out: every role leaves
+  int poison;     // a non-finite V was zeroed in some tile
+  int pad;
+  uint8_t bad[8];  // per tile, bit i: tokens 16 i .. + 15 have no page
+  ChunkShare<kPair ? 12 : 40> share;
+  union {
+    long long red[33];                // share_init
+    float2 ml[2][kPair ? 128 : 1];   // kPair: maximum and sum of each group's rows
+  };
+};
+static_assert(Shape<false>::kTileArea + sizeof(Control<false>) <= 227 * 1024, "shared memory");
+static_assert(Shape<true>::kTileArea + sizeof(Control<true>) <= 227 * 1024, "shared memory");
+
+// A bounded wait of a whole warp or a lane; false once anything has timed out.
+struct Waiter {
+  volatile int *abort;
+  int *status;
+  unsigned long long limit;
+  __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    if (mbar_wait(bar, parity, limit)) return true;
+    flag_error(status, KV_ERR_DEVICE_TIMEOUT);
+    *abort = 1;
+    return false;
+  }
+};
+
+template <int kStages> struct Ring {
+  int s = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++s == kStages) {
+      s = 0;
+      ph ^= 1;
+    }
+  }
+  __device__ __forceinline__ void next(int n) {
+    for (int i = 0; i < n; ++i) next();
+  }
+};
+
+// What the V of a tile needs before the product reads it.
+struct Mend {
+  int zero_lo, zero_hi;  // token rows past the end in the last page
+  int scan;              // rows [0, scan): some row does not see some of them
+};
+__device__ __forceinline__ Mend mend_of(const ChunkArgs &a, const ChunkSeg &g, int tile) {
+  const int tok0 = tile * kTile;
+  Mend m{0, 0, 0};
+  const int valid = min(kTile, g.len - tok0);
+  if (valid < kTile && (g.len & (a.ps - 1)) != 0 && valid > 0) {
+    m.zero_lo = valid;
+    m.zero_hi = min(kTile, ((g.len + a.ps - 1) & -a.ps) - tok0);
+  }
+  if (valid > 0 &&
+      (tok0 + valid - 1 > g.t_first || (a.window > 0 && tok0 <= g.t_last - a.window)))
+    m.scan = valid;
+  return m;
+}
+__device__ __forceinline__ bool needs_mend(const Mend &m) {
+  return m.scan > 0 || m.zero_hi > m.zero_lo;
+}
+
+// the exponent field, and what carries out of it when it is all ones
+template <class T> struct NonFinite;
+template <> struct NonFinite<__half> {
+  static constexpr uint32_t kMask = 0x7C007C00u, kOne = 0x04000400u;
+};
+template <> struct NonFinite<__nv_bfloat16> {
+  static constexpr uint32_t kMask = 0x7F807F80u, kOne = 0x00800080u;
+};
+
+// Rows that see a non-finite V of a scanned tile get NaN in its channels
+// [c0, c1): the values are read again from the cache.
+template <class T>
+__device__ __noinline__ void poison_row(const ChunkArgs &a, const ChunkSeg &g, int t, int c0,
+                                        int c1, T *out, float *part) {
+  for (int tile = g.tile_lo; tile < g.tile_hi; ++tile) {
+    if (mend_of(a, g, tile).scan == 0) continue;
+    const int lo = max(tile * kTile, a.window > 0 ? t - a.window + 1 : 0);
+    const int hi = min(min(tile * kTile + kTile - 1, t), g.len - 1);
+    for (int j = lo; j <= hi; ++j) {
+      const int ph = a.bt[(long long)g.b * a.maxP + j / a.ps];
+      if (ph < 0 || ph >= a.nphys) continue;
+      const uint32_t *v = reinterpret_cast<const uint32_t *>(
+          static_cast<const T *>(a.v) +
+          (((long long)ph * a.Hkv + g.kvh) * a.ps + j % a.ps) * kHeadDim);
+      for (int c = c0; c < c1; c += 2) {
+        const uint32_t x = (v[c / 2] & NonFinite<T>::kMask) + NonFinite<T>::kOne;
+        for (int h = 0; h < 2; ++h) {
+          if (!(x & (h ? 0x80000000u : 0x8000u))) continue;
+          if (part) part[c + h] = __uint_as_float(0x7FC00000u);
+          else reinterpret_cast<uint16_t *>(out)[c + h] = 0x7FFFu;
+        }
+      }
+    }
+  }
+}
+
+template <class T> __device__ __forceinline__ constexpr float weight_bias() { return 0.f; }
+template <> __device__ __forceinline__ constexpr float weight_bias<__half>() { return 7.f; }
+
+template <class T, bool kPair>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_mma_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tk,
+                     const __grid_constant__ CUtensorMap tv) {
+  using Sh = Shape<kPair>;
+  constexpr int kStages = Sh::kStages;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t *q_area = smem;
+  uint8_t *ring = smem + Sh::kQTiles * kTileBytes;
+  Control<kPair> &ctl = *reinterpret_cast<Control<kPair> *>(smem + Sh::kTileArea);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (smem_u32(smem) & 1023u) {  // the swizzled tiles need it
+    if (tid == 0) flag_error(a.status, KV_ERR_INVALID_ARG);
+    return;
+  }
+  if (warp == 9) tmem_alloc(smem_u32(&ctl.tmem), kTmemCols);
+  if (tid == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tk)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tv)) : "memory");
+    for (int i = 0; i < 6; ++i) {
+      mbar_init(smem_u32(&ctl.full[i]), 1);
+      mbar_init(smem_u32(&ctl.empty[i]), 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(smem_u32(&ctl.q_full[x]), 1);
+      mbar_init(smem_u32(&ctl.q_free[x]), 1);
+      mbar_init(smem_u32(&ctl.s_full[x]), 1);
+      mbar_init(smem_u32(&ctl.p_full[x]), 4);
+      mbar_init(smem_u32(&ctl.o_done[x]), 1);
+      mbar_init(smem_u32(&ctl.mend[x]), 1);
+      mbar_init(smem_u32(&ctl.mended[x]), 1);
+    }
+    mbar_init(smem_u32(&ctl.joined), 8);
+    mbar_init(smem_u32(&ctl.read), 8);
+    mbar_init(smem_u32(&ctl.drain), 1);
+    fence_mbar_init();
+    ctl.abort = 0;
+    ctl.poison = 0;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl.tmem;
+  pdl_wait();
+  if (tid == 0) a.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
+  share_init(a, Sh::kRows, kTile, &ctl.share, ctl.red);
+  const Waiter wait{&ctl.abort, a.status, a.wait_limit_ns};
+  const auto &share = ctl.share;
+  const int group = warp >> 2;  // softmax group (warps 0-7)
+
+  // state that lives across lists of segments
+  Ring<kStages> ld;              // loader: next slot; mender: the next tile's K slot
+  Ring<kStages> qk, pv;          // products: slot of the next K / of the next tile's K
+  uint32_t tiles_loaded = 0;     // loader, softmax: tiles so far
+  uint32_t q_ph = 0, p_ph = 0, mend_ph = 0;  // bit x
+  uint32_t s_ph = 0, o_ph = 0, j_ph = 0;
+  uint32_t q_uses = 0;           // bit x: the Q tile has been used before
+
+  // the next list of segments; all threads ask together
+  auto next_list = [&]() -> bool {
+    __syncthreads();
+    if (tid == 0) {
+      share_next(a, Sh::kRows, kTile, &ctl.share);
+      if (*reinterpret_cast<volatile int *>(&ctl.abort)) ctl.share.nseg = 0;
+    }
+    __syncthreads();
+    return share.nseg != 0;
+  };
+
+  // registers: 256 threads x 200 + 128 x 104 = 384 x 168, the launch's; the
+  // four warps of a warpgroup change theirs together
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+  }
+  if (warp < 8) {
+    // --------------------------------------------------------------- softmax
+    while (next_list()) {
+      const int x = group;
+      const int row = (warp & 3) * 32 + lane;
+      const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+      const uint32_t s_at = tmem + lanes + x * 128, o_at = tmem + lanes + 256 + x * 128;
+      // (the Q loader has seen to the sign of the scale, and to 0)
+      const float sc = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
+      bool live = true;
+      for (int sg = 0; sg < share.nseg && live; ++sg) {
+        const ChunkSeg &g = share.seg[sg];
+        const int urow = kPair ? row : x * 128 + row;  // row of the unit
+        const bool active = kPair || x == 0 || g.nrows > 128;
+        if (!active) {
+          tiles_loaded += g.tile_hi - g.tile_lo;
+          continue;
+        }
+        const bool any_row = (kPair ? 0 : x * 128) + (warp & 3) * 32 < g.nrows;
+        const int t = g.len - g.n + (g.r0 + min(urow, g.nrows - 1)) / a.G;
+        float m = -INFINITY, l = 0.f;
+        bool begun = false;
+        for (int tile = g.tile_lo + (kPair ? x : 0); tile < g.tile_hi; tile += kPair ? 2 : 1) {
+          if (!wait(smem_u32(&ctl.s_full[x]), s_ph)) {
+            live = false;
+            break;
+          }
+          s_ph ^= 1;
+          // the product of the tile before (it came before this tile's scores)
+          if (begun && !wait(smem_u32(&ctl.o_done[x]), o_ph ^ 1)) {
+            live = false;
+            break;
+          }
+          const uint32_t seq = tiles_loaded + (uint32_t)(tile - g.tile_lo);
+          if (any_row) {
+            tc_fence_after();
+            float s[128];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, s + 32 * c);
+            tc_wait_ld();
+            const int tok0 = tile * kTile;
+            int hi = vis_hi(t, tok0), lo = vis_lo(t, tok0, a.window);
+            const uint32_t bad = ctl.bad[seq & 7];
+            if (!__all_sync(0xFFFFFFFFu, hi >= kTile - 1 && lo <= 0) || bad) {
+              int span = hi - lo;
+              if (span < 0) {
+                lo = kTile;
+                span = 0;
+              }
+#pragma unroll
+              for (int c = 0; c < 128; ++c) {
+                const bool see = (uint32_t)(c - lo) <= (uint32_t)span && !((bad >> (c >> 4)) & 1);
+                s[c] = see ? s[c] : -INFINITY;
+              }
+            }
+            float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
+#pragma unroll
+            for (int c = 4; c < 128; c += 4) {
+              mx0 = fmaxf(mx0, s[c]);
+              mx1 = fmaxf(mx1, s[c + 1]);
+              mx2 = fmaxf(mx2, s[c + 2]);
+              mx3 = fmaxf(mx3, s[c + 3]);
+            }
+            const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
+            // m = -inf: nothing seen so far (a difference of two -inf is NaN: no move)
+            const bool move = (mx - m) * sc > kMoveAt;
+            if (begun && __any_sync(0xFFFFFFFFu, move)) {
+              const float alpha = !move ? 1.f : m == -INFINITY ? 0.f : ex2((m - mx) * sc);
+              l *= alpha;
+#pragma unroll 1
+              for (int c = 0; c < kHeadDim; c += 32) {
+                float o[32];
+                tmem_ld32(o_at + c, o);
+                tc_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] *= alpha;
+                tmem_st32(o_at + c, o);
+              }
+            }
+            if (move) m = mx;
+            const float base = m == -INFINITY ? 0.f : m * sc - weight_bias<T>();
+            float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t p[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float p0 = ex2(fmaf(s[32 * c + 2 * i], sc, -base));
+                const float p1 = ex2(fmaf(s[32 * c + 2 * i + 1], sc, -base));
+                sum0 += p0;
+                sum1 += p1;
+                p[i] = pack2(p0, p1, T{});
+              }
+              tmem_st16(s_at + 16 * c, p);
+            }
+            l += sum0 + sum1;
+            tc_wait_st();
+            tc_fence_before();
+          }
+          begun = true;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&ctl.p_full[x]));
+          // the product of this tile, for the wait after the last one
+          o_ph ^= 1;
+        }
+        if (!live) break;
+        tiles_loaded += g.tile_hi - g.tile_lo;
+        if (begun && !wait(smem_u32(&ctl.o_done[x]), o_ph ^ 1)) {
+          live = false;
+          break;
+        }
+        tc_fence_after();
+        float M = m == -INFINITY ? -INFINITY : m * sc - weight_bias<T>();
+        const bool whole = g.whole();
+        const int pr = g.r0 + min(urow, g.nrows - 1);
+        T *out = static_cast<T *>(a.out) +
+                 ((long long)(g.q0 + pr / a.G) * a.Hq + g.kvh * a.G + pr % a.G) * kHeadDim;
+        float *part = nullptr;
+        long long prow = 0;
+        if (!whole) {
+          prow = (long long)part_slot(g) * a.slot_rows + min(urow, g.nrows - 1);
+          part = a.part_o + prow * kHeadDim;
+        }
+        float f0 = 1.f, f1 = 0.f;
+        constexpr int kCols = kPair ? 64 : 128;  // channels this thread writes
+        const int c0 = kPair ? 64 * x : 0;
+        const bool second = kPair && g.tile_hi - g.tile_lo > 1;
+        if constexpr (kPair) {
+          // both groups hold part of every row: each writes half the channels
+          ctl.ml[x][row] = make_float2(M, l);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&ctl.joined));
+          if (!wait(smem_u32(&ctl.joined), j_ph)) {
+            live = false;
+            break;
+          }
+          tc_fence_after();
+          const float2 u = ctl.ml[0][row], v = ctl.ml[1][row];
+          M = fmaxf(u.x, v.x);
+          const float b = M == -INFINITY ? 0.f : M;
+          f0 = ex2(u.x - b);
+          f1 = ex2(v.x - b);
+          l = u.y * f0 + v.y * f1;
+        }
+        if (any_row) {
+          const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+          f0 *= inv;
+          f1 *= inv;
+          const uint32_t o0 = tmem + lanes + 256 + (kPair ? 0 : x * 128) + c0;
+#pragma unroll
+          for (int c = 0; c < kCols; c += 32) {
+            float o[32];
+            tmem_ld32(o0 + c, o);
+            tc_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = f0 == 0.f ? 0.f : o[i] * f0;
+            if (second) {
+              float o1[32];
+              tmem_ld32(o0 + 128 + c, o1);
+              tc_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] += f1 == 0.f ? 0.f : o1[i] * f1;
+            }
+            if (urow < g.nrows) {
+              if (whole) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 8)
+                  *reinterpret_cast<uint4 *>(out + c0 + c + i) = make_uint4(
+                      pack2(o[i], o[i + 1], T{}), pack2(o[i + 2], o[i + 3], T{}),
+                      pack2(o[i + 4], o[i + 5], T{}), pack2(o[i + 6], o[i + 7], T{}));
+              } else {
+#pragma unroll
+                for (int i = 0; i < 32; i += 4)
+                  *reinterpret_cast<float4 *>(part + c0 + c + i) =
+                      make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+              }
+            }
+          }
+          if (urow < g.nrows) {
+            if (!whole && (!kPair || x == 0)) {
+              a.part_ml[2 * prow] = M;
+              a.part_ml[2 * prow + 1] = l;
+            }
+            if (*reinterpret_cast<volatile int *>(&ctl.poison))
+              poison_row<T>(a, g, t, c0, c0 + kCols, out, part);
+          }
+          tc_fence_before();
+        }
+        if constexpr (kPair) {
+          // O may be overwritten once both groups have read it
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&ctl.read));
+          if (!wait(smem_u32(&ctl.read), j_ph)) {
+            live = false;
+            break;
+          }
+          j_ph ^= 1;
+        }
+      }
+    }
+  } else if (warp == 8) {
+    // ---------------------------------------------------------------- loader
+    while (next_list()) {
+      const int npg = kTile / a.ps;
+      const int rows_total = (int)(a.nphys * a.Hkv * a.ps);
+      bool live = true;
+      for (int sg = 0; sg < share.nseg && live; ++sg) {
+        const ChunkSeg &g = share.seg[sg];
+        for (int tile = g.tile_lo; tile < g.tile_hi; ++tile, ++tiles_loaded) {
+          int y = rows_total;  // past the end: the copy fills zeros
+          uint32_t bad = 0;
+          if (lane < npg) {
+            const int page = tile * npg + lane;
+            if ((long long)page * a.ps < g.len) {
+              const int ph = a.bt[(long long)g.b * a.maxP + page];
+              if (ph >= 0 && ph < a.nphys) {
+                y = (ph * a.Hkv + g.kvh) * a.ps;
+              } else {
+                flag_error(a.status, KV_ERR_BOUNDS);
+                bad = ((1u << (a.ps / 16)) - 1u) << (lane * (a.ps / 16));
+              }
+            }
+          }
+          bad = __reduce_or_sync(0xFFFFFFFFu, bad);
+          for (int w = 0; w < 2; ++w, ld.next()) {
+            if (!wait(smem_u32(&ctl.empty[ld.s]), ld.ph ^ 1)) {
+              live = false;
+              break;
+            }
+            if ((int)tiles_loaded == a.debug_skip_tile) continue;
+            const uint32_t bar = smem_u32(&ctl.full[ld.s]);
+            if (lane == 0) {
+              if (w == 0) ctl.bad[tiles_loaded & 7] = (uint8_t)bad;
+              mbar_arrive_expect_tx(bar, kTileBytes);
+            }
+            __syncwarp();
+            if (lane < npg) {
+              const uint32_t dst = smem_u32(ring) + ld.s * kTileBytes + lane * a.ps * 128;
+              const CUtensorMap *map = w ? &tv : &tk;
+              tma_load_2d(dst, map, 0, y, bar);
+              tma_load_2d(dst + kSlab, map, 64, y, bar);
+            }
+          }
+          if (!live) break;
+        }
+      }
+    }
+  } else if (warp == 9) {
+    // -------------------------------------------------------------- products
+    while (next_list()) {
+      if (lane == 0) {
+        constexpr uint32_t id_qk = umma_idesc<T>(128, 128, false);
+        constexpr uint32_t id_pv = umma_idesc<T>(128, 128, true);
+        struct Cur {
+          int sg, tile;
+        };
+        Cur c{0, share.seg[0].tile_lo}, p = c;
+        const int nseg = share.nseg;
+        auto active = [&](int x, const Cur &u) {
+          const ChunkSeg &g = share.seg[u.sg];
+          return x == 0 || (kPair ? u.tile + 1 < g.tile_hi : g.nrows > 128);
+        };
+        auto advance = [&](Cur &u, Ring<kStages> &r) {
+          const int step = kPair && active(1, u) ? 2 : 1;
+          r.next(2 * step);
+          u.tile += step;
+          if (u.tile >= share.seg[u.sg].tile_hi) {
+            ++u.sg;
+            u.tile = u.sg < nseg ? share.seg[u.sg].tile_lo : 0;
+          }
+        };
+        auto issue_qk = [&](int x) -> bool {
+          const ChunkSeg &g = share.seg[c.sg];
+          const int qx = kPair ? 0 : x;
+          Ring<kStages> r = qk;
+          if (kPair) r.next(2 * x);
+          if (c.tile == g.tile_lo && (!kPair || x == 0)) {
+            if (!wait(smem_u32(&ctl.q_full[qx]), (q_ph >> qx) & 1)) return false;
+            q_ph ^= 1u << qx;
+          }
+          if (!wait(smem_u32(&ctl.full[r.s]), r.ph)) return false;
+          tc_fence_after();
+          const uint32_t qa = smem_u32(q_area) + qx * kTileBytes;
+          const uint32_t ka = smem_u32(ring) + r.s * kTileBytes;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t off = (k >> 2) * kSlab + (k & 3) * 32;
+            umma_ss(tmem + x * 128, umma_desc(qa + off, 16, 1024), umma_desc(ka + off, 16, 1024),
+                    id_qk, k > 0);
+          }
+          tc_commit(smem_u32(&ctl.s_full[x]));
+          const int tile = c.tile + (kPair ? x : 0);
+          if ((kPair || x == 0) && needs_mend(mend_of(a, g, tile))) mbar_arrive(smem_u32(&ctl.mend[x]));
+          if (tile + 1 == g.tile_hi) tc_commit(smem_u32(&ctl.q_free[qx]));
+          if (kPair || x == 1 || g.nrows <= 128) tc_commit(smem_u32(&ctl.empty[r.s]));
+          return true;
+        };
+        auto issue_pv = [&](int x) -> bool {
+          const ChunkSeg &g = share.seg[p.sg];
+          Ring<kStages> r = pv;
+          r.next(1 + (kPair ? 2 * x : 0));
+          if (kPair || x == 0) {
+            if (!wait(smem_u32(&ctl.full[r.s]), r.ph)) return false;
+            if (needs_mend(mend_of(a, g, p.tile + (kPair ? x : 0)))) {
+              if (!wait(smem_u32(&ctl.mended[x]), (mend_ph >> x) & 1)) return false;
+              mend_ph ^= 1u << x;
+            }
+          }
+          if (!wait(smem_u32(&ctl.p_full[x]), (p_ph >> x) & 1)) return false;
+          p_ph ^= 1u << x;
+          tc_fence_after();
+          const uint32_t va = smem_u32(ring) + r.s * kTileBytes;
+          const bool add = p.tile > g.tile_lo;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            umma_ts(tmem + 256 + x * 128, tmem + x * 128 + k * 8,
+                    umma_desc(va + k * 2048, kSlab, 1024), id_pv, add || k > 0);
+          tc_commit(smem_u32(&ctl.o_done[x]));
+          if (kPair || x == 1 || g.nrows <= 128) tc_commit(smem_u32(&ctl.empty[r.s]));
+          return true;
+        };
+        bool live = issue_qk(0) && (!active(1, c) || issue_qk(1));
+        if (live) advance(c, qk);
+        while (live && p.sg < nseg) {
+          // the next tile's scores follow at once, but those of a new unit
+          // only behind this tile's products: they wait for its Q
+          const bool more = c.sg < nseg, same = more && c.sg == p.sg;
+          live = issue_pv(0);
+          if (live && same) live = issue_qk(0);
+          if (live && active(1, p)) live = issue_pv(1);
+          if (live && same && active(1, c)) live = issue_qk(1);
+          if (live && more && !same) live = issue_qk(0) && (!active(1, c) || issue_qk(1));
+          if (more) advance(c, qk);
+          advance(p, pv);
+        }
+      }
+      __syncwarp();
+    }
+  } else if (warp == 10) {
+    // ---------------------------------------------------------------- mender
+    while (next_list()) {
+      bool live = true;
+      for (int sg = 0; sg < share.nseg && live; ++sg) {
+        const ChunkSeg &g = share.seg[sg];
+        for (int tile = g.tile_lo; tile < g.tile_hi; ++tile, ld.next(2)) {
+          const Mend m = mend_of(a, g, tile);
+          if (!needs_mend(m)) continue;
+          Ring<kStages> r = ld;
+          r.next();
+          // the product warp asks when it has issued the tile's scores: then
+          // the copy of this V is the slot's current or last one
+          const int x = kPair ? (tile - g.tile_lo) & 1 : 0;
+          if (!wait(smem_u32(&ctl.mend[x]), (mend_ph >> x) & 1) ||
+              !wait(smem_u32(&ctl.full[r.s]), r.ph)) {
+            live = false;
+            break;
+          }
+          mend_ph ^= 1u << x;
+          uint8_t *v = ring + r.s * kTileBytes;
+          for (int i = lane; i < (m.zero_hi - m.zero_lo) * 16; i += 32) {
+            const int tok = m.zero_lo + (i >> 4), ch = i & 15;
+            *reinterpret_cast<uint4 *>(v + (ch >> 3) * kSlab + swz(tok, ch & 7)) =
+                make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll 8
+          for (int i = lane; i < m.scan * 16; i += 32) {
+            // 16 bytes of a row; where in the row does not matter here
+            uint4 *at = reinterpret_cast<uint4 *>(v + (i & 1 ? kSlab : 0)) + (i >> 1);
+            const uint4 w = *at;
+            constexpr uint32_t M = NonFinite<T>::kMask, O = NonFinite<T>::kOne;
+            const uint32_t any = (((w.x & M) + O) | ((w.y & M) + O) | ((w.z & M) + O) |
+                                  ((w.w & M) + O)) & 0x80008000u;
+            if (any) {
+              uint32_t u[4] = {w.x, w.y, w.z, w.w};
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t b = ((u[k] & M) + O) & 0x80008000u;
+                if (b & 0x8000u) u[k] &= 0xFFFF0000u;
+                if (b & 0x80000000u) u[k] &= 0x0000FFFFu;
+              }
+              *at = make_uint4(u[0], u[1], u[2], u[3]);
+              *reinterpret_cast<volatile int *>(&ctl.poison) = 1;
+            }
+          }
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&ctl.mended[x]));
+        }
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- Q loader
+    while (next_list()) {
+      bool live = true;
+      for (int sg = 0; sg < share.nseg && live; ++sg) {
+        const ChunkSeg &g = share.seg[sg];
+        for (int x = 0; x < Sh::kQTiles && x * 128 < g.nrows; ++x) {
+          if ((q_uses >> x) & 1) {
+            if (!wait(smem_u32(&ctl.q_free[x]), (q_ph >> x) & 1)) {
+              live = false;
+              break;
+            }
+            q_ph ^= 1u << x;
+          }
+          q_uses |= 1u << x;
+          uint8_t *q = q_area + x * kTileBytes;
+          const int ch = lane & 15;
+          int r = lane >> 4;
+          const int pr = g.r0 + x * 128 + r;
+          int tok = pr / a.G, hd = pr % a.G;
+          const int left = g.nrows - x * 128;
+          for (; r < 128; r += 2) {
+            uint8_t *dst = q + (ch >> 3) * kSlab + swz(r, ch & 7);
+            if (r < left) {
+              const T *src = static_cast<const T *>(a.q) +
+                             ((long long)(g.q0 + tok) * a.Hq + g.kvh * a.G + hd) * kHeadDim;
+              if (a.scale_log2 > 0.f) {
+                cp_async16(smem_u32(dst), src + ch * 8);
+              } else {  // a negative scale turns q, a zero one clears it
+                uint4 w = *reinterpret_cast<const uint4 *>(src + ch * 8);
+                const uint32_t flip = 0x80008000u, keep = a.scale_log2 < 0.f ? ~0u : 0u;
+                *reinterpret_cast<uint4 *>(dst) =
+                    make_uint4((w.x ^ flip) & keep, (w.y ^ flip) & keep, (w.z ^ flip) & keep,
+                               (w.w ^ flip) & keep);
+              }
+            } else if (r < 128) {
+              *reinterpret_cast<uint4 *>(dst) = make_uint4(0, 0, 0, 0);
+            }
+            hd += 2;
+            while (hd >= a.G) {
+              hd -= a.G;
+              ++tok;
+            }
+          }
+          cp_async_wait_all();
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&ctl.q_full[x]));
+        }
+      }
+    }
+  }
+  pdl_trigger();
+  if (ctl.abort) {
+    // leave no copy and no product in flight: every slot's last copy (slots
+    // before ld.s were filled in this lap of the ring, the others in the one
+    // before), and a last commit
+    if (warp == 8) {
+      for (int i = 0; i < kStages; ++i)
+        mbar_wait(smem_u32(&ctl.full[i]), i < ld.s ? ld.ph : ld.ph ^ 1, a.wait_limit_ns);
+    }
+    if (warp == 9 && lane == 0) {
+      tc_commit(smem_u32(&ctl.drain));
+      mbar_wait(smem_u32(&ctl.drain), 0, a.wait_limit_ns);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_free(tmem, kTmemCols);
+  }
+}
+
+template <class T, bool kPair>
+cudaError_t mma_go(const ChunkArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
+                   cudaStream_t st) {
+  constexpr int bytes = Shape<kPair>::kTileArea + (int)sizeof(Control<kPair>);
+  const cudaError_t e = cudaFuncSetAttribute(
+      chunk_mma_kernel<T, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(chunk_mma_kernel<T, kPair>, dim3(ctas), dim3(kThreads), bytes, st, a, tk, tv);
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_mma(int dtype, bool pair, const ChunkArgs &a, const CUtensorMap &tk,
+                             const CUtensorMap &tv, int ctas, cudaStream_t st) {
+  if (dtype == KV_F16)
+    return pair ? mma_go<__half, true>(a, tk, tv, ctas, st)
+                : mma_go<__half, false>(a, tk, tv, ctas, st);
+  return pair ? mma_go<__nv_bfloat16, true>(a, tk, tv, ctas, st)
+              : mma_go<__nv_bfloat16, false>(a, tk, tv, ctas, st);
+}
+
+}  // namespace kvs

@@ -80,8 +80,13 @@ cudaError_t launch_combine_lists(const float *part_o, const float *part_ml, cons
 // the chunk operators (kv_chunk.cuh): rows = packed rows per unit, ctas = the
 // shares the work is cut into
 struct ChunkArgs;
-cudaError_t launch_chunk_core(int dtype, const ChunkArgs &a, bool q8, int rows, int ctas,
-                              cudaStream_t st);
+cudaError_t launch_chunk_core(const ChunkArgs &a, bool q8, int rows, int ctas, cudaStream_t st);
+// 16-bit data on the tensor cores; pair: units of at most 128 rows
+cudaError_t launch_chunk_mma(int dtype, bool pair, const ChunkArgs &a, const CUtensorMap &tk,
+                             const CUtensorMap &tv, int ctas, cudaStream_t st);
+// the pages it needs into device memory in 16 bits (table: their new block table, or null)
+cudaError_t launch_chunk_stage(int dtype, bool q8, const ChunkArgs &c, void *k_out, void *v_out,
+                               int32_t *table, cudaStream_t st);
 cudaError_t launch_chunk_combine(int dtype, const ChunkArgs &a, int ctas, cudaStream_t st);
 // the 8-bit cache (device-visible addresses)
 cudaError_t launch_q8_append(int dtype, const void *k_new, const void *v_new,

@@ -11,6 +11,7 @@
 // so memory bounds them; a decode step's append is bounded by latency.
 #include <algorithm>
 
+#include "kv_chunk.cuh"
 #include "kv_launch.h"
 #include "kv_q8.cuh"
 
@@ -198,7 +199,122 @@ __global__ void __launch_bounds__(kThreads) q8_read_kernel(const ReadArgs a, lon
   }
 }
 
+// Pages a chunk attention needs, brought into device memory in 16 bits:
+// from the 8-bit cache, or from one in host memory.  Item and lanes as above.
+struct StageArgs {
+  const void *src[2];  // K, V: 16-bit data or codes
+  const uint8_t *scale[2];
+  void *out[2];
+  const int32_t *q_start, *bt, *ctx;
+  int32_t *table;  // [B][maxP] page in out, or null: the source's own page numbers
+  int *status;
+  long long nphys;
+  int Hkv, ps, maxP, tiles, total_q, max_q_len, window;
+};
+template <class T, bool Q8>
+__global__ void __launch_bounds__(kThreads) stage_kernel(const StageArgs a, long long items) {
+  pdl_wait();
+  const int t = threadIdx.x / kLanesPerVec, l = threadIdx.x % kLanesPerVec;
+  uint4 data[kUnits][2];  // 16-bit data, or the codes in the first half
+  uint32_t byte[kUnits][2];
+  long long dst[kUnits];
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) {
+    const long long it = (long long)blockIdx.x * kUnits + u;
+    dst[u] = -1;
+    if (it >= items) continue;
+    const int h = (int)(it % a.Hkv);
+    const long long bt_tile = it / a.Hkv;
+    const int tile = (int)(bt_tile % a.tiles), b = (int)(bt_tile / a.tiles);
+    const int tok0 = tile * kTileTokens, pos = tok0 + t, page = tok0 / a.ps;
+    const int q0 = a.q_start[b], q1 = a.q_start[b + 1], len = a.ctx[b];
+    // sequences the attention skips (and records), and tokens no row sees
+    if (q0 < 0 || q1 <= q0 || q1 > a.total_q || q1 - q0 > a.max_q_len || len < 0 ||
+        (long long)len > (long long)a.maxP * a.ps || tok0 >= len)
+      continue;
+    if (a.window > 0 &&
+        (long long)(tok0 / kChunkTile + 1) * kChunkTile <= (long long)len - (q1 - q0) - a.window + 1)
+      continue;
+    const long long row = (long long)b * a.maxP + page;
+    const int src = a.bt[row];
+    const bool ok = src >= 0 && src < a.nphys;
+    if (a.table && h == 0 && threadIdx.x == 0 && tok0 % a.ps == 0)
+      a.table[row] = ok ? (int32_t)row : -1;
+    if (!ok || pos >= len) continue;
+    const long long in = ((long long)src * a.Hkv + h) * a.ps + pos % a.ps;
+    dst[u] = a.table ? (row * a.Hkv + h) * a.ps + pos % a.ps : in;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      if constexpr (Q8) {
+        const uint2 c = *reinterpret_cast<const uint2 *>(
+            static_cast<const uint8_t *>(a.src[w]) + in * kHeadDim + l * 8);
+        data[u][w] = make_uint4(c.x, c.y, 0, 0);
+        byte[u][w] = a.scale[w][in];
+      } else {
+        data[u][w] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.src[w]) +
+                                                      in * kHeadDim + l * 8);
+      }
+    }
+  }
+  pdl_trigger();
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) {
+    if (dst[u] < 0) continue;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      T *to = static_cast<T *>(a.out[w]) + dst[u] * kHeadDim + l * 8;
+      if constexpr (Q8) {
+        float lo[4], hi[4], x[8];
+        q8_unpack4(data[u][w].x, lo);
+        q8_unpack4(data[u][w].y, hi);
+        const float s = q8_scale(byte[u][w]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          x[c] = lo[c] * s;
+          x[4 + c] = hi[c] * s;
+        }
+        store8(to, x);
+      } else {
+        *reinterpret_cast<uint4 *>(to) = data[u][w];
+      }
+    }
+  }
+}
+
 }  // namespace
+
+cudaError_t launch_chunk_stage(int dtype, bool q8, const ChunkArgs &c, void *k_out, void *v_out,
+                               int32_t *table, cudaStream_t st) {
+  StageArgs a = {};
+  a.src[0] = c.k;
+  a.src[1] = c.v;
+  a.scale[0] = c.k_scale;
+  a.scale[1] = c.v_scale;
+  a.out[0] = k_out;
+  a.out[1] = v_out;
+  a.q_start = c.q_start;
+  a.bt = c.bt;
+  a.ctx = c.ctx;
+  a.table = table;
+  a.status = c.status;
+  a.nphys = c.nphys;
+  a.Hkv = c.Hkv;
+  a.ps = c.ps;
+  a.maxP = c.maxP;
+  a.tiles = (int)((long long)c.maxP * c.ps / kTileTokens);
+  a.total_q = c.total_q;
+  a.max_q_len = c.max_q_len;
+  a.window = c.window;
+  const long long items = (long long)c.B * a.tiles * a.Hkv;
+  const long long blocks = (items + kUnits - 1) / kUnits;
+  if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
+  const dim3 grid((unsigned)blocks), block(kThreads);
+  if (dtype == KV_F16)
+    return q8 ? launch_pdl(stage_kernel<__half, true>, grid, block, 0, st, a, items)
+              : launch_pdl(stage_kernel<__half, false>, grid, block, 0, st, a, items);
+  return q8 ? launch_pdl(stage_kernel<__nv_bfloat16, true>, grid, block, 0, st, a, items)
+            : launch_pdl(stage_kernel<__nv_bfloat16, false>, grid, block, 0, st, a, items);
+}
 
 cudaError_t launch_q8_append(int dtype, const void *k_new, const void *v_new,
                              const kv_q8_cache &c, const int32_t *q_start, const int32_t *bt,

@@ -295,3 +295,21 @@ def test_the_path_together(dtype):
     kv.kv_dense_decode_attn(p.shape, q.cuda(), back[0], back[1], p.d_table, ctx, p.scale, out, ws,
                             ws.numel(), st)
     check(out, want, tol + 2e-5)
+
+
+@pytest.mark.parametrize("q8", [False, True], ids=["own", "q8"])
+@pytest.mark.parametrize("news", [[3, 1], [90, 200]])
+def test_a_wait_that_runs_out_is_reported(news, q8):
+    """A K/V tile that is never filled (the testing hook): the bounded waits give
+    up, the status says so, and the next call is exact."""
+    p = Problem("bf16", 8, 2, 16, [700, 300], news, q8=q8).upload()
+    kv.kv_debug_config(0, 2_000_000)
+    try:
+        p.attend()
+        assert kv.kv_device_status() == kv.KV_ERR_DEVICE_TIMEOUT
+    finally:
+        kv.kv_debug_config(-1, 2_000_000_000)
+    p.d_out.fill_(7)
+    p.attend()
+    torch.cuda.synchronize()
+    check(p.d_out, *p.expected())
