@@ -18,6 +18,8 @@
 // sequence and many short ones are balanced by the same rule to one tile.
 #pragma once
 
+#include <climits>
+
 #include "kv_internal.cuh"
 
 namespace kvs {
@@ -75,6 +77,9 @@ struct ChunkSeg {
   int tile_lo, tile_hi;   // the KV tiles of this segment
   int parts;              // bit 0: it holds the unit's first tile, bit 1: its last
   int t_first, t_last;    // tokens of the unit's first and last row
+  // KV tiles in which some row does not see some token, or that end behind the
+  // sequence inside a page: those >= edge_from and those <= edge_upto
+  int edge_from, edge_upto;
   __device__ __forceinline__ bool first() const { return parts & 1; }
   __device__ __forceinline__ bool whole() const { return parts == 3; }
 };
@@ -207,6 +212,10 @@ __device__ __forceinline__ void share_next(const ChunkArgs &a, int rows, int til
       g.parts = (off == 0 ? 1 : 0) | (take == have ? 2 : 0);
       g.t_first = s.len - s.n + r0 / a.G;
       g.t_last = s.len - s.n + (r0 + nrows - 1) / a.G;
+      g.edge_from = g.t_first < s.len - 1        ? max(g.t_first + 1, 0) / tile
+                    : (s.len & (a.ps - 1)) != 0 ? s.len / tile
+                                                : INT_MAX;
+      g.edge_upto = a.window > 0 && g.t_last >= a.window ? (g.t_last - a.window) / tile : -1;
       if (g.parts == 1) {
         // the CTA whose share holds the unit's last tile
         const long long end = sh->hi - left + (t.hi - t.lo) - 1;

@@ -66,7 +66,7 @@ template <bool kPair> struct Control {
   int poison;     // a non-finite V was zeroed in some tile
   int pad;
   uint8_t bad[8];  // per tile, bit i: tokens 16 i .. + 15 have no page
-  ChunkShare<kPair ? 12 : 40> share;
+  ChunkShare<kPair ? 10 : 32> share;
   union {
     long long red[33];                // share_init
     float2 ml[2][kPair ? 128 : 1];   // kPair: maximum and sum of each group's rows
@@ -122,8 +122,8 @@ __device__ __forceinline__ Mend mend_of(const ChunkArgs &a, const ChunkSeg &g, i
     m.scan = valid;
   return m;
 }
-__device__ __forceinline__ bool needs_mend(const Mend &m) {
-  return m.scan > 0 || m.zero_hi > m.zero_lo;
+__device__ __forceinline__ bool at_edge(const ChunkSeg &g, int tile) {
+  return tile >= g.edge_from || tile <= g.edge_upto;
 }
 
 // the exponent field, and what carries out of it when it is all ones
@@ -251,8 +251,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (the Q loader has seen to the sign of the scale, and to 0)
       const float sc = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
       bool live = true;
-      for (int sg = 0; sg < share.nseg && live; ++sg) {
-        const ChunkSeg &g = share.seg[sg];
+      const int nseg = share.nseg;
+      for (int sg = 0; sg < nseg && live; ++sg) {
+        const ChunkSeg g = share.seg[sg];
         const int urow = kPair ? row : x * 128 + row;  // row of the unit
         const bool active = kPair || x == 0 || g.nrows > 128;
         if (!active) {
@@ -298,13 +299,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
 #pragma unroll
-            for (int c = 4; c < 128; c += 4) {
-              mx0 = fmaxf(mx0, s[c]);
-              mx1 = fmaxf(mx1, s[c + 1]);
-              mx2 = fmaxf(mx2, s[c + 2]);
-              mx3 = fmaxf(mx3, s[c + 3]);
+            for (int c = 4; c < 124; c += 8) {
+              mx0 = max3(mx0, s[c], s[c + 1]);
+              mx1 = max3(mx1, s[c + 2], s[c + 3]);
+              mx2 = max3(mx2, s[c + 4], s[c + 5]);
+              mx3 = max3(mx3, s[c + 6], s[c + 7]);
             }
-            const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
+            mx0 = max3(mx0, s[124], s[125]);
+            mx1 = max3(mx1, s[126], s[127]);
+            const float mx = fmaxf(max3(mx0, mx1, mx2), mx3);
             // m = -inf: nothing seen so far (a difference of two -inf is NaN: no move)
             const bool move = (mx - m) * sc > kMoveAt;
             if (begun && __any_sync(0xFFFFFFFFu, move)) {
@@ -322,20 +325,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (move) m = mx;
             const float base = m == -INFINITY ? 0.f : m * sc - weight_bias<T>();
-            float sum0 = 0.f, sum1 = 0.f;
+            const uint64_t sc2 = f2_pack(sc, sc), base2 = f2_pack(-base, -base);
+            uint64_t sum2 = 0, sum2b = 0;  // pairs of zeros
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               uint32_t p[16];
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
-                const float p0 = ex2(fmaf(s[32 * c + 2 * i], sc, -base));
-                const float p1 = ex2(fmaf(s[32 * c + 2 * i + 1], sc, -base));
-                sum0 += p0;
-                sum1 += p1;
+                float p0, p1;
+                f2_unpack(f2_fma(f2_pack(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), sc2, base2),
+                          p0, p1);
+                p0 = ex2(p0);
+                p1 = ex2(p1);
+                if (i & 1) sum2b = f2_add(sum2b, f2_pack(p0, p1));
+                else sum2 = f2_add(sum2, f2_pack(p0, p1));
                 p[i] = pack2(p0, p1, T{});
               }
               tmem_st16(s_at + 16 * c, p);
             }
+            float sum0, sum1;
+            f2_unpack(f2_add(sum2, sum2b), sum0, sum1);
             l += sum0 + sum1;
             tc_wait_st();
             tc_fence_before();
@@ -426,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               a.part_ml[2 * prow + 1] = l;
             }
             if (*reinterpret_cast<volatile int *>(&ctl.poison))
-              poison_row<T>(a, g, t, c0, c0 + kCols, out, part);
+              poison_row<T>(a, share.seg[sg], t, c0, c0 + kCols, out, part);
           }
           tc_fence_before();
         }
@@ -447,9 +456,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (next_list()) {
       const int npg = kTile / a.ps;
       const int rows_total = (int)(a.nphys * a.Hkv * a.ps);
+      const uint32_t full0 = smem_u32(&ctl.full[0]), empty0 = smem_u32(&ctl.empty[0]);
       bool live = true;
-      for (int sg = 0; sg < share.nseg && live; ++sg) {
-        const ChunkSeg &g = share.seg[sg];
+      const int nseg = share.nseg;
+      for (int sg = 0; sg < nseg && live; ++sg) {
+        const ChunkSeg g = share.seg[sg];
         for (int tile = g.tile_lo; tile < g.tile_hi; ++tile, ++tiles_loaded) {
           int y = rows_total;  // past the end: the copy fills zeros
           uint32_t bad = 0;
@@ -467,12 +478,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           bad = __reduce_or_sync(0xFFFFFFFFu, bad);
           for (int w = 0; w < 2; ++w, ld.next()) {
-            if (!wait(smem_u32(&ctl.empty[ld.s]), ld.ph ^ 1)) {
+            if (!wait(empty0 + 8 * ld.s, ld.ph ^ 1)) {
               live = false;
               break;
             }
             if ((int)tiles_loaded == a.debug_skip_tile) continue;
-            const uint32_t bar = smem_u32(&ctl.full[ld.s]);
+            const uint32_t bar = full0 + 8 * ld.s;
             if (lane == 0) {
               if (w == 0) ctl.bad[tiles_loaded & 7] = (uint8_t)bad;
               mbar_arrive_expect_tx(bar, kTileBytes);
@@ -495,72 +506,91 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         constexpr uint32_t id_qk = umma_idesc<T>(128, 128, false);
         constexpr uint32_t id_pv = umma_idesc<T>(128, 128, true);
+        // a position in the list, with what is needed of its segment in registers
         struct Cur {
-          int sg, tile;
+          int sg, tile, lo, hi, from, upto;
+          bool two;
         };
-        Cur c{0, share.seg[0].tile_lo}, p = c;
         const int nseg = share.nseg;
-        auto active = [&](int x, const Cur &u) {
+        auto enter = [&](Cur &u) {
+          if (u.sg >= nseg) return;
           const ChunkSeg &g = share.seg[u.sg];
-          return x == 0 || (kPair ? u.tile + 1 < g.tile_hi : g.nrows > 128);
+          u.tile = u.lo = g.tile_lo;
+          u.hi = g.tile_hi;
+          u.from = g.edge_from;
+          u.upto = g.edge_upto;
+          u.two = g.nrows > 128;
         };
+        Cur c;
+        c.sg = 0;
+        enter(c);
+        Cur p = c;
+        auto active = [&](int x, const Cur &u) {
+          return x == 0 || (kPair ? u.tile + 1 < u.hi : u.two);
+        };
+        auto edge = [&](const Cur &u, int tile) { return tile >= u.from || tile <= u.upto; };
         auto advance = [&](Cur &u, Ring<kStages> &r) {
           const int step = kPair && active(1, u) ? 2 : 1;
           r.next(2 * step);
           u.tile += step;
-          if (u.tile >= share.seg[u.sg].tile_hi) {
+          if (u.tile >= u.hi) {
             ++u.sg;
-            u.tile = u.sg < nseg ? share.seg[u.sg].tile_lo : 0;
+            enter(u);
           }
         };
+        const uint32_t full0 = smem_u32(&ctl.full[0]), empty0 = smem_u32(&ctl.empty[0]);
+        const uint32_t s_full0 = smem_u32(&ctl.s_full[0]), p_full0 = smem_u32(&ctl.p_full[0]);
+        const uint32_t o_done0 = smem_u32(&ctl.o_done[0]), mend0 = smem_u32(&ctl.mend[0]);
+        const uint32_t mended0 = smem_u32(&ctl.mended[0]);
+        const uint32_t q_full0 = smem_u32(&ctl.q_full[0]), q_free0 = smem_u32(&ctl.q_free[0]);
+        const uint64_t dq = umma_desc(smem_u32(q_area), 16, 1024);
+        const uint64_t dk = umma_desc(smem_u32(ring), 16, 1024);
+        const uint64_t dv = umma_desc(smem_u32(ring), kSlab, 1024);
         auto issue_qk = [&](int x) -> bool {
-          const ChunkSeg &g = share.seg[c.sg];
           const int qx = kPair ? 0 : x;
           Ring<kStages> r = qk;
           if (kPair) r.next(2 * x);
-          if (c.tile == g.tile_lo && (!kPair || x == 0)) {
-            if (!wait(smem_u32(&ctl.q_full[qx]), (q_ph >> qx) & 1)) return false;
+          if (c.tile == c.lo && (!kPair || x == 0)) {
+            if (!wait(q_full0 + 8 * qx, (q_ph >> qx) & 1)) return false;
             q_ph ^= 1u << qx;
           }
-          if (!wait(smem_u32(&ctl.full[r.s]), r.ph)) return false;
+          if (!wait(full0 + 8 * r.s, r.ph)) return false;
           tc_fence_after();
-          const uint32_t qa = smem_u32(q_area) + qx * kTileBytes;
-          const uint32_t ka = smem_u32(ring) + r.s * kTileBytes;
+          const uint64_t a0 = dq + (uint64_t)(qx * (kTileBytes >> 4));
+          const uint64_t b0 = dk + (uint64_t)(r.s * (kTileBytes >> 4));
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const uint32_t off = (k >> 2) * kSlab + (k & 3) * 32;
-            umma_ss(tmem + x * 128, umma_desc(qa + off, 16, 1024), umma_desc(ka + off, 16, 1024),
-                    id_qk, k > 0);
+            const uint64_t off = ((k >> 2) * kSlab + (k & 3) * 32) >> 4;
+            umma_ss(tmem + x * 128, a0 + off, b0 + off, id_qk, k > 0);
           }
-          tc_commit(smem_u32(&ctl.s_full[x]));
+          tc_commit(s_full0 + 8 * x);
           const int tile = c.tile + (kPair ? x : 0);
-          if ((kPair || x == 0) && needs_mend(mend_of(a, g, tile))) mbar_arrive(smem_u32(&ctl.mend[x]));
-          if (tile + 1 == g.tile_hi) tc_commit(smem_u32(&ctl.q_free[qx]));
-          if (kPair || x == 1 || g.nrows <= 128) tc_commit(smem_u32(&ctl.empty[r.s]));
+          if (tile + 1 == c.hi) tc_commit(q_free0 + 8 * qx);
+          if (kPair || x == 1 || !c.two) tc_commit(empty0 + 8 * r.s);
+          if ((kPair || x == 0) && edge(c, tile)) mbar_arrive(mend0 + 8 * x);
           return true;
         };
         auto issue_pv = [&](int x) -> bool {
-          const ChunkSeg &g = share.seg[p.sg];
           Ring<kStages> r = pv;
           r.next(1 + (kPair ? 2 * x : 0));
           if (kPair || x == 0) {
-            if (!wait(smem_u32(&ctl.full[r.s]), r.ph)) return false;
-            if (needs_mend(mend_of(a, g, p.tile + (kPair ? x : 0)))) {
-              if (!wait(smem_u32(&ctl.mended[x]), (mend_ph >> x) & 1)) return false;
+            if (!wait(full0 + 8 * r.s, r.ph)) return false;
+            if (edge(p, p.tile + (kPair ? x : 0))) {
+              if (!wait(mended0 + 8 * x, (mend_ph >> x) & 1)) return false;
               mend_ph ^= 1u << x;
             }
           }
-          if (!wait(smem_u32(&ctl.p_full[x]), (p_ph >> x) & 1)) return false;
+          if (!wait(p_full0 + 8 * x, (p_ph >> x) & 1)) return false;
           p_ph ^= 1u << x;
           tc_fence_after();
-          const uint32_t va = smem_u32(ring) + r.s * kTileBytes;
-          const bool add = p.tile > g.tile_lo;
+          const uint64_t b0 = dv + (uint64_t)(r.s * (kTileBytes >> 4));
+          const bool add = p.tile > p.lo;
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            umma_ts(tmem + 256 + x * 128, tmem + x * 128 + k * 8,
-                    umma_desc(va + k * 2048, kSlab, 1024), id_pv, add || k > 0);
-          tc_commit(smem_u32(&ctl.o_done[x]));
-          if (kPair || x == 1 || g.nrows <= 128) tc_commit(smem_u32(&ctl.empty[r.s]));
+            umma_ts(tmem + 256 + x * 128, tmem + x * 128 + k * 8, b0 + k * (2048 >> 4), id_pv,
+                    add || k > 0);
+          tc_commit(o_done0 + 8 * x);
+          if (kPair || x == 1 || !p.two) tc_commit(empty0 + 8 * r.s);
           return true;
         };
         bool live = issue_qk(0) && (!active(1, c) || issue_qk(1));
@@ -584,11 +614,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------------- mender
     while (next_list()) {
       bool live = true;
-      for (int sg = 0; sg < share.nseg && live; ++sg) {
-        const ChunkSeg &g = share.seg[sg];
+      const int nseg = share.nseg;
+      for (int sg = 0; sg < nseg && live; ++sg) {
+        const ChunkSeg g = share.seg[sg];
         for (int tile = g.tile_lo; tile < g.tile_hi; ++tile, ld.next(2)) {
+          if (!at_edge(g, tile)) continue;
           const Mend m = mend_of(a, g, tile);
-          if (!needs_mend(m)) continue;
           Ring<kStages> r = ld;
           r.next();
           // the product warp asks when it has issued the tile's scores: then
@@ -606,23 +637,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint4 *>(v + (ch >> 3) * kSlab + swz(tok, ch & 7)) =
                 make_uint4(0, 0, 0, 0);
           }
-#pragma unroll 8
-          for (int i = lane; i < m.scan * 16; i += 32) {
-            // 16 bytes of a row; where in the row does not matter here
-            uint4 *at = reinterpret_cast<uint4 *>(v + (i & 1 ? kSlab : 0)) + (i >> 1);
-            const uint4 w = *at;
-            constexpr uint32_t M = NonFinite<T>::kMask, O = NonFinite<T>::kOne;
-            const uint32_t any = (((w.x & M) + O) | ((w.y & M) + O) | ((w.z & M) + O) |
-                                  ((w.w & M) + O)) & 0x80008000u;
-            if (any) {
-              uint32_t u[4] = {w.x, w.y, w.z, w.w};
-              for (int k = 0; k < 4; ++k) {
-                const uint32_t b = ((u[k] & M) + O) & 0x80008000u;
-                if (b & 0x8000u) u[k] &= 0xFFFF0000u;
-                if (b & 0x80000000u) u[k] &= 0x0000FFFFu;
-              }
-              *at = make_uint4(u[0], u[1], u[2], u[3]);
+          // m.scan rows of 16 chunks of 16 bytes; where in the row a chunk
+          // sits does not matter here.  Eight loads before the first test.
+          constexpr uint32_t M = NonFinite<T>::kMask, O = NonFinite<T>::kOne;
+          for (int slab = 0; slab < 2; ++slab) {
+            uint4 *at = reinterpret_cast<uint4 *>(v + slab * kSlab);
+            const int chunks = m.scan * 8;
+            for (int i0 = lane; i0 < chunks; i0 += 256) {
+              uint4 w[8];
+              uint32_t any = 0;
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                w[k] = i0 + 32 * k < chunks ? at[i0 + 32 * k] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                any |= ((w[k].x & M) + O) | ((w[k].y & M) + O) | ((w[k].z & M) + O) |
+                       ((w[k].w & M) + O);
+              if (!(any & 0x80008000u)) continue;
               *reinterpret_cast<volatile int *>(&ctl.poison) = 1;
+#pragma unroll 1
+              for (int i = i0; i < min(chunks, i0 + 256); i += 32) {
+                uint32_t *u = reinterpret_cast<uint32_t *>(at + i);
+                for (int k = 0; k < 4; ++k) {
+                  const uint32_t b = ((u[k] & M) + O) & 0x80008000u;
+                  if (b & 0x8000u) u[k] &= 0xFFFF0000u;
+                  if (b & 0x80000000u) u[k] &= 0x0000FFFFu;
+                }
+              }
             }
           }
           fence_async_shared();
@@ -635,8 +676,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // -------------------------------------------------------------- Q loader
     while (next_list()) {
       bool live = true;
-      for (int sg = 0; sg < share.nseg && live; ++sg) {
-        const ChunkSeg &g = share.seg[sg];
+      const int nseg = share.nseg;
+      const int ch = lane & 15, half = lane >> 4;  // 16 bytes of row 2 i + half
+      for (int sg = 0; sg < nseg && live; ++sg) {
+        const ChunkSeg g = share.seg[sg];
         for (int x = 0; x < Sh::kQTiles && x * 128 < g.nrows; ++x) {
           if ((q_uses >> x) & 1) {
             if (!wait(smem_u32(&ctl.q_free[x]), (q_ph >> x) & 1)) {
@@ -646,33 +689,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             q_ph ^= 1u << x;
           }
           q_uses |= 1u << x;
-          uint8_t *q = q_area + x * kTileBytes;
-          const int ch = lane & 15;
-          int r = lane >> 4;
-          const int pr = g.r0 + x * 128 + r;
-          int tok = pr / a.G, hd = pr % a.G;
-          const int left = g.nrows - x * 128;
-          for (; r < 128; r += 2) {
-            uint8_t *dst = q + (ch >> 3) * kSlab + swz(r, ch & 7);
-            if (r < left) {
-              const T *src = static_cast<const T *>(a.q) +
-                             ((long long)(g.q0 + tok) * a.Hq + g.kvh * a.G + hd) * kHeadDim;
-              if (a.scale_log2 > 0.f) {
-                cp_async16(smem_u32(dst), src + ch * 8);
-              } else {  // a negative scale turns q, a zero one clears it
-                uint4 w = *reinterpret_cast<const uint4 *>(src + ch * 8);
-                const uint32_t flip = 0x80008000u, keep = a.scale_log2 < 0.f ? ~0u : 0u;
-                *reinterpret_cast<uint4 *>(dst) =
-                    make_uint4((w.x ^ flip) & keep, (w.y ^ flip) & keep, (w.z ^ flip) & keep,
-                               (w.w ^ flip) & keep);
+          const uint32_t q = smem_u32(q_area) + x * kTileBytes + (ch >> 3) * kSlab;
+          const int pr = g.r0 + x * 128 + half, left = g.nrows - x * 128;
+          int hd = pr % a.G;
+          const T *src = static_cast<const T *>(a.q) +
+                         ((long long)(g.q0 + pr / a.G) * a.Hq + g.kvh * a.G + hd) * kHeadDim +
+                         ch * 8;
+          const long long wrap = (long long)(a.Hq - a.G) * kHeadDim;  // to the next token's heads
+          for (int r = half; r < 128; r += 2) {
+            const uint32_t dst = q + swz(r, ch & 7);
+            if (r < left && a.scale_log2 > 0.f) {
+              cp_async16(dst, src);
+            } else {  // a negative scale turns q, a zero one clears it
+              uint4 w = make_uint4(0, 0, 0, 0);
+              if (r < left && a.scale_log2 < 0.f) {
+                w = *reinterpret_cast<const uint4 *>(src);
+                w = make_uint4(w.x ^ 0x80008000u, w.y ^ 0x80008000u, w.z ^ 0x80008000u,
+                               w.w ^ 0x80008000u);
               }
-            } else if (r < 128) {
-              *reinterpret_cast<uint4 *>(dst) = make_uint4(0, 0, 0, 0);
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w.x),
+                           "r"(w.y), "r"(w.z), "r"(w.w)
+                           : "memory");
             }
+            src += 2 * kHeadDim;
             hd += 2;
             while (hd >= a.G) {
               hd -= a.G;
-              ++tok;
+              src += wrap;
             }
           }
           cp_async_wait_all();
