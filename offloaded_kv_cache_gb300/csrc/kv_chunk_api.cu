@@ -38,9 +38,12 @@ int resolve_q8(const kv_shape *s, const kv_q8_cache *c, kv_q8_cache *dev) {
   return KV_OK;
 }
 
+#ifndef KVS_Q8_DIRECT_ROWS
+#define KVS_Q8_DIRECT_ROWS 64
+#endif
 struct ChunkPlan {
   bool mma = false;   // tensor cores (16-bit data)
-  bool pair = false;  // units of at most 128 rows
+  bool q8 = false;    // the kernel reads the 8-bit cache itself
   bool stage = false; // K/V pass through the workspace in 16 bits
   bool renumber = false;  // the staged pages have a block table of their own
   long long stage_pages = 0;
@@ -64,9 +67,9 @@ ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, bool q8) {
   if (pl.mma) {
     tile = kChunkTile;
     per_sm = 1;
-    pl.pair = packed <= 128;
-    pl.rows = pl.pair ? 128 : 256;
-    pl.stage = q8 || s->kv_loc == KV_LOC_HOST_PINNED;
+    pl.q8 = q8 && s->kv_loc == KV_LOC_HBM && packed <= KVS_Q8_DIRECT_ROWS;
+    pl.rows = pl.q8 ? 64 : packed <= 128 ? 128 : 256;
+    pl.stage = (q8 && !pl.q8) || s->kv_loc == KV_LOC_HOST_PINNED;
   } else {
     pl.rows = packed <= 16 ? 16 : 64;
   }
@@ -216,10 +219,12 @@ int chunk_common(const kv_shape *s, const kv_chunk *c, const void *q, const void
       if (table) a.bt = table;
       a.nphys = pages = pl.stage_pages;
     }
-    CUtensorMap tk, tv;
-    if ((rc = page_map(s, a.k, pages, dev, &tk)) != KV_OK) return rc;
-    if ((rc = page_map(s, a.v, pages, dev, &tv)) != KV_OK) return rc;
-    e = launch_chunk_mma(s->dtype, pl.pair, a, tk, tv, pl.ctas, st);
+    CUtensorMap tk = {}, tv = {};
+    if (!pl.q8) {
+      if ((rc = page_map(s, a.k, pages, dev, &tk)) != KV_OK) return rc;
+      if ((rc = page_map(s, a.v, pages, dev, &tv)) != KV_OK) return rc;
+    }
+    e = launch_chunk_mma(s->dtype, pl.rows, pl.q8, a, tk, tv, pl.ctas, st);
   } else {
     e = launch_chunk_core(a, is_q8, pl.rows, pl.ctas, st);
   }

@@ -13,9 +13,9 @@
 // weights P in 16 bits over S; O += P V.  While one group computes, the tensor
 // cores work for the other.  TMEM: S and P of the groups at columns 0 and 128,
 // O at 256 and 384.
-//   * kPair = false: a unit is 256 packed rows, 128 per group; both groups use
+//   * kWide: a unit is 256 packed rows, 128 per group; both groups use
 //     each K/V tile, which halves the reads of K and V per product.
-//   * kPair = true: a unit is up to 128 rows; the groups take its KV tiles in
+//   * kPair: a unit is up to 128 rows; the groups take its KV tiles in
 //     turn (even, odd) and join their results at the end.  For few rows per
 //     sequence, where the K/V stream is the bound and each tile's chain of
 //     product, softmax and product would otherwise be exposed.
@@ -43,22 +43,38 @@
 namespace kvs {
 namespace {
 
-constexpr int kThreads = 384;
 constexpr int kTile = kChunkTile;
 constexpr int kTileBytes = kTile * kHeadDim * 2;  // 32 KB
 constexpr int kSlab = kTile * 128;                // 64 channels of a tile
+constexpr int kRawBytes = kTile * kHeadDim;       // a tile of codes
 constexpr uint32_t kTmemCols = 512;
 constexpr float kMoveAt = 8.f;  // log2 of the largest weight before the maximum moves
 
-template <bool kPair> struct Shape {
-  static constexpr int kRows = kPair ? 128 : 256;
-  static constexpr int kQTiles = kPair ? 1 : 2;
-  static constexpr int kStages = kPair ? 6 : 5;  // K and V tiles in the ring
-  static constexpr int kTileArea = (kQTiles + kStages) * kTileBytes;
+// How a CTA works: kWide and kPair as above; kPair8 is kPair over the 8-bit
+// cache, with 64 rows per unit and four more warps that convert.
+enum Mode { kWide, kPair, kPair8 };
+template <int kMode> struct Shape {
+  static constexpr bool kTurns = kMode != kWide;  // the groups take tiles in turn
+  static constexpr bool kQ8 = kMode == kPair8;
+  static constexpr int kThreads = kQ8 ? 512 : 384;
+  static constexpr int kRows = kMode == kWide ? 256 : kMode == kPair ? 128 : 64;
+  static constexpr int kQTiles = kMode == kWide ? 2 : 1;
+  // rows of a Q tile in shared memory; the product reads 128, and what stands
+  // in the place of the others only reaches rows of S that nobody reads
+  static constexpr int kQRows = kQ8 ? 64 : 128;
+  static constexpr int kQBytes = kQRows * kHeadDim * 2;
+  static constexpr int kStages = kMode == kWide ? 5 : kQ8 ? 4 : 6;  // 16-bit K and V tiles
+  static constexpr int kRaw = kQ8 ? 5 : 0;                           // tiles of codes
+  static constexpr int kRingAt = kQTiles * kQBytes;
+  static constexpr int kRawAt = kRingAt + kStages * kTileBytes;
+  static constexpr int kTileArea = kRawAt + kRaw * kRawBytes;
+  static constexpr int kSegs = kMode == kWide ? 32 : kQ8 ? 12 : 10;
 };
 
-template <bool kPair> struct Control {
-  uint64_t full[6], empty[6];
+template <int kMode> struct Control {
+  using Sh = Shape<kMode>;
+  uint64_t full[Sh::kStages], empty[Sh::kStages];
+  uint64_t raw_full[Sh::kQ8 ? Sh::kRaw : 1], raw_empty[Sh::kQ8 ? Sh::kRaw : 1];
   uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_done[2], mend[2], mended[2];
   uint64_t joined, read, drain;
   uint32_t tmem;
@@ -66,14 +82,21 @@ template <bool kPair> struct Control {
   int poison;     // a non-finite V was zeroed in some tile
   int pad;
   uint8_t bad[8];  // per tile, bit i: tokens 16 i .. + 15 have no page
-  ChunkShare<kPair ? 10 : 32> share;
+  ChunkShare<Sh::kSegs> share;
   union {
-    long long red[33];                // share_init
-    float2 ml[2][kPair ? 128 : 1];   // kPair: maximum and sum of each group's rows
+    long long red[33];                         // share_init
+    float2 ml[2][Sh::kTurns ? Sh::kRows : 1];  // maximum and sum of each group's rows
   };
+  // per tile of codes: its scale bytes, and its rows that hold a token
+  alignas(16) uint8_t scale[Sh::kQ8 ? Sh::kRaw : 1][Sh::kQ8 ? kTile : 16];
+  int raw_rows[Sh::kQ8 ? Sh::kRaw : 1], raw_bad[Sh::kQ8 ? Sh::kRaw : 1];
 };
-static_assert(Shape<false>::kTileArea + sizeof(Control<false>) <= 227 * 1024, "shared memory");
-static_assert(Shape<true>::kTileArea + sizeof(Control<true>) <= 227 * 1024, "shared memory");
+template <int kMode> constexpr int smem_bytes() {
+  return Shape<kMode>::kTileArea + (int)sizeof(Control<kMode>);
+}
+static_assert(smem_bytes<kWide>() <= 227 * 1024, "shared memory");
+static_assert(smem_bytes<kPair>() <= 227 * 1024, "shared memory");
+static_assert(smem_bytes<kPair8>() <= 227 * 1024, "shared memory");
 
 // A bounded wait of a whole warp or a lane; false once anything has timed out.
 struct Waiter {
@@ -135,21 +158,28 @@ template <> struct NonFinite<__nv_bfloat16> {
   static constexpr uint32_t kMask = 0x7F807F80u, kOne = 0x00800080u;
 };
 
-// Rows that see a non-finite V of a scanned tile get NaN in its channels
-// [c0, c1): the values are read again from the cache.
-template <class T>
+// Rows that see a non-finite V of a scanned tile (8-bit: a NaN vector of any
+// tile) get NaN in its channels [c0, c1): the cache is read again.
+template <class T, bool kQ8>
 __device__ __noinline__ void poison_row(const ChunkArgs &a, const ChunkSeg &g, int t, int c0,
                                         int c1, T *out, float *part) {
   for (int tile = g.tile_lo; tile < g.tile_hi; ++tile) {
-    if (mend_of(a, g, tile).scan == 0) continue;
+    if (!kQ8 && mend_of(a, g, tile).scan == 0) continue;
     const int lo = max(tile * kTile, a.window > 0 ? t - a.window + 1 : 0);
     const int hi = min(min(tile * kTile + kTile - 1, t), g.len - 1);
     for (int j = lo; j <= hi; ++j) {
       const int ph = a.bt[(long long)g.b * a.maxP + j / a.ps];
       if (ph < 0 || ph >= a.nphys) continue;
-      const uint32_t *v = reinterpret_cast<const uint32_t *>(
-          static_cast<const T *>(a.v) +
-          (((long long)ph * a.Hkv + g.kvh) * a.ps + j % a.ps) * kHeadDim);
+      const long long vec = ((long long)ph * a.Hkv + g.kvh) * a.ps + j % a.ps;
+      if (kQ8) {
+        for (int c = c0; c < c1 && a.v_scale[vec] == kQ8NanScale; ++c) {
+          if (part) part[c] = __uint_as_float(0x7FC00000u);
+          else reinterpret_cast<uint16_t *>(out)[c] = 0x7FFFu;
+        }
+        continue;
+      }
+      const uint32_t *v =
+          reinterpret_cast<const uint32_t *>(static_cast<const T *>(a.v) + vec * kHeadDim);
       for (int c = c0; c < c1; c += 2) {
         const uint32_t x = (v[c / 2] & NonFinite<T>::kMask) + NonFinite<T>::kOne;
         for (int h = 0; h < 2; ++h) {
@@ -165,16 +195,56 @@ __device__ __noinline__ void poison_row(const ChunkArgs &a, const ChunkSeg &g, i
 template <class T> __device__ __forceinline__ constexpr float weight_bias() { return 0.f; }
 template <> __device__ __forceinline__ constexpr float weight_bias<__half>() { return 7.f; }
 
-template <class T, bool kPair>
-__global__ void __launch_bounds__(kThreads, 1)
+// 16 codes times a power of two, as 16 elements of T.  f16: the hardware's
+// conversion and a multiplication.
+template <class T> __device__ __forceinline__ uint32_t q8_factor(uint32_t byte);
+template <> __device__ __forceinline__ uint32_t q8_factor<__half>(uint32_t byte) {
+  const uint32_t h = pack2(q8_scale(byte), 0.f, __half{}) & 0xFFFFu;
+  return h | (h << 16);
+}
+__device__ __forceinline__ void q8_expand(uint4 w, uint32_t f, uint32_t (&x)[8], __half) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t a, b;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(a) : "h"((uint16_t)(u[i] & 0xFFFFu)));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b) : "h"((uint16_t)(u[i] >> 16)));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(x[2 * i]) : "r"(a), "r"(f));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(x[2 * i + 1]) : "r"(b), "r"(f));
+  }
+}
+// bf16: a code's exponent and mantissa, moved to where bf16 has them, are the
+// code times 2^-120 (subnormal codes too: they become subnormal bf16), so one
+// exact multiplication by 2^(e + 120), e + 120 <= 127, gives the value.
+template <> __device__ __forceinline__ uint32_t q8_factor<__nv_bfloat16>(uint32_t byte) {
+  const uint32_t h = byte == (uint32_t)kQ8NanScale ? 0x7FFFu : min(byte + 120u, 254u) << 7;
+  return h | (h << 16);
+}
+__device__ __forceinline__ void q8_expand(uint4 w, uint32_t f, uint32_t (&x)[8], __nv_bfloat16) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // the low and the high byte of each of the four results, then two by two
+    const uint32_t lo = (u[i] & 0x0F0F0F0Fu) << 4;
+    const uint32_t hi = (u[i] & 0x80808080u) | ((u[i] >> 4) & 0x07070707u);
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(x[2 * i]) : "r"(__byte_perm(lo, hi, 0x5140)), "r"(f));
+    asm("mul.rn.bf16x2 %0, %1, %2;"
+        : "=r"(x[2 * i + 1])
+        : "r"(__byte_perm(lo, hi, 0x7362)), "r"(f));
+  }
+}
+
+template <class T, int kMode>
+__global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
     chunk_mma_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tk,
                      const __grid_constant__ CUtensorMap tv) {
-  using Sh = Shape<kPair>;
+  using Sh = Shape<kMode>;
+  constexpr bool kTurns = Sh::kTurns, kQ8 = Sh::kQ8;
   constexpr int kStages = Sh::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t *q_area = smem;
-  uint8_t *ring = smem + Sh::kQTiles * kTileBytes;
-  Control<kPair> &ctl = *reinterpret_cast<Control<kPair> *>(smem + Sh::kTileArea);
+  uint8_t *ring = smem + Sh::kRingAt;
+  Control<kMode> &ctl = *reinterpret_cast<Control<kMode> *>(smem + Sh::kTileArea);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (smem_u32(smem) & 1023u) {  // the swizzled tiles need it
     if (tid == 0) flag_error(a.status, KV_ERR_INVALID_ARG);
@@ -182,11 +252,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 9) tmem_alloc(smem_u32(&ctl.tmem), kTmemCols);
   if (tid == 0) {
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tk)) : "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tv)) : "memory");
-    for (int i = 0; i < 6; ++i) {
-      mbar_init(smem_u32(&ctl.full[i]), 1);
+    if (!kQ8) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tk)) : "memory");
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tv)) : "memory");
+    }
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_u32(&ctl.full[i]), kQ8 ? 4 : 1);
       mbar_init(smem_u32(&ctl.empty[i]), 1);
+    }
+    for (int i = 0; i < Sh::kRaw; ++i) {
+      mbar_init(smem_u32(&ctl.raw_full[i]), 1);
+      mbar_init(smem_u32(&ctl.raw_empty[i]), 4);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(smem_u32(&ctl.q_full[x]), 1);
@@ -217,6 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // state that lives across lists of segments
   Ring<kStages> ld;              // loader: next slot; mender: the next tile's K slot
+  Ring<kQ8 ? Sh::kRaw : 1> raw;  // loader and converter: next tile of codes
   Ring<kStages> qk, pv;          // products: slot of the next K / of the next tile's K
   uint32_t tiles_loaded = 0;     // loader, softmax: tiles so far
   uint32_t q_ph = 0, p_ph = 0, mend_ph = 0;  // bit x
@@ -234,12 +311,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     return share.nseg != 0;
   };
 
-  // registers: 256 threads x 200 + 128 x 104 = 384 x 168, the launch's; the
-  // four warps of a warpgroup change theirs together
+  // registers: 256 threads x 200 + 128 x 104 = 384 x 168, and 256 x 184 + 256 x
+  // 72 = 512 x 128, the launch's; the four warps of a warpgroup change theirs
+  // together
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    if constexpr (kQ8) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if constexpr (kQ8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
   }
   if (warp < 8) {
     // --------------------------------------------------------------- softmax
@@ -254,17 +334,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int nseg = share.nseg;
       for (int sg = 0; sg < nseg && live; ++sg) {
         const ChunkSeg g = share.seg[sg];
-        const int urow = kPair ? row : x * 128 + row;  // row of the unit
-        const bool active = kPair || x == 0 || g.nrows > 128;
+        const int urow = kTurns ? row : x * 128 + row;  // row of the unit
+        const bool active = kTurns || x == 0 || g.nrows > 128;
         if (!active) {
           tiles_loaded += g.tile_hi - g.tile_lo;
           continue;
         }
-        const bool any_row = (kPair ? 0 : x * 128) + (warp & 3) * 32 < g.nrows;
+        const bool any_row = (kTurns ? 0 : x * 128) + (warp & 3) * 32 < g.nrows;
         const int t = g.len - g.n + (g.r0 + min(urow, g.nrows - 1)) / a.G;
         float m = -INFINITY, l = 0.f;
         bool begun = false;
-        for (int tile = g.tile_lo + (kPair ? x : 0); tile < g.tile_hi; tile += kPair ? 2 : 1) {
+        for (int tile = g.tile_lo + (kTurns ? x : 0); tile < g.tile_hi; tile += kTurns ? 2 : 1) {
           if (!wait(smem_u32(&ctl.s_full[x]), s_ph)) {
             live = false;
             break;
@@ -374,12 +454,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           part = a.part_o + prow * kHeadDim;
         }
         float f0 = 1.f, f1 = 0.f;
-        constexpr int kCols = kPair ? 64 : 128;  // channels this thread writes
-        const int c0 = kPair ? 64 * x : 0;
-        const bool second = kPair && g.tile_hi - g.tile_lo > 1;
-        if constexpr (kPair) {
+        constexpr int kCols = kTurns ? 64 : 128;  // channels this thread writes
+        const int c0 = kTurns ? 64 * x : 0;
+        const bool second = kTurns && g.tile_hi - g.tile_lo > 1;
+        if constexpr (kTurns) {
           // both groups hold part of every row: each writes half the channels
-          ctl.ml[x][row] = make_float2(M, l);
+          if (any_row) ctl.ml[x][row] = make_float2(M, l);
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&ctl.joined));
@@ -388,7 +468,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           tc_fence_after();
-          const float2 u = ctl.ml[0][row], v = ctl.ml[1][row];
+          const int at = any_row ? row : 0;
+          const float2 u = ctl.ml[0][at], v = ctl.ml[1][at];
           M = fmaxf(u.x, v.x);
           const float b = M == -INFINITY ? 0.f : M;
           f0 = ex2(u.x - b);
@@ -399,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
           f0 *= inv;
           f1 *= inv;
-          const uint32_t o0 = tmem + lanes + 256 + (kPair ? 0 : x * 128) + c0;
+          const uint32_t o0 = tmem + lanes + 256 + (kTurns ? 0 : x * 128) + c0;
 #pragma unroll
           for (int c = 0; c < kCols; c += 32) {
             float o[32];
@@ -430,16 +511,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (urow < g.nrows) {
-            if (!whole && (!kPair || x == 0)) {
+            if (!whole && (!kTurns || x == 0)) {
               a.part_ml[2 * prow] = M;
               a.part_ml[2 * prow + 1] = l;
             }
             if (*reinterpret_cast<volatile int *>(&ctl.poison))
-              poison_row<T>(a, share.seg[sg], t, c0, c0 + kCols, out, part);
+              poison_row<T, kQ8>(a, share.seg[sg], t, c0, c0 + kCols, out, part);
           }
           tc_fence_before();
         }
-        if constexpr (kPair) {
+        if constexpr (kTurns) {
           // O may be overwritten once both groups have read it
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&ctl.read));
@@ -477,6 +558,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           bad = __reduce_or_sync(0xFFFFFFFFu, bad);
+          if constexpr (kQ8) {
+            const bool have = y != rows_total;
+            const int bytes = __popc(__ballot_sync(0xFFFFFFFFu, have)) * a.ps;
+            for (int w = 0; w < 2; ++w, raw.next()) {
+              if (!wait(smem_u32(&ctl.raw_empty[raw.s]), raw.ph ^ 1)) {
+                live = false;
+                break;
+              }
+              if ((int)tiles_loaded == a.debug_skip_tile) continue;
+              const uint32_t bar = smem_u32(&ctl.raw_full[raw.s]);
+              if (lane == 0) {
+                if (w == 0) ctl.bad[tiles_loaded & 7] = (uint8_t)bad;
+                ctl.raw_rows[raw.s] = min(kTile, g.len - tile * kTile);
+                ctl.raw_bad[raw.s] = (int)bad;
+                mbar_arrive_expect_tx(bar, bytes * (kHeadDim + 1));
+              }
+              __syncwarp();
+              if (have) {
+                bulk_load(smem_u32(smem) + Sh::kRawAt + raw.s * kRawBytes + lane * a.ps * kHeadDim,
+                          static_cast<const uint8_t *>(w ? a.v : a.k) + (long long)y * kHeadDim,
+                          a.ps * kHeadDim, bar);
+                bulk_load(smem_u32(&ctl.scale[raw.s][lane * a.ps]),
+                          (w ? a.v_scale : a.k_scale) + y, a.ps, bar);
+              }
+            }
+          } else {
           for (int w = 0; w < 2; ++w, ld.next()) {
             if (!wait(empty0 + 8 * ld.s, ld.ph ^ 1)) {
               live = false;
@@ -495,6 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_2d(dst, map, 0, y, bar);
               tma_load_2d(dst + kSlab, map, 64, y, bar);
             }
+          }
           }
           if (!live) break;
         }
@@ -526,11 +634,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         enter(c);
         Cur p = c;
         auto active = [&](int x, const Cur &u) {
-          return x == 0 || (kPair ? u.tile + 1 < u.hi : u.two);
+          return x == 0 || (kTurns ? u.tile + 1 < u.hi : u.two);
         };
         auto edge = [&](const Cur &u, int tile) { return tile >= u.from || tile <= u.upto; };
         auto advance = [&](Cur &u, Ring<kStages> &r) {
-          const int step = kPair && active(1, u) ? 2 : 1;
+          const int step = kTurns && active(1, u) ? 2 : 1;
           r.next(2 * step);
           u.tile += step;
           if (u.tile >= u.hi) {
@@ -544,38 +652,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t mended0 = smem_u32(&ctl.mended[0]);
         const uint32_t q_full0 = smem_u32(&ctl.q_full[0]), q_free0 = smem_u32(&ctl.q_free[0]);
         const uint64_t dq = umma_desc(smem_u32(q_area), 16, 1024);
+        constexpr int kQSlab = Sh::kQRows * 128;
         const uint64_t dk = umma_desc(smem_u32(ring), 16, 1024);
         const uint64_t dv = umma_desc(smem_u32(ring), kSlab, 1024);
         auto issue_qk = [&](int x) -> bool {
-          const int qx = kPair ? 0 : x;
+          const int qx = kTurns ? 0 : x;
           Ring<kStages> r = qk;
-          if (kPair) r.next(2 * x);
-          if (c.tile == c.lo && (!kPair || x == 0)) {
+          if (kTurns) r.next(2 * x);
+          if (c.tile == c.lo && (!kTurns || x == 0)) {
             if (!wait(q_full0 + 8 * qx, (q_ph >> qx) & 1)) return false;
             q_ph ^= 1u << qx;
           }
           if (!wait(full0 + 8 * r.s, r.ph)) return false;
           tc_fence_after();
-          const uint64_t a0 = dq + (uint64_t)(qx * (kTileBytes >> 4));
+          const uint64_t a0 = dq + (uint64_t)(qx * (Sh::kQBytes >> 4));
           const uint64_t b0 = dk + (uint64_t)(r.s * (kTileBytes >> 4));
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const uint64_t off = ((k >> 2) * kSlab + (k & 3) * 32) >> 4;
-            umma_ss(tmem + x * 128, a0 + off, b0 + off, id_qk, k > 0);
+            const uint64_t qa = ((k >> 2) * kQSlab + (k & 3) * 32) >> 4;
+            const uint64_t ka = ((k >> 2) * kSlab + (k & 3) * 32) >> 4;
+            umma_ss(tmem + x * 128, a0 + qa, b0 + ka, id_qk, k > 0);
           }
           tc_commit(s_full0 + 8 * x);
-          const int tile = c.tile + (kPair ? x : 0);
+          const int tile = c.tile + (kTurns ? x : 0);
           if (tile + 1 == c.hi) tc_commit(q_free0 + 8 * qx);
-          if (kPair || x == 1 || !c.two) tc_commit(empty0 + 8 * r.s);
-          if ((kPair || x == 0) && edge(c, tile)) mbar_arrive(mend0 + 8 * x);
+          if (kTurns || x == 1 || !c.two) tc_commit(empty0 + 8 * r.s);
+          if (!kQ8 && (kTurns || x == 0) && edge(c, tile)) mbar_arrive(mend0 + 8 * x);
           return true;
         };
         auto issue_pv = [&](int x) -> bool {
           Ring<kStages> r = pv;
-          r.next(1 + (kPair ? 2 * x : 0));
-          if (kPair || x == 0) {
+          r.next(1 + (kTurns ? 2 * x : 0));
+          if (kTurns || x == 0) {
             if (!wait(full0 + 8 * r.s, r.ph)) return false;
-            if (edge(p, p.tile + (kPair ? x : 0))) {
+            if (!kQ8 && edge(p, p.tile + (kTurns ? x : 0))) {
               if (!wait(mended0 + 8 * x, (mend_ph >> x) & 1)) return false;
               mend_ph ^= 1u << x;
             }
@@ -590,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma_ts(tmem + 256 + x * 128, tmem + x * 128 + k * 8, b0 + k * (2048 >> 4), id_pv,
                     add || k > 0);
           tc_commit(o_done0 + 8 * x);
-          if (kPair || x == 1 || !p.two) tc_commit(empty0 + 8 * r.s);
+          if (kTurns || x == 1 || !p.two) tc_commit(empty0 + 8 * r.s);
           return true;
         };
         bool live = issue_qk(0) && (!active(1, c) || issue_qk(1));
@@ -618,13 +728,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int sg = 0; sg < nseg && live; ++sg) {
         const ChunkSeg g = share.seg[sg];
         for (int tile = g.tile_lo; tile < g.tile_hi; ++tile, ld.next(2)) {
-          if (!at_edge(g, tile)) continue;
+          if (kQ8 || !at_edge(g, tile)) continue;
           const Mend m = mend_of(a, g, tile);
           Ring<kStages> r = ld;
           r.next();
           // the product warp asks when it has issued the tile's scores: then
           // the copy of this V is the slot's current or last one
-          const int x = kPair ? (tile - g.tile_lo) & 1 : 0;
+          const int x = kTurns ? (tile - g.tile_lo) & 1 : 0;
           if (!wait(smem_u32(&ctl.mend[x]), (mend_ph >> x) & 1) ||
               !wait(smem_u32(&ctl.full[r.s]), r.ph)) {
             live = false;
@@ -672,6 +782,61 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+  } else if (warp >= 12) {
+    // ------------------------------------------------------------- converter
+    // A thread takes 16 codes of a token at a time, 16 times per tile: eight
+    // lanes read a row of codes, and write two 16-byte chunks each into the
+    // row's two swizzled slabs (the lanes of the second slab in the other
+    // order, so that the eight meet distinct banks).
+    if constexpr (kQ8) {
+      const int ct = tid - 384, c16 = ct & 7, row0 = ct >> 3;
+      while (next_list()) {
+        bool live = true;
+        const int nseg = share.nseg;
+        for (int sg = 0; sg < nseg && live; ++sg) {
+          const int tiles = share.seg[sg].tile_hi - share.seg[sg].tile_lo;
+          for (int i = 0; i < 2 * tiles; ++i, ld.next(), raw.next()) {
+            if (!wait(smem_u32(&ctl.raw_full[raw.s]), raw.ph) ||
+                !wait(smem_u32(&ctl.empty[ld.s]), ld.ph ^ 1)) {
+              live = false;
+              break;
+            }
+            const bool is_v = i & 1;
+            const uint8_t *codes = smem + Sh::kRawAt + raw.s * kRawBytes;
+            uint8_t *slab = ring + ld.s * kTileBytes + (c16 >> 2) * kSlab;
+            const int rows = ctl.raw_rows[raw.s], bad = ctl.raw_bad[raw.s];
+#pragma unroll 4
+            for (int r = row0; r < kTile; r += 16) {
+              const uint4 w = *reinterpret_cast<const uint4 *>(codes + r * kHeadDim + c16 * 16);
+              const uint32_t byte = ctl.scale[raw.s][r];
+              uint32_t x[8];
+              q8_expand(w, q8_factor<T>(byte), x, T{});
+              if (is_v) {
+                const bool token = r < rows && !((bad >> (r >> 4)) & 1);
+                if (token && byte == (uint32_t)kQ8NanScale)
+                  *reinterpret_cast<volatile int *>(&ctl.poison) = 1;
+                if (!token || byte == (uint32_t)kQ8NanScale) {
+#pragma unroll
+                  for (int k = 0; k < 8; ++k) x[k] = 0;
+                }
+              }
+              const int ch = (c16 & 3) * 2;
+              const bool swap = c16 >= 4;
+              const uint4 u = make_uint4(x[0], x[1], x[2], x[3]);
+              const uint4 v = make_uint4(x[4], x[5], x[6], x[7]);
+              *reinterpret_cast<uint4 *>(slab + swz(r, ch + swap)) = swap ? v : u;
+              *reinterpret_cast<uint4 *>(slab + swz(r, ch + !swap)) = swap ? u : v;
+            }
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(smem_u32(&ctl.full[ld.s]));
+              mbar_arrive(smem_u32(&ctl.raw_empty[raw.s]));
+            }
+          }
+        }
+      }
+    }
   } else {
     // -------------------------------------------------------------- Q loader
     while (next_list()) {
@@ -689,14 +854,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             q_ph ^= 1u << x;
           }
           q_uses |= 1u << x;
-          const uint32_t q = smem_u32(q_area) + x * kTileBytes + (ch >> 3) * kSlab;
+          const uint32_t q = smem_u32(q_area) + x * Sh::kQBytes + (ch >> 3) * Sh::kQRows * 128;
           const int pr = g.r0 + x * 128 + half, left = g.nrows - x * 128;
           int hd = pr % a.G;
           const T *src = static_cast<const T *>(a.q) +
                          ((long long)(g.q0 + pr / a.G) * a.Hq + g.kvh * a.G + hd) * kHeadDim +
                          ch * 8;
           const long long wrap = (long long)(a.Hq - a.G) * kHeadDim;  // to the next token's heads
-          for (int r = half; r < 128; r += 2) {
+          for (int r = half; r < Sh::kQRows; r += 2) {
             const uint32_t dst = q + swz(r, ch & 7);
             if (r < left && a.scale_log2 > 0.f) {
               cp_async16(dst, src);
@@ -731,7 +896,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // leave no copy and no product in flight: every slot's last copy (slots
     // before ld.s were filled in this lap of the ring, the others in the one
     // before), and a last commit
-    if (warp == 8) {
+    if (warp == 8 && kQ8) {
+      for (int i = 0; i < Sh::kRaw; ++i)
+        mbar_wait(smem_u32(&ctl.raw_full[i]), i < raw.s ? raw.ph : raw.ph ^ 1, a.wait_limit_ns);
+    }
+    if (warp == 8 && !kQ8) {
       for (int i = 0; i < kStages; ++i)
         mbar_wait(smem_u32(&ctl.full[i]), i < ld.s ? ld.ph : ld.ph ^ 1, a.wait_limit_ns);
     }
@@ -748,25 +917,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <class T, bool kPair>
+template <class T, int kMode>
 cudaError_t mma_go(const ChunkArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
                    cudaStream_t st) {
-  constexpr int bytes = Shape<kPair>::kTileArea + (int)sizeof(Control<kPair>);
+  constexpr int bytes = smem_bytes<kMode>();
   const cudaError_t e = cudaFuncSetAttribute(
-      chunk_mma_kernel<T, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+      chunk_mma_kernel<T, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  return launch_pdl(chunk_mma_kernel<T, kPair>, dim3(ctas), dim3(kThreads), bytes, st, a, tk, tv);
+  return launch_pdl(chunk_mma_kernel<T, kMode>, dim3(ctas), dim3(Shape<kMode>::kThreads), bytes,
+                    st, a, tk, tv);
+}
+template <class T>
+cudaError_t mma_type(int rows, bool q8, const ChunkArgs &a, const CUtensorMap &tk,
+                     const CUtensorMap &tv, int ctas, cudaStream_t st) {
+  if (q8) return mma_go<T, kPair8>(a, tk, tv, ctas, st);
+  return rows == 128 ? mma_go<T, kPair>(a, tk, tv, ctas, st)
+                     : mma_go<T, kWide>(a, tk, tv, ctas, st);
 }
 
 }  // namespace
 
-cudaError_t launch_chunk_mma(int dtype, bool pair, const ChunkArgs &a, const CUtensorMap &tk,
-                             const CUtensorMap &tv, int ctas, cudaStream_t st) {
-  if (dtype == KV_F16)
-    return pair ? mma_go<__half, true>(a, tk, tv, ctas, st)
-                : mma_go<__half, false>(a, tk, tv, ctas, st);
-  return pair ? mma_go<__nv_bfloat16, true>(a, tk, tv, ctas, st)
-              : mma_go<__nv_bfloat16, false>(a, tk, tv, ctas, st);
+cudaError_t launch_chunk_mma(int dtype, int rows, bool q8, const ChunkArgs &a,
+                             const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
+                             cudaStream_t st) {
+  return dtype == KV_F16 ? mma_type<__half>(rows, q8, a, tk, tv, ctas, st)
+                         : mma_type<__nv_bfloat16>(rows, q8, a, tk, tv, ctas, st);
 }
 
 }  // namespace kvs

@@ -81,9 +81,11 @@ cudaError_t launch_combine_lists(const float *part_o, const float *part_ml, cons
 // shares the work is cut into
 struct ChunkArgs;
 cudaError_t launch_chunk_core(const ChunkArgs &a, bool q8, int rows, int ctas, cudaStream_t st);
-// 16-bit data on the tensor cores; pair: units of at most 128 rows
-cudaError_t launch_chunk_mma(int dtype, bool pair, const ChunkArgs &a, const CUtensorMap &tk,
-                             const CUtensorMap &tv, int ctas, cudaStream_t st);
+// 16-bit q on the tensor cores: 16-bit K/V in units of 256 or 128 rows, or the
+// 8-bit cache (in device memory) in units of 64; the maps are of 16-bit K/V
+cudaError_t launch_chunk_mma(int dtype, int rows, bool q8, const ChunkArgs &a,
+                             const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
+                             cudaStream_t st);
 // the pages it needs into device memory in 16 bits (table: their new block table, or null)
 cudaError_t launch_chunk_stage(int dtype, bool q8, const ChunkArgs &c, void *k_out, void *v_out,
                                int32_t *table, cudaStream_t st);

@@ -129,10 +129,11 @@ def test_unseen_keys_do_not_reach_a_row(dtype):
     run(p)
 
 
-def test_unseen_8_bit_vectors_do_not_reach_a_row():
+@pytest.mark.parametrize("n", [100, 51, 20])
+def test_unseen_8_bit_vectors_do_not_reach_a_row(n):
     for name in "kv":
         for dtype in ("f16", "bf16", "f32"):
-            p = Problem(dtype, 2, 1, 16, [200, 33], [100, 1], q8=True)
+            p = Problem(dtype, 2, 1, 16, [160, 33], [n, 1], q8=True)
             p.code[name][p.table[0, 150 // 16], :, 150 % 16] = 0x7F
             p.scale8[name][p.table[0, 150 // 16], :, 150 % 16] = 255
             run(p)
