@@ -260,4 +260,33 @@ __device__ __forceinline__ int vis_lo(int t, int tile0, int window) {
   return window > 0 ? t - window + 1 - tile0 : 0;
 }
 
+// A bounded wait of a whole warp or a lane; false once anything has timed out.
+struct Waiter {
+  volatile int *abort;
+  int *status;
+  unsigned long long limit;
+  __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    if (mbar_wait(bar, parity, limit)) return true;
+    flag_error(status, KV_ERR_DEVICE_TIMEOUT);
+    *abort = 1;
+    return false;
+  }
+};
+
+template <int kStages> struct Ring {
+  int s = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++s == kStages) {
+      s = 0;
+      ph ^= 1;
+    }
+  }
+  __device__ __forceinline__ void next(int n) {
+    for (int i = 0; i < n; ++i) next();
+  }
+};
+
 }  // namespace kvs

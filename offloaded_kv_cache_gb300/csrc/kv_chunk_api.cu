@@ -43,7 +43,8 @@ int resolve_q8(const kv_shape *s, const kv_q8_cache *c, kv_q8_cache *dev) {
 #endif
 struct ChunkPlan {
   bool mma = false;   // tensor cores (16-bit data)
-  bool q8 = false;    // the kernel reads the 8-bit cache itself
+  bool q8 = false;    // the kernel reads the 8-bit cache itself ...
+  bool few = false;   // ... and is the one for few rows
   bool stage = false; // K/V pass through the workspace in 16 bits
   bool renumber = false;  // the staged pages have a block table of their own
   long long stage_pages = 0;
@@ -68,7 +69,12 @@ ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, bool q8) {
     tile = kChunkTile;
     per_sm = 1;
     pl.q8 = q8 && s->kv_loc == KV_LOC_HBM && packed <= KVS_Q8_DIRECT_ROWS;
-    pl.rows = pl.q8 ? 64 : packed <= 128 ? 128 : 256;
+    pl.few = pl.q8 && packed <= 16;
+    pl.rows = pl.few ? (packed <= 8 ? 8 : 16) : pl.q8 ? 64 : packed <= 128 ? 128 : 256;
+    if (pl.few) {
+      tile = 64;
+      per_sm = pl.rows == 8 ? 2 : 1;
+    }
     pl.stage = (q8 && !pl.q8) || s->kv_loc == KV_LOC_HOST_PINNED;
   } else {
     pl.rows = packed <= 16 ? 16 : 64;
@@ -102,11 +108,12 @@ ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, bool q8) {
   return pl;
 }
 
-// 2-D view [rows = pages * Hkv * ps][128 elements] of 16-bit pages; a box is
-// 64 channels (128 bytes, swizzled) of one page.  Encoding takes host time on
+// 2-D view [rows = pages * Hkv * ps][128 elements] of pages; a box is 128
+// bytes, swizzled, of a page's tokens: 64 channels of 16-bit data, all 128 (of
+// 64 tokens at most) of codes.  Encoding takes host time on
 // every call, so the last ones are kept; an entry depends on its key alone.
 struct MapEntry {
-  int dev, dtype, ps;
+  int dev, dtype, ps;  // dtype -1: codes
   const void *base;
   long long rows;
   CUtensorMap map;
@@ -115,12 +122,14 @@ std::mutex g_map_mutex;
 MapEntry g_maps[16];
 unsigned g_map_n = 0;
 
-int page_map(const kv_shape *s, const void *base, long long pages, int dev, CUtensorMap *map) {
+int page_map(const kv_shape *s, bool codes, const void *base, long long pages, int dev,
+             CUtensorMap *map) {
+  const int dtype = codes ? -1 : s->dtype;
   const long long rows = pages * s->num_kv_heads * s->page_size;
   std::lock_guard<std::mutex> lock(g_map_mutex);
   for (unsigned i = 0; i < std::min(g_map_n, 16u); ++i) {
     const MapEntry &e = g_maps[i];
-    if (e.dev == dev && e.base == base && e.rows == rows && e.dtype == s->dtype &&
+    if (e.dev == dev && e.base == base && e.rows == rows && e.dtype == dtype &&
         e.ps == s->page_size) {
       *map = e.map;
       return KV_OK;
@@ -129,17 +138,18 @@ int page_map(const kv_shape *s, const void *base, long long pages, int dev, CUte
   auto fn = encode_fn();
   if (!fn) return KV_ERR_CUDA;
   cuuint64_t dims[2] = {(cuuint64_t)kHeadDim, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)kHeadDim * 2};
-  cuuint32_t box[2] = {64, (cuuint32_t)s->page_size};
+  cuuint64_t strides[1] = {(cuuint64_t)kHeadDim * (codes ? 1 : 2)};
+  cuuint32_t box[2] = {codes ? 128u : 64u, (cuuint32_t)(codes ? std::min(s->page_size, 64) : s->page_size)};
   cuuint32_t estr[2] = {1, 1};
-  const CUresult r =
-      fn(map, s->dtype == KV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-         2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUtensorMapDataType type = codes                ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : s->dtype == KV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                        : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const CUresult r = fn(map, type, 2, const_cast<void *>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return KV_ERR_CUDA;
   MapEntry &e = g_maps[g_map_n % 16];
-  e = MapEntry{dev, s->dtype, s->page_size, base, rows, *map};
+  e = MapEntry{dev, dtype, s->page_size, base, rows, *map};
   ++g_map_n;
   if (g_map_n >= 32) g_map_n -= 16;
   return KV_OK;
@@ -220,11 +230,12 @@ int chunk_common(const kv_shape *s, const kv_chunk *c, const void *q, const void
       a.nphys = pages = pl.stage_pages;
     }
     CUtensorMap tk = {}, tv = {};
-    if (!pl.q8) {
-      if ((rc = page_map(s, a.k, pages, dev, &tk)) != KV_OK) return rc;
-      if ((rc = page_map(s, a.v, pages, dev, &tv)) != KV_OK) return rc;
+    if (!pl.q8 || pl.few) {
+      if ((rc = page_map(s, pl.few, a.k, pages, dev, &tk)) != KV_OK) return rc;
+      if ((rc = page_map(s, pl.few, a.v, pages, dev, &tv)) != KV_OK) return rc;
     }
-    e = launch_chunk_mma(s->dtype, pl.rows, pl.q8, a, tk, tv, pl.ctas, st);
+    e = pl.few ? launch_chunk_few(s->dtype, pl.rows, a, tk, tv, pl.ctas, st)
+               : launch_chunk_mma(s->dtype, pl.rows, pl.q8, a, tk, tv, pl.ctas, st);
   } else {
     e = launch_chunk_core(a, is_q8, pl.rows, pl.ctas, st);
   }

@@ -98,35 +98,6 @@ static_assert(smem_bytes<kWide>() <= 227 * 1024, "shared memory");
 static_assert(smem_bytes<kPair>() <= 227 * 1024, "shared memory");
 static_assert(smem_bytes<kPair8>() <= 227 * 1024, "shared memory");
 
-// A bounded wait of a whole warp or a lane; false once anything has timed out.
-struct Waiter {
-  volatile int *abort;
-  int *status;
-  unsigned long long limit;
-  __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*abort) return false;
-    if (mbar_wait(bar, parity, limit)) return true;
-    flag_error(status, KV_ERR_DEVICE_TIMEOUT);
-    *abort = 1;
-    return false;
-  }
-};
-
-template <int kStages> struct Ring {
-  int s = 0;
-  uint32_t ph = 0;
-  __device__ __forceinline__ void next() {
-    if (++s == kStages) {
-      s = 0;
-      ph ^= 1;
-    }
-  }
-  __device__ __forceinline__ void next(int n) {
-    for (int i = 0; i < n; ++i) next();
-  }
-};
-
 // What the V of a tile needs before the product reads it.
 struct Mend {
   int zero_lo, zero_hi;  // token rows past the end in the last page
@@ -801,31 +772,38 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
               live = false;
               break;
             }
-            const bool is_v = i & 1;
-            const uint8_t *codes = smem + Sh::kRawAt + raw.s * kRawBytes;
+            // rows row0 + 16 j: they share their swizzle
+            const uint4 *codes = reinterpret_cast<const uint4 *>(smem + Sh::kRawAt +
+                                                                 raw.s * kRawBytes) + ct;
+            const uint8_t *scale = ctl.scale[raw.s] + row0;
             uint8_t *slab = ring + ld.s * kTileBytes + (c16 >> 2) * kSlab;
-            const int rows = ctl.raw_rows[raw.s], bad = ctl.raw_bad[raw.s];
+            const int ch = (c16 & 3) * 2;
+            const bool swap = c16 >= 4;
+            uint8_t *to0 = slab + swz(row0, ch + swap), *to1 = slab + swz(row0, ch + !swap);
+            bool nan = false;
 #pragma unroll 4
-            for (int r = row0; r < kTile; r += 16) {
-              const uint4 w = *reinterpret_cast<const uint4 *>(codes + r * kHeadDim + c16 * 16);
-              const uint32_t byte = ctl.scale[raw.s][r];
+            for (int r = 0; r < kTile / 16; ++r) {
+              const uint32_t byte = scale[16 * r];
               uint32_t x[8];
-              q8_expand(w, q8_factor<T>(byte), x, T{});
-              if (is_v) {
-                const bool token = r < rows && !((bad >> (r >> 4)) & 1);
-                if (token && byte == (uint32_t)kQ8NanScale)
-                  *reinterpret_cast<volatile int *>(&ctl.poison) = 1;
-                if (!token || byte == (uint32_t)kQ8NanScale) {
-#pragma unroll
-                  for (int k = 0; k < 8; ++k) x[k] = 0;
-                }
-              }
-              const int ch = (c16 & 3) * 2;
-              const bool swap = c16 >= 4;
+              q8_expand(codes[r * 128], q8_factor<T>(byte), x, T{});
+              nan |= byte == (uint32_t)kQ8NanScale;
               const uint4 u = make_uint4(x[0], x[1], x[2], x[3]);
               const uint4 v = make_uint4(x[4], x[5], x[6], x[7]);
-              *reinterpret_cast<uint4 *>(slab + swz(r, ch + swap)) = swap ? v : u;
-              *reinterpret_cast<uint4 *>(slab + swz(r, ch + !swap)) = swap ? u : v;
+              *reinterpret_cast<uint4 *>(to0 + r * 2048) = swap ? v : u;
+              *reinterpret_cast<uint4 *>(to1 + r * 2048) = swap ? u : v;
+            }
+            // of V, rows without a token and NaN vectors must not meet a weight of 0
+            const int rows = ctl.raw_rows[raw.s], bad = ctl.raw_bad[raw.s];
+            if ((i & 1) && (nan || rows < kTile || bad != 0)) {
+#pragma unroll 1
+              for (int r = 0; r < kTile / 16; ++r) {
+                const bool token = row0 + 16 * r < rows && !((bad >> r) & 1);
+                const bool nan_row = scale[16 * r] == kQ8NanScale;
+                if (token && nan_row) *reinterpret_cast<volatile int *>(&ctl.poison) = 1;
+                if (token && !nan_row) continue;
+                *reinterpret_cast<uint4 *>(to0 + r * 2048) = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4 *>(to1 + r * 2048) = make_uint4(0, 0, 0, 0);
+              }
             }
             fence_async_shared();
             __syncwarp();

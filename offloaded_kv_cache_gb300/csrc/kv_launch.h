@@ -86,6 +86,10 @@ cudaError_t launch_chunk_core(const ChunkArgs &a, bool q8, int rows, int ctas, c
 cudaError_t launch_chunk_mma(int dtype, int rows, bool q8, const ChunkArgs &a,
                              const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
                              cudaStream_t st);
+// 16-bit q over the 8-bit cache in device memory, units of 8 or 16 rows; the
+// maps are of the codes
+cudaError_t launch_chunk_few(int dtype, int rows, const ChunkArgs &a, const CUtensorMap &tk,
+                             const CUtensorMap &tv, int ctas, cudaStream_t st);
 // the pages it needs into device memory in 16 bits (table: their new block table, or null)
 cudaError_t launch_chunk_stage(int dtype, bool q8, const ChunkArgs &c, void *k_out, void *v_out,
                                int32_t *table, cudaStream_t st);

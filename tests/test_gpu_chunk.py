@@ -68,6 +68,36 @@ def test_windows(dtype, window, q8):
     run(Problem(dtype, 2, 1, 16, [420, 90], [140, 90], window, q8=q8, seed=window))
 
 
+# few rows per kv head: units of 8, 16, 64 and 128 packed rows
+FEW = [(8, 2, 2), (8, 1, 1), (7, 1, 2), (16, 1, 1), (4, 1, 4), (6, 2, 11), (8, 1, 8), (8, 1, 16)]
+
+
+@pytest.mark.parametrize("q8", [False, True], ids=["own", "q8"])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("hq,hkv,n", FEW)
+@pytest.mark.parametrize("window", [0, 40])
+@pytest.mark.parametrize("ps", [16, 128])
+def test_few_rows(dtype, hq, hkv, n, window, ps, q8):
+    run(Problem(dtype, hq, hkv, ps, [n + 120, n, 390, 5], [n, n, 1, 0], window, q8=q8, seed=n))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("n", [2, 20])
+def test_few_rows_with_vectors_of_very_different_size(dtype, n):
+    """Keys and values of the 8-bit cache whose scales differ by up to 2^20, queries
+    whose rows do; scores reach tens either way."""
+    p = Problem(dtype, 4, 2, 16, [300, 64], [n, 1], q8=True, seed=n)
+    g = torch.Generator().manual_seed(5)
+    for name in "kv":
+        scale = p.scale8[name]
+        lo = 127 - (15 if dtype == "f16" else 20)
+        new = torch.randint(lo, 121, scale.shape, generator=g).to(torch.uint8)
+        p.scale8[name] = torch.where(scale == 255, scale, new)
+    p.q = (p.q.float() * torch.exp2(torch.randint(-12, 3, (p.total, 4, 1), generator=g).float())
+           ).to(TORCH[dtype])
+    run(p)
+
+
 @pytest.mark.parametrize("q8", [False, True], ids=["own", "q8"])
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 def test_rows_that_see_nothing(dtype, q8):
@@ -79,17 +109,19 @@ def test_rows_that_see_nothing(dtype, q8):
 @pytest.mark.parametrize("dtype,scale,q_size", [
     ("f32", -0.2, 1.0), ("bf16", -0.2, 1.0), ("f16", 0.0, 1.0), ("bf16", 1.0, 16.0),
     ("f16", 0.5, 8.0), ("f32", 1.0, 8.0)])
-def test_scales(dtype, scale, q_size, q8):
+@pytest.mark.parametrize("n", [3, 20, 150])
+def test_scales(dtype, scale, q_size, n, q8):
     """Negative and zero scales, and scores in the hundreds (one weight near 1)."""
-    run(Problem(dtype, 4, 2, 16, [260, 30], [20, 1], scale=scale, q_size=q_size, q8=q8))
+    run(Problem(dtype, 4, 2, 16, [260, 30], [n, 1], scale=scale, q_size=q_size, q8=q8))
 
 
 @pytest.mark.parametrize("q8", [False, True], ids=["own", "q8"])
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("order", [1, -1])
-def test_running_maximum_moves(dtype, order, q8):
+@pytest.mark.parametrize("n", [4, 30, 150])
+def test_running_maximum_moves(dtype, order, n, q8):
     """Scores that rise (fall) by 20 powers of two from tile to tile."""
-    p = Problem(dtype, 2, 1, 16, [700], [150], q8=False, scale=1.0)
+    p = Problem(dtype, 2, 1, 16, [700], [n], q8=False, scale=1.0)
     ramp = order * torch.linspace(-100, 100, 700)
     p.q = torch.zeros_like(p.q)
     p.q[:, :, 0] = 1
@@ -129,13 +161,13 @@ def test_unseen_keys_do_not_reach_a_row(dtype):
     run(p)
 
 
-@pytest.mark.parametrize("n", [100, 51, 20])
+@pytest.mark.parametrize("n", [100, 51, 20, 7])
 def test_unseen_8_bit_vectors_do_not_reach_a_row(n):
     for name in "kv":
         for dtype in ("f16", "bf16", "f32"):
             p = Problem(dtype, 2, 1, 16, [160, 33], [n, 1], q8=True)
-            p.code[name][p.table[0, 150 // 16], :, 150 % 16] = 0x7F
-            p.scale8[name][p.table[0, 150 // 16], :, 150 % 16] = 255
+            p.code[name][p.table[0, 155 // 16], :, 155 % 16] = 0x7F
+            p.scale8[name][p.table[0, 155 // 16], :, 155 % 16] = 255
             run(p)
 
 
@@ -299,7 +331,7 @@ def test_the_path_together(dtype):
 
 
 @pytest.mark.parametrize("q8", [False, True], ids=["own", "q8"])
-@pytest.mark.parametrize("news", [[3, 1], [90, 200]])
+@pytest.mark.parametrize("news", [[1, 1], [13, 1], [90, 200]])
 def test_a_wait_that_runs_out_is_reported(news, q8):
     """A K/V tile that is never filled (the testing hook): the bounded waits give
     up, the status says so, and the next call is exact."""
