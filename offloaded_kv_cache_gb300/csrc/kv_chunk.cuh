@@ -39,6 +39,8 @@ struct ChunkArgs {
   long long nphys;
   int B, Hq, Hkv, G, ps, maxP, total_q, max_q_len, window;
   int slot_rows;
+  int row_tile;      // tensor cores: packed rows per Q tile
+  int q_tma;         // tensor cores: Q tiles are whole tokens, copied by the TMA unit
   float scale_log2;  // scale * log2(e)
   unsigned long long wait_limit_ns;
   int debug_skip_tile;  // >= 0: the producer never fills that tile of a share (timeout test)

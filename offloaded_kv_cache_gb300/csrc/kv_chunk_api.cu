@@ -49,6 +49,8 @@ struct ChunkPlan {
   bool renumber = false;  // the staged pages have a block table of their own
   long long stage_pages = 0;
   int rows = 64;      // packed rows per unit
+  int row_tile = 0;   // tensor cores: packed rows per Q tile (a unit is one, or two when wide)
+  bool wide = false;
   int ctas = 1;
   int slot_rows = 1;  // rows of a partial result
   size_t off_meta = 0, off_ml = 0, off_o = 0, off_table = 0, off_k = 0, off_v = 0;
@@ -70,10 +72,16 @@ ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, bool q8) {
     per_sm = 1;
     pl.q8 = q8 && s->kv_loc == KV_LOC_HBM && packed <= KVS_Q8_DIRECT_ROWS;
     pl.few = pl.q8 && packed <= 16;
-    pl.rows = pl.few ? (packed <= 8 ? 8 : 16) : pl.q8 ? 64 : packed <= 128 ? 128 : 256;
     if (pl.few) {
+      pl.rows = packed <= 8 ? 8 : 16;
       tile = 64;
       per_sm = pl.rows == 8 ? 2 : 1;
+    } else {
+      // a Q tile holds whole tokens, for the TMA unit, where a token's heads fit
+      const int most = pl.q8 ? 64 : 128;
+      pl.row_tile = G <= most ? most / G * G : most;
+      pl.wide = !pl.q8 && packed > pl.row_tile;
+      pl.rows = pl.row_tile * (pl.wide ? 2 : 1);
     }
     pl.stage = (q8 && !pl.q8) || s->kv_loc == KV_LOC_HOST_PINNED;
   } else {
@@ -108,51 +116,76 @@ ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, bool q8) {
   return pl;
 }
 
-// 2-D view [rows = pages * Hkv * ps][128 elements] of pages; a box is 128
-// bytes, swizzled, of a page's tokens: 64 channels of 16-bit data, all 128 (of
-// 64 tokens at most) of codes.  Encoding takes host time on
-// every call, so the last ones are kept; an entry depends on its key alone.
-struct MapEntry {
-  int dev, dtype, ps;  // dtype -1: codes
+// Tensor maps, all of rows of 128 channels under the 128-byte swizzle.
+// Encoding takes host time on every call, so the last ones are kept; a map
+// follows from its key alone.
+struct MapKey {
+  int dev, type;       // CUtensorMapDataType
   const void *base;
-  long long rows;
+  long long rows;      // pages * Hkv * ps, or tokens of q
+  int heads, box, box2;  // heads: 0 for pages; box: rows, or heads and tokens (box2)
+  bool operator==(const MapKey &o) const {
+    return dev == o.dev && type == o.type && base == o.base && rows == o.rows &&
+           heads == o.heads && box == o.box && box2 == o.box2;
+  }
+};
+struct MapEntry {
+  MapKey key;
   CUtensorMap map;
 };
 std::mutex g_map_mutex;
 MapEntry g_maps[16];
-unsigned g_map_n = 0;
+unsigned g_map_n = 0;  // entries made, the last 16 of which are there
 
-int page_map(const kv_shape *s, bool codes, const void *base, long long pages, int dev,
-             CUtensorMap *map) {
-  const int dtype = codes ? -1 : s->dtype;
-  const long long rows = pages * s->num_kv_heads * s->page_size;
+int cached_map(const MapKey &k, CUtensorMap *map) {
   std::lock_guard<std::mutex> lock(g_map_mutex);
   for (unsigned i = 0; i < std::min(g_map_n, 16u); ++i) {
-    const MapEntry &e = g_maps[i];
-    if (e.dev == dev && e.base == base && e.rows == rows && e.dtype == dtype &&
-        e.ps == s->page_size) {
-      *map = e.map;
+    if (g_maps[i].key == k) {
+      *map = g_maps[i].map;
       return KV_OK;
     }
   }
   auto fn = encode_fn();
   if (!fn) return KV_ERR_CUDA;
-  cuuint64_t dims[2] = {(cuuint64_t)kHeadDim, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)kHeadDim * (codes ? 1 : 2)};
-  cuuint32_t box[2] = {codes ? 128u : 64u, (cuuint32_t)(codes ? std::min(s->page_size, 64) : s->page_size)};
-  cuuint32_t estr[2] = {1, 1};
-  const CUtensorMapDataType type = codes                ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                   : s->dtype == KV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                                        : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  const CUresult r = fn(map, type, 2, const_cast<void *>(base), dims, strides, box, estr,
+  const bool codes = k.type == CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  const cuuint64_t row = (cuuint64_t)kHeadDim * (codes ? 1 : 2);
+  const cuuint32_t across = codes ? 128 : 64;  // 128 bytes
+  const cuuint32_t estr[3] = {1, 1, 1};
+  cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)k.rows, 0}, strides[2] = {row, 0};
+  cuuint32_t box[3] = {across, (cuuint32_t)k.box, 0};
+  if (k.heads) {  // q: [tokens][heads][128]
+    dims[1] = (cuuint64_t)k.heads;
+    dims[2] = (cuuint64_t)k.rows;
+    strides[1] = row * k.heads;
+    box[2] = (cuuint32_t)k.box2;
+  }
+  const CUresult r = fn(map, (CUtensorMapDataType)k.type, k.heads ? 3 : 2,
+                        const_cast<void *>(k.base), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return KV_ERR_CUDA;
-  MapEntry &e = g_maps[g_map_n % 16];
-  e = MapEntry{dev, dtype, s->page_size, base, rows, *map};
-  ++g_map_n;
-  if (g_map_n >= 32) g_map_n -= 16;
+  g_maps[g_map_n % 16] = MapEntry{k, *map};
+  if (++g_map_n >= 32) g_map_n -= 16;
   return KV_OK;
+}
+
+int type16(const kv_shape *s) {
+  return s->dtype == KV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+}
+// Pages as rows [pages * Hkv * ps][128]: a box is 128 bytes of a page's
+// tokens, 64 channels of 16-bit data or all 128 (of 64 tokens at most) of codes.
+int page_map(const kv_shape *s, bool codes, const void *base, long long pages, int dev,
+             CUtensorMap *map) {
+  return cached_map(MapKey{dev, codes ? (int)CU_TENSOR_MAP_DATA_TYPE_UINT8 : type16(s), base,
+                           pages * s->num_kv_heads * s->page_size, 0,
+                           codes ? std::min(s->page_size, 64) : s->page_size, 0},
+                    map);
+}
+// q: a box is 64 channels of the G heads of row_tile / G tokens.
+int q_map(const kv_shape *s, const kv_chunk *c, const void *q, int row_tile, int dev,
+          CUtensorMap *map) {
+  const int G = s->num_q_heads / s->num_kv_heads;
+  return cached_map(MapKey{dev, type16(s), q, c->total_q, s->num_q_heads, G, row_tile / G}, map);
 }
 
 size_t chunk_bytes(const kv_shape *s, const kv_chunk *c, bool q8) {
@@ -229,13 +262,17 @@ int chunk_common(const kv_shape *s, const kv_chunk *c, const void *q, const void
       if (table) a.bt = table;
       a.nphys = pages = pl.stage_pages;
     }
-    CUtensorMap tk = {}, tv = {};
+    CUtensorMap tq = {}, tk = {}, tv = {};
+    a.row_tile = pl.row_tile;
+    // a scale that is not positive is applied to Q as it is loaded
+    a.q_tma = !pl.few && a.G <= pl.row_tile && pl.row_tile % a.G == 0 && a.scale_log2 > 0.f;
+    if (a.q_tma && (rc = q_map(s, c, q, pl.row_tile, dev, &tq)) != KV_OK) return rc;
     if (!pl.q8 || pl.few) {
       if ((rc = page_map(s, pl.few, a.k, pages, dev, &tk)) != KV_OK) return rc;
       if ((rc = page_map(s, pl.few, a.v, pages, dev, &tv)) != KV_OK) return rc;
     }
     e = pl.few ? launch_chunk_few(s->dtype, pl.rows, a, tk, tv, pl.ctas, st)
-               : launch_chunk_mma(s->dtype, pl.rows, pl.q8, a, tk, tv, pl.ctas, st);
+               : launch_chunk_mma(s->dtype, pl.wide, pl.q8, a, tq, tk, tv, pl.ctas, st);
   } else {
     e = launch_chunk_core(a, is_q8, pl.rows, pl.ctas, st);
   }

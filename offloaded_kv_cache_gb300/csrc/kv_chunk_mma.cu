@@ -207,7 +207,8 @@ __device__ __forceinline__ void q8_expand(uint4 w, uint32_t f, uint32_t (&x)[8],
 
 template <class T, int kMode>
 __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
-    chunk_mma_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tk,
+    chunk_mma_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tq,
+                     const __grid_constant__ CUtensorMap tk,
                      const __grid_constant__ CUtensorMap tv) {
   using Sh = Shape<kMode>;
   constexpr bool kTurns = Sh::kTurns, kQ8 = Sh::kQ8;
@@ -257,7 +258,8 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
   const uint32_t tmem = ctl.tmem;
   pdl_wait();
   if (tid == 0) a.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
-  share_init(a, Sh::kRows, kTile, &ctl.share, ctl.red);
+  const int rt = a.row_tile, unit_rows = rt * Sh::kQTiles;
+  share_init(a, unit_rows, kTile, &ctl.share, ctl.red);
   const Waiter wait{&ctl.abort, a.status, a.wait_limit_ns};
   const auto &share = ctl.share;
   const int group = warp >> 2;  // softmax group (warps 0-7)
@@ -275,7 +277,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
   auto next_list = [&]() -> bool {
     __syncthreads();
     if (tid == 0) {
-      share_next(a, Sh::kRows, kTile, &ctl.share);
+      share_next(a, unit_rows, kTile, &ctl.share);
       if (*reinterpret_cast<volatile int *>(&ctl.abort)) ctl.share.nseg = 0;
     }
     __syncthreads();
@@ -305,13 +307,15 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
       const int nseg = share.nseg;
       for (int sg = 0; sg < nseg && live; ++sg) {
         const ChunkSeg g = share.seg[sg];
-        const int urow = kTurns ? row : x * 128 + row;  // row of the unit
-        const bool active = kTurns || x == 0 || g.nrows > 128;
+        const int r_lo = kTurns ? 0 : x * rt;  // the group's rows of the unit
+        const int urow = r_lo + row;
+        const bool mine = row < rt && urow < g.nrows;
+        const bool active = kTurns || x == 0 || g.nrows > rt;
         if (!active) {
           tiles_loaded += g.tile_hi - g.tile_lo;
           continue;
         }
-        const bool any_row = (kTurns ? 0 : x * 128) + (warp & 3) * 32 < g.nrows;
+        const bool any_row = (warp & 3) * 32 < min(rt, g.nrows - r_lo);
         const int t = g.len - g.n + (g.r0 + min(urow, g.nrows - 1)) / a.G;
         float m = -INFINITY, l = 0.f;
         bool begun = false;
@@ -466,7 +470,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 32; ++i) o[i] += f1 == 0.f ? 0.f : o1[i] * f1;
             }
-            if (urow < g.nrows) {
+            if (mine) {
               if (whole) {
 #pragma unroll
                 for (int i = 0; i < 32; i += 8)
@@ -481,7 +485,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
               }
             }
           }
-          if (urow < g.nrows) {
+          if (mine) {
             if (!whole && (!kTurns || x == 0)) {
               a.part_ml[2 * prow] = M;
               a.part_ml[2 * prow + 1] = l;
@@ -598,7 +602,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
           u.hi = g.tile_hi;
           u.from = g.edge_from;
           u.upto = g.edge_upto;
-          u.two = g.nrows > 128;
+          u.two = g.nrows > rt;
         };
         Cur c;
         c.sg = 0;
@@ -823,7 +827,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
       const int ch = lane & 15, half = lane >> 4;  // 16 bytes of row 2 i + half
       for (int sg = 0; sg < nseg && live; ++sg) {
         const ChunkSeg g = share.seg[sg];
-        for (int x = 0; x < Sh::kQTiles && x * 128 < g.nrows; ++x) {
+        for (int x = 0; x < Sh::kQTiles && x * rt < g.nrows; ++x) {
           if ((q_uses >> x) & 1) {
             if (!wait(smem_u32(&ctl.q_free[x]), (q_ph >> x) & 1)) {
               live = false;
@@ -832,8 +836,22 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
             q_ph ^= 1u << x;
           }
           q_uses |= 1u << x;
+          if (a.q_tma) {
+            // row_tile / G tokens of G heads; behind the sequence's end come
+            // rows that nobody reads
+            if (lane == 0) {
+              const uint32_t bar = smem_u32(&ctl.q_full[x]);
+              const uint32_t dst = smem_u32(q_area) + x * Sh::kQBytes;
+              const int tok = g.q0 + (g.r0 + x * rt) / a.G;
+              mbar_arrive_expect_tx(bar, 2 * rt * 128);
+              tma_load_3d(dst, &tq, 0, g.kvh * a.G, tok, bar);
+              tma_load_3d(dst + Sh::kQRows * 128, &tq, 64, g.kvh * a.G, tok, bar);
+            }
+            __syncwarp();
+            continue;
+          }
           const uint32_t q = smem_u32(q_area) + x * Sh::kQBytes + (ch >> 3) * Sh::kQRows * 128;
-          const int pr = g.r0 + x * 128 + half, left = g.nrows - x * 128;
+          const int pr = g.r0 + x * rt + half, left = min(rt, g.nrows - x * rt);
           int hd = pr % a.G;
           const T *src = static_cast<const T *>(a.q) +
                          ((long long)(g.q0 + pr / a.G) * a.Hq + g.kvh * a.G + hd) * kHeadDim +
@@ -882,6 +900,12 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
       for (int i = 0; i < kStages; ++i)
         mbar_wait(smem_u32(&ctl.full[i]), i < ld.s ? ld.ph : ld.ph ^ 1, a.wait_limit_ns);
     }
+    if (warp == 11 && a.q_tma) {
+      // q_full's phase in flight: as many as there were uses
+      for (int x = 0; x < Sh::kQTiles; ++x)
+        if ((q_uses >> x) & 1)
+          mbar_wait(smem_u32(&ctl.q_full[x]), (q_ph >> x) & 1, a.wait_limit_ns);
+    }
     if (warp == 9 && lane == 0) {
       tc_commit(smem_u32(&ctl.drain));
       mbar_wait(smem_u32(&ctl.drain), 0, a.wait_limit_ns);
@@ -896,30 +920,30 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
 }
 
 template <class T, int kMode>
-cudaError_t mma_go(const ChunkArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
-                   cudaStream_t st) {
+cudaError_t mma_go(const ChunkArgs &a, const CUtensorMap &tq, const CUtensorMap &tk,
+                   const CUtensorMap &tv, int ctas, cudaStream_t st) {
   constexpr int bytes = smem_bytes<kMode>();
   const cudaError_t e = cudaFuncSetAttribute(
       chunk_mma_kernel<T, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
   return launch_pdl(chunk_mma_kernel<T, kMode>, dim3(ctas), dim3(Shape<kMode>::kThreads), bytes,
-                    st, a, tk, tv);
+                    st, a, tq, tk, tv);
 }
 template <class T>
-cudaError_t mma_type(int rows, bool q8, const ChunkArgs &a, const CUtensorMap &tk,
-                     const CUtensorMap &tv, int ctas, cudaStream_t st) {
-  if (q8) return mma_go<T, kPair8>(a, tk, tv, ctas, st);
-  return rows == 128 ? mma_go<T, kPair>(a, tk, tv, ctas, st)
-                     : mma_go<T, kWide>(a, tk, tv, ctas, st);
+cudaError_t mma_type(bool wide, bool q8, const ChunkArgs &a, const CUtensorMap &tq,
+                     const CUtensorMap &tk, const CUtensorMap &tv, int ctas, cudaStream_t st) {
+  if (q8) return mma_go<T, kPair8>(a, tq, tk, tv, ctas, st);
+  return wide ? mma_go<T, kWide>(a, tq, tk, tv, ctas, st)
+              : mma_go<T, kPair>(a, tq, tk, tv, ctas, st);
 }
 
 }  // namespace
 
-cudaError_t launch_chunk_mma(int dtype, int rows, bool q8, const ChunkArgs &a,
-                             const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
-                             cudaStream_t st) {
-  return dtype == KV_F16 ? mma_type<__half>(rows, q8, a, tk, tv, ctas, st)
-                         : mma_type<__nv_bfloat16>(rows, q8, a, tk, tv, ctas, st);
+cudaError_t launch_chunk_mma(int dtype, bool wide, bool q8, const ChunkArgs &a,
+                             const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                             int ctas, cudaStream_t st) {
+  return dtype == KV_F16 ? mma_type<__half>(wide, q8, a, tq, tk, tv, ctas, st)
+                         : mma_type<__nv_bfloat16>(wide, q8, a, tq, tk, tv, ctas, st);
 }
 
 }  // namespace kvs

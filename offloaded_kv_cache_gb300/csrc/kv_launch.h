@@ -81,11 +81,11 @@ cudaError_t launch_combine_lists(const float *part_o, const float *part_ml, cons
 // shares the work is cut into
 struct ChunkArgs;
 cudaError_t launch_chunk_core(const ChunkArgs &a, bool q8, int rows, int ctas, cudaStream_t st);
-// 16-bit q on the tensor cores: 16-bit K/V in units of 256 or 128 rows, or the
-// 8-bit cache (in device memory) in units of 64; the maps are of 16-bit K/V
-cudaError_t launch_chunk_mma(int dtype, int rows, bool q8, const ChunkArgs &a,
-                             const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
-                             cudaStream_t st);
+// 16-bit q on the tensor cores: 16-bit K/V in units of two Q tiles (wide) or of
+// one, or the 8-bit cache (in device memory); the maps are of q and 16-bit K/V
+cudaError_t launch_chunk_mma(int dtype, bool wide, bool q8, const ChunkArgs &a,
+                             const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                             int ctas, cudaStream_t st);
 // 16-bit q over the 8-bit cache in device memory, units of 8 or 16 rows; the
 // maps are of the codes
 cudaError_t launch_chunk_few(int dtype, int rows, const ChunkArgs &a, const CUtensorMap &tk,
