@@ -75,7 +75,7 @@ template <int kMode> struct Control {
   using Sh = Shape<kMode>;
   uint64_t full[Sh::kStages], empty[Sh::kStages];
   uint64_t raw_full[Sh::kQ8 ? Sh::kRaw : 1], raw_empty[Sh::kQ8 ? Sh::kRaw : 1];
-  uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_done[2], mend[2], mended[2];
+  uint64_t q_full[2], q_free[2], s_full[2], p_half[2], p_full[2], o_done[2], mend[2], mended[2];
   uint64_t joined, read, drain;
   uint32_t tmem;
   int abort;      // a wait ran out: every role leaves
@@ -101,19 +101,23 @@ static_assert(smem_bytes<kPair8>() <= 227 * 1024, "shared memory");
 // What the V of a tile needs before the product reads it.
 struct Mend {
   int zero_lo, zero_hi;  // token rows past the end in the last page
-  int scan;              // rows [0, scan): some row does not see some of them
+  // rows that some row of the unit does not see: [0, lo_end) before its last
+  // row's window, [hi, hi_end) behind its first row's token
+  int lo_end, hi, hi_end;
+  __device__ __forceinline__ bool scans() const { return lo_end > 0 || hi < hi_end; }
 };
 __device__ __forceinline__ Mend mend_of(const ChunkArgs &a, const ChunkSeg &g, int tile) {
   const int tok0 = tile * kTile;
-  Mend m{0, 0, 0};
+  Mend m{0, 0, 0, 0, 0};
   const int valid = min(kTile, g.len - tok0);
-  if (valid < kTile && (g.len & (a.ps - 1)) != 0 && valid > 0) {
+  if (valid <= 0) return m;
+  if (valid < kTile && (g.len & (a.ps - 1)) != 0) {
     m.zero_lo = valid;
     m.zero_hi = min(kTile, ((g.len + a.ps - 1) & -a.ps) - tok0);
   }
-  if (valid > 0 &&
-      (tok0 + valid - 1 > g.t_first || (a.window > 0 && tok0 <= g.t_last - a.window)))
-    m.scan = valid;
+  m.hi = max(0, g.t_first + 1 - tok0);
+  m.hi_end = valid;
+  if (a.window > 0) m.lo_end = min(m.hi < valid ? m.hi : valid, g.t_last - a.window + 1 - tok0);
   return m;
 }
 __device__ __forceinline__ bool at_edge(const ChunkSeg &g, int tile) {
@@ -129,13 +133,66 @@ template <> struct NonFinite<__nv_bfloat16> {
   static constexpr uint32_t kMask = 0x7F807F80u, kOne = 0x00800080u;
 };
 
+__device__ __forceinline__ uint32_t times_zero(uint32_t x, uint32_t acc, __half) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(acc));
+  return r;
+}
+__device__ __forceinline__ uint32_t times_zero(uint32_t x, uint32_t acc, __nv_bfloat16) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(acc));
+  return r;
+}
+// Zeroes the infinities and NaN in rows [r0, r1) of a V tile (the warp does
+// it together) and says whether this lane found any.  x * 0 + 0 is NaN for
+// those alone, so one packed operation per two elements looks them over, with
+// eight sums apart to keep the operations independent.
+template <class T>
+__device__ __forceinline__ bool clean_rows(uint8_t *v, int r0, int r1, int lane) {
+  bool found = false;
+  for (int slab = 0; slab < 2; ++slab) {
+    // where in its row a chunk of 16 bytes sits does not matter here
+    uint4 *at = reinterpret_cast<uint4 *>(v + slab * kSlab) + r0 * 8;
+    const int chunks = (r1 - r0) * 8;
+    for (int i0 = lane; i0 < chunks; i0 += 256) {
+      uint32_t acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (i0 + 32 * k < chunks) {
+          const uint4 w = at[i0 + 32 * k];
+          acc[(2 * k) & 7] = times_zero(w.x, acc[(2 * k) & 7], T{});
+          acc[(2 * k + 1) & 7] = times_zero(w.y, acc[(2 * k + 1) & 7], T{});
+          acc[(2 * k) & 7] = times_zero(w.z, acc[(2 * k) & 7], T{});
+          acc[(2 * k + 1) & 7] = times_zero(w.w, acc[(2 * k + 1) & 7], T{});
+        }
+      }
+      uint32_t any = 0;  // NaN has bits, +-0 at most the signs
+#pragma unroll
+      for (int k = 0; k < 8; ++k) any |= acc[k] & 0x7FFF7FFFu;
+      if (!any) continue;
+      found = true;
+      constexpr uint32_t M = NonFinite<T>::kMask, O = NonFinite<T>::kOne;
+#pragma unroll 1
+      for (int i = i0; i < min(chunks, i0 + 256); i += 32) {
+        uint32_t *u = reinterpret_cast<uint32_t *>(at + i);
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t b = ((u[k] & M) + O) & 0x80008000u;
+          if (b & 0x8000u) u[k] &= 0xFFFF0000u;
+          if (b & 0x80000000u) u[k] &= 0x0000FFFFu;
+        }
+      }
+    }
+  }
+  return found;
+}
+
 // Rows that see a non-finite V of a scanned tile (8-bit: a NaN vector of any
 // tile) get NaN in its channels [c0, c1): the cache is read again.
 template <class T, bool kQ8>
 __device__ __noinline__ void poison_row(const ChunkArgs &a, const ChunkSeg &g, int t, int c0,
                                         int c1, T *out, float *part) {
   for (int tile = g.tile_lo; tile < g.tile_hi; ++tile) {
-    if (!kQ8 && mend_of(a, g, tile).scan == 0) continue;
+    if (!kQ8 && !mend_of(a, g, tile).scans()) continue;
     const int lo = max(tile * kTile, a.window > 0 ? t - a.window + 1 : 0);
     const int hi = min(min(tile * kTile + kTile - 1, t), g.len - 1);
     for (int j = lo; j <= hi; ++j) {
@@ -240,6 +297,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
       mbar_init(smem_u32(&ctl.q_full[x]), 1);
       mbar_init(smem_u32(&ctl.q_free[x]), 1);
       mbar_init(smem_u32(&ctl.s_full[x]), 1);
+      mbar_init(smem_u32(&ctl.p_half[x]), 4);
       mbar_init(smem_u32(&ctl.p_full[x]), 4);
       mbar_init(smem_u32(&ctl.o_done[x]), 1);
       mbar_init(smem_u32(&ctl.mend[x]), 1);
@@ -397,12 +455,21 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
                 p[i] = pack2(p0, p1, T{});
               }
               tmem_st16(s_at + 16 * c, p);
+              if (c == 1) {
+                // the product starts with the first 64 tokens' weights
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ctl.p_half[x]));
+              }
             }
             float sum0, sum1;
             f2_unpack(f2_add(sum2, sum2b), sum0, sum1);
             l += sum0 + sum1;
             tc_wait_st();
             tc_fence_before();
+          } else if (lane == 0) {
+            mbar_arrive(smem_u32(&ctl.p_half[x]));
           }
           begun = true;
           __syncwarp();
@@ -456,6 +523,19 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
           f0 *= inv;
           f1 *= inv;
           const uint32_t o0 = tmem + lanes + 256 + (kTurns ? 0 : x * 128) + c0;
+          // rows of this lane's quad, for the transposed stores
+          T *quad_out[4];
+          bool quad_mine[4];
+          if (whole) {
+            const uint32_t valid = __ballot_sync(0xFFFFFFFFu, mine);
+            const unsigned long long at = reinterpret_cast<unsigned long long>(out);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int src = (lane & ~3) + k;
+              quad_out[k] = reinterpret_cast<T *>(__shfl_sync(0xFFFFFFFFu, at, src));
+              quad_mine[k] = (valid >> src) & 1;
+            }
+          }
 #pragma unroll
           for (int c = 0; c < kCols; c += 32) {
             float o[32];
@@ -470,27 +550,48 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 32; ++i) o[i] += f1 == 0.f ? 0.f : o1[i] * f1;
             }
-            if (mine) {
-              if (whole) {
+            if (whole) {
+              // A lane holds four 16-byte chunks of its row.  Transposed among
+              // the quad's lanes, a store writes 64 bytes in a row instead of 16.
+              uint32_t h[4][4];  // [chunk][word]
 #pragma unroll
-                for (int i = 0; i < 32; i += 8)
-                  *reinterpret_cast<uint4 *>(out + c0 + c + i) = make_uint4(
-                      pack2(o[i], o[i + 1], T{}), pack2(o[i + 2], o[i + 3], T{}),
-                      pack2(o[i + 4], o[i + 5], T{}), pack2(o[i + 6], o[i + 7], T{}));
-              } else {
+              for (int k = 0; k < 4; ++k)
 #pragma unroll
-                for (int i = 0; i < 32; i += 4)
-                  *reinterpret_cast<float4 *>(part + c0 + c + i) =
-                      make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                for (int i = 0; i < 4; ++i)
+                  h[k][i] = pack2(o[8 * k + 2 * i], o[8 * k + 2 * i + 1], T{});
+#pragma unroll
+              for (int step = 1; step < 4; step *= 2) {
+                const bool up = lane & step;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  if (k & step) continue;
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    const uint32_t give = up ? h[k][i] : h[k + step][i];
+                    const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, give, step);
+                    (up ? h[k][i] : h[k + step][i]) = got;
+                  }
+                }
               }
+#pragma unroll
+              for (int k = 0; k < 4; ++k)  // row k of the quad, chunk lane & 3
+                if (quad_mine[k])
+                  *reinterpret_cast<uint4 *>(quad_out[k] + c0 + c + 8 * (lane & 3)) =
+                      make_uint4(h[k][0], h[k][1], h[k][2], h[k][3]);
+            } else if (mine) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<float4 *>(part + c0 + c + i) =
+                    make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
             }
           }
+          __syncwarp();  // a row's poisoned channels are written after its quad's stores
           if (mine) {
             if (!whole && (!kTurns || x == 0)) {
               a.part_ml[2 * prow] = M;
               a.part_ml[2 * prow + 1] = l;
             }
-            if (*reinterpret_cast<volatile int *>(&ctl.poison))
+            if (*reinterpret_cast<volatile int *>(&ctl.poison))  // (seldom)
               poison_row<T, kQ8>(a, share.seg[sg], t, c0, c0 + kCols, out, part);
           }
           tc_fence_before();
@@ -623,6 +724,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
         };
         const uint32_t full0 = smem_u32(&ctl.full[0]), empty0 = smem_u32(&ctl.empty[0]);
         const uint32_t s_full0 = smem_u32(&ctl.s_full[0]), p_full0 = smem_u32(&ctl.p_full[0]);
+        const uint32_t p_half0 = smem_u32(&ctl.p_half[0]);
         const uint32_t o_done0 = smem_u32(&ctl.o_done[0]), mend0 = smem_u32(&ctl.mend[0]);
         const uint32_t mended0 = smem_u32(&ctl.mended[0]);
         const uint32_t q_full0 = smem_u32(&ctl.q_full[0]), q_free0 = smem_u32(&ctl.q_free[0]);
@@ -665,15 +767,18 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
               mend_ph ^= 1u << x;
             }
           }
-          if (!wait(p_full0 + 8 * x, (p_ph >> x) & 1)) return false;
-          p_ph ^= 1u << x;
-          tc_fence_after();
           const uint64_t b0 = dv + (uint64_t)(r.s * (kTileBytes >> 4));
           const bool add = p.tile > p.lo;
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            umma_ts(tmem + 256 + x * 128, tmem + x * 128 + k * 8, b0 + k * (2048 >> 4), id_pv,
-                    add || k > 0);
+          for (int h = 0; h < 2; ++h) {
+            if (!wait((h ? p_full0 : p_half0) + 8 * x, (p_ph >> x) & 1)) return false;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 4 * h; k < 4 * h + 4; ++k)
+              umma_ts(tmem + 256 + x * 128, tmem + x * 128 + k * 8, b0 + k * (2048 >> 4), id_pv,
+                      add || k > 0);
+          }
+          p_ph ^= 1u << x;
           tc_commit(o_done0 + 8 * x);
           if (kTurns || x == 1 || !p.two) tc_commit(empty0 + 8 * r.s);
           return true;
@@ -722,34 +827,10 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
             *reinterpret_cast<uint4 *>(v + (ch >> 3) * kSlab + swz(tok, ch & 7)) =
                 make_uint4(0, 0, 0, 0);
           }
-          // m.scan rows of 16 chunks of 16 bytes; where in the row a chunk
-          // sits does not matter here.  Eight loads before the first test.
-          constexpr uint32_t M = NonFinite<T>::kMask, O = NonFinite<T>::kOne;
-          for (int slab = 0; slab < 2; ++slab) {
-            uint4 *at = reinterpret_cast<uint4 *>(v + slab * kSlab);
-            const int chunks = m.scan * 8;
-            for (int i0 = lane; i0 < chunks; i0 += 256) {
-              uint4 w[8];
-              uint32_t any = 0;
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                w[k] = i0 + 32 * k < chunks ? at[i0 + 32 * k] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                any |= ((w[k].x & M) + O) | ((w[k].y & M) + O) | ((w[k].z & M) + O) |
-                       ((w[k].w & M) + O);
-              if (!(any & 0x80008000u)) continue;
-              *reinterpret_cast<volatile int *>(&ctl.poison) = 1;
-#pragma unroll 1
-              for (int i = i0; i < min(chunks, i0 + 256); i += 32) {
-                uint32_t *u = reinterpret_cast<uint32_t *>(at + i);
-                for (int k = 0; k < 4; ++k) {
-                  const uint32_t b = ((u[k] & M) + O) & 0x80008000u;
-                  if (b & 0x8000u) u[k] &= 0xFFFF0000u;
-                  if (b & 0x80000000u) u[k] &= 0x0000FFFFu;
-                }
-              }
-            }
+          if (m.scans()) {
+            bool bad = clean_rows<T>(v, m.hi, m.hi_end, lane);
+            if (m.lo_end > 0) bad |= clean_rows<T>(v, 0, m.lo_end, lane);
+            if (bad) *reinterpret_cast<volatile int *>(&ctl.poison) = 1;
           }
           fence_async_shared();
           __syncwarp();
