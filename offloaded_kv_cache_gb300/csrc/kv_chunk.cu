@@ -51,7 +51,7 @@ __device__ __forceinline__ void cached8(const void *base, const uint8_t *scale, 
 }
 
 template <int MR, bool Q8>
-__global__ void __launch_bounds__(kThreads) chunk_core_kernel(const ChunkArgs a) {
+__global__ void __launch_bounds__(kThreads) chunk_core_kernel(const __grid_constant__ ChunkArgs a) {
   using Sh = Shape<MR>;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ ChunkShare<16> share;

@@ -104,6 +104,7 @@ __device__ __forceinline__ long long head_tiles(const ChunkArgs &a, const ChunkS
                                                 int tile) {
   const int R = packed_rows(a, s);
   long long w = 0;
+#pragma unroll 1
   for (int r0 = 0; r0 < R; r0 += rows) {
     const TileRange t = unit_tiles(a, s, r0, min(rows, R - r0), tile);
     w += t.hi - t.lo;
@@ -124,6 +125,7 @@ __device__ __forceinline__ void share_init(const ChunkArgs &a, int rows, int til
                                            ChunkShare<kSegs> *sh, long long *red) {
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, nw = blockDim.x >> 5;
   long long mine = 0;
+#pragma unroll 1
   for (int b = t; b < a.B; b += blockDim.x)
     mine += head_tiles(a, chunk_seq(a, b, blockIdx.x == 0), rows, tile);
   mine = warp_sum(mine);
@@ -131,6 +133,7 @@ __device__ __forceinline__ void share_init(const ChunkArgs &a, int rows, int til
   __syncthreads();
   if (t == 0) {
     long long w = 0;
+#pragma unroll 1
     for (int i = 0; i < nw; ++i) w += red[i];
     w *= a.Hkv;
     const long long n = min((long long)gridDim.x, w), i = min((long long)blockIdx.x, n);
@@ -148,6 +151,7 @@ __device__ __forceinline__ void share_init(const ChunkArgs &a, int rows, int til
   if (warp == 0) {
     long long base = 0;
     const long long want = sh->lo;
+#pragma unroll 1
     for (int b0 = 0; b0 < a.B; b0 += 32) {
       const int b = b0 + lane;
       ChunkSeq s{0, 0, 0};
@@ -168,6 +172,7 @@ __device__ __forceinline__ void share_init(const ChunkArgs &a, int rows, int til
         rem %= hw;
         int r0 = 0;
         const int R = packed_rows(a, s);
+#pragma unroll 1
         for (;; r0 += rows) {
           const TileRange t2 = unit_tiles(a, s, r0, min(rows, R - r0), tile);
           if (rem < t2.hi - t2.lo || r0 + rows >= R) break;
@@ -196,6 +201,7 @@ __device__ __forceinline__ void share_next(const ChunkArgs &a, int rows, int til
     long long left = sh->left;
     ChunkSeq s = chunk_seq(a, b, false);
     int R = packed_rows(a, s);
+#pragma unroll 1
     while (n < kSegs && left > 0) {
       const int nrows = min(rows, R - r0);
       const TileRange t = unit_tiles(a, s, r0, nrows, tile);
@@ -233,6 +239,7 @@ __device__ __forceinline__ void share_next(const ChunkArgs &a, int rows, int til
         if (++kvh == a.Hkv) {
           kvh = 0;
           s.n = 0;
+#pragma unroll 1
           while (left > 0 && ++b < a.B) {
             s = chunk_seq(a, b, false);
             if (s.n > 0) break;
@@ -262,17 +269,20 @@ __device__ __forceinline__ int vis_lo(int t, int tile0, int window) {
   return window > 0 ? t - window + 1 - tile0 : 0;
 }
 
-// A bounded wait of a whole warp or a lane; false once anything has timed out.
+// A bounded wait of a whole warp or a lane; false once anything has timed out
+// (the kernel records that at its end).  Kept short: a kernel whose roles do
+// not fit the instruction cache together stalls on fetches.
 struct Waiter {
   volatile int *abort;
-  int *status;
   unsigned long long limit;
   __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
     if (mbar_try_wait(bar, parity)) return true;
-    if (*abort) return false;
-    if (mbar_wait(bar, parity, limit)) return true;
-    flag_error(status, KV_ERR_DEVICE_TIMEOUT);
-    *abort = 1;
+    const uint64_t t0 = global_ns();
+#pragma unroll 1
+    while (!*abort) {
+      if (mbar_try_wait(bar, parity)) return true;
+      if (global_ns() - t0 > limit) *abort = 1;
+    }
     return false;
   }
 };
@@ -286,8 +296,12 @@ template <int kStages> struct Ring {
       ph ^= 1;
     }
   }
-  __device__ __forceinline__ void next(int n) {
-    for (int i = 0; i < n; ++i) next();
+  __device__ __forceinline__ void next(int n) {  // n <= kStages
+    s += n;
+    if (s >= kStages) {
+      s -= kStages;
+      ph ^= 1;
+    }
   }
 };
 

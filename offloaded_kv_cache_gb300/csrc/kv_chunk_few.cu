@@ -83,7 +83,7 @@ __device__ __forceinline__ uint32_t f16_hi(uint32_t w) {
 // Rows of a unit: 8 NB.
 template <class T, int NB>
 __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
-    chunk_few_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tk,
+    chunk_few_kernel(const __grid_constant__ ChunkArgs a, const __grid_constant__ CUtensorMap tk,
                      const __grid_constant__ CUtensorMap tv) {
   constexpr int kRows = 8 * NB;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -108,11 +108,11 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
   pdl_wait();
   if (tid == 0) a.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
   share_init(a, kRows, kTile, &sh.share, sh.red);
-  const Waiter wait{&sh.abort, a.status, a.wait_limit_ns};
+  const Waiter wait{&sh.abort, a.wait_limit_ns};
   // the next list of segments; all threads ask together
-  auto next_list = [&]() -> bool {
+  auto next_list = [&](bool list) -> bool {
     __syncthreads();
-    if (tid == 0) {
+    if (list && tid == 0) {
       share_next(a, kRows, kTile, &sh.share);
       if (*reinterpret_cast<volatile int *>(&sh.abort)) sh.share.nseg = 0;
     }
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
     const int npg = kTile / pt;
     const int rows_total = (int)(a.nphys * a.Hkv * a.ps);
     int filled = 0;
-    while (next_list()) {
+    while (next_list(false)) {
       bool live = true;
       const int nseg = sh.share.nseg;
       for (int sg = 0; sg < nseg && live; ++sg) {
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
     // ----------------------------------------------------------- consumers
     const int g8 = lane >> 2, t4 = lane & 3;  // row and column group of the fragments
     uint32_t join_ph = 0;
-    while (next_list()) {
+    while (next_list(true)) {
       bool live = true;
       const int nseg = sh.share.nseg;
       for (int sg = 0; sg < nseg && live; ++sg) {
@@ -452,6 +452,8 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
       }
     }
   }
+  if (tid == 0 && *reinterpret_cast<volatile int *>(&sh.abort))
+    flag_error(a.status, KV_ERR_DEVICE_TIMEOUT);
   pdl_trigger();
 }
 

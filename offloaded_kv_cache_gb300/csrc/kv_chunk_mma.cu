@@ -220,6 +220,14 @@ __device__ __noinline__ void poison_row(const ChunkArgs &a, const ChunkSeg &g, i
   }
 }
 
+// bits lo .. hi of 32 columns, less those of the two 16-token pages in `bad`
+__device__ __forceinline__ uint32_t visible_bits(int lo, int hi, uint32_t bad) {
+  const uint32_t upto = hi < 0 ? 0u : hi >= 31 ? ~0u : (2u << hi) - 1u;
+  const uint32_t from = lo <= 0 ? ~0u : lo > 31 ? 0u : ~0u << lo;
+  const uint32_t out = ((bad & 1) ? 0xFFFFu : 0u) | ((bad & 2) ? 0xFFFF0000u : 0u);
+  return upto & from & ~out;
+}
+
 template <class T> __device__ __forceinline__ constexpr float weight_bias() { return 0.f; }
 template <> __device__ __forceinline__ constexpr float weight_bias<__half>() { return 7.f; }
 
@@ -264,7 +272,7 @@ __device__ __forceinline__ void q8_expand(uint4 w, uint32_t f, uint32_t (&x)[8],
 
 template <class T, int kMode>
 __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
-    chunk_mma_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tq,
+    chunk_mma_kernel(const __grid_constant__ ChunkArgs a, const __grid_constant__ CUtensorMap tq,
                      const __grid_constant__ CUtensorMap tk,
                      const __grid_constant__ CUtensorMap tv) {
   using Sh = Shape<kMode>;
@@ -274,7 +282,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
   uint8_t *q_area = smem;
   uint8_t *ring = smem + Sh::kRingAt;
   Control<kMode> &ctl = *reinterpret_cast<Control<kMode> *>(smem + Sh::kTileArea);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   if (smem_u32(smem) & 1023u) {  // the swizzled tiles need it
     if (tid == 0) flag_error(a.status, KV_ERR_INVALID_ARG);
     return;
@@ -318,7 +326,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
   if (tid == 0) a.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
   const int rt = a.row_tile, unit_rows = rt * Sh::kQTiles;
   share_init(a, unit_rows, kTile, &ctl.share, ctl.red);
-  const Waiter wait{&ctl.abort, a.status, a.wait_limit_ns};
+  const Waiter wait{&ctl.abort, a.wait_limit_ns};
   const auto &share = ctl.share;
   const int group = warp >> 2;  // softmax group (warps 0-7)
 
@@ -332,9 +340,9 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
   uint32_t q_uses = 0;           // bit x: the Q tile has been used before
 
   // the next list of segments; all threads ask together
-  auto next_list = [&]() -> bool {
+  auto next_list = [&](bool list) -> bool {
     __syncthreads();
-    if (tid == 0) {
+    if (list && tid == 0) {
       share_next(a, unit_rows, kTile, &ctl.share);
       if (*reinterpret_cast<volatile int *>(&ctl.abort)) ctl.share.nseg = 0;
     }
@@ -354,7 +362,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
   }
   if (warp < 8) {
     // --------------------------------------------------------------- softmax
-    while (next_list()) {
+    while (next_list(true)) {
       const int x = group;
       const int row = (warp & 3) * 32 + lane;
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -383,11 +391,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
             break;
           }
           s_ph ^= 1;
-          // the product of the tile before (it came before this tile's scores)
-          if (begun && !wait(smem_u32(&ctl.o_done[x]), o_ph ^ 1)) {
-            live = false;
-            break;
-          }
+          // (and every product issued before: O holds the tiles before this one)
           const uint32_t seq = tiles_loaded + (uint32_t)(tile - g.tile_lo);
           if (any_row) {
             tc_fence_after();
@@ -396,18 +400,16 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
             for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, s + 32 * c);
             tc_wait_ld();
             const int tok0 = tile * kTile;
-            int hi = vis_hi(t, tok0), lo = vis_lo(t, tok0, a.window);
+            const int hi = vis_hi(t, tok0), lo = vis_lo(t, tok0, a.window);
             const uint32_t bad = ctl.bad[seq & 7];
             if (!__all_sync(0xFFFFFFFFu, hi >= kTile - 1 && lo <= 0) || bad) {
-              int span = hi - lo;
-              if (span < 0) {
-                lo = kTile;
-                span = 0;
-              }
 #pragma unroll
-              for (int c = 0; c < 128; ++c) {
-                const bool see = (uint32_t)(c - lo) <= (uint32_t)span && !((bad >> (c >> 4)) & 1);
-                s[c] = see ? s[c] : -INFINITY;
+              for (int w = 0; w < 4; ++w) {
+                const uint32_t see = visible_bits(lo - 32 * w, hi - 32 * w, bad >> (2 * w));
+                if (__all_sync(0xFFFFFFFFu, see == ~0u)) continue;
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                  s[32 * w + c] = (see >> c) & 1 ? s[32 * w + c] : -INFINITY;
               }
             }
             float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
@@ -474,14 +476,15 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
           begun = true;
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&ctl.p_full[x]));
-          // the product of this tile, for the wait after the last one
-          o_ph ^= 1;
         }
         if (!live) break;
         tiles_loaded += g.tile_hi - g.tile_lo;
-        if (begun && !wait(smem_u32(&ctl.o_done[x]), o_ph ^ 1)) {
-          live = false;
-          break;
+        if (begun) {
+          if (!wait(smem_u32(&ctl.o_done[x]), o_ph)) {
+            live = false;
+            break;
+          }
+          o_ph ^= 1;
         }
         tc_fence_after();
         float M = m == -INFINITY ? -INFINITY : m * sc - weight_bias<T>();
@@ -536,7 +539,9 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
               quad_mine[k] = (valid >> src) & 1;
             }
           }
-#pragma unroll
+          // (code that runs once per unit is kept short: its instructions are
+          // fetched each time)
+#pragma unroll 1
           for (int c = 0; c < kCols; c += 32) {
             float o[32];
             tmem_ld32(o0 + c, o);
@@ -610,7 +615,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
     }
   } else if (warp == 8) {
     // ---------------------------------------------------------------- loader
-    while (next_list()) {
+    while (next_list(false)) {
       const int npg = kTile / a.ps;
       const int rows_total = (int)(a.nphys * a.Hkv * a.ps);
       const uint32_t full0 = smem_u32(&ctl.full[0]), empty0 = smem_u32(&ctl.empty[0]);
@@ -686,123 +691,141 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
     }
   } else if (warp == 9) {
     // -------------------------------------------------------------- products
-    while (next_list()) {
-      if (lane == 0) {
-        constexpr uint32_t id_qk = umma_idesc<T>(128, 128, false);
-        constexpr uint32_t id_pv = umma_idesc<T>(128, 128, true);
-        // a position in the list, with what is needed of its segment in registers
-        struct Cur {
-          int sg, tile, lo, hi, from, upto;
-          bool two;
-        };
-        const int nseg = share.nseg;
-        auto enter = [&](Cur &u) {
-          if (u.sg >= nseg) return;
-          const ChunkSeg &g = share.seg[u.sg];
-          u.tile = u.lo = g.tile_lo;
-          u.hi = g.tile_hi;
-          u.from = g.edge_from;
-          u.upto = g.edge_upto;
-          u.two = g.nrows > rt;
-        };
-        Cur c;
-        c.sg = 0;
-        enter(c);
-        Cur p = c;
-        auto active = [&](int x, const Cur &u) {
-          return x == 0 || (kTurns ? u.tile + 1 < u.hi : u.two);
-        };
-        auto edge = [&](const Cur &u, int tile) { return tile >= u.from || tile <= u.upto; };
-        auto advance = [&](Cur &u, Ring<kStages> &r) {
-          const int step = kTurns && active(1, u) ? 2 : 1;
-          r.next(2 * step);
-          u.tile += step;
-          if (u.tile >= u.hi) {
-            ++u.sg;
-            enter(u);
+    // The whole warp walks the list, so that positions and descriptors are
+    // uniform values; one lane issues.
+    while (next_list(false)) {
+      constexpr uint32_t id_qk = umma_idesc<T>(128, 128, false);
+      constexpr uint32_t id_pv = umma_idesc<T>(128, 128, true);
+      constexpr uint32_t hi = umma_desc_hi(1024);
+      constexpr int kQSlab = Sh::kQRows * 128;
+      // a position in the list, with what is needed of its segment in registers
+      struct Cur {
+        int sg, tile, lo, hi, from, upto;
+        bool two;
+      };
+      const int nseg = uniform(share.nseg);
+      auto enter = [&](Cur &u) {
+        if (u.sg >= nseg) return;
+        const ChunkSeg &g = share.seg[u.sg];
+        u.tile = u.lo = uniform(g.tile_lo);
+        u.hi = uniform(g.tile_hi);
+        u.from = uniform(g.edge_from);
+        u.upto = uniform(g.edge_upto);
+        u.two = uniform(g.nrows) > rt;
+      };
+      Cur c, p;  // of the next scores, and of the weights that follow
+      c.sg = 0;
+      enter(c);
+      p = c;
+      auto active = [&](int x, const Cur &u) {
+        return x == 0 || (kTurns ? u.tile + 1 < u.hi : u.two);
+      };
+      auto edge = [&](const Cur &u, int tile) { return tile >= u.from || tile <= u.upto; };
+      auto advance = [&](Cur &u, Ring<kStages> &r) {
+        const int step = kTurns && active(1, u) ? 2 : 1;
+        r.next(2 * step);
+        u.tile += step;
+        if (u.tile >= u.hi) {
+          ++u.sg;
+          enter(u);
+        }
+      };
+      auto ready = [&](uint32_t bar, uint32_t parity) -> bool {
+        return __all_sync(0xFFFFFFFFu, wait(bar, parity));
+      };
+      const uint32_t ctl0 = smem_u32(&ctl);
+      auto at = [&](const uint64_t &bar) {
+        return ctl0 + (uint32_t)(reinterpret_cast<const uint8_t *>(&bar) -
+                                 reinterpret_cast<const uint8_t *>(&ctl));
+      };
+      const uint32_t full0 = at(ctl.full[0]), empty0 = at(ctl.empty[0]);
+      const uint32_t dq = umma_desc_lo(smem_u32(q_area), 16);
+      const uint32_t dk = umma_desc_lo(smem_u32(ring), 16);
+      const uint32_t dv = umma_desc_lo(smem_u32(ring), kSlab);
+      auto issue_qk = [&](auto xc) -> bool {
+        constexpr int x = decltype(xc)::value, qx = kTurns ? 0 : x;
+        Ring<kStages> r = qk;
+        if (kTurns) r.next(2 * x);
+        if (c.tile == c.lo && (!kTurns || x == 0)) {
+          if (!ready(at(ctl.q_full[qx]), (q_ph >> qx) & 1)) return false;
+          q_ph ^= 1u << qx;
+        }
+        if ((kTurns || x == 0) && !ready(full0 + 8 * r.s, r.ph)) return false;
+        tc_fence_after();
+        const uint32_t a0 = dq + qx * (Sh::kQBytes >> 4), b0 = dk + r.s * (kTileBytes >> 4);
+        const int tile = c.tile + (kTurns ? x : 0);
+        const bool last = tile + 1 == c.hi, frees = kTurns || x == 1 || !c.two;
+        const bool mend = !kQ8 && (kTurns || x == 0) && edge(c, tile);
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            umma_ss(tmem + x * 128, a0 + (((k >> 2) * kQSlab + (k & 3) * 32) >> 4),
+                    b0 + (((k >> 2) * kSlab + (k & 3) * 32) >> 4), hi, hi, id_qk, k > 0);
+          // (also says that every product issued before is done)
+          tc_commit(at(ctl.s_full[x]));
+          if (last) tc_commit(at(ctl.q_free[qx]));
+          if (frees) tc_commit(empty0 + 8 * r.s);
+          if (mend) mbar_arrive(at(ctl.mend[x]));
+        }
+        __syncwarp();
+        return true;
+      };
+      auto issue_pv = [&](auto xc) -> bool {
+        constexpr int x = decltype(xc)::value;
+        Ring<kStages> r = pv;
+        r.next(1 + (kTurns ? 2 * x : 0));
+        const int tile = p.tile + (kTurns ? x : 0);
+        if (kTurns || x == 0) {
+          if (!ready(full0 + 8 * r.s, r.ph)) return false;
+          if (!kQ8 && edge(p, tile)) {
+            if (!ready(at(ctl.mended[x]), (mend_ph >> x) & 1)) return false;
+            mend_ph ^= 1u << x;
           }
-        };
-        const uint32_t full0 = smem_u32(&ctl.full[0]), empty0 = smem_u32(&ctl.empty[0]);
-        const uint32_t s_full0 = smem_u32(&ctl.s_full[0]), p_full0 = smem_u32(&ctl.p_full[0]);
-        const uint32_t p_half0 = smem_u32(&ctl.p_half[0]);
-        const uint32_t o_done0 = smem_u32(&ctl.o_done[0]), mend0 = smem_u32(&ctl.mend[0]);
-        const uint32_t mended0 = smem_u32(&ctl.mended[0]);
-        const uint32_t q_full0 = smem_u32(&ctl.q_full[0]), q_free0 = smem_u32(&ctl.q_free[0]);
-        const uint64_t dq = umma_desc(smem_u32(q_area), 16, 1024);
-        constexpr int kQSlab = Sh::kQRows * 128;
-        const uint64_t dk = umma_desc(smem_u32(ring), 16, 1024);
-        const uint64_t dv = umma_desc(smem_u32(ring), kSlab, 1024);
-        auto issue_qk = [&](int x) -> bool {
-          const int qx = kTurns ? 0 : x;
-          Ring<kStages> r = qk;
-          if (kTurns) r.next(2 * x);
-          if (c.tile == c.lo && (!kTurns || x == 0)) {
-            if (!wait(q_full0 + 8 * qx, (q_ph >> qx) & 1)) return false;
-            q_ph ^= 1u << qx;
-          }
-          if (!wait(full0 + 8 * r.s, r.ph)) return false;
+        }
+        const uint32_t b0 = dv + r.s * (kTileBytes >> 4);
+        const uint32_t add = p.tile > p.lo;
+        const bool last = tile + (kTurns ? 2 : 1) >= p.hi, frees = kTurns || x == 1 || !p.two;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (!ready(h ? at(ctl.p_full[x]) : at(ctl.p_half[x]), (p_ph >> x) & 1)) return false;
           tc_fence_after();
-          const uint64_t a0 = dq + (uint64_t)(qx * (Sh::kQBytes >> 4));
-          const uint64_t b0 = dk + (uint64_t)(r.s * (kTileBytes >> 4));
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint64_t qa = ((k >> 2) * kQSlab + (k & 3) * 32) >> 4;
-            const uint64_t ka = ((k >> 2) * kSlab + (k & 3) * 32) >> 4;
-            umma_ss(tmem + x * 128, a0 + qa, b0 + ka, id_qk, k > 0);
-          }
-          tc_commit(s_full0 + 8 * x);
-          const int tile = c.tile + (kTurns ? x : 0);
-          if (tile + 1 == c.hi) tc_commit(q_free0 + 8 * qx);
-          if (kTurns || x == 1 || !c.two) tc_commit(empty0 + 8 * r.s);
-          if (!kQ8 && (kTurns || x == 0) && edge(c, tile)) mbar_arrive(mend0 + 8 * x);
-          return true;
-        };
-        auto issue_pv = [&](int x) -> bool {
-          Ring<kStages> r = pv;
-          r.next(1 + (kTurns ? 2 * x : 0));
-          if (kTurns || x == 0) {
-            if (!wait(full0 + 8 * r.s, r.ph)) return false;
-            if (!kQ8 && edge(p, p.tile + (kTurns ? x : 0))) {
-              if (!wait(mended0 + 8 * x, (mend_ph >> x) & 1)) return false;
-              mend_ph ^= 1u << x;
-            }
-          }
-          const uint64_t b0 = dv + (uint64_t)(r.s * (kTileBytes >> 4));
-          const bool add = p.tile > p.lo;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (!wait((h ? p_full0 : p_half0) + 8 * x, (p_ph >> x) & 1)) return false;
-            tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
             for (int k = 4 * h; k < 4 * h + 4; ++k)
-              umma_ts(tmem + 256 + x * 128, tmem + x * 128 + k * 8, b0 + k * (2048 >> 4), id_pv,
-                      add || k > 0);
+              umma_ts(tmem + 256 + x * 128, tmem + x * 128 + k * 8, b0 + k * (2048 >> 4), hi,
+                      id_pv, k > 0 ? 1u : add);
+            if (h) {
+              if (last) tc_commit(at(ctl.o_done[x]));
+              if (frees) tc_commit(empty0 + 8 * r.s);
+            }
           }
-          p_ph ^= 1u << x;
-          tc_commit(o_done0 + 8 * x);
-          if (kTurns || x == 1 || !p.two) tc_commit(empty0 + 8 * r.s);
-          return true;
-        };
-        bool live = issue_qk(0) && (!active(1, c) || issue_qk(1));
-        if (live) advance(c, qk);
-        while (live && p.sg < nseg) {
-          // the next tile's scores follow at once, but those of a new unit
-          // only behind this tile's products: they wait for its Q
-          const bool more = c.sg < nseg, same = more && c.sg == p.sg;
-          live = issue_pv(0);
-          if (live && same) live = issue_qk(0);
-          if (live && active(1, p)) live = issue_pv(1);
-          if (live && same && active(1, c)) live = issue_qk(1);
-          if (live && more && !same) live = issue_qk(0) && (!active(1, c) || issue_qk(1));
-          if (more) advance(c, qk);
-          advance(p, pv);
+          __syncwarp();
         }
+        p_ph ^= 1u << x;
+        return true;
+      };
+      // Step by step: the products of tile p's weights, and the scores of the
+      // tile behind it.  Those of a new unit come only behind both of p's: they
+      // wait for its Q.
+      const std::integral_constant<int, 0> x0;
+      const std::integral_constant<int, 1> x1;
+      bool have = false;
+      while (have || c.sg < nseg) {
+        const bool more = c.sg < nseg, same = have && more && c.sg == p.sg;
+        if (have && !issue_pv(x0)) break;
+        if (same && !issue_qk(x0)) break;
+        if (have && active(1, p) && !issue_pv(x1)) break;
+        if (same && active(1, c) && !issue_qk(x1)) break;
+        if (more && !same && (!issue_qk(x0) || (active(1, c) && !issue_qk(x1)))) break;
+        p = c;
+        pv = qk;
+        have = more;
+        if (more) advance(c, qk);
       }
-      __syncwarp();
     }
   } else if (warp == 10) {
     // ---------------------------------------------------------------- mender
-    while (next_list()) {
+    while (next_list(false)) {
       bool live = true;
       const int nseg = share.nseg;
       for (int sg = 0; sg < nseg && live; ++sg) {
@@ -846,7 +869,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
     // order, so that the eight meet distinct banks).
     if constexpr (kQ8) {
       const int ct = tid - 384, c16 = ct & 7, row0 = ct >> 3;
-      while (next_list()) {
+      while (next_list(false)) {
         bool live = true;
         const int nseg = share.nseg;
         for (int sg = 0; sg < nseg && live; ++sg) {
@@ -902,7 +925,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
     }
   } else {
     // -------------------------------------------------------------- Q loader
-    while (next_list()) {
+    while (next_list(false)) {
       bool live = true;
       const int nseg = share.nseg;
       const int ch = lane & 15, half = lane >> 4;  // 16 bytes of row 2 i + half
@@ -970,6 +993,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
   }
   pdl_trigger();
   if (ctl.abort) {
+    if (tid == 0) flag_error(a.status, KV_ERR_DEVICE_TIMEOUT);
     // leave no copy and no product in flight: every slot's last copy (slots
     // before ld.s were filled in this lap of the ring, the others in the one
     // before), and a last commit
@@ -987,8 +1011,8 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
         if ((q_uses >> x) & 1)
           mbar_wait(smem_u32(&ctl.q_full[x]), (q_ph >> x) & 1, a.wait_limit_ns);
     }
-    if (warp == 9 && lane == 0) {
-      tc_commit(smem_u32(&ctl.drain));
+    if (warp == 9) {
+      if (elect_one()) tc_commit(smem_u32(&ctl.drain));
       mbar_wait(smem_u32(&ctl.drain), 0, a.wait_limit_ns);
     }
   }
