@@ -441,19 +441,15 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
             if (move) m = mx;
             const float base = m == -INFINITY ? 0.f : m * sc - weight_bias<T>();
             const uint64_t sc2 = f2_pack(sc, sc), base2 = f2_pack(-base, -base);
-            uint64_t sum2 = 0, sum2b = 0;  // pairs of zeros
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               uint32_t p[16];
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
-                float p0, p1;
-                f2_unpack(f2_fma(f2_pack(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), sc2, base2),
-                          p0, p1);
+                float &p0 = s[32 * c + 2 * i], &p1 = s[32 * c + 2 * i + 1];
+                f2_unpack(f2_fma(f2_pack(p0, p1), sc2, base2), p0, p1);
                 p0 = ex2(p0);
                 p1 = ex2(p1);
-                if (i & 1) sum2b = f2_add(sum2b, f2_pack(p0, p1));
-                else sum2 = f2_add(sum2, f2_pack(p0, p1));
                 p[i] = pack2(p0, p1, T{});
               }
               tmem_st16(s_at + 16 * c, p);
@@ -465,17 +461,23 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
                 if (lane == 0) mbar_arrive(smem_u32(&ctl.p_half[x]));
               }
             }
-            float sum0, sum1;
-            f2_unpack(f2_add(sum2, sum2b), sum0, sum1);
-            l += sum0 + sum1;
             tc_wait_st();
             tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ctl.p_full[x]));
+            // the sum, while the product runs
+            uint64_t sum[4] = {0, 0, 0, 0};  // pairs of zeros
+#pragma unroll
+            for (int c = 0; c < 128; c += 2)
+              sum[(c >> 1) & 3] = f2_add(sum[(c >> 1) & 3], f2_pack(s[c], s[c + 1]));
+            float sum0, sum1;
+            f2_unpack(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])), sum0, sum1);
+            l += sum0 + sum1;
           } else if (lane == 0) {
             mbar_arrive(smem_u32(&ctl.p_half[x]));
+            mbar_arrive(smem_u32(&ctl.p_full[x]));
           }
           begun = true;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&ctl.p_full[x]));
         }
         if (!live) break;
         tiles_loaded += g.tile_hi - g.tile_lo;
