@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kThreads) chunk_core_kernel(const __grid_const
   using Sh = Shape<MR>;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ ChunkShare<16> share;
-  __shared__ long long red[33];
+  __shared__ int red[32];
   __shared__ int tok_ok[kTile];
   float *Qs = reinterpret_cast<float *>(smem);
   float *Ks = Qs + Sh::kRows * kQStr;
@@ -212,50 +212,106 @@ __global__ void __launch_bounds__(kThreads) chunk_core_kernel(const __grid_const
       }
     }
   }
-  pdl_trigger();
 }
 
 // Joins the parts of every unit that several CTAs share: CTA i of the
 // attention left part 2 i + 1, the CTAs i + 1 .. j parts 2 (i + 1) .. 2 j.  A
-// warp takes a row, a lane four channels.
-template <class T>
-__global__ void __launch_bounds__(256) chunk_combine_kernel(const ChunkArgs a) {
-  pdl_wait();
-  const int4 u = a.meta[2 * blockIdx.x];
-  if (u.x < 0) return;
-  const int4 w = a.meta[2 * blockIdx.x + 1];
-  const int first = blockIdx.x, last = w.y, lane = threadIdx.x & 31;
-  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < u.w; r += gridDim.y * 8) {
-    float M = -INFINITY;
-    for (int j = first + lane; j <= last; j += 32) {
-      const int slot = j == first ? 2 * j + 1 : 2 * j;
-      M = fmaxf(M, a.part_ml[2 * ((long long)slot * a.slot_rows + r)]);
+// lane takes four channels, a warp four rows, so that the loads of four rows
+// are in flight together (one row at a time took three times as long).  Few
+// parts: each warp joins all parts of its rows (of one, when there are no more
+// rows than that).  Many (a long context and few rows): the block's warps share
+// the parts of four rows.
+constexpr int kJoinRows = 4;
+struct Joined {
+  float m, l;
+  float4 o;
+};
+__device__ __forceinline__ void join_one(Joined &a, float m, float l, const float4 &o) {
+  const float M = fmaxf(a.m, m), base = M == -INFINITY ? 0.f : M;
+  const float f = ex2(a.m - base), h = ex2(m - base);
+  a.m = M;
+  a.l = a.l * f + l * h;
+  a.o = make_float4(a.o.x * f + o.x * h, a.o.y * f + o.y * h, a.o.z * f + o.z * h,
+                    a.o.w * f + o.w * h);
+}
+// rows r0 .. r0 + 3 of the parts first_part, first_part + step, .. up to CTA `last`
+template <int R>
+__device__ __forceinline__ void join_rows(const ChunkArgs &a, int first, int last, int from,
+                                          int step, int r0, int nrows, int lane,
+                                          Joined (&acc)[R]) {
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+    acc[i] = Joined{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll (8 / R)
+  for (int j = from; j <= last; j += step) {
+    const long long row0 = (long long)(j == first ? 2 * j + 1 : 2 * j) * a.slot_rows + r0;
+    float2 ml[R];
+    float4 o[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const long long row = row0 + min(i, nrows - 1 - r0);
+      ml[i] = *reinterpret_cast<const float2 *>(a.part_ml + 2 * row);
+      o[i] = *reinterpret_cast<const float4 *>(a.part_o + row * kHeadDim + lane * 4);
     }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, off));
-    const float base = M == -INFINITY ? 0.f : M;
-    float L = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int j = first; j <= last; ++j) {
-      const long long row = (long long)(j == first ? 2 * j + 1 : 2 * j) * a.slot_rows + r;
-      const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + 2 * row);
-      const float4 x = *reinterpret_cast<const float4 *>(a.part_o + row * kHeadDim + lane * 4);
-      const float f = ex2(ml.x - base);
-      L += ml.y * f;
-      o.x += x.x * f;
-      o.y += x.y * f;
-      o.z += x.z * f;
-      o.w += x.w * f;
+    for (int i = 0; i < R; ++i) join_one(acc[i], ml[i].x, ml[i].y, o[i]);
+  }
+}
+template <class T>
+__device__ __forceinline__ void join_store(const ChunkArgs &a, const int4 &u, int q0, int r,
+                                           int lane, const Joined &x) {
+  const float inv = x.l == 0.f ? 0.f : 1.f / x.l;
+  const int pr = u.z + r, row = q0 + pr / a.G, head = u.y * a.G + pr % a.G;
+  T *dst = static_cast<T *>(a.out) + ((long long)row * a.Hq + head) * kHeadDim + lane * 4;
+  if constexpr (std::is_same_v<T, float>)
+    *reinterpret_cast<float4 *>(dst) =
+        make_float4(x.o.x * inv, x.o.y * inv, x.o.z * inv, x.o.w * inv);
+  else
+    *reinterpret_cast<uint2 *>(dst) =
+        make_uint2(pack2(x.o.x * inv, x.o.y * inv, T{}), pack2(x.o.z * inv, x.o.w * inv, T{}));
+}
+template <class T>
+__global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constant__ ChunkArgs a) {
+  __shared__ Joined part[8][kJoinRows][32];
+  pdl_wait();
+  const int4 u = a.meta[2 * blockIdx.x], w = a.meta[2 * blockIdx.x + 1];
+  if (u.x < 0) return;
+  const int first = blockIdx.x, last = w.y, nrows = u.w;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (last - first < 8 && nrows <= 8 * (int)gridDim.y) {
+    const int r = blockIdx.y * 8 + warp;
+    if (r >= nrows) return;
+    Joined one[1];
+    join_rows(a, first, last, first, 1, r, nrows, lane, one);
+    join_store<T>(a, u, w.x, r, lane, one[0]);
+    return;
+  }
+  Joined acc[kJoinRows];
+  if (last - first < 8) {
+    for (int r0 = (blockIdx.y * 8 + warp) * kJoinRows; r0 < nrows;
+         r0 += gridDim.y * 8 * kJoinRows) {
+      join_rows(a, first, last, first, 1, r0, nrows, lane, acc);
+#pragma unroll
+      for (int i = 0; i < kJoinRows; ++i)
+        if (r0 + i < nrows) join_store<T>(a, u, w.x, r0 + i, lane, acc[i]);
     }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    const int pr = u.z + r, row = w.x + pr / a.G, head = u.y * a.G + pr % a.G;
-    T *dst = static_cast<T *>(a.out) + ((long long)row * a.Hq + head) * kHeadDim + lane * 4;
-    if constexpr (std::is_same_v<T, float>)
-      *reinterpret_cast<float4 *>(dst) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-    else
-      *reinterpret_cast<uint2 *>(dst) =
-          make_uint2(pack2(o.x * inv, o.y * inv, T{}), pack2(o.z * inv, o.w * inv, T{}));
+    return;
+  }
+  for (int r0 = blockIdx.y * kJoinRows; r0 < nrows; r0 += gridDim.y * kJoinRows) {
+    join_rows(a, first, last, first + warp, 8, r0, nrows, lane, acc);
+#pragma unroll
+    for (int i = 0; i < kJoinRows; ++i) part[warp][i][lane] = acc[i];
+    __syncthreads();
+    if (warp < kJoinRows && r0 + warp < nrows) {
+      Joined x = part[0][warp][lane];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) {
+        const Joined &y = part[i][warp][lane];
+        join_one(x, y.m, y.l, y.o);
+      }
+      join_store<T>(a, u, w.x, r0 + warp, lane, x);
+    }
+    __syncthreads();
   }
 }
 
@@ -275,7 +331,7 @@ cudaError_t launch_chunk_core(const ChunkArgs &a, bool q8, int rows, int ctas, c
 }
 
 cudaError_t launch_chunk_combine(int dtype, const ChunkArgs &a, int ctas, cudaStream_t st) {
-  const dim3 grid(ctas, std::min(32, (a.slot_rows + 7) / 8)), block(256);
+  const dim3 grid(ctas, std::min(8, (a.slot_rows + kJoinRows - 1) / kJoinRows)), block(256);
   return dtype == KV_F32   ? launch_pdl(chunk_combine_kernel<float>, grid, block, 0, st, a)
          : dtype == KV_F16 ? launch_pdl(chunk_combine_kernel<__half>, grid, block, 0, st, a)
                            : launch_pdl(chunk_combine_kernel<__nv_bfloat16>, grid, block, 0, st, a);

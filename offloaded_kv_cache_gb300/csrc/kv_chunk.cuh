@@ -88,11 +88,12 @@ struct ChunkSeg {
 
 // A CTA's share, kSegs segments of it listed at a time.
 template <int kSegs> struct ChunkShare {
-  long long work, lo, hi;  // all tiles; this CTA's share
+  // (the host refuses calls whose tiles might not fit int32)
+  int per, extra;          // tiles per share; the first `extra` shares hold one more
+  int hi;                  // end of this CTA's share in the units laid end to end
   int b, kvh, r0, off;     // walk: the next unit, and its tiles already passed
-  long long left;          // tiles of the share not listed yet
+  int left;                // tiles of the share not listed yet
   int nseg;
-  int ctas;                // CTAs with a share: no more than there are tiles
   ChunkSeg seg[kSegs];
 };
 
@@ -100,10 +101,10 @@ __device__ __forceinline__ int packed_rows(const ChunkArgs &a, const ChunkSeq &s
   return s.n * a.G;  // checked on the host against int32 (max_q_len * G)
 }
 // tiles of all row blocks of one kv head of sequence s
-__device__ __forceinline__ long long head_tiles(const ChunkArgs &a, const ChunkSeq &s, int rows,
-                                                int tile) {
+__device__ __forceinline__ int head_tiles(const ChunkArgs &a, const ChunkSeq &s, int rows,
+                                          int tile) {
   const int R = packed_rows(a, s);
-  long long w = 0;
+  int w = 0;
 #pragma unroll 1
   for (int r0 = 0; r0 < R; r0 += rows) {
     const TileRange t = unit_tiles(a, s, r0, min(rows, R - r0), tile);
@@ -112,36 +113,29 @@ __device__ __forceinline__ long long head_tiles(const ChunkArgs &a, const ChunkS
   return w;
 }
 
-__device__ __forceinline__ long long warp_sum(long long x) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, off);
-  return x;
-}
-
 // Every thread of the CTA: the total work, this CTA's share and where it
-// starts.  red: 33 long longs of shared scratch.
+// starts.  red: 32 ints of shared scratch.
 template <int kSegs>
 __device__ __forceinline__ void share_init(const ChunkArgs &a, int rows, int tile,
-                                           ChunkShare<kSegs> *sh, long long *red) {
+                                           ChunkShare<kSegs> *sh, int *red) {
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, nw = blockDim.x >> 5;
-  long long mine = 0;
+  int mine = 0;
 #pragma unroll 1
   for (int b = t; b < a.B; b += blockDim.x)
     mine += head_tiles(a, chunk_seq(a, b, blockIdx.x == 0), rows, tile);
-  mine = warp_sum(mine);
+  mine = __reduce_add_sync(0xFFFFFFFFu, mine);
   if (lane == 0) red[warp] = mine;
   __syncthreads();
   if (t == 0) {
-    long long w = 0;
+    int w = 0;
 #pragma unroll 1
     for (int i = 0; i < nw; ++i) w += red[i];
     w *= a.Hkv;
-    const long long n = min((long long)gridDim.x, w), i = min((long long)blockIdx.x, n);
-    sh->work = w;
-    sh->ctas = (int)n;
-    sh->lo = n > 0 ? w * i / n : 0;
-    sh->hi = i < n ? w * (i + 1) / n : sh->lo;
-    sh->left = sh->hi - sh->lo;
+    const int n = gridDim.x, i = blockIdx.x;
+    sh->per = w / n;
+    sh->extra = w % n;
+    sh->left = sh->per + (i < sh->extra ? 1 : 0);
+    sh->hi = sh->per * i + min(i, sh->extra) + sh->left;
     sh->b = -1;
     sh->nseg = 0;
   }
@@ -149,26 +143,26 @@ __device__ __forceinline__ void share_init(const ChunkArgs &a, int rows, int til
   if (sh->left == 0) return;
   // the sequence holding tile lo: one warp walks the sequences 32 at a time
   if (warp == 0) {
-    long long base = 0;
-    const long long want = sh->lo;
+    int base = 0;
+    const int want = sh->hi - sh->left;
 #pragma unroll 1
     for (int b0 = 0; b0 < a.B; b0 += 32) {
       const int b = b0 + lane;
       ChunkSeq s{0, 0, 0};
       if (b < a.B) s = chunk_seq(a, b, false);
-      const long long hw = head_tiles(a, s, rows, tile), w = hw * a.Hkv;
-      long long inc = w;
+      const int hw = head_tiles(a, s, rows, tile), w = hw * a.Hkv;
+      int inc = w;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
-        const long long x = __shfl_up_sync(0xFFFFFFFFu, inc, off);
+        const int x = __shfl_up_sync(0xFFFFFFFFu, inc, off);
         if (lane >= off) inc += x;
       }
-      const long long first = base + inc - w;
+      const int first = base + inc - w;
       const bool here = want >= first && want < first + w;
       if (here) {
-        long long rem = want - first;
+        int rem = want - first;
         sh->b = b;
-        sh->kvh = (int)(rem / hw);
+        sh->kvh = rem / hw;
         rem %= hw;
         int r0 = 0;
         const int R = packed_rows(a, s);
@@ -179,7 +173,7 @@ __device__ __forceinline__ void share_init(const ChunkArgs &a, int rows, int til
           rem -= t2.hi - t2.lo;
         }
         sh->r0 = r0;
-        sh->off = (int)rem;
+        sh->off = rem;
       }
       if (__any_sync(0xFFFFFFFFu, here)) break;
       base += __shfl_sync(0xFFFFFFFFu, inc, 31);
@@ -198,7 +192,7 @@ __device__ __forceinline__ void share_next(const ChunkArgs &a, int rows, int til
   int n = 0;
   if (sh->left > 0) {
     int b = sh->b, kvh = sh->kvh, r0 = sh->r0, off = sh->off;
-    long long left = sh->left;
+    int left = sh->left;
     ChunkSeq s = chunk_seq(a, b, false);
     int R = packed_rows(a, s);
 #pragma unroll 1
@@ -206,7 +200,7 @@ __device__ __forceinline__ void share_next(const ChunkArgs &a, int rows, int til
       const int nrows = min(rows, R - r0);
       const TileRange t = unit_tiles(a, s, r0, nrows, tile);
       const int have = t.hi - t.lo - off;
-      const int take = (int)min((long long)have, left);
+      const int take = min(have, left);
       ChunkSeg &g = sh->seg[n++];
       g.b = b;
       g.kvh = kvh;
@@ -226,8 +220,8 @@ __device__ __forceinline__ void share_next(const ChunkArgs &a, int rows, int til
       g.edge_upto = a.window > 0 && g.t_last >= a.window ? (g.t_last - a.window) / tile : -1;
       if (g.parts == 1) {
         // the CTA whose share holds the unit's last tile
-        const long long end = sh->hi - left + (t.hi - t.lo) - 1;
-        const int j = (int)(((end + 1) * sh->ctas - 1) / sh->work);
+        const int end = sh->hi - left + (t.hi - t.lo) - 1, big = sh->extra * (sh->per + 1);
+        const int j = end < big ? end / (sh->per + 1) : sh->extra + (end - big) / sh->per;
         a.meta[2 * blockIdx.x] = make_int4(b, kvh, r0, nrows);
         a.meta[2 * blockIdx.x + 1] = make_int4(s.q0, j, 0, 0);
       }

@@ -51,6 +51,7 @@ struct ChunkPlan {
   int rows = 64;      // packed rows per unit
   int row_tile = 0;   // tensor cores: packed rows per Q tile (a unit is one, or two when wide)
   bool wide = false;
+  double most_tiles = 0;  // an upper bound of the call's (unit, KV tile) pairs
   int ctas = 1;
   int slot_rows = 1;  // rows of a partial result
   size_t off_meta = 0, off_ml = 0, off_o = 0, off_table = 0, off_k = 0, off_v = 0;
@@ -85,13 +86,20 @@ ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, bool q8) {
     }
     pl.stage = (q8 && !pl.q8) || s->kv_loc == KV_LOC_HOST_PINNED;
   } else {
-    pl.rows = packed <= 16 ? 16 : 64;
+    // units of 16 rows until they fill the GPU (33 rows over 4096 tokens: 47
+    // us in units of 64, the latency of one unit's tile, ...), then of 64,
+    // which read K and V a quarter as often
+    const double few = (double)s->batch * s->num_kv_heads * ((packed + 15) / 16) *
+                       (((double)s->max_pages_per_seq * s->page_size + tile - 1) / tile);
+    pl.rows = packed <= 16 || few <= 2.0 * sms ? 16 : 64;
   }
-  const long long blocks = (packed + pl.rows - 1) / pl.rows;
+  // units of all sequences: full ones and one more each; no more CTAs than
+  // there can be tiles
+  const double units = std::min((double)s->batch * ((packed + pl.rows - 1) / pl.rows),
+                                (double)c->total_q * G / pl.rows + s->batch);
   const long long tiles = ((long long)s->max_pages_per_seq * s->page_size + tile - 1) / tile;
-  // no more CTAs than there can be tiles
-  const double most = (double)s->batch * s->num_kv_heads * blocks * tiles;
-  pl.ctas = (int)std::min<double>((double)per_sm * sms, std::max(1.0, most));
+  pl.most_tiles = units * s->num_kv_heads * tiles;
+  pl.ctas = (int)std::min<double>((double)per_sm * sms, std::max(1.0, pl.most_tiles));
   pl.slot_rows = (int)std::min<long long>(pl.rows, packed);
   size_t off = align256((size_t)pl.ctas * 32);
   pl.off_ml = off;
@@ -217,7 +225,9 @@ int chunk_common(const kv_shape *s, const kv_chunk *c, const void *q, const void
     if ((rc = resolve_kv(s, v_cache, &a.v)) != KV_OK) return rc;
   }
   const ChunkPlan pl = make_chunk_plan(s, c, is_q8);
-  // the staged cache's rows are indexed as a cache's own
+  // the kernels count tiles in int32, and index the staged cache's rows as a
+  // cache's own
+  if (pl.most_tiles > INT_MAX) return KV_ERR_UNSUPPORTED;
   if (pl.stage_pages > INT_MAX / ((long long)s->num_kv_heads * s->page_size))
     return KV_ERR_UNSUPPORTED;
   if (!al16(workspace) || ws_bytes < pl.total) return KV_ERR_WORKSPACE;

@@ -52,7 +52,7 @@ template <int NB> struct Shared {
   int tokens[kStages];  // per stage: bit i: the pages of tokens 16 i .. + 15 are in range
   int abort, pad;
   ChunkShare<16> share;
-  long long red[33];
+  int red[32];
 };
 
 __device__ __forceinline__ uint32_t movm_t(uint32_t x) {
@@ -454,7 +454,6 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
   }
   if (tid == 0 && *reinterpret_cast<volatile int *>(&sh.abort))
     flag_error(a.status, KV_ERR_DEVICE_TIMEOUT);
-  pdl_trigger();
 }
 
 template <class T, int NB>

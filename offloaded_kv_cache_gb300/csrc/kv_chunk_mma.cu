@@ -84,7 +84,7 @@ template <int kMode> struct Control {
   uint8_t bad[8];  // per tile, bit i: tokens 16 i .. + 15 have no page
   ChunkShare<Sh::kSegs> share;
   union {
-    long long red[33];                         // share_init
+    int red[32];                         // share_init
     float2 ml[2][Sh::kTurns ? Sh::kRows : 1];  // maximum and sum of each group's rows
   };
   // per tile of codes: its scale bytes, and its rows that hold a token
@@ -993,7 +993,6 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
       }
     }
   }
-  pdl_trigger();
   if (ctl.abort) {
     if (tid == 0) flag_error(a.status, KV_ERR_DEVICE_TIMEOUT);
     // leave no copy and no product in flight: every slot's last copy (slots

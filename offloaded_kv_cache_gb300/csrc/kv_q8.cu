@@ -19,6 +19,9 @@ namespace kvs {
 namespace {
 
 constexpr int kThreads = 256;
+#ifndef KVS_APPEND_BLOCKS
+#define KVS_APPEND_BLOCKS 2432  // 16 per SM; 8: 37.3 us, 32: 36.2 us where this takes 35.0
+#endif
 constexpr int kLanesPerVec = 16;  // 8 elements a lane: 16 bytes of 16-bit data, 8 bytes of codes
 
 struct AppendArgs {
@@ -28,7 +31,7 @@ struct AppendArgs {
   int32_t *ctx_out;
   int *status;
   long long nphys;
-  int B, Hkv, ps, maxP, total_q, max_q_len;
+  int B, Hkv, ps, ps_log2, maxP, total_q, max_q_len;
   int blocks;      // blocks per sequence
   int write_lens;  // this launch writes ctx_out
 };
@@ -58,17 +61,47 @@ __device__ __forceinline__ bool pages_ok(const AppendArgs &a, int b, const RowSp
   return !__syncthreads_or(bad);
 }
 
-// Block (b, j): vectors j, j + blocks, ... of the n_b * Hkv (token, head)
-// pairs in steps of 16 vectors, K and V of each, so that two vectors per lane
-// group are in flight.  Lengths: with one block per sequence, or with
-// context_lens_out apart from context_lens, the sequence's first block writes
-// them (every read of context_lens[b] in that block comes first); a chunk of
-// several blocks updated in place takes a second launch (advance_kernel).
+// Block (b, j) walks the n_b * Hkv (token, head) pairs of its sequence in steps
+// of kSteps * 16, K and V of each pair, sixteen lanes a vector; the next step's
+// loads are issued before this step's vectors are quantised, so that the
+// round trips to the lengths and to the data are paid once per block and not
+// once per step.  Lengths: with one block per sequence, or with context_lens_out
+// apart from context_lens, the sequence's first block writes them (every read
+// of context_lens[b] in that block comes first); a chunk of several blocks
+// updated in place takes a second launch (advance_kernel).
+constexpr int kVecs = kThreads / kLanesPerVec;
+constexpr int kSteps = 2;
+template <class T> struct AppendStep {
+  uint4 w[kSteps][2][sizeof(T) / 2];
+  int page[kSteps], pos[kSteps];
+};
 template <class T>
 __global__ void __launch_bounds__(kThreads) q8_append_kernel(const AppendArgs a) {
   pdl_wait();
   const int b = blockIdx.x / a.blocks, j = blockIdx.x % a.blocks;
   const RowSpan r = append_span(a, b);
+  const int sub = threadIdx.x / kLanesPerVec, l = threadIdx.x % kLanesPerVec;
+  const int items = r.n > 0 ? r.n * a.Hkv : 0;  // <= total_q * Hq, an int32
+  const long long row0 = (long long)r.q0 * a.Hkv * kHeadDim + l * 8;
+  const T *src[2] = {static_cast<const T *>(a.k_new) + row0,
+                     static_cast<const T *>(a.v_new) + row0};
+  auto load = [&](AppendStep<T> &s, long long step) {
+#pragma unroll
+    for (int u = 0; u < kSteps; ++u) {
+      const long long it = step * (kVecs * kSteps) + u * kVecs + sub;
+      s.page[u] = -1;
+      if (it >= items) continue;
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+#pragma unroll
+        for (int c = 0; c < (int)sizeof(T) / 2; ++c)
+          s.w[u][w][c] = reinterpret_cast<const uint4 *>(src[w] + it * kHeadDim)[c];
+      s.pos[u] = r.len + (int)it / a.Hkv;
+      s.page[u] = a.bt[(long long)b * a.maxP + (s.pos[u] >> a.ps_log2)];
+    }
+  };
+  AppendStep<T> now;
+  load(now, j);
   if (j == 0) {
     const bool ok = r.n >= 0 && pages_ok(a, b, r);  // ends in a barrier when it asks
     if (threadIdx.x == 0) {
@@ -77,42 +110,42 @@ __global__ void __launch_bounds__(kThreads) q8_append_kernel(const AppendArgs a)
     }
   }
   pdl_trigger();
-  if (r.n <= 0) return;
-  const int sub = threadIdx.x / kLanesPerVec, l = threadIdx.x % kLanesPerVec;
-  constexpr int kVecs = kThreads / kLanesPerVec;
-  const long long items = (long long)r.n * a.Hkv;
   const uint32_t half_mask = 0xFFFFu << (threadIdx.x & 16);
-  const T *kn = static_cast<const T *>(a.k_new) + (long long)r.q0 * a.Hkv * kHeadDim;
-  const T *vn = static_cast<const T *>(a.v_new) + (long long)r.q0 * a.Hkv * kHeadDim;
-  for (long long it = (long long)j * kVecs + sub; it < items; it += (long long)a.blocks * kVecs) {
-    const int i = (int)(it / a.Hkv), h = (int)(it % a.Hkv);
-    const int pos = r.len + i;
-    const int ph = a.bt[(long long)b * a.maxP + pos / a.ps];
-    float x[2][8];
-    load8(kn + it * kHeadDim + l * 8, x[0]);
-    load8(vn + it * kHeadDim + l * 8, x[1]);
-    if (ph < 0 || ph >= a.nphys) continue;  // recorded by the sequence's first block
-    const long long vec = ((long long)ph * a.Hkv + h) * a.ps + pos % a.ps;
+  for (long long step = j; step * (kVecs * kSteps) < items; step += a.blocks) {
+    AppendStep<T> next;
+    load(next, step + a.blocks);
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      uint32_t top = 0;  // magnitudes order as their bits do, infinities and NaN above all
+    for (int u = 0; u < kSteps; ++u) {
+      // (a page out of range was recorded by the sequence's first block)
+      if (now.page[u] < 0 || now.page[u] >= a.nphys) continue;
+      const int it = (int)step * (kVecs * kSteps) + u * kVecs + sub;
+      const int h = it - (now.pos[u] - r.len) * a.Hkv;
+      // (rows of the cache fit int32)
+      const long long vec = (now.page[u] * a.Hkv + h) * a.ps + (now.pos[u] & (a.ps - 1));
 #pragma unroll
-      for (int c = 0; c < 8; ++c) top = max(top, __float_as_uint(x[w][c]) & 0x7FFFFFFFu);
+      for (int w = 0; w < 2; ++w) {
+        float x[8];
+        load8(reinterpret_cast<const T *>(&now.w[u][w]), x);
+        uint32_t top = 0;  // magnitudes order as their bits do, infinities and NaN above all
 #pragma unroll
-      for (int off = 8; off > 0; off >>= 1)
-        top = max(top, __shfl_xor_sync(half_mask, top, off, kLanesPerVec));
-      uint2 code = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-      int byte = kQ8NanScale;
-      if (top < 0x7F800000u) {
-        const int e = q8_exponent(top, q8_min_exp<T>());
-        const float s = pow2f(-e);
-        code.x = q8_codes4(x[w][0] * s, x[w][1] * s, x[w][2] * s, x[w][3] * s);
-        code.y = q8_codes4(x[w][4] * s, x[w][5] * s, x[w][6] * s, x[w][7] * s);
-        byte = e + 127;
+        for (int c = 0; c < 8; ++c) top = max(top, __float_as_uint(x[c]) & 0x7FFFFFFFu);
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1)
+          top = max(top, __shfl_xor_sync(half_mask, top, off, kLanesPerVec));
+        uint2 code = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+        int byte = kQ8NanScale;
+        if (top < 0x7F800000u) {
+          const int e = q8_exponent(top, q8_min_exp<T>());
+          const float s = pow2f(-e);
+          code.x = q8_codes4(x[0] * s, x[1] * s, x[2] * s, x[3] * s);
+          code.y = q8_codes4(x[4] * s, x[5] * s, x[6] * s, x[7] * s);
+          byte = e + 127;
+        }
+        *reinterpret_cast<uint2 *>((w ? a.v_codes : a.k_codes) + vec * kHeadDim + l * 8) = code;
+        if (l == 0) (w ? a.v_scale : a.k_scale)[vec] = (uint8_t)byte;
       }
-      *reinterpret_cast<uint2 *>((w ? a.v_codes : a.k_codes) + vec * kHeadDim + l * 8) = code;
-      if (l == 0) (w ? a.v_scale : a.k_scale)[vec] = (uint8_t)byte;
     }
+    now = next;
   }
 }
 
@@ -132,32 +165,32 @@ struct ReadArgs {
   const int32_t *bt, *ctx, *out_table;
   int *status;
   long long nphys, out_pages;
-  int Hkv, ps, maxP;
-  int tiles;  // 16-token tiles of a row: maxP * ps / 16
+  int Hkv, ps, ps_log2, maxP;
+  int items;   // of a sequence: (16-token tile, kv head) pairs
+  int blocks;  // per sequence
 };
 
 // Work item: (b, 16-token tile, kv head), 16 x 128 codes of K and of V.  A
 // lane takes 8 codes and writes 8 elements, so that a half-warp reads and
 // writes whole vectors; a block takes kUnits items, all loads issued before
 // the first store.
-constexpr int kUnits = 4;
+constexpr int kUnits = 2;
 template <class T>
-__global__ void __launch_bounds__(kThreads) q8_read_kernel(const ReadArgs a, long long items) {
+__global__ void __launch_bounds__(kThreads) q8_read_kernel(const ReadArgs a) {
   pdl_wait();
   const int t = threadIdx.x / kLanesPerVec, l = threadIdx.x % kLanesPerVec;
+  const int b = blockIdx.x / a.blocks, j = blockIdx.x % a.blocks;
+  const int len = a.ctx[b];
   uint2 code[kUnits][2];
   uint32_t byte[kUnits][2];
-  long long dst[kUnits];
+  int dst[kUnits];  // (rows of a cache fit int32)
 #pragma unroll
   for (int u = 0; u < kUnits; ++u) {
-    const long long it = (long long)blockIdx.x * kUnits + u;
+    const int it = j * kUnits + u;
     dst[u] = -1;
-    if (it >= items) continue;
-    const int h = (int)(it % a.Hkv);
-    const long long bt_tile = it / a.Hkv;
-    const int tile = (int)(bt_tile % a.tiles), b = (int)(bt_tile / a.tiles);
-    const int len = a.ctx[b];
-    const int pos = tile * kTileTokens + t, page = tile * kTileTokens / a.ps;
+    if (it >= a.items) continue;
+    const int tile = it / a.Hkv, h = it - tile * a.Hkv;
+    const int pos = tile * kTileTokens + t, page = (tile * kTileTokens) >> a.ps_log2;
     if (len < 0 || (long long)len > (long long)a.maxP * a.ps) {
       if (threadIdx.x == 0 && tile == 0) flag_error(a.status, KV_ERR_BOUNDS);
       continue;
@@ -171,11 +204,11 @@ __global__ void __launch_bounds__(kThreads) q8_read_kernel(const ReadArgs a, lon
       continue;
     }
     if (pos >= len) continue;
-    const long long in = ((long long)src * a.Hkv + h) * a.ps + pos % a.ps;
-    dst[u] = ((long long)to * a.Hkv + h) * a.ps + pos % a.ps;
+    const int in = (src * a.Hkv + h) * a.ps + (pos & (a.ps - 1));
+    dst[u] = (to * a.Hkv + h) * a.ps + (pos & (a.ps - 1));
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-      code[u][w] = *reinterpret_cast<const uint2 *>(a.codes[w] + in * kHeadDim + l * 8);
+      code[u][w] = *reinterpret_cast<const uint2 *>(a.codes[w] + (long long)in * kHeadDim + l * 8);
       byte[u][w] = a.scale[w][in];
     }
   }
@@ -194,7 +227,7 @@ __global__ void __launch_bounds__(kThreads) q8_read_kernel(const ReadArgs a, lon
         x[c] = lo[c] * s;
         x[4 + c] = hi[c] * s;
       }
-      store8(static_cast<T *>(a.out[w]) + dst[u] * kHeadDim + l * 8, x);
+      store8(static_cast<T *>(a.out[w]) + (long long)dst[u] * kHeadDim + l * 8, x);
     }
   }
 }
@@ -209,25 +242,24 @@ struct StageArgs {
   int32_t *table;  // [B][maxP] page in out, or null: the source's own page numbers
   int *status;
   long long nphys;
-  int Hkv, ps, maxP, tiles, total_q, max_q_len, window;
+  int Hkv, ps, ps_log2, maxP, items, blocks, total_q, max_q_len, window;
 };
 template <class T, bool Q8>
-__global__ void __launch_bounds__(kThreads) stage_kernel(const StageArgs a, long long items) {
+__global__ void __launch_bounds__(kThreads) stage_kernel(const StageArgs a) {
   pdl_wait();
   const int t = threadIdx.x / kLanesPerVec, l = threadIdx.x % kLanesPerVec;
+  const int b = blockIdx.x / a.blocks, j = blockIdx.x % a.blocks;
+  const int q0 = a.q_start[b], q1 = a.q_start[b + 1], len = a.ctx[b];
   uint4 data[kUnits][2];  // 16-bit data, or the codes in the first half
   uint32_t byte[kUnits][2];
-  long long dst[kUnits];
+  int dst[kUnits];
 #pragma unroll
   for (int u = 0; u < kUnits; ++u) {
-    const long long it = (long long)blockIdx.x * kUnits + u;
+    const int it = j * kUnits + u;
     dst[u] = -1;
-    if (it >= items) continue;
-    const int h = (int)(it % a.Hkv);
-    const long long bt_tile = it / a.Hkv;
-    const int tile = (int)(bt_tile % a.tiles), b = (int)(bt_tile / a.tiles);
-    const int tok0 = tile * kTileTokens, pos = tok0 + t, page = tok0 / a.ps;
-    const int q0 = a.q_start[b], q1 = a.q_start[b + 1], len = a.ctx[b];
+    if (it >= a.items) continue;
+    const int tile = it / a.Hkv, h = it - tile * a.Hkv;
+    const int tok0 = tile * kTileTokens, pos = tok0 + t, page = tok0 >> a.ps_log2;
     // sequences the attention skips (and records), and tokens no row sees
     if (q0 < 0 || q1 <= q0 || q1 > a.total_q || q1 - q0 > a.max_q_len || len < 0 ||
         (long long)len > (long long)a.maxP * a.ps || tok0 >= len)
@@ -241,18 +273,18 @@ __global__ void __launch_bounds__(kThreads) stage_kernel(const StageArgs a, long
     if (a.table && h == 0 && threadIdx.x == 0 && tok0 % a.ps == 0)
       a.table[row] = ok ? (int32_t)row : -1;
     if (!ok || pos >= len) continue;
-    const long long in = ((long long)src * a.Hkv + h) * a.ps + pos % a.ps;
-    dst[u] = a.table ? (row * a.Hkv + h) * a.ps + pos % a.ps : in;
+    const int in = (src * a.Hkv + h) * a.ps + (pos & (a.ps - 1));
+    dst[u] = a.table ? ((int)row * a.Hkv + h) * a.ps + (pos & (a.ps - 1)) : in;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
       if constexpr (Q8) {
         const uint2 c = *reinterpret_cast<const uint2 *>(
-            static_cast<const uint8_t *>(a.src[w]) + in * kHeadDim + l * 8);
+            static_cast<const uint8_t *>(a.src[w]) + (long long)in * kHeadDim + l * 8);
         data[u][w] = make_uint4(c.x, c.y, 0, 0);
         byte[u][w] = a.scale[w][in];
       } else {
         data[u][w] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.src[w]) +
-                                                      in * kHeadDim + l * 8);
+                                                      (long long)in * kHeadDim + l * 8);
       }
     }
   }
@@ -262,7 +294,7 @@ __global__ void __launch_bounds__(kThreads) stage_kernel(const StageArgs a, long
     if (dst[u] < 0) continue;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-      T *to = static_cast<T *>(a.out[w]) + dst[u] * kHeadDim + l * 8;
+      T *to = static_cast<T *>(a.out[w]) + (long long)dst[u] * kHeadDim + l * 8;
       if constexpr (Q8) {
         float lo[4], hi[4], x[8];
         q8_unpack4(data[u][w].x, lo);
@@ -283,6 +315,17 @@ __global__ void __launch_bounds__(kThreads) stage_kernel(const StageArgs a, long
 
 }  // namespace
 
+namespace {
+// (16-token tile, kv head) items of a sequence, and the blocks they take
+bool item_grid(int B, int maxP, int ps, int Hkv, int *items, int *blocks) {
+  const long long n = (long long)maxP * ps / kTileTokens * Hkv, k = (n + kUnits - 1) / kUnits;
+  if (n > 0x7FFFFFFFLL - kUnits || k * B > 0x7FFFFFFFLL) return false;
+  *items = (int)n;
+  *blocks = (int)k;
+  return true;
+}
+}  // namespace
+
 cudaError_t launch_chunk_stage(int dtype, bool q8, const ChunkArgs &c, void *k_out, void *v_out,
                                int32_t *table, cudaStream_t st) {
   StageArgs a = {};
@@ -300,20 +343,18 @@ cudaError_t launch_chunk_stage(int dtype, bool q8, const ChunkArgs &c, void *k_o
   a.nphys = c.nphys;
   a.Hkv = c.Hkv;
   a.ps = c.ps;
+  a.ps_log2 = __builtin_ctz(c.ps);
   a.maxP = c.maxP;
-  a.tiles = (int)((long long)c.maxP * c.ps / kTileTokens);
   a.total_q = c.total_q;
   a.max_q_len = c.max_q_len;
   a.window = c.window;
-  const long long items = (long long)c.B * a.tiles * a.Hkv;
-  const long long blocks = (items + kUnits - 1) / kUnits;
-  if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
-  const dim3 grid((unsigned)blocks), block(kThreads);
+  if (!item_grid(c.B, c.maxP, c.ps, c.Hkv, &a.items, &a.blocks)) return cudaErrorInvalidConfiguration;
+  const dim3 grid((unsigned)(a.blocks * c.B)), block(kThreads);
   if (dtype == KV_F16)
-    return q8 ? launch_pdl(stage_kernel<__half, true>, grid, block, 0, st, a, items)
-              : launch_pdl(stage_kernel<__half, false>, grid, block, 0, st, a, items);
-  return q8 ? launch_pdl(stage_kernel<__nv_bfloat16, true>, grid, block, 0, st, a, items)
-            : launch_pdl(stage_kernel<__nv_bfloat16, false>, grid, block, 0, st, a, items);
+    return q8 ? launch_pdl(stage_kernel<__half, true>, grid, block, 0, st, a)
+              : launch_pdl(stage_kernel<__half, false>, grid, block, 0, st, a);
+  return q8 ? launch_pdl(stage_kernel<__nv_bfloat16, true>, grid, block, 0, st, a)
+            : launch_pdl(stage_kernel<__nv_bfloat16, false>, grid, block, 0, st, a);
 }
 
 cudaError_t launch_q8_append(int dtype, const void *k_new, const void *v_new,
@@ -337,14 +378,15 @@ cudaError_t launch_q8_append(int dtype, const void *k_new, const void *v_new,
   a.B = B;
   a.Hkv = Hkv;
   a.ps = ps;
+  a.ps_log2 = __builtin_ctz(ps);
   a.maxP = maxP;
   a.total_q = total_q;
   a.max_q_len = max_q_len;
-  // two steps of 16 vectors per block, up to a grid of 2^30 blocks
   const long long items = (long long)std::min(max_q_len, total_q) * Hkv;
-  long long blocks = (items + 31) / 32;
-  blocks = std::max(1LL, std::min(blocks, (1LL << 30) / B));
-  a.blocks = (int)blocks;
+  // as many blocks as there are steps, up to what keeps every SM busy
+  const long long steps = (items + kVecs * kSteps - 1) / (kVecs * kSteps);
+  a.blocks = (int)std::max(1LL, std::min(steps, (KVS_APPEND_BLOCKS + B - 1LL) / B));
+  const long long blocks = a.blocks;
   const bool in_place = ctx_out && ctx_out < ctx + B && ctx < ctx_out + B;
   const bool later = in_place && blocks > 1;
   a.write_lens = ctx_out && !later;
@@ -376,15 +418,13 @@ cudaError_t launch_q8_read(int dtype, const kv_q8_cache &c, const int32_t *bt, c
   a.out_pages = out_pages;
   a.Hkv = Hkv;
   a.ps = ps;
+  a.ps_log2 = __builtin_ctz(ps);
   a.maxP = maxP;
-  a.tiles = (int)((long long)maxP * ps / kTileTokens);
-  const long long items = (long long)B * a.tiles * Hkv;
-  const long long blocks = (items + kUnits - 1) / kUnits;
-  if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
-  const dim3 grid((unsigned)blocks), block(kThreads);
-  return dtype == KV_F32   ? launch_pdl(q8_read_kernel<float>, grid, block, 0, st, a, items)
-         : dtype == KV_F16 ? launch_pdl(q8_read_kernel<__half>, grid, block, 0, st, a, items)
-                           : launch_pdl(q8_read_kernel<__nv_bfloat16>, grid, block, 0, st, a, items);
+  if (!item_grid(B, maxP, ps, Hkv, &a.items, &a.blocks)) return cudaErrorInvalidConfiguration;
+  const dim3 grid((unsigned)(a.blocks * B)), block(kThreads);
+  return dtype == KV_F32   ? launch_pdl(q8_read_kernel<float>, grid, block, 0, st, a)
+         : dtype == KV_F16 ? launch_pdl(q8_read_kernel<__half>, grid, block, 0, st, a)
+                           : launch_pdl(q8_read_kernel<__nv_bfloat16>, grid, block, 0, st, a);
 }
 
 }  // namespace kvs
