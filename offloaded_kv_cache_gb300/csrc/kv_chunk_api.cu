@@ -38,8 +38,19 @@ int resolve_q8(const kv_shape *s, const kv_q8_cache *c, kv_q8_cache *dev) {
   return KV_OK;
 }
 
+// Up to this many packed rows the 16-bit kernels' converting form reads the
+// 8-bit cache itself, in units of 64 rows; above, the cache is expanded into the
+// workspace first and read in units of 256.  (4 x 32k tokens, 8 kv heads, us,
+// direct / expanded, bf16: 64 rows 88 / 170, 128 rows 130 / 175, 192 rows 180 /
+// 184, 256 rows 224 / 185; f16: 192 rows 161 / 184, 256 rows 200 / 184.)
 #ifndef KVS_Q8_DIRECT_ROWS
-#define KVS_Q8_DIRECT_ROWS 64
+#define KVS_Q8_DIRECT_ROWS 192
+#endif
+// Up to this many rows codes are expanded in registers (kv_chunk_few.cu; the
+// same shape, against the converting form: 8 rows 50 / 96, 16 rows 70 / 84; 24
+// rows, in units of 16, 89 / 85).
+#ifndef KVS_Q8_FEW_ROWS
+#define KVS_Q8_FEW_ROWS 16
 #endif
 struct ChunkPlan {
   bool mma = false;   // tensor cores (16-bit data)
@@ -72,7 +83,7 @@ ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, bool q8) {
     tile = kChunkTile;
     per_sm = 1;
     pl.q8 = q8 && s->kv_loc == KV_LOC_HBM && packed <= KVS_Q8_DIRECT_ROWS;
-    pl.few = pl.q8 && packed <= 16;
+    pl.few = pl.q8 && packed <= KVS_Q8_FEW_ROWS;
     if (pl.few) {
       pl.rows = packed <= 8 ? 8 : 16;
       tile = 64;
