@@ -63,6 +63,7 @@ __global__ void __launch_bounds__(kThreads) chunk_core_kernel(const __grid_const
   float *Ps = Ks;
   pdl_wait();
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  const int ps_log2 = 31 - __clz(a.ps);
   if (tid == 0) a.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
   share_init(a, Sh::kRows, kTile, &share, red);
   for (;;) {
@@ -92,27 +93,43 @@ __global__ void __launch_bounds__(kThreads) chunk_core_kernel(const __grid_const
 #pragma unroll
         for (int c = 0; c < 8; ++c) o[r][c] = 0.f;
       }
+      // the pages of this thread's tokens of a tile (-1: none, -2: out of
+      // range), looked up a tile ahead
+      constexpr int kLoads = kTile * 16 / kThreads;
+      int ph[kLoads];
+      auto look_up = [&](int tile) {
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) {
+          const int pos = tile * kTile + (tid >> 4) + k * (kThreads / 16);
+          ph[k] = -1;
+          if (tile < g.tile_hi && pos < g.len) {
+            const int p = a.bt[(long long)g.b * a.maxP + (pos >> ps_log2)];
+            ph[k] = p >= 0 && p < a.nphys ? p : -2;
+          }
+        }
+      };
+      look_up(g.tile_lo);
       for (int tile = g.tile_lo; tile < g.tile_hi; ++tile) {
         const int tok0 = tile * kTile;
         // K and V of the tile; tokens past the end or of a bad page are zero
-        for (int i = tid; i < kTile * 16; i += kThreads) {
-          const int tok = i >> 4, c = (i & 15) * 8, pos = tok0 + tok;
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) {
+          const int tok = (tid >> 4) + k * (kThreads / 16), c = (tid & 15) * 8;
           float kx[8] = {}, vx[8] = {};
-          bool ok = pos < g.len;
+          const bool ok = ph[k] >= 0;
           if (ok) {
-            const int ph = a.bt[(long long)g.b * a.maxP + pos / a.ps];
-            ok = ph >= 0 && ph < a.nphys;
-            if (!ok && c == 0) flag_error(a.status, KV_ERR_BOUNDS);
-            if (ok) {
-              const long long vec = ((long long)ph * a.Hkv + g.kvh) * a.ps + pos % a.ps;
-              cached8<Q8>(a.k, a.k_scale, vec, c, kx);
-              cached8<Q8>(a.v, a.v_scale, vec, c, vx);
-            }
+            // (rows of the cache fit int32)
+            const int vec = (ph[k] * a.Hkv + g.kvh) * a.ps + ((tok0 + tok) & (a.ps - 1));
+            cached8<Q8>(a.k, a.k_scale, vec, c, kx);
+            cached8<Q8>(a.v, a.v_scale, vec, c, vx);
+          } else if (ph[k] == -2 && c == 0) {
+            flag_error(a.status, KV_ERR_BOUNDS);
           }
           if (c == 0) tok_ok[tok] = ok;
           store8(Ks + tok * kQStr + c, kx);
           store8(Vs + tok * kHeadDim + c, vx);
         }
+        look_up(tile + 1);
         __syncthreads();
         float s[MR][4] = {};
 #pragma unroll 4
