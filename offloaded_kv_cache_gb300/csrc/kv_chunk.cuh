@@ -68,7 +68,8 @@ __device__ __forceinline__ TileRange unit_tiles(const ChunkArgs &a, const ChunkS
   const int t_first = s.len - s.n + r0 / a.G;
   const int t_last = s.len - s.n + (r0 + nrows - 1) / a.G;
   if (t_last < 0) return TileRange{0, 1};
-  const int lo = a.window > 0 ? max(0, t_first - a.window + 1) : 0;
+  // (t_first >= -1 here: a window may be as large as an int32)
+  const int lo = a.window > 0 ? max(0, max(t_first, -1) - a.window + 1) : 0;
   return TileRange{lo / tile, t_last / tile + 1};
 }
 
@@ -260,7 +261,7 @@ __device__ __forceinline__ int part_slot(const ChunkSeg &g) {
 // visible columns [lo, hi] of a tile starting at token tile0, for token t
 __device__ __forceinline__ int vis_hi(int t, int tile0) { return t - tile0; }
 __device__ __forceinline__ int vis_lo(int t, int tile0, int window) {
-  return window > 0 ? t - window + 1 - tile0 : 0;
+  return window > 0 ? t - tile0 - window + 1 : 0;
 }
 
 // A bounded wait of a whole warp or a lane; false once anything has timed out

@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
               const int k = i >> 1, h = i & 1;
               const int pos = tok0 + g8 + 8 * k;
               const bool see = token[k] && pos <= tq[nb][h] &&
-                               (a.window <= 0 || pos > tq[nb][h] - a.window);
+                               (a.window <= 0 || pos - tq[nb][h] > -a.window);
               z[i] = see ? s[nb][i] * (kf[k] * qf[nb][h]) : -INFINITY;
               y[i] = see ? z[i] + ev[k] : -INFINITY;
               move |= z[i] > m[nb][h] + kMoveAt || y[i] > r[nb][h] + kMoveAt;

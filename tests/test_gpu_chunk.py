@@ -222,6 +222,102 @@ def test_longer_and_many(dtype, hq, hkv, lens, news, q8):
 
 
 @pytest.mark.parametrize("q8", [False, True], ids=["own", "q8"])
+@pytest.mark.parametrize("hq,n", [(130, 1), (130, 3), (200, 2), (256, 1)])
+def test_more_heads_per_kv_head_than_a_tile_has_rows(hq, n, q8):
+    run(Problem("bf16", hq, 1, 16, [150, 33], [n, 1], 0, q8=q8))
+
+
+@pytest.mark.parametrize("n", [1, 3, 40])
+@pytest.mark.parametrize("dtype,pages,q8", [("bf16", 140_000, False), ("f32", 70_000, False),
+                                            ("f16", 270_000, True)])
+def test_offsets_past_32_bits(dtype, pages, n, q8):
+    """Pages at the end of caches of more than 4 GiB each."""
+    p = Problem(dtype, 16, 8, 16, [150, 40], [n, 1], q8=q8).upload()
+    small = p.pages
+    p.shape.num_phys_pages = pages
+    p.d_table.copy_(torch.where(p.table >= 0, p.table + (pages - small), -1))
+    big = {}
+
+    def grow(name, x):
+        big[name] = torch.empty((pages, *x.shape[1:]), dtype=x.dtype, device="cuda")
+        big[name][pages - small:] = x
+        return big[name]
+
+    if q8:
+        c, s = p.d_code, p.d_scale
+        p.cache = kv.make_q8_cache(grow("k", c["k"]), grow("v", c["v"]), grow("ks", s["k"]),
+                                   grow("vs", s["v"]))
+        p.ws = torch.empty(kv.kv_q8_chunk_workspace_bytes(p.shape, p.chunk), dtype=torch.uint8,
+                           device="cuda")
+    else:
+        p.d_k, p.d_v = grow("k", p.d_k), grow("v", p.d_v)
+    p.attend()
+    torch.cuda.synchronize()
+    check(p.d_out, *p.expected())
+
+
+@pytest.mark.parametrize("q8", [False, True], ids=["own", "q8"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_no_rows_at_all(dtype, q8):
+    """A batch none of whose sequences brings a token: nothing is written."""
+    p = Problem(dtype, 4, 2, 16, [30, 0], [0, 0], q8=q8).upload()
+    p.attend()
+    torch.cuda.synchronize()
+    assert (p.d_out == 7).all()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+def test_pages_shared_by_sequences(dtype):
+    """A common prefix held once; the rest of each sequence in pages of its own."""
+    for q8 in (False, True):
+        for loc in ("hbm", "host"):
+            p = Problem(dtype, 4, 2, 16, [100, 90, 80], [4, 1, 30], q8=q8, loc=loc)
+            p.table[1, :3] = p.table[0, :3]
+            p.table[2, :3] = p.table[0, :3]
+            run(p)
+
+
+@pytest.mark.parametrize("q8", [False, True], ids=["own", "q8"])
+@pytest.mark.parametrize("n", [1, 20, 300])
+def test_a_workspace_too_small_is_refused(n, q8):
+    p = Problem("bf16", 8, 2, 16, [400], [n], q8=q8).upload()
+    for ws in (p.ws[:-256], p.ws[:16]):
+        assert p.attend(ws=ws, check=False) == kv.KV_ERR_WORKSPACE
+    torch.cuda.synchronize()
+    assert (p.d_out == 7).all()
+
+
+@pytest.mark.parametrize("q8", [False, True], ids=["own", "q8"])
+def test_cache_memory_of_the_wrong_kind_is_refused(q8):
+    p = Problem("bf16", 8, 2, 16, [40], [2], q8=q8, loc="host").upload()
+    p.shape.kv_loc = kv.KV_LOC_HBM
+    assert p.attend(check=False) == kv.KV_ERR_LOCATION
+    p = Problem("bf16", 8, 2, 16, [40], [2], q8=q8).upload()
+    p.shape.kv_loc = kv.KV_LOC_HOST_PINNED
+    assert p.attend(check=False) in (kv.KV_ERR_LOCATION, kv.KV_ERR_WORKSPACE)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_a_chunk_in_pieces_equals_the_chunk(dtype):
+    """60 tokens at once, and as 25 + 1 + 34 on the cache as it stood then."""
+    for q8 in (False, True):
+        p = run(Problem(dtype, 4, 2, 16, [200], [60], q8=q8))
+        whole, (want, tol) = p.d_out.clone(), p.expected()
+        q = p.d_q.clone()
+        at = 0
+        for n in (25, 1, 34):
+            p.d_q[:n] = q[at:at + n]
+            p.d_start.copy_(torch.tensor([0, n], dtype=torch.int32))
+            p.d_lens.fill_(140 + at + n)
+            p.d_out.fill_(7)
+            p.attend()
+            check(p.d_out[:n], want[at:at + n], tol[at:at + n])
+            assert (p.d_out[n:] == 7).all()
+            at += n
+        check(whole, want, tol)
+
+
+@pytest.mark.parametrize("q8", [False, True], ids=["own", "q8"])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_repeats_bit_for_bit_and_in_a_graph(dtype, q8):
     p = run(Problem(dtype, 8, 2, 16, [700, 333, 12], [40, 1, 12], q8=q8))
