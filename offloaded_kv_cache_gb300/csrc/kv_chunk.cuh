@@ -83,6 +83,7 @@ struct ChunkSeg {
   // KV tiles in which some row does not see some token, or that end behind the
   // sequence inside a page: those >= edge_from and those <= edge_upto
   int edge_from, edge_upto;
+  int half_hi;            // end of the tiles that the first half of a full unit's rows sees
   __device__ __forceinline__ bool first() const { return parts & 1; }
   __device__ __forceinline__ bool whole() const { return parts == 3; }
 };
@@ -219,6 +220,8 @@ __device__ __forceinline__ void share_next(const ChunkArgs &a, int rows, int til
                     : (s.len & (a.ps - 1)) != 0 ? s.len / tile
                                                 : INT_MAX;
       g.edge_upto = a.window > 0 && g.t_last >= a.window ? (g.t_last - a.window) / tile : -1;
+      const int t_half = s.len - s.n + (r0 + min(nrows, rows / 2) - 1) / a.G;
+      g.half_hi = max(t_half, 0) / tile + 1;
       if (g.parts == 1) {
         // the CTA whose share holds the unit's last tile
         const int end = sh->hi - left + (t.hi - t.lo) - 1, big = sh->extra * (sh->per + 1);

@@ -6,8 +6,7 @@
 //   warps 0-3, 4-7  two softmax groups, a thread per packed row
 //   warp 8          loads K and V tiles (TMA, one box per page and 64 channels)
 //   warp 9          issues the matrix products (one lane)
-//   warp 10         mends V at the edges (below)
-//   warp 11         loads Q
+//   warp 10, 11     mend V at the edges (below); warp 11 loads Q
 // Per KV tile of 128 tokens and softmax group: S = Q K^T (128 x 128 x 128)
 // into TMEM; the group takes its maximum and exponentials and writes the
 // weights P in 16 bits over S; O += P V.  While one group computes, the tensor
@@ -143,43 +142,43 @@ __device__ __forceinline__ uint32_t times_zero(uint32_t x, uint32_t acc, __nv_bf
   asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(acc));
   return r;
 }
-// Zeroes the infinities and NaN in rows [r0, r1) of a V tile (the warp does
-// it together) and says whether this lane found any.  x * 0 + 0 is NaN for
-// those alone, so one packed operation per two elements looks them over, with
-// eight sums apart to keep the operations independent.
+// Zeroes the infinities and NaN in rows [r0, r1) of 64 channels of a V tile (the
+// warp does it together) and says whether this lane found any.  x * 0 + 0 is
+// NaN for those alone, so one packed operation per two elements looks them
+// over, with eight sums apart to keep the operations independent.
 template <class T>
-__device__ __forceinline__ bool clean_rows(uint8_t *v, int r0, int r1, int lane) {
+__device__ __forceinline__ bool clean_rows(uint8_t *slab, int r0, int r1, int lane) {
   bool found = false;
-  for (int slab = 0; slab < 2; ++slab) {
-    // where in its row a chunk of 16 bytes sits does not matter here
-    uint4 *at = reinterpret_cast<uint4 *>(v + slab * kSlab) + r0 * 8;
-    const int chunks = (r1 - r0) * 8;
-    for (int i0 = lane; i0 < chunks; i0 += 256) {
-      uint32_t acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (i0 + 32 * k < chunks) {
-          const uint4 w = at[i0 + 32 * k];
-          acc[(2 * k) & 7] = times_zero(w.x, acc[(2 * k) & 7], T{});
-          acc[(2 * k + 1) & 7] = times_zero(w.y, acc[(2 * k + 1) & 7], T{});
-          acc[(2 * k) & 7] = times_zero(w.z, acc[(2 * k) & 7], T{});
-          acc[(2 * k + 1) & 7] = times_zero(w.w, acc[(2 * k + 1) & 7], T{});
-        }
-      }
-      uint32_t any = 0;  // NaN has bits, +-0 at most the signs
-#pragma unroll
-      for (int k = 0; k < 8; ++k) any |= acc[k] & 0x7FFF7FFFu;
-      if (!any) continue;
-      found = true;
-      constexpr uint32_t M = NonFinite<T>::kMask, O = NonFinite<T>::kOne;
+  // where in its row a chunk of 16 bytes sits does not matter here
+  uint4 *at = reinterpret_cast<uint4 *>(slab) + r0 * 8;
+  const int chunks = (r1 - r0) * 8;
 #pragma unroll 1
-      for (int i = i0; i < min(chunks, i0 + 256); i += 32) {
-        uint32_t *u = reinterpret_cast<uint32_t *>(at + i);
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t b = ((u[k] & M) + O) & 0x80008000u;
-          if (b & 0x8000u) u[k] &= 0xFFFF0000u;
-          if (b & 0x80000000u) u[k] &= 0x0000FFFFu;
-        }
+  for (int i0 = lane; i0 < chunks; i0 += 256) {
+    uint32_t acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (i0 + 32 * k < chunks) {
+        const uint4 w = at[i0 + 32 * k];
+        acc[(2 * k) & 7] = times_zero(w.x, acc[(2 * k) & 7], T{});
+        acc[(2 * k + 1) & 7] = times_zero(w.y, acc[(2 * k + 1) & 7], T{});
+        acc[(2 * k) & 7] = times_zero(w.z, acc[(2 * k) & 7], T{});
+        acc[(2 * k + 1) & 7] = times_zero(w.w, acc[(2 * k + 1) & 7], T{});
+      }
+    }
+    uint32_t any = 0;  // NaN has bits, +-0 at most the signs
+#pragma unroll
+    for (int k = 0; k < 8; ++k) any |= acc[k] & 0x7FFF7FFFu;
+    if (!any) continue;
+    found = true;
+    constexpr uint32_t M = NonFinite<T>::kMask, O = NonFinite<T>::kOne;
+#pragma unroll 1
+    for (int i = i0; i < min(chunks, i0 + 256); i += 32) {
+      uint32_t *u = reinterpret_cast<uint32_t *>(at + i);
+#pragma unroll 1
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t b = ((u[k] & M) + O) & 0x80008000u;
+        if (b & 0x8000u) u[k] &= 0xFFFF0000u;
+        if (b & 0x80000000u) u[k] &= 0x0000FFFFu;
       }
     }
   }
@@ -309,7 +308,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
       mbar_init(smem_u32(&ctl.p_full[x]), 4);
       mbar_init(smem_u32(&ctl.o_done[x]), 1);
       mbar_init(smem_u32(&ctl.mend[x]), 1);
-      mbar_init(smem_u32(&ctl.mended[x]), 1);
+      mbar_init(smem_u32(&ctl.mended[x]), 2);
     }
     mbar_init(smem_u32(&ctl.joined), 8);
     mbar_init(smem_u32(&ctl.read), 8);
@@ -331,7 +330,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
   const int group = warp >> 2;  // softmax group (warps 0-7)
 
   // state that lives across lists of segments
-  Ring<kStages> ld;              // loader: next slot; mender: the next tile's K slot
+  Ring<kStages> ld;              // loader: next slot; menders: the next tile's K slot
   Ring<kQ8 ? Sh::kRaw : 1> raw;  // loader and converter: next tile of codes
   Ring<kStages> qk, pv;          // products: slot of the next K / of the next tile's K
   uint32_t tiles_loaded = 0;     // loader, softmax: tiles so far
@@ -376,7 +375,9 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
         const int r_lo = kTurns ? 0 : x * rt;  // the group's rows of the unit
         const int urow = r_lo + row;
         const bool mine = row < rt && urow < g.nrows;
-        const bool active = kTurns || x == 0 || g.nrows > rt;
+        // the first group's rows see no tile from half_hi on
+        const int end = !kTurns && x == 0 ? min(g.tile_hi, g.half_hi) : g.tile_hi;
+        const bool active = kTurns || (x == 0 ? r_lo < g.nrows : g.nrows > rt);
         if (!active) {
           tiles_loaded += g.tile_hi - g.tile_lo;
           continue;
@@ -385,7 +386,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
         const int t = g.len - g.n + (g.r0 + min(urow, g.nrows - 1)) / a.G;
         float m = -INFINITY, l = 0.f;
         bool begun = false;
-        for (int tile = g.tile_lo + (kTurns ? x : 0); tile < g.tile_hi; tile += kTurns ? 2 : 1) {
+        for (int tile = g.tile_lo + (kTurns ? x : 0); tile < end; tile += kTurns ? 2 : 1) {
           if (!wait(smem_u32(&ctl.s_full[x]), s_ph)) {
             live = false;
             break;
@@ -500,7 +501,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
           prow = (long long)part_slot(g) * a.slot_rows + min(urow, g.nrows - 1);
           part = a.part_o + prow * kHeadDim;
         }
-        float f0 = 1.f, f1 = 0.f;
+        float f0 = kTurns || begun ? 1.f : 0.f, f1 = 0.f;
         constexpr int kCols = kTurns ? 64 : 128;  // channels this thread writes
         const int c0 = kTurns ? 64 * x : 0;
         const bool second = kTurns && g.tile_hi - g.tile_lo > 1;
@@ -524,7 +525,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
           l = u.y * f0 + v.y * f1;
         }
         if (any_row) {
-          const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+          const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;  // (a part stays as it is)
           f0 *= inv;
           f1 *= inv;
           const uint32_t o0 = tmem + lanes + 256 + (kTurns ? 0 : x * 128) + c0;
@@ -703,7 +704,8 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
       // a position in the list, with what is needed of its segment in registers
       struct Cur {
         int sg, tile, lo, hi, from, upto;
-        bool two;
+        int hi0;   // end of the first group's tiles
+        bool two;  // the second group has rows
       };
       const int nseg = uniform(share.nseg);
       auto enter = [&](Cur &u) {
@@ -713,14 +715,15 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
         u.hi = uniform(g.tile_hi);
         u.from = uniform(g.edge_from);
         u.upto = uniform(g.edge_upto);
-        u.two = uniform(g.nrows) > rt;
+        u.two = !kTurns && uniform(g.nrows) > rt;
+        u.hi0 = u.two ? min(u.hi, uniform(g.half_hi)) : u.hi;
       };
       Cur c, p;  // of the next scores, and of the weights that follow
       c.sg = 0;
       enter(c);
       p = c;
       auto active = [&](int x, const Cur &u) {
-        return x == 0 || (kTurns ? u.tile + 1 < u.hi : u.two);
+        return kTurns ? u.tile + x < u.hi : x == 0 ? u.tile < u.hi0 : u.two;
       };
       auto edge = [&](const Cur &u, int tile) { return tile >= u.from || tile <= u.upto; };
       auto advance = [&](Cur &u, Ring<kStages> &r) {
@@ -752,12 +755,15 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
           if (!ready(at(ctl.q_full[qx]), (q_ph >> qx) & 1)) return false;
           q_ph ^= 1u << qx;
         }
-        if ((kTurns || x == 0) && !ready(full0 + 8 * r.s, r.ph)) return false;
+        const int tile = c.tile + (kTurns ? x : 0);
+        const bool leads = kTurns || x == 0 || !active(0, c);  // first to use this K
+        if (!kQ8 && leads && edge(c, tile) && elect_one()) mbar_arrive(at(ctl.mend[kTurns ? x : 0]));
+        __syncwarp();
+        if (leads && !ready(full0 + 8 * r.s, r.ph)) return false;
         tc_fence_after();
         const uint32_t a0 = dq + qx * (Sh::kQBytes >> 4), b0 = dk + r.s * (kTileBytes >> 4);
-        const int tile = c.tile + (kTurns ? x : 0);
-        const bool last = tile + 1 == c.hi, frees = kTurns || x == 1 || !c.two;
-        const bool mend = !kQ8 && (kTurns || x == 0) && edge(c, tile);
+        const bool last = tile + 1 == (x == 0 && !kTurns ? c.hi0 : c.hi);
+        const bool frees = kTurns || x == 1 || !c.two;
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
@@ -767,7 +773,6 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
           tc_commit(at(ctl.s_full[x]));
           if (last) tc_commit(at(ctl.q_free[qx]));
           if (frees) tc_commit(empty0 + 8 * r.s);
-          if (mend) mbar_arrive(at(ctl.mend[x]));
         }
         __syncwarp();
         return true;
@@ -777,16 +782,18 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
         Ring<kStages> r = pv;
         r.next(1 + (kTurns ? 2 * x : 0));
         const int tile = p.tile + (kTurns ? x : 0);
-        if (kTurns || x == 0) {
+        if (kTurns || x == 0 || !active(0, p)) {  // first to use this V
+          constexpr int mx = kTurns ? x : 0;
           if (!ready(full0 + 8 * r.s, r.ph)) return false;
           if (!kQ8 && edge(p, tile)) {
-            if (!ready(at(ctl.mended[x]), (mend_ph >> x) & 1)) return false;
-            mend_ph ^= 1u << x;
+            if (!ready(at(ctl.mended[mx]), (mend_ph >> mx) & 1)) return false;
+            mend_ph ^= 1u << mx;
           }
         }
         const uint32_t b0 = dv + r.s * (kTileBytes >> 4);
         const uint32_t add = p.tile > p.lo;
-        const bool last = tile + (kTurns ? 2 : 1) >= p.hi, frees = kTurns || x == 1 || !p.two;
+        const bool last = tile + (kTurns ? 2 : 1) >= (x == 0 && !kTurns ? p.hi0 : p.hi);
+        const bool frees = kTurns || x == 1 || !p.two;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (!ready(h ? at(ctl.p_full[x]) : at(ctl.p_half[x]), (p_ph >> x) & 1)) return false;
@@ -814,53 +821,17 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
       bool have = false;
       while (have || c.sg < nseg) {
         const bool more = c.sg < nseg, same = have && more && c.sg == p.sg;
-        if (have && !issue_pv(x0)) break;
-        if (same && !issue_qk(x0)) break;
+        if (have && active(0, p) && !issue_pv(x0)) break;
+        if (same && active(0, c) && !issue_qk(x0)) break;
         if (have && active(1, p) && !issue_pv(x1)) break;
         if (same && active(1, c) && !issue_qk(x1)) break;
-        if (more && !same && (!issue_qk(x0) || (active(1, c) && !issue_qk(x1)))) break;
+        if (more && !same &&
+            ((active(0, c) && !issue_qk(x0)) || (active(1, c) && !issue_qk(x1))))
+          break;
         p = c;
         pv = qk;
         have = more;
         if (more) advance(c, qk);
-      }
-    }
-  } else if (warp == 10) {
-    // ---------------------------------------------------------------- mender
-    while (next_list(false)) {
-      bool live = true;
-      const int nseg = share.nseg;
-      for (int sg = 0; sg < nseg && live; ++sg) {
-        const ChunkSeg g = share.seg[sg];
-        for (int tile = g.tile_lo; tile < g.tile_hi; ++tile, ld.next(2)) {
-          if (kQ8 || !at_edge(g, tile)) continue;
-          const Mend m = mend_of(a, g, tile);
-          Ring<kStages> r = ld;
-          r.next();
-          // the product warp asks when it has issued the tile's scores: then
-          // the copy of this V is the slot's current or last one
-          const int x = kTurns ? (tile - g.tile_lo) & 1 : 0;
-          if (!wait(smem_u32(&ctl.mend[x]), (mend_ph >> x) & 1) ||
-              !wait(smem_u32(&ctl.full[r.s]), r.ph)) {
-            live = false;
-            break;
-          }
-          mend_ph ^= 1u << x;
-          uint8_t *v = ring + r.s * kTileBytes;
-          for (int i = lane; i < (m.zero_hi - m.zero_lo) * 16; i += 32) {
-            const int tok = m.zero_lo + (i >> 4), ch = i & 15;
-            *reinterpret_cast<uint4 *>(v + (ch >> 3) * kSlab + swz(tok, ch & 7)) =
-                make_uint4(0, 0, 0, 0);
-          }
-          if (m.scans()) {
-            bool bad = clean_rows<T>(v, m.hi, m.hi_end, lane);
-            if (m.lo_end > 0) bad |= clean_rows<T>(v, 0, m.lo_end, lane);
-            if (bad) *reinterpret_cast<volatile int *>(&ctl.poison) = 1;
-          }
-          fence_async_shared();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&ctl.mended[x]));
-        }
       }
     }
   } else if (warp >= 12) {
@@ -926,14 +897,19 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
       }
     }
   } else {
-    // -------------------------------------------------------------- Q loader
+    // --------------------------------------------------- Q loader and menders
+    // Warp 11 loads the segment's Q; then both warps see to V at the edges,
+    // 64 channels each.  (A segment's Q waits for the scores of the one before, and
+    // those never for more than that segment's own edges.)
     while (next_list(false)) {
       bool live = true;
       const int nseg = share.nseg;
       const int ch = lane & 15, half = lane >> 4;  // 16 bytes of row 2 i + half
       for (int sg = 0; sg < nseg && live; ++sg) {
         const ChunkSeg g = share.seg[sg];
-        for (int x = 0; x < Sh::kQTiles && x * rt < g.nrows; ++x) {
+        for (int x = 0; warp == 11 && x < Sh::kQTiles && x * rt < g.nrows; ++x) {
+          // (the first of two groups may have no tile in this segment)
+          if (!kTurns && x == 0 && g.nrows > rt && g.tile_lo >= g.half_hi) continue;
           if ((q_uses >> x) & 1) {
             if (!wait(smem_u32(&ctl.q_free[x]), (q_ph >> x) & 1)) {
               live = false;
@@ -989,6 +965,34 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
           fence_async_shared();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&ctl.q_full[x]));
+        }
+        for (int tile = g.tile_lo; !kQ8 && live && tile < g.tile_hi; ++tile, ld.next(2)) {
+          if (!at_edge(g, tile)) continue;
+          const Mend m = mend_of(a, g, tile);
+          Ring<kStages> r = ld;
+          r.next();
+          // the product warp asks when it comes to the tile's scores: then the
+          // copy of this V is the slot's current or next one
+          const int x = kTurns ? (tile - g.tile_lo) & 1 : 0;
+          if (!wait(smem_u32(&ctl.mend[x]), (mend_ph >> x) & 1) ||
+              !wait(smem_u32(&ctl.full[r.s]), r.ph)) {
+            live = false;
+            break;
+          }
+          mend_ph ^= 1u << x;
+          uint8_t *v = ring + r.s * kTileBytes + (warp - 10) * kSlab;
+          for (int i = lane; i < (m.zero_hi - m.zero_lo) * 8; i += 32)
+            reinterpret_cast<uint4 *>(v)[m.zero_lo * 8 + i] = make_uint4(0, 0, 0, 0);
+          if (m.scans()) {
+            bool bad = false;
+#pragma unroll 1
+            for (int k = 0; k < 2; ++k)
+              bad |= clean_rows<T>(v, k ? 0 : m.hi, k ? m.lo_end : m.hi_end, lane);
+            if (bad) *reinterpret_cast<volatile int *>(&ctl.poison) = 1;
+          }
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&ctl.mended[x]));
         }
       }
     }
