@@ -15,19 +15,58 @@ constexpr int kTile = 64;             // tokens per KV tile
 constexpr int kQStr = kHeadDim + 4;   // padded rows: 16-byte reads of 16 rows meet distinct banks
 constexpr int kPStr = kTile + 4;
 
-// Rows of a unit = 16 * MR.  256 threads as 16 x 16: thread (ty, tx) holds
-// rows ty * MR .. + MR - 1; of the scores the columns tx + 16 j, of the output
+// Units of 64 rows.  256 threads as 16 x 16: thread (ty, tx) holds rows
+// 4 ty .. + 3; of the scores the columns tx + 16 j, of the output
 // the channels 4 tx .. + 3 and 64 + 4 tx .. + 3.  Per tile: scores = Q K^T
-// (a 4 x MR register block per thread), one streaming-softmax step (row
+// (a 4 x 4 register block per thread), one streaming-softmax step (row
 // maximum and sum over the 16 tx lanes), output += P V.  The weights P take
 // K's place in shared memory once the scores are done, so that two CTAs fit an
 // SM.  FP32 multiply-adds bound it for many rows, the K/V stream for few.
-template <int MR> struct Shape {
-  static constexpr int kRows = 16 * MR;
-  static constexpr int kKBytes = kTile * kQStr * 4;
-  static constexpr int kSmem = kRows * kQStr * 4 + kKBytes + kTile * kHeadDim * 4;
-  static_assert(kRows * kPStr * 4 <= kKBytes, "P takes K's place");
+constexpr int MR = 4;
+constexpr int kTileRows = 16 * MR;
+constexpr int kKBytes = kTile * kQStr * 4;
+constexpr int kTileSmem = kTileRows * kQStr * 4 + kKBytes + kTile * kHeadDim * 4;
+static_assert(kTileRows * kPStr * 4 <= kKBytes, "P takes K's place");
+
+// A row's running result: log2-domain maximum, sum, and four channels.
+struct Joined {
+  float m, l;
+  float4 o;
 };
+__device__ __forceinline__ void join_one(Joined &a, float m, float l, const float4 &o) {
+  const float M = fmaxf(a.m, m), base = M == -INFINITY ? 0.f : M;
+  const float f = ex2(a.m - base), h = ex2(m - base);
+  a.m = M;
+  a.l = a.l * f + l * h;
+  a.o = make_float4(a.o.x * f + o.x * h, a.o.y * f + o.y * h, a.o.z * f + o.z * h,
+                    a.o.w * f + o.w * h);
+}
+template <class T>
+__device__ __forceinline__ void join_store(const ChunkArgs &a, const int4 &u, int q0, int r,
+                                           int lane, const Joined &x) {
+  const float inv = x.l == 0.f ? 0.f : 1.f / x.l;
+  const int pr = u.z + r, row = q0 + pr / a.G, head = u.y * a.G + pr % a.G;
+  T *dst = static_cast<T *>(a.out) + ((long long)row * a.Hq + head) * kHeadDim + lane * 4;
+  if constexpr (std::is_same_v<T, float>)
+    *reinterpret_cast<float4 *>(dst) =
+        make_float4(x.o.x * inv, x.o.y * inv, x.o.z * inv, x.o.w * inv);
+  else
+    *reinterpret_cast<uint2 *>(dst) =
+        make_uint2(pack2(x.o.x * inv, x.o.y * inv, T{}), pack2(x.o.z * inv, x.o.w * inv, T{}));
+}
+// 4 channels (of lane `lane`) of one cached vector in fp32
+template <bool Q8>
+__device__ __forceinline__ float4 cached4(const void *base, const uint8_t *scale, long long vec,
+                                          int lane) {
+  if constexpr (Q8) {
+    float x[4];
+    q8_unpack4(reinterpret_cast<const uint32_t *>(base)[vec * (kHeadDim / 4) + lane], x);
+    const float s = q8_scale(scale[vec]);
+    return make_float4(x[0] * s, x[1] * s, x[2] * s, x[3] * s);
+  } else {
+    return reinterpret_cast<const float4 *>(base)[vec * (kHeadDim / 4) + lane];
+  }
+}
 
 // 8 channels of one cached vector in fp32
 template <bool Q8>
@@ -50,31 +89,30 @@ __device__ __forceinline__ void cached8(const void *base, const uint8_t *scale, 
   }
 }
 
-template <int MR, bool Q8>
+template <bool Q8>
 __global__ void __launch_bounds__(kThreads) chunk_core_kernel(const __grid_constant__ ChunkArgs a) {
-  using Sh = Shape<MR>;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ ChunkShare<16> share;
   __shared__ int red[32];
   __shared__ int tok_ok[kTile];
   float *Qs = reinterpret_cast<float *>(smem);
-  float *Ks = Qs + Sh::kRows * kQStr;
+  float *Ks = Qs + kTileRows * kQStr;
   float *Vs = Ks + kTile * kQStr;
   float *Ps = Ks;
   pdl_wait();
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
   const int ps_log2 = 31 - __clz(a.ps);
   if (tid == 0) a.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
-  share_init(a, Sh::kRows, kTile, &share, red);
+  share_init(a, kTileRows, kTile, &share, red);
   for (;;) {
     __syncthreads();
-    if (tid == 0) share_next(a, Sh::kRows, kTile, &share);
+    if (tid == 0) share_next(a, kTileRows, kTile, &share);
     __syncthreads();
     if (share.nseg == 0) break;
     for (int sg = 0; sg < share.nseg; ++sg) {
       const ChunkSeg g = share.seg[sg];
       __syncthreads();  // the previous segment's Q is read
-      for (int i = tid; i < Sh::kRows * 16; i += kThreads) {
+      for (int i = tid; i < kTileRows * 16; i += kThreads) {
         const int r = i >> 4, c = (i & 15) * 8;
         float x[8] = {};
         if (r < g.nrows) {
@@ -231,6 +269,200 @@ __global__ void __launch_bounds__(kThreads) chunk_core_kernel(const __grid_const
   }
 }
 
+// Few rows: units of R = 4 or 8.  A warp takes 8 of a tile's 64 tokens, with a
+// softmax of its own, and K and V go from memory to registers: lane l holds
+// channels 4 l .. + 3 of the unit's q, of its output and of the token at hand.
+// The 8 R partial dot products of eight tokens are summed over the lanes by
+// halving exchanges (one shuffle per sum), which leaves lane l the rows
+// (l & 3) R / 4 .. of token l / 4; the weights come back through shared memory.
+// The K/V stream bounds it at one row per kv head; at 8, multiply-adds and
+// shuffles about as much.
+constexpr int kFewWarps = kThreads / 32;
+constexpr float kMoveAt = 8.f;  // the maximum moves when a weight would exceed 2^8
+template <int R> struct FewShared {
+  float p[kFewWarps][8][R];  // weights of a warp's tokens
+  float alpha[kFewWarps][R];
+  float o[kFewWarps][R][kHeadDim];  // at the end of a segment
+  float m[kFewWarps][R], l[kFewWarps][R];
+  ChunkShare<16> share;
+  int red[32];
+};
+
+template <int R, bool Q8>
+__global__ void __launch_bounds__(kThreads, R == 4 ? 2 : 1)
+    chunk_rows_kernel(const __grid_constant__ ChunkArgs a) {
+  constexpr int L = R / 4;  // rows whose sums a lane ends up with
+  extern __shared__ __align__(16) uint8_t smem[];
+  FewShared<R> &sh = *reinterpret_cast<FewShared<R> *>(smem);
+  pdl_wait();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int ps_log2 = 31 - __clz(a.ps);
+  const int tok = lane >> 2, row0 = (lane & 3) * L;
+  if (tid == 0) a.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
+  share_init(a, R, kTile, &sh.share, sh.red);
+  for (;;) {
+    __syncthreads();
+    if (tid == 0) share_next(a, R, kTile, &sh.share);
+    __syncthreads();
+    if (sh.share.nseg == 0) break;
+    for (int sg = 0; sg < sh.share.nseg; ++sg) {
+      const ChunkSeg g = sh.share.seg[sg];
+      float4 q[R], o[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        o[r] = q[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < g.nrows) {
+          const int pr = g.r0 + r;
+          q[r] = *reinterpret_cast<const float4 *>(
+              static_cast<const float *>(a.q) +
+              ((long long)(g.q0 + pr / a.G) * a.Hq + g.kvh * a.G + pr % a.G) * kHeadDim + 4 * lane);
+        }
+      }
+      int t[L];
+      float m[L], l[L];
+#pragma unroll
+      for (int i = 0; i < L; ++i) {
+        t[i] = g.len - g.n + (g.r0 + min(row0 + i, g.nrows - 1)) / a.G;
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+      }
+      // page of this warp's eight tokens of a tile, a tile ahead
+      auto look_up = [&](int tile) -> int {
+        const int pos = tile * kTile + warp * 8;
+        if (tile >= g.tile_hi || pos >= g.len) return -1;
+        const int ph = a.bt[(long long)g.b * a.maxP + (pos >> ps_log2)];
+        return ph >= 0 && ph < a.nphys ? ph : -2;
+      };
+      int next = look_up(g.tile_lo);
+      for (int tile = g.tile_lo; tile < g.tile_hi; ++tile) {
+        const int ph = next, pos0 = tile * kTile + warp * 8;
+        next = look_up(tile + 1);
+        if (ph < 0) {  // no token, or a bad page
+          if (ph == -2 && lane == 0) flag_error(a.status, KV_ERR_BOUNDS);
+          continue;
+        }
+        const int count = min(8, g.len - pos0);
+        // (rows of the cache fit int32)
+        const int vec0 = (ph * a.Hkv + g.kvh) * a.ps + (pos0 & (a.ps - 1));
+        float4 kx[8], vx[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          kx[j] = vx[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (j < count) {
+            kx[j] = cached4<Q8>(a.k, a.k_scale, vec0 + j, lane);
+            vx[j] = cached4<Q8>(a.v, a.v_scale, vec0 + j, lane);
+          }
+        }
+        float s[8 * R];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+            s[j * R + r] = q[r].x * kx[j].x + q[r].y * kx[j].y + q[r].z * kx[j].z +
+                           q[r].w * kx[j].w;
+#pragma unroll
+        for (int off = 16, n = 8 * R; off > 0; off >>= 1, n >>= 1) {
+          const bool up = lane & off;
+#pragma unroll
+          for (int i = 0; i < n / 2; ++i) {
+            const float give = up ? s[i] : s[i + n / 2], keep = up ? s[i + n / 2] : s[i];
+            s[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, off);
+          }
+        }
+        const int pos = pos0 + tok;
+        bool move = false;
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+          const bool see = tok < count && pos <= t[i] &&
+                           (a.window <= 0 || pos - t[i] > -a.window);
+          s[i] = see ? s[i] * a.scale_log2 : -INFINITY;
+          move |= s[i] > m[i] + kMoveAt;
+        }
+        if (__any_sync(0xFFFFFFFFu, move)) {
+#pragma unroll
+          for (int i = 0; i < L; ++i) {
+            float mx = s[i];
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1)
+              mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
+            mx = fmaxf(mx, m[i]);
+            const float f = mx == -INFINITY ? 1.f : ex2(m[i] - mx);
+            m[i] = mx;
+            l[i] *= f;
+            if (tok == 0) sh.alpha[warp][row0 + i] = f;
+          }
+          __syncwarp();
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const float f = sh.alpha[warp][r];
+            o[r] = make_float4(o[r].x * f, o[r].y * f, o[r].z * f, o[r].w * f);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+          const float p = ex2(s[i] - (m[i] == -INFINITY ? 0.f : m[i]));
+          l[i] += p;
+          sh.p[warp][tok][row0 + i] = p;
+        }
+        __syncwarp();
+        // where some row does not see some token, a weight of 0 must not meet
+        // an infinity or NaN of V
+        const bool edge = pos0 + 7 > g.t_first || a.window > 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+#pragma unroll
+          for (int r0 = 0; r0 < R; r0 += 4) {
+            const float4 w = *reinterpret_cast<const float4 *>(&sh.p[warp][j][r0]);
+            const float ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              if (edge && ww[r] == 0.f) continue;
+              float4 &x = o[r0 + r];
+              x = make_float4(x.x + ww[r] * vx[j].x, x.y + ww[r] * vx[j].y, x.z + ww[r] * vx[j].z,
+                              x.w + ww[r] * vx[j].w);
+            }
+          }
+        }
+        __syncwarp();
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        *reinterpret_cast<float4 *>(&sh.o[warp][r][4 * lane]) = o[r];
+#pragma unroll
+      for (int i = 0; i < L; ++i) {
+        float sum = l[i];
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
+        if (tok == 0) {
+          sh.m[warp][row0 + i] = m[i];
+          sh.l[warp][row0 + i] = sum;
+        }
+      }
+      __syncthreads();
+      // a warp joins a row (of 4 rows: half the warps), a lane four channels
+      if (warp < g.nrows) {
+        const int r = warp;
+        Joined x{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll
+        for (int w = 0; w < kFewWarps; ++w)
+          join_one(x, sh.m[w][r], sh.l[w][r],
+                   *reinterpret_cast<const float4 *>(&sh.o[w][r][4 * lane]));
+        if (g.whole()) {
+          join_store<float>(a, make_int4(g.b, g.kvh, g.r0, g.nrows), g.q0, r, lane, x);
+        } else {
+          const long long at = (long long)part_slot(g) * a.slot_rows + r;
+          *reinterpret_cast<float4 *>(a.part_o + at * kHeadDim + 4 * lane) = x.o;
+          if (lane == 0) {
+            a.part_ml[2 * at] = x.m;
+            a.part_ml[2 * at + 1] = x.l;
+          }
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
 // Joins the parts of every unit that several CTAs share: CTA i of the
 // attention left part 2 i + 1, the CTAs i + 1 .. j parts 2 (i + 1) .. 2 j.  A
 // lane takes four channels, a warp four rows, so that the loads of four rows
@@ -239,18 +471,6 @@ __global__ void __launch_bounds__(kThreads) chunk_core_kernel(const __grid_const
 // rows than that).  Many (a long context and few rows): the block's warps share
 // the parts of four rows.
 constexpr int kJoinRows = 4;
-struct Joined {
-  float m, l;
-  float4 o;
-};
-__device__ __forceinline__ void join_one(Joined &a, float m, float l, const float4 &o) {
-  const float M = fmaxf(a.m, m), base = M == -INFINITY ? 0.f : M;
-  const float f = ex2(a.m - base), h = ex2(m - base);
-  a.m = M;
-  a.l = a.l * f + l * h;
-  a.o = make_float4(a.o.x * f + o.x * h, a.o.y * f + o.y * h, a.o.z * f + o.z * h,
-                    a.o.w * f + o.w * h);
-}
 // rows r0 .. r0 + 3 of the parts first_part, first_part + step, .. up to CTA `last`
 template <int R>
 __device__ __forceinline__ void join_rows(const ChunkArgs &a, int first, int last, int from,
@@ -273,19 +493,6 @@ __device__ __forceinline__ void join_rows(const ChunkArgs &a, int first, int las
 #pragma unroll
     for (int i = 0; i < R; ++i) join_one(acc[i], ml[i].x, ml[i].y, o[i]);
   }
-}
-template <class T>
-__device__ __forceinline__ void join_store(const ChunkArgs &a, const int4 &u, int q0, int r,
-                                           int lane, const Joined &x) {
-  const float inv = x.l == 0.f ? 0.f : 1.f / x.l;
-  const int pr = u.z + r, row = q0 + pr / a.G, head = u.y * a.G + pr % a.G;
-  T *dst = static_cast<T *>(a.out) + ((long long)row * a.Hq + head) * kHeadDim + lane * 4;
-  if constexpr (std::is_same_v<T, float>)
-    *reinterpret_cast<float4 *>(dst) =
-        make_float4(x.o.x * inv, x.o.y * inv, x.o.z * inv, x.o.w * inv);
-  else
-    *reinterpret_cast<uint2 *>(dst) =
-        make_uint2(pack2(x.o.x * inv, x.o.y * inv, T{}), pack2(x.o.z * inv, x.o.w * inv, T{}));
 }
 template <class T>
 __global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constant__ ChunkArgs a) {
@@ -332,19 +539,25 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constan
   }
 }
 
-template <int MR, bool Q8>
-cudaError_t core_go(const ChunkArgs &a, int ctas, cudaStream_t st) {
-  const cudaError_t e = cudaFuncSetAttribute(
-      chunk_core_kernel<MR, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<MR>::kSmem);
+template <class K>
+cudaError_t core_go(K kernel, int bytes, const ChunkArgs &a, int ctas, cudaStream_t st) {
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  return launch_pdl(chunk_core_kernel<MR, Q8>, dim3(ctas), dim3(kThreads), Shape<MR>::kSmem, st, a);
+  return launch_pdl(kernel, dim3(ctas), dim3(kThreads), bytes, st, a);
 }
 
 }  // namespace
 
 cudaError_t launch_chunk_core(const ChunkArgs &a, bool q8, int rows, int ctas, cudaStream_t st) {
-  if (rows == 16) return q8 ? core_go<1, true>(a, ctas, st) : core_go<1, false>(a, ctas, st);
-  return q8 ? core_go<4, true>(a, ctas, st) : core_go<4, false>(a, ctas, st);
+  if (rows == 4)
+    return q8 ? core_go(chunk_rows_kernel<4, true>, sizeof(FewShared<4>), a, ctas, st)
+              : core_go(chunk_rows_kernel<4, false>, sizeof(FewShared<4>), a, ctas, st);
+  if (rows == 8)
+    return q8 ? core_go(chunk_rows_kernel<8, true>, sizeof(FewShared<8>), a, ctas, st)
+              : core_go(chunk_rows_kernel<8, false>, sizeof(FewShared<8>), a, ctas, st);
+  return q8 ? core_go(chunk_core_kernel<true>, kTileSmem, a, ctas, st)
+            : core_go(chunk_core_kernel<false>, kTileSmem, a, ctas, st);
 }
 
 cudaError_t launch_chunk_combine(int dtype, const ChunkArgs &a, int ctas, cudaStream_t st) {

@@ -52,6 +52,13 @@ int resolve_q8(const kv_shape *s, const kv_q8_cache *c, kv_q8_cache *dev) {
 #ifndef KVS_Q8_FEW_ROWS
 #define KVS_Q8_FEW_ROWS 16
 #endif
+// fp32: up to this many packed rows K and V go straight to registers, in units of
+// 4 or 8 rows; above, through shared memory in units of 64.  (4 x 8k tokens, 8 kv
+// heads, us, units of 8 / of 64: 12 rows 73 / 175, 24 rows 111 / 176, 32 rows 131 /
+// 176; about even at 48.)
+#ifndef KVS_F32_FEW_ROWS
+#define KVS_F32_FEW_ROWS 40
+#endif
 struct ChunkPlan {
   bool mma = false;   // tensor cores (16-bit data)
   bool q8 = false;    // the kernel reads the 8-bit cache itself ...
@@ -97,12 +104,13 @@ ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, bool q8) {
     }
     pl.stage = (q8 && !pl.q8) || s->kv_loc == KV_LOC_HOST_PINNED;
   } else {
-    // units of 16 rows until they fill the GPU (33 rows over 4096 tokens: 47
-    // us in units of 64, the latency of one unit's tile, ...), then of 64,
-    // which read K and V a quarter as often
-    const double few = (double)s->batch * s->num_kv_heads * ((packed + 15) / 16) *
-                       (((double)s->max_pages_per_seq * s->page_size + tile - 1) / tile);
-    pl.rows = packed <= 16 || few <= 2.0 * sms ? 16 : 64;
+    // few rows in units of 4 or 8, also while units of 64 would not fill the GPU
+    const double units64 = std::min((double)s->batch * ((packed + 63) / 64),
+                                    (double)c->total_q * G / 64 + s->batch);
+    const bool fills = units64 * s->num_kv_heads *
+                           (((double)s->max_pages_per_seq * s->page_size + tile - 1) / tile) >=
+                       per_sm * (double)sms;
+    pl.rows = packed <= 4 ? 4 : packed <= KVS_F32_FEW_ROWS || !fills ? 8 : 64;
   }
   // units of all sequences: full ones and one more each; no more CTAs than
   // there can be tiles
