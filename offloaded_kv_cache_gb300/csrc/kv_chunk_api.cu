@@ -111,6 +111,7 @@ ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, bool q8) {
                            (((double)s->max_pages_per_seq * s->page_size + tile - 1) / tile) >=
                        per_sm * (double)sms;
     pl.rows = packed <= 4 ? 4 : packed <= KVS_F32_FEW_ROWS || !fills ? 8 : 64;
+    if (pl.rows == 8) per_sm = 1;  // resident CTAs of its kernel (registers)
   }
   // units of all sequences: full ones and one more each; no more CTAs than
   // there can be tiles
