@@ -12,6 +12,13 @@ binding:
     enable_window(C), window_attn() -> kv_window_reset, kv_sparse_decode_attn_window
     dense_step()   -> kv_dense_decode_attn
     host_step()    -> kv_decode_step (host q / lengths in, out back)
+    chunk_attn()   -> kv_chunk_attn (a ragged chunk of new tokens per sequence)
+
+`Q8Cache` owns a cache in 8 bits:
+
+    append()       -> kv_q8_append (chunks or single tokens, quantised)
+    attend()       -> kv_q8_chunk_attn
+    read_back()    -> kv_q8_read (into a cache every other call takes)
 
 PyTorch is used for allocation, host<->device copies and streams only; every
 step of the computation runs in libkvsparse's kernels.
@@ -246,9 +253,79 @@ class DecodeLayer:
     def host_step(self, io, stream=None):
         kv.kv_decode_step(self.shape, io, self._st(stream))
 
+    def chunk_attn(self, q: torch.Tensor, q_start: torch.Tensor, max_q_len: int, window: int = 0,
+                   out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """Attention of the last q_start[b + 1] - q_start[b] of context_lens[b]
+        cached tokens of every sequence, whose K and V are in the cache.
+
+        q: [total_q][Hq][d] on the device, q_start: [B + 1] int32 on the device."""
+        stream = self._st(stream)
+        chunk = kv.make_chunk(q_start, q.shape[0], max_q_len, window)
+        out = torch.empty_like(q) if out is None else out
+        need = kv.kv_chunk_workspace_bytes(self.shape, chunk)
+        if need > self.workspace.numel():
+            self.workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+        kv.kv_chunk_attn(self.shape, chunk, q, self.k_cache, self.v_cache, self.block_table,
+                         self.context_lens, self.scale, out, self.workspace,
+                         self.workspace.numel(), stream)
+        return out
+
     # --- host views --------------------------------------------------------
     def minmax_bits(self) -> np.ndarray:
         return torch_to_bits(self.minmax)
 
     def mean_bits(self) -> np.ndarray:
         return torch_to_bits(self.mean)
+
+
+class Q8Cache:
+    """A paged cache held in 8 bits, in device memory or (kv_loc = "host") pinned
+    host memory, with the block table and lengths of its sequences.
+
+    shape: the kv_shape of the sequences (dtype = the model's); its kv_loc is
+    replaced by this cache's."""
+
+    def __init__(self, shape: kv.kv_shape, block_table: torch.Tensor, context_lens: torch.Tensor,
+                 kv_loc: str = "hbm", device: str = "cuda"):
+        self.shape = kv.kv_shape.from_buffer_copy(shape)
+        self.shape.kv_loc = kv.LOC_CODE[kv_loc]
+        self.device = torch.device(device)
+        self.block_table, self.context_lens = block_table, context_lens
+        s = self.shape
+        rows = (s.num_phys_pages, s.num_kv_heads, s.page_size)
+        where = dict(pin_memory=True) if kv_loc == "host" else dict(device=self.device)
+        self.k_codes, self.v_codes = (torch.zeros((*rows, s.head_dim), dtype=torch.uint8, **where)
+                                      for _ in range(2))
+        self.k_scale, self.v_scale = (torch.zeros(rows, dtype=torch.uint8, **where)
+                                      for _ in range(2))
+        self.cache = kv.make_q8_cache(self.k_codes, self.v_codes, self.k_scale, self.v_scale)
+        self.workspace = torch.empty(16, dtype=torch.uint8, device=self.device)
+
+    def append(self, k_new: torch.Tensor, v_new: torch.Tensor, q_start: torch.Tensor,
+               max_q_len: int, stream=None):
+        """Quantise and store the new tokens (k_new, v_new: [total_q][Hkv][d]) behind
+        each sequence's cached ones; context_lens grows in place."""
+        chunk = kv.make_chunk(q_start, k_new.shape[0], max_q_len)
+        kv.kv_q8_append(self.shape, chunk, k_new, v_new, self.cache, self.block_table,
+                        self.context_lens, self.context_lens, DecodeLayer._st(stream))
+
+    def attend(self, q: torch.Tensor, q_start: torch.Tensor, max_q_len: int, scale: float,
+               window: int = 0, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """Attention of the chunk whose tokens were appended last (q: [total_q][Hq][d])."""
+        chunk = kv.make_chunk(q_start, q.shape[0], max_q_len, window)
+        out = torch.empty_like(q) if out is None else out
+        need = kv.kv_q8_chunk_workspace_bytes(self.shape, chunk)
+        if need > self.workspace.numel():
+            self.workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+        kv.kv_q8_chunk_attn(self.shape, chunk, q, self.cache, self.block_table, self.context_lens,
+                            scale, out, self.workspace, self.workspace.numel(),
+                            DecodeLayer._st(stream))
+        return out
+
+    def read_back(self, k_out: torch.Tensor, v_out: torch.Tensor,
+                  out_table: torch.Tensor | None = None, stream=None):
+        """The cached tokens in the model's type, into pages out_table[b][p] (default:
+        the same page numbers) of k_out, v_out [pages][Hkv][ps][d] on the device."""
+        table = self.block_table if out_table is None else out_table
+        kv.kv_q8_read(self.shape, self.cache, self.block_table, self.context_lens, table,
+                      k_out.shape[0], k_out, v_out, DecodeLayer._st(stream))

@@ -442,3 +442,35 @@ def test_a_wait_that_runs_out_is_reported(news, q8):
     p.attend()
     torch.cuda.synchronize()
     check(p.d_out, *p.expected())
+
+
+@pytest.mark.parametrize("loc", ["hbm", "host"])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_pipeline_classes(dtype, loc):
+    """DecodeLayer.chunk_attn and Q8Cache run the calls and keep the lengths."""
+    from offloaded_kv_cache_gb300 import workloads as W
+    from offloaded_kv_cache_gb300.pipeline import DecodeLayer, Q8Cache
+    spec = W.tiny_spec(dtype=dtype, batch=2, hq=8, hkv=2, context=90, ps=16, topk=2, index=5)
+    layer = DecodeLayer(W.generate(spec, context_lens=[90, 41]), kv_loc=loc)
+    t = TORCH[dtype]
+    q8 = Q8Cache(layer.shape, layer.block_table, torch.zeros(2, dtype=torch.int32, device="cuda"),
+                 kv_loc=loc)
+    g = torch.Generator().manual_seed(1)
+    for n in ([50, 12], [1, 1], [0, 3]):
+        start = torch.tensor([0, n[0], sum(n)], dtype=torch.int32, device="cuda")
+        k, v = (torch.randn(sum(n), 2, D, generator=g).to(t).cuda() for _ in "kv")
+        q = torch.randn(sum(n), 8, D, generator=g).to(t).cuda()
+        q8.append(k, v, start, max(n))
+        got = q8.attend(q, start, max(n), layer.scale)
+    assert q8.context_lens.tolist() == [51, 16]
+    back = [torch.zeros(spec.num_phys_pages, 2, 16, D, dtype=t, device="cuda") for _ in "kv"]
+    q8.read_back(*back)
+    layer.context_lens.copy_(q8.context_lens)
+    torch.cuda.synchronize()
+    layer.k_cache.copy_(back[0])
+    layer.v_cache.copy_(back[1])
+    again = layer.chunk_attn(q, start, max(n))
+    torch.cuda.synchronize()
+    # both compute the same sums, each within 2^-8 (2^-11, 2^-24) of weights and result
+    tol = {"f32": 1e-5, "f16": 2.0 ** -9, "bf16": 2.0 ** -6}[dtype]
+    assert float((got.float() - again.float()).abs().max()) <= tol * (1 + float(back[1].abs().max()))
