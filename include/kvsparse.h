@@ -456,6 +456,9 @@ typedef struct {
  * KV_ERR_BOUNDS.  With K/V in pinned host memory and 16-bit data the pages
  * the call needs cross the link once, into the workspace.  Results do not
  * depend on what ran before and repeat bit for bit on the same device.
+ * KV_ERR_UNSUPPORTED where the rows and KV tiles of the call might not count
+ * in int32 (some 10^11 token pairs per kv head).  A cache in another kind of
+ * memory than kv_loc says is KV_ERR_LOCATION.
  * kv_chunk_workspace_bytes: the workspace for this shape and chunk on the
  * current device (0 for an invalid one); q_start itself is not read.  Calls
  * that may run at the same time need workspaces of their own. */
@@ -489,8 +492,8 @@ typedef struct {
  * context_lens[b] + i, context_lens being the lengths BEFORE the append (as
  * kv_append_token; context_lens[b] + n_b <= maxP * ps).
  *   k_new, v_new [total_q][Hkv][d] dtype, device memory.
- * context_lens_out (may be NULL, may equal context_lens): receives
- * context_lens[b] + n_b.  A token whose block-table entry is out of range is
+ * context_lens_out (may be NULL, may equal context_lens; not overlap it in
+ * part): receives context_lens[b] + n_b.  A token whose block-table entry is out of range is
  * dropped; its sequence keeps its length, and KV_ERR_BOUNDS is recorded (the
  * same for a sequence that is skipped whole).  The pages written must not be
  * shared with another row. */
@@ -531,7 +534,8 @@ const char *kv_status_string(int status);
 
 /* Testing hook for the bounded device-side waits (failure detection without
  * a GPU fault).  wait_limit_ns (1 ns .. 60 s; default 2 s) bounds every
- * pipeline wait of the attention kernels; skip_page >= 0 makes the producer
+ * pipeline wait of the attention kernels (of chunk attention: those for 16-bit
+ * types; its tile that holds the skip_page-th 16 tokens stays unfilled); skip_page >= 0 makes the producer
  * of every attention CTA leave its skip_page-th 16-token K/V tile unfilled, so
  * the consumer waiting for it gives up after the limit, the call's kernels finish, and
  * kv_device_status reports KV_ERR_DEVICE_TIMEOUT.  skip_page < 0 restores

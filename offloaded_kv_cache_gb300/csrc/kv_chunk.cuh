@@ -192,7 +192,7 @@ template <int kSegs>
 __device__ __forceinline__ void share_next(const ChunkArgs &a, int rows, int tile,
                                            ChunkShare<kSegs> *sh) {
   int n = 0;
-  if (sh->left > 0) {
+  if (sh->left > 0 && sh->b >= 0) {
     int b = sh->b, kvh = sh->kvh, r0 = sh->r0, off = sh->off;
     int left = sh->left;
     ChunkSeq s = chunk_seq(a, b, false);

@@ -216,9 +216,17 @@ int q_map(const kv_shape *s, const kv_chunk *c, const void *q, int row_tile, int
   return cached_map(MapKey{dev, type16(s), q, c->total_q, s->num_q_heads, G, row_tile / G}, map);
 }
 
+// The kernels count tiles in int32, and index the staged cache's rows as a
+// cache's own.
+bool plan_fits(const kv_shape *s, const ChunkPlan &pl) {
+  return pl.most_tiles <= INT_MAX &&
+         pl.stage_pages <= INT_MAX / ((long long)s->num_kv_heads * s->page_size);
+}
+
 size_t chunk_bytes(const kv_shape *s, const kv_chunk *c, bool q8) {
   if (check_shape(s) != KV_OK || check_chunk(s, c) != KV_OK) return 0;
-  return make_chunk_plan(s, c, q8).total;
+  const ChunkPlan pl = make_chunk_plan(s, c, q8);
+  return plan_fits(s, pl) ? pl.total : 0;
 }
 
 int chunk_common(const kv_shape *s, const kv_chunk *c, const void *q, const void *k_cache,
@@ -230,6 +238,8 @@ int chunk_common(const kv_shape *s, const kv_chunk *c, const void *q, const void
   if ((rc = check_chunk(s, c)) != KV_OK) return rc;
   if (!al16(q) || !al16(out) || !al4(bt) || !al4(ctx) || !std::isfinite(scale))
     return KV_ERR_INVALID_ARG;
+  const ChunkPlan pl = make_chunk_plan(s, c, is_q8);
+  if (!plan_fits(s, pl)) return KV_ERR_UNSUPPORTED;
   const int dev = current_device();
   if (dev < 0) return KV_ERR_CUDA;
   ChunkArgs a = {};
@@ -244,12 +254,6 @@ int chunk_common(const kv_shape *s, const kv_chunk *c, const void *q, const void
     if ((rc = resolve_kv(s, k_cache, &a.k)) != KV_OK) return rc;
     if ((rc = resolve_kv(s, v_cache, &a.v)) != KV_OK) return rc;
   }
-  const ChunkPlan pl = make_chunk_plan(s, c, is_q8);
-  // the kernels count tiles in int32, and index the staged cache's rows as a
-  // cache's own
-  if (pl.most_tiles > INT_MAX) return KV_ERR_UNSUPPORTED;
-  if (pl.stage_pages > INT_MAX / ((long long)s->num_kv_heads * s->page_size))
-    return KV_ERR_UNSUPPORTED;
   if (!al16(workspace) || ws_bytes < pl.total) return KV_ERR_WORKSPACE;
   int *status = status_ptr(dev);
   if (!status) return KV_ERR_CUDA;
@@ -349,6 +353,11 @@ int kv_q8_append(const kv_shape *shape, const kv_chunk *chunk, const void *k_new
   if ((rc = check_chunk(shape, chunk)) != KV_OK) return rc;
   if (!al16(k_new) || !al16(v_new) || !al4(block_table) || !al4(context_lens) ||
       (context_lens_out && !al4(context_lens_out)))
+    return KV_ERR_INVALID_ARG;
+  // the same array or one apart, not one that overlaps
+  if (context_lens_out && context_lens_out != context_lens &&
+      context_lens_out < context_lens + shape->batch &&
+      context_lens < context_lens_out + shape->batch)
     return KV_ERR_INVALID_ARG;
   const int dev = current_device();
   if (dev < 0) return KV_ERR_CUDA;

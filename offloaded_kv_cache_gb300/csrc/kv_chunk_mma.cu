@@ -190,6 +190,7 @@ __device__ __forceinline__ bool clean_rows(uint8_t *slab, int r0, int r1, int la
 template <class T, bool kQ8>
 __device__ __noinline__ void poison_row(const ChunkArgs &a, const ChunkSeg &g, int t, int c0,
                                         int c1, T *out, float *part) {
+  if (t < 0) return;
   for (int tile = g.tile_lo; tile < g.tile_hi; ++tile) {
     if (!kQ8 && !mend_of(a, g, tile).scans()) continue;
     const int lo = max(tile * kTile, a.window > 0 ? t - a.window + 1 : 0);

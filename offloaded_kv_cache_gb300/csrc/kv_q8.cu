@@ -387,8 +387,7 @@ cudaError_t launch_q8_append(int dtype, const void *k_new, const void *v_new,
   const long long steps = (items + kVecs * kSteps - 1) / (kVecs * kSteps);
   a.blocks = (int)std::max(1LL, std::min(steps, (KVS_APPEND_BLOCKS + B - 1LL) / B));
   const long long blocks = a.blocks;
-  const bool in_place = ctx_out && ctx_out < ctx + B && ctx < ctx_out + B;
-  const bool later = in_place && blocks > 1;
+  const bool later = ctx_out == ctx && blocks > 1;
   a.write_lens = ctx_out && !later;
   const dim3 grid((unsigned)(blocks * B)), block(kThreads);
   cudaError_t e = dtype == KV_F32 ? launch_pdl(q8_append_kernel<float>, grid, block, 0, st, a)

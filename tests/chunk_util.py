@@ -144,20 +144,16 @@ class Problem:
     # --- the definition
     def tokens(self, name, b, h):
         """fp64 vectors of sequence b's cached tokens, and which of their pages are in range."""
-        out, ok = [], []
-        for j in range(self.lens[b]):
-            p = int(self.table[b, j // self.ps])
-            good = 0 <= p < self.pages
-            ok.append(good)
-            p = p if good else 0
-            if self.q8:
-                x = restore(self.code[name][p, h, j % self.ps].numpy(),
-                            self.scale8[name][p, h, j % self.ps].numpy())
-                out.append(torch.from_numpy(x))
-            else:
-                out.append(getattr(self, name)[p, h, j % self.ps].double())
-        return (torch.stack(out) if out else torch.zeros(0, D, dtype=torch.float64),
-                torch.tensor(ok, dtype=torch.bool))
+        at = torch.arange(self.lens[b])
+        page = self.table[b].long()[at // self.ps]
+        ok = (page >= 0) & (page < self.pages)
+        page = torch.where(ok, page, 0)
+        if self.q8:
+            x = torch.from_numpy(restore(self.code[name][page, h, at % self.ps].numpy(),
+                                         self.scale8[name][page, h, at % self.ps].numpy()))
+        else:
+            x = getattr(self, name)[page, h, at % self.ps].double()
+        return x, ok
 
     def expected(self):
         """(out, tolerance) in 64 bits; rows no sequence owns are 7, tolerance 0.

@@ -80,6 +80,19 @@ def test_bad_pointers_are_refused(kvlib, kw):
     assert calls(shape(), chunk(), **kw) == (kv.KV_ERR_INVALID_ARG,) * 3
 
 
+def test_lengths_that_overlap_in_part_are_refused(kvlib):
+    for d in (4, -4):
+        assert kv.kv_q8_append(shape(), chunk(), FAKE, FAKE, CACHE, FAKE, FAKE, FAKE + d,
+                               check=False) == kv.KV_ERR_INVALID_ARG
+
+
+def test_more_tiles_than_an_int_are_refused(kvlib):
+    s = shape(batch=1, num_q_heads=8, num_kv_heads=8, page_size=128, num_phys_pages=1 << 20,
+              max_pages_per_seq=1 << 20)
+    assert kv.kv_chunk_workspace_bytes(s, chunk(total_q=1 << 27, max_q_len=1 << 27)) == 0
+    assert calls(s, chunk(total_q=1 << 27, max_q_len=1 << 27))[0] == kv.KV_ERR_UNSUPPORTED
+
+
 def test_bad_scales_and_outputs_are_refused(kvlib):
     for scale in (float("nan"), float("inf")):
         assert calls(shape(), chunk(), scale=scale)[:2] == (kv.KV_ERR_INVALID_ARG,) * 2
