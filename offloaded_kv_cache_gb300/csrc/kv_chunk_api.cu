@@ -46,11 +46,17 @@ int resolve_q8(const kv_shape *s, const kv_q8_cache *c, kv_q8_cache *dev) {
 #ifndef KVS_Q8_DIRECT_ROWS
 #define KVS_Q8_DIRECT_ROWS 192
 #endif
-// Up to this many rows codes are expanded in registers (kv_chunk_few.cu; the
-// same shape, against the converting form: 8 rows 50 / 96, 16 rows 70 / 84; 24
-// rows, in units of 16, 89 / 85).
-#ifndef KVS_Q8_FEW_ROWS
-#define KVS_Q8_FEW_ROWS 16
+// Up to this many rows the kernel for few rows is taken (kv_chunk_few.cu), in us
+// against the other one: the 8-bit cache, 4 x 32k tokens, 8 kv heads, bf16 q, 8
+// rows 50 / 96, 16 rows 70 / 84, 24 rows, in units of 16, 89 / 85; fp32 q 70 /
+// 410 and 106 / 655; 16-bit caches, 1 to 8 rows, 17 x 456 tokens, 32 kv heads, 25 /
+// 35, 4 x 700 tokens, 8 kv heads, 9.5 / 13, 4 x 32k tokens 64 / 66 (16 rows, in units of
+// 16, 40 / 35, 12.4 / 13.3 and 73 / 68).
+#ifndef KVS_FEW_ROWS_8BIT
+#define KVS_FEW_ROWS_8BIT 16
+#endif
+#ifndef KVS_FEW_ROWS_16BIT
+#define KVS_FEW_ROWS_16BIT 8
 #endif
 // fp32: up to this many packed rows K and V go straight to registers, in units of
 // 4 or 8 rows; above, through shared memory in units of 64.  (4 x 8k tokens, 8 kv
@@ -61,12 +67,13 @@ int resolve_q8(const kv_shape *s, const kv_q8_cache *c, kv_q8_cache *dev) {
 #endif
 struct ChunkPlan {
   bool mma = false;   // tensor cores (16-bit data)
-  bool q8 = false;    // the kernel reads the 8-bit cache itself ...
-  bool few = false;   // ... and is the one for few rows
+  bool q8 = false;    // the kernel reads the 8-bit cache itself
+  bool few = false;   // the kernel for few rows
   bool stage = false; // K/V pass through the workspace in 16 bits
   bool renumber = false;  // the staged pages have a block table of their own
   long long stage_pages = 0;
   int rows = 64;      // packed rows per unit
+  int tile = 64;      // tokens per KV tile
   int row_tile = 0;   // tensor cores: packed rows per Q tile (a unit is one, or two when wide)
   bool wide = false;
   double most_tiles = 0;  // an upper bound of the call's (unit, KV tile) pairs
@@ -85,30 +92,32 @@ ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, bool q8) {
   const int G = s->num_q_heads / s->num_kv_heads;
   const long long packed = (long long)std::min(c->max_q_len, c->total_q) * G;
   pl.mma = s->dtype != KV_F32;
-  int tile = 64, per_sm = 2;
-  if (pl.mma) {
-    tile = kChunkTile;
+  const bool hbm = s->kv_loc == KV_LOC_HBM;
+  int per_sm = 2;
+  pl.q8 = q8 && hbm;
+  if (packed <= (pl.q8 ? KVS_FEW_ROWS_8BIT : KVS_FEW_ROWS_16BIT) && (pl.mma || pl.q8)) {
+    pl.few = true;
+    pl.stage = !hbm;
+    pl.rows = packed <= 8 || !pl.mma ? 8 : 16;
+    const FewShape sh = chunk_few_shape(s->dtype, pl.q8, pl.rows);
+    pl.tile = sh.tile;
+    per_sm = sh.per_sm;
+  } else if (pl.mma) {
+    pl.tile = kChunkTile;
     per_sm = 1;
-    pl.q8 = q8 && s->kv_loc == KV_LOC_HBM && packed <= KVS_Q8_DIRECT_ROWS;
-    pl.few = pl.q8 && packed <= KVS_Q8_FEW_ROWS;
-    if (pl.few) {
-      pl.rows = packed <= 8 ? 8 : 16;
-      tile = 64;
-      per_sm = pl.rows == 8 ? 2 : 1;
-    } else {
-      // a Q tile holds whole tokens, for the TMA unit, where a token's heads fit
-      const int most = pl.q8 ? 64 : 128;
-      pl.row_tile = G <= most ? most / G * G : most;
-      pl.wide = !pl.q8 && packed > pl.row_tile;
-      pl.rows = pl.row_tile * (pl.wide ? 2 : 1);
-    }
-    pl.stage = (q8 && !pl.q8) || s->kv_loc == KV_LOC_HOST_PINNED;
+    pl.q8 &= packed <= KVS_Q8_DIRECT_ROWS;
+    pl.stage = (q8 && !pl.q8) || !hbm;
+    // a Q tile holds whole tokens, for the TMA unit, where a token's heads fit
+    const int most = pl.q8 ? 64 : 128;
+    pl.row_tile = G <= most ? most / G * G : most;
+    pl.wide = !pl.q8 && packed > pl.row_tile;
+    pl.rows = pl.row_tile * (pl.wide ? 2 : 1);
   } else {
     // few rows in units of 4 or 8, also while units of 64 would not fill the GPU
     const double units64 = std::min((double)s->batch * ((packed + 63) / 64),
                                     (double)c->total_q * G / 64 + s->batch);
     const bool fills = units64 * s->num_kv_heads *
-                           (((double)s->max_pages_per_seq * s->page_size + tile - 1) / tile) >=
+                           (((double)s->max_pages_per_seq * s->page_size + pl.tile - 1) / pl.tile) >=
                        per_sm * (double)sms;
     pl.rows = packed <= 4 ? 4 : packed <= KVS_F32_FEW_ROWS || !fills ? 8 : 64;
     if (pl.rows == 8) per_sm = 1;  // resident CTAs of its kernel (registers)
@@ -117,7 +126,7 @@ ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, bool q8) {
   // there can be tiles
   const double units = std::min((double)s->batch * ((packed + pl.rows - 1) / pl.rows),
                                 (double)c->total_q * G / pl.rows + s->batch);
-  const long long tiles = ((long long)s->max_pages_per_seq * s->page_size + tile - 1) / tile;
+  const long long tiles = ((long long)s->max_pages_per_seq * s->page_size + pl.tile - 1) / pl.tile;
   pl.most_tiles = units * s->num_kv_heads * tiles;
   pl.ctas = (int)std::min<double>((double)per_sm * sms, std::max(1.0, pl.most_tiles));
   pl.slot_rows = (int)std::min<long long>(pl.rows, packed);
@@ -200,13 +209,13 @@ int cached_map(const MapKey &k, CUtensorMap *map) {
 int type16(const kv_shape *s) {
   return s->dtype == KV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
 }
-// Pages as rows [pages * Hkv * ps][128]: a box is 128 bytes of a page's
-// tokens, 64 channels of 16-bit data or all 128 (of 64 tokens at most) of codes.
-int page_map(const kv_shape *s, bool codes, const void *base, long long pages, int dev,
+// Pages as rows [pages * Hkv * ps][128]: a box is 128 bytes, 64 channels of 16-bit
+// data or all 128 of codes, of a page's tokens that fall into one KV tile.
+int page_map(const kv_shape *s, bool codes, int tile, const void *base, long long pages, int dev,
              CUtensorMap *map) {
   return cached_map(MapKey{dev, codes ? (int)CU_TENSOR_MAP_DATA_TYPE_UINT8 : type16(s), base,
                            pages * s->num_kv_heads * s->page_size, 0,
-                           codes ? std::min(s->page_size, 64) : s->page_size, 0},
+                           std::min(s->page_size, tile), 0},
                     map);
 }
 // q: a box is 64 channels of the G heads of row_tile / G tokens.
@@ -281,32 +290,33 @@ int chunk_common(const kv_shape *s, const kv_chunk *c, const void *q, const void
   a.slot_rows = pl.slot_rows;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.wait_limit_ns = wait_limit_ns();
-  a.debug_skip_tile = debug_skip_page() < 0 ? -1 : debug_skip_page() / (kChunkTile / kTileTokens);
+  a.debug_skip_tile = debug_skip_page() < 0 ? -1 : debug_skip_page() / (pl.tile / kTileTokens);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (pl.mma) {
-    long long pages = s->num_phys_pages;
-    if (pl.stage) {
-      int32_t *table = pl.renumber ? reinterpret_cast<int32_t *>(ws + pl.off_table) : nullptr;
-      if (launch_chunk_stage(s->dtype, is_q8, a, ws + pl.off_k, ws + pl.off_v, table, st) !=
-          cudaSuccess)
-        return KV_ERR_CUDA;
-      a.k = ws + pl.off_k;
-      a.v = ws + pl.off_v;
-      if (table) a.bt = table;
-      a.nphys = pages = pl.stage_pages;
-    }
-    CUtensorMap tq = {}, tk = {}, tv = {};
+  long long pages = s->num_phys_pages;
+  if (pl.stage) {
+    int32_t *table = pl.renumber ? reinterpret_cast<int32_t *>(ws + pl.off_table) : nullptr;
+    if (launch_chunk_stage(s->dtype, is_q8, a, ws + pl.off_k, ws + pl.off_v, table, st) !=
+        cudaSuccess)
+      return KV_ERR_CUDA;
+    a.k = ws + pl.off_k;
+    a.v = ws + pl.off_v;
+    if (table) a.bt = table;
+    a.nphys = pages = pl.stage_pages;
+  }
+  CUtensorMap tq = {}, tk = {}, tv = {};
+  if (pl.few || (pl.mma && !pl.q8)) {
+    if ((rc = page_map(s, pl.q8, pl.tile, a.k, pages, dev, &tk)) != KV_OK) return rc;
+    if ((rc = page_map(s, pl.q8, pl.tile, a.v, pages, dev, &tv)) != KV_OK) return rc;
+  }
+  if (pl.few) {
+    e = launch_chunk_few(s->dtype, pl.q8, pl.rows, a, tk, tv, pl.ctas, st);
+  } else if (pl.mma) {
     a.row_tile = pl.row_tile;
     // a scale that is not positive is applied to Q as it is loaded
-    a.q_tma = !pl.few && a.G <= pl.row_tile && pl.row_tile % a.G == 0 && a.scale_log2 > 0.f;
+    a.q_tma = a.G <= pl.row_tile && pl.row_tile % a.G == 0 && a.scale_log2 > 0.f;
     if (a.q_tma && (rc = q_map(s, c, q, pl.row_tile, dev, &tq)) != KV_OK) return rc;
-    if (!pl.q8 || pl.few) {
-      if ((rc = page_map(s, pl.few, a.k, pages, dev, &tk)) != KV_OK) return rc;
-      if ((rc = page_map(s, pl.few, a.v, pages, dev, &tv)) != KV_OK) return rc;
-    }
-    e = pl.few ? launch_chunk_few(s->dtype, pl.rows, a, tk, tv, pl.ctas, st)
-               : launch_chunk_mma(s->dtype, pl.wide, pl.q8, a, tq, tk, tv, pl.ctas, st);
+    e = launch_chunk_mma(s->dtype, pl.wide, pl.q8, a, tq, tk, tv, pl.ctas, st);
   } else {
     e = launch_chunk_core(a, is_q8, pl.rows, pl.ctas, st);
   }

@@ -1,30 +1,36 @@
-// kv_chunk_few.cu -- chunk attention over the 8-bit cache for few rows per kv
-// head (a decode step, a few proposed tokens).  kv_chunk.cuh has the formula
-// and how the work is cut.
+// kv_chunk_few.cu -- chunk attention for few rows per kv head (a decode step, a
+// few proposed tokens): the 8-bit cache, and 16-bit ones.  kv_chunk.cuh has the
+// formula and how the work is cut.
 //
-// The codes are the bound: 33 KB per 128 tokens of K and V pass each SM in
-// about 0.75 us at the memory's rate.  Expanding them into 16-bit tiles in shared memory
-// for the tensor cores' large products moves each byte through shared memory
-// seven times and took 2.7 times as long; here a warp expands codes in
-// registers, straight into the operands of 16 x 8 x 16 products, so a byte is
-// written to and read from shared memory once.
+// The K/V stream is the bound.  For the 8-bit cache, 33 KB per 128 tokens of K
+// and V pass each SM in about 0.75 us at the memory's rate.  Expanding the codes
+// into 16-bit tiles in shared memory for the tensor cores' large products
+// moves each byte through shared memory seven times and took 2.7 times as long;
+// here a warp expands codes in registers, straight into the operands of 16 x 8
+// x 16 products, so a byte is written to and read from shared memory once.  For
+// 16-bit caches the large products need no expansion and stream as fast over
+// long contexts, but their chain of product, softmax and product takes some 2
+// us per 128 tokens whatever the rows: here it is a fraction of that, which
+// short contexts and many kv heads show.
 //
-// CTA: four consumer warps and a producer warp, two CTAs per SM.  A stage is a
-// 64-token tile of K and V codes (TMA, 128-byte swizzle) and their scale bytes; a
-// consumer warp takes 16 tokens of it with a softmax of its own; the warps'
-// results are joined at the end of a segment.
+// CTA: four consumer warps and a producer warp, two CTAs per SM for 8 rows.  A
+// stage is a 64-token tile of K and V (TMA, 128-byte swizzle) and the scale bytes; a consumer warp takes 16 tokens of it
+// with a softmax of its own; the warps' results are joined at the end of a
+// segment.
 //   S^T (16 tokens x 8 rows) = K Q^T: the products sum over the channels, in
 //     any order that K and Q share: a thread's 16-byte reads of its rows of K
 //     are its operands.
 //   O^T (128 channels x 8 rows) += V^T P^T: likewise which channel is which row of
-//     O^T is free, so a thread reads 16 consecutive codes of four tokens and
-//     pairs the tokens' bytes.
-// Both swizzled reads meet distinct banks.  Products are f16, which holds e4m3
-// exactly: the scales stay outside.  K's multiplies the scores; V's joins the
-// weight's exponent, weight = 2^(z + e_v - R) with R the row's running
-// maximum of z + e_v, next to m, that of z, for the softmax's sum: z, e_v and
-// both maxima in the log2 domain.  bf16 rows of q are scaled into f16 by a power of
-// two per row, which is exact but for channels 2^39 below the row's largest.
+//     O^T is free, so a thread reads 16 bytes (twice for 16-bit data) of four
+//     tokens and pairs the tokens' elements.
+// All swizzled reads meet distinct banks.  For codes the products are f16,
+// which holds e4m3 exactly: the scales stay outside.  K's multiplies the scores;
+// V's joins the weight's exponent, weight = 2^(z + e_v - R) with R the row's
+// running maximum of z + e_v, next to m, that of z, for the softmax's sum: z,
+// e_v and both maxima in the log2 domain.  bf16 rows of q are scaled into f16 by a
+// power of two per row, which is exact but for channels 2^39 below the row's
+// largest; fp32 rows of q, and their weights, are taken as two f16 terms (22
+// bits), with the value products of each tile summed apart and added in fp32.
 #include <type_traits>
 
 #include "kv_chunk.cuh"
@@ -35,23 +41,31 @@
 namespace kvs {
 namespace {
 
-constexpr int kConsumers = 4;
-constexpr int kThreads = 32 * (kConsumers + 1);
-constexpr int kTile = 64;                     // tokens per stage, 16 per consumer warp
-constexpr int kCodeBytes = kTile * kHeadDim;  // of K or V
-constexpr int kStages = 5;
 constexpr float kMoveAt = 8.f;  // the maxima move when a weight would exceed 2^8 ...
-constexpr float kBias = 7.f;    // ... times 2^7, so that small f16 weights keep their bits
+constexpr float kBias = 7.f;    // ... times 2^7 for f16, so that small weights keep their bits
 
-template <int NB> struct Shared {
-  alignas(1024) uint8_t code[kStages][2][kCodeBytes];
-  float o[kConsumers][8 * NB][kHeadDim];  // per warp, at the end of a segment
-  float m[kConsumers][8 * NB], r[kConsumers][8 * NB], l[kConsumers][8 * NB];
-  alignas(16) uint8_t scale[kStages][2][kTile];
-  uint64_t full[kStages], empty[kStages], joined, read;
-  int tokens[kStages];  // per stage: bit i: the pages of tokens 16 i .. + 15 are in range
+template <class T, int NB, bool Q8> struct Shape {
+  static constexpr int kConsumers = 4;
+  static constexpr int kThreads = 32 * (kConsumers + 1);
+  static constexpr int kTile = 16 * kConsumers;  // tokens per stage
+  static constexpr int kRowBytes = kHeadDim * (Q8 ? 1 : 2);
+  static constexpr int kSlabs = kRowBytes / 128;
+  static constexpr int kBytes = kTile * kRowBytes;  // of K or V
+  static constexpr int kStages = Q8 ? 5 : 3;
+  static constexpr int kCtas = NB == 1 && sizeof(T) == 2 ? 2 : 1;  // per SM
+  static constexpr int kRows = 8 * NB;
+};
+
+template <class T, int NB, bool Q8> struct Shared {
+  using Sh = Shape<T, NB, Q8>;
+  alignas(1024) uint8_t kv[Sh::kStages][2][Sh::kBytes];  // slabs of [token][128 bytes]
+  float o[Sh::kConsumers][Sh::kRows][kHeadDim];          // per warp, at the end of a segment
+  float m[Sh::kConsumers][Sh::kRows], r[Sh::kConsumers][Sh::kRows], l[Sh::kConsumers][Sh::kRows];
+  alignas(16) uint8_t scale[Sh::kStages][2][Q8 ? Sh::kTile : 16];
+  uint64_t full[Sh::kStages], empty[Sh::kStages], joined, read;
+  int tokens[Sh::kStages];  // per stage: bit i: the pages of tokens 16 i .. + 15 are in range
   int abort, pad;
-  ChunkShare<16> share;
+  ChunkShare<Q8 ? 8 : 4> share;
   int red[32];
 };
 
@@ -61,12 +75,27 @@ __device__ __forceinline__ uint32_t movm_t(uint32_t x) {
   return y;
 }
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+                                         uint32_t a3, uint32_t b0, uint32_t b1, __half) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1, __nv_bfloat16) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// which of two packed 16-bit elements are infinities or NaN (bits 15 and 31)
+__device__ __forceinline__ uint32_t non_finite(uint32_t w, __half) {
+  return ((w & 0x7C007C00u) + 0x04000400u) & 0x80008000u;
+}
+__device__ __forceinline__ uint32_t non_finite(uint32_t w, __nv_bfloat16) {
+  return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
 }
 // codes 0, 1 (codes 2, 3) of a word as two f16
 __device__ __forceinline__ uint32_t f16_lo(uint32_t w) {
@@ -81,13 +110,19 @@ __device__ __forceinline__ uint32_t f16_hi(uint32_t w) {
 }
 
 // Rows of a unit: 8 NB.
-template <class T, int NB>
-__global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
+template <class T, int NB, bool Q8>
+__global__ void __launch_bounds__(Shape<T, NB, Q8>::kThreads, Shape<T, NB, Q8>::kCtas)
     chunk_few_kernel(const __grid_constant__ ChunkArgs a, const __grid_constant__ CUtensorMap tk,
                      const __grid_constant__ CUtensorMap tv) {
-  constexpr int kRows = 8 * NB;
+  using Sh = Shape<T, NB, Q8>;
+  constexpr int kConsumers = Sh::kConsumers, kTile = Sh::kTile, kStages = Sh::kStages;
+  constexpr int kRows = Sh::kRows, kSlab = kTile * 128;
+  using M = typename std::conditional<Q8, __half, T>::type;  // what the products take
+  constexpr bool kTwo = sizeof(T) == 4;                      // q and the weights in two terms
+  constexpr int kTerms = kTwo ? 2 : 1;
+  constexpr float kShift = std::is_same<M, __half>::value ? kBias : 0.f;
   extern __shared__ __align__(1024) uint8_t smem[];
-  Shared<NB> &sh = *reinterpret_cast<Shared<NB> *>(smem);
+  Shared<T, NB, Q8> &sh = *reinterpret_cast<Shared<T, NB, Q8> *>(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (smem_u32(smem) & 1023u) {  // the swizzled tiles need it
     if (tid == 0) flag_error(a.status, KV_ERR_INVALID_ARG);
@@ -140,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
             if (tok < g.len) {
               const int ph = a.bt[(long long)g.b * a.maxP + tok / a.ps];
               if (ph >= 0 && ph < a.nphys) {
-                y = (ph * a.Hkv + g.kvh) * a.ps + tok % a.ps;
+                y = (ph * a.Hkv + g.kvh) * a.ps + (tok & (a.ps - 1));
                 ok = ((1u << (pt / 16)) - 1u) << (lane * (pt / 16));
               } else {
                 flag_error(a.status, KV_ERR_BOUNDS);
@@ -157,15 +192,18 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
           const uint32_t bar = smem_u32(&sh.full[ring.s]);
           if (lane == 0) {
             sh.tokens[ring.s] = (int)all;
-            mbar_arrive_expect_tx(bar, 2 * kCodeBytes + 2 * have * pt);
+            mbar_arrive_expect_tx(bar, 2 * Sh::kBytes + (Q8 ? 2 * have * pt : 0));
           }
           __syncwarp();
           if (lane < npg) {
-            tma_load_2d(smem_u32(&sh.code[ring.s][0][lane * pt * kHeadDim]), &tk, 0, y, bar);
-            tma_load_2d(smem_u32(&sh.code[ring.s][1][lane * pt * kHeadDim]), &tv, 0, y, bar);
-            if (ok) {
-              bulk_load(smem_u32(&sh.scale[ring.s][0][lane * pt]), a.k_scale + y, pt, bar);
-              bulk_load(smem_u32(&sh.scale[ring.s][1][lane * pt]), a.v_scale + y, pt, bar);
+            for (int w = 0; w < 2; ++w) {
+              const uint32_t dst = smem_u32(&sh.kv[ring.s][w][lane * pt * 128]);
+#pragma unroll
+              for (int slab = 0; slab < Sh::kSlabs; ++slab)
+                tma_load_2d(dst + slab * kSlab, w ? &tv : &tk, 64 * slab, y, bar);
+              if (Q8 && ok)
+                bulk_load(smem_u32(&sh.scale[ring.s][w][lane * pt]), (w ? a.v_scale : a.k_scale) + y,
+                          pt, bar);
             }
           }
         }
@@ -186,8 +224,10 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
       const int nseg = sh.share.nseg;
       for (int sg = 0; sg < nseg && live; ++sg) {
         const ChunkSeg g = sh.share.seg[sg];
-        // Q: row n = 8 nb + g8, channels 32 t4 .. + 31, as f16 pairs
-        uint32_t q[NB][16];
+        // Q: row n = 8 nb + g8, the 32 channels this thread reads of K's rows,
+        // as pairs: codes, 32 t4 .. + 31; 16-bit data, 8 of each of the 16-byte
+        // chunks 2 t4, 2 t4 + 1 of both slabs
+        uint32_t q[NB][kTerms][16];
         float qf[NB][2];  // scale * log2(e) / the row's power of two, rows 2 t4 and + 1
         int tq[NB][2];    // their tokens
 #pragma unroll
@@ -199,18 +239,17 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
           if (n < g.nrows) {
             const int pr = g.r0 + n;
             const T *src = static_cast<const T *>(a.q) +
-                           ((long long)(g.q0 + pr / a.G) * a.Hq + g.kvh * a.G + pr % a.G) *
-                               kHeadDim + 32 * t4;
+                           ((long long)(g.q0 + pr / a.G) * a.Hq + g.kvh * a.G + pr % a.G) * kHeadDim;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               float y[8];
-              load8(src + 8 * i, y);
+              load8(src + (Q8 ? 32 * t4 + 8 * i : 64 * (i >> 1) + 8 * (2 * t4 + (i & 1))), y);
 #pragma unroll
               for (int k = 0; k < 8; ++k) x[8 * i + k] = y[k];
             }
           }
           float f = a.scale_log2;
-          if constexpr (!std::is_same_v<T, __half>) {
+          if constexpr (Q8 && !std::is_same<T, __half>::value) {
             uint32_t top = 0;
 #pragma unroll
             for (int i = 0; i < 32; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
@@ -223,7 +262,13 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
             f *= pow2f(-up);
           }
 #pragma unroll
-          for (int i = 0; i < 16; ++i) q[nb][i] = pack2(x[2 * i], x[2 * i + 1], __half{});
+          for (int i = 0; i < 16; ++i) {
+            q[nb][0][i] = pack2(x[2 * i], x[2 * i + 1], M{});
+            if constexpr (kTwo) {
+              const float2 h = unpack2(q[nb][0][i], M{});
+              q[nb][1][i] = pack2(x[2 * i] - h.x, x[2 * i + 1] - h.y, M{});
+            }
+          }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             qf[nb][h] = __shfl_sync(0xFFFFFFFFu, f, 4 * (2 * t4 + h));
@@ -249,8 +294,8 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
             break;
           }
           const int tok0 = tile * kTile + warp * 16;
-          const uint8_t *kc = sh.code[ring.s][0] + warp * 16 * kHeadDim;
-          const uint8_t *vc = sh.code[ring.s][1] + warp * 16 * kHeadDim;
+          const uint8_t *kc = sh.kv[ring.s][0] + warp * 16 * 128;
+          const uint8_t *vc = sh.kv[ring.s][1] + warp * 16 * 128;
           const bool pages = (sh.tokens[ring.s] >> warp) & 1;
           // S^T: tokens g8 and g8 + 8
           float s[NB][4];
@@ -259,25 +304,28 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) s[nb][i] = 0.f;
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int at = g8 * kHeadDim + (((2 * t4 + c) ^ g8) << 4);
+          for (int c = 0; c < (Q8 ? 2 : 4); ++c) {
+            const int at = (c >> 1) * kSlab + g8 * 128 + (((2 * t4 + (c & 1)) ^ g8) << 4);
             const uint4 u = *reinterpret_cast<const uint4 *>(kc + at);
-            const uint4 v = *reinterpret_cast<const uint4 *>(kc + at + 8 * kHeadDim);
+            const uint4 v = *reinterpret_cast<const uint4 *>(kc + at + 8 * 128);
             const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
+            // a word of codes is four channels, one step; two words of 16-bit
+            // data are
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t a0 = f16_lo(uu[i]), a2 = f16_hi(uu[i]);
-              const uint32_t a1 = f16_lo(vv[i]), a3 = f16_hi(vv[i]);
+            for (int i = 0; i < (Q8 ? 4 : 2); ++i) {
+              uint32_t a0, a1, a2, a3;
+              if constexpr (Q8) {
+                a0 = f16_lo(uu[i]), a2 = f16_hi(uu[i]), a1 = f16_lo(vv[i]), a3 = f16_hi(vv[i]);
+              } else {
+                a0 = uu[2 * i], a2 = uu[2 * i + 1], a1 = vv[2 * i], a3 = vv[2 * i + 1];
+              }
+              const int k = Q8 ? 8 * c + 2 * i : 4 * c + 2 * i;
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb)
-                mma16816(s[nb], a0, a1, a2, a3, q[nb][8 * c + 2 * i], q[nb][8 * c + 2 * i + 1]);
-            }
-          }
-          uint32_t kb[2], vb[2];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            kb[i] = sh.scale[ring.s][0][warp * 16 + g8 + 8 * i];
-            vb[i] = sh.scale[ring.s][1][warp * 16 + g8 + 8 * i];
+                for (int e = kTerms - 1; e >= 0; --e)  // the small term first
+                  mma16816(s[nb], a0, a1, a2, a3, q[nb][e][k], q[nb][e][k + 1], M{});
+            }
           }
           // tokens this thread's lane speaks for: g8 + 8 i
           bool token[2], vbad[2];
@@ -285,14 +333,21 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             token[i] = pages && tok0 + g8 + 8 * i < g.len;
-            vbad[i] = !token[i] || vb[i] == (uint32_t)kQ8NanScale;
-            kf[i] = q8_scale(kb[i]);
-            ev[i] = vb[i] == (uint32_t)kQ8NanScale ? __uint_as_float(0x7FC00000u)
-                                                   : (float)((int)vb[i] - 127);
+            vbad[i] = !token[i];
+            kf[i] = 1.f;
+            ev[i] = 0.f;
+            if constexpr (Q8) {
+              const uint32_t kb = sh.scale[ring.s][0][warp * 16 + g8 + 8 * i];
+              const uint32_t vb = sh.scale[ring.s][1][warp * 16 + g8 + 8 * i];
+              vbad[i] |= vb == (uint32_t)kQ8NanScale;
+              kf[i] = q8_scale(kb);
+              ev[i] = vb == (uint32_t)kQ8NanScale ? __uint_as_float(0x7FC00000u)
+                                                  : (float)((int)vb - 127);
+            }
           }
           const uint32_t bad0 = __ballot_sync(0xFFFFFFFFu, vbad[0]);
           const uint32_t bad1 = __ballot_sync(0xFFFFFFFFu, vbad[1]);
-          uint32_t p[NB][2];
+          uint32_t p[NB][kTerms][2];
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
             float z[4], y[4];  // element i: token g8 + 8 (i >> 1), row 2 t4 + (i & 1)
@@ -304,8 +359,8 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
               const bool see = token[k] && pos <= tq[nb][h] &&
                                (a.window <= 0 || pos - tq[nb][h] > -a.window);
               z[i] = see ? s[nb][i] * (kf[k] * qf[nb][h]) : -INFINITY;
-              y[i] = see ? z[i] + ev[k] : -INFINITY;
-              move |= z[i] > m[nb][h] + kMoveAt || y[i] > r[nb][h] + kMoveAt;
+              y[i] = Q8 && see ? z[i] + ev[k] : z[i];
+              move |= z[i] > m[nb][h] + kMoveAt || (Q8 && y[i] > r[nb][h] + kMoveAt);
             }
             if (__any_sync(0xFFFFFFFFu, move)) {
 #pragma unroll
@@ -314,10 +369,10 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) {
                   mz = fmaxf(mz, __shfl_xor_sync(0xFFFFFFFFu, mz, off));
-                  my = fmaxf(my, __shfl_xor_sync(0xFFFFFFFFu, my, off));
+                  if (Q8) my = fmaxf(my, __shfl_xor_sync(0xFFFFFFFFu, my, off));
                 }
                 mz = fmaxf(mz, m[nb][h]);
-                my = fmaxf(my, r[nb][h]);
+                my = Q8 ? fmaxf(my, r[nb][h]) : mz;
                 // (from -inf: 0, and 1 where it stays there)
                 const float al = mz == -INFINITY ? 1.f : ex2(m[nb][h] - mz);
                 const float ao = my == -INFINITY ? 1.f : ex2(r[nb][h] - my);
@@ -336,51 +391,126 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
             for (int i = 0; i < 4; ++i) {
               const int h = i & 1;
               const float bm = m[nb][h] == -INFINITY ? 0.f : m[nb][h];
-              const float br = r[nb][h] == -INFINITY ? 0.f : r[nb][h] - kBias;
+              const float br = r[nb][h] == -INFINITY ? 0.f : r[nb][h] - kShift;
               l[nb][h] += ex2(z[i] - bm);
               w[i] = ex2(y[i] - br);
             }
-            p[nb][0] = movm_t(pack2(w[0], w[1], __half{}));
-            p[nb][1] = movm_t(pack2(w[2], w[3], __half{}));
-          }
-          // O^T: tokens 2 t4, 2 t4 + 1 (+ 8), channels 16 g8 .. + 15
-          uint4 v4[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int row = 2 * t4 + (i & 1) + 8 * (i >> 1);
-            v4[i] = *reinterpret_cast<const uint4 *>(vc + row * kHeadDim +
-                                                     ((g8 ^ (row & 7)) << 4));
-          }
-          if (bad0 | bad1) {
-            // rows without a token and NaN vectors must not meet a weight of 0
-            // (a row that sees a NaN vector has a NaN weight)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int row = 2 * t4 + (i & 1);  // lanes 4 row .. speak for it
-              if (((i >> 1 ? bad1 : bad0) >> (4 * row)) & 1) v4[i] = make_uint4(0, 0, 0, 0);
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t hi = pack2(w[2 * k], w[2 * k + 1], M{});
+              p[nb][0][k] = movm_t(hi);
+              if constexpr (kTwo) {
+                const float2 h = unpack2(hi, M{});
+                p[nb][1][k] = movm_t(pack2(w[2 * k] - h.x, w[2 * k + 1] - h.y, M{}));
+              }
             }
           }
+          // O^T: tokens 2 t4, 2 t4 + 1 (+ 8); channels 16 g8 .. + 15 of codes, 8 g8
+          // .. + 7 of both slabs of 16-bit data
+          uint4 v4[Sh::kSlabs][4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t wa = i == 0 ? v4[0].x : i == 1 ? v4[0].y : i == 2 ? v4[0].z : v4[0].w;
-            const uint32_t wb = i == 0 ? v4[1].x : i == 1 ? v4[1].y : i == 2 ? v4[1].z : v4[1].w;
-            const uint32_t wc = i == 0 ? v4[2].x : i == 1 ? v4[2].y : i == 2 ? v4[2].z : v4[2].w;
-            const uint32_t wd = i == 0 ? v4[3].x : i == 1 ? v4[3].y : i == 2 ? v4[3].z : v4[3].w;
+          for (int c = 0; c < Sh::kSlabs; ++c)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t ab = __byte_perm(wa, wb, h ? 0x7362 : 0x5140);
-              const uint32_t cd = __byte_perm(wc, wd, h ? 0x7362 : 0x5140);
-              const uint32_t a0 = f16_lo(ab), a1 = f16_hi(ab), a2 = f16_lo(cd), a3 = f16_hi(cd);
+            for (int i = 0; i < 4; ++i) {
+              const int row = 2 * t4 + (i & 1) + 8 * (i >> 1);
+              v4[c][i] = *reinterpret_cast<const uint4 *>(vc + c * kSlab + row * 128 +
+                                                          ((g8 ^ (row & 7)) << 4));
+              // rows without a token and NaN vectors must not meet a weight of
+              // 0 (a row that sees a NaN vector of codes has a NaN weight);
+              // lanes 4 (row & 7) .. speak for the row
+              if ((bad0 | bad1) && (((i >> 1 ? bad1 : bad0) >> (4 * (row & 7))) & 1))
+                v4[c][i] = make_uint4(0, 0, 0, 0);
+            }
+          if constexpr (!Q8) {
+            // where some row does not see some token, the same holds for
+            // infinities and NaN: they are cleared, and the rows that do see
+            // them become NaN in their channels (seldom)
+            if (tok0 + 15 > g.t_first || a.window > 0) {
+              uint32_t any = 0;
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb)
-                mma16816(o[nb][2 * i + h], a0, a1, a2, a3, p[nb][0], p[nb][1]);
+              for (int c = 0; c < Sh::kSlabs; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  any |= non_finite(v4[c][i].x, M{}) | non_finite(v4[c][i].y, M{}) |
+                         non_finite(v4[c][i].z, M{}) | non_finite(v4[c][i].w, M{});
+              if (__any_sync(0xFFFFFFFFu, any != 0)) {
+                // bit 8 c + 2 k + e of found[i]: element e of word k
+                uint32_t found[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  found[i] = 0;
+#pragma unroll
+                  for (int c = 0; c < Sh::kSlabs; ++c) {
+                    uint32_t w[4] = {v4[c][i].x, v4[c][i].y, v4[c][i].z, v4[c][i].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                      const uint32_t b = non_finite(w[k], M{});
+                      if (b & 0x8000u) w[k] &= 0xFFFF0000u, found[i] |= 1u << (8 * c + 2 * k);
+                      if (b & 0x80000000u) w[k] &= 0xFFFFu, found[i] |= 2u << (8 * c + 2 * k);
+                    }
+                    v4[c][i] = make_uint4(w[0], w[1], w[2], w[3]);
+                  }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+#pragma unroll 1
+                  for (int src = 0; src < 4; ++src) {
+                    const uint32_t f = __shfl_sync(0xFFFFFFFFu, found[i], src, 4);
+                    const int pos = tok0 + 2 * src + (i & 1) + 8 * (i >> 1);
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                      for (int h = 0; h < 2; ++h) {
+                        const bool see = pos <= tq[nb][h] &&
+                                         (a.window <= 0 || pos - tq[nb][h] > -a.window);
+#pragma unroll
+                        for (int d = 0; d < 8; ++d) {
+                          const float nan = __uint_as_float(0x7FC00000u);
+                          if (see && ((f >> (2 * d)) & 1)) o[nb][d][h] = nan;
+                          if (see && ((f >> (2 * d)) & 2)) o[nb][d][h + 2] = nan;
+                        }
+                      }
+                  }
+                }
+              }
+            }
+          }
+          // block d of O^T: of codes, channels 16 g8 + 2 d and + 1; of 16-bit
+          // data, 64 (d >> 2) + 8 g8 + 2 (d & 3) and + 1
+#pragma unroll
+          for (int d = 0; d < 8; ++d) {
+            const uint4 *x = v4[Q8 ? 0 : d >> 2];
+            const int k = Q8 ? d >> 1 : d & 3;
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = k == 0 ? x[i].x : k == 1 ? x[i].y : k == 2 ? x[i].z : x[i].w;
+            uint32_t a0, a1, a2, a3;
+            if constexpr (Q8) {
+              const uint32_t ab = __byte_perm(w[0], w[1], d & 1 ? 0x7362 : 0x5140);
+              const uint32_t cd = __byte_perm(w[2], w[3], d & 1 ? 0x7362 : 0x5140);
+              a0 = f16_lo(ab), a1 = f16_hi(ab), a2 = f16_lo(cd), a3 = f16_hi(cd);
+            } else {
+              a0 = __byte_perm(w[0], w[1], 0x5410), a1 = __byte_perm(w[0], w[1], 0x7632);
+              a2 = __byte_perm(w[2], w[3], 0x5410), a3 = __byte_perm(w[2], w[3], 0x7632);
+            }
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              if constexpr (kTwo) {
+                float t[4] = {0.f, 0.f, 0.f, 0.f};
+                mma16816(t, a0, a1, a2, a3, p[nb][1][0], p[nb][1][1], M{});
+                mma16816(t, a0, a1, a2, a3, p[nb][0][0], p[nb][0][1], M{});
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[nb][d][i] += t[i];
+              } else {
+                mma16816(o[nb][d], a0, a1, a2, a3, p[nb][0][0], p[nb][0][1], M{});
+              }
             }
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sh.empty[ring.s]));
         }
         if (!live) break;
-        // o[nb][d]: channels 16 g8 + 2 d (elements 0, 1) and + 1 (2, 3), rows 2 t4, 2 t4 + 1
+        // elements 0, 1 of o[nb][d]: its even channel, rows 2 t4 and 2 t4 + 1; 2, 3: the odd one
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -389,14 +519,14 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) lt += __shfl_xor_sync(0xFFFFFFFFu, lt, off);
             const int n = 8 * nb + 2 * t4 + h;
-            float *dst = &sh.o[warp][n][16 * g8];
 #pragma unroll
             for (int d = 0; d < 8; d += 2)
-              *reinterpret_cast<float4 *>(dst + 2 * d) = make_float4(
-                  o[nb][d][h], o[nb][d][h + 2], o[nb][d + 1][h], o[nb][d + 1][h + 2]);
+              *reinterpret_cast<float4 *>(
+                  &sh.o[warp][n][Q8 ? 16 * g8 + 2 * d : 64 * (d >> 2) + 8 * g8 + 2 * (d & 3)]) =
+                  make_float4(o[nb][d][h], o[nb][d][h + 2], o[nb][d + 1][h], o[nb][d + 1][h + 2]);
             if (g8 == 0) {
               sh.m[warp][n] = m[nb][h];
-              sh.r[warp][n] = r[nb][h] == -INFINITY ? -INFINITY : r[nb][h] - kBias;
+              sh.r[warp][n] = r[nb][h] == -INFINITY ? -INFINITY : r[nb][h] - kShift;
               sh.l[warp][n] = lt;
             }
           }
@@ -408,25 +538,23 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
           break;
         }
         const bool whole = g.whole();
+        for (int n = tid >> 4; n < min(kRows, g.nrows); n += 2 * kConsumers) {
+          const int c = (tid & 15) * 8;
+          float top = -INFINITY;
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          const int n = 8 * nb + (tid >> 4), c = (tid & 15) * 8;
-          if (n >= g.nrows) continue;
-          float M = -INFINITY;
-#pragma unroll
-          for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, sh.m[w][n]);
-          const float base = M == -INFINITY ? 0.f : M;
-          float L = 0.f, x[8] = {};
+          for (int w = 0; w < kConsumers; ++w) top = fmaxf(top, sh.m[w][n]);
+          const float base = top == -INFINITY ? 0.f : top;
+          float sum = 0.f, x[8] = {};
 #pragma unroll
           for (int w = 0; w < kConsumers; ++w) {
-            L += sh.l[w][n] * ex2(sh.m[w][n] - base);
+            sum += sh.l[w][n] * ex2(sh.m[w][n] - base);
             const float f = ex2(sh.r[w][n] - base);
 #pragma unroll
             for (int k = 0; k < 8; ++k) x[k] += sh.o[w][n][c + k] * f;
           }
           const int pr = g.r0 + n;
           if (whole) {
-            const float inv = L == 0.f ? 0.f : 1.f / L;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
             for (int k = 0; k < 8; ++k) x[k] *= inv;
             store8(static_cast<T *>(a.out) +
@@ -437,8 +565,8 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
             const long long at = (long long)part_slot(g) * a.slot_rows + n;
             store8(a.part_o + at * kHeadDim + c, x);
             if (c == 0) {
-              a.part_ml[2 * at] = M;
-              a.part_ml[2 * at + 1] = L;
+              a.part_ml[2 * at] = top;
+              a.part_ml[2 * at + 1] = sum;
             }
           }
         }
@@ -456,26 +584,44 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
     flag_error(a.status, KV_ERR_DEVICE_TIMEOUT);
 }
 
-template <class T, int NB>
+template <class T, int NB, bool Q8>
 cudaError_t few_go(const ChunkArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
                    cudaStream_t st) {
-  constexpr int bytes = (int)sizeof(Shared<NB>);
-  static_assert(bytes <= (NB == 1 ? 113 : 227) * 1024, "shared memory");
+  using Sh = Shape<T, NB, Q8>;
+  constexpr int bytes = (int)sizeof(Shared<T, NB, Q8>);
+  static_assert(bytes <= (Sh::kCtas == 2 ? 113 : 227) * 1024, "shared memory");
   const cudaError_t e = cudaFuncSetAttribute(
-      chunk_few_kernel<T, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+      chunk_few_kernel<T, NB, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  return launch_pdl(chunk_few_kernel<T, NB>, dim3(ctas), dim3(kThreads), bytes, st, a, tk, tv);
+  return launch_pdl(chunk_few_kernel<T, NB, Q8>, dim3(ctas), dim3(Sh::kThreads), bytes, st, a, tk,
+                    tv);
+}
+template <class T, bool Q8>
+cudaError_t few_rows(int rows, const ChunkArgs &a, const CUtensorMap &tk, const CUtensorMap &tv,
+                     int ctas, cudaStream_t st) {
+  if constexpr (Q8)  // (16-bit caches: 8 rows at most)
+    if (rows == 16) return few_go<T, 2, Q8>(a, tk, tv, ctas, st);
+  return few_go<T, 1, Q8>(a, tk, tv, ctas, st);
 }
 
 }  // namespace
 
-cudaError_t launch_chunk_few(int dtype, int rows, const ChunkArgs &a, const CUtensorMap &tk,
-                             const CUtensorMap &tv, int ctas, cudaStream_t st) {
+FewShape chunk_few_shape(int dtype, bool q8, int rows) {
+  if (!q8) return FewShape{Shape<__half, 1, false>::kTile, Shape<__half, 1, false>::kCtas};
+  if (dtype == KV_F32 || rows != 8)
+    return FewShape{Shape<float, 1, true>::kTile, Shape<float, 1, true>::kCtas};
+  return FewShape{Shape<__half, 1, true>::kTile, Shape<__half, 1, true>::kCtas};
+}
+
+cudaError_t launch_chunk_few(int dtype, bool q8, int rows, const ChunkArgs &a,
+                             const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
+                             cudaStream_t st) {
+  if (dtype == KV_F32) return few_go<float, 1, true>(a, tk, tv, ctas, st);  // (units of 8)
   if (dtype == KV_F16)
-    return rows == 8 ? few_go<__half, 1>(a, tk, tv, ctas, st)
-                     : few_go<__half, 2>(a, tk, tv, ctas, st);
-  return rows == 8 ? few_go<__nv_bfloat16, 1>(a, tk, tv, ctas, st)
-                   : few_go<__nv_bfloat16, 2>(a, tk, tv, ctas, st);
+    return q8 ? few_rows<__half, true>(rows, a, tk, tv, ctas, st)
+              : few_rows<__half, false>(rows, a, tk, tv, ctas, st);
+  return q8 ? few_rows<__nv_bfloat16, true>(rows, a, tk, tv, ctas, st)
+            : few_rows<__nv_bfloat16, false>(rows, a, tk, tv, ctas, st);
 }
 
 }  // namespace kvs
