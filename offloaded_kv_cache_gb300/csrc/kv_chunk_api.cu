@@ -48,8 +48,9 @@ int resolve_q8(const kv_shape *s, const kv_q8_cache *c, kv_q8_cache *dev) {
 #endif
 // Up to this many rows the kernel for few rows is taken (kv_chunk_few.cu), in us
 // against the other one: the 8-bit cache, 4 x 32k tokens, 8 kv heads, bf16 q, 8
-// rows 50 / 96, 16 rows 70 / 84, 24 rows, in units of 16, 89 / 85; fp32 q 70 /
-// 410 and 106 / 655; 16-bit caches, 1 to 8 rows, 17 x 456 tokens, 32 kv heads, 25 /
+// rows 50 / 96, 16 rows 70 / 84, 24 rows, in units of 16, 89 / 85; fp32 q at every
+// number of rows, 8 rows 70 / 410, 16 rows 106 / 655, and 2048 over 8k tokens 1064 /
+// 1735; 16-bit caches, 1 to 8 rows, 17 x 456 tokens, 32 kv heads, 25 /
 // 35, 4 x 700 tokens, 8 kv heads, 9.5 / 13, 4 x 32k tokens 64 / 66 (16 rows, in units of
 // 16, 40 / 35, 12.4 / 13.3 and 73 / 68).
 #ifndef KVS_FEW_ROWS_8BIT
@@ -95,8 +96,9 @@ ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, bool q8) {
   const bool hbm = s->kv_loc == KV_LOC_HBM;
   int per_sm = 2;
   pl.q8 = q8 && hbm;
-  if (packed <= (pl.q8 ? KVS_FEW_ROWS_8BIT : KVS_FEW_ROWS_16BIT) && (pl.mma || pl.q8)) {
-    pl.few = true;
+  // (fp32 q over the 8-bit cache: always, see above)
+  pl.few = pl.mma ? packed <= (pl.q8 ? KVS_FEW_ROWS_8BIT : KVS_FEW_ROWS_16BIT) : pl.q8;
+  if (pl.few) {
     pl.stage = !hbm;
     pl.rows = packed <= 8 || !pl.mma ? 8 : 16;
     const FewShape sh = chunk_few_shape(s->dtype, pl.q8, pl.rows);
