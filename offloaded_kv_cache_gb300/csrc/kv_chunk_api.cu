@@ -41,24 +41,27 @@ int resolve_q8(const kv_shape *s, const kv_q8_cache *c, kv_q8_cache *dev) {
 // Up to this many packed rows the 16-bit kernels' converting form reads the
 // 8-bit cache itself, in units of 64 rows; above, the cache is expanded into the
 // workspace first and read in units of 256.  (4 x 32k tokens, 8 kv heads, us,
-// direct / expanded, bf16: 64 rows 88 / 170, 128 rows 130 / 175, 192 rows 180 /
-// 184, 256 rows 224 / 185; f16: 192 rows 161 / 184, 256 rows 200 / 184.)
+// direct / expanded, bf16: 64 rows 72 / 170, 128 rows 104 / 175, 256 rows 177 /
+// 186, 320 rows 210 / 191; f16: 256 rows 154 / 185, 384 rows 216 / 192.)
 #ifndef KVS_Q8_DIRECT_ROWS
-#define KVS_Q8_DIRECT_ROWS 192
+#define KVS_Q8_DIRECT_ROWS 256
 #endif
-// Up to this many rows the kernel for few rows is taken (kv_chunk_few.cu), in us
-// against the other one: the 8-bit cache, 4 x 32k tokens, 8 kv heads, bf16 q, 8
-// rows 50 / 96, 16 rows 70 / 84, 24 rows, in units of 16, 89 / 85; fp32 q at every
-// number of rows, 8 rows 70 / 410, 16 rows 106 / 655, and 2048 over 8k tokens 1064 /
-// 1735; 16-bit caches, 1 to 8 rows, 17 x 456 tokens, 32 kv heads, 25 /
-// 35, 4 x 700 tokens, 8 kv heads, 9.5 / 13, 4 x 32k tokens 64 / 66 (16 rows, in units of
-// 16, 40 / 35, 12.4 / 13.3 and 73 / 68).
-#ifndef KVS_FEW_ROWS_8BIT
-#define KVS_FEW_ROWS_8BIT 16
-#endif
-#ifndef KVS_FEW_ROWS_16BIT
-#define KVS_FEW_ROWS_16BIT 8
-#endif
+// Up to this many packed rows the kernel for few rows is taken (kv_chunk_few.cu,
+// units of 8 that each read K and V; fp32 q over the 8-bit cache: at every
+// number).  Its reads cost more the longer the contexts may be, which the host
+// knows by the block table's width.  us, few / the other kernel, bf16 q, 8 kv heads:
+//   8-bit, 4 x 32k tokens: 8 rows 43 / 69, 16 rows 66 / 69, 24 rows 89 / 70;
+//     16 x 2k: 16 rows 22 / 27, 24 rows 26 / 27; 17 x 456, 32 kv heads: 24 rows 31 / 38
+//   16-bit, 4 x 32k: 8 rows 66 / 68, 16 rows 100 / 68; 16 x 2k: 16 rows 24.5 / 26.7,
+//     24 rows 29.7 / 26.9; 17 x 456, 32 kv heads: 8 rows 24 / 34, 16 rows 30 / 35
+//   fp32 q, 8-bit, 4 x 32k: 8 rows 70 / 410, 16 rows 106 / 655; 2048 rows over 8k
+//     tokens 1064 / 1735
+constexpr int kShortContext = 4096;  // tokens
+int few_rows_limit(const kv_shape *s, bool q8) {
+  if (s->dtype == KV_F32) return q8 ? INT_MAX : 0;
+  const bool is_short = (long long)s->max_pages_per_seq * s->page_size <= kShortContext;
+  return q8 ? (is_short ? 24 : 16) : (is_short ? 16 : 8);
+}
 // fp32: up to this many packed rows K and V go straight to registers, in units of
 // 4 or 8 rows; above, through shared memory in units of 64.  (4 x 8k tokens, 8 kv
 // heads, us, units of 8 / of 64: 12 rows 73 / 175, 24 rows 111 / 176, 32 rows 131 /
@@ -96,12 +99,11 @@ ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, bool q8) {
   const bool hbm = s->kv_loc == KV_LOC_HBM;
   int per_sm = 2;
   pl.q8 = q8 && hbm;
-  // (fp32 q over the 8-bit cache: always, see above)
-  pl.few = pl.mma ? packed <= (pl.q8 ? KVS_FEW_ROWS_8BIT : KVS_FEW_ROWS_16BIT) : pl.q8;
+  pl.few = packed <= few_rows_limit(s, pl.q8);
   if (pl.few) {
     pl.stage = !hbm;
-    pl.rows = packed <= 8 || !pl.mma ? 8 : 16;
-    const FewShape sh = chunk_few_shape(s->dtype, pl.q8, pl.rows);
+    const FewShape sh = chunk_few_shape(s->dtype, pl.q8);
+    pl.rows = sh.rows;
     pl.tile = sh.tile;
     per_sm = sh.per_sm;
   } else if (pl.mma) {
@@ -312,7 +314,7 @@ int chunk_common(const kv_shape *s, const kv_chunk *c, const void *q, const void
     if ((rc = page_map(s, pl.q8, pl.tile, a.v, pages, dev, &tv)) != KV_OK) return rc;
   }
   if (pl.few) {
-    e = launch_chunk_few(s->dtype, pl.q8, pl.rows, a, tk, tv, pl.ctas, st);
+    e = launch_chunk_few(s->dtype, pl.q8, a, tk, tv, pl.ctas, st);
   } else if (pl.mma) {
     a.row_tile = pl.row_tile;
     // a scale that is not positive is applied to Q as it is loaded

@@ -13,8 +13,8 @@
 // us per 128 tokens whatever the rows: here it is a fraction of that, which
 // short contexts and many kv heads show.
 //
-// CTA: four consumer warps and a producer warp, two CTAs per SM for 8 rows.  A
-// stage is a 64-token tile of K and V (TMA, 128-byte swizzle) and the scale bytes; a consumer warp takes 16 tokens of it
+// Units of 8 rows.  CTA: four consumer warps and a producer warp, two CTAs per SM (one
+// for fp32).  A stage is a 64-token tile of K and V (TMA, 128-byte swizzle) and the scale bytes; a consumer warp takes 16 tokens of it
 // with a softmax of its own; the warps' results are joined at the end of a
 // segment.
 //   S^T (16 tokens x 8 rows) = K Q^T: the products sum over the channels, in
@@ -44,7 +44,9 @@ namespace {
 constexpr float kMoveAt = 8.f;  // the maxima move when a weight would exceed 2^8 ...
 constexpr float kBias = 7.f;    // ... times 2^7 for f16, so that small weights keep their bits
 
-template <class T, int NB, bool Q8> struct Shape {
+constexpr int kRows = 8;  // rows of a unit
+
+template <class T, bool Q8> struct Shape {
   static constexpr int kConsumers = 4;
   static constexpr int kThreads = 32 * (kConsumers + 1);
   static constexpr int kTile = 16 * kConsumers;  // tokens per stage
@@ -52,15 +54,14 @@ template <class T, int NB, bool Q8> struct Shape {
   static constexpr int kSlabs = kRowBytes / 128;
   static constexpr int kBytes = kTile * kRowBytes;  // of K or V
   static constexpr int kStages = Q8 ? 5 : 3;
-  static constexpr int kCtas = NB == 1 && sizeof(T) == 2 ? 2 : 1;  // per SM
-  static constexpr int kRows = 8 * NB;
+  static constexpr int kCtas = sizeof(T) == 2 ? 2 : 1;  // per SM
 };
 
-template <class T, int NB, bool Q8> struct Shared {
-  using Sh = Shape<T, NB, Q8>;
+template <class T, bool Q8> struct Shared {
+  using Sh = Shape<T, Q8>;
   alignas(1024) uint8_t kv[Sh::kStages][2][Sh::kBytes];  // slabs of [token][128 bytes]
-  float o[Sh::kConsumers][Sh::kRows][kHeadDim];          // per warp, at the end of a segment
-  float m[Sh::kConsumers][Sh::kRows], r[Sh::kConsumers][Sh::kRows], l[Sh::kConsumers][Sh::kRows];
+  float o[Sh::kConsumers][kRows][kHeadDim];          // per warp, at the end of a segment
+  float m[Sh::kConsumers][kRows], r[Sh::kConsumers][kRows], l[Sh::kConsumers][kRows];
   alignas(16) uint8_t scale[Sh::kStages][2][Q8 ? Sh::kTile : 16];
   uint64_t full[Sh::kStages], empty[Sh::kStages], joined, read;
   int tokens[Sh::kStages];  // per stage: bit i: the pages of tokens 16 i .. + 15 are in range
@@ -109,20 +110,19 @@ __device__ __forceinline__ uint32_t f16_hi(uint32_t w) {
   return x;
 }
 
-// Rows of a unit: 8 NB.
-template <class T, int NB, bool Q8>
-__global__ void __launch_bounds__(Shape<T, NB, Q8>::kThreads, Shape<T, NB, Q8>::kCtas)
+template <class T, bool Q8>
+__global__ void __launch_bounds__(Shape<T, Q8>::kThreads, Shape<T, Q8>::kCtas)
     chunk_few_kernel(const __grid_constant__ ChunkArgs a, const __grid_constant__ CUtensorMap tk,
                      const __grid_constant__ CUtensorMap tv) {
-  using Sh = Shape<T, NB, Q8>;
+  using Sh = Shape<T, Q8>;
   constexpr int kConsumers = Sh::kConsumers, kTile = Sh::kTile, kStages = Sh::kStages;
-  constexpr int kRows = Sh::kRows, kSlab = kTile * 128;
+  constexpr int kSlab = kTile * 128;
   using M = typename std::conditional<Q8, __half, T>::type;  // what the products take
   constexpr bool kTwo = sizeof(T) == 4;                      // q and the weights in two terms
   constexpr int kTerms = kTwo ? 2 : 1;
   constexpr float kShift = std::is_same<M, __half>::value ? kBias : 0.f;
   extern __shared__ __align__(1024) uint8_t smem[];
-  Shared<T, NB, Q8> &sh = *reinterpret_cast<Shared<T, NB, Q8> *>(smem);
+  Shared<T, Q8> &sh = *reinterpret_cast<Shared<T, Q8> *>(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (smem_u32(smem) & 1023u) {  // the swizzled tiles need it
     if (tid == 0) flag_error(a.status, KV_ERR_INVALID_ARG);
@@ -224,70 +224,63 @@ __global__ void __launch_bounds__(Shape<T, NB, Q8>::kThreads, Shape<T, NB, Q8>::
       const int nseg = sh.share.nseg;
       for (int sg = 0; sg < nseg && live; ++sg) {
         const ChunkSeg g = sh.share.seg[sg];
-        // Q: row n = 8 nb + g8, the 32 channels this thread reads of K's rows,
+        // Q: row n = g8, the 32 channels this thread reads of K's rows,
         // as pairs: codes, 32 t4 .. + 31; 16-bit data, 8 of each of the 16-byte
         // chunks 2 t4, 2 t4 + 1 of both slabs
-        uint32_t q[NB][kTerms][16];
-        float qf[NB][2];  // scale * log2(e) / the row's power of two, rows 2 t4 and + 1
-        int tq[NB][2];    // their tokens
+        uint32_t q[kTerms][16];
+        float qf[2];  // scale * log2(e) / the row's power of two, rows 2 t4 and + 1
+        int tq[2];    // their tokens
+        float x[32];
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          const int n = 8 * nb + g8;
-          float x[32];
+        for (int i = 0; i < 32; ++i) x[i] = 0.f;
+        if (g8 < g.nrows) {
+          const int pr = g.r0 + g8;
+          const T *src = static_cast<const T *>(a.q) +
+                         ((long long)(g.q0 + pr / a.G) * a.Hq + g.kvh * a.G + pr % a.G) * kHeadDim;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = 0.f;
-          if (n < g.nrows) {
-            const int pr = g.r0 + n;
-            const T *src = static_cast<const T *>(a.q) +
-                           ((long long)(g.q0 + pr / a.G) * a.Hq + g.kvh * a.G + pr % a.G) * kHeadDim;
+          for (int i = 0; i < 4; ++i) {
+            float y[8];
+            load8(src + (Q8 ? 32 * t4 + 8 * i : 64 * (i >> 1) + 8 * (2 * t4 + (i & 1))), y);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float y[8];
-              load8(src + (Q8 ? 32 * t4 + 8 * i : 64 * (i >> 1) + 8 * (2 * t4 + (i & 1))), y);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) x[8 * i + k] = y[k];
-            }
-          }
-          float f = a.scale_log2;
-          if constexpr (Q8 && !std::is_same<T, __half>::value) {
-            uint32_t top = 0;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-            const int up = top == 0 ? 0 : min(14 - ((int)(top >> 23) - 127), 100);
-            const float s = pow2f(up);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] *= s;
-            f *= pow2f(-up);
-          }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            q[nb][0][i] = pack2(x[2 * i], x[2 * i + 1], M{});
-            if constexpr (kTwo) {
-              const float2 h = unpack2(q[nb][0][i], M{});
-              q[nb][1][i] = pack2(x[2 * i] - h.x, x[2 * i + 1] - h.y, M{});
-            }
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            qf[nb][h] = __shfl_sync(0xFFFFFFFFu, f, 4 * (2 * t4 + h));
-            tq[nb][h] = g.len - g.n + (g.r0 + min(8 * nb + 2 * t4 + h, g.nrows - 1)) / a.G;
+            for (int k = 0; k < 8; ++k) x[8 * i + k] = y[k];
           }
         }
-        float m[NB][2], r[NB][2], l[NB][2], o[NB][8][4];
+        float f = a.scale_log2;
+        if constexpr (Q8 && !std::is_same<T, __half>::value) {
+          uint32_t top = 0;
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
+          for (int i = 0; i < 32; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+          const int up = top == 0 ? 0 : min(14 - ((int)(top >> 23) - 127), 100);
+          const float s = pow2f(up);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            m[nb][h] = r[nb][h] = -INFINITY;
-            l[nb][h] = 0.f;
-          }
-#pragma unroll
-          for (int d = 0; d < 8; ++d)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[nb][d][i] = 0.f;
+          for (int i = 0; i < 32; ++i) x[i] *= s;
+          f *= pow2f(-up);
         }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          q[0][i] = pack2(x[2 * i], x[2 * i + 1], M{});
+          if constexpr (kTwo) {
+            const float2 h = unpack2(q[0][i], M{});
+            q[1][i] = pack2(x[2 * i] - h.x, x[2 * i + 1] - h.y, M{});
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          qf[h] = __shfl_sync(0xFFFFFFFFu, f, 4 * (2 * t4 + h));
+          tq[h] = g.len - g.n + (g.r0 + min(2 * t4 + h, g.nrows - 1)) / a.G;
+        }
+        float m[2], r[2], l[2], o[8][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          m[h] = r[h] = -INFINITY;
+          l[h] = 0.f;
+        }
+#pragma unroll
+        for (int d = 0; d < 8; ++d)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[d][i] = 0.f;
         for (int tile = g.tile_lo; tile < g.tile_hi; ++tile, ring.next()) {
           if (!wait(smem_u32(&sh.full[ring.s]), ring.ph)) {
             live = false;
@@ -298,11 +291,9 @@ __global__ void __launch_bounds__(Shape<T, NB, Q8>::kThreads, Shape<T, NB, Q8>::
           const uint8_t *vc = sh.kv[ring.s][1] + warp * 16 * 128;
           const bool pages = (sh.tokens[ring.s] >> warp) & 1;
           // S^T: tokens g8 and g8 + 8
-          float s[NB][4];
+          float s[4];
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[nb][i] = 0.f;
+          for (int i = 0; i < 4; ++i) s[i] = 0.f;
 #pragma unroll
           for (int c = 0; c < (Q8 ? 2 : 4); ++c) {
             const int at = (c >> 1) * kSlab + g8 * 128 + (((2 * t4 + (c & 1)) ^ g8) << 4);
@@ -321,10 +312,8 @@ __global__ void __launch_bounds__(Shape<T, NB, Q8>::kThreads, Shape<T, NB, Q8>::
               }
               const int k = Q8 ? 8 * c + 2 * i : 4 * c + 2 * i;
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                for (int e = kTerms - 1; e >= 0; --e)  // the small term first
-                  mma16816(s[nb], a0, a1, a2, a3, q[nb][e][k], q[nb][e][k + 1], M{});
+              for (int e = kTerms - 1; e >= 0; --e)  // the small term first
+                mma16816(s, a0, a1, a2, a3, q[e][k], q[e][k + 1], M{});
             }
           }
           // tokens this thread's lane speaks for: g8 + 8 i
@@ -347,62 +336,59 @@ __global__ void __launch_bounds__(Shape<T, NB, Q8>::kThreads, Shape<T, NB, Q8>::
           }
           const uint32_t bad0 = __ballot_sync(0xFFFFFFFFu, vbad[0]);
           const uint32_t bad1 = __ballot_sync(0xFFFFFFFFu, vbad[1]);
-          uint32_t p[NB][kTerms][2];
+          uint32_t p[kTerms][2];
+          float z[4], y[4];  // element i: token g8 + 8 (i >> 1), row 2 t4 + (i & 1)
+          bool move = false;
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            float z[4], y[4];  // element i: token g8 + 8 (i >> 1), row 2 t4 + (i & 1)
-            bool move = false;
+          for (int i = 0; i < 4; ++i) {
+            const int k = i >> 1, h = i & 1;
+            const int pos = tok0 + g8 + 8 * k;
+            const bool see = token[k] && pos <= tq[h] &&
+                             (a.window <= 0 || pos - tq[h] > -a.window);
+            z[i] = see ? s[i] * (kf[k] * qf[h]) : -INFINITY;
+            y[i] = Q8 && see ? z[i] + ev[k] : z[i];
+            move |= z[i] > m[h] + kMoveAt || (Q8 && y[i] > r[h] + kMoveAt);
+          }
+          if (__any_sync(0xFFFFFFFFu, move)) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int k = i >> 1, h = i & 1;
-              const int pos = tok0 + g8 + 8 * k;
-              const bool see = token[k] && pos <= tq[nb][h] &&
-                               (a.window <= 0 || pos - tq[nb][h] > -a.window);
-              z[i] = see ? s[nb][i] * (kf[k] * qf[nb][h]) : -INFINITY;
-              y[i] = Q8 && see ? z[i] + ev[k] : z[i];
-              move |= z[i] > m[nb][h] + kMoveAt || (Q8 && y[i] > r[nb][h] + kMoveAt);
-            }
-            if (__any_sync(0xFFFFFFFFu, move)) {
+            for (int h = 0; h < 2; ++h) {
+              float mz = fmaxf(z[h], z[h + 2]), my = fmaxf(y[h], y[h + 2]);
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                float mz = fmaxf(z[h], z[h + 2]), my = fmaxf(y[h], y[h + 2]);
+              for (int off = 4; off < 32; off <<= 1) {
+                mz = fmaxf(mz, __shfl_xor_sync(0xFFFFFFFFu, mz, off));
+                if (Q8) my = fmaxf(my, __shfl_xor_sync(0xFFFFFFFFu, my, off));
+              }
+              mz = fmaxf(mz, m[h]);
+              my = Q8 ? fmaxf(my, r[h]) : mz;
+              // (from -inf: 0, and 1 where it stays there)
+              const float al = mz == -INFINITY ? 1.f : ex2(m[h] - mz);
+              const float ao = my == -INFINITY ? 1.f : ex2(r[h] - my);
+              m[h] = mz;
+              r[h] = my;
+              l[h] *= al;
 #pragma unroll
-                for (int off = 4; off < 32; off <<= 1) {
-                  mz = fmaxf(mz, __shfl_xor_sync(0xFFFFFFFFu, mz, off));
-                  if (Q8) my = fmaxf(my, __shfl_xor_sync(0xFFFFFFFFu, my, off));
-                }
-                mz = fmaxf(mz, m[nb][h]);
-                my = Q8 ? fmaxf(my, r[nb][h]) : mz;
-                // (from -inf: 0, and 1 where it stays there)
-                const float al = mz == -INFINITY ? 1.f : ex2(m[nb][h] - mz);
-                const float ao = my == -INFINITY ? 1.f : ex2(r[nb][h] - my);
-                m[nb][h] = mz;
-                r[nb][h] = my;
-                l[nb][h] *= al;
-#pragma unroll
-                for (int d = 0; d < 8; ++d) {
-                  o[nb][d][h] *= ao;
-                  o[nb][d][h + 2] *= ao;
-                }
+              for (int d = 0; d < 8; ++d) {
+                o[d][h] *= ao;
+                o[d][h + 2] *= ao;
               }
             }
-            float w[4];
+          }
+          float w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int h = i & 1;
-              const float bm = m[nb][h] == -INFINITY ? 0.f : m[nb][h];
-              const float br = r[nb][h] == -INFINITY ? 0.f : r[nb][h] - kShift;
-              l[nb][h] += ex2(z[i] - bm);
-              w[i] = ex2(y[i] - br);
-            }
+          for (int i = 0; i < 4; ++i) {
+            const int h = i & 1;
+            const float bm = m[h] == -INFINITY ? 0.f : m[h];
+            const float br = r[h] == -INFINITY ? 0.f : r[h] - kShift;
+            l[h] += ex2(z[i] - bm);
+            w[i] = ex2(y[i] - br);
+          }
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const uint32_t hi = pack2(w[2 * k], w[2 * k + 1], M{});
-              p[nb][0][k] = movm_t(hi);
-              if constexpr (kTwo) {
-                const float2 h = unpack2(hi, M{});
-                p[nb][1][k] = movm_t(pack2(w[2 * k] - h.x, w[2 * k + 1] - h.y, M{}));
-              }
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t hi = pack2(w[2 * k], w[2 * k + 1], M{});
+            p[0][k] = movm_t(hi);
+            if constexpr (kTwo) {
+              const float2 h = unpack2(hi, M{});
+              p[1][k] = movm_t(pack2(w[2 * k] - h.x, w[2 * k + 1] - h.y, M{}));
             }
           }
           // O^T: tokens 2 t4, 2 t4 + 1 (+ 8); channels 16 g8 .. + 15 of codes, 8 g8
@@ -458,18 +444,16 @@ __global__ void __launch_bounds__(Shape<T, NB, Q8>::kThreads, Shape<T, NB, Q8>::
                     const uint32_t f = __shfl_sync(0xFFFFFFFFu, found[i], src, 4);
                     const int pos = tok0 + 2 * src + (i & 1) + 8 * (i >> 1);
 #pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
+                    for (int h = 0; h < 2; ++h) {
+                      const bool see = pos <= tq[h] &&
+                                       (a.window <= 0 || pos - tq[h] > -a.window);
 #pragma unroll
-                      for (int h = 0; h < 2; ++h) {
-                        const bool see = pos <= tq[nb][h] &&
-                                         (a.window <= 0 || pos - tq[nb][h] > -a.window);
-#pragma unroll
-                        for (int d = 0; d < 8; ++d) {
-                          const float nan = __uint_as_float(0x7FC00000u);
-                          if (see && ((f >> (2 * d)) & 1)) o[nb][d][h] = nan;
-                          if (see && ((f >> (2 * d)) & 2)) o[nb][d][h + 2] = nan;
-                        }
+                      for (int d = 0; d < 8; ++d) {
+                        const float nan = __uint_as_float(0x7FC00000u);
+                        if (see && ((f >> (2 * d)) & 1)) o[d][h] = nan;
+                        if (see && ((f >> (2 * d)) & 2)) o[d][h + 2] = nan;
                       }
+                    }
                   }
                 }
               }
@@ -483,7 +467,8 @@ __global__ void __launch_bounds__(Shape<T, NB, Q8>::kThreads, Shape<T, NB, Q8>::
             const int k = Q8 ? d >> 1 : d & 3;
             uint32_t w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = k == 0 ? x[i].x : k == 1 ? x[i].y : k == 2 ? x[i].z : x[i].w;
+            for (int i = 0; i < 4; ++i)
+              w[i] = k == 0 ? x[i].x : k == 1 ? x[i].y : k == 2 ? x[i].z : x[i].w;
             uint32_t a0, a1, a2, a3;
             if constexpr (Q8) {
               const uint32_t ab = __byte_perm(w[0], w[1], d & 1 ? 0x7362 : 0x5140);
@@ -493,42 +478,36 @@ __global__ void __launch_bounds__(Shape<T, NB, Q8>::kThreads, Shape<T, NB, Q8>::
               a0 = __byte_perm(w[0], w[1], 0x5410), a1 = __byte_perm(w[0], w[1], 0x7632);
               a2 = __byte_perm(w[2], w[3], 0x5410), a3 = __byte_perm(w[2], w[3], 0x7632);
             }
+            if constexpr (kTwo) {
+              float t[4] = {0.f, 0.f, 0.f, 0.f};
+              mma16816(t, a0, a1, a2, a3, p[1][0], p[1][1], M{});
+              mma16816(t, a0, a1, a2, a3, p[0][0], p[0][1], M{});
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-              if constexpr (kTwo) {
-                float t[4] = {0.f, 0.f, 0.f, 0.f};
-                mma16816(t, a0, a1, a2, a3, p[nb][1][0], p[nb][1][1], M{});
-                mma16816(t, a0, a1, a2, a3, p[nb][0][0], p[nb][0][1], M{});
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[nb][d][i] += t[i];
-              } else {
-                mma16816(o[nb][d], a0, a1, a2, a3, p[nb][0][0], p[nb][0][1], M{});
-              }
+              for (int i = 0; i < 4; ++i) o[d][i] += t[i];
+            } else {
+              mma16816(o[d], a0, a1, a2, a3, p[0][0], p[0][1], M{});
             }
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sh.empty[ring.s]));
         }
         if (!live) break;
-        // elements 0, 1 of o[nb][d]: its even channel, rows 2 t4 and 2 t4 + 1; 2, 3: the odd one
+        // elements 0, 1 of o[d]: its even channel, rows 2 t4 and 2 t4 + 1; 2, 3: the odd one
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
+        for (int h = 0; h < 2; ++h) {
+          float lt = l[h];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float lt = l[nb][h];
+          for (int off = 4; off < 32; off <<= 1) lt += __shfl_xor_sync(0xFFFFFFFFu, lt, off);
+          const int n = 2 * t4 + h;
 #pragma unroll
-            for (int off = 4; off < 32; off <<= 1) lt += __shfl_xor_sync(0xFFFFFFFFu, lt, off);
-            const int n = 8 * nb + 2 * t4 + h;
-#pragma unroll
-            for (int d = 0; d < 8; d += 2)
-              *reinterpret_cast<float4 *>(
-                  &sh.o[warp][n][Q8 ? 16 * g8 + 2 * d : 64 * (d >> 2) + 8 * g8 + 2 * (d & 3)]) =
-                  make_float4(o[nb][d][h], o[nb][d][h + 2], o[nb][d + 1][h], o[nb][d + 1][h + 2]);
-            if (g8 == 0) {
-              sh.m[warp][n] = m[nb][h];
-              sh.r[warp][n] = r[nb][h] == -INFINITY ? -INFINITY : r[nb][h] - kShift;
-              sh.l[warp][n] = lt;
-            }
+          for (int d = 0; d < 8; d += 2)
+            *reinterpret_cast<float4 *>(
+                &sh.o[warp][n][Q8 ? 16 * g8 + 2 * d : 64 * (d >> 2) + 8 * g8 + 2 * (d & 3)]) =
+                make_float4(o[d][h], o[d][h + 2], o[d + 1][h], o[d + 1][h + 2]);
+          if (g8 == 0) {
+            sh.m[warp][n] = m[h];
+            sh.r[warp][n] = r[h] == -INFINITY ? -INFINITY : r[h] - kShift;
+            sh.l[warp][n] = lt;
           }
         }
         __syncwarp();
@@ -584,44 +563,38 @@ __global__ void __launch_bounds__(Shape<T, NB, Q8>::kThreads, Shape<T, NB, Q8>::
     flag_error(a.status, KV_ERR_DEVICE_TIMEOUT);
 }
 
-template <class T, int NB, bool Q8>
+template <class T, bool Q8>
 cudaError_t few_go(const ChunkArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
                    cudaStream_t st) {
-  using Sh = Shape<T, NB, Q8>;
-  constexpr int bytes = (int)sizeof(Shared<T, NB, Q8>);
+  using Sh = Shape<T, Q8>;
+  constexpr int bytes = (int)sizeof(Shared<T, Q8>);
   static_assert(bytes <= (Sh::kCtas == 2 ? 113 : 227) * 1024, "shared memory");
   const cudaError_t e = cudaFuncSetAttribute(
-      chunk_few_kernel<T, NB, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+      chunk_few_kernel<T, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  return launch_pdl(chunk_few_kernel<T, NB, Q8>, dim3(ctas), dim3(Sh::kThreads), bytes, st, a, tk,
+  return launch_pdl(chunk_few_kernel<T, Q8>, dim3(ctas), dim3(Sh::kThreads), bytes, st, a, tk,
                     tv);
-}
-template <class T, bool Q8>
-cudaError_t few_rows(int rows, const ChunkArgs &a, const CUtensorMap &tk, const CUtensorMap &tv,
-                     int ctas, cudaStream_t st) {
-  if constexpr (Q8)  // (16-bit caches: 8 rows at most)
-    if (rows == 16) return few_go<T, 2, Q8>(a, tk, tv, ctas, st);
-  return few_go<T, 1, Q8>(a, tk, tv, ctas, st);
 }
 
 }  // namespace
 
-FewShape chunk_few_shape(int dtype, bool q8, int rows) {
-  if (!q8) return FewShape{Shape<__half, 1, false>::kTile, Shape<__half, 1, false>::kCtas};
-  if (dtype == KV_F32 || rows != 8)
-    return FewShape{Shape<float, 1, true>::kTile, Shape<float, 1, true>::kCtas};
-  return FewShape{Shape<__half, 1, true>::kTile, Shape<__half, 1, true>::kCtas};
+FewShape chunk_few_shape(int dtype, bool q8) {
+  using Own = Shape<__half, false>;
+  using Codes = Shape<__half, true>;
+  using Codes32 = Shape<float, true>;
+  return !q8                ? FewShape{kRows, Own::kTile, Own::kCtas}
+         : dtype == KV_F32 ? FewShape{kRows, Codes32::kTile, Codes32::kCtas}
+                           : FewShape{kRows, Codes::kTile, Codes::kCtas};
 }
 
-cudaError_t launch_chunk_few(int dtype, bool q8, int rows, const ChunkArgs &a,
-                             const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
-                             cudaStream_t st) {
-  if (dtype == KV_F32) return few_go<float, 1, true>(a, tk, tv, ctas, st);  // (units of 8)
+cudaError_t launch_chunk_few(int dtype, bool q8, const ChunkArgs &a, const CUtensorMap &tk,
+                             const CUtensorMap &tv, int ctas, cudaStream_t st) {
+  if (dtype == KV_F32) return few_go<float, true>(a, tk, tv, ctas, st);
   if (dtype == KV_F16)
-    return q8 ? few_rows<__half, true>(rows, a, tk, tv, ctas, st)
-              : few_rows<__half, false>(rows, a, tk, tv, ctas, st);
-  return q8 ? few_rows<__nv_bfloat16, true>(rows, a, tk, tv, ctas, st)
-            : few_rows<__nv_bfloat16, false>(rows, a, tk, tv, ctas, st);
+    return q8 ? few_go<__half, true>(a, tk, tv, ctas, st)
+              : few_go<__half, false>(a, tk, tv, ctas, st);
+  return q8 ? few_go<__nv_bfloat16, true>(a, tk, tv, ctas, st)
+            : few_go<__nv_bfloat16, false>(a, tk, tv, ctas, st);
 }
 
 }  // namespace kvs

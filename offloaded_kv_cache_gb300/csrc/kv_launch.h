@@ -86,16 +86,16 @@ cudaError_t launch_chunk_core(const ChunkArgs &a, bool q8, int rows, int ctas, c
 cudaError_t launch_chunk_mma(int dtype, bool wide, bool q8, const ChunkArgs &a,
                              const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                              int ctas, cudaStream_t st);
-// few rows: 16-bit q over a 16-bit or the 8-bit cache in units of 8 or 16 rows,
-// fp32 q over the 8-bit cache in units of 8; the maps are of K and V or the codes
+// few rows: 16-bit q over a 16-bit or the 8-bit cache, fp32 q over the 8-bit
+// cache; the maps are of K and V or the codes
 struct FewShape {
+  int rows;    // of a unit
   int tile;    // tokens per KV tile
   int per_sm;  // resident CTAs
 };
-FewShape chunk_few_shape(int dtype, bool q8, int rows);
-cudaError_t launch_chunk_few(int dtype, bool q8, int rows, const ChunkArgs &a,
-                             const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
-                             cudaStream_t st);
+FewShape chunk_few_shape(int dtype, bool q8);
+cudaError_t launch_chunk_few(int dtype, bool q8, const ChunkArgs &a, const CUtensorMap &tk,
+                             const CUtensorMap &tv, int ctas, cudaStream_t st);
 // the pages it needs into device memory in 16 bits (table: their new block table, or null)
 cudaError_t launch_chunk_stage(int dtype, bool q8, const ChunkArgs &c, void *k_out, void *v_out,
                                int32_t *table, cudaStream_t st);
