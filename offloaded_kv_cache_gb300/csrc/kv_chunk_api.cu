@@ -39,27 +39,30 @@ int resolve_q8(const kv_shape *s, const kv_q8_cache *c, kv_q8_cache *dev) {
 }
 
 // Up to this many packed rows the 16-bit kernels' converting form reads the
-// 8-bit cache itself, in units of 64 rows; above, the cache is expanded into the
+// 8-bit cache itself, in units of 128 rows; above, the cache is expanded into the
 // workspace first and read in units of 256.  (4 x 32k tokens, 8 kv heads, us,
-// direct / expanded, bf16: 64 rows 72 / 170, 128 rows 104 / 175, 256 rows 177 /
-// 186, 320 rows 210 / 191; f16: 256 rows 154 / 185, 384 rows 216 / 192.)
+// direct / expanded, bf16: 128 rows 78 / 175, 256 rows 111 / 186, 512 rows 183 /
+// 215, 640 rows 217 / 238; f16: 640 rows 189 / 239.)
 #ifndef KVS_Q8_DIRECT_ROWS
-#define KVS_Q8_DIRECT_ROWS 256
+#define KVS_Q8_DIRECT_ROWS 768
 #endif
 // Up to this many packed rows the kernel for few rows is taken (kv_chunk_few.cu,
-// units of 8 that each read K and V; fp32 q over the 8-bit cache: at every
-// number).  Its reads cost more the longer the contexts may be, which the host
-// knows by the block table's width.  us, few / the other kernel, bf16 q, 8 kv heads:
+// units of 8 that each read K and V).  Its reads cost more the longer what a row
+// sees may be, which the host knows by the block table's width and the window.
+// For fp32 q over the 8-bit cache the other kernel computes on the CUDA cores:
+// only many rows that see little are left to that one.  us, few / the other
+// kernel, 8 kv heads, bf16 q:
 //   8-bit, 4 x 32k tokens: 8 rows 43 / 69, 16 rows 66 / 69, 24 rows 89 / 70;
 //     16 x 2k: 16 rows 22 / 27, 24 rows 26 / 27; 17 x 456, 32 kv heads: 24 rows 31 / 38
 //   16-bit, 4 x 32k: 8 rows 66 / 68, 16 rows 100 / 68; 16 x 2k: 16 rows 24.5 / 26.7,
 //     24 rows 29.7 / 26.9; 17 x 456, 32 kv heads: 8 rows 24 / 34, 16 rows 30 / 35
-//   fp32 q, 8-bit, 4 x 32k: 8 rows 70 / 410, 16 rows 106 / 655; 2048 rows over 8k
-//     tokens 1064 / 1735
-constexpr int kShortContext = 4096;  // tokens
-int few_rows_limit(const kv_shape *s, bool q8) {
-  if (s->dtype == KV_F32) return q8 ? INT_MAX : 0;
-  const bool is_short = (long long)s->max_pages_per_seq * s->page_size <= kShortContext;
+//   fp32 q, 8-bit, 4 x 32k: 8 rows 70 / 410, 16 rows 106 / 655; 4 x 1.9k: 256 rows
+//     74 / 132; 8448 rows over 528, 2 kv heads: 289 / 112; window 90, 880 rows: 104 / 53
+int few_rows_limit(const kv_shape *s, int window, bool q8) {
+  const long long tokens = (long long)s->max_pages_per_seq * s->page_size;
+  const long long seen = window > 0 ? std::min<long long>(tokens, window) : tokens;
+  if (s->dtype == KV_F32) return !q8 ? 0 : seen <= 1024 ? 64 : INT_MAX;
+  const bool is_short = seen <= 4096;
   return q8 ? (is_short ? 24 : 16) : (is_short ? 16 : 8);
 }
 // fp32: up to this many packed rows K and V go straight to registers, in units of
@@ -99,7 +102,7 @@ ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, bool q8) {
   const bool hbm = s->kv_loc == KV_LOC_HBM;
   int per_sm = 2;
   pl.q8 = q8 && hbm;
-  pl.few = packed <= few_rows_limit(s, pl.q8);
+  pl.few = packed <= few_rows_limit(s, c->window, pl.q8);
   if (pl.few) {
     pl.stage = !hbm;
     const FewShape sh = chunk_few_shape(s->dtype, pl.q8);
@@ -112,8 +115,7 @@ ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, bool q8) {
     pl.q8 &= packed <= KVS_Q8_DIRECT_ROWS;
     pl.stage = (q8 && !pl.q8) || !hbm;
     // a Q tile holds whole tokens, for the TMA unit, where a token's heads fit
-    const int most = pl.q8 ? 64 : 128;
-    pl.row_tile = G <= most ? most / G * G : most;
+    pl.row_tile = G <= 128 ? 128 / G * G : 128;
     pl.wide = !pl.q8 && packed > pl.row_tile;
     pl.rows = pl.row_tile * (pl.wide ? 2 : 1);
   } else {

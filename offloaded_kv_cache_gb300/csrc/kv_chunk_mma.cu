@@ -50,20 +50,18 @@ constexpr uint32_t kTmemCols = 512;
 constexpr float kMoveAt = 8.f;  // log2 of the largest weight before the maximum moves
 
 // How a CTA works: kWide and kPair as above; kPair8 is kPair over the 8-bit
-// cache, with 64 rows per unit and four more warps that convert.
+// cache, with four more warps that convert.
 enum Mode { kWide, kPair, kPair8 };
 template <int kMode> struct Shape {
   static constexpr bool kTurns = kMode != kWide;  // the groups take tiles in turn
   static constexpr bool kQ8 = kMode == kPair8;
   static constexpr int kThreads = kQ8 ? 512 : 384;
-  static constexpr int kRows = kMode == kWide ? 256 : kMode == kPair ? 128 : 64;
   static constexpr int kQTiles = kMode == kWide ? 2 : 1;
-  // rows of a Q tile in shared memory; the product reads 128, and what stands
-  // in the place of the others only reaches rows of S that nobody reads
-  static constexpr int kQRows = kQ8 ? 64 : 128;
+  static constexpr int kQRows = 128;  // of a Q tile
+  static constexpr int kRows = kQTiles * kQRows;
   static constexpr int kQBytes = kQRows * kHeadDim * 2;
   static constexpr int kStages = kMode == kWide ? 5 : kQ8 ? 4 : 6;  // 16-bit K and V tiles
-  static constexpr int kRaw = kQ8 ? 5 : 0;                           // tiles of codes
+  static constexpr int kRaw = kQ8 ? 3 : 0;                           // tiles of codes
   static constexpr int kRingAt = kQTiles * kQBytes;
   static constexpr int kRawAt = kRingAt + kStages * kTileBytes;
   static constexpr int kTileArea = kRawAt + kRaw * kRawBytes;
