@@ -3,7 +3,6 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
-#include <mutex>
 
 #include "kv_chunk.cuh"
 #include "kv_host.h"
@@ -159,35 +158,14 @@ ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, bool q8) {
   return pl;
 }
 
-// Tensor maps, all of rows of 128 channels under the 128-byte swizzle.
-// Encoding takes host time on every call, so the last ones are kept; a map
-// follows from its key alone.
-struct MapKey {
-  int dev, type;       // CUtensorMapDataType
+// A tensor map of rows of 128 channels under the 128-byte swizzle.
+struct MapShape {
+  int type;              // CUtensorMapDataType
   const void *base;
-  long long rows;      // pages * Hkv * ps, or tokens of q
+  long long rows;        // pages * Hkv * ps, or tokens of q
   int heads, box, box2;  // heads: 0 for pages; box: rows, or heads and tokens (box2)
-  bool operator==(const MapKey &o) const {
-    return dev == o.dev && type == o.type && base == o.base && rows == o.rows &&
-           heads == o.heads && box == o.box && box2 == o.box2;
-  }
 };
-struct MapEntry {
-  MapKey key;
-  CUtensorMap map;
-};
-std::mutex g_map_mutex;
-MapEntry g_maps[16];
-unsigned g_map_n = 0;  // entries made, the last 16 of which are there
-
-int cached_map(const MapKey &k, CUtensorMap *map) {
-  std::lock_guard<std::mutex> lock(g_map_mutex);
-  for (unsigned i = 0; i < std::min(g_map_n, 16u); ++i) {
-    if (g_maps[i].key == k) {
-      *map = g_maps[i].map;
-      return KV_OK;
-    }
-  }
+int encode_map(const MapShape &k, CUtensorMap *map) {
   auto fn = encode_fn();
   if (!fn) return KV_ERR_CUDA;
   const bool codes = k.type == CU_TENSOR_MAP_DATA_TYPE_UINT8;
@@ -206,10 +184,7 @@ int cached_map(const MapKey &k, CUtensorMap *map) {
                         const_cast<void *>(k.base), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return KV_ERR_CUDA;
-  g_maps[g_map_n % 16] = MapEntry{k, *map};
-  if (++g_map_n >= 32) g_map_n -= 16;
-  return KV_OK;
+  return r == CUDA_SUCCESS ? KV_OK : KV_ERR_CUDA;
 }
 
 int type16(const kv_shape *s) {
@@ -217,18 +192,18 @@ int type16(const kv_shape *s) {
 }
 // Pages as rows [pages * Hkv * ps][128]: a box is 128 bytes, 64 channels of 16-bit
 // data or all 128 of codes, of a page's tokens that fall into one KV tile.
-int page_map(const kv_shape *s, bool codes, int tile, const void *base, long long pages, int dev,
+int page_map(const kv_shape *s, bool codes, int tile, const void *base, long long pages,
              CUtensorMap *map) {
-  return cached_map(MapKey{dev, codes ? (int)CU_TENSOR_MAP_DATA_TYPE_UINT8 : type16(s), base,
-                           pages * s->num_kv_heads * s->page_size, 0,
-                           std::min(s->page_size, tile), 0},
+  return encode_map(MapShape{codes ? (int)CU_TENSOR_MAP_DATA_TYPE_UINT8 : type16(s), base,
+                             pages * s->num_kv_heads * s->page_size, 0,
+                             std::min(s->page_size, tile), 0},
                     map);
 }
 // q: a box is 64 channels of the G heads of row_tile / G tokens.
-int q_map(const kv_shape *s, const kv_chunk *c, const void *q, int row_tile, int dev,
+int q_map(const kv_shape *s, const kv_chunk *c, const void *q, int row_tile,
           CUtensorMap *map) {
   const int G = s->num_q_heads / s->num_kv_heads;
-  return cached_map(MapKey{dev, type16(s), q, c->total_q, s->num_q_heads, G, row_tile / G}, map);
+  return encode_map(MapShape{type16(s), q, c->total_q, s->num_q_heads, G, row_tile / G}, map);
 }
 
 // The kernels count tiles in int32, and index the staged cache's rows as a
@@ -312,8 +287,8 @@ int chunk_common(const kv_shape *s, const kv_chunk *c, const void *q, const void
   }
   CUtensorMap tq = {}, tk = {}, tv = {};
   if (pl.few || (pl.mma && !pl.q8)) {
-    if ((rc = page_map(s, pl.q8, pl.tile, a.k, pages, dev, &tk)) != KV_OK) return rc;
-    if ((rc = page_map(s, pl.q8, pl.tile, a.v, pages, dev, &tv)) != KV_OK) return rc;
+    if ((rc = page_map(s, pl.q8, pl.tile, a.k, pages, &tk)) != KV_OK) return rc;
+    if ((rc = page_map(s, pl.q8, pl.tile, a.v, pages, &tv)) != KV_OK) return rc;
   }
   if (pl.few) {
     e = launch_chunk_few(s->dtype, pl.q8, a, tk, tv, pl.ctas, st);
@@ -321,7 +296,7 @@ int chunk_common(const kv_shape *s, const kv_chunk *c, const void *q, const void
     a.row_tile = pl.row_tile;
     // a scale that is not positive is applied to Q as it is loaded
     a.q_tma = a.G <= pl.row_tile && pl.row_tile % a.G == 0 && a.scale_log2 > 0.f;
-    if (a.q_tma && (rc = q_map(s, c, q, pl.row_tile, dev, &tq)) != KV_OK) return rc;
+    if (a.q_tma && (rc = q_map(s, c, q, pl.row_tile, &tq)) != KV_OK) return rc;
     e = launch_chunk_mma(s->dtype, pl.wide, pl.q8, a, tq, tk, tv, pl.ctas, st);
   } else {
     e = launch_chunk_core(a, is_q8, pl.rows, pl.ctas, st);
