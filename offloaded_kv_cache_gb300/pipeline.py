@@ -32,6 +32,7 @@ from . import kvsparse as kv
 from .workloads import Workload
 
 TORCH_DTYPE = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+TORCH_OF_CODE = {kv.DTYPE_CODE[name]: t for name, t in TORCH_DTYPE.items()}
 
 
 def storage_to_torch(a: np.ndarray, dtype: str) -> torch.Tensor:
@@ -48,6 +49,36 @@ def torch_to_bits(t: torch.Tensor) -> np.ndarray:
     if t.dtype == torch.float32:
         return t.view(torch.int32).numpy().view(np.uint32)
     return t.view(torch.int16).numpy().view(np.uint16)
+
+
+def _need(x: torch.Tensor, name: str, shape: tuple, dtype: torch.dtype):
+    """Refuses a tensor that the kernels would misread: they take a bare address."""
+    if (not x.is_cuda or x.dtype != dtype or tuple(x.shape) != tuple(shape) or
+            not x.is_contiguous()):
+        raise ValueError(f"{name}: a contiguous CUDA tensor {list(shape)} of {dtype} is needed, "
+                         f"not {list(x.shape)} of {x.dtype} on {x.device}")
+
+
+def _chunk_inputs(shape: kv.kv_shape, q_start: torch.Tensor, heads: int, **rows: torch.Tensor):
+    _need(q_start, "q_start", (shape.batch + 1,), torch.int32)
+    total = next(iter(rows.values())).shape[0]
+    for name, x in rows.items():
+        _need(x, name, (total, heads, shape.head_dim), TORCH_OF_CODE[shape.dtype])
+
+
+def _chunk_buffers(q: torch.Tensor, out, nbytes: int, stream):
+    """The output and the workspace of one chunk attention, allocated on its stream.
+
+    Each call has a workspace of its own: calls on different streams and captured
+    graphs share none, and a layer's page lists, which live in its own workspace
+    from select to attention, stay there."""
+    st = torch.cuda.ExternalStream(stream, q.device) if isinstance(stream, int) else stream
+    with torch.cuda.stream(st):
+        if out is None:
+            out = torch.empty_like(q)
+        else:
+            _need(out, "out", q.shape, q.dtype)
+        return out, torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
 
 
 class DecodeLayer:
@@ -260,14 +291,11 @@ class DecodeLayer:
 
         q: [total_q][Hq][d] on the device, q_start: [B + 1] int32 on the device."""
         stream = self._st(stream)
+        _chunk_inputs(self.shape, q_start, self.shape.num_q_heads, q=q)
         chunk = kv.make_chunk(q_start, q.shape[0], max_q_len, window)
-        out = torch.empty_like(q) if out is None else out
-        need = kv.kv_chunk_workspace_bytes(self.shape, chunk)
-        if need > self.workspace.numel():
-            self.workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+        out, space = _chunk_buffers(q, out, kv.kv_chunk_workspace_bytes(self.shape, chunk), stream)
         kv.kv_chunk_attn(self.shape, chunk, q, self.k_cache, self.v_cache, self.block_table,
-                         self.context_lens, self.scale, out, self.workspace,
-                         self.workspace.numel(), stream)
+                         self.context_lens, self.scale, out, space, space.numel(), stream)
         return out
 
     # --- host views --------------------------------------------------------
@@ -299,12 +327,12 @@ class Q8Cache:
         self.k_scale, self.v_scale = (torch.zeros(rows, dtype=torch.uint8, **where)
                                       for _ in range(2))
         self.cache = kv.make_q8_cache(self.k_codes, self.v_codes, self.k_scale, self.v_scale)
-        self.workspace = torch.empty(16, dtype=torch.uint8, device=self.device)
 
     def append(self, k_new: torch.Tensor, v_new: torch.Tensor, q_start: torch.Tensor,
                max_q_len: int, stream=None):
         """Quantise and store the new tokens (k_new, v_new: [total_q][Hkv][d]) behind
         each sequence's cached ones; context_lens grows in place."""
+        _chunk_inputs(self.shape, q_start, self.shape.num_kv_heads, k_new=k_new, v_new=v_new)
         chunk = kv.make_chunk(q_start, k_new.shape[0], max_q_len)
         kv.kv_q8_append(self.shape, chunk, k_new, v_new, self.cache, self.block_table,
                         self.context_lens, self.context_lens, DecodeLayer._st(stream))
@@ -312,14 +340,13 @@ class Q8Cache:
     def attend(self, q: torch.Tensor, q_start: torch.Tensor, max_q_len: int, scale: float,
                window: int = 0, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """Attention of the chunk whose tokens were appended last (q: [total_q][Hq][d])."""
+        stream = DecodeLayer._st(stream)
+        _chunk_inputs(self.shape, q_start, self.shape.num_q_heads, q=q)
         chunk = kv.make_chunk(q_start, q.shape[0], max_q_len, window)
-        out = torch.empty_like(q) if out is None else out
-        need = kv.kv_q8_chunk_workspace_bytes(self.shape, chunk)
-        if need > self.workspace.numel():
-            self.workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+        out, space = _chunk_buffers(q, out, kv.kv_q8_chunk_workspace_bytes(self.shape, chunk),
+                                    stream)
         kv.kv_q8_chunk_attn(self.shape, chunk, q, self.cache, self.block_table, self.context_lens,
-                            scale, out, self.workspace, self.workspace.numel(),
-                            DecodeLayer._st(stream))
+                            scale, out, space, space.numel(), stream)
         return out
 
     def read_back(self, k_out: torch.Tensor, v_out: torch.Tensor,
@@ -327,5 +354,10 @@ class Q8Cache:
         """The cached tokens in the model's type, into pages out_table[b][p] (default:
         the same page numbers) of k_out, v_out [pages][Hkv][ps][d] on the device."""
         table = self.block_table if out_table is None else out_table
+        s = self.shape
+        pages = (k_out.shape[0], s.num_kv_heads, s.page_size, s.head_dim)
+        _need(k_out, "k_out", pages, TORCH_OF_CODE[s.dtype])
+        _need(v_out, "v_out", pages, TORCH_OF_CODE[s.dtype])
+        _need(table, "out_table", (s.batch, s.max_pages_per_seq), torch.int32)
         kv.kv_q8_read(self.shape, self.cache, self.block_table, self.context_lens, table,
                       k_out.shape[0], k_out, v_out, DecodeLayer._st(stream))

@@ -137,3 +137,25 @@ def test_quantiser_definition(dtype, least):
     assert np.array_equal(c[same], t[same])
     err = np.abs(restore(c, s) - np.clip(x, -57344, 57344))
     assert (err <= np.maximum(np.abs(x) * 2.0 ** -4, 2.0 ** -10 * 2.0 ** e[:, None])).all()
+
+
+def test_pipeline_refuses_tensors_the_kernels_would_misread():
+    """A bare address says nothing of type, shape, order or place."""
+    from offloaded_kv_cache_gb300 import pipeline
+    x = torch.zeros(3, 2, 128)
+    for got, shape, dtype in ((x, (3, 2, 128), torch.float32),      # not on the device
+                              (x, (3, 2, 128), torch.float16),
+                              (x, (3, 4, 128), torch.float32)):
+        with pytest.raises(ValueError, match="contiguous CUDA tensor"):
+            pipeline._need(got, "q", shape, dtype)
+    table = torch.zeros(1, 2, dtype=torch.int32)
+    lens = torch.zeros(1, dtype=torch.int32)
+    q8 = pipeline.Q8Cache(kv.make_shape(1, 4, 2, 128, 16, 2, 2, "f32", "hbm"), table, lens,
+                          device="cpu")
+    start = torch.tensor([0, 3], dtype=torch.int32)
+    with pytest.raises(ValueError, match="q_start"):
+        q8.append(x, x, start, 3, stream=0)
+    with pytest.raises(ValueError, match="q_start"):
+        q8.attend(torch.zeros(3, 4, 128), start, 3, 1.0, stream=0)
+    with pytest.raises(ValueError, match="k_out"):
+        q8.read_back(torch.zeros(2, 2, 16, 128), torch.zeros(2, 2, 16, 128), stream=0)

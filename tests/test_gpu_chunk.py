@@ -474,3 +474,66 @@ def test_pipeline_classes(dtype, loc):
     # both compute the same sums, each within 2^-8 (2^-11, 2^-24) of weights and result
     tol = {"f32": 1e-5, "f16": 2.0 ** -9, "bf16": 2.0 ** -6}[dtype]
     assert float((got.float() - again.float()).abs().max()) <= tol * (1 + float(back[1].abs().max()))
+
+
+def _small_layer(dtype="bf16"):
+    from offloaded_kv_cache_gb300 import workloads as W
+    from offloaded_kv_cache_gb300.pipeline import DecodeLayer
+    spec = W.tiny_spec(dtype=dtype, batch=2, hq=8, hkv=2, context=600, ps=16, topk=5, index=7)
+    layer = DecodeLayer(W.generate(spec, context_lens=[600, 333]))
+    g = torch.Generator().manual_seed(3)
+
+    def rows(*n):
+        start = torch.tensor([0, n[0], sum(n)], dtype=torch.int32, device="cuda")
+        return torch.randn(sum(n), 8, D, generator=g).to(TORCH[dtype]).cuda(), start, max(n)
+    return layer, rows
+
+
+def test_pipeline_chunk_leaves_the_selected_pages():
+    """The page lists of select_fused stay in the layer's workspace over a chunk."""
+    layer, rows = _small_layer()
+    layer.build_index()
+    layer.sparse_step_fused()
+    want = layer.out.clone()
+    layer.select_fused()
+    layer.chunk_attn(*rows(200, 300))
+    layer.sparse_attn_selected()
+    assert torch.equal(layer.out, want)
+
+
+def test_pipeline_chunk_in_graphs():
+    """Two captured calls replay together, and after larger eager ones, as they ran alone."""
+    layer, rows = _small_layer()
+    calls = [rows(1, 1), rows(40, 60)]
+    want = [layer.chunk_attn(*c) for c in calls]
+    graphs, got, streams = [], [], []
+    for c in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append(layer.chunk_attn(*c))
+        graphs.append(g)
+        streams.append(torch.cuda.Stream())
+    big = rows(500, 333)
+    alone = layer.chunk_attn(*big)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+        assert torch.equal(layer.chunk_attn(*big), alone)
+    torch.cuda.synchronize()
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
+
+
+def test_pipeline_chunk_refusals():
+    layer, rows = _small_layer()
+    q, start, most = rows(3, 4)
+    for bad in (q.half(), q[:, :4], q.transpose(0, 1).contiguous().transpose(0, 1),
+                torch.zeros(7, 8, D, dtype=q.dtype)):
+        with pytest.raises(ValueError, match="q: a contiguous"):
+            layer.chunk_attn(bad, start, most)
+    with pytest.raises(ValueError, match="q_start"):
+        layer.chunk_attn(q, start[:2], most)
+    with pytest.raises(ValueError, match="out"):
+        layer.chunk_attn(q, start, most, out=torch.empty_like(q, dtype=torch.float32))
