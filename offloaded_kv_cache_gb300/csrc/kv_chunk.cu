@@ -21,7 +21,9 @@ constexpr int kPStr = kTile + 4;
 // (a 4 x 4 register block per thread), one streaming-softmax step (row
 // maximum and sum over the 16 tx lanes), output += P V.  The weights P take
 // K's place in shared memory once the scores are done, so that two CTAs fit an
-// SM.  FP32 multiply-adds bound it for many rows, the K/V stream for few.
+// SM.  FP32 multiply-adds and the shared-memory reads that feed them bound it: 256
+// rows over 8192 tokens, 32/8 heads, 875 us on one GB300, 38.7 TFLOP/s (two products
+// per instruction, with the sums over even and odd channels apart, 978 us).
 constexpr int MR = 4;
 constexpr int kTileRows = 16 * MR;
 constexpr int kKBytes = kTile * kQStr * 4;
@@ -290,7 +292,9 @@ __global__ void __launch_bounds__(kThreads) chunk_core_kernel(const __grid_const
 // halving exchanges (one shuffle per sum), which leaves lane l the rows
 // (l & 3) R / 4 .. of token l / 4; the weights come back through shared memory.
 // The K/V stream bounds it at one row per kv head; at 8, multiply-adds and
-// shuffles about as much.
+// shuffles about as much.  One token over 4 x 8192 tokens, 32/8 heads: 44 us on one
+// GB300, 6.1 TB/s; 33 rows over 4096 tokens, one head: 15 us, the chain of a
+// CTA's few tiles and the combine.
 constexpr int kFewWarps = kThreads / 32;
 constexpr float kMoveAt = 8.f;  // the maximum moves when a weight would exceed 2^8
 template <int R> struct FewShared {

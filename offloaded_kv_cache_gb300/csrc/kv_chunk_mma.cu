@@ -2,11 +2,12 @@
 // (tcgen05, accumulators in TMEM).  kv_chunk.cuh has the formula and how the
 // work is cut into shares of segments.
 //
-// One CTA per SM, twelve warps:
+// One CTA per SM, twelve warps, or sixteen over the 8-bit cache:
 //   warps 0-3, 4-7  two softmax groups, a thread per packed row
 //   warp 8          loads K and V tiles (TMA, one box per page and 64 channels)
 //   warp 9          issues the matrix products (one lane)
 //   warp 10, 11     mend V at the edges (below); warp 11 loads Q
+//   warps 12-15     (8-bit) expand tiles of codes into the ring's 16-bit tiles
 // Per KV tile of 128 tokens and softmax group: S = Q K^T (128 x 128 x 128)
 // into TMEM; the group takes its maximum and exponentials and writes the
 // weights P in 16 bits over S; O += P V.  While one group computes, the tensor
@@ -18,6 +19,23 @@
 //     turn (even, odd) and join their results at the end.  For few rows per
 //     sequence, where the K/V stream is the bound and each tile's chain of
 //     product, softmax and product would otherwise be exposed.
+//   * kPair8: kPair over the 8-bit cache, up to kv_chunk_api.cu's limit of rows.
+//
+// What bounds it, measured on one GB300 (a copy reaches 6.68 TB/s, a large bf16
+// matrix product 1.91 PFLOP/s):
+//   * kWide, 2048 new tokens at the end of 32768, 32/8 heads, bf16: 676-741 us
+//     from box to box, 1.44-1.58 PFLOP/s.  Products and softmax share the time: the
+//     tensor pipe is active for two thirds of it, and what is left is each
+//     group's chain of scores, maximum, exponentials and weights.
+//   * kWide, 32 prompts of 512, 32/32 heads, f16: 110 us for 41 us of bytes.  A
+//     unit has two or four tiles, one or two of them at the diagonal, so a fill
+//     and a drain of the chain comes with every few tiles (units of 128 rows
+//     whose groups take tiles in turn 127 us).
+//   * kPair, 5 new tokens over 8 x 65536, 64/8 heads, bf16: 224 us, 6.7 TB/s: the
+//     K/V stream.
+//   * kPair8, 4 x 32768 tokens, 8 kv heads, bf16: 69 us up to 32 rows, 78 us for
+//     128, 183 us for 512.  The four converting warps (eight, which leave the
+//     others fewer registers, were no faster).
 //
 // The running maximum is moved only when a row's new maximum exceeds it by
 // more than 2^8 in the weights: until then the weights may be as large as 2^8,
