@@ -8,9 +8,10 @@
 // Work.  The G query heads of a kv head read the same K and V, so their rows
 // are packed: packed row r = i * G + g is token i, head kvh * G + g.  A unit
 // is `rows` consecutive packed rows of one (sequence, kv head); it meets the
-// KV tiles [tile_lo, tile_hi) its rows can see, one at least.  All units' tiles laid end to end
-// (sequence, kv head, row block; lengths differ, so the total is known on the
-// device only) are cut into equal shares, one per CTA, one CTA per SM.  A
+// KV tiles [tile_lo, tile_hi) its rows can see, one at least.  All units' tiles, and a
+// cost of a tile or two per unit, laid end to end (sequence, kv head, row block;
+// lengths differ, so the total is known on the device only) are cut into equal
+// shares, one per CTA, as many CTAs as are resident.  A
 // share is a list of segments: the end of one unit, whole units, the start of
 // another.  A unit within one share is written to out; the others leave
 // partial results (at most two per CTA, so the workspace does not grow with
@@ -39,6 +40,7 @@ struct ChunkArgs {
   long long nphys;
   int B, Hq, Hkv, G, ps, maxP, total_q, max_q_len, window;
   int slot_rows;
+  int unit_cost;     // tiles that a unit counts beyond its own when the work is cut
   int row_tile;      // tensor cores: packed rows per Q tile
   int q_tma;         // tensor cores: Q tiles are whole tokens, copied by the TMA unit
   float scale_log2;  // scale * log2(e)
@@ -91,10 +93,10 @@ struct ChunkSeg {
 // A CTA's share, kSegs segments of it listed at a time.
 template <int kSegs> struct ChunkShare {
   // (the host refuses calls whose tiles might not fit int32)
-  int per, extra;          // tiles per share; the first `extra` shares hold one more
+  int per, extra;          // share: what it counts; the first `extra` shares hold one more
   int hi;                  // end of this CTA's share in the units laid end to end
-  int b, kvh, r0, off;     // walk: the next unit, and its tiles already passed
-  int left;                // tiles of the share not listed yet
+  int b, kvh, r0, off;     // walk: the next unit, and how much of it is passed
+  int left;                // of the share, not listed yet
   int nseg;
   ChunkSeg seg[kSegs];
 };
@@ -102,7 +104,9 @@ template <int kSegs> struct ChunkShare {
 __device__ __forceinline__ int packed_rows(const ChunkArgs &a, const ChunkSeq &s) {
   return s.n * a.G;  // checked on the host against int32 (max_q_len * G)
 }
-// tiles of all row blocks of one kv head of sequence s
+// What all row blocks of one kv head of sequence s count when the work is cut: their
+// tiles, and unit_cost for each.  (A unit counts its tiles first: a share that ends
+// among the rest ends behind the unit, whole.)
 __device__ __forceinline__ int head_tiles(const ChunkArgs &a, const ChunkSeq &s, int rows,
                                           int tile) {
   const int R = packed_rows(a, s);
@@ -110,7 +114,7 @@ __device__ __forceinline__ int head_tiles(const ChunkArgs &a, const ChunkSeq &s,
 #pragma unroll 1
   for (int r0 = 0; r0 < R; r0 += rows) {
     const TileRange t = unit_tiles(a, s, r0, min(rows, R - r0), tile);
-    w += t.hi - t.lo;
+    w += t.hi - t.lo + a.unit_cost;
   }
   return w;
 }
@@ -171,8 +175,9 @@ __device__ __forceinline__ void share_init(const ChunkArgs &a, int rows, int til
 #pragma unroll 1
         for (;; r0 += rows) {
           const TileRange t2 = unit_tiles(a, s, r0, min(rows, R - r0), tile);
-          if (rem < t2.hi - t2.lo || r0 + rows >= R) break;
-          rem -= t2.hi - t2.lo;
+          const int cost = t2.hi - t2.lo + a.unit_cost;
+          if (rem < cost || r0 + rows >= R) break;
+          rem -= cost;
         }
         sh->r0 = r0;
         sh->off = rem;
@@ -201,9 +206,12 @@ __device__ __forceinline__ void share_next(const ChunkArgs &a, int rows, int til
     while (n < kSegs && left > 0) {
       const int nrows = min(rows, R - r0);
       const TileRange t = unit_tiles(a, s, r0, nrows, tile);
-      const int have = t.hi - t.lo - off;
-      const int take = min(have, left);
-      ChunkSeg &g = sh->seg[n++];
+      const int tiles = t.hi - t.lo;
+      const int take = min(tiles + a.unit_cost - off, left);
+      const int tile_hi = min(off + take, tiles);
+      // (written over by the next one where none of the unit's tiles is in the share)
+      ChunkSeg &g = sh->seg[n];
+      if (off < tiles) ++n;
       g.b = b;
       g.kvh = kvh;
       g.r0 = r0;
@@ -212,8 +220,8 @@ __device__ __forceinline__ void share_next(const ChunkArgs &a, int rows, int til
       g.n = s.n;
       g.len = s.len;
       g.tile_lo = t.lo + off;
-      g.tile_hi = t.lo + off + take;
-      g.parts = (off == 0 ? 1 : 0) | (take == have ? 2 : 0);
+      g.tile_hi = t.lo + tile_hi;
+      g.parts = (off == 0 ? 1 : 0) | (tile_hi == tiles ? 2 : 0);
       g.t_first = s.len - s.n + r0 / a.G;
       g.t_last = s.len - s.n + (r0 + nrows - 1) / a.G;
       g.edge_from = g.t_first < s.len - 1        ? max(g.t_first + 1, 0) / tile
@@ -224,7 +232,7 @@ __device__ __forceinline__ void share_next(const ChunkArgs &a, int rows, int til
       g.half_hi = max(t_half, 0) / tile + 1;
       if (g.parts == 1) {
         // the CTA whose share holds the unit's last tile
-        const int end = sh->hi - left + (t.hi - t.lo) - 1, big = sh->extra * (sh->per + 1);
+        const int end = sh->hi - left + tiles - 1, big = sh->extra * (sh->per + 1);
         const int j = end < big ? end / (sh->per + 1) : sh->extra + (end - big) / sh->per;
         a.meta[2 * blockIdx.x] = make_int4(b, kvh, r0, nrows);
         a.meta[2 * blockIdx.x + 1] = make_int4(s.q0, j, 0, 0);

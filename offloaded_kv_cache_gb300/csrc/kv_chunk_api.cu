@@ -45,6 +45,25 @@ int resolve_q8(const kv_shape *s, const kv_q8_cache *c, kv_q8_cache *dev) {
 #ifndef KVS_Q8_DIRECT_ROWS
 #define KVS_Q8_DIRECT_ROWS 768
 #endif
+// What a row may see, as far as the host knows.
+long long seen_tokens(const kv_shape *s, int window) {
+  const long long tokens = (long long)s->max_pages_per_seq * s->page_size;
+  return window > 0 ? std::min<long long>(tokens, window) : tokens;
+}
+// 16-bit K/V on the tensor cores: while a row sees few tokens the loads of Q, the
+// diagonal and the way out are most of a unit, and two CTAs with a unit of 128
+// rows each cover them for one another (kSolo); over long contexts units of 256
+// rows read K and V half as often (kWide), and few rows keep more of the stream in
+// flight with an SM's whole memory (kPair).  us, two CTAs / one, bf16: 32 prompts of
+// 512, 32/32 heads 82 / 95, of 800 142 / 155, of 1000 194 / 195, of 1400 336 / 290;
+// 4 of 800, 64/8 heads 54 / 52; 20 new tokens over 32 x 1000, 32/32 heads 61 / 68;
+// 32/8 heads, over 32 x 4000 66 / 73, over 32 x 8000 110 / 120, over 1 x 8000 31 / 25.
+#ifndef KVS_SOLO_TOKENS
+#define KVS_SOLO_TOKENS 896
+#endif
+#ifndef KVS_SOLO_FEW
+#define KVS_SOLO_FEW 4096
+#endif
 // Up to this many packed rows the kernel for few rows is taken (kv_chunk_few.cu,
 // units of 8 that each read K and V).  Its reads cost more the longer what a row
 // sees may be, which the host knows by the block table's width and the window.
@@ -58,8 +77,7 @@ int resolve_q8(const kv_shape *s, const kv_q8_cache *c, kv_q8_cache *dev) {
 //   fp32 q, 8-bit, 4 x 32k: 8 rows 70 / 410, 16 rows 106 / 655; 4 x 1.9k: 256 rows
 //     74 / 132; 8448 rows over 528, 2 kv heads: 289 / 112; window 90, 880 rows: 104 / 53
 int few_rows_limit(const kv_shape *s, int window, bool q8) {
-  const long long tokens = (long long)s->max_pages_per_seq * s->page_size;
-  const long long seen = window > 0 ? std::min<long long>(tokens, window) : tokens;
+  const long long seen = seen_tokens(s, window);
   if (s->dtype == KV_F32) return !q8 ? 0 : seen <= 1024 ? 64 : INT_MAX;
   const bool is_short = seen <= 4096;
   return q8 ? (is_short ? 24 : 16) : (is_short ? 16 : 8);
@@ -81,7 +99,12 @@ struct ChunkPlan {
   int rows = 64;      // packed rows per unit
   int tile = 64;      // tokens per KV tile
   int row_tile = 0;   // tensor cores: packed rows per Q tile (a unit is one, or two when wide)
-  bool wide = false;
+  ChunkForm form = kPair;
+  // Tiles that a unit counts beyond its own: its start and its end.  (us at 0 / 1 / 2:
+  // 32 prompts of 2000, 32/8 heads, kWide 405 / 385 / 374; of 512, kSolo 75 / 68 / 68;
+  // fp32 over 8 bits, 32 x 300 tokens 17.6 / 16.2 / 16.0; one token, 4 x 700, 8 bits 9.7
+  // / 10.1 / 10.2.)
+  int unit_cost = 1;
   double most_tiles = 0;  // an upper bound of the call's (unit, KV tile) pairs
   int ctas = 1;
   int slot_rows = 1;  // rows of a partial result
@@ -110,13 +133,19 @@ ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, bool q8) {
     per_sm = sh.per_sm;
   } else if (pl.mma) {
     pl.tile = kChunkTile;
-    per_sm = 1;
     pl.q8 &= packed <= KVS_Q8_DIRECT_ROWS;
     pl.stage = (q8 && !pl.q8) || !hbm;
     // a Q tile holds whole tokens, for the TMA unit, where a token's heads fit
     pl.row_tile = G <= 128 ? 128 / G * G : 128;
-    pl.wide = !pl.q8 && packed > pl.row_tile;
-    pl.rows = pl.row_tile * (pl.wide ? 2 : 1);
+    const long long seen = seen_tokens(s, c->window);
+    const bool many = packed > pl.row_tile;
+    pl.form = pl.q8                                               ? kPair8
+              : seen <= (many ? KVS_SOLO_TOKENS : KVS_SOLO_FEW) ? kSolo
+              : many                                              ? kWide
+                                                                  : kPair;
+    pl.rows = pl.row_tile * (pl.form == kWide ? 2 : 1);
+    per_sm = pl.form == kSolo ? 2 : 1;
+    if (pl.form != kSolo) pl.unit_cost = 2;
   } else {
     // few rows in units of 4 or 8, also while units of 64 would not fill the GPU
     const double units64 = std::min((double)s->batch * ((packed + 63) / 64),
@@ -132,7 +161,7 @@ ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, bool q8) {
   const double units = std::min((double)s->batch * ((packed + pl.rows - 1) / pl.rows),
                                 (double)c->total_q * G / pl.rows + s->batch);
   const long long tiles = ((long long)s->max_pages_per_seq * s->page_size + pl.tile - 1) / pl.tile;
-  pl.most_tiles = units * s->num_kv_heads * tiles;
+  pl.most_tiles = units * s->num_kv_heads * (tiles + pl.unit_cost);
   pl.ctas = (int)std::min<double>((double)per_sm * sms, std::max(1.0, pl.most_tiles));
   pl.slot_rows = (int)std::min<long long>(pl.rows, packed);
   size_t off = align256((size_t)pl.ctas * 32);
@@ -269,6 +298,7 @@ int chunk_common(const kv_shape *s, const kv_chunk *c, const void *q, const void
   // a window as wide as the longest row is no window
   a.window = c->window >= (long long)a.maxP * a.ps ? 0 : c->window;
   a.slot_rows = pl.slot_rows;
+  a.unit_cost = pl.unit_cost;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.wait_limit_ns = wait_limit_ns();
   a.debug_skip_tile = debug_skip_page() < 0 ? -1 : debug_skip_page() / (pl.tile / kTileTokens);
@@ -297,7 +327,7 @@ int chunk_common(const kv_shape *s, const kv_chunk *c, const void *q, const void
     // a scale that is not positive is applied to Q as it is loaded
     a.q_tma = a.G <= pl.row_tile && pl.row_tile % a.G == 0 && a.scale_log2 > 0.f;
     if (a.q_tma && (rc = q_map(s, c, q, pl.row_tile, &tq)) != KV_OK) return rc;
-    e = launch_chunk_mma(s->dtype, pl.wide, pl.q8, a, tq, tk, tv, pl.ctas, st);
+    e = launch_chunk_mma(s->dtype, pl.form, a, tq, tk, tv, pl.ctas, st);
   } else {
     e = launch_chunk_core(a, is_q8, pl.rows, pl.ctas, st);
   }

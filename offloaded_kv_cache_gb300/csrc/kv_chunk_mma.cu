@@ -2,23 +2,25 @@
 // (tcgen05, accumulators in TMEM).  kv_chunk.cuh has the formula and how the
 // work is cut into shares of segments.
 //
-// One CTA per SM, twelve warps, or sixteen over the 8-bit cache:
-//   warps 0-3, 4-7  two softmax groups, a thread per packed row
-//   warp 8          loads K and V tiles (TMA, one box per page and 64 channels)
-//   warp 9          issues the matrix products (one lane)
-//   warp 10, 11     mend V at the edges (below); warp 11 loads Q
-//   warps 12-15     (8-bit) expand tiles of codes into the ring's 16-bit tiles
+// A CTA's warps:
+//   4 or 8    one or two softmax groups, a thread per packed row
+//   1         loads K and V tiles (TMA, one box per page and 64 channels)
+//   1         issues the matrix products (one lane)
+//   2         mend V at the edges (below); the second loads Q
+//   4         (8-bit) expand tiles of codes into the ring's 16-bit tiles
 // Per KV tile of 128 tokens and softmax group: S = Q K^T (128 x 128 x 128)
 // into TMEM; the group takes its maximum and exponentials and writes the
 // weights P in 16 bits over S; O += P V.  While one group computes, the tensor
-// cores work for the other.  TMEM: S and P of the groups at columns 0 and 128,
-// O at 256 and 384.
+// cores work for the other, of the same CTA or of another.  TMEM: S and P of
+// two groups at columns 0 and 128, O at 256 and 384; of one at 0 and at 128.
 //   * kWide: a unit is 256 packed rows, 128 per group; both groups use
 //     each K/V tile, which halves the reads of K and V per product.
 //   * kPair: a unit is up to 128 rows; the groups take its KV tiles in
 //     turn (even, odd) and join their results at the end.  For few rows per
 //     sequence, where the K/V stream is the bound and each tile's chain of
 //     product, softmax and product would otherwise be exposed.
+//   * kSolo: a unit is up to 128 rows and a CTA has one group; two CTAs per SM.
+//     For short contexts, where a unit's start and end are much of it.
 //   * kPair8: kPair over the 8-bit cache, up to kv_chunk_api.cu's limit of rows.
 //
 // What bounds it, measured on one GB300 (a copy reaches 6.68 TB/s, a large bf16
@@ -27,10 +29,10 @@
 //     from box to box, 1.44-1.58 PFLOP/s.  Products and softmax share the time: the
 //     tensor pipe is active for two thirds of it, and what is left is each
 //     group's chain of scores, maximum, exponentials and weights.
-//   * kWide, 32 prompts of 512, 32/32 heads, f16: 110 us for 41 us of bytes.  A
-//     unit has two or four tiles, one or two of them at the diagonal, so a fill
-//     and a drain of the chain comes with every few tiles (units of 128 rows
-//     whose groups take tiles in turn 127 us).
+//   * kSolo, 32 prompts of up to 512, 32/32 heads, f16: 81 us for 41 us of bytes
+//     (kWide 95).  A unit has one to four tiles, each a chain of some 2900 cycles
+//     (product, maximum, exponentials, product), and 3500 more to write out, which
+//     two CTAs per SM cover for one another in part.
 //   * kPair, 5 new tokens over 8 x 65536, 64/8 heads, bf16: 224 us, 6.7 TB/s: the
 //     K/V stream.
 //   * kPair8, 4 x 32768 tokens, 8 kv heads, bf16: 69 us up to 32 rows, 78 us for
@@ -64,25 +66,27 @@ constexpr int kTile = kChunkTile;
 constexpr int kTileBytes = kTile * kHeadDim * 2;  // 32 KB
 constexpr int kSlab = kTile * 128;                // 64 channels of a tile
 constexpr int kRawBytes = kTile * kHeadDim;       // a tile of codes
-constexpr uint32_t kTmemCols = 512;
 constexpr float kMoveAt = 8.f;  // log2 of the largest weight before the maximum moves
 
-// How a CTA works: kWide and kPair as above; kPair8 is kPair over the 8-bit
-// cache, with four more warps that convert.
-enum Mode { kWide, kPair, kPair8 };
+// How a CTA works: kMode is a ChunkForm.
 template <int kMode> struct Shape {
-  static constexpr bool kTurns = kMode != kWide;  // the groups take tiles in turn
+  static constexpr bool kHalves = kMode == kWide;  // each group has half a unit's rows
+  static constexpr bool kTurns = kMode == kPair || kMode == kPair8;  // the groups take tiles in turn
+  static constexpr int kGroups = kMode == kSolo ? 1 : 2;
+  static constexpr int kCtas = kMode == kSolo ? 2 : 1;  // per SM
   static constexpr bool kQ8 = kMode == kPair8;
-  static constexpr int kThreads = kQ8 ? 512 : 384;
+  static constexpr int kThreads = kMode == kSolo ? 256 : kQ8 ? 512 : 384;
   static constexpr int kQTiles = kMode == kWide ? 2 : 1;
   static constexpr int kQRows = 128;  // of a Q tile
   static constexpr int kRows = kQTiles * kQRows;
   static constexpr int kQBytes = kQRows * kHeadDim * 2;
-  static constexpr int kStages = kMode == kWide ? 5 : kQ8 ? 4 : 6;  // 16-bit K and V tiles
+  static constexpr int kStages = kMode == kWide ? 5 : kMode == kSolo ? 2 : kQ8 ? 4 : 6;  // 16-bit K and V tiles
   static constexpr int kRaw = kQ8 ? 3 : 0;                           // tiles of codes
   static constexpr int kRingAt = kQTiles * kQBytes;
   static constexpr int kRawAt = kRingAt + kStages * kTileBytes;
   static constexpr int kTileArea = kRawAt + kRaw * kRawBytes;
+  static constexpr uint32_t kTmemCols = 256 * kGroups;
+  static constexpr int kOAt = 128 * kGroups;  // O's columns
   static constexpr int kSegs = kMode == kWide ? 32 : kQ8 ? 12 : 10;
 };
 
@@ -112,6 +116,7 @@ template <int kMode> constexpr int smem_bytes() {
 static_assert(smem_bytes<kWide>() <= 227 * 1024, "shared memory");
 static_assert(smem_bytes<kPair>() <= 227 * 1024, "shared memory");
 static_assert(smem_bytes<kPair8>() <= 227 * 1024, "shared memory");
+static_assert(2 * (smem_bytes<kSolo>() + 1024) <= 228 * 1024, "shared memory");
 
 // What the V of a tile needs before the product reads it.
 struct Mend {
@@ -287,12 +292,14 @@ __device__ __forceinline__ void q8_expand(uint4 w, uint32_t f, uint32_t (&x)[8],
 }
 
 template <class T, int kMode>
-__global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
+__global__ void __launch_bounds__(Shape<kMode>::kThreads, Shape<kMode>::kCtas)
     chunk_mma_kernel(const __grid_constant__ ChunkArgs a, const __grid_constant__ CUtensorMap tq,
                      const __grid_constant__ CUtensorMap tk,
                      const __grid_constant__ CUtensorMap tv) {
   using Sh = Shape<kMode>;
-  constexpr bool kTurns = Sh::kTurns, kQ8 = Sh::kQ8;
+  constexpr bool kHalves = Sh::kHalves, kTurns = Sh::kTurns, kQ8 = Sh::kQ8;
+  constexpr int kLoad = 4 * Sh::kGroups;  // the loader's warp; the others' follow
+  constexpr int kOAt = Sh::kOAt;
   constexpr int kStages = Sh::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t *q_area = smem;
@@ -303,7 +310,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
     if (tid == 0) flag_error(a.status, KV_ERR_INVALID_ARG);
     return;
   }
-  if (warp == 9) tmem_alloc(smem_u32(&ctl.tmem), kTmemCols);
+  if (warp == kLoad + 1) tmem_alloc(smem_u32(&ctl.tmem), Sh::kTmemCols);
   if (tid == 0) {
     if (!kQ8) {
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tk)) : "memory");
@@ -344,7 +351,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
   share_init(a, unit_rows, kTile, &ctl.share, ctl.red);
   const Waiter wait{&ctl.abort, a.wait_limit_ns};
   const auto &share = ctl.share;
-  const int group = warp >> 2;  // softmax group (warps 0-7)
+  const int group = Sh::kGroups == 1 ? 0 : warp >> 2;  // softmax group
 
   // state that lives across lists of segments
   Ring<kStages> ld;              // loader: next slot; menders: the next tile's K slot
@@ -366,35 +373,35 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
     return share.nseg != 0;
   };
 
-  // registers: 256 threads x 200 + 128 x 104 = 384 x 168, and 256 x 184 + 256 x
-  // 72 = 512 x 128, the launch's; the four warps of a warpgroup change theirs
-  // together
-  if (warp < 8) {
-    if constexpr (kQ8) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+  // registers: 256 threads x 200 + 128 x 104 = 384 x 168, 256 x 184 + 256 x 72 = 512
+  // x 128 and 128 x 184 + 128 x 72 = 256 x 128, the launch's; the four warps of a
+  // warpgroup change theirs together
+  if (warp < kLoad) {
+    if constexpr (kQ8 || kMode == kSolo) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
   } else {
-    if constexpr (kQ8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if constexpr (kQ8 || kMode == kSolo) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
   }
-  if (warp < 8) {
+  if (warp < kLoad) {
     // --------------------------------------------------------------- softmax
     while (next_list(true)) {
       const int x = group;
       const int row = (warp & 3) * 32 + lane;
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-      const uint32_t s_at = tmem + lanes + x * 128, o_at = tmem + lanes + 256 + x * 128;
+      const uint32_t s_at = tmem + lanes + x * 128, o_at = tmem + lanes + kOAt + x * 128;
       // (the Q loader has seen to the sign of the scale, and to 0)
       const float sc = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
       bool live = true;
       const int nseg = share.nseg;
       for (int sg = 0; sg < nseg && live; ++sg) {
         const ChunkSeg g = share.seg[sg];
-        const int r_lo = kTurns ? 0 : x * rt;  // the group's rows of the unit
+        const int r_lo = kHalves ? x * rt : 0;  // the group's rows of the unit
         const int urow = r_lo + row;
         const bool mine = row < rt && urow < g.nrows;
         // the first group's rows see no tile from half_hi on
-        const int end = !kTurns && x == 0 ? min(g.tile_hi, g.half_hi) : g.tile_hi;
-        const bool active = kTurns || (x == 0 ? r_lo < g.nrows : g.nrows > rt);
+        const int end = kHalves && x == 0 ? min(g.tile_hi, g.half_hi) : g.tile_hi;
+        const bool active = !kHalves || (x == 0 ? r_lo < g.nrows : g.nrows > rt);
         if (!active) {
           tiles_loaded += g.tile_hi - g.tile_lo;
           continue;
@@ -545,7 +552,8 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
           const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;  // (a part stays as it is)
           f0 *= inv;
           f1 *= inv;
-          const uint32_t o0 = tmem + lanes + 256 + (kTurns ? 0 : x * 128) + c0;
+          const uint32_t o0 = tmem + lanes + kOAt + (kTurns ? 0 : x * 128) + c0;
+          const bool nothing = __any_sync(0xFFFFFFFFu, f0 == 0.f);  // (of O, at f0 = 0)
           // rows of this lane's quad, for the transposed stores
           T *quad_out[4];
           bool quad_mine[4];
@@ -567,7 +575,11 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
             tmem_ld32(o0 + c, o);
             tc_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = f0 == 0.f ? 0.f : o[i] * f0;
+            for (int i = 0; i < 32; ++i) o[i] *= f0;
+            if (nothing && f0 == 0.f) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = 0.f;
+            }
             if (second) {
               float o1[32];
               tmem_ld32(o0 + 128 + c, o1);
@@ -633,7 +645,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
         }
       }
     }
-  } else if (warp == 8) {
+  } else if (warp == kLoad) {
     // ---------------------------------------------------------------- loader
     while (next_list(false)) {
       const int npg = kTile / a.ps;
@@ -709,7 +721,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
         }
       }
     }
-  } else if (warp == 9) {
+  } else if (warp == kLoad + 1) {
     // -------------------------------------------------------------- products
     // The whole warp walks the list, so that positions and descriptors are
     // uniform values; one lane issues.
@@ -732,7 +744,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
         u.hi = uniform(g.tile_hi);
         u.from = uniform(g.edge_from);
         u.upto = uniform(g.edge_upto);
-        u.two = !kTurns && uniform(g.nrows) > rt;
+        u.two = kHalves && uniform(g.nrows) > rt;
         u.hi0 = u.two ? min(u.hi, uniform(g.half_hi)) : u.hi;
       };
       Cur c, p;  // of the next scores, and of the weights that follow
@@ -740,7 +752,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
       enter(c);
       p = c;
       auto active = [&](int x, const Cur &u) {
-        return kTurns ? u.tile + x < u.hi : x == 0 ? u.tile < u.hi0 : u.two;
+        return kTurns ? u.tile + x < u.hi : x == 0 ? u.tile < u.hi0 : kHalves && u.two;
       };
       auto edge = [&](const Cur &u, int tile) { return tile >= u.from || tile <= u.upto; };
       auto advance = [&](Cur &u, Ring<kStages> &r) {
@@ -773,14 +785,14 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
           q_ph ^= 1u << qx;
         }
         const int tile = c.tile + (kTurns ? x : 0);
-        const bool leads = kTurns || x == 0 || !active(0, c);  // first to use this K
+        const bool leads = !kHalves || x == 0 || !active(0, c);  // first to use this K
         if (!kQ8 && leads && edge(c, tile) && elect_one()) mbar_arrive(at(ctl.mend[kTurns ? x : 0]));
         __syncwarp();
         if (leads && !ready(full0 + 8 * r.s, r.ph)) return false;
         tc_fence_after();
         const uint32_t a0 = dq + qx * (Sh::kQBytes >> 4), b0 = dk + r.s * (kTileBytes >> 4);
-        const bool last = tile + 1 == (x == 0 && !kTurns ? c.hi0 : c.hi);
-        const bool frees = kTurns || x == 1 || !c.two;
+        const bool last = tile + 1 == (x == 0 && kHalves ? c.hi0 : c.hi);
+        const bool frees = !kHalves || x == 1 || !c.two;
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
@@ -799,7 +811,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
         Ring<kStages> r = pv;
         r.next(1 + (kTurns ? 2 * x : 0));
         const int tile = p.tile + (kTurns ? x : 0);
-        if (kTurns || x == 0 || !active(0, p)) {  // first to use this V
+        if (!kHalves || x == 0 || !active(0, p)) {  // first to use this V
           constexpr int mx = kTurns ? x : 0;
           if (!ready(full0 + 8 * r.s, r.ph)) return false;
           if (!kQ8 && edge(p, tile)) {
@@ -809,8 +821,8 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
         }
         const uint32_t b0 = dv + r.s * (kTileBytes >> 4);
         const uint32_t add = p.tile > p.lo;
-        const bool last = tile + (kTurns ? 2 : 1) >= (x == 0 && !kTurns ? p.hi0 : p.hi);
-        const bool frees = kTurns || x == 1 || !p.two;
+        const bool last = tile + (kTurns ? 2 : 1) >= (x == 0 && kHalves ? p.hi0 : p.hi);
+        const bool frees = !kHalves || x == 1 || !p.two;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (!ready(h ? at(ctl.p_full[x]) : at(ctl.p_half[x]), (p_ph >> x) & 1)) return false;
@@ -818,7 +830,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
           if (elect_one()) {
 #pragma unroll
             for (int k = 4 * h; k < 4 * h + 4; ++k)
-              umma_ts(tmem + 256 + x * 128, tmem + x * 128 + k * 8, b0 + k * (2048 >> 4), hi,
+              umma_ts(tmem + kOAt + x * 128, tmem + x * 128 + k * 8, b0 + k * (2048 >> 4), hi,
                       id_pv, k > 0 ? 1u : add);
             if (h) {
               if (last) tc_commit(at(ctl.o_done[x]));
@@ -851,7 +863,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
         if (more) advance(c, qk);
       }
     }
-  } else if (warp >= 12) {
+  } else if (kQ8 && warp >= kLoad + 4) {
     // ------------------------------------------------------------- converter
     // A thread takes 16 codes of a token at a time, eight times per tile: eight
     // lanes read a row of codes, and write two 16-byte chunks each into the
@@ -934,9 +946,9 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
       const int ch = lane & 15, half = lane >> 4;  // 16 bytes of row 2 i + half
       for (int sg = 0; sg < nseg && live; ++sg) {
         const ChunkSeg g = share.seg[sg];
-        for (int x = 0; warp == 11 && x < Sh::kQTiles && x * rt < g.nrows; ++x) {
+        for (int x = 0; warp == kLoad + 3 && x < Sh::kQTiles && x * rt < g.nrows; ++x) {
           // (the first of two groups may have no tile in this segment)
-          if (!kTurns && x == 0 && g.nrows > rt && g.tile_lo >= g.half_hi) continue;
+          if (kHalves && x == 0 && g.nrows > rt && g.tile_lo >= g.half_hi) continue;
           if ((q_uses >> x) & 1) {
             if (!wait(smem_u32(&ctl.q_free[x]), (q_ph >> x) & 1)) {
               live = false;
@@ -1007,7 +1019,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
             break;
           }
           mend_ph ^= 1u << x;
-          uint8_t *v = ring + r.s * kTileBytes + (warp - 10) * kSlab;
+          uint8_t *v = ring + r.s * kTileBytes + (warp - kLoad - 2) * kSlab;
           for (int i = lane; i < (m.zero_hi - m.zero_lo) * 8; i += 32)
             reinterpret_cast<uint4 *>(v)[m.zero_lo * 8 + i] = make_uint4(0, 0, 0, 0);
           if (m.scans()) {
@@ -1029,30 +1041,30 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, 1)
     // leave no copy and no product in flight: every slot's last copy (slots
     // before ld.s were filled in this lap of the ring, the others in the one
     // before), and a last commit
-    if (warp == 8 && kQ8) {
+    if (warp == kLoad && kQ8) {
       for (int i = 0; i < Sh::kRaw; ++i)
         mbar_wait(smem_u32(&ctl.raw_full[i]), i < raw.s ? raw.ph : raw.ph ^ 1, a.wait_limit_ns);
     }
-    if (warp == 8 && !kQ8) {
+    if (warp == kLoad && !kQ8) {
       for (int i = 0; i < kStages; ++i)
         mbar_wait(smem_u32(&ctl.full[i]), i < ld.s ? ld.ph : ld.ph ^ 1, a.wait_limit_ns);
     }
-    if (warp == 11 && a.q_tma) {
+    if (warp == kLoad + 3 && a.q_tma) {
       // q_full's phase in flight: as many as there were uses
       for (int x = 0; x < Sh::kQTiles; ++x)
         if ((q_uses >> x) & 1)
           mbar_wait(smem_u32(&ctl.q_full[x]), (q_ph >> x) & 1, a.wait_limit_ns);
     }
-    if (warp == 9) {
+    if (warp == kLoad + 1) {
       if (elect_one()) tc_commit(smem_u32(&ctl.drain));
       mbar_wait(smem_u32(&ctl.drain), 0, a.wait_limit_ns);
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kLoad + 1) {
     tc_fence_after();
-    tmem_free(tmem, kTmemCols);
+    tmem_free(tmem, Sh::kTmemCols);
   }
 }
 
@@ -1067,20 +1079,23 @@ cudaError_t mma_go(const ChunkArgs &a, const CUtensorMap &tq, const CUtensorMap 
                     st, a, tq, tk, tv);
 }
 template <class T>
-cudaError_t mma_type(bool wide, bool q8, const ChunkArgs &a, const CUtensorMap &tq,
+cudaError_t mma_type(ChunkForm form, const ChunkArgs &a, const CUtensorMap &tq,
                      const CUtensorMap &tk, const CUtensorMap &tv, int ctas, cudaStream_t st) {
-  if (q8) return mma_go<T, kPair8>(a, tq, tk, tv, ctas, st);
-  return wide ? mma_go<T, kWide>(a, tq, tk, tv, ctas, st)
-              : mma_go<T, kPair>(a, tq, tk, tv, ctas, st);
+  switch (form) {
+    case kPair: return mma_go<T, kPair>(a, tq, tk, tv, ctas, st);
+    case kPair8: return mma_go<T, kPair8>(a, tq, tk, tv, ctas, st);
+    case kSolo: return mma_go<T, kSolo>(a, tq, tk, tv, ctas, st);
+    default: return mma_go<T, kWide>(a, tq, tk, tv, ctas, st);
+  }
 }
 
 }  // namespace
 
-cudaError_t launch_chunk_mma(int dtype, bool wide, bool q8, const ChunkArgs &a,
-                             const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
-                             int ctas, cudaStream_t st) {
-  return dtype == KV_F16 ? mma_type<__half>(wide, q8, a, tq, tk, tv, ctas, st)
-                         : mma_type<__nv_bfloat16>(wide, q8, a, tq, tk, tv, ctas, st);
+cudaError_t launch_chunk_mma(int dtype, ChunkForm form, const ChunkArgs &a, const CUtensorMap &tq,
+                             const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
+                             cudaStream_t st) {
+  return dtype == KV_F16 ? mma_type<__half>(form, a, tq, tk, tv, ctas, st)
+                         : mma_type<__nv_bfloat16>(form, a, tq, tk, tv, ctas, st);
 }
 
 }  // namespace kvs

@@ -81,11 +81,13 @@ cudaError_t launch_combine_lists(const float *part_o, const float *part_ml, cons
 // shares the work is cut into
 struct ChunkArgs;
 cudaError_t launch_chunk_core(const ChunkArgs &a, bool q8, int rows, int ctas, cudaStream_t st);
-// 16-bit q on the tensor cores: 16-bit K/V in units of two Q tiles (wide) or of
-// one, or the 8-bit cache (in device memory); the maps are of q and 16-bit K/V
-cudaError_t launch_chunk_mma(int dtype, bool wide, bool q8, const ChunkArgs &a,
-                             const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
-                             int ctas, cudaStream_t st);
+// 16-bit q on the tensor cores, in one of four forms (kv_chunk_mma.cu): over 16-bit
+// K/V in units of two Q tiles (kWide) or of one (kPair, kSolo), or over the 8-bit
+// cache in device memory (kPair8); the maps are of q and 16-bit K/V
+enum ChunkForm { kWide, kPair, kPair8, kSolo };
+cudaError_t launch_chunk_mma(int dtype, ChunkForm form, const ChunkArgs &a, const CUtensorMap &tq,
+                             const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
+                             cudaStream_t st);
 // few rows: 16-bit q over a 16-bit or the 8-bit cache, fp32 q over the 8-bit
 // cache; the maps are of K and V or the codes
 struct FewShape {

@@ -222,6 +222,23 @@ def test_longer_and_many(dtype, hq, hkv, lens, news, q8):
 
 
 @pytest.mark.parametrize("q8", [False, True], ids=["own", "q8"])
+@pytest.mark.parametrize("dtype,hq,hkv,ps,lens,news,window", [
+    ("bf16", 8, 2, 16, [2600, 1300, 1101], [150, 90, 40], 1100),
+    ("f16", 2, 2, 128, [1500, 1400], [300, 1], 1030),
+    ("f16", 4, 1, 64, [9000, 4300], [20, 25], 4200),
+    ("bf16", 6, 1, 32, [4500], [9], 4097)])
+def test_long_windows(dtype, hq, hkv, ps, lens, news, window, q8):
+    """Windows that end in long contexts, and vectors that are not finite before, at and
+    in them."""
+    p = Problem(dtype, hq, hkv, ps, lens, news, window, q8=q8)
+    if not q8:
+        first = lens[0] - news[0]  # the first row's token
+        for j, c in ((first - window, 5), (first - window + 3, 77), (first - 40, 20)):
+            p.v[p.table[0, j // ps], 0, j % ps, c] = math.nan
+    run(p)
+
+
+@pytest.mark.parametrize("q8", [False, True], ids=["own", "q8"])
 @pytest.mark.parametrize("hq,n", [(130, 1), (130, 3), (200, 2), (256, 1)])
 def test_more_heads_per_kv_head_than_a_tile_has_rows(hq, n, q8):
     run(Problem("bf16", hq, 1, 16, [150, 33], [n, 1], 0, q8=q8))

@@ -40,7 +40,9 @@ def draw(seed):
     p = Problem(dtype, hq, hkv, ps, lens, news, r.choice([0, 0, 0, 1, 17, 128, r.randint(1, 700)]),
                 q8=q8, seed=seed, scale=r.choice([None, None, None, 0.5, -0.1, 0.0]),
                 q_size=r.choice([1.0, 1.0, 4.0]), loc=r.choice(["hbm", "hbm", "host"]),
-                extra_rows=r.randint(0 if sum(news) else 1, 3))  # (a call has a row)
+                extra_rows=r.randint(0 if sum(news) else 1, 3),  # (a call has a row)
+                # (a wide block table takes the forms for long contexts)
+                extra_pages=random.Random(-1 - seed).choice([1, 1500 // ps, 6000 // ps]))
     pages = [(b, i) for b in range(len(lens)) for i in range(-(-lens[b] // ps))]
     bad = bool(pages) and r.random() < 0.25
     if bad:
