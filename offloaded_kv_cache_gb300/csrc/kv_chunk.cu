@@ -47,8 +47,7 @@ template <class T>
 __device__ __forceinline__ void join_store(const ChunkArgs &a, const int4 &u, int q0, int r,
                                            int lane, const Joined &x) {
   const float inv = x.l == 0.f ? 0.f : 1.f / x.l;
-  const int pr = u.z + r, row = q0 + pr / a.G, head = u.y * a.G + pr % a.G;
-  T *dst = static_cast<T *>(a.out) + ((long long)row * a.Hq + head) * kHeadDim + lane * 4;
+  T *dst = static_cast<T *>(a.out) + row_offset(a, q0, u.y, u.z + r) + lane * 4;
   if constexpr (std::is_same_v<T, float>)
     *reinterpret_cast<float4 *>(dst) =
         make_float4(x.o.x * inv, x.o.y * inv, x.o.z * inv, x.o.w * inv);
@@ -118,8 +117,7 @@ __global__ void __launch_bounds__(kThreads) chunk_core_kernel(const __grid_const
         const int r = i >> 4, c = (i & 15) * 8;
         float x[8] = {};
         if (r < g.nrows) {
-          const int pr = g.r0 + r, row = g.q0 + pr / a.G, head = g.kvh * a.G + pr % a.G;
-          load8(static_cast<const float *>(a.q) + ((long long)row * a.Hq + head) * kHeadDim + c, x);
+          load8(static_cast<const float *>(a.q) + row_offset(a, g.q0, g.kvh, g.r0 + r) + c, x);
         }
         store8(Qs + r * kQStr + c, x);
       }
@@ -127,7 +125,7 @@ __global__ void __launch_bounds__(kThreads) chunk_core_kernel(const __grid_const
       float m[MR], l[MR], o[MR][8];
 #pragma unroll
       for (int r = 0; r < MR; ++r) {
-        t[r] = g.len - g.n + (g.r0 + min(ty * MR + r, g.nrows - 1)) / a.G;
+        t[r] = g.len - g.n + token_of(a, g.r0 + min(ty * MR + r, g.nrows - 1));
         m[r] = -INFINITY;
         l[r] = 0.f;
 #pragma unroll
@@ -263,8 +261,7 @@ __global__ void __launch_bounds__(kThreads) chunk_core_kernel(const __grid_const
         if (rr >= g.nrows) continue;
         if (whole) {
           const float inv = sum == 0.f ? 0.f : 1.f / sum;
-          const int pr = g.r0 + rr, row = g.q0 + pr / a.G, head = g.kvh * a.G + pr % a.G;
-          float *dst = static_cast<float *>(a.out) + ((long long)row * a.Hq + head) * kHeadDim;
+          float *dst = static_cast<float *>(a.out) + row_offset(a, g.q0, g.kvh, g.r0 + rr);
 #pragma unroll
           for (int h = 0; h < 2; ++h)
             *reinterpret_cast<float4 *>(dst + 64 * h + tx * 4) =
@@ -330,17 +327,15 @@ __global__ void __launch_bounds__(kThreads, R == 4 ? 2 : 1)
       for (int r = 0; r < R; ++r) {
         o[r] = q[r] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (r < g.nrows) {
-          const int pr = g.r0 + r;
-          q[r] = *reinterpret_cast<const float4 *>(
-              static_cast<const float *>(a.q) +
-              ((long long)(g.q0 + pr / a.G) * a.Hq + g.kvh * a.G + pr % a.G) * kHeadDim + 4 * lane);
+          q[r] = *reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) +
+                                                   row_offset(a, g.q0, g.kvh, g.r0 + r) + 4 * lane);
         }
       }
       int t[L];
       float m[L], l[L];
 #pragma unroll
       for (int i = 0; i < L; ++i) {
-        t[i] = g.len - g.n + (g.r0 + min(row0 + i, g.nrows - 1)) / a.G;
+        t[i] = g.len - g.n + token_of(a, g.r0 + min(row0 + i, g.nrows - 1));
         m[i] = -INFINITY;
         l[i] = 0.f;
       }

@@ -40,6 +40,8 @@ struct ChunkArgs {
   long long nphys;
   int B, Hq, Hkv, G, ps, maxP, total_q, max_q_len, window;
   int slot_rows;
+  uint32_t g_mul;    // row / G = (high half of row * g_mul, + row) >> g_shift
+  int g_shift;
   int unit_cost;     // tiles that a unit counts beyond its own when the work is cut
   int row_tile;      // tensor cores: packed rows per Q tile
   int q_tma;         // tensor cores: Q tiles are whole tokens, copied by the TMA unit
@@ -47,6 +49,18 @@ struct ChunkArgs {
   unsigned long long wait_limit_ns;
   int debug_skip_tile;  // >= 0: the producer never fills that tile of a share (timeout test)
 };
+
+// The token of a packed row (>= 0).  A unit's start asks several times, in a chain
+// that nothing hides: a division by a variable is four times as long.
+__device__ __forceinline__ int token_of(const ChunkArgs &a, int row) {
+  return (int)((__umulhi((uint32_t)row, a.g_mul) + (uint32_t)row) >> a.g_shift);
+}
+
+// where packed row `row` of kv head kvh lies in q and out, rows of its sequence from q0
+__device__ __forceinline__ long long row_offset(const ChunkArgs &a, int q0, int kvh, int row) {
+  const int i = token_of(a, row);
+  return ((long long)(q0 + i) * a.Hq + kvh * a.G + row - i * a.G) * kHeadDim;
+}
 
 // One sequence of the call; n = 0 when it has no rows or is skipped.
 struct ChunkSeq {
@@ -67,8 +81,8 @@ struct TileRange {
 };
 __device__ __forceinline__ TileRange unit_tiles(const ChunkArgs &a, const ChunkSeq &s, int r0,
                                                 int nrows, int tile) {
-  const int t_first = s.len - s.n + r0 / a.G;
-  const int t_last = s.len - s.n + (r0 + nrows - 1) / a.G;
+  const int t_first = s.len - s.n + token_of(a, r0);
+  const int t_last = s.len - s.n + token_of(a, r0 + nrows - 1);
   if (t_last < 0) return TileRange{0, 1};
   // (t_first >= -1 here: a window may be as large as an int32)
   const int lo = a.window > 0 ? max(0, max(t_first, -1) - a.window + 1) : 0;
@@ -104,31 +118,54 @@ template <int kSegs> struct ChunkShare {
 __device__ __forceinline__ int packed_rows(const ChunkArgs &a, const ChunkSeq &s) {
   return s.n * a.G;  // checked on the host against int32 (max_q_len * G)
 }
-// What all row blocks of one kv head of sequence s count when the work is cut: their
-// tiles, and unit_cost for each.  (A unit counts its tiles first: a share that ends
-// among the rest ends behind the unit, whole.)
-__device__ __forceinline__ int head_tiles(const ChunkArgs &a, const ChunkSeq &s, int rows,
-                                          int tile) {
+// What the unit of packed rows from r0 on counts when the work is cut: its tiles,
+// and unit_cost.  (Its tiles come first: a share that ends among the rest ends
+// behind the unit, whole.)
+__device__ __forceinline__ int unit_counts(const ChunkArgs &a, const ChunkSeq &s, int r0, int R,
+                                           int rows, int tile) {
+  const TileRange t = unit_tiles(a, s, r0, min(rows, R - r0), tile);
+  return t.hi - t.lo + a.unit_cost;
+}
+// all row blocks of one kv head of sequence s from r0 on, every `step` rows
+__device__ __forceinline__ int head_counts(const ChunkArgs &a, const ChunkSeq &s, int r0, int step,
+                                           int rows, int tile) {
   const int R = packed_rows(a, s);
   int w = 0;
 #pragma unroll 1
-  for (int r0 = 0; r0 < R; r0 += rows) {
-    const TileRange t = unit_tiles(a, s, r0, min(rows, R - r0), tile);
-    w += t.hi - t.lo + a.unit_cost;
+  for (; r0 < R; r0 += step) w += unit_counts(a, s, r0, R, rows, tile);
+  return w;
+}
+__device__ __forceinline__ int scan_lanes(int w, int lane) {  // inclusive
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int x = __shfl_up_sync(0xFFFFFFFFu, w, off);
+    if (lane >= off) w += x;
   }
   return w;
 }
 
 // Every thread of the CTA: the total work, this CTA's share and where it
-// starts.  red: 32 ints of shared scratch.
+// starts.  red: 32 ints of shared scratch.  A warp takes a sequence's row blocks
+// 32 at a time where there are no more sequences than warps, else a thread does
+// (2 sequences of 16 row blocks: 176 -> 169 us of a call of 1000 new tokens over 16000).
 template <int kSegs>
 __device__ __forceinline__ void share_init(const ChunkArgs &a, int rows, int tile,
                                            ChunkShare<kSegs> *sh, int *red) {
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, nw = blockDim.x >> 5;
-  int mine = 0;
+  const bool by_warp = a.B <= nw;
+  int first = 0, mine = 0;  // counts of this thread's first sequence, of all of its
+  if (by_warp) {
+    if (warp < a.B)
+      mine = head_counts(a, chunk_seq(a, warp, blockIdx.x == 0 && lane == 0), lane * rows,
+                         32 * rows, rows, tile);
+  } else {
 #pragma unroll 1
-  for (int b = t; b < a.B; b += blockDim.x)
-    mine += head_tiles(a, chunk_seq(a, b, blockIdx.x == 0), rows, tile);
+    for (int b = t; b < a.B; b += blockDim.x) {
+      const int w = head_counts(a, chunk_seq(a, b, blockIdx.x == 0), 0, rows, rows, tile);
+      if (b == t) first = w;
+      mine += w;
+    }
+  }
   mine = __reduce_add_sync(0xFFFFFFFFu, mine);
   if (lane == 0) red[warp] = mine;
   __syncthreads();
@@ -147,7 +184,8 @@ __device__ __forceinline__ void share_init(const ChunkArgs &a, int rows, int til
   }
   __syncthreads();
   if (sh->left == 0) return;
-  // the sequence holding tile lo: one warp walks the sequences 32 at a time
+  // the sequence in which the share begins: one warp walks the sequences 32 at a
+  // time, and then its row blocks
   if (warp == 0) {
     int base = 0;
     const int want = sh->hi - sh->left;
@@ -156,33 +194,43 @@ __device__ __forceinline__ void share_init(const ChunkArgs &a, int rows, int til
       const int b = b0 + lane;
       ChunkSeq s{0, 0, 0};
       if (b < a.B) s = chunk_seq(a, b, false);
-      const int hw = head_tiles(a, s, rows, tile), w = hw * a.Hkv;
-      int inc = w;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int x = __shfl_up_sync(0xFFFFFFFFu, inc, off);
-        if (lane >= off) inc += x;
-      }
-      const int first = base + inc - w;
-      const bool here = want >= first && want < first + w;
+      const int hw = by_warp   ? (b < a.B ? red[lane] : 0)
+                     : b0 == 0 ? first
+                               : head_counts(a, s, 0, rows, rows, tile);
+      const int inc = scan_lanes(hw * a.Hkv, lane), from = base + inc - hw * a.Hkv;
+      const uint32_t here = __ballot_sync(0xFFFFFFFFu, want >= from && want < base + inc);
       if (here) {
-        int rem = want - first;
-        sh->b = b;
-        sh->kvh = rem / hw;
-        rem %= hw;
+        const int src = __ffs(here) - 1, head = __shfl_sync(0xFFFFFFFFu, hw, src);
+        const ChunkSeq q{__shfl_sync(0xFFFFFFFFu, s.q0, src), __shfl_sync(0xFFFFFFFFu, s.n, src),
+                         __shfl_sync(0xFFFFFFFFu, s.len, src)};
+        int rem = want - __shfl_sync(0xFFFFFFFFu, from, src);
+        const int kvh = rem / head, R = packed_rows(a, q);
+        rem -= kvh * head;
         int r0 = 0;
-        const int R = packed_rows(a, s);
 #pragma unroll 1
-        for (;; r0 += rows) {
-          const TileRange t2 = unit_tiles(a, s, r0, min(rows, R - r0), tile);
-          const int cost = t2.hi - t2.lo + a.unit_cost;
-          if (rem < cost || r0 + rows >= R) break;
-          rem -= cost;
+        while (true) {
+          const int mr = r0 + lane * rows;
+          const int c = mr < R ? unit_counts(a, q, mr, R, rows, tile) : 0;
+          const int ci = scan_lanes(c, lane);
+          const uint32_t past = __ballot_sync(0xFFFFFFFFu, ci > rem);
+          if (past) {
+            const int k = __ffs(past) - 1;
+            r0 += k * rows;
+            rem -= __shfl_sync(0xFFFFFFFFu, ci - c, k);
+            break;
+          }
+          if (r0 + 32 * rows >= R) break;  // (not reached: the counts add up to head)
+          rem -= __shfl_sync(0xFFFFFFFFu, ci, 31);
+          r0 += 32 * rows;
         }
-        sh->r0 = r0;
-        sh->off = rem;
+        if (lane == 0) {
+          sh->b = b0 + src;
+          sh->kvh = kvh;
+          sh->r0 = r0;
+          sh->off = rem;
+        }
+        break;
       }
-      if (__any_sync(0xFFFFFFFFu, here)) break;
       base += __shfl_sync(0xFFFFFFFFu, inc, 31);
     }
   }
@@ -222,13 +270,13 @@ __device__ __forceinline__ void share_next(const ChunkArgs &a, int rows, int til
       g.tile_lo = t.lo + off;
       g.tile_hi = t.lo + tile_hi;
       g.parts = (off == 0 ? 1 : 0) | (tile_hi == tiles ? 2 : 0);
-      g.t_first = s.len - s.n + r0 / a.G;
-      g.t_last = s.len - s.n + (r0 + nrows - 1) / a.G;
+      g.t_first = s.len - s.n + token_of(a, r0);
+      g.t_last = s.len - s.n + token_of(a, r0 + nrows - 1);
       g.edge_from = g.t_first < s.len - 1        ? max(g.t_first + 1, 0) / tile
                     : (s.len & (a.ps - 1)) != 0 ? s.len / tile
                                                 : INT_MAX;
       g.edge_upto = a.window > 0 && g.t_last >= a.window ? (g.t_last - a.window) / tile : -1;
-      const int t_half = s.len - s.n + (r0 + min(nrows, rows / 2) - 1) / a.G;
+      const int t_half = s.len - s.n + token_of(a, r0 + min(nrows, rows / 2) - 1);
       g.half_hi = max(t_half, 0) / tile + 1;
       if (g.parts == 1) {
         // the CTA whose share holds the unit's last tile

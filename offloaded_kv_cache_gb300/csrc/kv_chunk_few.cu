@@ -241,9 +241,7 @@ __global__ void __launch_bounds__(Shape<T, Q8>::kThreads, Shape<T, Q8>::kCtas)
 #pragma unroll
         for (int i = 0; i < 32; ++i) x[i] = 0.f;
         if (g8 < g.nrows) {
-          const int pr = g.r0 + g8;
-          const T *src = static_cast<const T *>(a.q) +
-                         ((long long)(g.q0 + pr / a.G) * a.Hq + g.kvh * a.G + pr % a.G) * kHeadDim;
+          const T *src = static_cast<const T *>(a.q) + row_offset(a, g.q0, g.kvh, g.r0 + g8);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             float y[8];
@@ -276,7 +274,7 @@ __global__ void __launch_bounds__(Shape<T, Q8>::kThreads, Shape<T, Q8>::kCtas)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           qf[h] = __shfl_sync(0xFFFFFFFFu, f, 4 * (2 * t4 + h));
-          tq[h] = g.len - g.n + (g.r0 + min(2 * t4 + h, g.nrows - 1)) / a.G;
+          tq[h] = g.len - g.n + token_of(a, g.r0 + min(2 * t4 + h, g.nrows - 1));
         }
         float m[2], r[2], l[2], o[8][4];
 #pragma unroll
@@ -543,10 +541,7 @@ __global__ void __launch_bounds__(Shape<T, Q8>::kThreads, Shape<T, Q8>::kCtas)
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
             for (int k = 0; k < 8; ++k) x[k] *= inv;
-            store8(static_cast<T *>(a.out) +
-                       ((long long)(g.q0 + pr / a.G) * a.Hq + g.kvh * a.G + pr % a.G) * kHeadDim +
-                       c,
-                   x);
+            store8(static_cast<T *>(a.out) + row_offset(a, g.q0, g.kvh, pr) + c, x);
           } else {
             const long long at = (long long)part_slot(g) * a.slot_rows + n;
             store8(a.part_o + at * kHeadDim + c, x);

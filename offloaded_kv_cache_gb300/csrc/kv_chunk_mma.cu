@@ -29,7 +29,7 @@
 //     from box to box, 1.44-1.58 PFLOP/s.  Products and softmax share the time: the
 //     tensor pipe is active for two thirds of it, and what is left is each
 //     group's chain of scores, maximum, exponentials and weights.
-//   * kSolo, 32 prompts of up to 512, 32/32 heads, f16: 81 us for 41 us of bytes
+//   * kSolo, 32 prompts of up to 512, 32/32 heads, f16: 79 us for 41 us of bytes
 //     (kWide 95).  A unit has one to four tiles, each a chain of some 2900 cycles
 //     (product, maximum, exponentials, product), and 3500 more to write out, which
 //     two CTAs per SM cover for one another in part.
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, Shape<kMode>::kCtas)
           continue;
         }
         const bool any_row = (warp & 3) * 32 < min(rt, g.nrows - r_lo);
-        const int t = g.len - g.n + (g.r0 + min(urow, g.nrows - 1)) / a.G;
+        const int t = g.len - g.n + token_of(a, g.r0 + min(urow, g.nrows - 1));
         float m = -INFINITY, l = 0.f;
         bool begun = false;
         for (int tile = g.tile_lo + (kTurns ? x : 0); tile < end; tile += kTurns ? 2 : 1) {
@@ -517,8 +517,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, Shape<kMode>::kCtas)
         float M = m == -INFINITY ? -INFINITY : m * sc - weight_bias<T>();
         const bool whole = g.whole();
         const int pr = g.r0 + min(urow, g.nrows - 1);
-        T *out = static_cast<T *>(a.out) +
-                 ((long long)(g.q0 + pr / a.G) * a.Hq + g.kvh * a.G + pr % a.G) * kHeadDim;
+        T *out = static_cast<T *>(a.out) + row_offset(a, g.q0, g.kvh, pr);
         float *part = nullptr;
         long long prow = 0;
         if (!whole) {
@@ -963,7 +962,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, Shape<kMode>::kCtas)
             if (lane == 0) {
               const uint32_t bar = smem_u32(&ctl.q_full[x]);
               const uint32_t dst = smem_u32(q_area) + x * Sh::kQBytes;
-              const int tok = g.q0 + (g.r0 + x * rt) / a.G;
+              const int tok = g.q0 + token_of(a, g.r0 + x * rt);
               mbar_arrive_expect_tx(bar, 2 * rt * 128);
               tma_load_3d(dst, &tq, 0, g.kvh * a.G, tok, bar);
               tma_load_3d(dst + Sh::kQRows * 128, &tq, 64, g.kvh * a.G, tok, bar);
@@ -973,10 +972,8 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, Shape<kMode>::kCtas)
           }
           const uint32_t q = smem_u32(q_area) + x * Sh::kQBytes + (ch >> 3) * Sh::kQRows * 128;
           const int pr = g.r0 + x * rt + half, left = min(rt, g.nrows - x * rt);
-          int hd = pr % a.G;
-          const T *src = static_cast<const T *>(a.q) +
-                         ((long long)(g.q0 + pr / a.G) * a.Hq + g.kvh * a.G + hd) * kHeadDim +
-                         ch * 8;
+          int hd = pr - token_of(a, pr) * a.G;
+          const T *src = static_cast<const T *>(a.q) + row_offset(a, g.q0, g.kvh, pr) + ch * 8;
           const long long wrap = (long long)(a.Hq - a.G) * kHeadDim;  // to the next token's heads
           for (int r = half; r < Sh::kQRows; r += 2) {
             const uint32_t dst = q + swz(r, ch & 7);
