@@ -22,6 +22,7 @@
 #include <climits>
 
 #include "kv_internal.cuh"
+#include "kv_q8.cuh"
 
 namespace kvs {
 
@@ -40,8 +41,7 @@ struct ChunkArgs {
   long long nphys;
   int B, Hq, Hkv, G, ps, maxP, total_q, max_q_len, window;
   int slot_rows;
-  uint32_t g_mul;    // row / G = (high half of row * g_mul, + row) >> g_shift
-  int g_shift;
+  Divisor by_g;      // packed row / G
   int unit_cost;     // tiles that a unit counts beyond its own when the work is cut
   int row_tile;      // tensor cores: packed rows per Q tile
   int q_tma;         // tensor cores: Q tiles are whole tokens, copied by the TMA unit
@@ -50,11 +50,8 @@ struct ChunkArgs {
   int debug_skip_tile;  // >= 0: the producer never fills that tile of a share (timeout test)
 };
 
-// The token of a packed row (>= 0).  A unit's start asks several times, in a chain
-// that nothing hides: a division by a variable is four times as long.
-__device__ __forceinline__ int token_of(const ChunkArgs &a, int row) {
-  return (int)((__umulhi((uint32_t)row, a.g_mul) + (uint32_t)row) >> a.g_shift);
-}
+// the token of a packed row (>= 0)
+__device__ __forceinline__ int token_of(const ChunkArgs &a, int row) { return a.by_g(row); }
 
 // where packed row `row` of kv head kvh lies in q and out, rows of its sequence from q0
 __device__ __forceinline__ long long row_offset(const ChunkArgs &a, int q0, int kvh, int row) {

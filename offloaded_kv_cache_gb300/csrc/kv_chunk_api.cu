@@ -299,12 +299,7 @@ int chunk_common(const kv_shape *s, const kv_chunk *c, const void *q, const void
   a.window = c->window >= (long long)a.maxP * a.ps ? 0 : c->window;
   a.slot_rows = pl.slot_rows;
   a.unit_cost = pl.unit_cost;
-  // With 2^s >= G > 2^(s-1) and m = floor(2^32 (2^s - G) / G) + 1, 2^32 + m is 2^(32+s) / G
-  // + e, 0 < e <= 1: n (2^32 + m) / 2^(32+s) exceeds n / G by less than 2^-(s+1) < 1 / G for
-  // every n < 2^31, and its floor is that of n / G.
-  a.g_shift = 0;
-  while ((1ll << a.g_shift) < a.G) ++a.g_shift;
-  a.g_mul = (uint32_t)((((1ull << a.g_shift) - a.G) << 32) / a.G + 1);
+  a.by_g = Divisor::of(a.G);
   a.scale_log2 = scale * 1.4426950408889634f;
   a.wait_limit_ns = wait_limit_ns();
   a.debug_skip_tile = debug_skip_page() < 0 ? -1 : debug_skip_page() / (pl.tile / kTileTokens);

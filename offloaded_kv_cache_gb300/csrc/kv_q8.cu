@@ -7,12 +7,13 @@
 // the link.  e4m3 codes with one scale byte per vector are 129 bytes where
 // 16-bit data takes 256.
 //
-// Both kernels move each byte once and compute a few operations per element,
-// so memory bounds them; a decode step's append is bounded by latency.  Measured on
-// one GB300, where a copy reaches 6.68 TB/s: append of 32 chunks of 513 tokens, 32 kv
-// heads, f16: 35 us, 5.0 TB/s; of 4 x 2048 tokens, 8 kv heads: 7.6 us; of one token
-// for 32 sequences: 2.3 us; read back of 4 x 32768 tokens, 8 kv heads, bf16: 108 us,
-// 6.15 TB/s; of 2 x 544, 32 kv heads: 5.7 us.
+// Both kernels move each byte once and compute a few operations per element, few
+// enough to let memory bound them; a decode step's append is bounded by latency.
+// Measured on one GB300, where a copy reaches 6.68 TB/s: append of 32 chunks of up
+// to 513 tokens, 32 kv heads, f16: 30.3 us, 5.7 TB/s (in fp32, with divisions and each
+// vector's maximum on its own: 35.0); of 4 x 2048 tokens, 8 kv heads: 6.4 us; of one
+// token for 32 sequences: 2.1 us; read back of 4 x 32768 tokens, 8 kv heads, bf16: 106
+// us, 6.3 TB/s; of 2 x 544, 32 kv heads: 5.5 us.
 #include <algorithm>
 
 #include "kv_chunk.cuh"
@@ -24,7 +25,7 @@ namespace {
 
 constexpr int kThreads = 256;
 #ifndef KVS_APPEND_BLOCKS
-#define KVS_APPEND_BLOCKS 2432  // 16 per SM; 8: 37.3 us, 32: 36.2 us where this takes 35.0
+#define KVS_APPEND_BLOCKS 2432  // 16 per SM; 8: 32.1 us, 32: 31.1 us where this takes 30.3
 #endif
 constexpr int kLanesPerVec = 16;  // 8 elements a lane: 16 bytes of 16-bit data, 8 bytes of codes
 
@@ -37,6 +38,7 @@ struct AppendArgs {
   long long nphys;
   int B, Hkv, ps, ps_log2, maxP, total_q, max_q_len;
   int blocks;      // blocks per sequence
+  Divisor by_blocks, by_heads;
   int write_lens;  // this launch writes ctx_out
 };
 
@@ -82,7 +84,7 @@ template <class T> struct AppendStep {
 template <class T>
 __global__ void __launch_bounds__(kThreads) q8_append_kernel(const AppendArgs a) {
   pdl_wait();
-  const int b = blockIdx.x / a.blocks, j = blockIdx.x % a.blocks;
+  const int b = a.by_blocks(blockIdx.x), j = (int)blockIdx.x - b * a.blocks;
   const RowSpan r = append_span(a, b);
   const int sub = threadIdx.x / kLanesPerVec, l = threadIdx.x % kLanesPerVec;
   const int items = r.n > 0 ? r.n * a.Hkv : 0;  // <= total_q * Hq, an int32
@@ -100,7 +102,7 @@ __global__ void __launch_bounds__(kThreads) q8_append_kernel(const AppendArgs a)
 #pragma unroll
         for (int c = 0; c < (int)sizeof(T) / 2; ++c)
           s.w[u][w][c] = reinterpret_cast<const uint4 *>(src[w] + it * kHeadDim)[c];
-      s.pos[u] = r.len + (int)it / a.Hkv;
+      s.pos[u] = r.len + a.by_heads((int)it);
       s.page[u] = a.bt[(long long)b * a.maxP + (s.pos[u] >> a.ps_log2)];
     }
   };
@@ -126,23 +128,29 @@ __global__ void __launch_bounds__(kThreads) q8_append_kernel(const AppendArgs a)
       const int h = it - (now.pos[u] - r.len) * a.Hkv;
       // (rows of the cache fit int32)
       const long long vec = (now.page[u] * a.Hkv + h) * a.ps + (now.pos[u] & (a.ps - 1));
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        float x[8];
-        load8(reinterpret_cast<const T *>(&now.w[u][w]), x);
-        uint32_t top = 0;  // magnitudes order as their bits do, infinities and NaN above all
-#pragma unroll
-        for (int c = 0; c < 8; ++c) top = max(top, __float_as_uint(x[c]) & 0x7FFFFFFFu);
+      uint32_t tops[2] = {q8_top(now.w[u][0]), q8_top(now.w[u][1])};
+      if constexpr (sizeof(T) == 2) {  // K's and V's go through the lanes together
+        uint32_t both = tops[0] | (tops[1] << 16);
 #pragma unroll
         for (int off = 8; off > 0; off >>= 1)
-          top = max(top, __shfl_xor_sync(half_mask, top, off, kLanesPerVec));
+          both = __vmaxu2(both, __shfl_xor_sync(half_mask, both, off, kLanesPerVec));
+        tops[0] = both & 0xFFFFu;
+        tops[1] = both >> 16;
+      } else {
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1)
+#pragma unroll
+          for (int w = 0; w < 2; ++w)
+            tops[w] = max(tops[w], __shfl_xor_sync(half_mask, tops[w], off, kLanesPerVec));
+      }
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const uint32_t top = q8_top_f32(tops[w], T{});
         uint2 code = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
         int byte = kQ8NanScale;
         if (top < 0x7F800000u) {
           const int e = q8_exponent(top, q8_min_exp<T>());
-          const float s = pow2f(-e);
-          code.x = q8_codes4(x[0] * s, x[1] * s, x[2] * s, x[3] * s);
-          code.y = q8_codes4(x[4] * s, x[5] * s, x[6] * s, x[7] * s);
+          code = q8_codes8(now.w[u][w], e, T{});
           byte = e + 127;
         }
         *reinterpret_cast<uint2 *>((w ? a.v_codes : a.k_codes) + vec * kHeadDim + l * 8) = code;
@@ -172,6 +180,7 @@ struct ReadArgs {
   int Hkv, ps, ps_log2, maxP;
   int items;   // of a sequence: (16-token tile, kv head) pairs
   int blocks;  // per sequence
+  Divisor by_blocks, by_heads;
 };
 
 // Work item: (b, 16-token tile, kv head), 16 x 128 codes of K and of V.  A
@@ -183,7 +192,7 @@ template <class T>
 __global__ void __launch_bounds__(kThreads) q8_read_kernel(const ReadArgs a) {
   pdl_wait();
   const int t = threadIdx.x / kLanesPerVec, l = threadIdx.x % kLanesPerVec;
-  const int b = blockIdx.x / a.blocks, j = blockIdx.x % a.blocks;
+  const int b = a.by_blocks(blockIdx.x), j = (int)blockIdx.x - b * a.blocks;
   const int len = a.ctx[b];
   uint2 code[kUnits][2];
   uint32_t byte[kUnits][2];
@@ -193,7 +202,7 @@ __global__ void __launch_bounds__(kThreads) q8_read_kernel(const ReadArgs a) {
     const int it = j * kUnits + u;
     dst[u] = -1;
     if (it >= a.items) continue;
-    const int tile = it / a.Hkv, h = it - tile * a.Hkv;
+    const int tile = a.by_heads(it), h = it - tile * a.Hkv;
     const int pos = tile * kTileTokens + t, page = (tile * kTileTokens) >> a.ps_log2;
     if (len < 0 || (long long)len > (long long)a.maxP * a.ps) {
       if (threadIdx.x == 0 && tile == 0) flag_error(a.status, KV_ERR_BOUNDS);
@@ -247,12 +256,13 @@ struct StageArgs {
   int *status;
   long long nphys;
   int Hkv, ps, ps_log2, maxP, items, blocks, total_q, max_q_len, window;
+  Divisor by_blocks, by_heads;
 };
 template <class T, bool Q8>
 __global__ void __launch_bounds__(kThreads) stage_kernel(const StageArgs a) {
   pdl_wait();
   const int t = threadIdx.x / kLanesPerVec, l = threadIdx.x % kLanesPerVec;
-  const int b = blockIdx.x / a.blocks, j = blockIdx.x % a.blocks;
+  const int b = a.by_blocks(blockIdx.x), j = (int)blockIdx.x - b * a.blocks;
   const int q0 = a.q_start[b], q1 = a.q_start[b + 1], len = a.ctx[b];
   uint4 data[kUnits][2];  // 16-bit data, or the codes in the first half
   uint32_t byte[kUnits][2];
@@ -262,7 +272,7 @@ __global__ void __launch_bounds__(kThreads) stage_kernel(const StageArgs a) {
     const int it = j * kUnits + u;
     dst[u] = -1;
     if (it >= a.items) continue;
-    const int tile = it / a.Hkv, h = it - tile * a.Hkv;
+    const int tile = a.by_heads(it), h = it - tile * a.Hkv;
     const int tok0 = tile * kTileTokens, pos = tok0 + t, page = tok0 >> a.ps_log2;
     // sequences the attention skips (and records), and tokens no row sees
     if (q0 < 0 || q1 <= q0 || q1 > a.total_q || q1 - q0 > a.max_q_len || len < 0 ||
@@ -352,7 +362,10 @@ cudaError_t launch_chunk_stage(int dtype, bool q8, const ChunkArgs &c, void *k_o
   a.total_q = c.total_q;
   a.max_q_len = c.max_q_len;
   a.window = c.window;
-  if (!item_grid(c.B, c.maxP, c.ps, c.Hkv, &a.items, &a.blocks)) return cudaErrorInvalidConfiguration;
+  if (!item_grid(c.B, c.maxP, c.ps, c.Hkv, &a.items, &a.blocks))
+    return cudaErrorInvalidConfiguration;
+  a.by_blocks = Divisor::of(a.blocks);
+  a.by_heads = Divisor::of(c.Hkv);
   const dim3 grid((unsigned)(a.blocks * c.B)), block(kThreads);
   if (dtype == KV_F16)
     return q8 ? launch_pdl(stage_kernel<__half, true>, grid, block, 0, st, a)
@@ -390,6 +403,8 @@ cudaError_t launch_q8_append(int dtype, const void *k_new, const void *v_new,
   // as many blocks as there are steps, up to what keeps every SM busy
   const long long steps = (items + kVecs * kSteps - 1) / (kVecs * kSteps);
   a.blocks = (int)std::max(1LL, std::min(steps, (KVS_APPEND_BLOCKS + B - 1LL) / B));
+  a.by_blocks = Divisor::of(a.blocks);
+  a.by_heads = Divisor::of(Hkv);
   const long long blocks = a.blocks;
   const bool later = ctx_out == ctx && blocks > 1;
   a.write_lens = ctx_out && !later;
@@ -424,6 +439,8 @@ cudaError_t launch_q8_read(int dtype, const kv_q8_cache &c, const int32_t *bt, c
   a.ps_log2 = __builtin_ctz(ps);
   a.maxP = maxP;
   if (!item_grid(B, maxP, ps, Hkv, &a.items, &a.blocks)) return cudaErrorInvalidConfiguration;
+  a.by_blocks = Divisor::of(a.blocks);
+  a.by_heads = Divisor::of(Hkv);
   const dim3 grid((unsigned)(a.blocks * B)), block(kThreads);
   return dtype == KV_F32   ? launch_pdl(q8_read_kernel<float>, grid, block, 0, st, a)
          : dtype == KV_F16 ? launch_pdl(q8_read_kernel<__half>, grid, block, 0, st, a)
