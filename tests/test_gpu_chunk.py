@@ -222,6 +222,18 @@ def test_longer_and_many(dtype, hq, hkv, lens, news, q8):
 
 
 @pytest.mark.parametrize("q8", [False, True], ids=["own", "q8"])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("batch,most,n", [(33, 300, 1), (33, 300, 90), (70, 200, 5), (600, 60, 3),
+                                          (1100, 17, 1)])
+def test_many_sequences(dtype, batch, most, n, q8):
+    """More sequences than a CTA has warps, lanes of a warp, threads; some empty."""
+    g = torch.Generator().manual_seed(batch)
+    lens = torch.randint(0, most, (batch,), generator=g).tolist()
+    news = [min(x, int(torch.randint(0, n + 1, (1,), generator=g))) for x in lens]
+    run(Problem(dtype, 4, 2, 16, lens, news, q8=q8, seed=n))
+
+
+@pytest.mark.parametrize("q8", [False, True], ids=["own", "q8"])
 @pytest.mark.parametrize("dtype,hq,hkv,ps,lens,news,window", [
     ("bf16", 8, 2, 16, [2600, 1300, 1101], [150, 90, 40], 1100),
     ("f16", 2, 2, 128, [1500, 1400], [300, 1], 1030),
