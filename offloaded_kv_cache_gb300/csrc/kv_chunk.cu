@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kThreads) chunk_core_kernel(const __grid_const
 // (l & 3) R / 4 .. of token l / 4; the weights come back through shared memory.
 // The K/V stream bounds it at one row per kv head; at 8, multiply-adds and
 // shuffles about as much.  One token over 4 x 8192 tokens, 32/8 heads: 44 us on one
-// GB300, 6.1 TB/s; 33 rows over 4096 tokens, one head: 15 us, the chain of a
+// GB300, 6.1 TB/s; 33 rows over 4096 tokens, one head: 13.6 us, the chain of a
 // CTA's few tiles and the combine.
 constexpr int kFewWarps = kThreads / 32;
 constexpr float kMoveAt = 8.f;  // the maximum moves when a weight would exceed 2^8
@@ -482,29 +482,41 @@ __global__ void __launch_bounds__(kThreads, R == 4 ? 2 : 1)
 // are in flight together (one row at a time took three times as long).  Few
 // parts: each warp joins all parts of its rows (of one, when there are no more
 // rows than that).  Many (a long context and few rows): the block's warps share
-// the parts of four rows.
+// the parts of four rows, or of one, when there are blocks enough (8 rows of one kv
+// head over 30000 tokens, 304 parts: the call 25 -> 15.5 us).
 constexpr int kJoinRows = 4;
-// rows r0 .. r0 + 3 of the parts first_part, first_part + step, .. up to CTA `last`
-template <int R>
+// rows r0 .. r0 + R - 1 of the parts of the CTAs from, from + step, .. up to `last`, U of
+// them in flight
+template <int R, int U>
 __device__ __forceinline__ void join_rows(const ChunkArgs &a, int first, int last, int from,
                                           int step, int r0, int nrows, int lane,
                                           Joined (&acc)[R]) {
 #pragma unroll
   for (int i = 0; i < R; ++i)
     acc[i] = Joined{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-#pragma unroll (8 / R)
-  for (int j = from; j <= last; j += step) {
-    const long long row0 = (long long)(j == first ? 2 * j + 1 : 2 * j) * a.slot_rows + r0;
-    float2 ml[R];
-    float4 o[R];
+#pragma unroll 1
+  for (int j0 = from; j0 <= last; j0 += step * U) {
+    float2 ml[U][R];
+    float4 o[U][R];
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const long long row = row0 + min(i, nrows - 1 - r0);
-      ml[i] = *reinterpret_cast<const float2 *>(a.part_ml + 2 * row);
-      o[i] = *reinterpret_cast<const float4 *>(a.part_o + row * kHeadDim + lane * 4);
+    for (int k = 0; k < U; ++k) {
+      const int j = j0 + k * step;
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        ml[k][i] = make_float2(-INFINITY, 0.f);
+        o[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j <= last) {
+          const long long row = (long long)(j == first ? 2 * j + 1 : 2 * j) * a.slot_rows + r0 +
+                                min(i, nrows - 1 - r0);
+          ml[k][i] = *reinterpret_cast<const float2 *>(a.part_ml + 2 * row);
+          o[k][i] = *reinterpret_cast<const float4 *>(a.part_o + row * kHeadDim + lane * 4);
+        }
+      }
     }
 #pragma unroll
-    for (int i = 0; i < R; ++i) join_one(acc[i], ml[i].x, ml[i].y, o[i]);
+    for (int k = 0; k < U; ++k)
+#pragma unroll
+      for (int i = 0; i < R; ++i) join_one(acc[i], ml[k][i].x, ml[k][i].y, o[k][i]);
   }
 }
 template <class T>
@@ -519,7 +531,7 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constan
     const int r = blockIdx.y * 8 + warp;
     if (r >= nrows) return;
     Joined one[1];
-    join_rows(a, first, last, first, 1, r, nrows, lane, one);
+    join_rows<1, 8>(a, first, last, first, 1, r, nrows, lane, one);
     join_store<T>(a, u, w.x, r, lane, one[0]);
     return;
   }
@@ -527,19 +539,26 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constan
   if (last - first < 8) {
     for (int r0 = (blockIdx.y * 8 + warp) * kJoinRows; r0 < nrows;
          r0 += gridDim.y * 8 * kJoinRows) {
-      join_rows(a, first, last, first, 1, r0, nrows, lane, acc);
+      join_rows<kJoinRows, 2>(a, first, last, first, 1, r0, nrows, lane, acc);
 #pragma unroll
       for (int i = 0; i < kJoinRows; ++i)
         if (r0 + i < nrows) join_store<T>(a, u, w.x, r0 + i, lane, acc[i]);
     }
     return;
   }
-  for (int r0 = blockIdx.y * kJoinRows; r0 < nrows; r0 += gridDim.y * kJoinRows) {
-    join_rows(a, first, last, first + warp, 8, r0, nrows, lane, acc);
+  const int per = nrows <= (int)gridDim.y ? 1 : kJoinRows;  // rows a block takes at a time
+  for (int r0 = blockIdx.y * per; r0 < nrows; r0 += gridDim.y * per) {
+    if (per == 1) {
+      Joined one[1];
+      join_rows<1, 8>(a, first, last, first + warp, 8, r0, nrows, lane, one);
+      part[warp][0][lane] = one[0];
+    } else {
+      join_rows<kJoinRows, 2>(a, first, last, first + warp, 8, r0, nrows, lane, acc);
 #pragma unroll
-    for (int i = 0; i < kJoinRows; ++i) part[warp][i][lane] = acc[i];
+      for (int i = 0; i < kJoinRows; ++i) part[warp][i][lane] = acc[i];
+    }
     __syncthreads();
-    if (warp < kJoinRows && r0 + warp < nrows) {
+    if (warp < per && r0 + warp < nrows) {
       Joined x = part[0][warp][lane];
 #pragma unroll
       for (int i = 1; i < 8; ++i) {
@@ -573,8 +592,10 @@ cudaError_t launch_chunk_core(const ChunkArgs &a, bool q8, int rows, int ctas, c
             : core_go(chunk_core_kernel<false>, kTileSmem, a, ctas, st);
 }
 
-cudaError_t launch_chunk_combine(int dtype, const ChunkArgs &a, int ctas, cudaStream_t st) {
-  const dim3 grid(ctas, std::min(8, (a.slot_rows + kJoinRows - 1) / kJoinRows)), block(256);
+cudaError_t launch_chunk_combine(int dtype, const ChunkArgs &a, int ctas, bool many,
+                                 cudaStream_t st) {
+  const int per = many ? 1 : kJoinRows;
+  const dim3 grid(ctas, std::min(8, (a.slot_rows + per - 1) / per)), block(256);
   return dtype == KV_F32   ? launch_pdl(chunk_combine_kernel<float>, grid, block, 0, st, a)
          : dtype == KV_F16 ? launch_pdl(chunk_combine_kernel<__half>, grid, block, 0, st, a)
                            : launch_pdl(chunk_combine_kernel<__nv_bfloat16>, grid, block, 0, st, a);

@@ -107,6 +107,7 @@ struct ChunkPlan {
   int unit_cost = 1;
   double most_tiles = 0;  // an upper bound of the call's (unit, KV tile) pairs
   int ctas = 1;
+  bool many_parts = false;  // units are shared by 16 CTAs and more
   int slot_rows = 1;  // rows of a partial result
   size_t off_meta = 0, off_ml = 0, off_o = 0, off_table = 0, off_k = 0, off_v = 0;
   size_t total = 0;
@@ -163,6 +164,7 @@ ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, bool q8) {
   const long long tiles = ((long long)s->max_pages_per_seq * s->page_size + pl.tile - 1) / pl.tile;
   pl.most_tiles = units * s->num_kv_heads * (tiles + pl.unit_cost);
   pl.ctas = (int)std::min<double>((double)per_sm * sms, std::max(1.0, pl.most_tiles));
+  pl.many_parts = pl.ctas >= 16 * units * s->num_kv_heads;
   pl.slot_rows = (int)std::min<long long>(pl.rows, packed);
   size_t off = align256((size_t)pl.ctas * 32);
   pl.off_ml = off;
@@ -332,7 +334,7 @@ int chunk_common(const kv_shape *s, const kv_chunk *c, const void *q, const void
   } else {
     e = launch_chunk_core(a, is_q8, pl.rows, pl.ctas, st);
   }
-  if (e == cudaSuccess) e = launch_chunk_combine(s->dtype, a, pl.ctas, st);
+  if (e == cudaSuccess) e = launch_chunk_combine(s->dtype, a, pl.ctas, pl.many_parts, st);
   return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
 }
 

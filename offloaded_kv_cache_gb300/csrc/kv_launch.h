@@ -101,7 +101,8 @@ cudaError_t launch_chunk_few(int dtype, bool q8, const ChunkArgs &a, const CUten
 // the pages it needs into device memory in 16 bits (table: their new block table, or null)
 cudaError_t launch_chunk_stage(int dtype, bool q8, const ChunkArgs &c, void *k_out, void *v_out,
                                int32_t *table, cudaStream_t st);
-cudaError_t launch_chunk_combine(int dtype, const ChunkArgs &a, int ctas, cudaStream_t st);
+cudaError_t launch_chunk_combine(int dtype, const ChunkArgs &a, int ctas, bool many,
+                                 cudaStream_t st);
 // the 8-bit cache (device-visible addresses)
 cudaError_t launch_q8_append(int dtype, const void *k_new, const void *v_new,
                              const kv_q8_cache &c, const int32_t *q_start, const int32_t *bt,
