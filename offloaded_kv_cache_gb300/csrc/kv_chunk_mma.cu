@@ -25,8 +25,8 @@
 //
 // What bounds it, measured on one GB300 (a copy reaches 6.68 TB/s, a large bf16
 // matrix product 1.91 PFLOP/s):
-//   * kWide, 2048 new tokens at the end of 32768, 32/8 heads, bf16: 676-741 us
-//     from box to box, 1.44-1.58 PFLOP/s.  Products and softmax share the time: the
+//   * kWide, 2048 new tokens at the end of 32768, 32/8 heads, bf16: 676-747 us
+//     from box to box, 1.43-1.58 PFLOP/s.  Products and softmax share the time: the
 //     tensor pipe is active for two thirds of it, and what is left is each
 //     group's chain of scores, maximum, exponentials and weights.
 //   * kSolo, 32 prompts of up to 512, 32/32 heads, f16: 79 us for 41 us of bytes
