@@ -52,18 +52,27 @@ def torch_to_bits(t: torch.Tensor) -> np.ndarray:
 
 
 def _need(x: torch.Tensor, name: str, shape: tuple, dtype: torch.dtype):
-    """Refuses a tensor that the kernels would misread: they take a bare address."""
+    """Refuses a tensor that the kernels would misread: they take a bare address, and
+    run on the current device."""
     if (not x.is_cuda or x.dtype != dtype or tuple(x.shape) != tuple(shape) or
-            not x.is_contiguous()):
-        raise ValueError(f"{name}: a contiguous CUDA tensor {list(shape)} of {dtype} is needed, "
-                         f"not {list(x.shape)} of {x.dtype} on {x.device}")
+            not x.is_contiguous() or x.device.index != torch.cuda.current_device()):
+        raise ValueError(f"{name}: a contiguous CUDA tensor {list(shape)} of {dtype} on the current "
+                         f"device is needed, not {list(x.shape)} of {x.dtype} on {x.device}")
 
 
-def _chunk_inputs(shape: kv.kv_shape, q_start: torch.Tensor, heads: int, **rows: torch.Tensor):
+def _sequences(shape: kv.kv_shape, block_table: torch.Tensor, context_lens: torch.Tensor):
+    _need(block_table, "block_table", (shape.batch, shape.max_pages_per_seq), torch.int32)
+    _need(context_lens, "context_lens", (shape.batch,), torch.int32)
+
+
+def _chunk_inputs(of, q_start: torch.Tensor, heads: int, **rows: torch.Tensor):
+    """of: the DecodeLayer or Q8Cache whose sequences the chunk belongs to."""
+    shape = of.shape
     _need(q_start, "q_start", (shape.batch + 1,), torch.int32)
     total = next(iter(rows.values())).shape[0]
     for name, x in rows.items():
         _need(x, name, (total, heads, shape.head_dim), TORCH_OF_CODE[shape.dtype])
+    _sequences(shape, of.block_table, of.context_lens)
 
 
 def _chunk_buffers(q: torch.Tensor, out, nbytes: int, stream):
@@ -291,7 +300,7 @@ class DecodeLayer:
 
         q: [total_q][Hq][d] on the device, q_start: [B + 1] int32 on the device."""
         stream = self._st(stream)
-        _chunk_inputs(self.shape, q_start, self.shape.num_q_heads, q=q)
+        _chunk_inputs(self, q_start, self.shape.num_q_heads, q=q)
         chunk = kv.make_chunk(q_start, q.shape[0], max_q_len, window)
         out, space = _chunk_buffers(q, out, kv.kv_chunk_workspace_bytes(self.shape, chunk), stream)
         kv.kv_chunk_attn(self.shape, chunk, q, self.k_cache, self.v_cache, self.block_table,
@@ -311,7 +320,8 @@ class Q8Cache:
     host memory, with the block table and lengths of its sequences.
 
     shape: the kv_shape of the sequences (dtype = the model's); its kv_loc is
-    replaced by this cache's."""
+    replaced by this cache's.  block_table [B][maxP] and context_lens [B] are int32
+    tensors on the device, kept and not copied; every call looks at them again."""
 
     def __init__(self, shape: kv.kv_shape, block_table: torch.Tensor, context_lens: torch.Tensor,
                  kv_loc: str = "hbm", device: str = "cuda"):
@@ -332,7 +342,7 @@ class Q8Cache:
                max_q_len: int, stream=None):
         """Quantise and store the new tokens (k_new, v_new: [total_q][Hkv][d]) behind
         each sequence's cached ones; context_lens grows in place."""
-        _chunk_inputs(self.shape, q_start, self.shape.num_kv_heads, k_new=k_new, v_new=v_new)
+        _chunk_inputs(self, q_start, self.shape.num_kv_heads, k_new=k_new, v_new=v_new)
         chunk = kv.make_chunk(q_start, k_new.shape[0], max_q_len)
         kv.kv_q8_append(self.shape, chunk, k_new, v_new, self.cache, self.block_table,
                         self.context_lens, self.context_lens, DecodeLayer._st(stream))
@@ -341,7 +351,7 @@ class Q8Cache:
                window: int = 0, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """Attention of the chunk whose tokens were appended last (q: [total_q][Hq][d])."""
         stream = DecodeLayer._st(stream)
-        _chunk_inputs(self.shape, q_start, self.shape.num_q_heads, q=q)
+        _chunk_inputs(self, q_start, self.shape.num_q_heads, q=q)
         chunk = kv.make_chunk(q_start, q.shape[0], max_q_len, window)
         out, space = _chunk_buffers(q, out, kv.kv_q8_chunk_workspace_bytes(self.shape, chunk),
                                     stream)
@@ -353,11 +363,14 @@ class Q8Cache:
                   out_table: torch.Tensor | None = None, stream=None):
         """The cached tokens in the model's type, into pages out_table[b][p] (default:
         the same page numbers) of k_out, v_out [pages][Hkv][ps][d] on the device."""
-        table = self.block_table if out_table is None else out_table
         s = self.shape
         pages = (k_out.shape[0], s.num_kv_heads, s.page_size, s.head_dim)
         _need(k_out, "k_out", pages, TORCH_OF_CODE[s.dtype])
         _need(v_out, "v_out", pages, TORCH_OF_CODE[s.dtype])
-        _need(table, "out_table", (s.batch, s.max_pages_per_seq), torch.int32)
+        _sequences(s, self.block_table, self.context_lens)
+        table = self.block_table
+        if out_table is not None:
+            table = out_table
+            _need(table, "out_table", (s.batch, s.max_pages_per_seq), torch.int32)
         kv.kv_q8_read(self.shape, self.cache, self.block_table, self.context_lens, table,
                       k_out.shape[0], k_out, v_out, DecodeLayer._st(stream))
