@@ -320,18 +320,20 @@ __device__ __forceinline__ int vis_lo(int t, int tile0, int window) {
   return window > 0 ? t - tile0 - window + 1 : 0;
 }
 
-// A bounded wait of a whole warp or a lane; false once anything has timed out
-// (the kernel records that at its end).  Kept short: a kernel whose roles do
-// not fit the instruction cache together stalls on fetches.
+// A bounded wait of a whole warp; false once anything has timed out (the kernel
+// records that at its end).  The lanes vote: a barrier that completes while another
+// warp calls the kernel off may look done to some lanes and not to others, which
+// must not part.  Kept short: a kernel whose roles do not fit the instruction cache
+// together stalls on fetches.
 struct Waiter {
   volatile int *abort;
   unsigned long long limit;
   __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
     const uint64_t t0 = global_ns();
 #pragma unroll 1
-    while (!*abort) {
-      if (mbar_try_wait(bar, parity)) return true;
+    while (!__any_sync(0xFFFFFFFFu, *abort)) {
+      if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
       if (global_ns() - t0 > limit) *abort = 1;
     }
     return false;

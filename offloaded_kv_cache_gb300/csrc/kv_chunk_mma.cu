@@ -763,9 +763,6 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, Shape<kMode>::kCtas)
           enter(u);
         }
       };
-      auto ready = [&](uint32_t bar, uint32_t parity) -> bool {
-        return __all_sync(0xFFFFFFFFu, wait(bar, parity));
-      };
       const uint32_t ctl0 = smem_u32(&ctl);
       auto at = [&](const uint64_t &bar) {
         return ctl0 + (uint32_t)(reinterpret_cast<const uint8_t *>(&bar) -
@@ -780,14 +777,14 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, Shape<kMode>::kCtas)
         Ring<kStages> r = qk;
         if (kTurns) r.next(2 * x);
         if (c.tile == c.lo && (!kTurns || x == 0)) {
-          if (!ready(at(ctl.q_full[qx]), (q_ph >> qx) & 1)) return false;
+          if (!wait(at(ctl.q_full[qx]), (q_ph >> qx) & 1)) return false;
           q_ph ^= 1u << qx;
         }
         const int tile = c.tile + (kTurns ? x : 0);
         const bool leads = !kHalves || x == 0 || !active(0, c);  // first to use this K
         if (!kQ8 && leads && edge(c, tile) && elect_one()) mbar_arrive(at(ctl.mend[kTurns ? x : 0]));
         __syncwarp();
-        if (leads && !ready(full0 + 8 * r.s, r.ph)) return false;
+        if (leads && !wait(full0 + 8 * r.s, r.ph)) return false;
         tc_fence_after();
         const uint32_t a0 = dq + qx * (Sh::kQBytes >> 4), b0 = dk + r.s * (kTileBytes >> 4);
         const bool last = tile + 1 == (x == 0 && kHalves ? c.hi0 : c.hi);
@@ -812,9 +809,9 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, Shape<kMode>::kCtas)
         const int tile = p.tile + (kTurns ? x : 0);
         if (!kHalves || x == 0 || !active(0, p)) {  // first to use this V
           constexpr int mx = kTurns ? x : 0;
-          if (!ready(full0 + 8 * r.s, r.ph)) return false;
+          if (!wait(full0 + 8 * r.s, r.ph)) return false;
           if (!kQ8 && edge(p, tile)) {
-            if (!ready(at(ctl.mended[mx]), (mend_ph >> mx) & 1)) return false;
+            if (!wait(at(ctl.mended[mx]), (mend_ph >> mx) & 1)) return false;
             mend_ph ^= 1u << mx;
           }
         }
@@ -824,7 +821,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, Shape<kMode>::kCtas)
         const bool frees = !kHalves || x == 1 || !p.two;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (!ready(h ? at(ctl.p_full[x]) : at(ctl.p_half[x]), (p_ph >> x) & 1)) return false;
+          if (!wait(h ? at(ctl.p_full[x]) : at(ctl.p_half[x]), (p_ph >> x) & 1)) return false;
           tc_fence_after();
           if (elect_one()) {
 #pragma unroll
