@@ -340,6 +340,14 @@ struct Waiter {
   }
 };
 
+// How long a kernel that was called off waits for its own copies and products in flight
+// before its shared memory and TMEM pass to another CTA.  They end by themselves, within
+// microseconds (a copy from host memory too): the limit, which the waits that ran out
+// may have had far shorter, only bounds the wait for a tile that was never filled.
+__device__ __forceinline__ unsigned long long drain_limit(const ChunkArgs &a) {
+  return max(a.wait_limit_ns, 50'000'000ull);
+}
+
 template <int kStages> struct Ring {
   int s = 0;
   uint32_t ph = 0;

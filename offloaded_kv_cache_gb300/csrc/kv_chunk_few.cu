@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(Shape<T, Q8>::kThreads, Shape<T, Q8>::kCtas)
       // leave no copy in flight: each stage's last one (stages before ring.s
       // were filled in this lap, the others in the one before)
       for (int i = 0; i < kStages; ++i)
-        mbar_wait(smem_u32(&sh.full[i]), i < ring.s ? ring.ph : ring.ph ^ 1, a.wait_limit_ns);
+        mbar_wait(smem_u32(&sh.full[i]), i < ring.s ? ring.ph : ring.ph ^ 1, drain_limit(a));
     }
   } else {
     // ----------------------------------------------------------- consumers

@@ -1037,21 +1037,21 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, Shape<kMode>::kCtas)
     // before), and a last commit
     if (warp == kLoad && kQ8) {
       for (int i = 0; i < Sh::kRaw; ++i)
-        mbar_wait(smem_u32(&ctl.raw_full[i]), i < raw.s ? raw.ph : raw.ph ^ 1, a.wait_limit_ns);
+        mbar_wait(smem_u32(&ctl.raw_full[i]), i < raw.s ? raw.ph : raw.ph ^ 1, drain_limit(a));
     }
     if (warp == kLoad && !kQ8) {
       for (int i = 0; i < kStages; ++i)
-        mbar_wait(smem_u32(&ctl.full[i]), i < ld.s ? ld.ph : ld.ph ^ 1, a.wait_limit_ns);
+        mbar_wait(smem_u32(&ctl.full[i]), i < ld.s ? ld.ph : ld.ph ^ 1, drain_limit(a));
     }
     if (warp == kLoad + 3 && a.q_tma) {
       // q_full's phase in flight: as many as there were uses
       for (int x = 0; x < Sh::kQTiles; ++x)
         if ((q_uses >> x) & 1)
-          mbar_wait(smem_u32(&ctl.q_full[x]), (q_ph >> x) & 1, a.wait_limit_ns);
+          mbar_wait(smem_u32(&ctl.q_full[x]), (q_ph >> x) & 1, drain_limit(a));
     }
     if (warp == kLoad + 1) {
       if (elect_one()) tc_commit(smem_u32(&ctl.drain));
-      mbar_wait(smem_u32(&ctl.drain), 0, a.wait_limit_ns);
+      mbar_wait(smem_u32(&ctl.drain), 0, drain_limit(a));
     }
   }
   tc_fence_before();
