@@ -451,11 +451,14 @@ typedef struct {
  * out has the type of q (what the next projection takes), rounded once;
  * scores, the softmax and the sums are fp32, and the softmax weights enter
  * the value product in dtype.  What unseen tokens and unused slots of a page
- * hold, infinities and NaN among it, does not reach a row.  A page whose
- * block-table entry is out of range is skipped and recorded as
- * KV_ERR_BOUNDS.  With K/V in pinned host memory and 16-bit data the pages
- * the call needs cross the link once, into the workspace.  Results do not
- * depend on what ran before and repeat bit for bit on the same device.
+ * hold, infinities and NaN among it, does not reach a row.  Needed are the pages
+ * of the tokens that some row sees, those from max(0, context_lens[b] - n_b -
+ * window + 1) on with a window: one whose block-table entry is out of range is
+ * skipped and recorded as KV_ERR_BOUNDS.  Entries before may be anything (pages
+ * given back, or another sequence's).  With K/V in pinned host memory and
+ * 16-bit data the pages the call needs cross the link once, into the
+ * workspace.  Results do not depend on what ran before and repeat bit for bit
+ * on the same device.
  * KV_ERR_UNSUPPORTED where the rows and KV tiles of the call might not count
  * in int32 (some 10^11 token pairs per kv head).  A cache in another kind of
  * memory than kv_loc says is KV_ERR_LOCATION.

@@ -131,8 +131,9 @@ __global__ void __launch_bounds__(kThreads) chunk_core_kernel(const __grid_const
 #pragma unroll
         for (int c = 0; c < 8; ++c) o[r][c] = 0.f;
       }
-      // the pages of this thread's tokens of a tile (-1: none, -2: out of
-      // range), looked up a tile ahead
+      // the pages of this thread's tokens of a tile (-1: none, or one that no row
+      // sees; -2: out of range), looked up a tile ahead
+      const int from = seen_from(a, g);
       constexpr int kLoads = kTile * 16 / kThreads;
       int ph[kLoads];
       auto look_up = [&](int tile) {
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__(kThreads) chunk_core_kernel(const __grid_const
           ph[k] = -1;
           if (tile < g.tile_hi && pos < g.len) {
             const int p = a.bt[(long long)g.b * a.maxP + (pos >> ps_log2)];
-            ph[k] = p >= 0 && p < a.nphys ? p : -2;
+            ph[k] = p >= 0 && p < a.nphys ? p : pos >= from ? -2 : -1;
           }
         }
       };
@@ -339,18 +340,19 @@ __global__ void __launch_bounds__(kThreads, R == 4 ? 2 : 1)
         m[i] = -INFINITY;
         l[i] = 0.f;
       }
-      // page of this warp's eight tokens of a tile, a tile ahead
+      // page of this warp's eight tokens of a tile, a tile ahead (as above)
+      const int from = seen_from(a, g);
       auto look_up = [&](int tile) -> int {
         const int pos = tile * kTile + warp * 8;
         if (tile >= g.tile_hi || pos >= g.len) return -1;
         const int ph = a.bt[(long long)g.b * a.maxP + (pos >> ps_log2)];
-        return ph >= 0 && ph < a.nphys ? ph : -2;
+        return ph >= 0 && ph < a.nphys ? ph : pos + 8 > from ? -2 : -1;
       };
       int next = look_up(g.tile_lo);
       for (int tile = g.tile_lo; tile < g.tile_hi; ++tile) {
         const int ph = next, pos0 = tile * kTile + warp * 8;
         next = look_up(tile + 1);
-        if (ph < 0) {  // no token, or a bad page
+        if (ph < 0) {  // no token that a row sees, or a bad page
           if (ph == -2 && lane == 0) flag_error(a.status, KV_ERR_BOUNDS);
           continue;
         }

@@ -100,6 +100,11 @@ struct ChunkSeg {
   __device__ __forceinline__ bool first() const { return parts & 1; }
   __device__ __forceinline__ bool whole() const { return parts == 3; }
 };
+// The first token that some row of the segment's unit sees.  A page out of range before
+// it is nobody's: the caller may have given it back.  (t_first >= -1, as in unit_tiles)
+__device__ __forceinline__ int seen_from(const ChunkArgs &a, const ChunkSeg &g) {
+  return a.window > 0 ? max(g.t_first, -1) - a.window + 1 : 0;
+}
 
 // A CTA's share, kSegs segments of it listed at a time.
 template <int kSegs> struct ChunkShare {

@@ -174,6 +174,7 @@ __global__ void __launch_bounds__(Shape<T, Q8>::kThreads, Shape<T, Q8>::kCtas)
       const int nseg = sh.share.nseg;
       for (int sg = 0; sg < nseg && live; ++sg) {
         const ChunkSeg g = sh.share.seg[sg];
+        const int from = seen_from(a, g);
         for (int tile = g.tile_lo; tile < g.tile_hi; ++tile, ++filled, ring.next()) {
           int y = rows_total;  // past the end: the copy fills zeros
           uint32_t ok = 0;
@@ -184,7 +185,7 @@ __global__ void __launch_bounds__(Shape<T, Q8>::kThreads, Shape<T, Q8>::kCtas)
               if (ph >= 0 && ph < a.nphys) {
                 y = (ph * a.Hkv + g.kvh) * a.ps + (tok & (a.ps - 1));
                 ok = ((1u << (pt / 16)) - 1u) << (lane * (pt / 16));
-              } else {
+              } else if (tok + pt > from) {
                 flag_error(a.status, KV_ERR_BOUNDS);
               }
             }

@@ -654,6 +654,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, Shape<kMode>::kCtas)
       const int nseg = share.nseg;
       for (int sg = 0; sg < nseg && live; ++sg) {
         const ChunkSeg g = share.seg[sg];
+        const int from = seen_from(a, g);
         for (int tile = g.tile_lo; tile < g.tile_hi; ++tile, ++tiles_loaded) {
           int y = rows_total;  // past the end: the copy fills zeros
           uint32_t bad = 0;
@@ -664,7 +665,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, Shape<kMode>::kCtas)
               if (ph >= 0 && ph < a.nphys) {
                 y = (ph * a.Hkv + g.kvh) * a.ps;
               } else {
-                flag_error(a.status, KV_ERR_BOUNDS);
+                if ((page + 1) * a.ps > from) flag_error(a.status, KV_ERR_BOUNDS);
                 bad = ((1u << (a.ps / 16)) - 1u) << (lane * (a.ps / 16));
               }
             }
