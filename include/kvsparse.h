@@ -451,7 +451,9 @@ typedef struct {
  * out has the type of q (what the next projection takes), rounded once;
  * scores, the softmax and the sums are fp32, and the softmax weights enter
  * the value product in dtype.  What unseen tokens and unused slots of a page
- * hold, infinities and NaN among it, does not reach a row.  Needed are the pages
+ * hold, infinities and NaN among it, does not reach a row.  A channel in which a
+ * row sees infinities or NaN of V is their sum, however small their weights: the
+ * infinity where all are of one sign, else NaN.  Needed are the pages
  * of the tokens that some row sees, those from max(0, context_lens[b] - n_b -
  * window + 1) on with a window: one whose block-table entry is out of range is
  * skipped and recorded as KV_ERR_BOUNDS.  Entries before may be anything (pages

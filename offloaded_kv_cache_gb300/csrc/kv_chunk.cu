@@ -43,6 +43,21 @@ __device__ __forceinline__ void join_one(Joined &a, float m, float l, const floa
   a.o = make_float4(a.o.x * f + o.x * h, a.o.y * f + o.y * h, a.o.z * f + o.z * h,
                     a.o.w * f + o.w * h);
 }
+// Four channels from c on of a row at token t, whose weights' sum is l: the infinities and
+// NaN it sees among them in V of type T, in KV tiles [lo, hi), where its result is not
+// finite.  (A result over the 8-bit cache stays: codes have no infinity, and a NaN vector
+// is NaN in every channel.)
+template <class T>
+__device__ __forceinline__ void put_odd(const ChunkArgs &a, int b, int kvh, int t, int c, int lo,
+                                        int hi, int tile, float l, float4 &x) {
+  if (finite(x) || l != l) return;
+  const Seen s = seen_tokens(a, t, lo, hi, tile);
+  const Odd odd = odd_values<T, 4>(a, b, kvh, s.lo, s.hi, c);
+  if (odd.any(0)) x.x = odd.sum(0);
+  if (odd.any(1)) x.y = odd.sum(1);
+  if (odd.any(2)) x.z = odd.sum(2);
+  if (odd.any(3)) x.w = odd.sum(3);
+}
 template <class T>
 __device__ __forceinline__ void join_store(const ChunkArgs &a, const int4 &u, int q0, int r,
                                            int lane, const Joined &x) {
@@ -55,6 +70,10 @@ __device__ __forceinline__ void join_store(const ChunkArgs &a, const int4 &u, in
     *reinterpret_cast<uint2 *>(dst) =
         make_uint2(pack2(x.o.x * inv, x.o.y * inv, T{}), pack2(x.o.z * inv, x.o.w * inv, T{}));
 }
+// A weight of a token that the row does not see is -0: it must not meet an infinity or
+// NaN of V.  One that the row sees may be 0.
+__device__ __forceinline__ bool unseen(float weight) { return __float_as_uint(weight) == 0x80000000u; }
+
 // 4 channels (of lane `lane`) of one cached vector in fp32
 template <bool Q8>
 __device__ __forceinline__ float4 cached4(const void *base, const uint8_t *scale, long long vec,
@@ -210,7 +229,7 @@ __global__ void __launch_bounds__(kThreads) chunk_core_kernel(const __grid_const
           float sum = 0.f;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float p = ex2(s[r][j] - base);
+            const float p = s[r][j] == -INFINITY ? -0.f : ex2(s[r][j] - base);
             sum += p;
             Ps[(ty * MR + r) * kPStr + tx + 16 * j] = p;
           }
@@ -219,8 +238,7 @@ __global__ void __launch_bounds__(kThreads) chunk_core_kernel(const __grid_const
           for (int c = 0; c < 8; ++c) o[r][c] *= alpha;
         }
         __syncthreads();
-        // where some row does not see some token, a weight of 0 must not meet
-        // an infinity or NaN of V
+        // whether some row does not see some token
         const bool edge = tok0 + kTile - 1 > g.t_first || a.window > 0;
 #pragma unroll 2
         for (int j0 = 0; j0 < kTile; j0 += 4) {
@@ -243,7 +261,7 @@ __global__ void __launch_bounds__(kThreads) chunk_core_kernel(const __grid_const
             const float vv[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
             for (int r = 0; r < MR; ++r) {
-              if (edge && pw[r][j] == 0.f) continue;
+              if (edge && unseen(pw[r][j])) continue;
 #pragma unroll
               for (int c = 0; c < 8; ++c) o[r][c] += pw[r][j] * vv[c];
             }
@@ -260,19 +278,24 @@ __global__ void __launch_bounds__(kThreads) chunk_core_kernel(const __grid_const
         for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off, 16);
         const int rr = ty * MR + r;
         if (rr >= g.nrows) continue;
+        float4 x0 = make_float4(o[r][0], o[r][1], o[r][2], o[r][3]);
+        float4 x1 = make_float4(o[r][4], o[r][5], o[r][6], o[r][7]);
         if (whole) {
+          if constexpr (!Q8) {
+            put_odd<float>(a, g.b, g.kvh, t[r], tx * 4, g.tile_lo, g.tile_hi, kTile, sum, x0);
+            put_odd<float>(a, g.b, g.kvh, t[r], 64 + tx * 4, g.tile_lo, g.tile_hi, kTile, sum, x1);
+          }
           const float inv = sum == 0.f ? 0.f : 1.f / sum;
           float *dst = static_cast<float *>(a.out) + row_offset(a, g.q0, g.kvh, g.r0 + rr);
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            *reinterpret_cast<float4 *>(dst + 64 * h + tx * 4) =
-                make_float4(o[r][4 * h] * inv, o[r][4 * h + 1] * inv, o[r][4 * h + 2] * inv,
-                            o[r][4 * h + 3] * inv);
+          *reinterpret_cast<float4 *>(dst + tx * 4) =
+              make_float4(x0.x * inv, x0.y * inv, x0.z * inv, x0.w * inv);
+          *reinterpret_cast<float4 *>(dst + 64 + tx * 4) =
+              make_float4(x1.x * inv, x1.y * inv, x1.z * inv, x1.w * inv);
         } else {
           const long long pr = (long long)slot * a.slot_rows + rr;
           float *dst = a.part_o + pr * kHeadDim + tx * 4;
-          *reinterpret_cast<float4 *>(dst) = make_float4(o[r][0], o[r][1], o[r][2], o[r][3]);
-          *reinterpret_cast<float4 *>(dst + 64) = make_float4(o[r][4], o[r][5], o[r][6], o[r][7]);
+          *reinterpret_cast<float4 *>(dst) = x0;
+          *reinterpret_cast<float4 *>(dst + 64) = x1;
           if (tx == 0) {
             a.part_ml[2 * pr] = m[r];
             a.part_ml[2 * pr + 1] = sum;
@@ -415,13 +438,13 @@ __global__ void __launch_bounds__(kThreads, R == 4 ? 2 : 1)
         }
 #pragma unroll
         for (int i = 0; i < L; ++i) {
-          const float p = ex2(s[i] - (m[i] == -INFINITY ? 0.f : m[i]));
+          const float p =
+              s[i] == -INFINITY ? -0.f : ex2(s[i] - (m[i] == -INFINITY ? 0.f : m[i]));
           l[i] += p;
           sh.p[warp][tok][row0 + i] = p;
         }
         __syncwarp();
-        // where some row does not see some token, a weight of 0 must not meet
-        // an infinity or NaN of V
+        // whether some row does not see some token
         const bool edge = pos0 + 7 > g.t_first || a.window > 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -431,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, R == 4 ? 2 : 1)
             const float ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              if (edge && ww[r] == 0.f) continue;
+              if (edge && unseen(ww[r])) continue;
               float4 &x = o[r0 + r];
               x = make_float4(x.x + ww[r] * vx[j].x, x.y + ww[r] * vx[j].y, x.z + ww[r] * vx[j].z,
                               x.w + ww[r] * vx[j].w);
@@ -463,6 +486,9 @@ __global__ void __launch_bounds__(kThreads, R == 4 ? 2 : 1)
           join_one(x, sh.m[w][r], sh.l[w][r],
                    *reinterpret_cast<const float4 *>(&sh.o[w][r][4 * lane]));
         if (g.whole()) {
+          if constexpr (!Q8)
+            put_odd<float>(a, g.b, g.kvh, g.len - g.n + token_of(a, g.r0 + r), 4 * lane, g.tile_lo,
+                           g.tile_hi, kTile, x.l, x.o);
           join_store<float>(a, make_int4(g.b, g.kvh, g.r0, g.nrows), g.q0, r, lane, x);
         } else {
           const long long at = (long long)part_slot(g) * a.slot_rows + r;
@@ -521,6 +547,42 @@ __device__ __forceinline__ void join_rows(const ChunkArgs &a, int first, int las
       for (int i = 0; i < R; ++i) join_one(acc[i], ml[k][i].x, ml[k][i].y, o[k][i]);
   }
 }
+// join_store, and whether the result is not finite: such channels are infinities until
+// mend_rows has read the cache again (NaN stays where the row's weights are).
+template <class T>
+__device__ __forceinline__ bool combine_store(const ChunkArgs &a, const int4 &u, int q0, int r,
+                                              int lane, Joined x) {
+  const bool odd = !finite(x.o) && x.l == x.l && !a.k_scale;
+  if (odd) {
+    x.o.x = finite(x.o.x) ? x.o.x : INFINITY;
+    x.o.y = finite(x.o.y) ? x.o.y : INFINITY;
+    x.o.z = finite(x.o.z) ? x.o.z : INFINITY;
+    x.o.w = finite(x.o.w) ? x.o.w : INFINITY;
+  }
+  join_store<T>(a, u, q0, r, lane, x);
+  return odd;
+}
+// Rows r .. r + count - 1 of the unit, and so on every `step` rows, all written by this
+// thread: put_odd for what combine_store left.  At the kernel's end, by itself: in
+// combine_store it cost the registers of the loads in flight (8 rows over 32k tokens in
+// 8 bits 86 -> 96 us).
+template <class T>
+__device__ __noinline__ void mend_rows(const ChunkArgs &a, int4 u, int q0, int r, int step, int count,
+                                       int lane) {
+  const int t0 = a.ctx[u.x] - (a.q_start[u.x + 1] - q0);
+  for (; r < u.w; r += step)
+    for (int i = r; i < min(r + count, u.w); ++i) {
+      T *dst = static_cast<T *>(a.out) + row_offset(a, q0, u.y, u.z + i) + 4 * lane;
+      float x[4];
+      load_n(dst, x);
+      if (finite(make_float4(x[0], x[1], x[2], x[3]))) continue;
+      const Seen s = seen_tokens(a, t0 + token_of(a, u.z + i), 0, INT_MAX, 1);
+      const Odd odd = odd_values<T, 4>(a, u.x, u.y, s.lo, s.hi, 4 * lane);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (odd.any(k) && x[k] == INFINITY) dst[k] = (T)odd.sum(k);
+    }
+}
 template <class T>
 __global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constant__ ChunkArgs a) {
   __shared__ Joined part[8][kJoinRows][32];
@@ -529,48 +591,55 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constan
   if (u.x < 0) return;
   const int first = blockIdx.x, last = w.y, nrows = u.w;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  bool odd = false;
+  int from, step, count = 1;  // the rows this thread writes
   if (last - first < 8 && nrows <= 8 * (int)gridDim.y) {
-    const int r = blockIdx.y * 8 + warp;
-    if (r >= nrows) return;
+    from = blockIdx.y * 8 + warp;
+    step = nrows;
+    if (from >= nrows) return;
     Joined one[1];
-    join_rows<1, 8>(a, first, last, first, 1, r, nrows, lane, one);
-    join_store<T>(a, u, w.x, r, lane, one[0]);
-    return;
-  }
-  Joined acc[kJoinRows];
-  if (last - first < 8) {
-    for (int r0 = (blockIdx.y * 8 + warp) * kJoinRows; r0 < nrows;
-         r0 += gridDim.y * 8 * kJoinRows) {
+    join_rows<1, 8>(a, first, last, first, 1, from, nrows, lane, one);
+    odd = combine_store<T>(a, u, w.x, from, lane, one[0]);
+  } else if (last - first < 8) {
+    Joined acc[kJoinRows];
+    from = (blockIdx.y * 8 + warp) * kJoinRows;
+    step = gridDim.y * 8 * kJoinRows;
+    count = kJoinRows;
+    for (int r0 = from; r0 < nrows; r0 += step) {
       join_rows<kJoinRows, 2>(a, first, last, first, 1, r0, nrows, lane, acc);
 #pragma unroll
       for (int i = 0; i < kJoinRows; ++i)
-        if (r0 + i < nrows) join_store<T>(a, u, w.x, r0 + i, lane, acc[i]);
+        if (r0 + i < nrows) odd |= combine_store<T>(a, u, w.x, r0 + i, lane, acc[i]);
     }
-    return;
-  }
-  const int per = nrows <= (int)gridDim.y ? 1 : kJoinRows;  // rows a block takes at a time
-  for (int r0 = blockIdx.y * per; r0 < nrows; r0 += gridDim.y * per) {
-    if (per == 1) {
-      Joined one[1];
-      join_rows<1, 8>(a, first, last, first + warp, 8, r0, nrows, lane, one);
-      part[warp][0][lane] = one[0];
-    } else {
-      join_rows<kJoinRows, 2>(a, first, last, first + warp, 8, r0, nrows, lane, acc);
+  } else {
+    const int per = nrows <= (int)gridDim.y ? 1 : kJoinRows;  // rows a block takes at a time
+    from = blockIdx.y * per + warp;
+    step = gridDim.y * per;
+    for (int r0 = blockIdx.y * per; r0 < nrows; r0 += step) {
+      if (per == 1) {
+        Joined one[1];
+        join_rows<1, 8>(a, first, last, first + warp, 8, r0, nrows, lane, one);
+        part[warp][0][lane] = one[0];
+      } else {
+        Joined acc[kJoinRows];
+        join_rows<kJoinRows, 2>(a, first, last, first + warp, 8, r0, nrows, lane, acc);
 #pragma unroll
-      for (int i = 0; i < kJoinRows; ++i) part[warp][i][lane] = acc[i];
-    }
-    __syncthreads();
-    if (warp < per && r0 + warp < nrows) {
-      Joined x = part[0][warp][lane];
-#pragma unroll
-      for (int i = 1; i < 8; ++i) {
-        const Joined &y = part[i][warp][lane];
-        join_one(x, y.m, y.l, y.o);
+        for (int i = 0; i < kJoinRows; ++i) part[warp][i][lane] = acc[i];
       }
-      join_store<T>(a, u, w.x, r0 + warp, lane, x);
+      __syncthreads();
+      if (warp < per && r0 + warp < nrows) {
+        Joined x = part[0][warp][lane];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) {
+          const Joined &y = part[i][warp][lane];
+          join_one(x, y.m, y.l, y.o);
+        }
+        odd |= combine_store<T>(a, u, w.x, r0 + warp, lane, x);
+      }
+      __syncthreads();
     }
-    __syncthreads();
   }
+  if (odd) mend_rows<T>(a, u, w.x, from, step, count, lane);  // (seldom)
 }
 
 template <class K>

@@ -325,6 +325,77 @@ __device__ __forceinline__ int vis_lo(int t, int tile0, int window) {
   return window > 0 ? t - tile0 - window + 1 : 0;
 }
 
+// Infinities and NaN of V.  A channel in which a row sees some is their sum: the
+// weights are positive, however small.  The products do not give that everywhere: a
+// weight may have rounded to 0, and where some row does not see a token its infinities
+// and NaN are kept out of the products.  So where a row's result is not finite, or
+// something was kept out, the cache is read again (seldom) and the sum written over the
+// channel: by the attention kernels for whole units, by the combine for the others.
+// (Rows whose weights are NaN stay as they are, NaN in every channel.)
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
+__device__ __forceinline__ bool finite(const float4 &x) {
+  return finite(x.x) && finite(x.y) && finite(x.z) && finite(x.w);
+}
+__device__ __forceinline__ void load_n(const float *p, float (&x)[4]) {
+  const float4 w = *reinterpret_cast<const float4 *>(p);
+  x[0] = w.x; x[1] = w.y; x[2] = w.z; x[3] = w.w;
+}
+template <class T>
+__device__ __forceinline__ void load_n(const T *p, float (&x)[4]) {
+  const uint2 w = *reinterpret_cast<const uint2 *>(p);
+  const float2 u = unpack2(w.x, T{}), v = unpack2(w.y, T{});
+  x[0] = u.x; x[1] = u.y; x[2] = v.x; x[3] = v.y;
+}
+template <class T> __device__ __forceinline__ void load_n(const T *p, float (&x)[8]) { load8(p, x); }
+// The tokens lo .. hi of KV tiles [first, end) that the row at token t sees.
+struct Seen {
+  int lo, hi;
+};
+__device__ __forceinline__ Seen seen_tokens(const ChunkArgs &a, int t, int first, int end, int tile) {
+  return Seen{max(first * tile, a.window > 0 ? t - a.window + 1 : 0),
+              min((end - 1) * tile + tile - 1, t)};
+}
+// What of `N` channels is not finite, a bit each: +infinities and NaN, -infinities and NaN.
+// Their sum is an infinity where one of the two holds, NaN where both do.
+struct Odd {
+  uint32_t plus = 0, minus = 0;
+  __device__ __forceinline__ void see(int i, float x) {
+    if (!(x <= 3.402823466e38f)) plus |= 1u << i;
+    if (!(x >= -3.402823466e38f)) minus |= 1u << i;
+  }
+  __device__ __forceinline__ bool any(int i) const { return ((plus | minus) >> i) & 1; }
+  __device__ __forceinline__ float sum(int i) const {
+    return __uint_as_float(!((minus >> i) & 1)  ? 0x7F800000u
+                           : !((plus >> i) & 1) ? 0xFF800000u
+                                                : 0x7FC00000u);
+  }
+};
+// Of tokens lo .. hi: what is not finite in channels c .. c + N - 1.  (Eight loads in
+// flight: 32k tokens take a few ms.)
+template <class T, int N>
+__device__ __noinline__ Odd odd_values(const ChunkArgs &a, int b, int kvh, int lo, int hi, int c) {
+  Odd odd;
+  for (int p0 = lo & -16; p0 <= hi; p0 += 16) {
+    const int ph = a.bt[(long long)b * a.maxP + p0 / a.ps];
+    if (ph < 0 || ph >= a.nphys) continue;
+    const T *v = static_cast<const T *>(a.v) +
+                 (((long long)ph * a.Hkv + kvh) * a.ps + (p0 & (a.ps - 1))) * kHeadDim + c;
+#pragma unroll 1
+    for (int j0 = 0; j0 < 16; j0 += 8) {
+      float x[8][N];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) load_n(v + (j0 + j) * kHeadDim, x[j]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (p0 + j0 + j >= lo && p0 + j0 + j <= hi)
+#pragma unroll
+          for (int i = 0; i < N; ++i) odd.see(i, x[j][i]);
+    }
+    if ((odd.plus & odd.minus) == (1u << N) - 1u) break;  // NaN stays NaN
+  }
+  return odd;
+}
+
 // A bounded wait of a whole warp; false once anything has timed out (the kernel
 // records that at its end).  The lanes vote: a barrier that completes while another
 // warp calls the kernel off may look done to some lanes and not to others, which

@@ -416,7 +416,8 @@ __global__ void __launch_bounds__(Shape<T, Q8>::kThreads, Shape<T, Q8>::kCtas)
           if constexpr (!Q8) {
             // where some row does not see some token, the same holds for
             // infinities and NaN: they are cleared, and the rows that do see
-            // them become NaN in their channels (seldom)
+            // them become NaN in their channels, which has the cache read again
+            // when they are written (seldom)
             if (tok0 + 15 > g.t_first || a.window > 0) {
               uint32_t any = 0;
 #pragma unroll
@@ -539,6 +540,19 @@ __global__ void __launch_bounds__(Shape<T, Q8>::kThreads, Shape<T, Q8>::kCtas)
           }
           const int pr = g.r0 + n;
           if (whole) {
+            if constexpr (!Q8) {
+              bool odd = false;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) odd |= !finite(x[k]);
+              if (odd && sum == sum) {  // (seldom)
+                const Seen s = seen_tokens(a, g.len - g.n + token_of(a, pr), g.tile_lo, g.tile_hi,
+                                           kTile);
+                const Odd seen = odd_values<T, 8>(a, g.b, g.kvh, s.lo, s.hi, c);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  if (seen.any(k)) x[k] = seen.sum(k);
+              }
+            }
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
             for (int k = 0; k < 8; ++k) x[k] *= inv;

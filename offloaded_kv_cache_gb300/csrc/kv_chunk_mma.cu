@@ -49,9 +49,9 @@
 // care (its scores are replaced), V does.  Slots past the sequence's end in its
 // last page are zeroed in shared memory before the product.  In tiles where
 // some row does not see some token, infinities and NaN of V are zeroed as
-// well, and the rows that do see them get their NaN when they are written
-// (a slow path that only such data takes).  Pages past the end or out of range
-// are filled with zeros by the TMA unit.
+// well.  Rows that do see them get them when they are written, here and where a
+// result is not finite (kv_chunk.cuh; a slow path that only such data takes).
+// Pages past the end or out of range are filled with zeros by the TMA unit.
 #include <type_traits>
 
 #include "kv_chunk.cuh"
@@ -206,38 +206,101 @@ __device__ __forceinline__ bool clean_rows(uint8_t *slab, int r0, int r1, int la
   return found;
 }
 
-// Rows that see a non-finite V of a scanned tile (8-bit: a NaN vector of any
-// tile) get NaN in its channels [c0, c1): the cache is read again.
+// Writes over channels [c0, c1) of each lane's row, the unit's row r, where it sees
+// infinities or NaN of V; 8-bit: NaN, where it sees a NaN vector.  A warp's lanes look the
+// cache over together: all tiles of the segment, or those that were scanned, which alone
+// can hold such values where every result is finite.  need: the row is there and its
+// weights are not NaN.
 template <class T, bool kQ8>
-__device__ __noinline__ void poison_row(const ChunkArgs &a, const ChunkSeg &g, int t, int c0,
-                                        int c1, T *out, float *part) {
-  if (t < 0) return;
+__device__ __forceinline__ void put_odd(const ChunkArgs &a, const ChunkSeg &g, int r, int c0, int c1,
+                                        bool need, bool all) {
+  const int lane = threadIdx.x & 31;
+  const int t = g.len - g.n + token_of(a, g.r0 + r), from = a.window > 0 ? t - a.window + 1 : 0;
+  Odd row[4];  // of channels 32 i .. + 31
+#pragma unroll 1
   for (int tile = g.tile_lo; tile < g.tile_hi; ++tile) {
-    if (!kQ8 && !mend_of(a, g, tile).scans()) continue;
-    const int lo = max(tile * kTile, a.window > 0 ? t - a.window + 1 : 0);
-    const int hi = min(min(tile * kTile + kTile - 1, t), g.len - 1);
-    for (int j = lo; j <= hi; ++j) {
-      const int ph = a.bt[(long long)g.b * a.maxP + j / a.ps];
+    if (!kQ8 && !all && !mend_of(a, g, tile).scans()) continue;
+#pragma unroll 1
+    for (int j0 = tile * kTile; j0 < min(g.len, (tile + 1) * kTile); j0 += 16) {
+      const int ph = a.bt[(long long)g.b * a.maxP + j0 / a.ps];
       if (ph < 0 || ph >= a.nphys) continue;
-      const long long vec = ((long long)ph * a.Hkv + g.kvh) * a.ps + j % a.ps;
-      if (kQ8) {
-        for (int c = c0; c < c1 && a.v_scale[vec] == kQ8NanScale; ++c) {
-          if (part) part[c] = __uint_as_float(0x7FC00000u);
-          else reinterpret_cast<uint16_t *>(out)[c] = 0x7FFFu;
+      const long long vec = ((long long)ph * a.Hkv + g.kvh) * a.ps + (j0 & (a.ps - 1));
+      if constexpr (kQ8) {
+        uint32_t nan = __ballot_sync(0xFFFFFFFFu, a.v_scale[vec + (lane & 15)] == kQ8NanScale);
+        for (nan &= 0xFFFFu; nan; nan &= nan - 1) {
+          const int j = j0 + __ffs(nan) - 1;
+          if (j <= t && j >= from)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) row[i].plus = row[i].minus = ~0u;
         }
-        continue;
-      }
-      const uint32_t *v =
-          reinterpret_cast<const uint32_t *>(static_cast<const T *>(a.v) + vec * kHeadDim);
-      for (int c = c0; c < c1; c += 2) {
-        const uint32_t x = (v[c / 2] & NonFinite<T>::kMask) + NonFinite<T>::kOne;
-        for (int h = 0; h < 2; ++h) {
-          if (!(x & (h ? 0x80000000u : 0x8000u))) continue;
-          if (part) part[c + h] = __uint_as_float(0x7FC00000u);
-          else reinterpret_cast<uint16_t *>(out)[c + h] = 0x7FFFu;
+      } else {
+        // half a warp reads a vector
+        const uint4 *v = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.v) +
+                                                         vec * kHeadDim) + lane;
+        uint4 w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[k] = v[32 * k];
+        Odd eight[8];  // of this lane's channels of token 2 k + (lane >> 4)
+        uint32_t some = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          float x[8];
+          load8(reinterpret_cast<const T *>(&w[k]), x);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) eight[k].see(i, x[i]);
+          some |= (eight[k].plus | eight[k].minus) ? 1u << k : 0u;
+        }
+        some = __reduce_or_sync(0xFFFFFFFFu, some);
+        if (!some) continue;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (!((some >> k) & 1)) continue;
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            const int j = j0 + 2 * k + h;
+            const bool sees = j <= t && j >= from;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const bool mine = lane >> 2 == 4 * h + i;
+              const uint32_t plus = __reduce_or_sync(
+                  0xFFFFFFFFu, mine ? eight[k].plus << (8 * (lane & 3)) : 0u);
+              const uint32_t minus = __reduce_or_sync(
+                  0xFFFFFFFFu, mine ? eight[k].minus << (8 * (lane & 3)) : 0u);
+              if (sees) row[i].plus |= plus, row[i].minus |= minus;
+            }
+          }
         }
       }
     }
+  }
+  if (!need) return;
+  T *out = static_cast<T *>(a.out) + row_offset(a, g.q0, g.kvh, g.r0 + r);
+  float *part =
+      g.whole() ? nullptr : a.part_o + ((long long)part_slot(g) * a.slot_rows + r) * kHeadDim;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll 1
+    for (int c = max(c0, 32 * i); c < min(c1, 32 * i + 32); ++c) {
+      if (!row[i].any(c & 31)) continue;
+      const float x = row[i].sum(c & 31);
+      if (part) part[c] = x;
+      else out[c] = (T)x;
+    }
+}
+
+// The same for a list of segments, once all are written: the group's rows start at row
+// r_lo of a unit.  Bit i of `odd` and `nan`: in segment i a result of the lane's row is not
+// finite, its weights are NaN.  (Where a segment is written, a call costs the registers
+// of what goes on there: 32 prompts of 512 80 -> 85 us.)
+template <class T, bool kQ8>
+__device__ __noinline__ void put_odd_list(const ChunkArgs &a, const ChunkSeg *seg, int nseg, int r_lo,
+                                          int c0, int c1, uint32_t odd, uint32_t nan, bool zeroed) {
+  const int row = threadIdx.x & 127;
+  for (int i = 0; i < nseg; ++i) {
+    const bool need = row < a.row_tile && r_lo + row < seg[i].nrows && !((nan >> i) & 1);
+    const bool all = __any_sync(0xFFFFFFFFu, need && ((odd >> i) & 1));
+    if (!all && !(zeroed && __any_sync(0xFFFFFFFFu, need))) continue;
+    put_odd<T, kQ8>(a, seg[i], min(r_lo + row, seg[i].nrows - 1), c0, c1, need, all);
   }
 }
 
@@ -393,6 +456,8 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, Shape<kMode>::kCtas)
       // (the Q loader has seen to the sign of the scale, and to 0)
       const float sc = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
       bool live = true;
+      uint32_t odd_segs = 0, nan_segs = 0;  // for put_odd_list
+      static_assert(Sh::kSegs <= 32, "bits");
       const int nseg = share.nseg;
       for (int sg = 0; sg < nseg && live; ++sg) {
         const ChunkSeg g = share.seg[sg];
@@ -524,7 +589,8 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, Shape<kMode>::kCtas)
           prow = (long long)part_slot(g) * a.slot_rows + min(urow, g.nrows - 1);
           part = a.part_o + prow * kHeadDim;
         }
-        float f0 = kTurns || begun ? 1.f : 0.f, f1 = 0.f;
+        float f0 = 1.f, f1 = 0.f;
+        bool none0 = m == -INFINITY, none1 = true;  // the row saw nothing (or O is not there)
         constexpr int kCols = kTurns ? 64 : 128;  // channels this thread writes
         const int c0 = kTurns ? 64 * x : 0;
         const bool second = kTurns && g.tile_hi - g.tile_lo > 1;
@@ -543,6 +609,8 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, Shape<kMode>::kCtas)
           const float2 u = ctl.ml[0][at], v = ctl.ml[1][at];
           M = fmaxf(u.x, v.x);
           const float b = M == -INFINITY ? 0.f : M;
+          none0 = u.x == -INFINITY;
+          none1 = v.x == -INFINITY;
           f0 = ex2(u.x - b);
           f1 = ex2(v.x - b);
           l = u.y * f0 + v.y * f1;
@@ -552,7 +620,8 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, Shape<kMode>::kCtas)
           f0 *= inv;
           f1 *= inv;
           const uint32_t o0 = tmem + lanes + kOAt + (kTurns ? 0 : x * 128) + c0;
-          const bool nothing = __any_sync(0xFFFFFFFFu, f0 == 0.f);  // (of O, at f0 = 0)
+          const bool nothing = __any_sync(0xFFFFFFFFu, none0);
+          bool odd = false;  // a result is not finite
           // rows of this lane's quad, for the transposed stores
           T *quad_out[4];
           bool quad_mine[4];
@@ -575,7 +644,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, Shape<kMode>::kCtas)
             tc_wait_ld();
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] *= f0;
-            if (nothing && f0 == 0.f) {
+            if (nothing && none0) {
 #pragma unroll
               for (int i = 0; i < 32; ++i) o[i] = 0.f;
             }
@@ -584,7 +653,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, Shape<kMode>::kCtas)
               tmem_ld32(o0 + 128 + c, o1);
               tc_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] += f1 == 0.f ? 0.f : o1[i] * f1;
+              for (int i = 0; i < 32; ++i) o[i] += none1 ? 0.f : o1[i] * f1;
             }
             if (whole) {
               // A lane holds four 16-byte chunks of its row.  Transposed among
@@ -595,6 +664,14 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, Shape<kMode>::kCtas)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                   h[k][i] = pack2(o[8 * k + 2 * i], o[8 * k + 2 * i + 1], T{});
+              if constexpr (!kQ8) {
+                uint32_t z[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) z[i] = times_zero(h[k][i], z[i], T{});
+                odd |= ((z[0] | z[1] | z[2] | z[3]) & 0x7FFF7FFFu) != 0;
+              }
 #pragma unroll
               for (int step = 1; step < 4; step *= 2) {
                 const bool up = lane & step;
@@ -621,15 +698,12 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, Shape<kMode>::kCtas)
                     make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
             }
           }
-          __syncwarp();  // a row's poisoned channels are written after its quad's stores
-          if (mine) {
-            if (!whole && (!kTurns || x == 0)) {
-              a.part_ml[2 * prow] = M;
-              a.part_ml[2 * prow + 1] = l;
-            }
-            if (*reinterpret_cast<volatile int *>(&ctl.poison))  // (seldom)
-              poison_row<T, kQ8>(a, share.seg[sg], t, c0, c0 + kCols, out, part);
+          if (mine && !whole && (!kTurns || x == 0)) {
+            a.part_ml[2 * prow] = M;
+            a.part_ml[2 * prow + 1] = l;
           }
+          if (odd) odd_segs |= 1u << sg;
+          if (l != l) nan_segs |= 1u << sg;
           tc_fence_before();
         }
         if constexpr (kTurns) {
@@ -643,6 +717,11 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, Shape<kMode>::kCtas)
           j_ph ^= 1;
         }
       }
+      __syncwarp();  // (a row's stores were its quad's)
+      const bool zeroed = __any_sync(0xFFFFFFFFu, *reinterpret_cast<volatile int *>(&ctl.poison));
+      if (live && (zeroed || __any_sync(0xFFFFFFFFu, odd_segs)))  // (seldom)
+        put_odd_list<T, kQ8>(a, share.seg, nseg, kHalves ? x * rt : 0, kTurns ? 64 * x : 0,
+                             kTurns ? 64 * x + 64 : 128, odd_segs, nan_segs, zeroed);
     }
   } else if (warp == kLoad) {
     // ---------------------------------------------------------------- loader
