@@ -530,11 +530,14 @@ __global__ void __launch_bounds__(Shape<T, Q8>::kThreads, Shape<T, Q8>::kCtas)
 #pragma unroll
           for (int w = 0; w < kConsumers; ++w) top = fmaxf(top, sh.m[w][n]);
           const float base = top == -INFINITY ? 0.f : top;
+          // (the factors carry V's scales, 2^-110 and up: without 2^64 those of warps whose
+          // maximum is 2^-9 below the row's would be 0)
+          constexpr float kUp = Q8 ? 64.f : 0.f, kDown = Q8 ? 0x1p-64f : 1.f;
           float sum = 0.f, x[8] = {};
 #pragma unroll
           for (int w = 0; w < kConsumers; ++w) {
             sum += sh.l[w][n] * ex2(sh.m[w][n] - base);
-            const float f = ex2(sh.r[w][n] - base);
+            const float f = ex2(sh.r[w][n] - base + kUp);
 #pragma unroll
             for (int k = 0; k < 8; ++k) x[k] += sh.o[w][n][c + k] * f;
           }
@@ -553,12 +556,14 @@ __global__ void __launch_bounds__(Shape<T, Q8>::kThreads, Shape<T, Q8>::kCtas)
                   if (seen.any(k)) x[k] = seen.sum(k);
               }
             }
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const float inv = sum == 0.f ? 0.f : kDown / sum;
 #pragma unroll
             for (int k = 0; k < 8; ++k) x[k] *= inv;
             store8(static_cast<T *>(a.out) + row_offset(a, g.q0, g.kvh, pr) + c, x);
           } else {
             const long long at = (long long)part_slot(g) * a.slot_rows + n;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] *= kDown;
             store8(a.part_o + at * kHeadDim + c, x);
             if (c == 0) {
               a.part_ml[2 * at] = top;
