@@ -462,7 +462,8 @@ typedef struct {
  * workspace.  Results do not depend on what ran before and repeat bit for bit
  * on the same device.
  * KV_ERR_UNSUPPORTED where the rows and KV tiles of the call might not count
- * in int32 (some 10^11 token pairs per kv head).  A cache in another kind of
+ * in int32 (some 10^11 token pairs per kv head; where pages pass through the
+ * workspace, B * maxP * ps * Hkv tokens and heads of 2^36).  A cache in another kind of
  * memory than kv_loc says is KV_ERR_LOCATION.
  * kv_chunk_workspace_bytes: the workspace for this shape and chunk on the
  * current device (0 for an invalid one); q_start itself is not read.  Calls
@@ -515,7 +516,8 @@ int kv_q8_append(const kv_shape *shape, const kv_chunk *chunk, const void *k_new
  * that some pages only can be brought back; out_table may be block_table
  * itself.  Slots past the last token keep what they held.  0 <=
  * context_lens[b] <= maxP * ps; an entry of either table out of range skips
- * the page and records KV_ERR_BOUNDS. */
+ * the page and records KV_ERR_BOUNDS.  B * maxP * ps * Hkv of 2^36 and more is
+ * KV_ERR_UNSUPPORTED. */
 int kv_q8_read(const kv_shape *shape, const kv_q8_cache *cache, const int32_t *block_table,
                const int32_t *context_lens, const int32_t *out_table, int64_t out_pages,
                void *k_out, void *v_out, void *stream);

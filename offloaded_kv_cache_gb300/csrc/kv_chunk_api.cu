@@ -237,11 +237,13 @@ int q_map(const kv_shape *s, const kv_chunk *c, const void *q, int row_tile,
   return encode_map(MapShape{type16(s), q, c->total_q, s->num_q_heads, G, row_tile / G}, map);
 }
 
-// The kernels count tiles in int32, and index the staged cache's rows as a
-// cache's own.
+// The kernels count tiles and the staging's blocks in int32, and index the staged
+// cache's rows as a cache's own.
 bool plan_fits(const kv_shape *s, const ChunkPlan &pl) {
-  return pl.most_tiles <= INT_MAX &&
-         pl.stage_pages <= INT_MAX / ((long long)s->num_kv_heads * s->page_size);
+  if (pl.most_tiles > INT_MAX) return false;
+  return !pl.stage ||
+         (pl.stage_pages <= INT_MAX / ((long long)s->num_kv_heads * s->page_size) &&
+          q8_grid_fits(s->batch, s->max_pages_per_seq, s->page_size, s->num_kv_heads));
 }
 
 size_t chunk_bytes(const kv_shape *s, const kv_chunk *c, bool q8) {
@@ -406,7 +408,9 @@ int kv_q8_read(const kv_shape *shape, const kv_q8_cache *cache, const int32_t *b
   if (!al16(k_out) || !al16(v_out) || !al4(block_table) || !al4(context_lens) ||
       !al4(out_table) || out_pages < 1)
     return KV_ERR_INVALID_ARG;
-  if (out_pages > INT_MAX / ((long long)shape->num_kv_heads * shape->page_size))
+  if (out_pages > INT_MAX / ((long long)shape->num_kv_heads * shape->page_size) ||
+      !q8_grid_fits(shape->batch, shape->max_pages_per_seq, shape->page_size,
+                    shape->num_kv_heads))
     return KV_ERR_UNSUPPORTED;
   const int dev = current_device();
   if (dev < 0) return KV_ERR_CUDA;

@@ -103,6 +103,8 @@ cudaError_t launch_chunk_stage(int dtype, bool q8, const ChunkArgs &c, void *k_o
                                int32_t *table, cudaStream_t st);
 cudaError_t launch_chunk_combine(int dtype, const ChunkArgs &a, int ctas, bool many,
                                  cudaStream_t st);
+// whether the read back's and the staging's blocks count in int32
+bool q8_grid_fits(int B, int maxP, int ps, int Hkv);
 // the 8-bit cache (device-visible addresses)
 cudaError_t launch_q8_append(int dtype, const void *k_new, const void *v_new,
                              const kv_q8_cache &c, const int32_t *q_start, const int32_t *bt,

@@ -340,6 +340,11 @@ bool item_grid(int B, int maxP, int ps, int Hkv, int *items, int *blocks) {
 }
 }  // namespace
 
+bool q8_grid_fits(int B, int maxP, int ps, int Hkv) {
+  int items, blocks;
+  return item_grid(B, maxP, ps, Hkv, &items, &blocks);
+}
+
 cudaError_t launch_chunk_stage(int dtype, bool q8, const ChunkArgs &c, void *k_out, void *v_out,
                                int32_t *table, cudaStream_t st) {
   StageArgs a = {};
