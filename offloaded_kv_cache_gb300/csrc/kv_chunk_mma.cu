@@ -590,7 +590,8 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, Shape<kMode>::kCtas)
           part = a.part_o + prow * kHeadDim;
         }
         float f0 = 1.f, f1 = 0.f;
-        bool none0 = m == -INFINITY, none1 = true;  // the row saw nothing (or O is not there)
+        // the row saw nothing, or O is not there (of NaN scores alone, l is NaN)
+        bool none0 = m == -INFINITY && l == 0.f, none1 = true;
         constexpr int kCols = kTurns ? 64 : 128;  // channels this thread writes
         const int c0 = kTurns ? 64 * x : 0;
         const bool second = kTurns && g.tile_hi - g.tile_lo > 1;
@@ -609,8 +610,8 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, Shape<kMode>::kCtas)
           const float2 u = ctl.ml[0][at], v = ctl.ml[1][at];
           M = fmaxf(u.x, v.x);
           const float b = M == -INFINITY ? 0.f : M;
-          none0 = u.x == -INFINITY;
-          none1 = v.x == -INFINITY;
+          none0 = u.x == -INFINITY && u.y == 0.f;
+          none1 = v.x == -INFINITY && v.y == 0.f;
           f0 = ex2(u.x - b);
           f1 = ex2(v.x - b);
           l = u.y * f0 + v.y * f1;

@@ -139,3 +139,21 @@ def test_host_resident_cache(dtype, n):
     p = Problem(dtype, 4, 2, 16, [400], [n], loc="host")
     scatter(p, n)
     run(p)
+
+
+@pytest.mark.parametrize("q8", [False, True], ids=["own", "q8"])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("n", [1, 5, 30, 90, 200])
+@pytest.mark.parametrize("window,extra", [(1, 1), (1, 90), (2, 300)])
+def test_rows_that_see_nan_keys_alone(dtype, n, window, extra, q8):
+    p = Problem(dtype, 4, 2, 16, [700, 40], [n, 10], window, extra_pages=extra, q8=q8, seed=n)
+    for j in (699, 698, 699 - n // 2, 700 - n):
+        if q8:
+            p.code["k"][p.table[0, j // 16], 1, j % 16] = 0x7F
+            p.scale8["k"][p.table[0, j // 16], 1, j % 16] = 255
+        else:
+            p.k[p.table[0, j // 16], 1, j % 16, 9] = NAN
+    p.upload()
+    p.attend()
+    torch.cuda.synchronize()
+    check(p.d_out, *p.expected())
