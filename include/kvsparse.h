@@ -525,7 +525,9 @@ int kv_q8_read(const kv_shape *shape, const kv_q8_cache *cache, const int32_t *b
 /* Chunk attention over the 8-bit cache: kv_chunk_attn on the values it stands
  * for (a NaN vector makes the rows that see it NaN).  KV_F32 queries and weights
  * may enter the products as two f16 terms each (22 bits); a row of q is scaled by
- * a power of two for it, so its own size does not matter. */
+ * a power of two for it, 2^100 at most, so its own size does not matter (rows below
+ * 2^-86 lose bits, of scores below 2^-62 * scale).  16-bit q: the weights enter the
+ * value product in 16 bits, f16 or dtype. */
 size_t kv_q8_chunk_workspace_bytes(const kv_shape *shape, const kv_chunk *chunk);
 int kv_q8_chunk_attn(const kv_shape *shape, const kv_chunk *chunk, const void *q,
                      const kv_q8_cache *cache, const int32_t *block_table,

@@ -13,10 +13,11 @@
 // us per 128 tokens whatever the rows: here it is a fraction of that, which
 // short contexts and many kv heads show.
 //
-// Measured on one GB300: one token over 8 x 65536 tokens, 64/8 heads, bf16 q, 8-bit:
-// 136 us, 6.1 TB/s of the 6.68 a copy reaches; over 4 x 32768, 8-bit: 43 us, with
-// fp32 q 70 us (one CTA per SM); 4 x 700 tokens, 32/8 heads, f16: 9.5 us, of which the
-// launches, the lengths and the combine are the most.
+// Measured on one GB300, replayed from a graph: one token over 8 x 65536 tokens, 64/8
+// heads, bf16 q, 8-bit: 135 us, 6.1 TB/s of the 6.68 a copy reaches; over 4 x 32768,
+// 8-bit: 43 us, with fp32 q 70 us (one CTA per SM); 4 x 700 tokens, 32/8 heads, f16: 9.6
+// us, of which the launches, the lengths and the combine are the most (13.6 us as a
+// Python call, which the host bounds).
 //
 // Units of 8 rows (of 16, each byte served two groups of rows, but the registers
 // left room for half the warps: slower from 16 rows on).  CTA: four consumer warps
@@ -35,9 +36,13 @@
 // V's joins the weight's exponent, weight = 2^(z + e_v - R) with R the row's
 // running maximum of z + e_v, next to m, that of z, for the softmax's sum: z,
 // e_v and both maxima in the log2 domain.  bf16 rows of q are scaled into f16 by a
-// power of two per row, which is exact but for channels 2^39 below the row's
-// largest; fp32 rows of q, and their weights, are taken as two f16 terms (22
-// bits), with the value products of each tile summed apart and added in fp32.
+// power of two per row, which puts the row's largest channel at 2^14: exact for channels
+// down to 2^31 below it, with fewer and fewer bits for smaller ones, none from 2^39 on.
+// (The power is 2^100 at most: rows below 2^-86 keep fewer bits, of scores below 2^-62
+// times the scale.)  fp32 rows of q, and their weights, are taken as two f16 terms (22
+// bits), with the value products of each tile summed apart and added in fp32.  The
+// other weights enter the value products in 16 bits, f16 over codes and the cache's type
+// over 16-bit ones, which is what these products take; a second term would double them.
 #include <type_traits>
 
 #include "kv_chunk.cuh"

@@ -10,7 +10,8 @@
 //   4         (8-bit) expand tiles of codes into the ring's 16-bit tiles
 // Per KV tile of 128 tokens and softmax group: S = Q K^T (128 x 128 x 128)
 // into TMEM; the group takes its maximum and exponentials and writes the
-// weights P in 16 bits over S; O += P V.  While one group computes, the tensor
+// weights P in 16 bits over S, the type that the product takes with V's (a second
+// term of P would be a second product; the sum uses the unrounded weights); O += P V.  While one group computes, the tensor
 // cores work for the other, of the same CTA or of another.  TMEM: S and P of
 // two groups at columns 0 and 128, O at 256 and 384; of one at 0 and at 128.
 //   * kWide: a unit is 256 packed rows, 128 per group; both groups use

@@ -9,11 +9,15 @@
 //
 // Both kernels move each byte once and compute a few operations per element, few
 // enough to let memory bound them; a decode step's append is bounded by latency.
-// Measured on one GB300, where a copy reaches 6.68 TB/s: append of 32 chunks of up
-// to 513 tokens, 32 kv heads, f16: 30.3 us, 5.7 TB/s (in fp32, with divisions and each
-// vector's maximum on its own: 35.0); of 4 x 2048 tokens, 8 kv heads: 6.4 us; of one
-// token for 32 sequences: 2.1 us; read back of 4 x 32768 tokens, 8 kv heads, bf16: 106
-// us, 6.3 TB/s; of 2 x 544, 32 kv heads: 5.5 us.
+// Measured on one GB300, where a copy reaches 6.68 TB/s, replayed from graphs (as Python
+// calls the short ones take what the host does, in brackets): append of 32 chunks of up
+// to 513 tokens, 32 kv heads, f16: 30.3 us, 5.7 TB/s (computed in fp32, with divisions and
+// each vector's maximum on its own: 35.0), fp32 data 47.6 us, 6.1 TB/s; of 4 x 2048 tokens,
+// 8 kv heads: 6.4 us [21], fp32 12.4; of one token for 32 sequences: 2.1 us [16], fp32
+// 2.3; read back of 4 x 32768 tokens, 8 kv heads, bf16: 105 us, 6.3 TB/s; of 4 x 16384
+// into fp32: 103 us, 5.4 TB/s; of 2 x 544, 32 kv heads: 5.6 us [9.5], fp32 13.3.  The cache
+// in pinned host memory: append of 4 x 2048 53 us, of 32 x 513 371 us, 156-160 GB/s of the
+// link's 211 (the scales are single bytes); read back of 4 x 32768 1058 us, 211 GB/s.
 #include <algorithm>
 
 #include "kv_chunk.cuh"
