@@ -514,7 +514,8 @@ int kv_q8_append(const kv_shape *shape, const kv_chunk *chunk, const void *k_new
  * The result is a cache every other call takes (with num_phys_pages =
  * out_pages and KV_LOC_HBM).  A negative out_table entry skips its page, so
  * that some pages only can be brought back; out_table may be block_table
- * itself.  Slots past the last token keep what they held.  0 <=
+ * itself, and a page that it names twice has to be the same page read back.
+ * Slots past the last token keep what they held.  0 <=
  * context_lens[b] <= maxP * ps; an entry of either table out of range skips
  * the page and records KV_ERR_BOUNDS.  B * maxP * ps * Hkv of 2^36 and more is
  * KV_ERR_UNSUPPORTED. */

@@ -20,14 +20,12 @@ def _lib(kvlib):
 
 
 # chunk sizes for every kernel with such waits; extra pages for the forms that the table's width chooses
-@pytest.mark.parametrize("q8", [False, True], ids=["own", "q8"])
-@pytest.mark.parametrize("dtype,news", [("bf16", [1, 1]), ("f16", [13, 1]), ("bf16", [90, 200]),
-                                        ("f32", [2, 1])])
+@pytest.mark.parametrize("q8,dtype,news", [
+    (q8, *c) for q8 in (False, True) for c in (("bf16", [1, 1]), ("f16", [13, 1]), ("bf16", [90, 200]))
+] + [(True, "f32", [2, 1])])
 @pytest.mark.parametrize("extra", [1, 90, 300])
 @pytest.mark.parametrize("limit", [1, 500, 3000])
 def test_short_limits(dtype, news, extra, limit, q8):
-    if dtype == "f32" and not q8:
-        pytest.skip("no waits")
     p = Problem(dtype, 8, 2, 16, [700, 300], news, q8=q8, extra_pages=extra).upload()
     want, tol = p.expected()
     seen = []
