@@ -21,9 +21,13 @@
  *   kv_chunk_attn         -> attention of a chunk of new tokens per sequence (a
  *                            prefill step, proposed tokens to check) over the
  *                            cache that holds them
+ *   kv_rope_append        -> a chunk of new tokens into the cache, q and keys
+ *                            turned to their positions on the way, the index
+ *                            kept (kv_rope: the turning alone)
  *   kv_q8_append, kv_q8_chunk_attn, kv_q8_read -> the cache held in 8 bits:
  *                            quantised as it is written, attended in place,
  *                            read back into the shape's own type
+ *   kv_q4_append, kv_q4_chunk_attn, kv_q4_read -> the same in 4 bits
  * K/V pages live in device memory (HBM) or in pinned host memory that the GPU
  * reads in place, with no staging copy (DirectKV -- No Buffer, No Bottleneck:
  * Efficient Zero-Copy KV Cache Offloading for Long-Context LLMs, core method 1
@@ -474,6 +478,61 @@ int kv_chunk_attn(const kv_shape *shape, const kv_chunk *chunk, const void *q,
                   const int32_t *context_lens, float scale, void *out, void *workspace,
                   size_t workspace_bytes, void *stream);
 
+/* Rotary positions.  The first rotary_dim channels of a vector are rotary_dim / 2
+ * pairs: channels j and j + rotary_dim / 2 (interleaved = 0) or 2 j and 2 j + 1
+ * (interleaved = 1).  At position t pair j is turned by the angle t * freq[j]:
+ *   (a, b) -> scale * (a cos - b sin, a sin + b cos),
+ * the other channels stay as they are, bit for bit.  Frequencies changed for longer
+ * contexts are the caller's: they are in freq, and scale takes the factor that some
+ * such schemes put on the turned channels (else 1).
+ *   freq       [rotary_dim / 2] double, device memory: radians per position, below 2^54
+ *   positions  [total_q] int32, device memory, or NULL: row i of sequence b's chunk is
+ *              at position context_lens[b] + i
+ * The angle is kept as a fraction of a turn in 64 bits, so that far positions (int32, of
+ * either sign: -t turns back what t turned) lose nothing; sines, cosines and the turning
+ * itself are fp32, and a result is rounded once, to dtype.  rotary_dim is a multiple of
+ * 8 in 8 .. 128 (else KV_ERR_UNSUPPORTED). */
+typedef struct {
+  const double *freq;
+  const int32_t *positions;
+  int32_t rotary_dim;
+  int32_t interleaved;
+  float scale;      /* finite */
+  int32_t reserved; /* 0 */
+} kv_rope_plan;
+
+/* Turns the chunk's rows of q, of k, or of both (a NULL pair is left out): what precedes
+ * a quantising append, or an attention whose keys are cached already.
+ *   q, q_out [total_q][Hq][d] dtype      k, k_out [total_q][Hkv][d] dtype, device memory
+ * q_out may be q and k_out k; otherwise no two arrays overlap.  context_lens: the lengths
+ * BEFORE the chunk; it is not read, and may be NULL, where positions are given.  Rows
+ * no sequence owns are not written.  max_pages_per_seq does not bound the positions here. */
+int kv_rope(const kv_shape *shape, const kv_chunk *chunk, const kv_rope_plan *rope, const void *q,
+            void *q_out, const void *k, void *k_out, const int32_t *context_lens, void *stream);
+
+/* Chunk append: token i of sequence b's chunk is stored at position context_lens[b] + i of
+ * the cache, context_lens being the lengths BEFORE the append (0 <= context_lens[b],
+ * context_lens[b] + n_b <= maxP * ps), its key turned by `rope`; q, if given, is turned
+ * to q_out.  What kv_append_token is for one token of every sequence, for any number.
+ *   rope          NULL: keys are stored as they are (q and q_out must be NULL then)
+ *   q, q_out      [total_q][Hq][d] dtype, or both NULL; q_out may be q
+ *   k_new, v_new  [total_q][Hkv][d] dtype, device memory
+ *   k_cache, v_cache  where kv_loc says
+ *   minmax        may be NULL (no index update): the entry of every page that receives
+ *                 tokens becomes the channel-wise min/max of its tokens, bit-identical to
+ *                 kv_page_minmax_build on the new lengths; preconditions as in
+ *                 kv_append_token
+ *   context_lens_out  may be NULL, may equal context_lens, may not overlap it in part:
+ *                 receives context_lens[b] + n_b
+ * A token whose block-table entry is out of range is dropped; its sequence keeps its
+ * length, and KV_ERR_BOUNDS is recorded (the same for a sequence that is skipped whole,
+ * whose rows of q_out are not written).  The pages written must not be shared with
+ * another row. */
+int kv_rope_append(const kv_shape *shape, const kv_chunk *chunk, const kv_rope_plan *rope,
+                   const void *q, void *q_out, const void *k_new, const void *v_new, void *k_cache,
+                   void *v_cache, const int32_t *block_table, const int32_t *context_lens,
+                   int32_t *context_lens_out, void *minmax, void *stream);
+
 /* The cache in 8 bits (half the bytes that offloading moves and attention
  * reads).  Every key and value vector x of a token and kv head is held as d
  * e4m3 codes c and one power of two:
@@ -532,6 +591,48 @@ int kv_q8_read(const kv_shape *shape, const kv_q8_cache *cache, const int32_t *b
 size_t kv_q8_chunk_workspace_bytes(const kv_shape *shape, const kv_chunk *chunk);
 int kv_q8_chunk_attn(const kv_shape *shape, const kv_chunk *chunk, const void *q,
                      const kv_q8_cache *cache, const int32_t *block_table,
+                     const int32_t *context_lens, float scale, void *out, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+/* The cache in 4 bits: 73 bytes a vector, where 8 bits take 129 and 16 bits 256.  Every
+ * key and value vector x of a token and kv head is held as d integers c, a scale s (an
+ * e4m3 value) for every 16 channels, and one power of two:
+ *   e = the smallest integer with max |x| <= 7 * 448 * 2^e, kept in [-15, 4] for KV_F16
+ *       and in [-110, 4] for KV_BF16 and KV_F32
+ *   s = the smallest e4m3 value with max |x| <= 7 * s * 2^e over its 16 channels, at
+ *       most 448
+ *   c = floor(x / (s * 2^e) + 1/2), limited to +-7; 0 where s is 0
+ * and stands for c * s * 2^e, which is exact in every dtype (|x| > 50176 is limited to
+ * that).  Scales and powers are short enough for every comparison to be exact, so the
+ * codes do not depend on how they are computed.  A vector with an infinity or a NaN is
+ * kept as NaN (power byte 255, scales 0, integers 0).
+ *   k_codes, v_codes  [N][Hkv][ps][d / 2]   byte j holds c + 8 of channel 2 j in its
+ *                                           low half and of 2 j + 1 in its high half
+ *   k_scale, v_scale  [N][Hkv][ps][d / 16]  s as e4m3 codes
+ *   k_power, v_power  [N][Hkv][ps]          e + 127
+ * bytes, all where kv_loc says and 16-byte aligned.  A cache is read with the dtype it
+ * was written with. */
+typedef struct {
+  uint8_t *k_codes;
+  uint8_t *v_codes;
+  uint8_t *k_scale;
+  uint8_t *v_scale;
+  uint8_t *k_power;
+  uint8_t *v_power;
+} kv_q4_cache;
+
+/* kv_q8_append, kv_q8_read and kv_q8_chunk_attn for the 4-bit cache: the same arguments,
+ * checks and errors.  KV_F32 queries and weights enter the products as two f16 terms
+ * each, as there. */
+int kv_q4_append(const kv_shape *shape, const kv_chunk *chunk, const void *k_new,
+                 const void *v_new, const kv_q4_cache *cache, const int32_t *block_table,
+                 const int32_t *context_lens, int32_t *context_lens_out, void *stream);
+int kv_q4_read(const kv_shape *shape, const kv_q4_cache *cache, const int32_t *block_table,
+               const int32_t *context_lens, const int32_t *out_table, int64_t out_pages,
+               void *k_out, void *v_out, void *stream);
+size_t kv_q4_chunk_workspace_bytes(const kv_shape *shape, const kv_chunk *chunk);
+int kv_q4_chunk_attn(const kv_shape *shape, const kv_chunk *chunk, const void *q,
+                     const kv_q4_cache *cache, const int32_t *block_table,
                      const int32_t *context_lens, float scale, void *out, void *workspace,
                      size_t workspace_bytes, void *stream);
 

@@ -31,7 +31,8 @@ constexpr int kChunkTile = 128;  // tokens per KV tile of the tensor-core kernel
 struct ChunkArgs {
   const void *q;
   const void *k, *v;                // K and V (8-bit: the codes)
-  const uint8_t *k_scale, *v_scale; // 8-bit only
+  const uint8_t *k_scale, *v_scale; // 8-bit: the scale bytes; 4-bit: the power bytes
+  const uint8_t *k_group, *v_group; // 4-bit only: the scales of 16 channels
   const int32_t *q_start, *bt, *ctx;
   void *out;
   float *part_o;    // [2 * ctas][slot_rows][d]

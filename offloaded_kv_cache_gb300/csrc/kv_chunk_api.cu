@@ -37,6 +37,21 @@ int resolve_q8(const kv_shape *s, const kv_q8_cache *c, kv_q8_cache *dev) {
   return KV_OK;
 }
 
+// The six arrays of a 4-bit cache, likewise.
+int resolve_q4(const kv_shape *s, const kv_q4_cache *c, kv_q4_cache *dev) {
+  if (!c) return KV_ERR_INVALID_ARG;
+  uint8_t *const in[6] = {c->k_codes, c->v_codes, c->k_scale, c->v_scale, c->k_power, c->v_power};
+  uint8_t **const to[6] = {&dev->k_codes, &dev->v_codes, &dev->k_scale,
+                           &dev->v_scale, &dev->k_power, &dev->v_power};
+  for (int i = 0; i < 6; ++i) {
+    const void *at;
+    const int rc = resolve_kv(s, in[i], &at);
+    if (rc != KV_OK) return rc;
+    *to[i] = static_cast<uint8_t *>(const_cast<void *>(at));
+  }
+  return KV_OK;
+}
+
 // Up to this many packed rows the 16-bit kernels' converting form reads the
 // 8-bit cache itself, in units of 128 rows; above, the cache is expanded into the
 // workspace first and read in units of 256.  (4 x 32k tokens, 8 kv heads, us,
@@ -115,8 +130,9 @@ struct ChunkPlan {
 
 // Everything here follows from the shape and the host's bounds; the lengths
 // are known on the device only.
-ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, bool q8) {
+ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, CacheForm form) {
   ChunkPlan pl;
+  const bool q8 = form == kQ8Form, q4 = form == kQ4Form;
   const int dev = current_device();
   const int sms = dev >= 0 ? sm_count(dev) : 152;
   const int G = s->num_q_heads / s->num_kv_heads;
@@ -157,6 +173,7 @@ ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, bool q8) {
     pl.rows = packed <= 4 ? 4 : packed <= KVS_F32_FEW_ROWS || !fills ? 8 : 64;
     if (pl.rows == 8) per_sm = 1;  // resident CTAs of its kernel (registers)
   }
+  if (q4) pl.stage = true;
   // units of all sequences: full ones and one more each; no more CTAs than
   // there can be tiles
   const double units = std::min((double)s->batch * ((packed + pl.rows - 1) / pl.rows),
@@ -177,7 +194,7 @@ ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, bool q8) {
     const long long rows = (long long)s->batch * s->max_pages_per_seq;
     pl.renumber = rows < s->num_phys_pages;
     pl.stage_pages = pl.renumber ? rows : s->num_phys_pages;
-    const size_t page = (size_t)s->num_kv_heads * s->page_size * kHeadDim * 2;
+    const size_t page = (size_t)s->num_kv_heads * s->page_size * kHeadDim * elem_bytes(s->dtype);
     pl.off_table = off;
     if (pl.renumber) off = align256(off + (size_t)rows * 4);
     pl.off_k = off;
@@ -246,27 +263,36 @@ bool plan_fits(const kv_shape *s, const ChunkPlan &pl) {
           q8_grid_fits(s->batch, s->max_pages_per_seq, s->page_size, s->num_kv_heads));
 }
 
-size_t chunk_bytes(const kv_shape *s, const kv_chunk *c, bool q8) {
+size_t chunk_bytes(const kv_shape *s, const kv_chunk *c, CacheForm form) {
   if (check_shape(s) != KV_OK || check_chunk(s, c) != KV_OK) return 0;
-  const ChunkPlan pl = make_chunk_plan(s, c, q8);
+  const ChunkPlan pl = make_chunk_plan(s, c, form);
   return plan_fits(s, pl) ? pl.total : 0;
 }
 
 int chunk_common(const kv_shape *s, const kv_chunk *c, const void *q, const void *k_cache,
-                 const void *v_cache, const kv_q8_cache *q8, bool is_q8, const int32_t *bt,
-                 const int32_t *ctx, float scale, void *out, void *workspace, size_t ws_bytes,
-                 void *stream) {
+                 const void *v_cache, const kv_q8_cache *q8, const kv_q4_cache *q4, CacheForm form,
+                 const int32_t *bt, const int32_t *ctx, float scale, void *out, void *workspace,
+                 size_t ws_bytes, void *stream) {
   int rc = check_shape(s);
   if (rc) return rc;
   if ((rc = check_chunk(s, c)) != KV_OK) return rc;
   if (!al16(q) || !al16(out) || !al4(bt) || !al4(ctx) || !std::isfinite(scale))
     return KV_ERR_INVALID_ARG;
-  const ChunkPlan pl = make_chunk_plan(s, c, is_q8);
+  const ChunkPlan pl = make_chunk_plan(s, c, form);
   if (!plan_fits(s, pl)) return KV_ERR_UNSUPPORTED;
   const int dev = current_device();
   if (dev < 0) return KV_ERR_CUDA;
   ChunkArgs a = {};
-  if (is_q8) {
+  if (form == kQ4Form) {
+    kv_q4_cache d;
+    if ((rc = resolve_q4(s, q4, &d)) != KV_OK) return rc;
+    a.k = d.k_codes;
+    a.v = d.v_codes;
+    a.k_scale = d.k_power;
+    a.v_scale = d.v_power;
+    a.k_group = d.k_scale;
+    a.v_group = d.v_scale;
+  } else if (form == kQ8Form) {
     kv_q8_cache d;
     if ((rc = resolve_q8(s, q8, &d)) != KV_OK) return rc;
     a.k = d.k_codes;
@@ -312,7 +338,7 @@ int chunk_common(const kv_shape *s, const kv_chunk *c, const void *q, const void
   long long pages = s->num_phys_pages;
   if (pl.stage) {
     int32_t *table = pl.renumber ? reinterpret_cast<int32_t *>(ws + pl.off_table) : nullptr;
-    if (launch_chunk_stage(s->dtype, is_q8, a, ws + pl.off_k, ws + pl.off_v, table, st) !=
+    if (launch_chunk_stage(s->dtype, form, a, ws + pl.off_k, ws + pl.off_v, table, st) !=
         cudaSuccess)
       return KV_ERR_CUDA;
     a.k = ws + pl.off_k;
@@ -334,10 +360,79 @@ int chunk_common(const kv_shape *s, const kv_chunk *c, const void *q, const void
     if (a.q_tma && (rc = q_map(s, c, q, pl.row_tile, &tq)) != KV_OK) return rc;
     e = launch_chunk_mma(s->dtype, pl.form, a, tq, tk, tv, pl.ctas, st);
   } else {
-    e = launch_chunk_core(a, is_q8, pl.rows, pl.ctas, st);
+    e = launch_chunk_core(a, form == kQ8Form, pl.rows, pl.ctas, st);
   }
   if (e == cudaSuccess) e = launch_chunk_combine(s->dtype, a, pl.ctas, pl.many_parts, st);
   return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+}
+
+int check_append(const kv_shape *s, const kv_chunk *c, const void *k_new, const void *v_new,
+                 const int32_t *bt, const int32_t *ctx, const int32_t *ctx_out) {
+  int rc = check_shape(s);
+  if (rc) return rc;
+  if ((rc = check_chunk(s, c)) != KV_OK) return rc;
+  if (!al16(k_new) || !al16(v_new) || !al4(bt) || !al4(ctx) || (ctx_out && !al4(ctx_out)))
+    return KV_ERR_INVALID_ARG;
+  // the same array or one apart, not one that overlaps
+  if (ctx_out && ctx_out != ctx && ctx_out < ctx + s->batch && ctx < ctx_out + s->batch)
+    return KV_ERR_INVALID_ARG;
+  return KV_OK;
+}
+
+int check_read(const kv_shape *s, const int32_t *bt, const int32_t *ctx, const int32_t *out_table,
+               int64_t out_pages, const void *k_out, const void *v_out) {
+  const int rc = check_shape(s);
+  if (rc) return rc;
+  if (!al16(k_out) || !al16(v_out) || !al4(bt) || !al4(ctx) || !al4(out_table) || out_pages < 1)
+    return KV_ERR_INVALID_ARG;
+  if (out_pages > INT_MAX / ((long long)s->num_kv_heads * s->page_size) ||
+      !q8_grid_fits(s->batch, s->max_pages_per_seq, s->page_size, s->num_kv_heads))
+    return KV_ERR_UNSUPPORTED;
+  return KV_OK;
+}
+// The pages read back are in device memory whatever kv_loc says.
+int resolve_read(const kv_shape *s, void **k_out, void **v_out) {
+  kv_shape hbm = *s;
+  hbm.kv_loc = KV_LOC_HBM;
+  for (void **p : {k_out, v_out}) {
+    const void *at = nullptr;
+    const int rc = resolve_kv(&hbm, *p, &at);
+    if (rc != KV_OK) return rc;
+    *p = const_cast<void *>(at);
+  }
+  return KV_OK;
+}
+
+int check_rope(const kv_rope_plan *r) {
+  if (!r || !r->freq || ((uintptr_t)r->freq & 7u) || ((uintptr_t)r->positions & 3u) ||
+      (r->interleaved != 0 && r->interleaved != 1) || !std::isfinite(r->scale) || r->reserved != 0)
+    return KV_ERR_INVALID_ARG;
+  return r->rotary_dim >= 8 && r->rotary_dim <= kHeadDim && r->rotary_dim % 8 == 0
+             ? KV_OK
+             : KV_ERR_UNSUPPORTED;
+}
+// The bytes of a [total_q][heads][d] array.
+struct Rows {
+  const uint8_t *at;
+  size_t bytes;
+};
+Rows rows_of(const kv_shape *s, const kv_chunk *c, const void *p, bool q) {
+  return Rows{static_cast<const uint8_t *>(p), (size_t)c->total_q * kHeadDim * elem_bytes(s->dtype) *
+                                                   (q ? s->num_q_heads : s->num_kv_heads)};
+}
+// Whether arrays are aligned, and no output meets another array in part or out of place:
+// the first `in_out` pairs of rows are an input and its output, which may be one array.
+bool rows_apart(const Rows *r, int n, int in_out) {
+  for (int i = 0; i < n; ++i) {
+    if (r[i].at && !al16(r[i].at)) return false;
+    for (int j = 0; j < i; ++j) {
+      const bool out_i = i < 2 * in_out && (i & 1), out_j = j < 2 * in_out && (j & 1);
+      if (!r[i].at || !r[j].at || (!out_i && !out_j)) continue;
+      if (out_i && j == i - 1 && r[i].at == r[j].at) continue;
+      if (r[i].at < r[j].at + r[j].bytes && r[j].at < r[i].at + r[i].bytes) return false;
+    }
+  }
+  return true;
 }
 
 }  // namespace
@@ -345,11 +440,11 @@ int chunk_common(const kv_shape *s, const kv_chunk *c, const void *q, const void
 extern "C" {
 
 size_t kv_chunk_workspace_bytes(const kv_shape *shape, const kv_chunk *chunk) {
-  return chunk_bytes(shape, chunk, false);
+  return chunk_bytes(shape, chunk, kOwnForm);
 }
 
 size_t kv_q8_chunk_workspace_bytes(const kv_shape *shape, const kv_chunk *chunk) {
-  return chunk_bytes(shape, chunk, true);
+  return chunk_bytes(shape, chunk, kQ8Form);
 }
 
 int kv_chunk_attn(const kv_shape *shape, const kv_chunk *chunk, const void *q,
@@ -357,7 +452,7 @@ int kv_chunk_attn(const kv_shape *shape, const kv_chunk *chunk, const void *q,
                   const int32_t *context_lens, float scale, void *out, void *workspace,
                   size_t workspace_bytes, void *stream) {
   KV_API_RANGE();
-  return chunk_common(shape, chunk, q, k_cache, v_cache, nullptr, false, block_table,
+  return chunk_common(shape, chunk, q, k_cache, v_cache, nullptr, nullptr, kOwnForm, block_table,
                       context_lens, scale, out, workspace, workspace_bytes, stream);
 }
 
@@ -366,25 +461,16 @@ int kv_q8_chunk_attn(const kv_shape *shape, const kv_chunk *chunk, const void *q
                      const int32_t *context_lens, float scale, void *out, void *workspace,
                      size_t workspace_bytes, void *stream) {
   KV_API_RANGE();
-  return chunk_common(shape, chunk, q, nullptr, nullptr, cache, true, block_table, context_lens,
-                      scale, out, workspace, workspace_bytes, stream);
+  return chunk_common(shape, chunk, q, nullptr, nullptr, cache, nullptr, kQ8Form, block_table,
+                      context_lens, scale, out, workspace, workspace_bytes, stream);
 }
 
 int kv_q8_append(const kv_shape *shape, const kv_chunk *chunk, const void *k_new,
                  const void *v_new, const kv_q8_cache *cache, const int32_t *block_table,
                  const int32_t *context_lens, int32_t *context_lens_out, void *stream) {
   KV_API_RANGE();
-  int rc = check_shape(shape);
+  int rc = check_append(shape, chunk, k_new, v_new, block_table, context_lens, context_lens_out);
   if (rc) return rc;
-  if ((rc = check_chunk(shape, chunk)) != KV_OK) return rc;
-  if (!al16(k_new) || !al16(v_new) || !al4(block_table) || !al4(context_lens) ||
-      (context_lens_out && !al4(context_lens_out)))
-    return KV_ERR_INVALID_ARG;
-  // the same array or one apart, not one that overlaps
-  if (context_lens_out && context_lens_out != context_lens &&
-      context_lens_out < context_lens + shape->batch &&
-      context_lens < context_lens_out + shape->batch)
-    return KV_ERR_INVALID_ARG;
   const int dev = current_device();
   if (dev < 0) return KV_ERR_CUDA;
   kv_q8_cache d;
@@ -403,32 +489,127 @@ int kv_q8_read(const kv_shape *shape, const kv_q8_cache *cache, const int32_t *b
                const int32_t *context_lens, const int32_t *out_table, int64_t out_pages,
                void *k_out, void *v_out, void *stream) {
   KV_API_RANGE();
-  int rc = check_shape(shape);
+  int rc = check_read(shape, block_table, context_lens, out_table, out_pages, k_out, v_out);
   if (rc) return rc;
-  if (!al16(k_out) || !al16(v_out) || !al4(block_table) || !al4(context_lens) ||
-      !al4(out_table) || out_pages < 1)
-    return KV_ERR_INVALID_ARG;
-  if (out_pages > INT_MAX / ((long long)shape->num_kv_heads * shape->page_size) ||
-      !q8_grid_fits(shape->batch, shape->max_pages_per_seq, shape->page_size,
-                    shape->num_kv_heads))
-    return KV_ERR_UNSUPPORTED;
   const int dev = current_device();
   if (dev < 0) return KV_ERR_CUDA;
   kv_q8_cache d;
   if ((rc = resolve_q8(shape, cache, &d)) != KV_OK) return rc;
-  // the pages read back are in device memory whatever kv_loc says
-  kv_shape hbm = *shape;
-  hbm.kv_loc = KV_LOC_HBM;
-  const void *ko = nullptr, *vo = nullptr;
-  if ((rc = resolve_kv(&hbm, k_out, &ko)) != KV_OK) return rc;
-  if ((rc = resolve_kv(&hbm, v_out, &vo)) != KV_OK) return rc;
+  if ((rc = resolve_read(shape, &k_out, &v_out)) != KV_OK) return rc;
   int *status = status_ptr(dev);
   if (!status) return KV_ERR_CUDA;
   const cudaError_t e = launch_q8_read(
-      shape->dtype, d, block_table, context_lens, out_table, out_pages, const_cast<void *>(ko),
-      const_cast<void *>(vo), shape->batch, shape->num_kv_heads, shape->page_size,
-      shape->max_pages_per_seq, shape->num_phys_pages, status,
+      shape->dtype, d, block_table, context_lens, out_table, out_pages, k_out, v_out,
+      shape->batch, shape->num_kv_heads, shape->page_size, shape->max_pages_per_seq,
+      shape->num_phys_pages, status, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+}
+
+int kv_q4_append(const kv_shape *shape, const kv_chunk *chunk, const void *k_new,
+                 const void *v_new, const kv_q4_cache *cache, const int32_t *block_table,
+                 const int32_t *context_lens, int32_t *context_lens_out, void *stream) {
+  KV_API_RANGE();
+  int rc = check_append(shape, chunk, k_new, v_new, block_table, context_lens, context_lens_out);
+  if (rc) return rc;
+  const int dev = current_device();
+  if (dev < 0) return KV_ERR_CUDA;
+  kv_q4_cache d;
+  if ((rc = resolve_q4(shape, cache, &d)) != KV_OK) return rc;
+  int *status = status_ptr(dev);
+  if (!status) return KV_ERR_CUDA;
+  const cudaError_t e = launch_q4_append(
+      shape->dtype, k_new, v_new, d, chunk->q_start, block_table, context_lens, context_lens_out,
+      shape->batch, shape->num_kv_heads, shape->page_size, shape->max_pages_per_seq,
+      shape->num_phys_pages, chunk->total_q, chunk->max_q_len, status,
       static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+}
+
+int kv_q4_read(const kv_shape *shape, const kv_q4_cache *cache, const int32_t *block_table,
+               const int32_t *context_lens, const int32_t *out_table, int64_t out_pages,
+               void *k_out, void *v_out, void *stream) {
+  KV_API_RANGE();
+  int rc = check_read(shape, block_table, context_lens, out_table, out_pages, k_out, v_out);
+  if (rc) return rc;
+  const int dev = current_device();
+  if (dev < 0) return KV_ERR_CUDA;
+  kv_q4_cache d;
+  if ((rc = resolve_q4(shape, cache, &d)) != KV_OK) return rc;
+  if ((rc = resolve_read(shape, &k_out, &v_out)) != KV_OK) return rc;
+  int *status = status_ptr(dev);
+  if (!status) return KV_ERR_CUDA;
+  const cudaError_t e = launch_q4_read(
+      shape->dtype, d, block_table, context_lens, out_table, out_pages, k_out, v_out,
+      shape->batch, shape->num_kv_heads, shape->page_size, shape->max_pages_per_seq,
+      shape->num_phys_pages, status, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+}
+
+size_t kv_q4_chunk_workspace_bytes(const kv_shape *shape, const kv_chunk *chunk) {
+  return chunk_bytes(shape, chunk, kQ4Form);
+}
+
+int kv_q4_chunk_attn(const kv_shape *shape, const kv_chunk *chunk, const void *q,
+                     const kv_q4_cache *cache, const int32_t *block_table,
+                     const int32_t *context_lens, float scale, void *out, void *workspace,
+                     size_t workspace_bytes, void *stream) {
+  KV_API_RANGE();
+  return chunk_common(shape, chunk, q, nullptr, nullptr, nullptr, cache, kQ4Form, block_table,
+                      context_lens, scale, out, workspace, workspace_bytes, stream);
+}
+
+int kv_rope(const kv_shape *shape, const kv_chunk *chunk, const kv_rope_plan *rope, const void *q,
+            void *q_out, const void *k, void *k_out, const int32_t *context_lens, void *stream) {
+  KV_API_RANGE();
+  int rc = check_shape(shape);
+  if (rc) return rc;
+  if ((rc = check_chunk(shape, chunk)) != KV_OK) return rc;
+  if ((rc = check_rope(rope)) != KV_OK) return rc;
+  if ((!q && !k) || !q != !q_out || !k != !k_out) return KV_ERR_INVALID_ARG;
+  if (context_lens ? !al4(context_lens) : !rope->positions) return KV_ERR_INVALID_ARG;
+  const Rows rows[4] = {rows_of(shape, chunk, q, true), rows_of(shape, chunk, q_out, true),
+                        rows_of(shape, chunk, k, false), rows_of(shape, chunk, k_out, false)};
+  if (!rows_apart(rows, 4, 2)) return KV_ERR_INVALID_ARG;
+  int blocks;
+  if (!rope_grid(shape, chunk, false, 16, &blocks)) return KV_ERR_UNSUPPORTED;
+  const int dev = current_device();
+  if (dev < 0) return KV_ERR_CUDA;
+  int *status = status_ptr(dev);
+  if (!status) return KV_ERR_CUDA;
+  // (lengths that do not give the positions are not read)
+  const cudaError_t e =
+      launch_rope(shape, chunk, rope, q, q_out, k, k_out, nullptr, nullptr, nullptr,
+                  rope->positions ? nullptr : context_lens, nullptr, nullptr, status,
+                  static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+}
+
+int kv_rope_append(const kv_shape *shape, const kv_chunk *chunk, const kv_rope_plan *rope,
+                   const void *q, void *q_out, const void *k_new, const void *v_new, void *k_cache,
+                   void *v_cache, const int32_t *block_table, const int32_t *context_lens,
+                   int32_t *context_lens_out, void *minmax, void *stream) {
+  KV_API_RANGE();
+  int rc = check_append(shape, chunk, k_new, v_new, block_table, context_lens, context_lens_out);
+  if (rc) return rc;
+  if (rope && (rc = check_rope(rope)) != KV_OK) return rc;
+  if (!q != !q_out || (q && !rope) || (minmax && !al16(minmax))) return KV_ERR_INVALID_ARG;
+  const Rows rows[4] = {rows_of(shape, chunk, q, true), rows_of(shape, chunk, q_out, true),
+                        rows_of(shape, chunk, k_new, false), rows_of(shape, chunk, v_new, false)};
+  if (!rows_apart(rows, 4, 1)) return KV_ERR_INVALID_ARG;
+  int blocks;
+  if (!rope_grid(shape, chunk, true, minmax ? shape->page_size : 16, &blocks))
+    return KV_ERR_UNSUPPORTED;
+  const int dev = current_device();
+  if (dev < 0) return KV_ERR_CUDA;
+  const void *k = nullptr, *v = nullptr;
+  if ((rc = resolve_kv(shape, k_cache, &k)) != KV_OK) return rc;
+  if ((rc = resolve_kv(shape, v_cache, &v)) != KV_OK) return rc;
+  int *status = status_ptr(dev);
+  if (!status) return KV_ERR_CUDA;
+  const cudaError_t e = launch_rope(shape, chunk, rope, q, q_out, k_new, const_cast<void *>(k), v_new,
+                                    const_cast<void *>(v), block_table, context_lens,
+                                    context_lens_out, minmax, status,
+                                    static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
 }
 

@@ -77,6 +77,8 @@ cudaError_t launch_combine_lists(const float *part_o, const float *part_ml, cons
                                  const float *spa_ml, const int32_t *gmeta, float *out, int S,
                                  int B, int Hq, int Hkv, int nw, int *status, cudaStream_t st);
 
+// how a cache holds its vectors
+enum CacheForm { kOwnForm, kQ8Form, kQ4Form };
 // the chunk operators (kv_chunk.cuh): rows = packed rows per unit, ctas = the
 // shares the work is cut into
 struct ChunkArgs;
@@ -98,8 +100,9 @@ struct FewShape {
 FewShape chunk_few_shape(int dtype, bool q8);
 cudaError_t launch_chunk_few(int dtype, bool q8, const ChunkArgs &a, const CUtensorMap &tk,
                              const CUtensorMap &tv, int ctas, cudaStream_t st);
-// the pages it needs into device memory in 16 bits (table: their new block table, or null)
-cudaError_t launch_chunk_stage(int dtype, bool q8, const ChunkArgs &c, void *k_out, void *v_out,
+// the pages it needs into device memory in the shape's type (table: their new block table,
+// or null); 32 bits from the 4-bit cache only
+cudaError_t launch_chunk_stage(int dtype, CacheForm form, const ChunkArgs &c, void *k_out, void *v_out,
                                int32_t *table, cudaStream_t st);
 cudaError_t launch_chunk_combine(int dtype, const ChunkArgs &a, int ctas, bool many,
                                  cudaStream_t st);
@@ -115,5 +118,23 @@ cudaError_t launch_q8_read(int dtype, const kv_q8_cache &c, const int32_t *bt, c
                            const int32_t *out_table, long long out_pages, void *k_out,
                            void *v_out, int B, int Hkv, int ps, int maxP, long long nphys,
                            int *status, cudaStream_t st);
+
+// the 4-bit cache, likewise
+cudaError_t launch_q4_append(int dtype, const void *k_new, const void *v_new,
+                             const kv_q4_cache &c, const int32_t *q_start, const int32_t *bt,
+                             const int32_t *ctx, int32_t *ctx_out, int B, int Hkv, int ps,
+                             int maxP, long long nphys, int total_q, int max_q_len, int *status,
+                             cudaStream_t st);
+cudaError_t launch_q4_read(int dtype, const kv_q4_cache &c, const int32_t *bt, const int32_t *ctx,
+                           const int32_t *out_table, long long out_pages, void *k_out,
+                           void *v_out, int B, int Hkv, int ps, int maxP, long long nphys,
+                           int *status, cudaStream_t st);
+// rotary positions: rows of q and k (bt and v null), or the chunk append into the cache;
+// rope_grid: whether the launch's blocks count in int32 (tile: tokens a block covers)
+bool rope_grid(const kv_shape *s, const kv_chunk *c, bool paged, int tile, int *blocks);
+cudaError_t launch_rope(const kv_shape *s, const kv_chunk *c, const kv_rope_plan *rope,
+                        const void *q, void *q_out, const void *k, void *k_out, const void *v,
+                        void *v_out, const int32_t *bt, const int32_t *ctx, int32_t *ctx_out,
+                        void *mm, int *status, cudaStream_t st);
 
 }  // namespace kvs

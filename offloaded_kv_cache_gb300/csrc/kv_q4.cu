@@ -1,0 +1,227 @@
+// kv_q4.cu -- the 4-bit paged cache: chunks of new tokens quantised as they are written,
+// and pages read back into a cache of the model's own type.  (The same bytes expanded for
+// an attention that passes through the workspace: kv_q8.cu's staging.)
+//
+// 73 bytes a vector where 16-bit data takes 256: memory bounds both kernels, a decode
+// step's append the launch and two round trips.
+#include <algorithm>
+
+#include "kv_append.cuh"
+#include "kv_launch.h"
+#include "kv_q4.cuh"
+
+namespace kvs {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kLanesPerVec = 16;  // 8 channels a lane, two lanes a scale
+constexpr int kVecs = kThreads / kLanesPerVec;
+
+struct AppendArgs {
+  const void *src[2];  // K, V
+  uint8_t *codes[2], *scale[2], *power[2];
+  const int32_t *q_start, *bt, *ctx;
+  int32_t *ctx_out;
+  int *status;
+  long long nphys;
+  int Hkv, ps, ps_log2, maxP, total_q, max_q_len;
+  int blocks;  // per sequence
+  Divisor by_blocks, by_heads;
+  int write_lens;
+};
+
+// Block (b, j) walks the n_b * Hkv (token, head) pairs of its sequence, K and V of each,
+// sixteen lanes a vector.
+template <class T>
+__global__ void __launch_bounds__(kThreads) q4_append_kernel(const AppendArgs a) {
+  pdl_wait();
+  const int b = a.by_blocks(blockIdx.x), j = (int)blockIdx.x - b * a.blocks;
+  const RowSpan r = append_span(a, b);
+  const int sub = threadIdx.x / kLanesPerVec, l = threadIdx.x % kLanesPerVec;
+  const int items = r.n > 0 ? r.n * a.Hkv : 0;  // <= total_q * Hq, an int32
+  if (j == 0) {
+    const bool ok = r.n >= 0 && pages_ok(a, b, r);  // ends in a barrier when it asks
+    if (threadIdx.x == 0) {
+      if (!ok) flag_error(a.status, KV_ERR_BOUNDS);
+      if (a.write_lens) a.ctx_out[b] = ok ? r.len + r.n : r.len;
+    }
+  }
+  pdl_trigger();
+  const uint32_t mask = 0xFFFFu << (threadIdx.x & 16);
+  for (long long it = (long long)j * kVecs + sub; it < items; it += (long long)a.blocks * kVecs) {
+    const int tok = a.by_heads((int)it), h = (int)it - tok * a.Hkv, pos = r.len + tok;
+    const int ph = a.bt[(long long)b * a.maxP + (pos >> a.ps_log2)];
+    if (ph < 0 || ph >= a.nphys) continue;  // recorded by the sequence's first block
+    const long long vec = ((long long)ph * a.Hkv + h) * a.ps + (pos & (a.ps - 1));
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      float x[8];
+      load8(static_cast<const T *>(a.src[w]) + ((long long)r.q0 * a.Hkv + it) * kHeadDim + 8 * l, x);
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+      const uint32_t group = max(top, __shfl_xor_sync(mask, top, 1, kLanesPerVec));
+      top = group;
+#pragma unroll
+      for (int off = 2; off < kLanesPerVec; off <<= 1)
+        top = max(top, __shfl_xor_sync(mask, top, off, kLanesPerVec));
+      uint32_t code = 0x88888888u, scale = 0;
+      int byte = kQ4NanPower;
+      if (top < 0x7F800000u) {
+        const int e = q4_exponent(top, q8_min_exp<T>());
+        float s;
+        scale = q4_scale_code(__uint_as_float(group) * pow2f(-e), s);
+        code = q4_codes8(x, s, e, T{});
+        byte = e + 127;
+      }
+      *reinterpret_cast<uint32_t *>(a.codes[w] + vec * kQ4Bytes + 4 * l) = code;
+      if (!(l & 1)) a.scale[w][vec * kQ4Scales + l / 2] = (uint8_t)scale;
+      if (l == 0) a.power[w][vec] = (uint8_t)byte;
+    }
+  }
+}
+
+struct ReadArgs {
+  const uint8_t *codes[2], *scale[2], *power[2];
+  void *out[2];
+  const int32_t *bt, *ctx, *out_table;
+  int *status;
+  long long nphys, out_pages;
+  int Hkv, ps, ps_log2, maxP;
+  int items;   // of a sequence: (16-token tile, kv head) pairs
+  int blocks;  // per sequence
+  Divisor by_blocks, by_heads;
+};
+
+// Work item: (b, 16-token tile, kv head), a half-warp per token and lanes as above; a
+// block takes kUnits items, all loads issued before the first store.
+constexpr int kUnits = 2;
+template <class T>
+__global__ void __launch_bounds__(kThreads) q4_read_kernel(const ReadArgs a) {
+  pdl_wait();
+  const int t = threadIdx.x / kLanesPerVec, l = threadIdx.x % kLanesPerVec;
+  const int b = a.by_blocks(blockIdx.x), j = (int)blockIdx.x - b * a.blocks;
+  const int len = a.ctx[b];
+  uint32_t code[kUnits][2], scale[kUnits][2], byte[kUnits][2];
+  int dst[kUnits];  // (rows of a cache fit int32)
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) {
+    const int it = j * kUnits + u;
+    dst[u] = -1;
+    if (it >= a.items) continue;
+    const int tile = a.by_heads(it), h = it - tile * a.Hkv;
+    const int pos = tile * kTileTokens + t, page = (tile * kTileTokens) >> a.ps_log2;
+    if (len < 0 || (long long)len > (long long)a.maxP * a.ps) {
+      if (threadIdx.x == 0 && tile == 0) flag_error(a.status, KV_ERR_BOUNDS);
+      continue;
+    }
+    if (tile * kTileTokens >= len) continue;
+    const long long row = (long long)b * a.maxP + page;
+    const int src = a.bt[row], to = a.out_table[row];
+    if (to < 0) continue;
+    if (src < 0 || src >= a.nphys || to >= a.out_pages) {
+      if (threadIdx.x == 0) flag_error(a.status, KV_ERR_BOUNDS);
+      continue;
+    }
+    if (pos >= len) continue;
+    const int in = (src * a.Hkv + h) * a.ps + (pos & (a.ps - 1));
+    dst[u] = (to * a.Hkv + h) * a.ps + (pos & (a.ps - 1));
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      code[u][w] = *reinterpret_cast<const uint32_t *>(a.codes[w] + (long long)in * kQ4Bytes + 4 * l);
+      scale[u][w] = a.scale[w][(long long)in * kQ4Scales + l / 2];
+      byte[u][w] = a.power[w][in];
+    }
+  }
+  pdl_trigger();
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) {
+    if (dst[u] < 0) continue;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      float x[8];
+      q4_unpack8(code[u][w], e4m3_pair(scale[u][w]).x * q4_power(byte[u][w]), x);
+      store8(static_cast<T *>(a.out[w]) + (long long)dst[u] * kHeadDim + l * 8, x);
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_q4_append(int dtype, const void *k_new, const void *v_new,
+                             const kv_q4_cache &c, const int32_t *q_start, const int32_t *bt,
+                             const int32_t *ctx, int32_t *ctx_out, int B, int Hkv, int ps,
+                             int maxP, long long nphys, int total_q, int max_q_len, int *status,
+                             cudaStream_t st) {
+  AppendArgs a = {};
+  a.src[0] = k_new;
+  a.src[1] = v_new;
+  a.codes[0] = c.k_codes;
+  a.codes[1] = c.v_codes;
+  a.scale[0] = c.k_scale;
+  a.scale[1] = c.v_scale;
+  a.power[0] = c.k_power;
+  a.power[1] = c.v_power;
+  a.q_start = q_start;
+  a.bt = bt;
+  a.ctx = ctx;
+  a.ctx_out = ctx_out;
+  a.status = status;
+  a.nphys = nphys;
+  a.Hkv = Hkv;
+  a.ps = ps;
+  a.ps_log2 = __builtin_ctz(ps);
+  a.maxP = maxP;
+  a.total_q = total_q;
+  a.max_q_len = max_q_len;
+  const long long items = (long long)std::min(max_q_len, total_q) * Hkv;
+  const long long steps = (items + kVecs - 1) / kVecs;
+  a.blocks = (int)std::max(1LL, std::min(steps, (2432 + B - 1LL) / B));
+  a.by_blocks = Divisor::of(a.blocks);
+  a.by_heads = Divisor::of(Hkv);
+  const bool later = ctx_out == ctx && a.blocks > 1;
+  a.write_lens = ctx_out && !later;
+  const dim3 grid((unsigned)((long long)a.blocks * B)), block(kThreads);
+  cudaError_t e = dtype == KV_F32 ? launch_pdl(q4_append_kernel<float>, grid, block, 0, st, a)
+                  : dtype == KV_F16
+                      ? launch_pdl(q4_append_kernel<__half>, grid, block, 0, st, a)
+                      : launch_pdl(q4_append_kernel<__nv_bfloat16>, grid, block, 0, st, a);
+  if (e == cudaSuccess && later) e = launch_pdl(advance_kernel<AppendArgs>, dim3(B), block, 0, st, a);
+  return e;
+}
+
+cudaError_t launch_q4_read(int dtype, const kv_q4_cache &c, const int32_t *bt, const int32_t *ctx,
+                           const int32_t *out_table, long long out_pages, void *k_out,
+                           void *v_out, int B, int Hkv, int ps, int maxP, long long nphys,
+                           int *status, cudaStream_t st) {
+  ReadArgs a = {};
+  a.codes[0] = c.k_codes;
+  a.codes[1] = c.v_codes;
+  a.scale[0] = c.k_scale;
+  a.scale[1] = c.v_scale;
+  a.power[0] = c.k_power;
+  a.power[1] = c.v_power;
+  a.out[0] = k_out;
+  a.out[1] = v_out;
+  a.bt = bt;
+  a.ctx = ctx;
+  a.out_table = out_table;
+  a.status = status;
+  a.nphys = nphys;
+  a.out_pages = out_pages;
+  a.Hkv = Hkv;
+  a.ps = ps;
+  a.ps_log2 = __builtin_ctz(ps);
+  a.maxP = maxP;
+  // (the entry point has checked, by q8_grid_fits, that these count in int32)
+  a.items = (int)((long long)maxP * ps / kTileTokens * Hkv);
+  a.blocks = (a.items + kUnits - 1) / kUnits;
+  a.by_blocks = Divisor::of(a.blocks);
+  a.by_heads = Divisor::of(Hkv);
+  const dim3 grid((unsigned)((long long)a.blocks * B)), block(kThreads);
+  return dtype == KV_F32   ? launch_pdl(q4_read_kernel<float>, grid, block, 0, st, a)
+         : dtype == KV_F16 ? launch_pdl(q4_read_kernel<__half>, grid, block, 0, st, a)
+                           : launch_pdl(q4_read_kernel<__nv_bfloat16>, grid, block, 0, st, a);
+}
+
+}  // namespace kvs

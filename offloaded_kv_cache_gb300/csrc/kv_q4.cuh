@@ -1,0 +1,75 @@
+// kv_q4.cuh -- the 4-bit form of a key or value vector: integers c of 4 bits, an e4m3
+// scale s for every 16 channels, one power of two (see the header for the format).
+#pragma once
+
+#include "kv_internal.cuh"
+#include "kv_q8.cuh"
+
+namespace kvs {
+
+constexpr int kQ4Group = 16;                    // channels of a scale
+constexpr int kQ4Scales = kHeadDim / kQ4Group;  // bytes of scales a vector
+constexpr int kQ4Bytes = kHeadDim / 2;          // bytes of codes a vector
+constexpr int kQ4MaxExp = 4;                    // 7 * 448 * 2^4 = 50176: what f16 still holds
+constexpr int kQ4NanPower = 255;
+// (the least exponents are the 8-bit form's: 1 * 2^-9 * 2^-15 = 2^-24, the least f16)
+
+// The exponent of a vector whose largest magnitude has the fp32 bits `top` (finite): the
+// smallest e with top <= 3136 * 2^e = 1.53125 * 2^(e + 11).
+__device__ __forceinline__ int q4_exponent(uint32_t top, int least) {
+  const int x = (int)(top >> 23) - 127;
+  const int e = (top & 0x7FFFFFu) <= 0x440000u ? x - 11 : x - 10;
+  return min(max(e, least), kQ4MaxExp);
+}
+// two e4m3 codes -> floats
+__device__ __forceinline__ float2 e4m3_pair(uint32_t codes) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
+  return __half22float2(*reinterpret_cast<__half2 *>(&h));
+}
+// The code of the smallest s with 7 s >= top, 448 at most.  The code nearest to top / 7 is
+// that one or the one below (a quotient that rounds onto a code is one with it or above),
+// and 7 s is exact.
+__device__ __forceinline__ uint32_t q4_scale_code(float top, float &s) {
+  uint16_t c;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(0.f), "f"(top * (1.f / 7.f)));
+  uint32_t code = c & 0xFFu;
+  s = e4m3_pair(code).x;
+  if (7.f * s < top && code < 0x7Eu) s = e4m3_pair(++code).x;
+  return code;
+}
+// Eight channels as nibbles c + 8, x0 in the lowest.  t = x / (s 2^e) + 1/2 + 8 + 2^-13 +
+// 2^10 has its integer part in bits 13 .. 16.  The quotient by a rounded reciprocal is off by
+// 2^-21 at most, and t is rounded to 2^-13: a tie stays at or above it, and 16-bit data,
+// which differ from a tie (8 significant bits) by 2^-11 of it at least, 2^-12 here, stay below.
+// fp32 data may differ by less: the integer found is compared with its two borders, which
+// are exact.
+template <class T>
+__device__ __forceinline__ uint32_t q4_codes8(const float (&x)[8], float s, int e, T) {
+  const float down = pow2f(-e), f = s == 0.f ? 0.f : __frcp_rn(s) * down;
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float t = fmaf(x[i], f, 1032.5f + 0x1p-13f);
+    t = fminf(fmaxf(t, 1025.5f), 1039.5f);  // (a vector whose power is at its limit)
+    if constexpr (sizeof(T) == 4) {
+      const float c = (float)((__float_as_uint(t) >> 13) & 15u) - 8.f, y = x[i] * down;
+      if (fmaf(c, s, -0.5f * s) > y) t -= 1.f;
+      else if (s != 0.f && fmaf(c, s, 0.5f * s) <= y) t += 1.f;
+      t = fminf(fmaxf(t, 1025.5f), 1039.5f);
+    }
+    const uint32_t u = __float_as_uint(t);
+    w |= (4 * i <= 13 ? u >> (13 - 4 * i < 0 ? 0 : 13 - 4 * i) : u << (4 * i - 13 < 0 ? 0 : 4 * i - 13)) &
+         (15u << (4 * i));
+  }
+  return w;
+}
+// The factor of a vector's power byte; 255 is NaN.
+__device__ __forceinline__ float q4_power(uint32_t byte) { return q8_scale(byte); }
+// eight nibbles -> the floats c * f
+__device__ __forceinline__ void q4_unpack8(uint32_t w, float f, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = (float)((int)((w >> (4 * i)) & 15u) - 8) * f;
+}
+
+}  // namespace kvs

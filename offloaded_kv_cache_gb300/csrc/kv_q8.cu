@@ -20,8 +20,10 @@
 // link's 211 (the scales are single bytes); read back of 4 x 32768 1058 us, 211 GB/s.
 #include <algorithm>
 
+#include "kv_append.cuh"
 #include "kv_chunk.cuh"
 #include "kv_launch.h"
+#include "kv_q4.cuh"
 #include "kv_q8.cuh"
 
 namespace kvs {
@@ -45,31 +47,6 @@ struct AppendArgs {
   Divisor by_blocks, by_heads;
   int write_lens;  // this launch writes ctx_out
 };
-
-// A sequence's chunk: rows [q0, q0 + n), stored from position len on; n < 0
-// when the sequence is skipped.
-struct RowSpan {
-  int q0, n, len;
-};
-__device__ __forceinline__ RowSpan append_span(const AppendArgs &a, int b) {
-  const int q0 = a.q_start[b], q1 = a.q_start[b + 1], len = a.ctx[b];
-  const long long cap = (long long)a.maxP * a.ps;
-  const bool ok = q0 >= 0 && q1 >= q0 && q1 <= a.total_q && q1 - q0 <= a.max_q_len && len >= 0 &&
-                  len + (long long)(q1 - q0) <= cap;
-  return RowSpan{q0, ok ? q1 - q0 : -1, len};
-}
-// Whether every page the chunk touches is in range (the whole block asks).
-__device__ __forceinline__ bool pages_ok(const AppendArgs &a, int b, const RowSpan &r) {
-  bool bad = false;
-  if (r.n > 0) {
-    const int p0 = r.len / a.ps, p1 = (r.len + r.n - 1) / a.ps;
-    for (int p = p0 + (int)threadIdx.x; p <= p1; p += blockDim.x) {
-      const int ph = a.bt[(long long)b * a.maxP + p];
-      bad |= ph < 0 || ph >= a.nphys;
-    }
-  }
-  return !__syncthreads_or(bad);
-}
 
 // Block (b, j) walks the n_b * Hkv (token, head) pairs of its sequence in steps
 // of kSteps * 16, K and V of each pair, sixteen lanes a vector; the next step's
@@ -165,16 +142,6 @@ __global__ void __launch_bounds__(kThreads) q8_append_kernel(const AppendArgs a)
   }
 }
 
-// lengths of a chunk append in place, after every block has read them
-__global__ void __launch_bounds__(kThreads) advance_kernel(const AppendArgs a) {
-  pdl_wait();
-  const int b = blockIdx.x;
-  const RowSpan r = append_span(a, b);
-  const bool ok = r.n >= 0 && pages_ok(a, b, r);
-  __syncthreads();
-  if (threadIdx.x == 0 && ok) a.ctx_out[b] = r.len + r.n;
-}
-
 struct ReadArgs {
   const uint8_t *codes[2], *scale[2];  // K, V
   void *out[2];
@@ -249,11 +216,11 @@ __global__ void __launch_bounds__(kThreads) q8_read_kernel(const ReadArgs a) {
   }
 }
 
-// Pages a chunk attention needs, brought into device memory in 16 bits:
-// from the 8-bit cache, or from one in host memory.  Item and lanes as above.
+// Pages a chunk attention needs, brought into device memory in T: from the 8-bit or
+// the 4-bit cache, or from a 16-bit one in host memory.  Item and lanes as above.
 struct StageArgs {
   const void *src[2];  // K, V: 16-bit data or codes
-  const uint8_t *scale[2];
+  const uint8_t *scale[2], *group[2];  // 8-bit: scales; 4-bit: powers and scales
   void *out[2];
   const int32_t *q_start, *bt, *ctx;
   int32_t *table;  // [B][maxP] page in out, or null: the source's own page numbers
@@ -262,13 +229,13 @@ struct StageArgs {
   int Hkv, ps, ps_log2, maxP, items, blocks, total_q, max_q_len, window;
   Divisor by_blocks, by_heads;
 };
-template <class T, bool Q8>
+template <class T, CacheForm kForm>
 __global__ void __launch_bounds__(kThreads) stage_kernel(const StageArgs a) {
   pdl_wait();
   const int t = threadIdx.x / kLanesPerVec, l = threadIdx.x % kLanesPerVec;
   const int b = a.by_blocks(blockIdx.x), j = (int)blockIdx.x - b * a.blocks;
   const int q0 = a.q_start[b], q1 = a.q_start[b + 1], len = a.ctx[b];
-  uint4 data[kUnits][2];  // 16-bit data, or the codes in the first half
+  uint4 data[kUnits][2];  // 16-bit data, or the codes and what they need
   uint32_t byte[kUnits][2];
   int dst[kUnits];
 #pragma unroll
@@ -295,7 +262,12 @@ __global__ void __launch_bounds__(kThreads) stage_kernel(const StageArgs a) {
     dst[u] = a.table ? ((int)row * a.Hkv + h) * a.ps + (pos & (a.ps - 1)) : in;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-      if constexpr (Q8) {
+      if constexpr (kForm == kQ4Form) {
+        data[u][w].x = *reinterpret_cast<const uint32_t *>(
+            static_cast<const uint8_t *>(a.src[w]) + (long long)in * kQ4Bytes + l * 4);
+        data[u][w].y = a.group[w][(long long)in * kQ4Scales + l / 2];
+        byte[u][w] = a.scale[w][in];
+      } else if constexpr (kForm == kQ8Form) {
         const uint2 c = *reinterpret_cast<const uint2 *>(
             static_cast<const uint8_t *>(a.src[w]) + (long long)in * kHeadDim + l * 8);
         data[u][w] = make_uint4(c.x, c.y, 0, 0);
@@ -313,7 +285,11 @@ __global__ void __launch_bounds__(kThreads) stage_kernel(const StageArgs a) {
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
       T *to = static_cast<T *>(a.out[w]) + (long long)dst[u] * kHeadDim + l * 8;
-      if constexpr (Q8) {
+      if constexpr (kForm == kQ4Form) {
+        float x[8];
+        q4_unpack8(data[u][w].x, e4m3_pair(data[u][w].y).x * q4_power(byte[u][w]), x);
+        store8(to, x);
+      } else if constexpr (kForm == kQ8Form) {
         float lo[4], hi[4], x[8];
         q8_unpack4(data[u][w].x, lo);
         q8_unpack4(data[u][w].y, hi);
@@ -349,13 +325,15 @@ bool q8_grid_fits(int B, int maxP, int ps, int Hkv) {
   return item_grid(B, maxP, ps, Hkv, &items, &blocks);
 }
 
-cudaError_t launch_chunk_stage(int dtype, bool q8, const ChunkArgs &c, void *k_out, void *v_out,
-                               int32_t *table, cudaStream_t st) {
+cudaError_t launch_chunk_stage(int dtype, CacheForm form, const ChunkArgs &c, void *k_out,
+                               void *v_out, int32_t *table, cudaStream_t st) {
   StageArgs a = {};
   a.src[0] = c.k;
   a.src[1] = c.v;
   a.scale[0] = c.k_scale;
   a.scale[1] = c.v_scale;
+  a.group[0] = c.k_group;
+  a.group[1] = c.v_group;
   a.out[0] = k_out;
   a.out[1] = v_out;
   a.q_start = c.q_start;
@@ -376,11 +354,14 @@ cudaError_t launch_chunk_stage(int dtype, bool q8, const ChunkArgs &c, void *k_o
   a.by_blocks = Divisor::of(a.blocks);
   a.by_heads = Divisor::of(c.Hkv);
   const dim3 grid((unsigned)(a.blocks * c.B)), block(kThreads);
+  if (dtype == KV_F32) return launch_pdl(stage_kernel<float, kQ4Form>, grid, block, 0, st, a);
   if (dtype == KV_F16)
-    return q8 ? launch_pdl(stage_kernel<__half, true>, grid, block, 0, st, a)
-              : launch_pdl(stage_kernel<__half, false>, grid, block, 0, st, a);
-  return q8 ? launch_pdl(stage_kernel<__nv_bfloat16, true>, grid, block, 0, st, a)
-            : launch_pdl(stage_kernel<__nv_bfloat16, false>, grid, block, 0, st, a);
+    return form == kQ4Form   ? launch_pdl(stage_kernel<__half, kQ4Form>, grid, block, 0, st, a)
+           : form == kQ8Form ? launch_pdl(stage_kernel<__half, kQ8Form>, grid, block, 0, st, a)
+                             : launch_pdl(stage_kernel<__half, kOwnForm>, grid, block, 0, st, a);
+  return form == kQ4Form   ? launch_pdl(stage_kernel<__nv_bfloat16, kQ4Form>, grid, block, 0, st, a)
+         : form == kQ8Form ? launch_pdl(stage_kernel<__nv_bfloat16, kQ8Form>, grid, block, 0, st, a)
+                           : launch_pdl(stage_kernel<__nv_bfloat16, kOwnForm>, grid, block, 0, st, a);
 }
 
 cudaError_t launch_q8_append(int dtype, const void *k_new, const void *v_new,
@@ -422,7 +403,7 @@ cudaError_t launch_q8_append(int dtype, const void *k_new, const void *v_new,
                   : dtype == KV_F16
                       ? launch_pdl(q8_append_kernel<__half>, grid, block, 0, st, a)
                       : launch_pdl(q8_append_kernel<__nv_bfloat16>, grid, block, 0, st, a);
-  if (e == cudaSuccess && later) e = launch_pdl(advance_kernel, dim3(B), block, 0, st, a);
+  if (e == cudaSuccess && later) e = launch_pdl(advance_kernel<AppendArgs>, dim3(B), block, 0, st, a);
   return e;
 }
 

@@ -67,6 +67,18 @@ class kv_q8_cache(ctypes.Structure):
                 ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
 
 
+class kv_q4_cache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("k_power", ctypes.c_void_p), ("v_power", ctypes.c_void_p)]
+
+
+class kv_rope_plan(ctypes.Structure):
+    _fields_ = [("freq", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
 class KvError(RuntimeError):
     def __init__(self, code: int, where: str):
         super().__init__(f"{where}: {status_string(code)} ({code})")
@@ -126,6 +138,15 @@ def load(path: str = LIB_PATH):
         "kv_q8_read": (ctypes.c_int, [S, Q, P, P, P, ctypes.c_int64, P, P, P]),
         "kv_q8_chunk_workspace_bytes": (sz, [S, C]),
         "kv_q8_chunk_attn": (ctypes.c_int, [S, C, P, Q, P, P, f32, P, P, sz, P]),
+    })
+    Q4, R = ctypes.POINTER(kv_q4_cache), ctypes.POINTER(kv_rope_plan)
+    sig.update({
+        "kv_rope": (ctypes.c_int, [S, C, R, P, P, P, P, P, P]),
+        "kv_rope_append": (ctypes.c_int, [S, C, R, P, P, P, P, P, P, P, P, P, P, P]),
+        "kv_q4_append": (ctypes.c_int, [S, C, P, P, Q4, P, P, P, P]),
+        "kv_q4_read": (ctypes.c_int, [S, Q4, P, P, P, ctypes.c_int64, P, P, P]),
+        "kv_q4_chunk_workspace_bytes": (sz, [S, C]),
+        "kv_q4_chunk_attn": (ctypes.c_int, [S, C, P, Q4, P, P, f32, P, P, sz, P]),
     })
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -363,6 +384,61 @@ def kv_q8_chunk_attn(shape, chunk, q, cache, block_table, context_lens, scale, o
                                  _ptr(block_table), _ptr(context_lens), float(scale), _ptr(out),
                                  _ptr(workspace), int(workspace_bytes), _stream(stream))
     return _ret(rc, "kv_q8_chunk_attn", check)
+
+
+def make_q4_cache(k_codes, v_codes, k_scale, v_scale, k_power, v_power) -> kv_q4_cache:
+    return kv_q4_cache(_ptr(k_codes), _ptr(v_codes), _ptr(k_scale), _ptr(v_scale), _ptr(k_power),
+                       _ptr(v_power))
+
+
+def kv_q4_append(shape, chunk, k_new, v_new, cache, block_table, context_lens,
+                 context_lens_out=None, stream=None, check=True):
+    rc = load().kv_q4_append(ctypes.byref(shape), _ref(chunk), _ptr(k_new), _ptr(v_new),
+                             _ref(cache), _ptr(block_table), _ptr(context_lens),
+                             _ptr(context_lens_out), _stream(stream))
+    return _ret(rc, "kv_q4_append", check)
+
+
+def kv_q4_read(shape, cache, block_table, context_lens, out_table, out_pages, k_out, v_out,
+               stream=None, check=True):
+    rc = load().kv_q4_read(ctypes.byref(shape), _ref(cache), _ptr(block_table),
+                           _ptr(context_lens), _ptr(out_table), int(out_pages), _ptr(k_out),
+                           _ptr(v_out), _stream(stream))
+    return _ret(rc, "kv_q4_read", check)
+
+
+def kv_q4_chunk_workspace_bytes(shape, chunk) -> int:
+    return int(load().kv_q4_chunk_workspace_bytes(ctypes.byref(shape), _ref(chunk)))
+
+
+def kv_q4_chunk_attn(shape, chunk, q, cache, block_table, context_lens, scale, out, workspace,
+                     workspace_bytes, stream=None, check=True):
+    rc = load().kv_q4_chunk_attn(ctypes.byref(shape), _ref(chunk), _ptr(q), _ref(cache),
+                                 _ptr(block_table), _ptr(context_lens), float(scale), _ptr(out),
+                                 _ptr(workspace), int(workspace_bytes), _stream(stream))
+    return _ret(rc, "kv_q4_chunk_attn", check)
+
+
+def make_rope(freq, rotary_dim, interleaved=False, scale=1.0, positions=None) -> kv_rope_plan:
+    """Rotary positions: freq is a device float64 tensor [rotary_dim / 2], positions a
+    device int32 tensor [total_q] or None; both must outlive the calls."""
+    return kv_rope_plan(_ptr(freq), _ptr(positions), int(rotary_dim), int(interleaved),
+                        float(scale), 0)
+
+
+def kv_rope(shape, chunk, rope, q, q_out, k, k_out, context_lens, stream=None, check=True):
+    rc = load().kv_rope(ctypes.byref(shape), _ref(chunk), _ref(rope), _ptr(q), _ptr(q_out),
+                        _ptr(k), _ptr(k_out), _ptr(context_lens), _stream(stream))
+    return _ret(rc, "kv_rope", check)
+
+
+def kv_rope_append(shape, chunk, rope, q, q_out, k_new, v_new, k_cache, v_cache, block_table,
+                   context_lens, context_lens_out=None, minmax=None, stream=None, check=True):
+    rc = load().kv_rope_append(ctypes.byref(shape), _ref(chunk), _ref(rope), _ptr(q),
+                               _ptr(q_out), _ptr(k_new), _ptr(v_new), _ptr(k_cache),
+                               _ptr(v_cache), _ptr(block_table), _ptr(context_lens),
+                               _ptr(context_lens_out), _ptr(minmax), _stream(stream))
+    return _ret(rc, "kv_rope_append", check)
 
 
 def kv_device_status(stream=None) -> int:

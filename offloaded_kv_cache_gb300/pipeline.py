@@ -12,18 +12,24 @@ binding:
     enable_window(C), window_attn() -> kv_window_reset, kv_sparse_decode_attn_window
     dense_step()   -> kv_dense_decode_attn
     host_step()    -> kv_decode_step (host q / lengths in, out back)
+    append_chunk() -> kv_rope_append (a chunk of new tokens, q and keys turned)
     chunk_attn()   -> kv_chunk_attn (a ragged chunk of new tokens per sequence)
 
-`Q8Cache` owns a cache in 8 bits:
+`Q8Cache` and `Q4Cache` own a cache in 8 and in 4 bits:
 
-    append()       -> kv_q8_append (chunks or single tokens, quantised)
-    attend()       -> kv_q8_chunk_attn
-    read_back()    -> kv_q8_read (into a cache every other call takes)
+    append()       -> kv_q8_append, kv_q4_append (chunks or single tokens, quantised;
+                      with a Rotary, kv_rope before it)
+    attend()       -> kv_q8_chunk_attn, kv_q4_chunk_attn
+    read_back()    -> kv_q8_read, kv_q4_read (into a cache every other call takes)
+
+`Rotary` holds the frequencies of rotary positions.
 
 PyTorch is used for allocation, host<->device copies and streams only; every
 step of the computation runs in libkvsparse's kernels.
 """
 from __future__ import annotations
+
+import math
 
 import numpy as np
 import torch
@@ -88,6 +94,52 @@ def _chunk_buffers(q: torch.Tensor, out, nbytes: int, stream):
         else:
             _need(out, "out", q.shape, q.dtype)
         return out, torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+
+
+def _on(stream, device):
+    """The given stream as a context in which its temporaries are allocated."""
+    st = torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream
+    return torch.cuda.stream(st)
+
+
+class Rotary:
+    """Rotary positions of a model: which channels are paired, and how fast a pair turns.
+
+    The first rotary_dim channels turn; pairs are channels j and j + rotary_dim / 2, or
+    neighbours where interleaved.  Pair j turns by base ** (-2 j / rotary_dim) radians per
+    position.  For contexts `stretch` times the trained length `trained`: pairs that turn
+    `fast` times or more over the trained length keep their speed, those that turn `slow`
+    times or fewer are slowed by the stretch, those between in proportion (fast = slow:
+    all are slowed); the turned channels are multiplied by `scale` (None: 0.1 ln(stretch) + 1).
+    Frequencies of any other kind: freq, a tensor [rotary_dim / 2] of radians per position."""
+
+    def __init__(self, rotary_dim: int = 128, base: float = 10000.0, interleaved: bool = False,
+                 stretch: float = 1.0, trained: int = 8192, fast: float = 32.0, slow: float = 1.0,
+                 scale: float | None = None, freq: torch.Tensor | None = None,
+                 device: str = "cuda"):
+        if rotary_dim % 8 or not 8 <= rotary_dim <= 128:
+            raise ValueError(f"rotary_dim is a multiple of 8 in 8 .. 128, not {rotary_dim}")
+        if not (base > 0 and stretch >= 1 and trained > 0 and fast >= slow):
+            raise ValueError("base and trained are positive, stretch is 1 or more, fast is not "
+                             "below slow")
+        if freq is None:
+            freq = base ** (-torch.arange(0, rotary_dim, 2, dtype=torch.float64) / rotary_dim)
+            if stretch > 1:
+                turns = freq * trained / (2 * math.pi)
+                keep = ((turns - slow) / (fast - slow)).clamp(0, 1) if fast > slow else 0.0
+                freq = freq * (keep + (1 - keep) / stretch)
+        if tuple(freq.shape) != (rotary_dim // 2,):
+            raise ValueError(f"freq: [{rotary_dim // 2}] is needed, not {list(freq.shape)}")
+        self.rotary_dim, self.interleaved = rotary_dim, bool(interleaved)
+        self.freq = freq.to(device=device, dtype=torch.float64).contiguous()
+        self.scale = scale if scale is not None else 0.1 * math.log(stretch) + 1
+
+    def plan(self, total: int, positions: torch.Tensor | None = None) -> kv.kv_rope_plan:
+        """The plan of a call over `total` rows; positions: [total] int32 on the device."""
+        _need(self.freq, "freq", (self.rotary_dim // 2,), torch.float64)
+        if positions is not None:
+            _need(positions, "positions", (total,), torch.int32)
+        return kv.make_rope(self.freq, self.rotary_dim, self.interleaved, self.scale, positions)
 
 
 class DecodeLayer:
@@ -307,6 +359,32 @@ class DecodeLayer:
                          self.context_lens, self.scale, out, space, space.numel(), stream)
         return out
 
+    def append_chunk(self, k_new: torch.Tensor, v_new: torch.Tensor, q_start: torch.Tensor,
+                     max_q_len: int, rotary: Rotary | None = None, q: torch.Tensor | None = None,
+                     positions: torch.Tensor | None = None, advance: bool = True,
+                     update_index: bool = True, stream=None) -> torch.Tensor | None:
+        """Append a ragged chunk (k_new, v_new: [total_q][Hkv][d] on the device), keys
+        turned to their positions by `rotary`; returns q [total_q][Hq][d] turned, if given.
+
+        positions: [total_q] int32 where they are not the cache's own.  advance and
+        update_index as in append()."""
+        stream = self._st(stream)
+        _chunk_inputs(self, q_start, self.shape.num_kv_heads, k_new=k_new, v_new=v_new)
+        total, out = k_new.shape[0], None
+        if rotary is None and (q is not None or positions is not None):
+            raise ValueError("q and positions go with a rotary")
+        if q is not None:
+            _need(q, "q", (total, self.shape.num_q_heads, self.shape.head_dim), k_new.dtype)
+            with _on(stream, q.device):
+                out = torch.empty_like(q)
+        chunk = kv.make_chunk(q_start, total, max_q_len)
+        plan = rotary.plan(total, positions) if rotary is not None else None
+        kv.kv_rope_append(self.shape, chunk, plan, q, out, k_new, v_new, self.k_cache, self.v_cache,
+                          self.block_table, self.context_lens,
+                          self.context_lens if advance else None,
+                          self.minmax if update_index else None, stream)
+        return out
+
     # --- host views --------------------------------------------------------
     def minmax_bits(self) -> np.ndarray:
         return torch_to_bits(self.minmax)
@@ -315,13 +393,13 @@ class DecodeLayer:
         return torch_to_bits(self.mean)
 
 
-class Q8Cache:
-    """A paged cache held in 8 bits, in device memory or (kv_loc = "host") pinned
-    host memory, with the block table and lengths of its sequences.
+class _PackedCache:
+    """What Q8Cache and Q4Cache share: the calls, named by `bits`."""
 
-    shape: the kv_shape of the sequences (dtype = the model's); its kv_loc is
-    replaced by this cache's.  block_table [B][maxP] and context_lens [B] are int32
-    tensors on the device, kept and not copied; every call looks at them again."""
+    bits = ""  # "q8" or "q4"
+
+    def _call(self, name: str):
+        return getattr(kv, f"kv_{self.bits}_{name}")
 
     def __init__(self, shape: kv.kv_shape, block_table: torch.Tensor, context_lens: torch.Tensor,
                  kv_loc: str = "hbm", device: str = "cuda"):
@@ -330,22 +408,39 @@ class Q8Cache:
         self.device = torch.device(device)
         self.block_table, self.context_lens = block_table, context_lens
         s = self.shape
-        rows = (s.num_phys_pages, s.num_kv_heads, s.page_size)
-        where = dict(pin_memory=True) if kv_loc == "host" else dict(device=self.device)
-        self.k_codes, self.v_codes = (torch.zeros((*rows, s.head_dim), dtype=torch.uint8, **where)
-                                      for _ in range(2))
-        self.k_scale, self.v_scale = (torch.zeros(rows, dtype=torch.uint8, **where)
-                                      for _ in range(2))
-        self.cache = kv.make_q8_cache(self.k_codes, self.v_codes, self.k_scale, self.v_scale)
+        self._rows = (s.num_phys_pages, s.num_kv_heads, s.page_size)
+        self._where = dict(pin_memory=True) if kv_loc == "host" else dict(device=self.device)
+
+    def _pair(self, *row: int):
+        """Zeroed byte arrays of keys and values, `row` bytes a vector."""
+        return (torch.zeros((*self._rows, *row), dtype=torch.uint8, **self._where)
+                for _ in range(2))
 
     def append(self, k_new: torch.Tensor, v_new: torch.Tensor, q_start: torch.Tensor,
-               max_q_len: int, stream=None):
+               max_q_len: int, stream=None, rotary: Rotary | None = None,
+               q: torch.Tensor | None = None, positions: torch.Tensor | None = None):
         """Quantise and store the new tokens (k_new, v_new: [total_q][Hkv][d]) behind
-        each sequence's cached ones; context_lens grows in place."""
+        each sequence's cached ones; context_lens grows in place.  With a rotary, keys
+        are turned to their positions first, and so is q [total_q][Hq][d], which is then
+        returned."""
+        stream = DecodeLayer._st(stream)
         _chunk_inputs(self, q_start, self.shape.num_kv_heads, k_new=k_new, v_new=v_new)
-        chunk = kv.make_chunk(q_start, k_new.shape[0], max_q_len)
-        kv.kv_q8_append(self.shape, chunk, k_new, v_new, self.cache, self.block_table,
-                        self.context_lens, self.context_lens, DecodeLayer._st(stream))
+        if rotary is None and (q is not None or positions is not None):
+            raise ValueError("q and positions go with a rotary")
+        total, out = k_new.shape[0], None
+        if q is not None:
+            _need(q, "q", (total, self.shape.num_q_heads, self.shape.head_dim), k_new.dtype)
+        chunk = kv.make_chunk(q_start, total, max_q_len)
+        if rotary is not None:
+            plan = rotary.plan(total, positions)
+            with _on(stream, k_new.device):
+                turned = torch.empty_like(k_new)
+                out = None if q is None else torch.empty_like(q)
+            kv.kv_rope(self.shape, chunk, plan, q, out, k_new, turned, self.context_lens, stream)
+            k_new = turned
+        self._call("append")(self.shape, chunk, k_new, v_new, self.cache, self.block_table,
+                             self.context_lens, self.context_lens, stream)
+        return out
 
     def attend(self, q: torch.Tensor, q_start: torch.Tensor, max_q_len: int, scale: float,
                window: int = 0, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -353,10 +448,10 @@ class Q8Cache:
         stream = DecodeLayer._st(stream)
         _chunk_inputs(self, q_start, self.shape.num_q_heads, q=q)
         chunk = kv.make_chunk(q_start, q.shape[0], max_q_len, window)
-        out, space = _chunk_buffers(q, out, kv.kv_q8_chunk_workspace_bytes(self.shape, chunk),
+        out, space = _chunk_buffers(q, out, self._call("chunk_workspace_bytes")(self.shape, chunk),
                                     stream)
-        kv.kv_q8_chunk_attn(self.shape, chunk, q, self.cache, self.block_table, self.context_lens,
-                            scale, out, space, space.numel(), stream)
+        self._call("chunk_attn")(self.shape, chunk, q, self.cache, self.block_table,
+                                 self.context_lens, scale, out, space, space.numel(), stream)
         return out
 
     def read_back(self, k_out: torch.Tensor, v_out: torch.Tensor,
@@ -372,5 +467,38 @@ class Q8Cache:
         if out_table is not None:
             table = out_table
             _need(table, "out_table", (s.batch, s.max_pages_per_seq), torch.int32)
-        kv.kv_q8_read(self.shape, self.cache, self.block_table, self.context_lens, table,
-                      k_out.shape[0], k_out, v_out, DecodeLayer._st(stream))
+        self._call("read")(self.shape, self.cache, self.block_table, self.context_lens, table,
+                           k_out.shape[0], k_out, v_out, DecodeLayer._st(stream))
+
+
+class Q8Cache(_PackedCache):
+    """A paged cache held in 8 bits, in device memory or (kv_loc = "host") pinned
+    host memory, with the block table and lengths of its sequences.
+
+    shape: the kv_shape of the sequences (dtype = the model's); its kv_loc is
+    replaced by this cache's.  block_table [B][maxP] and context_lens [B] are int32
+    tensors on the device, kept and not copied; every call looks at them again."""
+
+    bits = "q8"
+
+    def __init__(self, shape: kv.kv_shape, block_table: torch.Tensor, context_lens: torch.Tensor,
+                 kv_loc: str = "hbm", device: str = "cuda"):
+        super().__init__(shape, block_table, context_lens, kv_loc, device)
+        self.k_codes, self.v_codes = self._pair(self.shape.head_dim)
+        self.k_scale, self.v_scale = self._pair()
+        self.cache = kv.make_q8_cache(self.k_codes, self.v_codes, self.k_scale, self.v_scale)
+
+
+class Q4Cache(_PackedCache):
+    """Q8Cache in 4 bits: 73 bytes a vector instead of 129."""
+
+    bits = "q4"
+
+    def __init__(self, shape: kv.kv_shape, block_table: torch.Tensor, context_lens: torch.Tensor,
+                 kv_loc: str = "hbm", device: str = "cuda"):
+        super().__init__(shape, block_table, context_lens, kv_loc, device)
+        self.k_codes, self.v_codes = self._pair(self.shape.head_dim // 2)
+        self.k_scale, self.v_scale = self._pair(self.shape.head_dim // 16)
+        self.k_power, self.v_power = self._pair()
+        self.cache = kv.make_q4_cache(self.k_codes, self.v_codes, self.k_scale, self.v_scale,
+                                      self.k_power, self.v_power)
