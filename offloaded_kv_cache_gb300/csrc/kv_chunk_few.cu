@@ -47,6 +47,7 @@
 
 #include "kv_chunk.cuh"
 #include "kv_launch.h"
+#include "kv_q4.cuh"
 #include "kv_q8.cuh"
 #include "kv_umma.cuh"
 
@@ -58,27 +59,30 @@ constexpr float kBias = 7.f;    // ... times 2^7 for f16, so that small weights 
 
 constexpr int kRows = 8;  // rows of a unit
 
-template <class T, bool Q8> struct Shape {
+template <class T, CacheForm kForm> struct Shape {
+  static constexpr bool kQ4 = kForm == kQ4Form, kCodes = kForm != kOwnForm;
   static constexpr int kConsumers = 4;
   static constexpr int kThreads = 32 * (kConsumers + 1);
   static constexpr int kTile = 16 * kConsumers;  // tokens per stage
-  static constexpr int kRowBytes = kHeadDim * (Q8 ? 1 : 2);
-  static constexpr int kSlabs = kRowBytes / 128;
+  static constexpr int kRowBytes = kQ4 ? kQ4Bytes : kHeadDim * (kCodes ? 1 : 2);
+  static constexpr int kSlabs = kCodes ? 1 : 2;
   static constexpr int kBytes = kTile * kRowBytes;  // of K or V
-  static constexpr int kStages = Q8 ? 5 : 3;
+  static constexpr int kStages = kQ4 ? 8 : kCodes ? 5 : 3;
   static constexpr int kCtas = sizeof(T) == 2 ? 2 : 1;  // per SM
 };
 
-template <class T, bool Q8> struct Shared {
-  using Sh = Shape<T, Q8>;
-  alignas(1024) uint8_t kv[Sh::kStages][2][Sh::kBytes];  // slabs of [token][128 bytes]
+template <class T, CacheForm kForm> struct Shared {
+  using Sh = Shape<T, kForm>;
+  // slabs of [token][128 bytes]; 4-bit: [token][64 bytes]
+  alignas(1024) uint8_t kv[Sh::kStages][2][Sh::kBytes];
   float o[Sh::kConsumers][kRows][kHeadDim];          // per warp, at the end of a segment
   float m[Sh::kConsumers][kRows], r[Sh::kConsumers][kRows], l[Sh::kConsumers][kRows];
-  alignas(16) uint8_t scale[Sh::kStages][2][Q8 ? Sh::kTile : 16];
+  alignas(16) uint8_t scale[Sh::kStages][2][Sh::kCodes ? Sh::kTile : 16];  // 4-bit: powers
+  alignas(16) uint8_t group[Sh::kQ4 ? Sh::kStages : 1][2][Sh::kQ4 ? Sh::kTile * kQ4Scales : 16];
   uint64_t full[Sh::kStages], empty[Sh::kStages], joined, read;
   int tokens[Sh::kStages];  // per stage: bit i: the pages of tokens 16 i .. + 15 are in range
   int abort, pad;
-  ChunkShare<Q8 ? 8 : 4> share;
+  ChunkShare<Sh::kCodes ? 8 : 4> share;
   int red[32];
 };
 
@@ -122,11 +126,31 @@ __device__ __forceinline__ uint32_t f16_hi(uint32_t w) {
   return x;
 }
 
-template <class T, bool Q8>
-__global__ void __launch_bounds__(Shape<T, Q8>::kThreads, Shape<T, Q8>::kCtas)
+// The integers n = c + 8 of nibbles i and i + 4 of a word, i < 4, times their scales: n is
+// put into the bits of 64 + n, and (64 + n) s - 72 s is exact (72 s has 8 significant bits).
+// s: the scales of the two, s72 = -72 s.
+template <int i> __device__ __forceinline__ uint32_t q4_pair(uint32_t w, uint32_t s, uint32_t s72) {
+  const uint32_t n = ((i == 0 ? w << 4 : w >> (4 * i - 4)) & 0x00F000F0u) | 0x54005400u;
+  uint32_t x;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(x) : "r"(n), "r"(s), "r"(s72));
+  return x;
+}
+__device__ __forceinline__ uint32_t times_m72(uint32_t s) {
+  uint32_t x;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(x) : "r"(s), "r"(0xD480D480u));
+  return x;
+}
+// Which of the first eight tokens of a warp's sixteen a row of its products is (and of the
+// last eight): with 64-byte rows under the 64-byte swizzle, rows in this order meet distinct
+// banks both as K's 16-byte and as V's 8-byte reads.
+__device__ __forceinline__ int q4_token(int row) { return (0x65742130u >> (4 * row)) & 7; }
+
+template <class T, CacheForm kForm>
+__global__ void __launch_bounds__(Shape<T, kForm>::kThreads, Shape<T, kForm>::kCtas)
     chunk_few_kernel(const __grid_constant__ ChunkArgs a, const __grid_constant__ CUtensorMap tk,
                      const __grid_constant__ CUtensorMap tv) {
-  using Sh = Shape<T, Q8>;
+  using Sh = Shape<T, kForm>;
+  constexpr bool Q8 = Sh::kCodes, Q4 = Sh::kQ4;  // 8 bits or 4; 4
   constexpr int kConsumers = Sh::kConsumers, kTile = Sh::kTile, kStages = Sh::kStages;
   constexpr int kSlab = kTile * 128;
   using M = typename std::conditional<Q8, __half, T>::type;  // what the products take
@@ -134,7 +158,7 @@ __global__ void __launch_bounds__(Shape<T, Q8>::kThreads, Shape<T, Q8>::kCtas)
   constexpr int kTerms = kTwo ? 2 : 1;
   constexpr float kShift = std::is_same<M, __half>::value ? kBias : 0.f;
   extern __shared__ __align__(1024) uint8_t smem[];
-  Shared<T, Q8> &sh = *reinterpret_cast<Shared<T, Q8> *>(smem);
+  Shared<T, kForm> &sh = *reinterpret_cast<Shared<T, kForm> *>(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (smem_u32(smem) & 1023u) {  // the swizzled tiles need it
     if (tid == 0) flag_error(a.status, KV_ERR_INVALID_ARG);
@@ -205,18 +229,23 @@ __global__ void __launch_bounds__(Shape<T, Q8>::kThreads, Shape<T, Q8>::kCtas)
           const uint32_t bar = smem_u32(&sh.full[ring.s]);
           if (lane == 0) {
             sh.tokens[ring.s] = (int)all;
-            mbar_arrive_expect_tx(bar, 2 * Sh::kBytes + (Q8 ? 2 * have * pt : 0));
+            mbar_arrive_expect_tx(bar, 2 * Sh::kBytes + (Q4   ? 2 * have * pt * (1 + kQ4Scales)
+                                                    : Q8 ? 2 * have * pt
+                                                         : 0));
           }
           __syncwarp();
           if (lane < npg) {
             for (int w = 0; w < 2; ++w) {
-              const uint32_t dst = smem_u32(&sh.kv[ring.s][w][lane * pt * 128]);
+              const uint32_t dst = smem_u32(&sh.kv[ring.s][w][lane * pt * (Q4 ? kQ4Bytes : 128)]);
 #pragma unroll
               for (int slab = 0; slab < Sh::kSlabs; ++slab)
                 tma_load_2d(dst + slab * kSlab, w ? &tv : &tk, 64 * slab, y, bar);
               if (Q8 && ok)
                 bulk_load(smem_u32(&sh.scale[ring.s][w][lane * pt]), (w ? a.v_scale : a.k_scale) + y,
                           pt, bar);
+              if (Q4 && ok)
+                bulk_load(smem_u32(&sh.group[ring.s][w][lane * pt * kQ4Scales]),
+                          (w ? a.v_group : a.k_group) + (long long)y * kQ4Scales, pt * kQ4Scales, bar);
             }
           }
         }
@@ -231,6 +260,7 @@ __global__ void __launch_bounds__(Shape<T, Q8>::kThreads, Shape<T, Q8>::kCtas)
   } else {
     // ----------------------------------------------------------- consumers
     const int g8 = lane >> 2, t4 = lane & 3;  // row and column group of the fragments
+    const int tg = Q4 ? q4_token(g8) : g8;    // the token of row g8 (and + 8)
     uint32_t join_ph = 0;
     while (next_list(true)) {
       bool live = true;
@@ -271,10 +301,12 @@ __global__ void __launch_bounds__(Shape<T, Q8>::kThreads, Shape<T, Q8>::kCtas)
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          q[0][i] = pack2(x[2 * i], x[2 * i + 1], M{});
+          // 4-bit: the pairs that a word's nibbles make
+          const int lo = Q4 ? 8 * (i >> 2) + (i & 3) : 2 * i, hi = Q4 ? lo + 4 : lo + 1;
+          q[0][i] = pack2(x[lo], x[hi], M{});
           if constexpr (kTwo) {
             const float2 h = unpack2(q[0][i], M{});
-            q[1][i] = pack2(x[2 * i] - h.x, x[2 * i + 1] - h.y, M{});
+            q[1][i] = pack2(x[lo] - h.x, x[hi] - h.y, M{});
           }
         }
 #pragma unroll
@@ -298,13 +330,40 @@ __global__ void __launch_bounds__(Shape<T, Q8>::kThreads, Shape<T, Q8>::kCtas)
             break;
           }
           const int tok0 = tile * kTile + warp * 16;
-          const uint8_t *kc = sh.kv[ring.s][0] + warp * 16 * 128;
-          const uint8_t *vc = sh.kv[ring.s][1] + warp * 16 * 128;
+          const uint8_t *kc = sh.kv[ring.s][0] + warp * 16 * (Q4 ? kQ4Bytes : 128);
+          const uint8_t *vc = sh.kv[ring.s][1] + warp * 16 * (Q4 ? kQ4Bytes : 128);
           const bool pages = (sh.tokens[ring.s] >> warp) & 1;
-          // S^T: tokens g8 and g8 + 8
+          // S^T: tokens tg and tg + 8
           float s[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) s[i] = 0.f;
+          if constexpr (Q4) {
+            const int at = tg * kQ4Bytes + ((t4 ^ ((tg >> 1) & 3)) << 4);
+            const uint4 u = *reinterpret_cast<const uint4 *>(kc + at);
+            const uint4 v = *reinterpret_cast<const uint4 *>(kc + at + 8 * kQ4Bytes);
+            const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
+            const uint8_t *gc = sh.group[ring.s][0] + (warp * 16 + tg) * kQ4Scales + 2 * t4;
+            uint32_t gs[2];  // two scales of token tg, of token tg + 8
+            gs[0] = f16_lo(*reinterpret_cast<const uint16_t *>(gc));
+            gs[1] = f16_lo(*reinterpret_cast<const uint16_t *>(gc + 8 * kQ4Scales));
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {  // 16 channels, two words
+              const uint32_t s0 = __byte_perm(gs[0], 0, c ? 0x3232 : 0x1010), m0 = times_m72(s0);
+              const uint32_t s1 = __byte_perm(gs[1], 0, c ? 0x3232 : 0x1010), m1 = times_m72(s1);
+#pragma unroll
+              for (int j = 2 * c; j < 2 * c + 2; ++j) {
+                const uint32_t a0 = q4_pair<0>(uu[j], s0, m0), a1 = q4_pair<0>(vv[j], s1, m1);
+                const uint32_t a2 = q4_pair<1>(uu[j], s0, m0), a3 = q4_pair<1>(vv[j], s1, m1);
+                const uint32_t b0 = q4_pair<2>(uu[j], s0, m0), b1 = q4_pair<2>(vv[j], s1, m1);
+                const uint32_t b2 = q4_pair<3>(uu[j], s0, m0), b3 = q4_pair<3>(vv[j], s1, m1);
+#pragma unroll
+                for (int e = kTerms - 1; e >= 0; --e) {  // the small term first
+                  mma16816(s, a0, a1, a2, a3, q[e][4 * j], q[e][4 * j + 1], M{});
+                  mma16816(s, b0, b1, b2, b3, q[e][4 * j + 2], q[e][4 * j + 3], M{});
+                }
+              }
+            }
+          } else {
 #pragma unroll
           for (int c = 0; c < (Q8 ? 2 : 4); ++c) {
             const int at = (c >> 1) * kSlab + g8 * 128 + (((2 * t4 + (c & 1)) ^ g8) << 4);
@@ -327,18 +386,19 @@ __global__ void __launch_bounds__(Shape<T, Q8>::kThreads, Shape<T, Q8>::kCtas)
                 mma16816(s, a0, a1, a2, a3, q[e][k], q[e][k + 1], M{});
             }
           }
-          // tokens this thread's lane speaks for: g8 + 8 i
+          }
+          // tokens this thread's lane speaks for: tg + 8 i
           bool token[2], vbad[2];
           float kf[2], ev[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            token[i] = pages && tok0 + g8 + 8 * i < g.len;
+            token[i] = pages && tok0 + tg + 8 * i < g.len;
             vbad[i] = !token[i];
             kf[i] = 1.f;
             ev[i] = 0.f;
             if constexpr (Q8) {
-              const uint32_t kb = sh.scale[ring.s][0][warp * 16 + g8 + 8 * i];
-              const uint32_t vb = sh.scale[ring.s][1][warp * 16 + g8 + 8 * i];
+              const uint32_t kb = sh.scale[ring.s][0][warp * 16 + tg + 8 * i];
+              const uint32_t vb = sh.scale[ring.s][1][warp * 16 + tg + 8 * i];
               vbad[i] |= vb == (uint32_t)kQ8NanScale;
               kf[i] = q8_scale(kb);
               ev[i] = vb == (uint32_t)kQ8NanScale ? __uint_as_float(0x7FC00000u)
@@ -348,12 +408,12 @@ __global__ void __launch_bounds__(Shape<T, Q8>::kThreads, Shape<T, Q8>::kCtas)
           const uint32_t bad0 = __ballot_sync(0xFFFFFFFFu, vbad[0]);
           const uint32_t bad1 = __ballot_sync(0xFFFFFFFFu, vbad[1]);
           uint32_t p[kTerms][2];
-          float z[4], y[4];  // element i: token g8 + 8 (i >> 1), row 2 t4 + (i & 1)
+          float z[4], y[4];  // element i: token tg + 8 (i >> 1), row 2 t4 + (i & 1)
           bool move = false;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int k = i >> 1, h = i & 1;
-            const int pos = tok0 + g8 + 8 * k;
+            const int pos = tok0 + tg + 8 * k;
             const bool see = token[k] && pos <= tq[h] &&
                              (a.window <= 0 || pos - tq[h] > -a.window);
             z[i] = see ? s[i] * (kf[k] * qf[h]) : -INFINITY;
@@ -404,6 +464,45 @@ __global__ void __launch_bounds__(Shape<T, Q8>::kThreads, Shape<T, Q8>::kCtas)
           }
           // O^T: tokens 2 t4, 2 t4 + 1 (+ 8); channels 16 g8 .. + 15 of codes, 8 g8
           // .. + 7 of both slabs of 16-bit data
+          if constexpr (Q4) {
+            uint2 v2[4];
+            uint32_t sb[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int row = 2 * t4 + (i & 1), tok = q4_token(row) + 8 * (i >> 1);
+              v2[i] = *reinterpret_cast<const uint2 *>(
+                  vc + tok * kQ4Bytes + (((g8 >> 1) ^ ((tok >> 1) & 3)) << 4) + 8 * (g8 & 1));
+              sb[i] = sh.group[ring.s][1][(warp * 16 + tok) * kQ4Scales + g8];
+              // (as below: a scale of 0 clears the vector)
+              if ((bad0 | bad1) && (((i >> 1 ? bad1 : bad0) >> (4 * row)) & 1)) sb[i] = 0;
+            }
+            const uint32_t s0 = f16_lo(sb[0] | (sb[1] << 8)), m0 = times_m72(s0);
+            const uint32_t s1 = f16_lo(sb[2] | (sb[3] << 8)), m1 = times_m72(s1);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {  // four channels: block d of O^T has two
+              const uint32_t u = __byte_perm(c < 2 ? v2[0].x : v2[0].y, c < 2 ? v2[1].x : v2[1].y,
+                                             c & 1 ? 0x7632 : 0x5410);
+              const uint32_t w = __byte_perm(c < 2 ? v2[2].x : v2[2].y, c < 2 ? v2[3].x : v2[3].y,
+                                             c & 1 ? 0x7632 : 0x5410);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t a0 = h ? q4_pair<2>(u, s0, m0) : q4_pair<0>(u, s0, m0);
+                const uint32_t a1 = h ? q4_pair<3>(u, s0, m0) : q4_pair<1>(u, s0, m0);
+                const uint32_t a2 = h ? q4_pair<2>(w, s1, m1) : q4_pair<0>(w, s1, m1);
+                const uint32_t a3 = h ? q4_pair<3>(w, s1, m1) : q4_pair<1>(w, s1, m1);
+                const int d = 2 * c + h;
+                if constexpr (kTwo) {
+                  float t[4] = {0.f, 0.f, 0.f, 0.f};
+                  mma16816(t, a0, a1, a2, a3, p[1][0], p[1][1], M{});
+                  mma16816(t, a0, a1, a2, a3, p[0][0], p[0][1], M{});
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) o[d][i] += t[i];
+                } else {
+                  mma16816(o[d], a0, a1, a2, a3, p[0][0], p[0][1], M{});
+                }
+              }
+            }
+          } else {
           uint4 v4[Sh::kSlabs][4];
 #pragma unroll
           for (int c = 0; c < Sh::kSlabs; ++c)
@@ -500,6 +599,7 @@ __global__ void __launch_bounds__(Shape<T, Q8>::kThreads, Shape<T, Q8>::kCtas)
               mma16816(o[d], a0, a1, a2, a3, p[0][0], p[0][1], M{});
             }
           }
+          }
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sh.empty[ring.s]));
         }
@@ -590,38 +690,43 @@ __global__ void __launch_bounds__(Shape<T, Q8>::kThreads, Shape<T, Q8>::kCtas)
     flag_error(a.status, KV_ERR_DEVICE_TIMEOUT);
 }
 
-template <class T, bool Q8>
+template <class T, CacheForm kForm>
 cudaError_t few_go(const ChunkArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
                    cudaStream_t st) {
-  using Sh = Shape<T, Q8>;
-  constexpr int bytes = (int)sizeof(Shared<T, Q8>);
+  using Sh = Shape<T, kForm>;
+  constexpr int bytes = (int)sizeof(Shared<T, kForm>);
   static_assert(bytes <= (Sh::kCtas == 2 ? 113 : 227) * 1024, "shared memory");
   const cudaError_t e = cudaFuncSetAttribute(
-      chunk_few_kernel<T, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+      chunk_few_kernel<T, kForm>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  return launch_pdl(chunk_few_kernel<T, Q8>, dim3(ctas), dim3(Sh::kThreads), bytes, st, a, tk,
+  return launch_pdl(chunk_few_kernel<T, kForm>, dim3(ctas), dim3(Sh::kThreads), bytes, st, a, tk,
                     tv);
 }
+template <class T>
+cudaError_t few_type(CacheForm form, const ChunkArgs &a, const CUtensorMap &tk,
+                     const CUtensorMap &tv, int ctas, cudaStream_t st) {
+  return form == kQ4Form   ? few_go<T, kQ4Form>(a, tk, tv, ctas, st)
+         : form == kQ8Form ? few_go<T, kQ8Form>(a, tk, tv, ctas, st)
+                           : few_go<T, kOwnForm>(a, tk, tv, ctas, st);
+}
+template <class Sh> FewShape few_shape() { return FewShape{kRows, Sh::kTile, Sh::kCtas}; }
 
 }  // namespace
 
-FewShape chunk_few_shape(int dtype, bool q8) {
-  using Own = Shape<__half, false>;
-  using Codes = Shape<__half, true>;
-  using Codes32 = Shape<float, true>;
-  return !q8                ? FewShape{kRows, Own::kTile, Own::kCtas}
-         : dtype == KV_F32 ? FewShape{kRows, Codes32::kTile, Codes32::kCtas}
-                           : FewShape{kRows, Codes::kTile, Codes::kCtas};
+FewShape chunk_few_shape(int dtype, CacheForm form) {
+  if (form == kOwnForm) return few_shape<Shape<__half, kOwnForm>>();
+  if (form == kQ4Form)
+    return dtype == KV_F32 ? few_shape<Shape<float, kQ4Form>>() : few_shape<Shape<__half, kQ4Form>>();
+  return dtype == KV_F32 ? few_shape<Shape<float, kQ8Form>>() : few_shape<Shape<__half, kQ8Form>>();
 }
 
-cudaError_t launch_chunk_few(int dtype, bool q8, const ChunkArgs &a, const CUtensorMap &tk,
+cudaError_t launch_chunk_few(int dtype, CacheForm form, const ChunkArgs &a, const CUtensorMap &tk,
                              const CUtensorMap &tv, int ctas, cudaStream_t st) {
-  if (dtype == KV_F32) return few_go<float, true>(a, tk, tv, ctas, st);
-  if (dtype == KV_F16)
-    return q8 ? few_go<__half, true>(a, tk, tv, ctas, st)
-              : few_go<__half, false>(a, tk, tv, ctas, st);
-  return q8 ? few_go<__nv_bfloat16, true>(a, tk, tv, ctas, st)
-            : few_go<__nv_bfloat16, false>(a, tk, tv, ctas, st);
+  if (dtype == KV_F32)
+    return form == kQ4Form ? few_go<float, kQ4Form>(a, tk, tv, ctas, st)
+                           : few_go<float, kQ8Form>(a, tk, tv, ctas, st);
+  return dtype == KV_F16 ? few_type<__half>(form, a, tk, tv, ctas, st)
+                         : few_type<__nv_bfloat16>(form, a, tk, tv, ctas, st);
 }
 
 }  // namespace kvs
