@@ -63,12 +63,13 @@ template <class T, CacheForm kForm> struct Shape {
   static constexpr bool kQ4 = kForm == kQ4Form, kCodes = kForm != kOwnForm;
   static constexpr int kConsumers = 4;
   static constexpr int kThreads = 32 * (kConsumers + 1);
-  static constexpr int kTile = 16 * kConsumers;  // tokens per stage
+  static constexpr int kSteps = kQ4 ? 2 : 1;            // of 16 tokens that a warp takes of a stage
+  static constexpr int kTile = 16 * kSteps * kConsumers;  // tokens per stage
   static constexpr int kRowBytes = kQ4 ? kQ4Bytes : kHeadDim * (kCodes ? 1 : 2);
   static constexpr int kSlabs = kCodes ? 1 : 2;
   static constexpr int kBytes = kTile * kRowBytes;  // of K or V
-  static constexpr int kStages = kQ4 ? 8 : kCodes ? 5 : 3;
-  static constexpr int kCtas = sizeof(T) == 2 ? 2 : 1;  // per SM
+  static constexpr int kStages = kQ4 ? 3 : kCodes ? 5 : 3;
+  static constexpr int kCtas = sizeof(T) != 2 ? 1 : kQ4 ? 3 : 2;  // per SM
 };
 
 template <class T, CacheForm kForm> struct Shared {
@@ -126,19 +127,20 @@ __device__ __forceinline__ uint32_t f16_hi(uint32_t w) {
   return x;
 }
 
-// The integers n = c + 8 of nibbles i and i + 4 of a word, i < 4, times their scales: n is
-// put into the bits of 64 + n, and (64 + n) s - 72 s is exact (72 s has 8 significant bits).
-// s: the scales of the two, s72 = -72 s.
-template <int i> __device__ __forceinline__ uint32_t q4_pair(uint32_t w, uint32_t s, uint32_t s72) {
-  const uint32_t n = ((i == 0 ? w << 4 : w >> (4 * i - 4)) & 0x00F000F0u) | 0x54005400u;
-  uint32_t x;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(x) : "r"(n), "r"(s), "r"(s72));
-  return x;
+// The integers n = c + 8 of the low (odd: high) nibbles of bytes 0 and 2 of a word, less 8,
+// times their scales s: n is put into the mantissa of 64 + n, and (64 + n) s - 72 s, in one
+// fma, is exact (72 s has 8 significant bits, at most 32256).
+struct Q4Factor {
+  __half2 s, s72;  // s, 72 s of the two
+};
+__device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<__half2 *>(&x); }
+__device__ __forceinline__ uint32_t as_word(__half2 x) { return *reinterpret_cast<uint32_t *>(&x); }
+__device__ __forceinline__ Q4Factor q4_factor(uint32_t s) {
+  return Q4Factor{as_half2(s), __hmul2(as_half2(s), as_half2(0xD480D480u))};
 }
-__device__ __forceinline__ uint32_t times_m72(uint32_t s) {
-  uint32_t x;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(x) : "r"(s), "r"(0xD480D480u));
-  return x;
+template <bool odd> __device__ __forceinline__ uint32_t q4_pair(uint32_t w, const Q4Factor &f) {
+  const uint32_t n = ((odd ? w : w << 4) & 0x00F000F0u) | 0x54005400u;
+  return as_word(__hfma2(as_half2(n), f.s, f.s72));
 }
 // Which of the first eight tokens of a warp's sixteen a row of its products is (and of the
 // last eight): with 64-byte rows under the 64-byte swizzle, rows in this order meet distinct
@@ -324,46 +326,187 @@ __global__ void __launch_bounds__(Shape<T, kForm>::kThreads, Shape<T, kForm>::kC
         for (int d = 0; d < 8; ++d)
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[d][i] = 0.f;
+        if constexpr (Q4) {
+          float bm[2] = {0.f, 0.f}, br[2] = {0.f, 0.f};  // the maxima that the weights refer to
+          for (int tile = g.tile_lo; tile < g.tile_hi; ++tile, ring.next()) {
+            if (!wait(smem_u32(&sh.full[ring.s]), ring.ph)) {
+              live = false;
+              break;
+            }
+            const int at0 = warp * 32, tok0 = tile * kTile + at0;
+            const uint32_t have = (sh.tokens[ring.s] >> (2 * warp)) & 3;
+            // every row sees all 32 tokens
+            const bool clear = have == 3 && tok0 + 31 <= g.t_first &&
+                               (a.window <= 0 || tok0 > g.t_last - a.window);
+            float z[2][4], y[2][4];  // element i: token tg + 8 (i >> 1), row 2 t4 + (i & 1)
+            uint32_t bad[2][2];
+#pragma unroll
+            for (int sub = 0; sub < 2; ++sub) {
+              const int tok = at0 + 16 * sub + tg;
+              const uint8_t *kc = sh.kv[ring.s][0] + tok * kQ4Bytes + ((t4 ^ ((tg >> 1) & 3)) << 4);
+              const uint4 u = *reinterpret_cast<const uint4 *>(kc);
+              const uint4 v = *reinterpret_cast<const uint4 *>(kc + 8 * kQ4Bytes);
+              const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
+              const uint8_t *gc = sh.group[ring.s][0] + tok * kQ4Scales + 2 * t4;
+              // two scales of token tg, of token tg + 8
+              const uint32_t g0 = f16_lo(*reinterpret_cast<const uint16_t *>(gc));
+              const uint32_t g1 = f16_lo(*reinterpret_cast<const uint16_t *>(gc + 8 * kQ4Scales));
+              float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {  // 16 channels, two words
+                const Q4Factor f0 = q4_factor(__byte_perm(g0, 0, c ? 0x3232 : 0x1010));
+                const Q4Factor f1 = q4_factor(__byte_perm(g1, 0, c ? 0x3232 : 0x1010));
+#pragma unroll
+                for (int j = 2 * c; j < 2 * c + 2; ++j) {
+                  const uint32_t a0 = q4_pair<0>(uu[j], f0), a1 = q4_pair<0>(vv[j], f1);
+                  const uint32_t a2 = q4_pair<1>(uu[j], f0), a3 = q4_pair<1>(vv[j], f1);
+                  const uint32_t b0 = q4_pair<0>(uu[j] >> 8, f0), b1 = q4_pair<0>(vv[j] >> 8, f1);
+                  const uint32_t b2 = q4_pair<1>(uu[j] >> 8, f0), b3 = q4_pair<1>(vv[j] >> 8, f1);
+#pragma unroll
+                  for (int e = kTerms - 1; e >= 0; --e) {  // the small term first
+                    mma16816(s, a0, a1, a2, a3, q[e][4 * j], q[e][4 * j + 1], M{});
+                    mma16816(s, b0, b1, b2, b3, q[e][4 * j + 2], q[e][4 * j + 3], M{});
+                  }
+                }
+              }
+              bool vbad[2];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint32_t kb = sh.scale[ring.s][0][tok + 8 * k];
+                const uint32_t vb = sh.scale[ring.s][1][tok + 8 * k];
+                vbad[k] = vb == (uint32_t)kQ4NanPower;
+                const float kf = q4_power(kb);
+                // vb - 127, in the mantissa of 2^23 + vb
+                const float ev = vbad[k] ? __uint_as_float(0x7FC00000u)
+                                         : __uint_as_float(0x4B000000u | vb) - 8388735.f;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  z[sub][2 * k + h] = s[2 * k + h] * (kf * qf[h]);
+                  y[sub][2 * k + h] = z[sub][2 * k + h] + ev;
+                }
+              }
+              if (!clear) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const int pos = tok0 + 16 * sub + tg + 8 * k;
+                  const bool token = ((have >> sub) & 1) && pos < g.len;
+                  vbad[k] |= !token;
+#pragma unroll
+                  for (int h = 0; h < 2; ++h)
+                    if (!(token && pos <= tq[h] && (a.window <= 0 || pos - tq[h] > -a.window)))
+                      z[sub][2 * k + h] = y[sub][2 * k + h] = -INFINITY;
+                }
+              }
+              bad[sub][0] = __ballot_sync(0xFFFFFFFFu, vbad[0]);
+              bad[sub][1] = __ballot_sync(0xFFFFFFFFu, vbad[1]);
+            }
+            // (a difference of two -inf is NaN, which max leaves out: no move)
+            float over = -INFINITY;
+#pragma unroll
+            for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                over = max3(over, z[sub][i] - (m[i & 1] + kMoveAt), y[sub][i] - (r[i & 1] + kMoveAt));
+            if (__any_sync(0xFFFFFFFFu, over > 0.f)) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                float mz = fmaxf(fmaxf(z[0][h], z[0][h + 2]), fmaxf(z[1][h], z[1][h + 2]));
+                float my = fmaxf(fmaxf(y[0][h], y[0][h + 2]), fmaxf(y[1][h], y[1][h + 2]));
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) {
+                  mz = fmaxf(mz, __shfl_xor_sync(0xFFFFFFFFu, mz, off));
+                  my = fmaxf(my, __shfl_xor_sync(0xFFFFFFFFu, my, off));
+                }
+                mz = fmaxf(mz, m[h]);
+                my = fmaxf(my, r[h]);
+                // (from -inf: 0, and 1 where it stays there)
+                const float al = mz == -INFINITY ? 1.f : ex2(m[h] - mz);
+                const float ao = my == -INFINITY ? 1.f : ex2(r[h] - my);
+                m[h] = mz;
+                r[h] = my;
+                bm[h] = mz == -INFINITY ? 0.f : mz;
+                br[h] = my == -INFINITY ? 0.f : my - kShift;
+                l[h] *= al;
+#pragma unroll
+                for (int d = 0; d < 8; ++d) {
+                  o[d][h] *= ao;
+                  o[d][h + 2] *= ao;
+                }
+              }
+            }
+#pragma unroll
+            for (int sub = 0; sub < 2; ++sub) {
+              float w[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                l[i & 1] += ex2(z[sub][i] - bm[i & 1]);
+                w[i] = ex2(y[sub][i] - br[i & 1]);
+              }
+              uint32_t p[kTerms][2];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint32_t hi = pack2(w[2 * k], w[2 * k + 1], M{});
+                p[0][k] = movm_t(hi);
+                if constexpr (kTwo) {
+                  const float2 h = unpack2(hi, M{});
+                  p[1][k] = movm_t(pack2(w[2 * k] - h.x, w[2 * k + 1] - h.y, M{}));
+                }
+              }
+              // O^T: rows 2 t4, 2 t4 + 1 (+ 8) of the tokens; channels 16 g8 .. + 15
+              uint2 v2[4];
+              uint32_t sb[4];
+              const bool some = (bad[sub][0] | bad[sub][1]) != 0;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int row = 2 * t4 + (i & 1), tk = q4_token(row);
+                const int tok = at0 + 16 * sub + tk + 8 * (i >> 1);
+                v2[i] = *reinterpret_cast<const uint2 *>(
+                    sh.kv[ring.s][1] + tok * kQ4Bytes + (((g8 >> 1) ^ ((tk >> 1) & 3)) << 4) + 8 * (g8 & 1));
+                sb[i] = sh.group[ring.s][1][tok * kQ4Scales + g8];
+                // rows without a token and NaN vectors must not meet a weight of 0: their scales
+                // are cleared (a row that sees a NaN vector has a NaN weight); lanes 4 row .. speak
+                // for the row
+                if (some && ((bad[sub][i >> 1] >> (4 * row)) & 1)) sb[i] = 0;
+              }
+              const Q4Factor f0 = q4_factor(f16_lo(sb[0] | (sb[1] << 8)));
+              const Q4Factor f1 = q4_factor(f16_lo(sb[2] | (sb[3] << 8)));
+              // adds the products of the small term and of the large one
+              auto add = [&](float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+                if constexpr (kTwo) {
+                  float t[4] = {0.f, 0.f, 0.f, 0.f};
+                  mma16816(t, a0, a1, a2, a3, p[1][0], p[1][1], M{});
+                  mma16816(t, a0, a1, a2, a3, p[0][0], p[0][1], M{});
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) c[i] += t[i];
+                } else {
+                  mma16816(c, a0, a1, a2, a3, p[0][0], p[0][1], M{});
+                }
+              };
+#pragma unroll
+              for (int d = 0; d < 8; ++d) {  // a byte of two channels: a block of O^T
+                const int byte = 0x0400 + 0x0101 * (d & 3);
+                const uint32_t u = __byte_perm(d < 4 ? v2[0].x : v2[0].y, d < 4 ? v2[1].x : v2[1].y, byte);
+                const uint32_t w = __byte_perm(d < 4 ? v2[2].x : v2[2].y, d < 4 ? v2[3].x : v2[3].y, byte);
+                add(o[d], q4_pair<0>(u, f0), q4_pair<1>(u, f0), q4_pair<0>(w, f1), q4_pair<1>(w, f1));
+              }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.empty[ring.s]));
+          }
+        } else {
         for (int tile = g.tile_lo; tile < g.tile_hi; ++tile, ring.next()) {
           if (!wait(smem_u32(&sh.full[ring.s]), ring.ph)) {
             live = false;
             break;
           }
           const int tok0 = tile * kTile + warp * 16;
-          const uint8_t *kc = sh.kv[ring.s][0] + warp * 16 * (Q4 ? kQ4Bytes : 128);
-          const uint8_t *vc = sh.kv[ring.s][1] + warp * 16 * (Q4 ? kQ4Bytes : 128);
+          const uint8_t *kc = sh.kv[ring.s][0] + warp * 16 * 128;
+          const uint8_t *vc = sh.kv[ring.s][1] + warp * 16 * 128;
           const bool pages = (sh.tokens[ring.s] >> warp) & 1;
-          // S^T: tokens tg and tg + 8
+          // S^T: tokens g8 and g8 + 8
           float s[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) s[i] = 0.f;
-          if constexpr (Q4) {
-            const int at = tg * kQ4Bytes + ((t4 ^ ((tg >> 1) & 3)) << 4);
-            const uint4 u = *reinterpret_cast<const uint4 *>(kc + at);
-            const uint4 v = *reinterpret_cast<const uint4 *>(kc + at + 8 * kQ4Bytes);
-            const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
-            const uint8_t *gc = sh.group[ring.s][0] + (warp * 16 + tg) * kQ4Scales + 2 * t4;
-            uint32_t gs[2];  // two scales of token tg, of token tg + 8
-            gs[0] = f16_lo(*reinterpret_cast<const uint16_t *>(gc));
-            gs[1] = f16_lo(*reinterpret_cast<const uint16_t *>(gc + 8 * kQ4Scales));
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {  // 16 channels, two words
-              const uint32_t s0 = __byte_perm(gs[0], 0, c ? 0x3232 : 0x1010), m0 = times_m72(s0);
-              const uint32_t s1 = __byte_perm(gs[1], 0, c ? 0x3232 : 0x1010), m1 = times_m72(s1);
-#pragma unroll
-              for (int j = 2 * c; j < 2 * c + 2; ++j) {
-                const uint32_t a0 = q4_pair<0>(uu[j], s0, m0), a1 = q4_pair<0>(vv[j], s1, m1);
-                const uint32_t a2 = q4_pair<1>(uu[j], s0, m0), a3 = q4_pair<1>(vv[j], s1, m1);
-                const uint32_t b0 = q4_pair<2>(uu[j], s0, m0), b1 = q4_pair<2>(vv[j], s1, m1);
-                const uint32_t b2 = q4_pair<3>(uu[j], s0, m0), b3 = q4_pair<3>(vv[j], s1, m1);
-#pragma unroll
-                for (int e = kTerms - 1; e >= 0; --e) {  // the small term first
-                  mma16816(s, a0, a1, a2, a3, q[e][4 * j], q[e][4 * j + 1], M{});
-                  mma16816(s, b0, b1, b2, b3, q[e][4 * j + 2], q[e][4 * j + 3], M{});
-                }
-              }
-            }
-          } else {
 #pragma unroll
           for (int c = 0; c < (Q8 ? 2 : 4); ++c) {
             const int at = (c >> 1) * kSlab + g8 * 128 + (((2 * t4 + (c & 1)) ^ g8) << 4);
@@ -386,19 +529,18 @@ __global__ void __launch_bounds__(Shape<T, kForm>::kThreads, Shape<T, kForm>::kC
                 mma16816(s, a0, a1, a2, a3, q[e][k], q[e][k + 1], M{});
             }
           }
-          }
-          // tokens this thread's lane speaks for: tg + 8 i
+          // tokens this thread's lane speaks for: g8 + 8 i
           bool token[2], vbad[2];
           float kf[2], ev[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            token[i] = pages && tok0 + tg + 8 * i < g.len;
+            token[i] = pages && tok0 + g8 + 8 * i < g.len;
             vbad[i] = !token[i];
             kf[i] = 1.f;
             ev[i] = 0.f;
             if constexpr (Q8) {
-              const uint32_t kb = sh.scale[ring.s][0][warp * 16 + tg + 8 * i];
-              const uint32_t vb = sh.scale[ring.s][1][warp * 16 + tg + 8 * i];
+              const uint32_t kb = sh.scale[ring.s][0][warp * 16 + g8 + 8 * i];
+              const uint32_t vb = sh.scale[ring.s][1][warp * 16 + g8 + 8 * i];
               vbad[i] |= vb == (uint32_t)kQ8NanScale;
               kf[i] = q8_scale(kb);
               ev[i] = vb == (uint32_t)kQ8NanScale ? __uint_as_float(0x7FC00000u)
@@ -408,12 +550,12 @@ __global__ void __launch_bounds__(Shape<T, kForm>::kThreads, Shape<T, kForm>::kC
           const uint32_t bad0 = __ballot_sync(0xFFFFFFFFu, vbad[0]);
           const uint32_t bad1 = __ballot_sync(0xFFFFFFFFu, vbad[1]);
           uint32_t p[kTerms][2];
-          float z[4], y[4];  // element i: token tg + 8 (i >> 1), row 2 t4 + (i & 1)
+          float z[4], y[4];  // element i: token g8 + 8 (i >> 1), row 2 t4 + (i & 1)
           bool move = false;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int k = i >> 1, h = i & 1;
-            const int pos = tok0 + tg + 8 * k;
+            const int pos = tok0 + g8 + 8 * k;
             const bool see = token[k] && pos <= tq[h] &&
                              (a.window <= 0 || pos - tq[h] > -a.window);
             z[i] = see ? s[i] * (kf[k] * qf[h]) : -INFINITY;
@@ -464,45 +606,6 @@ __global__ void __launch_bounds__(Shape<T, kForm>::kThreads, Shape<T, kForm>::kC
           }
           // O^T: tokens 2 t4, 2 t4 + 1 (+ 8); channels 16 g8 .. + 15 of codes, 8 g8
           // .. + 7 of both slabs of 16-bit data
-          if constexpr (Q4) {
-            uint2 v2[4];
-            uint32_t sb[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int row = 2 * t4 + (i & 1), tok = q4_token(row) + 8 * (i >> 1);
-              v2[i] = *reinterpret_cast<const uint2 *>(
-                  vc + tok * kQ4Bytes + (((g8 >> 1) ^ ((tok >> 1) & 3)) << 4) + 8 * (g8 & 1));
-              sb[i] = sh.group[ring.s][1][(warp * 16 + tok) * kQ4Scales + g8];
-              // (as below: a scale of 0 clears the vector)
-              if ((bad0 | bad1) && (((i >> 1 ? bad1 : bad0) >> (4 * row)) & 1)) sb[i] = 0;
-            }
-            const uint32_t s0 = f16_lo(sb[0] | (sb[1] << 8)), m0 = times_m72(s0);
-            const uint32_t s1 = f16_lo(sb[2] | (sb[3] << 8)), m1 = times_m72(s1);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {  // four channels: block d of O^T has two
-              const uint32_t u = __byte_perm(c < 2 ? v2[0].x : v2[0].y, c < 2 ? v2[1].x : v2[1].y,
-                                             c & 1 ? 0x7632 : 0x5410);
-              const uint32_t w = __byte_perm(c < 2 ? v2[2].x : v2[2].y, c < 2 ? v2[3].x : v2[3].y,
-                                             c & 1 ? 0x7632 : 0x5410);
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t a0 = h ? q4_pair<2>(u, s0, m0) : q4_pair<0>(u, s0, m0);
-                const uint32_t a1 = h ? q4_pair<3>(u, s0, m0) : q4_pair<1>(u, s0, m0);
-                const uint32_t a2 = h ? q4_pair<2>(w, s1, m1) : q4_pair<0>(w, s1, m1);
-                const uint32_t a3 = h ? q4_pair<3>(w, s1, m1) : q4_pair<1>(w, s1, m1);
-                const int d = 2 * c + h;
-                if constexpr (kTwo) {
-                  float t[4] = {0.f, 0.f, 0.f, 0.f};
-                  mma16816(t, a0, a1, a2, a3, p[1][0], p[1][1], M{});
-                  mma16816(t, a0, a1, a2, a3, p[0][0], p[0][1], M{});
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) o[d][i] += t[i];
-                } else {
-                  mma16816(o[d], a0, a1, a2, a3, p[0][0], p[0][1], M{});
-                }
-              }
-            }
-          } else {
           uint4 v4[Sh::kSlabs][4];
 #pragma unroll
           for (int c = 0; c < Sh::kSlabs; ++c)
@@ -599,9 +702,9 @@ __global__ void __launch_bounds__(Shape<T, kForm>::kThreads, Shape<T, kForm>::kC
               mma16816(o[d], a0, a1, a2, a3, p[0][0], p[0][1], M{});
             }
           }
-          }
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sh.empty[ring.s]));
+        }
         }
         if (!live) break;
         // elements 0, 1 of o[d]: its even channel, rows 2 t4 and 2 t4 + 1; 2, 3: the odd one
@@ -695,7 +798,7 @@ cudaError_t few_go(const ChunkArgs &a, const CUtensorMap &tk, const CUtensorMap 
                    cudaStream_t st) {
   using Sh = Shape<T, kForm>;
   constexpr int bytes = (int)sizeof(Shared<T, kForm>);
-  static_assert(bytes <= (Sh::kCtas == 2 ? 113 : 227) * 1024, "shared memory");
+  static_assert(bytes <= (228 / Sh::kCtas - 1) * 1024, "shared memory");
   const cudaError_t e = cudaFuncSetAttribute(
       chunk_few_kernel<T, kForm>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
