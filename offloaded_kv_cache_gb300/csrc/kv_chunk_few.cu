@@ -328,6 +328,7 @@ __global__ void __launch_bounds__(Shape<T, kForm>::kThreads, Shape<T, kForm>::kC
           for (int i = 0; i < 4; ++i) o[d][i] = 0.f;
         if constexpr (Q4) {
           float bm[2] = {0.f, 0.f}, br[2] = {0.f, 0.f};  // the maxima that the weights refer to
+          bool begun = false;                            // every row has seen a token
           for (int tile = g.tile_lo; tile < g.tile_hi; ++tile, ring.next()) {
             if (!wait(smem_u32(&sh.full[ring.s]), ring.ph)) {
               live = false;
@@ -338,8 +339,10 @@ __global__ void __launch_bounds__(Shape<T, kForm>::kThreads, Shape<T, kForm>::kC
             // every row sees all 32 tokens
             const bool clear = have == 3 && tok0 + 31 <= g.t_first &&
                                (a.window <= 0 || tok0 > g.t_last - a.window);
-            float z[2][4], y[2][4];  // element i: token tg + 8 (i >> 1), row 2 t4 + (i & 1)
-            uint32_t bad[2][2];
+            // log2 of the weights in the sum and in the product; element i: token tg + 8 (i >> 1),
+            // row 2 t4 + (i & 1)
+            float e1[2][4], e2[2][4];
+            uint32_t vb[2][2];  // V's power bytes
 #pragma unroll
             for (int sub = 0; sub < 2; ++sub) {
               const int tok = at0 + 16 * sub + tg;
@@ -369,49 +372,57 @@ __global__ void __launch_bounds__(Shape<T, kForm>::kThreads, Shape<T, kForm>::kC
                   }
                 }
               }
-              bool vbad[2];
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
-                const uint32_t kb = sh.scale[ring.s][0][tok + 8 * k];
-                const uint32_t vb = sh.scale[ring.s][1][tok + 8 * k];
-                vbad[k] = vb == (uint32_t)kQ4NanPower;
-                const float kf = q4_power(kb);
+                // (power 255 gives infinity here, and a NaN vector's scales are 0: NaN)
+                const float kf = __uint_as_float((uint32_t)sh.scale[ring.s][0][tok + 8 * k] << 23);
+                vb[sub][k] = sh.scale[ring.s][1][tok + 8 * k];
                 // vb - 127, in the mantissa of 2^23 + vb
-                const float ev = vbad[k] ? __uint_as_float(0x7FC00000u)
-                                         : __uint_as_float(0x4B000000u | vb) - 8388735.f;
+                const float ev = __uint_as_float(0x4B000000u | vb[sub][k]) - 8388735.f;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                  z[sub][2 * k + h] = s[2 * k + h] * (kf * qf[h]);
-                  y[sub][2 * k + h] = z[sub][2 * k + h] + ev;
+                  const float x = s[2 * k + h] * kf;
+                  e1[sub][2 * k + h] = fmaf(x, qf[h], -bm[h]);
+                  e2[sub][2 * k + h] = fmaf(x, qf[h], ev - br[h]);
                 }
               }
-              if (!clear) {
+            }
+            const uint32_t top = max(max(vb[0][0], vb[0][1]), max(vb[1][0], vb[1][1]));
+            float over1 = e1[0][0], over2 = e2[0][0];
+#pragma unroll
+            for (int i = 1; i < 7; i += 2) {
+              over1 = max3(over1, e1[i >> 2][i & 3], e1[(i + 1) >> 2][(i + 1) & 3]);
+              over2 = max3(over2, e2[i >> 2][i & 3], e2[(i + 1) >> 2][(i + 1) & 3]);
+            }
+            over1 = fmaxf(over1, e1[1][3]);
+            over2 = fmaxf(over2, e2[1][3]);
+            // bit 4 row + k + 2 sub: row + 8 k of the products has a V to be cleared
+            uint32_t bad = 0;
+            const bool rare = over1 > kMoveAt || over2 > kMoveAt + kShift || top == (uint32_t)kQ4NanPower;
+            if (__any_sync(0xFFFFFFFFu, rare) || !clear || !begun) {
+              // tokens that are not seen, NaN vectors, and maxima that move
+              begun = true;
+#pragma unroll
+              for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                   const int pos = tok0 + 16 * sub + tg + 8 * k;
                   const bool token = ((have >> sub) & 1) && pos < g.len;
-                  vbad[k] |= !token;
+                  const bool nan = vb[sub][k] == (uint32_t)kQ4NanPower;
+                  const uint32_t b = __ballot_sync(0xFFFFFFFFu, (!token || nan) && t4 == k + 2 * sub);
+                  bad |= b;
 #pragma unroll
-                  for (int h = 0; h < 2; ++h)
-                    if (!(token && pos <= tq[h] && (a.window <= 0 || pos - tq[h] > -a.window)))
-                      z[sub][2 * k + h] = y[sub][2 * k + h] = -INFINITY;
+                  for (int h = 0; h < 2; ++h) {
+                    float &z = e1[sub][2 * k + h], &y = e2[sub][2 * k + h];
+                    const bool see = token && pos <= tq[h] && (a.window <= 0 || pos - tq[h] > -a.window);
+                    z = see ? z + bm[h] : -INFINITY;
+                    y = !see ? -INFINITY : nan ? __uint_as_float(0x7FC00000u) : y + br[h];
+                  }
                 }
-              }
-              bad[sub][0] = __ballot_sync(0xFFFFFFFFu, vbad[0]);
-              bad[sub][1] = __ballot_sync(0xFFFFFFFFu, vbad[1]);
-            }
-            // (a difference of two -inf is NaN, which max leaves out: no move)
-            float over = -INFINITY;
-#pragma unroll
-            for (int sub = 0; sub < 2; ++sub)
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                over = max3(over, z[sub][i] - (m[i & 1] + kMoveAt), y[sub][i] - (r[i & 1] + kMoveAt));
-            if (__any_sync(0xFFFFFFFFu, over > 0.f)) {
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                float mz = fmaxf(fmaxf(z[0][h], z[0][h + 2]), fmaxf(z[1][h], z[1][h + 2]));
-                float my = fmaxf(fmaxf(y[0][h], y[0][h + 2]), fmaxf(y[1][h], y[1][h + 2]));
+                float mz = fmaxf(fmaxf(e1[0][h], e1[0][h + 2]), fmaxf(e1[1][h], e1[1][h + 2]));
+                float my = fmaxf(fmaxf(e2[0][h], e2[0][h + 2]), fmaxf(e2[1][h], e2[1][h + 2]));
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) {
                   mz = fmaxf(mz, __shfl_xor_sync(0xFFFFFFFFu, mz, off));
@@ -426,21 +437,30 @@ __global__ void __launch_bounds__(Shape<T, kForm>::kThreads, Shape<T, kForm>::kC
                 r[h] = my;
                 bm[h] = mz == -INFINITY ? 0.f : mz;
                 br[h] = my == -INFINITY ? 0.f : my - kShift;
+                begun &= mz != -INFINITY && my != -INFINITY;
                 l[h] *= al;
 #pragma unroll
                 for (int d = 0; d < 8; ++d) {
                   o[d][h] *= ao;
                   o[d][h + 2] *= ao;
                 }
+#pragma unroll
+                for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+                  for (int i = h; i < 4; i += 2) {
+                    e1[sub][i] -= bm[h];
+                    e2[sub][i] -= br[h];
+                  }
               }
+              begun = __all_sync(0xFFFFFFFFu, begun);
             }
 #pragma unroll
             for (int sub = 0; sub < 2; ++sub) {
               float w[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                l[i & 1] += ex2(z[sub][i] - bm[i & 1]);
-                w[i] = ex2(y[sub][i] - br[i & 1]);
+                l[i & 1] += ex2(e1[sub][i]);
+                w[i] = ex2(e2[sub][i]);
               }
               uint32_t p[kTerms][2];
 #pragma unroll
@@ -455,7 +475,6 @@ __global__ void __launch_bounds__(Shape<T, kForm>::kThreads, Shape<T, kForm>::kC
               // O^T: rows 2 t4, 2 t4 + 1 (+ 8) of the tokens; channels 16 g8 .. + 15
               uint2 v2[4];
               uint32_t sb[4];
-              const bool some = (bad[sub][0] | bad[sub][1]) != 0;
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const int row = 2 * t4 + (i & 1), tk = q4_token(row);
@@ -463,10 +482,13 @@ __global__ void __launch_bounds__(Shape<T, kForm>::kThreads, Shape<T, kForm>::kC
                 v2[i] = *reinterpret_cast<const uint2 *>(
                     sh.kv[ring.s][1] + tok * kQ4Bytes + (((g8 >> 1) ^ ((tk >> 1) & 3)) << 4) + 8 * (g8 & 1));
                 sb[i] = sh.group[ring.s][1][tok * kQ4Scales + g8];
-                // rows without a token and NaN vectors must not meet a weight of 0: their scales
-                // are cleared (a row that sees a NaN vector has a NaN weight); lanes 4 row .. speak
-                // for the row
-                if (some && ((bad[sub][i >> 1] >> (4 * row)) & 1)) sb[i] = 0;
+              }
+              // rows without a token and NaN vectors must not meet a weight of 0: their scales
+              // are cleared (a row that sees a NaN vector has a NaN weight)
+              if (bad) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if ((bad >> (4 * (2 * t4 + (i & 1)) + (i >> 1) + 2 * sub)) & 1) sb[i] = 0;
               }
               const Q4Factor f0 = q4_factor(f16_lo(sb[0] | (sb[1] << 8)));
               const Q4Factor f1 = q4_factor(f16_lo(sb[2] | (sb[3] << 8)));
