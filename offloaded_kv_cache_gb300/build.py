@@ -17,7 +17,7 @@ LIB = os.path.join(HERE, "libkvsparse.so")
 SOURCES = ["kv_api.cu", "kv_index.cu", "kv_topk.cu", "kv_attn_core.cu", "kv_attn_mma.cu",
            "kv_attn_win.cu", "kv_noalloc.cu", "kv_probe.cu", "kv_append.cu", "kv_window.cu",
            "kv_select_fused.cu", "kv_rope.cu", "kv_q4.cu", "kv_q8.cu", "kv_chunk.cu", "kv_chunk_mma.cu",
-           "kv_chunk_few.cu", "kv_chunk_api.cu"]
+           "kv_chunk_few.cu", "kv_chunk_q4.cu", "kv_chunk_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

@@ -7,7 +7,6 @@
 #include "kv_chunk.cuh"
 #include "kv_host.h"
 #include "kv_launch.h"
-#include "kv_q4.cuh"
 
 namespace {
 
@@ -108,7 +107,7 @@ int few_rows_limit(const kv_shape *s, int window, CacheForm form) {
 struct ChunkPlan {
   bool mma = false;   // tensor cores (16-bit data)
   bool q8 = false;    // the kernel reads the 8-bit cache itself
-  CacheForm form_read = kOwnForm;  // what the kernel for few rows reads
+  bool q4 = false;    // the kernel reads the 4-bit cache itself
   bool few = false;   // the kernel for few rows
   bool stage = false; // K/V pass through the workspace in 16 bits
   bool renumber = false;  // the staged pages have a block table of their own
@@ -143,11 +142,11 @@ ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, CacheForm form) 
   const bool hbm = s->kv_loc == KV_LOC_HBM;
   int per_sm = 2;
   pl.q8 = q8 && hbm;
-  pl.form_read = pl.q8 ? kQ8Form : q4 && hbm ? kQ4Form : kOwnForm;
-  pl.few = packed <= few_rows_limit(s, c->window, pl.form_read);
+  pl.q4 = q4 && hbm;
+  pl.few = packed <= few_rows_limit(s, c->window, pl.q8 ? kQ8Form : pl.q4 ? kQ4Form : kOwnForm);
   if (pl.few) {
     pl.stage = !hbm;
-    const FewShape sh = chunk_few_shape(s->dtype, pl.form_read);
+    const FewShape sh = pl.q4 ? chunk_q4_shape(s->dtype) : chunk_few_shape(s->dtype, pl.q8);
     pl.rows = sh.rows;
     pl.tile = sh.tile;
     per_sm = sh.per_sm;
@@ -176,7 +175,8 @@ ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, CacheForm form) 
     pl.rows = packed <= 4 ? 4 : packed <= KVS_F32_FEW_ROWS || !fills ? 8 : 64;
     if (pl.rows == 8) per_sm = 1;  // resident CTAs of its kernel (registers)
   }
-  if (q4 && !pl.few) pl.stage = true;
+  pl.q4 &= pl.few;
+  if (q4 && !pl.q4) pl.stage = true;
   // units of all sequences: full ones and one more each; no more CTAs than
   // there can be tiles
   const double units = std::min((double)s->batch * ((packed + pl.rows - 1) / pl.rows),
@@ -209,24 +209,21 @@ ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, CacheForm form) 
   return pl;
 }
 
-// A tensor map of rows of 128 channels under the 128-byte swizzle (of 64-byte rows of 4-bit
-// codes under the 64-byte one).
+// A tensor map of rows of 128 channels under the 128-byte swizzle.
 struct MapShape {
   int type;              // CUtensorMapDataType
   const void *base;
   long long rows;        // pages * Hkv * ps, or tokens of q
   int heads, box, box2;  // heads: 0 for pages; box: rows, or heads and tokens (box2)
-  int width;             // elements of a row, 0: 128
 };
 int encode_map(const MapShape &k, CUtensorMap *map) {
   auto fn = encode_fn();
   if (!fn) return KV_ERR_CUDA;
   const bool codes = k.type == CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  const int width = k.width ? k.width : kHeadDim;
-  const cuuint64_t row = (cuuint64_t)width * (codes ? 1 : 2);
-  const cuuint32_t across = codes ? width : 64;  // 128 bytes, or 64 of 4-bit codes
+  const cuuint64_t row = (cuuint64_t)kHeadDim * (codes ? 1 : 2);
+  const cuuint32_t across = codes ? 128 : 64;  // 128 bytes
   const cuuint32_t estr[3] = {1, 1, 1};
-  cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)k.rows, 0}, strides[2] = {row, 0};
+  cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)k.rows, 0}, strides[2] = {row, 0};
   cuuint32_t box[3] = {across, (cuuint32_t)k.box, 0};
   if (k.heads) {  // q: [tokens][heads][128]
     dims[1] = (cuuint64_t)k.heads;
@@ -236,8 +233,7 @@ int encode_map(const MapShape &k, CUtensorMap *map) {
   }
   const CUresult r = fn(map, (CUtensorMapDataType)k.type, k.heads ? 3 : 2,
                         const_cast<void *>(k.base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        width == kHeadDim ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? KV_OK : KV_ERR_CUDA;
 }
@@ -247,18 +243,18 @@ int type16(const kv_shape *s) {
 }
 // Pages as rows [pages * Hkv * ps][128]: a box is 128 bytes, 64 channels of 16-bit
 // data or all 128 of codes, of a page's tokens that fall into one KV tile.
-int page_map(const kv_shape *s, CacheForm form, int tile, const void *base, long long pages,
+int page_map(const kv_shape *s, bool codes, int tile, const void *base, long long pages,
              CUtensorMap *map) {
-  return encode_map(MapShape{form != kOwnForm ? (int)CU_TENSOR_MAP_DATA_TYPE_UINT8 : type16(s), base,
+  return encode_map(MapShape{codes ? (int)CU_TENSOR_MAP_DATA_TYPE_UINT8 : type16(s), base,
                              pages * s->num_kv_heads * s->page_size, 0,
-                             std::min(s->page_size, tile), 0, form == kQ4Form ? kQ4Bytes : 0},
+                             std::min(s->page_size, tile), 0},
                     map);
 }
 // q: a box is 64 channels of the G heads of row_tile / G tokens.
 int q_map(const kv_shape *s, const kv_chunk *c, const void *q, int row_tile,
           CUtensorMap *map) {
   const int G = s->num_q_heads / s->num_kv_heads;
-  return encode_map(MapShape{type16(s), q, c->total_q, s->num_q_heads, G, row_tile / G, 0}, map);
+  return encode_map(MapShape{type16(s), q, c->total_q, s->num_q_heads, G, row_tile / G}, map);
 }
 
 // The kernels count tiles and the staging's blocks in int32, and index the staged
@@ -354,13 +350,14 @@ int chunk_common(const kv_shape *s, const kv_chunk *c, const void *q, const void
     a.nphys = pages = pl.stage_pages;
   }
   CUtensorMap tq = {}, tk = {}, tv = {};
-  if (pl.few || (pl.mma && !pl.q8)) {
-    const CacheForm read = pl.few ? pl.form_read : kOwnForm;
-    if ((rc = page_map(s, read, pl.tile, a.k, pages, &tk)) != KV_OK) return rc;
-    if ((rc = page_map(s, read, pl.tile, a.v, pages, &tv)) != KV_OK) return rc;
+  if ((pl.few && !pl.q4) || (pl.mma && !pl.few && !pl.q8)) {
+    if ((rc = page_map(s, pl.q8, pl.tile, a.k, pages, &tk)) != KV_OK) return rc;
+    if ((rc = page_map(s, pl.q8, pl.tile, a.v, pages, &tv)) != KV_OK) return rc;
   }
-  if (pl.few) {
-    e = launch_chunk_few(s->dtype, pl.form_read, a, tk, tv, pl.ctas, st);
+  if (pl.q4) {
+    e = launch_chunk_q4(s->dtype, a, pl.ctas, st);
+  } else if (pl.few) {
+    e = launch_chunk_few(s->dtype, pl.q8, a, tk, tv, pl.ctas, st);
   } else if (pl.mma) {
     a.row_tile = pl.row_tile;
     // a scale that is not positive is applied to Q as it is loaded

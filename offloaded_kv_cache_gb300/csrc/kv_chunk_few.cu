@@ -47,7 +47,6 @@
 
 #include "kv_chunk.cuh"
 #include "kv_launch.h"
-#include "kv_q4.cuh"
 #include "kv_q8.cuh"
 #include "kv_umma.cuh"
 
@@ -59,31 +58,27 @@ constexpr float kBias = 7.f;    // ... times 2^7 for f16, so that small weights 
 
 constexpr int kRows = 8;  // rows of a unit
 
-template <class T, CacheForm kForm> struct Shape {
-  static constexpr bool kQ4 = kForm == kQ4Form, kCodes = kForm != kOwnForm;
+template <class T, bool Q8> struct Shape {
   static constexpr int kConsumers = 4;
   static constexpr int kThreads = 32 * (kConsumers + 1);
-  static constexpr int kSteps = kQ4 ? 2 : 1;            // of 16 tokens that a warp takes of a stage
-  static constexpr int kTile = 16 * kSteps * kConsumers;  // tokens per stage
-  static constexpr int kRowBytes = kQ4 ? kQ4Bytes : kHeadDim * (kCodes ? 1 : 2);
-  static constexpr int kSlabs = kCodes ? 1 : 2;
+  static constexpr int kTile = 16 * kConsumers;  // tokens per stage
+  static constexpr int kRowBytes = kHeadDim * (Q8 ? 1 : 2);
+  static constexpr int kSlabs = kRowBytes / 128;
   static constexpr int kBytes = kTile * kRowBytes;  // of K or V
-  static constexpr int kStages = kQ4 ? 3 : kCodes ? 5 : 3;
-  static constexpr int kCtas = sizeof(T) != 2 ? 1 : kQ4 ? 3 : 2;  // per SM
+  static constexpr int kStages = Q8 ? 5 : 3;
+  static constexpr int kCtas = sizeof(T) == 2 ? 2 : 1;  // per SM
 };
 
-template <class T, CacheForm kForm> struct Shared {
-  using Sh = Shape<T, kForm>;
-  // slabs of [token][128 bytes]; 4-bit: [token][64 bytes]
-  alignas(1024) uint8_t kv[Sh::kStages][2][Sh::kBytes];
+template <class T, bool Q8> struct Shared {
+  using Sh = Shape<T, Q8>;
+  alignas(1024) uint8_t kv[Sh::kStages][2][Sh::kBytes];  // slabs of [token][128 bytes]
   float o[Sh::kConsumers][kRows][kHeadDim];          // per warp, at the end of a segment
   float m[Sh::kConsumers][kRows], r[Sh::kConsumers][kRows], l[Sh::kConsumers][kRows];
-  alignas(16) uint8_t scale[Sh::kStages][2][Sh::kCodes ? Sh::kTile : 16];  // 4-bit: powers
-  alignas(16) uint8_t group[Sh::kQ4 ? Sh::kStages : 1][2][Sh::kQ4 ? Sh::kTile * kQ4Scales : 16];
+  alignas(16) uint8_t scale[Sh::kStages][2][Q8 ? Sh::kTile : 16];
   uint64_t full[Sh::kStages], empty[Sh::kStages], joined, read;
   int tokens[Sh::kStages];  // per stage: bit i: the pages of tokens 16 i .. + 15 are in range
   int abort, pad;
-  ChunkShare<Sh::kCodes ? 8 : 4> share;
+  ChunkShare<Q8 ? 8 : 4> share;
   int red[32];
 };
 
@@ -127,43 +122,11 @@ __device__ __forceinline__ uint32_t f16_hi(uint32_t w) {
   return x;
 }
 
-// The integers n = c + 8 of the low (odd: high) nibbles of bytes 0 and 2 of a word, less 8,
-// times their scales s: n is put into the mantissa of 64 + n, and (64 + n) s - 72 s, in one
-// fma, is exact (72 s has 8 significant bits, at most 32256).
-struct Q4Factor {
-  __half2 s, s72;  // s, 72 s of the two
-};
-__device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<__half2 *>(&x); }
-__device__ __forceinline__ uint32_t as_word(__half2 x) { return *reinterpret_cast<uint32_t *>(&x); }
-__device__ __forceinline__ Q4Factor q4_factor(uint32_t s) {
-  return Q4Factor{as_half2(s), __hmul2(as_half2(s), as_half2(0xD480D480u))};
-}
-// (One operation for mask and exponent, as long as both are in registers: of two immediates
-// the compiler makes two.  One token over 8 x 65536: 127 us with two.)
-struct Q4Bits {
-  uint32_t mask, one;
-  __device__ __forceinline__ Q4Bits() {
-    asm volatile("mov.b32 %0, 0x00F000F0;" : "=r"(mask));
-    asm volatile("mov.b32 %0, 0x54005400;" : "=r"(one));
-  }
-};
-template <bool odd>
-__device__ __forceinline__ uint32_t q4_pair(uint32_t w, const Q4Factor &f, const Q4Bits &b) {
-  uint32_t n;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(n) : "r"(odd ? w : w << 4), "r"(b.mask), "r"(b.one));
-  return as_word(__hfma2(as_half2(n), f.s, f.s72));
-}
-// Which of the first eight tokens of a warp's sixteen a row of its products is (and of the
-// last eight): with 64-byte rows under the 64-byte swizzle, rows in this order meet distinct
-// banks both as K's 16-byte and as V's 8-byte reads.
-__device__ __forceinline__ int q4_token(int row) { return (0x65742130u >> (4 * row)) & 7; }
-
-template <class T, CacheForm kForm>
-__global__ void __launch_bounds__(Shape<T, kForm>::kThreads, Shape<T, kForm>::kCtas)
+template <class T, bool Q8>
+__global__ void __launch_bounds__(Shape<T, Q8>::kThreads, Shape<T, Q8>::kCtas)
     chunk_few_kernel(const __grid_constant__ ChunkArgs a, const __grid_constant__ CUtensorMap tk,
                      const __grid_constant__ CUtensorMap tv) {
-  using Sh = Shape<T, kForm>;
-  constexpr bool Q8 = Sh::kCodes, Q4 = Sh::kQ4;  // 8 bits or 4; 4
+  using Sh = Shape<T, Q8>;
   constexpr int kConsumers = Sh::kConsumers, kTile = Sh::kTile, kStages = Sh::kStages;
   constexpr int kSlab = kTile * 128;
   using M = typename std::conditional<Q8, __half, T>::type;  // what the products take
@@ -171,7 +134,7 @@ __global__ void __launch_bounds__(Shape<T, kForm>::kThreads, Shape<T, kForm>::kC
   constexpr int kTerms = kTwo ? 2 : 1;
   constexpr float kShift = std::is_same<M, __half>::value ? kBias : 0.f;
   extern __shared__ __align__(1024) uint8_t smem[];
-  Shared<T, kForm> &sh = *reinterpret_cast<Shared<T, kForm> *>(smem);
+  Shared<T, Q8> &sh = *reinterpret_cast<Shared<T, Q8> *>(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (smem_u32(smem) & 1023u) {  // the swizzled tiles need it
     if (tid == 0) flag_error(a.status, KV_ERR_INVALID_ARG);
@@ -242,23 +205,18 @@ __global__ void __launch_bounds__(Shape<T, kForm>::kThreads, Shape<T, kForm>::kC
           const uint32_t bar = smem_u32(&sh.full[ring.s]);
           if (lane == 0) {
             sh.tokens[ring.s] = (int)all;
-            mbar_arrive_expect_tx(bar, 2 * Sh::kBytes + (Q4   ? 2 * have * pt * (1 + kQ4Scales)
-                                                    : Q8 ? 2 * have * pt
-                                                         : 0));
+            mbar_arrive_expect_tx(bar, 2 * Sh::kBytes + (Q8 ? 2 * have * pt : 0));
           }
           __syncwarp();
           if (lane < npg) {
             for (int w = 0; w < 2; ++w) {
-              const uint32_t dst = smem_u32(&sh.kv[ring.s][w][lane * pt * (Q4 ? kQ4Bytes : 128)]);
+              const uint32_t dst = smem_u32(&sh.kv[ring.s][w][lane * pt * 128]);
 #pragma unroll
               for (int slab = 0; slab < Sh::kSlabs; ++slab)
                 tma_load_2d(dst + slab * kSlab, w ? &tv : &tk, 64 * slab, y, bar);
               if (Q8 && ok)
                 bulk_load(smem_u32(&sh.scale[ring.s][w][lane * pt]), (w ? a.v_scale : a.k_scale) + y,
                           pt, bar);
-              if (Q4 && ok)
-                bulk_load(smem_u32(&sh.group[ring.s][w][lane * pt * kQ4Scales]),
-                          (w ? a.v_group : a.k_group) + (long long)y * kQ4Scales, pt * kQ4Scales, bar);
             }
           }
         }
@@ -273,7 +231,6 @@ __global__ void __launch_bounds__(Shape<T, kForm>::kThreads, Shape<T, kForm>::kC
   } else {
     // ----------------------------------------------------------- consumers
     const int g8 = lane >> 2, t4 = lane & 3;  // row and column group of the fragments
-    const int tg = Q4 ? q4_token(g8) : g8;    // the token of row g8 (and + 8)
     uint32_t join_ph = 0;
     while (next_list(true)) {
       bool live = true;
@@ -314,12 +271,10 @@ __global__ void __launch_bounds__(Shape<T, kForm>::kThreads, Shape<T, kForm>::kC
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          // 4-bit: the pairs that a word's nibbles make
-          const int lo = Q4 ? 8 * (i >> 2) + (i & 3) : 2 * i, hi = Q4 ? lo + 4 : lo + 1;
-          q[0][i] = pack2(x[lo], x[hi], M{});
+          q[0][i] = pack2(x[2 * i], x[2 * i + 1], M{});
           if constexpr (kTwo) {
             const float2 h = unpack2(q[0][i], M{});
-            q[1][i] = pack2(x[lo] - h.x, x[hi] - h.y, M{});
+            q[1][i] = pack2(x[2 * i] - h.x, x[2 * i + 1] - h.y, M{});
           }
         }
 #pragma unroll
@@ -337,197 +292,6 @@ __global__ void __launch_bounds__(Shape<T, kForm>::kThreads, Shape<T, kForm>::kC
         for (int d = 0; d < 8; ++d)
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[d][i] = 0.f;
-        if constexpr (Q4) {
-          const Q4Bits bits;
-          float bm[2] = {0.f, 0.f}, br[2] = {0.f, 0.f};  // the maxima that the weights refer to
-          bool begun = false;                            // every row has seen a token
-          for (int tile = g.tile_lo; tile < g.tile_hi; ++tile, ring.next()) {
-            if (!wait(smem_u32(&sh.full[ring.s]), ring.ph)) {
-              live = false;
-              break;
-            }
-            const int at0 = warp * 32, tok0 = tile * kTile + at0;
-            const uint32_t have = (sh.tokens[ring.s] >> (2 * warp)) & 3;
-            // every row sees all 32 tokens
-            const bool clear = have == 3 && tok0 + 31 <= g.t_first &&
-                               (a.window <= 0 || tok0 > g.t_last - a.window);
-            // log2 of the weights in the sum and in the product; element i: token tg + 8 (i >> 1),
-            // row 2 t4 + (i & 1)
-            float e1[2][4], e2[2][4];
-            uint32_t vb[2][2];  // V's power bytes
-#pragma unroll
-            for (int sub = 0; sub < 2; ++sub) {
-              const int tok = at0 + 16 * sub + tg;
-              const uint8_t *kc = sh.kv[ring.s][0] + tok * kQ4Bytes + ((t4 ^ ((tg >> 1) & 3)) << 4);
-              const uint4 u = *reinterpret_cast<const uint4 *>(kc);
-              const uint4 v = *reinterpret_cast<const uint4 *>(kc + 8 * kQ4Bytes);
-              const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
-              const uint8_t *gc = sh.group[ring.s][0] + tok * kQ4Scales + 2 * t4;
-              // two scales of token tg, of token tg + 8
-              const uint32_t g0 = f16_lo(*reinterpret_cast<const uint16_t *>(gc));
-              const uint32_t g1 = f16_lo(*reinterpret_cast<const uint16_t *>(gc + 8 * kQ4Scales));
-              float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {  // 16 channels, two words
-                const Q4Factor f0 = q4_factor(__byte_perm(g0, 0, c ? 0x3232 : 0x1010));
-                const Q4Factor f1 = q4_factor(__byte_perm(g1, 0, c ? 0x3232 : 0x1010));
-#pragma unroll
-                for (int j = 2 * c; j < 2 * c + 2; ++j) {
-                  const uint32_t a0 = q4_pair<0>(uu[j], f0, bits), a1 = q4_pair<0>(vv[j], f1, bits);
-                  const uint32_t a2 = q4_pair<1>(uu[j], f0, bits), a3 = q4_pair<1>(vv[j], f1, bits);
-                  const uint32_t b0 = q4_pair<0>(uu[j] >> 8, f0, bits), b1 = q4_pair<0>(vv[j] >> 8, f1, bits);
-                  const uint32_t b2 = q4_pair<1>(uu[j] >> 8, f0, bits), b3 = q4_pair<1>(vv[j] >> 8, f1, bits);
-#pragma unroll
-                  for (int e = kTerms - 1; e >= 0; --e) {  // the small term first
-                    mma16816(s, a0, a1, a2, a3, q[e][4 * j], q[e][4 * j + 1], M{});
-                    mma16816(s, b0, b1, b2, b3, q[e][4 * j + 2], q[e][4 * j + 3], M{});
-                  }
-                }
-              }
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                // (power 255 gives infinity here, and a NaN vector's scales are 0: NaN)
-                const float kf = __uint_as_float((uint32_t)sh.scale[ring.s][0][tok + 8 * k] << 23);
-                vb[sub][k] = sh.scale[ring.s][1][tok + 8 * k];
-                // vb - 127, in the mantissa of 2^23 + vb
-                const float ev = __uint_as_float(0x4B000000u | vb[sub][k]) - 8388735.f;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const float x = s[2 * k + h] * kf;
-                  e1[sub][2 * k + h] = fmaf(x, qf[h], -bm[h]);
-                  e2[sub][2 * k + h] = fmaf(x, qf[h], ev - br[h]);
-                }
-              }
-            }
-            const uint32_t top = max(max(vb[0][0], vb[0][1]), max(vb[1][0], vb[1][1]));
-            float over1 = e1[0][0], over2 = e2[0][0];
-#pragma unroll
-            for (int i = 1; i < 7; i += 2) {
-              over1 = max3(over1, e1[i >> 2][i & 3], e1[(i + 1) >> 2][(i + 1) & 3]);
-              over2 = max3(over2, e2[i >> 2][i & 3], e2[(i + 1) >> 2][(i + 1) & 3]);
-            }
-            over1 = fmaxf(over1, e1[1][3]);
-            over2 = fmaxf(over2, e2[1][3]);
-            // bit 4 row + k + 2 sub: row + 8 k of the products has a V to be cleared
-            uint32_t bad = 0;
-            const bool rare = over1 > kMoveAt || over2 > kMoveAt + kShift || top == (uint32_t)kQ4NanPower;
-            if (__any_sync(0xFFFFFFFFu, rare) || !clear || !begun) {
-              // tokens that are not seen, NaN vectors, and maxima that move
-              begun = true;
-#pragma unroll
-              for (int sub = 0; sub < 2; ++sub)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  const int pos = tok0 + 16 * sub + tg + 8 * k;
-                  const bool token = ((have >> sub) & 1) && pos < g.len;
-                  const bool nan = vb[sub][k] == (uint32_t)kQ4NanPower;
-                  const uint32_t b = __ballot_sync(0xFFFFFFFFu, (!token || nan) && t4 == k + 2 * sub);
-                  bad |= b;
-#pragma unroll
-                  for (int h = 0; h < 2; ++h) {
-                    float &z = e1[sub][2 * k + h], &y = e2[sub][2 * k + h];
-                    const bool see = token && pos <= tq[h] && (a.window <= 0 || pos - tq[h] > -a.window);
-                    z = see ? z + bm[h] : -INFINITY;
-                    y = !see ? -INFINITY : nan ? __uint_as_float(0x7FC00000u) : y + br[h];
-                  }
-                }
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                float mz = fmaxf(fmaxf(e1[0][h], e1[0][h + 2]), fmaxf(e1[1][h], e1[1][h + 2]));
-                float my = fmaxf(fmaxf(e2[0][h], e2[0][h + 2]), fmaxf(e2[1][h], e2[1][h + 2]));
-#pragma unroll
-                for (int off = 4; off < 32; off <<= 1) {
-                  mz = fmaxf(mz, __shfl_xor_sync(0xFFFFFFFFu, mz, off));
-                  my = fmaxf(my, __shfl_xor_sync(0xFFFFFFFFu, my, off));
-                }
-                mz = fmaxf(mz, m[h]);
-                my = fmaxf(my, r[h]);
-                // (from -inf: 0, and 1 where it stays there)
-                const float al = mz == -INFINITY ? 1.f : ex2(m[h] - mz);
-                const float ao = my == -INFINITY ? 1.f : ex2(r[h] - my);
-                m[h] = mz;
-                r[h] = my;
-                bm[h] = mz == -INFINITY ? 0.f : mz;
-                br[h] = my == -INFINITY ? 0.f : my - kShift;
-                begun &= mz != -INFINITY && my != -INFINITY;
-                l[h] *= al;
-#pragma unroll
-                for (int d = 0; d < 8; ++d) {
-                  o[d][h] *= ao;
-                  o[d][h + 2] *= ao;
-                }
-#pragma unroll
-                for (int sub = 0; sub < 2; ++sub)
-#pragma unroll
-                  for (int i = h; i < 4; i += 2) {
-                    e1[sub][i] -= bm[h];
-                    e2[sub][i] -= br[h];
-                  }
-              }
-              begun = __all_sync(0xFFFFFFFFu, begun);
-            }
-#pragma unroll
-            for (int sub = 0; sub < 2; ++sub) {
-              float w[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                l[i & 1] += ex2(e1[sub][i]);
-                w[i] = ex2(e2[sub][i]);
-              }
-              uint32_t p[kTerms][2];
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const uint32_t hi = pack2(w[2 * k], w[2 * k + 1], M{});
-                p[0][k] = movm_t(hi);
-                if constexpr (kTwo) {
-                  const float2 h = unpack2(hi, M{});
-                  p[1][k] = movm_t(pack2(w[2 * k] - h.x, w[2 * k + 1] - h.y, M{}));
-                }
-              }
-              // O^T: rows 2 t4, 2 t4 + 1 (+ 8) of the tokens; channels 16 g8 .. + 15
-              uint2 v2[4];
-              uint32_t sb[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int row = 2 * t4 + (i & 1), tk = q4_token(row);
-                const int tok = at0 + 16 * sub + tk + 8 * (i >> 1);
-                v2[i] = *reinterpret_cast<const uint2 *>(
-                    sh.kv[ring.s][1] + tok * kQ4Bytes + (((g8 >> 1) ^ ((tk >> 1) & 3)) << 4) + 8 * (g8 & 1));
-                sb[i] = sh.group[ring.s][1][tok * kQ4Scales + g8];
-              }
-              // rows without a token and NaN vectors must not meet a weight of 0: their scales
-              // are cleared (a row that sees a NaN vector has a NaN weight)
-              if (bad) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  if ((bad >> (4 * (2 * t4 + (i & 1)) + (i >> 1) + 2 * sub)) & 1) sb[i] = 0;
-              }
-              const Q4Factor f0 = q4_factor(f16_lo(sb[0] | (sb[1] << 8)));
-              const Q4Factor f1 = q4_factor(f16_lo(sb[2] | (sb[3] << 8)));
-              // adds the products of the small term and of the large one
-              auto add = [&](float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-                if constexpr (kTwo) {
-                  float t[4] = {0.f, 0.f, 0.f, 0.f};
-                  mma16816(t, a0, a1, a2, a3, p[1][0], p[1][1], M{});
-                  mma16816(t, a0, a1, a2, a3, p[0][0], p[0][1], M{});
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) c[i] += t[i];
-                } else {
-                  mma16816(c, a0, a1, a2, a3, p[0][0], p[0][1], M{});
-                }
-              };
-#pragma unroll
-              for (int d = 0; d < 8; ++d) {  // a byte of two channels: a block of O^T
-                const int byte = 0x0400 + 0x0101 * (d & 3);
-                const uint32_t u = __byte_perm(d < 4 ? v2[0].x : v2[0].y, d < 4 ? v2[1].x : v2[1].y, byte);
-                const uint32_t w = __byte_perm(d < 4 ? v2[2].x : v2[2].y, d < 4 ? v2[3].x : v2[3].y, byte);
-                add(o[d], q4_pair<0>(u, f0, bits), q4_pair<1>(u, f0, bits), q4_pair<0>(w, f1, bits), q4_pair<1>(w, f1, bits));
-              }
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sh.empty[ring.s]));
-          }
-        } else {
         for (int tile = g.tile_lo; tile < g.tile_hi; ++tile, ring.next()) {
           if (!wait(smem_u32(&sh.full[ring.s]), ring.ph)) {
             live = false;
@@ -739,7 +503,6 @@ __global__ void __launch_bounds__(Shape<T, kForm>::kThreads, Shape<T, kForm>::kC
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sh.empty[ring.s]));
         }
-        }
         if (!live) break;
         // elements 0, 1 of o[d]: its even channel, rows 2 t4 and 2 t4 + 1; 2, 3: the odd one
 #pragma unroll
@@ -827,43 +590,38 @@ __global__ void __launch_bounds__(Shape<T, kForm>::kThreads, Shape<T, kForm>::kC
     flag_error(a.status, KV_ERR_DEVICE_TIMEOUT);
 }
 
-template <class T, CacheForm kForm>
+template <class T, bool Q8>
 cudaError_t few_go(const ChunkArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
                    cudaStream_t st) {
-  using Sh = Shape<T, kForm>;
-  constexpr int bytes = (int)sizeof(Shared<T, kForm>);
-  static_assert(bytes <= (228 / Sh::kCtas - 1) * 1024, "shared memory");
+  using Sh = Shape<T, Q8>;
+  constexpr int bytes = (int)sizeof(Shared<T, Q8>);
+  static_assert(bytes <= (Sh::kCtas == 2 ? 113 : 227) * 1024, "shared memory");
   const cudaError_t e = cudaFuncSetAttribute(
-      chunk_few_kernel<T, kForm>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+      chunk_few_kernel<T, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  return launch_pdl(chunk_few_kernel<T, kForm>, dim3(ctas), dim3(Sh::kThreads), bytes, st, a, tk,
+  return launch_pdl(chunk_few_kernel<T, Q8>, dim3(ctas), dim3(Sh::kThreads), bytes, st, a, tk,
                     tv);
 }
-template <class T>
-cudaError_t few_type(CacheForm form, const ChunkArgs &a, const CUtensorMap &tk,
-                     const CUtensorMap &tv, int ctas, cudaStream_t st) {
-  return form == kQ4Form   ? few_go<T, kQ4Form>(a, tk, tv, ctas, st)
-         : form == kQ8Form ? few_go<T, kQ8Form>(a, tk, tv, ctas, st)
-                           : few_go<T, kOwnForm>(a, tk, tv, ctas, st);
-}
-template <class Sh> FewShape few_shape() { return FewShape{kRows, Sh::kTile, Sh::kCtas}; }
 
 }  // namespace
 
-FewShape chunk_few_shape(int dtype, CacheForm form) {
-  if (form == kOwnForm) return few_shape<Shape<__half, kOwnForm>>();
-  if (form == kQ4Form)
-    return dtype == KV_F32 ? few_shape<Shape<float, kQ4Form>>() : few_shape<Shape<__half, kQ4Form>>();
-  return dtype == KV_F32 ? few_shape<Shape<float, kQ8Form>>() : few_shape<Shape<__half, kQ8Form>>();
+FewShape chunk_few_shape(int dtype, bool q8) {
+  using Own = Shape<__half, false>;
+  using Codes = Shape<__half, true>;
+  using Codes32 = Shape<float, true>;
+  return !q8                ? FewShape{kRows, Own::kTile, Own::kCtas}
+         : dtype == KV_F32 ? FewShape{kRows, Codes32::kTile, Codes32::kCtas}
+                           : FewShape{kRows, Codes::kTile, Codes::kCtas};
 }
 
-cudaError_t launch_chunk_few(int dtype, CacheForm form, const ChunkArgs &a, const CUtensorMap &tk,
+cudaError_t launch_chunk_few(int dtype, bool q8, const ChunkArgs &a, const CUtensorMap &tk,
                              const CUtensorMap &tv, int ctas, cudaStream_t st) {
-  if (dtype == KV_F32)
-    return form == kQ4Form ? few_go<float, kQ4Form>(a, tk, tv, ctas, st)
-                           : few_go<float, kQ8Form>(a, tk, tv, ctas, st);
-  return dtype == KV_F16 ? few_type<__half>(form, a, tk, tv, ctas, st)
-                         : few_type<__nv_bfloat16>(form, a, tk, tv, ctas, st);
+  if (dtype == KV_F32) return few_go<float, true>(a, tk, tv, ctas, st);
+  if (dtype == KV_F16)
+    return q8 ? few_go<__half, true>(a, tk, tv, ctas, st)
+              : few_go<__half, false>(a, tk, tv, ctas, st);
+  return q8 ? few_go<__nv_bfloat16, true>(a, tk, tv, ctas, st)
+            : few_go<__nv_bfloat16, false>(a, tk, tv, ctas, st);
 }
 
 }  // namespace kvs

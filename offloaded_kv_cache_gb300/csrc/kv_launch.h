@@ -90,15 +90,19 @@ enum ChunkForm { kWide, kPair, kPair8, kSolo };
 cudaError_t launch_chunk_mma(int dtype, ChunkForm form, const ChunkArgs &a, const CUtensorMap &tq,
                              const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
                              cudaStream_t st);
-// few rows: 16-bit q over a 16-bit cache or one of codes, fp32 q over one of codes; the maps are of K and V or the codes
+// few rows: 16-bit q over a 16-bit or the 8-bit cache, fp32 q over the 8-bit
+// cache; the maps are of K and V or the codes
 struct FewShape {
   int rows;    // of a unit
   int tile;    // tokens per KV tile
   int per_sm;  // resident CTAs
 };
-FewShape chunk_few_shape(int dtype, CacheForm form);
-cudaError_t launch_chunk_few(int dtype, CacheForm form, const ChunkArgs &a, const CUtensorMap &tk,
+FewShape chunk_few_shape(int dtype, bool q8);
+cudaError_t launch_chunk_few(int dtype, bool q8, const ChunkArgs &a, const CUtensorMap &tk,
                              const CUtensorMap &tv, int ctas, cudaStream_t st);
+// few rows, and fp32 q, over the 4-bit cache
+FewShape chunk_q4_shape(int dtype);
+cudaError_t launch_chunk_q4(int dtype, const ChunkArgs &a, int ctas, cudaStream_t st);
 // the pages it needs into device memory in the shape's type (table: their new block table,
 // or null); 32 bits from the 4-bit cache only
 cudaError_t launch_chunk_stage(int dtype, CacheForm form, const ChunkArgs &c, void *k_out, void *v_out,
