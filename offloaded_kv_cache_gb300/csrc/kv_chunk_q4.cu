@@ -11,8 +11,8 @@
 // The products are 16 x 8 x 16, units 8 rows, as in kv_chunk_few.cu:
 //   S^T (16 tokens x 8 rows) = K Q^T: the products sum over the channels, in any order that
 //     K and Q share.  A thread's 16 bytes of codes are 32 channels of a token; a word's
-//     nibbles i and i + 4 lie in one half each of a register, so that one operation puts them into
-//     the mantissas of two f16 64 + n, n = c + 8, and one fma makes (64 + n) s - 72 s of them, exactly.
+//     nibbles i and i + 4 lie in one half each of a register, so that one operation puts
+//     them into the mantissas of two f16, and one fma makes c s / 8 of them, exactly.
 //   O^T (128 channels x 8 rows) += V^T P^T: pairs of two tokens' elements, a byte of two
 //     channels at a time.
 // Power bytes stay outside: K's multiplies the scores; V's joins the weight's exponent, weight
@@ -61,7 +61,7 @@ __device__ __forceinline__ uint32_t movm_t(uint32_t x) {
 }
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -77,26 +77,30 @@ __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_ca
 __device__ __forceinline__ uint32_t as_word(__half2 x) { return *reinterpret_cast<uint32_t *>(&x); }
 
 // The integers n = c + 8 of the low (odd: high) nibbles of bytes 0 and 2 of a word, less 8,
-// times their scales s: n is put into the mantissa of 64 + n, and (64 + n) s - 72 s, in one
-// fma, is exact (72 s has 8 significant bits, at most 32256).
+// times an eighth of their scales s.  n is put into the mantissa of 1024 + n (odd: 64 + n),
+// and (1024 + n) s / 8 - 129 s (odd: (64 + n) s / 8 - 9 s), in one fma, is exact: s is an
+// integer of 8 to 15 times a power of two, 129 * 15 has 11 bits, and 129 * 448 = 57792.
 struct Factor {
-  __half2 s, s72;  // s, -72 s of the two
+  __half2 s, even, odd;  // s / 8, -129 s, -9 s of the two
 };
 __device__ __forceinline__ Factor factor_of(uint32_t s) {
-  return Factor{as_half2(s), __hmul2(as_half2(s), as_half2(0xD480D480u))};
+  return Factor{__hmul2(as_half2(s), as_half2(0x30003000u)), __hmul2(as_half2(s), as_half2(0xD808D808u)),
+                __hmul2(as_half2(s), as_half2(0xC880C880u))};
 }
 // (One operation for mask and exponent, as long as both are in registers: of two immediates
 // the compiler makes two.  One token over 8 x 65536: 127 -> 110 us.)
 struct Bits {
-  uint32_t mask, one;
+  uint32_t mask[2], one[2];
   __device__ __forceinline__ Bits() {
-    asm volatile("mov.b32 %0, 0x00F000F0;" : "=r"(mask));
-    asm volatile("mov.b32 %0, 0x54005400;" : "=r"(one));
+    asm volatile("mov.b32 %0, 0x000F000F;" : "=r"(mask[0]));
+    asm volatile("mov.b32 %0, 0x00F000F0;" : "=r"(mask[1]));
+    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(one[0]));
+    asm volatile("mov.b32 %0, 0x54005400;" : "=r"(one[1]));
   }
   template <bool odd> __device__ __forceinline__ uint32_t pair(uint32_t w, const Factor &f) const {
     uint32_t n;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(n) : "r"(odd ? w : w << 4), "r"(mask), "r"(one));
-    return as_word(__hfma2(as_half2(n), f.s, f.s72));
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(n) : "r"(w), "r"(mask[odd]), "r"(one[odd]));
+    return as_word(__hfma2(as_half2(n), f.s, odd ? f.odd : f.even));
   }
 };
 // Which of the first eight tokens of sixteen a row of the products is (and of the last
@@ -174,32 +178,34 @@ __global__ void __launch_bounds__(kThreads, Shape<T>::kCtas)
       const int y = next_y;
       next_y = look_up();
       if (y == -2) flag_error(a.status, KV_ERR_BOUNDS);
-      const int y0 = __shfl_sync(0xFFFFFFFFu, y, 0), y1 = __shfl_sync(0xFFFFFFFFu, y, 1);
+      const uint32_t ok = __ballot_sync(0xFFFFFFFFu, y >= 0);  // (lanes 0 and 1)
+      // (sixteen tokens that are not there are copied from the cache's first, and not used)
+      const int y0 = uniform(__shfl_sync(0xFFFFFFFFu, max(y, 0), 0));
+      const int y1 = uniform(__shfl_sync(0xFFFFFFFFu, max(y, 0), 1));
       const uint32_t to = smem_u32(slots + fill * kSlot);
       fill = fill + 1 == kSlots ? 0 : fill + 1;
-      const uint32_t dst = to + chunk_at(lane >> 2, lane & 3);  // (eight tokens further: the same chunk)
+      if (ok) {
+        const uint32_t dst = to + chunk_at(lane >> 2, lane & 3);  // (eight tokens further: the same chunk)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = h ? y1 : y0;
-        if (row < 0) continue;
-        const long long from = (long long)row * kQ4Bytes + lane * 16;
-        const uint8_t *k = static_cast<const uint8_t *>(a.k) + from;
-        const uint8_t *v = static_cast<const uint8_t *>(a.v) + from;
+        for (int h = 0; h < 2; ++h) {
+          const long long from = (long long)(h ? y1 : y0) * kQ4Bytes + lane * 16;
+          const uint8_t *k = static_cast<const uint8_t *>(a.k) + from;
+          const uint8_t *v = static_cast<const uint8_t *>(a.v) + from;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          cp_async16(dst + (2 * h + i) * 8 * kQ4Bytes, k + i * 8 * kQ4Bytes);
-          cp_async16(dst + kVAt + (2 * h + i) * 8 * kQ4Bytes, v + i * 8 * kQ4Bytes);
+          for (int i = 0; i < 2; ++i) {
+            cp_async16(dst + (2 * h + i) * 8 * kQ4Bytes, k + i * 8 * kQ4Bytes);
+            cp_async16(dst + kVAt + (2 * h + i) * 8 * kQ4Bytes, v + i * 8 * kQ4Bytes);
+          }
         }
-      }
-      // scales: lanes 0 .. 15 K's, the others V's, eight lanes a half; powers: lanes 0 .. 3
-      const int row = lane & 8 ? y1 : y0, last = lane & 1 ? y1 : y0;
-      if (row >= 0)
+        // scales: lanes 0 .. 15 K's, the others V's, eight lanes a half; powers: lanes 0 .. 3
+        const int row = lane & 8 ? y1 : y0, last = lane & 1 ? y1 : y0;
         cp_async16(to + kGroupAt + lane * 16,
                    (lane & 16 ? a.v_group : a.k_group) + (long long)row * kQ4Scales + (lane & 7) * 16);
-      if (lane < 4 && last >= 0)
-        cp_async16(to + kPowerAt + lane * 16, (lane & 2 ? a.v_scale : a.k_scale) + last);
+        if (lane < 4)
+          cp_async16(to + kPowerAt + lane * 16, (lane & 2 ? a.v_scale : a.k_scale) + last);
+      }
       asm volatile("cp.async.commit_group;" ::: "memory");
-      return (y0 >= 0 ? 1u : 0u) | (y1 >= 0 ? 2u : 0u);
+      return ok;
     };
     uint32_t there[kSlots];  // of the steps in flight
 #pragma unroll
@@ -251,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T>::kCtas)
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          qf[h] = __shfl_sync(0xFFFFFFFFu, f, 4 * (2 * t4 + h));
+          qf[h] = 8.f * __shfl_sync(0xFFFFFFFFu, f, 4 * (2 * t4 + h));  // (K's values are eighths)
           tq[h] = g.len - g.n + token_of(a, g.r0 + min(2 * t4 + h, g.nrows - 1));
         }
       }
@@ -467,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T>::kCtas)
               make_float4(o[d][h], o[d][h + 2], o[d + 1][h], o[d + 1][h + 2]);
         if (g8 == 0) {
           sh.m[warp][n] = m[h];
-          sh.r[warp][n] = r[h] == -INFINITY ? -INFINITY : r[h] - kShift;
+          sh.r[warp][n] = r[h] == -INFINITY ? -INFINITY : r[h] - kShift + 3.f;  // (V's are eighths)
           sh.l[warp][n] = lt;
         }
       }
