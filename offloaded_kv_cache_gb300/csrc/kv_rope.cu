@@ -19,9 +19,14 @@
 namespace kvs {
 namespace {
 
-constexpr int kLanes = 16;        // of a vector: two times 4 channels each
-constexpr int kGroups = 16;       // half-warps per kv head of a block
-constexpr int kHeads = 4;         // q vectors in flight per half-warp
+#ifndef KVS_ROPE_VECTORS
+#define KVS_ROPE_VECTORS 12
+#endif
+
+constexpr int kLanes = 16;   // of a vector: two times 4 channels each
+constexpr int kGroups = 16;  // half-warps of a block
+constexpr int kFlight = 4;   // vectors in flight per half-warp
+constexpr int kKeyBytes = 64 * 1024;  // of keys that a block keeps for the index
 
 struct RopeArgs {
   const void *q, *k, *v;          // rows; null: left out
@@ -38,9 +43,11 @@ struct RopeArgs {
   float scale;
   int tile;                       // tokens per block: a page, or 16
   int per_token;                  // half-warps that share a token's vectors, a power of two
-  int heads;                      // kv heads a block walks
+  int heads;                      // kv heads of a block
   int blocks, parts;              // tiles per sequence, blocks per tile
-  Divisor by_blocks, by_parts;
+  int first_q;                    // vectors of a kv head before its q heads: its key, its value
+  int kinds;                      // vectors of a kv head
+  Divisor by_blocks, by_parts, by_kinds;
   int write_lens;
 };
 
@@ -118,18 +125,52 @@ __device__ __forceinline__ void turn(Piece<T> &p, const float (&c)[4], const flo
   p.w[1] = pack4(v, T{});
 }
 
-// Block (sequence, tile of tokens, kv heads): blockDim.x / 256 kv heads at a time, 16
-// half-warps each.  per_token half-warps share a token: its key (the first one), value
-// and the group's q heads.  A tile is a page where the index is kept, so that its keys
-// meet in one block, whose minima and maxima are taken over totalOrder keys in shared
-// memory, in any order.
+// The minimum and maximum of one word of the keys of `count` tokens, `stride` words apart, and
+// of what the index held: two channels of 16 bits, or one of 32.
+template <class T>
+__device__ __forceinline__ void word_bounds(const uint32_t *at, int stride, int count, bool old,
+                                            uint32_t *lo, uint32_t *hi) {
+  if constexpr (sizeof(T) == 2) {
+    uint32_t mn = old ? key16x2(*lo) : ~0u, mx = old ? key16x2(*hi) : 0;
+#pragma unroll 4
+    for (int i = 0; i < count; ++i) {
+      const uint32_t key = key16x2(at[i * stride]);
+      mn = __vminu2(mn, key);
+      mx = __vmaxu2(mx, key);
+    }
+    *lo = unkey16x2(mn);
+    *hi = unkey16x2(mx);
+  } else {
+    uint32_t mn = old ? key32(*lo) : ~0u, mx = old ? key32(*hi) : 0;
+#pragma unroll 4
+    for (int i = 0; i < count; ++i) {
+      const uint32_t key = key32(at[i * stride]);
+      mn = min(mn, key);
+      mx = max(mx, key);
+    }
+    *lo = unkey32(mn);
+    *hi = unkey32(mx);
+  }
+}
+
+// Block (sequence, tile of tokens, kv heads), a half-warp a vector.  per_token half-warps share
+// a token, whose sines and cosines each has once for all its vectors; of those, kFlight
+// are loaded before the first is turned and stored.  A tile is a page where the index is
+// kept, so that its keys meet in one block: they are left in shared memory too, and looked
+// over there, in totalOrder, at the end.
 template <class T, bool kInter>
-__global__ void __launch_bounds__(512) rope_kernel(const RopeArgs a) {
-  extern __shared__ uint32_t bounds[];  // [kv heads at a time][2][128], with an index only
+__global__ void __launch_bounds__(kLanes * kGroups) rope_kernel(const RopeArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];  // [token][kv head][128] keys, with an index only
   pdl_wait();
-  const int tid = threadIdx.x, l = tid % kLanes;
+  const int tid = threadIdx.x, l = tid % kLanes, grp = tid / kLanes;
   const int seq_tile = a.by_parts(blockIdx.x), part = (int)blockIdx.x - seq_tile * a.parts;
   const int b = a.by_blocks(seq_tile), j = seq_tile - b * a.blocks;
+  const bool turns = l < a.lanes;
+  double freq[4];
+  if (turns) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) freq[i] = a.freq[4 * l + i];
+  }
   RowSpan r{a.q_start[b], a.q_start[b + 1] - a.q_start[b], 0};
   if (a.bt) {
     r = append_span(a, b);
@@ -158,129 +199,92 @@ __global__ void __launch_bounds__(512) rope_kernel(const RopeArgs a) {
     if (ph < 0 || ph >= a.nphys) ph = -1;  // recorded by the sequence's first block
     slot0 = (r.len + lo) & (a.ps - 1);
   }
-  const bool turns = l < a.lanes;
   const int c0 = turns && !kInter ? 4 * l : 8 * l;
   const int c1 = turns && !kInter ? 4 * (a.lanes + l) : 8 * l + 4;
   uint64_t f[4] = {0, 0, 0, 0};
   if (turns) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = turns_of(a.freq[4 * l + i]);
+    for (int i = 0; i < 4; ++i) f[i] = turns_of(freq[i]);
   }
   using Word = typename Piece<T>::Word;
-  auto load = [&](const void *base, long long vec) {
-    const T *p = static_cast<const T *>(base) + vec * kHeadDim;
-    Piece<T> x;
-    x.w[0] = *reinterpret_cast<const Word *>(p + c0);
-    x.w[1] = *reinterpret_cast<const Word *>(p + c1);
-    return x;
-  };
-  auto store = [&](void *base, long long vec, const Piece<T> &x) {
-    T *p = static_cast<T *>(base) + vec * kHeadDim;
-    *reinterpret_cast<Word *>(p + c0) = x.w[0];
-    *reinterpret_cast<Word *>(p + c1) = x.w[1];
-  };
-  const int at_once = blockDim.x / (kLanes * kGroups), mine = tid / (kLanes * kGroups);
-  const int grp = tid / kLanes % kGroups, sub = grp & (a.per_token - 1);
-  const int first = grp / a.per_token, step = kGroups / a.per_token;
-  const int h_end = min(a.Hkv, (part + 1) * a.heads);
-  for (int h0 = part * a.heads; h0 < h_end; h0 += at_once) {
-    const int h = h0 + mine;
-    const bool on = h < h_end;
-    uint32_t *low = bounds + mine * 2 * kHeadDim, *high = low + kHeadDim;
-    if (a.mm) {
-      __syncthreads();
-      for (int i = tid % (kLanes * kGroups); i < kHeadDim; i += kLanes * kGroups) {
-        low[i] = ~0u;
-        high[i] = 0;
-      }
-      __syncthreads();
-    }
-    uint32_t mn[8], mx[8];
+  const int h0 = part * a.heads, heads = min(a.heads, a.Hkv - h0);
+  const int vectors = heads * a.kinds;
+  const int sub = grp & (a.per_token - 1);
+  for (int i = lo + grp / a.per_token; i < hi; i += kGroups / a.per_token) {
+    const long long row = r.q0 + i;
+    const int pos = a.at ? a.at[row] : r.len + i;
+    float c[4], s[4];
+    for (int v0 = sub; v0 < vectors; v0 += kFlight * a.per_token) {
+      Piece<T> x[kFlight];
+      T *dst[kFlight];
+      int kind[kFlight], head[kFlight];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      mn[i] = ~0u;
-      mx[i] = 0;
-    }
-    bool any = false;
-    for (int i = lo + first; on && i < hi; i += step) {
-      const long long row = r.q0 + i;
-      float c[4], s[4];
-      const int pos = a.at ? a.at[row] : r.len + i;
-      // (rows of the cache fit int32)
-      const long long to =
-          a.bt ? ((long long)ph * a.Hkv + h) * a.ps + slot0 + (i - lo) : row * a.Hkv + h;
-      const bool has = !a.bt || ph >= 0;
-      if (turns) {
+      for (int k = 0; k < kFlight; ++k) {
+        const int v = v0 + k * a.per_token;
+        dst[k] = nullptr;
+        if (v >= vectors) continue;
+        head[k] = a.by_kinds(v);
+        kind[k] = v - head[k] * a.kinds;
+        const int h = h0 + head[k];
+        const T *src;
+        if (kind[k] < a.first_q) {
+          // (without keys, the first vector would be the value: there is no such call)
+          src = static_cast<const T *>(kind[k] ? a.v : a.k) + (row * a.Hkv + h) * kHeadDim;
+          // (rows of the cache fit int32)
+          const long long to =
+              a.bt ? ((long long)ph * a.Hkv + h) * a.ps + slot0 + (i - lo) : row * a.Hkv + h;
+          if (a.bt && ph < 0) continue;
+          dst[k] = static_cast<T *>(kind[k] ? a.v_out : a.k_out) + to * kHeadDim;
+        } else {
+          const long long at = row * a.Hq + (long long)h * a.G + kind[k] - a.first_q;
+          src = static_cast<const T *>(a.q) + at * kHeadDim;
+          dst[k] = static_cast<T *>(a.q_out) + at * kHeadDim;
+        }
+        x[k].w[0] = *reinterpret_cast<const Word *>(src + c0);
+        x[k].w[1] = *reinterpret_cast<const Word *>(src + c1);
+      }
+      if (v0 == sub && turns) {  // (while the first vectors are on their way)
 #pragma unroll
         for (int k = 0; k < 4; ++k) cos_sin(f[k], pos, a.scale, c[k], s[k]);
       }
-      // vectors of the token: 0 its key, 1 its value, 2 .. the q heads
-      if (a.k && sub == 0 && has) {
-        Piece<T> x = load(a.k, row * a.Hkv + h);
-        if (turns) turn<T, kInter>(x, c, s);
-        store(a.k_out, to, x);
-        if (a.mm) {
-          float y[4];
-          any = true;
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            unpack4(x.w[w], y, T{});
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t key = key32(__float_as_uint(y[k]));
-              mn[4 * w + k] = min(mn[4 * w + k], key);
-              mx[4 * w + k] = max(mx[4 * w + k], key);
-            }
-          }
+      for (int k = 0; k < kFlight; ++k) {
+        if (!dst[k]) continue;
+        if (turns && !(kind[k] == 1 && a.first_q == 2)) turn<T, kInter>(x[k], c, s);
+        *reinterpret_cast<Word *>(dst[k] + c0) = x[k].w[0];
+        *reinterpret_cast<Word *>(dst[k] + c1) = x[k].w[1];
+        if (a.mm && kind[k] == 0) {
+          T *keep = reinterpret_cast<T *>(smem) + ((i - lo) * heads + head[k]) * kHeadDim;
+          *reinterpret_cast<Word *>(keep + c0) = x[k].w[0];
+          *reinterpret_cast<Word *>(keep + c1) = x[k].w[1];
         }
       }
-      if (a.v && sub == (1 & (a.per_token - 1)) && has)
-        store(a.v_out, to, load(a.v, row * a.Hkv + h));
-      if (a.q) {
-        const long long q0 = row * a.Hq + (long long)h * a.G;
-        for (int g = (sub - 2) & (a.per_token - 1); g < a.G; g += kHeads * a.per_token) {
-          Piece<T> x[kHeads];
-#pragma unroll
-          for (int k = 0; k < kHeads; ++k)
-            if (g + k * a.per_token < a.G) x[k] = load(a.q, q0 + g + k * a.per_token);
-#pragma unroll
-          for (int k = 0; k < kHeads; ++k)
-            if (g + k * a.per_token < a.G) {
-              if (turns) turn<T, kInter>(x[k], c, s);
-              store(a.q_out, q0 + g + k * a.per_token, x[k]);
-            }
-        }
-      }
-    }
-    if (!a.mm) continue;
-    if (any) {
-#pragma unroll
-      for (int w = 0; w < 2; ++w)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          atomicMin(&low[(w ? c1 : c0) + k], mn[4 * w + k]);
-          atomicMax(&high[(w ? c1 : c0) + k], mx[4 * w + k]);
-        }
-    }
-    __syncthreads();
-    if (on && ph >= 0 && grp < 2) {
-      // a half-warp writes the minima, another one the maxima, eight channels a lane
-      T *e = static_cast<T *>(a.mm) + (((long long)ph * a.Hkv + h) * 2 + grp) * kHeadDim + 8 * l;
-      const uint32_t *from = (grp ? high : low) + 8 * l;
-      float old[8], x[8];
-      if (slot0 > 0) load8(e, old);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        uint32_t key = from[k];
-        if (slot0 > 0) {
-          const uint32_t was = key32(__float_as_uint(old[k]));
-          key = grp ? max(key, was) : min(key, was);
-        }
-        x[k] = __uint_as_float(unkey32(key));
-      }
-      store8(e, x);
     }
   }
+  if (!a.mm || ph < 0) return;
+  __syncthreads();
+  constexpr int kWords = kHeadDim * sizeof(T) / 4;
+  for (int i = tid; i < heads * kWords; i += kLanes * kGroups) {
+    const int h = i / kWords, w = i % kWords;
+    uint32_t *e = static_cast<uint32_t *>(a.mm) + (((long long)ph * a.Hkv + h0 + h) * 2) * kWords + w;
+    uint32_t mn = 0, mx = 0;
+    if (slot0 > 0) mn = e[0], mx = e[kWords];
+    word_bounds<T>(reinterpret_cast<const uint32_t *>(smem) + i, heads * kWords, hi - lo, slot0 > 0,
+                   &mn, &mx);
+    e[0] = mn;
+    e[kWords] = mx;
+  }
+}
+
+template <class K>
+cudaError_t rope_go(K kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                    const RopeArgs &a) {
+  if (smem > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeyBytes);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(kernel, grid, block, smem, st, a);
 }
 
 }  // namespace
@@ -332,34 +336,38 @@ cudaError_t launch_rope(const kv_shape *s, const kv_chunk *c, const kv_rope_plan
   a.per_token = 1;
   const int tokens = std::min({c->max_q_len, c->total_q, a.tile});
   while (2 * a.per_token * tokens <= kGroups) a.per_token *= 2;
-  a.heads = 1;
-  int at_once = 1;
-  if (ctx_out && ctx_out == ctx && a.blocks == 1) {
-    // one block per sequence: it can write the lengths that it alone reads
-    a.heads = a.Hkv;
-    at_once = std::min(2, a.Hkv);
-  }
+  a.first_q = (k ? 1 : 0) + (v ? 1 : 0);
+  a.kinds = a.first_q + (q ? a.G : 0);
+  a.by_kinds = Divisor::of(a.kinds);
+  // kv heads of a block: a dozen vectors a half-warp, or as many half-warps as vectors; no
+  // more than whose keys the shared memory takes (a page of 128 tokens in fp32 is 64 KB)
+  a.heads = std::max(1, (a.per_token > 1 ? a.per_token : KVS_ROPE_VECTORS) / a.kinds);
+  const int key_bytes = tokens * kHeadDim * (s->dtype == KV_F32 ? 4 : 2);  // of a kv head's
+  if (ctx_out && ctx_out == ctx && a.blocks == 1)
+    a.heads = a.Hkv;  // one block per sequence: it can write the lengths that it alone reads
+  if (mm) a.heads = std::min(a.heads, kKeyBytes / key_bytes);
+  a.heads = std::min(a.heads, a.Hkv);
   a.parts = (a.Hkv + a.heads - 1) / a.heads;
   a.by_blocks = Divisor::of(a.blocks);
   a.by_parts = Divisor::of(a.parts);
   const bool later = ctx_out && ctx_out == ctx && (a.blocks > 1 || a.parts > 1);
   a.write_lens = ctx_out && !later;
-  const dim3 grid((unsigned)(a.blocks * s->batch * a.parts)), block(kLanes * kGroups * at_once);
-  const size_t smem = mm ? (size_t)at_once * 2 * kHeadDim * 4 : 0;
+  const dim3 grid((unsigned)(a.blocks * s->batch * a.parts)), block(kLanes * kGroups);
+  const size_t smem = mm ? (size_t)a.heads * key_bytes : 0;
   const bool inter = rope && rope->interleaved;
   cudaError_t e;
   switch (s->dtype) {
     case KV_F32:
-      e = inter ? launch_pdl(rope_kernel<float, true>, grid, block, smem, st, a)
-                : launch_pdl(rope_kernel<float, false>, grid, block, smem, st, a);
+      e = inter ? rope_go(rope_kernel<float, true>, grid, block, smem, st, a)
+                : rope_go(rope_kernel<float, false>, grid, block, smem, st, a);
       break;
     case KV_F16:
-      e = inter ? launch_pdl(rope_kernel<__half, true>, grid, block, smem, st, a)
-                : launch_pdl(rope_kernel<__half, false>, grid, block, smem, st, a);
+      e = inter ? rope_go(rope_kernel<__half, true>, grid, block, smem, st, a)
+                : rope_go(rope_kernel<__half, false>, grid, block, smem, st, a);
       break;
     default:
-      e = inter ? launch_pdl(rope_kernel<__nv_bfloat16, true>, grid, block, smem, st, a)
-                : launch_pdl(rope_kernel<__nv_bfloat16, false>, grid, block, smem, st, a);
+      e = inter ? rope_go(rope_kernel<__nv_bfloat16, true>, grid, block, smem, st, a)
+                : rope_go(rope_kernel<__nv_bfloat16, false>, grid, block, smem, st, a);
   }
   if (e == cudaSuccess && later)
     e = launch_pdl(advance_kernel<RopeArgs>, dim3(s->batch), dim3(256), 0, st, a);
