@@ -19,13 +19,14 @@
 namespace kvs {
 namespace {
 
-#ifndef KVS_ROPE_VECTORS
-#define KVS_ROPE_VECTORS 12
+#ifndef KVS_ROPE_BYTES
+#define KVS_ROPE_BYTES 6144
 #endif
 
 constexpr int kLanes = 16;   // of a vector: two times 4 channels each
-constexpr int kGroups = 16;  // half-warps of a block
+constexpr int kMaxGroups = 32;  // half-warps of a block: 16, or 32 for pages of more tokens
 constexpr int kFlight = 4;   // vectors in flight per half-warp
+constexpr int kPairs = kHeadDim / 2;
 constexpr int kKeyBytes = 64 * 1024;  // of keys that a block keeps for the index
 
 struct RopeArgs {
@@ -45,9 +46,7 @@ struct RopeArgs {
   int per_token;                  // half-warps that share a token's vectors, a power of two
   int heads;                      // kv heads of a block
   int blocks, parts;              // tiles per sequence, blocks per tile
-  int first_q;                    // vectors of a kv head before its q heads: its key, its value
-  int kinds;                      // vectors of a kv head
-  Divisor by_blocks, by_parts, by_kinds;
+  Divisor by_blocks, by_parts;
   int write_lens;
 };
 
@@ -153,24 +152,25 @@ __device__ __forceinline__ void word_bounds(const uint32_t *at, int stride, int 
   }
 }
 
-// Block (sequence, tile of tokens, kv heads), a half-warp a vector.  per_token half-warps share
-// a token, whose sines and cosines each has once for all its vectors; of those, kFlight
-// are loaded before the first is turned and stored.  A tile is a page where the index is
-// kept, so that its keys meet in one block: they are left in shared memory too, and looked
-// over there, in totalOrder, at the end.
+// Block (sequence, tile of tokens, kv heads), 16 or 32 tokens of the tile at a time: first a
+// thread a pair takes the tokens' sines and cosines into shared memory, then a half-warp
+// a vector turns and stores, kFlight vectors loaded before the first is stored; per_token
+// half-warps share a token.  A tile is a page where the index is kept, so that its keys meet
+// in one block: they are left in shared memory too, and looked over there, in totalOrder, at
+// the end.
 template <class T, bool kInter>
-__global__ void __launch_bounds__(kLanes * kGroups) rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kLanes * kMaxGroups, sizeof(T) == 2 ? 2 : 1) rope_kernel(const RopeArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];  // [token][kv head][128] keys, with an index only
+  __shared__ __align__(16) float cosine[kMaxGroups][kPairs], sine[kMaxGroups][kPairs];
   pdl_wait();
   const int tid = threadIdx.x, l = tid % kLanes, grp = tid / kLanes;
+  const int groups = blockDim.x / kLanes, at_once = groups / a.per_token;  // tokens at a time
   const int seq_tile = a.by_parts(blockIdx.x), part = (int)blockIdx.x - seq_tile * a.parts;
   const int b = a.by_blocks(seq_tile), j = seq_tile - b * a.blocks;
   const bool turns = l < a.lanes;
-  double freq[4];
-  if (turns) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) freq[i] = a.freq[4 * l + i];
-  }
+  const int pair = tid % kPairs;
+  double freq = 0.0;
+  if (pair < 4 * a.lanes) freq = a.freq[pair];
   RowSpan r{a.q_start[b], a.q_start[b + 1] - a.q_start[b], 0};
   if (a.bt) {
     r = append_span(a, b);
@@ -201,70 +201,72 @@ __global__ void __launch_bounds__(kLanes * kGroups) rope_kernel(const RopeArgs a
   }
   const int c0 = turns && !kInter ? 4 * l : 8 * l;
   const int c1 = turns && !kInter ? 4 * (a.lanes + l) : 8 * l + 4;
-  uint64_t f[4] = {0, 0, 0, 0};
-  if (turns) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = turns_of(freq[i]);
-  }
+  const int h0 = part * a.heads, heads = min(a.heads, a.Hkv - h0), sub = grp & (a.per_token - 1);
   using Word = typename Piece<T>::Word;
-  const int h0 = part * a.heads, heads = min(a.heads, a.Hkv - h0);
-  const int vectors = heads * a.kinds;
-  const int sub = grp & (a.per_token - 1);
-  for (int i = lo + grp / a.per_token; i < hi; i += kGroups / a.per_token) {
-    const long long row = r.q0 + i;
-    const int pos = a.at ? a.at[row] : r.len + i;
-    float c[4], s[4];
-    for (int v0 = sub; v0 < vectors; v0 += kFlight * a.per_token) {
-      Piece<T> x[kFlight];
-      T *dst[kFlight];
-      int kind[kFlight], head[kFlight];
+  // A token's vectors: its keys, its values, q heads; K's and V's heads lie a page's tokens
+  // apart in the cache.
+  const int keys = a.k ? heads : 0, rows_kv = keys + (a.v ? heads : 0);
+  const int count = rows_kv + (a.q ? heads * a.G : 0), apart = a.bt ? a.ps * kHeadDim : kHeadDim;
+  const uint64_t f = turns_of(freq);
+  for (int i0 = lo; i0 < hi; i0 += at_once) {
+    const int tokens = min(at_once, hi - i0);
+    if (pair < 4 * a.lanes) {
+      for (int k = tid / kPairs; k < tokens; k += blockDim.x / kPairs)
+        cos_sin(f, a.at ? a.at[r.q0 + i0 + k] : r.len + i0 + k, a.scale, cosine[k][pair], sine[k][pair]);
+    }
+    __syncthreads();
+    const int mine = grp / a.per_token, i = i0 + mine;
+    if (mine < tokens) {
+      const long long row = r.q0 + i;
+      const long long in = (row * a.Hkv + h0) * kHeadDim;
+      const long long at = (row * a.Hq + (long long)h0 * a.G) * kHeadDim;
+      // (rows of the cache fit int32)
+      const long long out =
+          a.bt ? (((long long)ph * a.Hkv + h0) * a.ps + slot0 + (i - lo)) * kHeadDim : in;
+      const bool there = !a.bt || ph >= 0;
+      float c[4], s[4];
+      if (turns) {
+        const float4 u = *reinterpret_cast<const float4 *>(&cosine[mine][4 * l]);
+        const float4 v = *reinterpret_cast<const float4 *>(&sine[mine][4 * l]);
+        c[0] = u.x; c[1] = u.y; c[2] = u.z; c[3] = u.w;
+        s[0] = v.x; s[1] = v.y; s[2] = v.z; s[3] = v.w;
+      }
+#pragma unroll 1
+      for (int v0 = sub; v0 < count; v0 += kFlight * a.per_token) {
+        Piece<T> x[kFlight];
 #pragma unroll
-      for (int k = 0; k < kFlight; ++k) {
-        const int v = v0 + k * a.per_token;
-        dst[k] = nullptr;
-        if (v >= vectors) continue;
-        head[k] = a.by_kinds(v);
-        kind[k] = v - head[k] * a.kinds;
-        const int h = h0 + head[k];
-        const T *src;
-        if (kind[k] < a.first_q) {
-          // (without keys, the first vector would be the value: there is no such call)
-          src = static_cast<const T *>(kind[k] ? a.v : a.k) + (row * a.Hkv + h) * kHeadDim;
-          // (rows of the cache fit int32)
-          const long long to =
-              a.bt ? ((long long)ph * a.Hkv + h) * a.ps + slot0 + (i - lo) : row * a.Hkv + h;
-          if (a.bt && ph < 0) continue;
-          dst[k] = static_cast<T *>(kind[k] ? a.v_out : a.k_out) + to * kHeadDim;
-        } else {
-          const long long at = row * a.Hq + (long long)h * a.G + kind[k] - a.first_q;
-          src = static_cast<const T *>(a.q) + at * kHeadDim;
-          dst[k] = static_cast<T *>(a.q_out) + at * kHeadDim;
+        for (int k = 0; k < kFlight; ++k) {
+          const int v = v0 + k * a.per_token;
+          if (v >= count) continue;
+          const T *src = v < keys      ? static_cast<const T *>(a.k) + in + v * kHeadDim
+                         : v < rows_kv ? static_cast<const T *>(a.v) + in + (v - keys) * kHeadDim
+                                       : static_cast<const T *>(a.q) + at + (v - rows_kv) * kHeadDim;
+          x[k].w[0] = *reinterpret_cast<const Word *>(src + c0);
+          x[k].w[1] = *reinterpret_cast<const Word *>(src + c1);
         }
-        x[k].w[0] = *reinterpret_cast<const Word *>(src + c0);
-        x[k].w[1] = *reinterpret_cast<const Word *>(src + c1);
-      }
-      if (v0 == sub && turns) {  // (while the first vectors are on their way)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) cos_sin(f[k], pos, a.scale, c[k], s[k]);
-      }
-#pragma unroll
-      for (int k = 0; k < kFlight; ++k) {
-        if (!dst[k]) continue;
-        if (turns && !(kind[k] == 1 && a.first_q == 2)) turn<T, kInter>(x[k], c, s);
-        *reinterpret_cast<Word *>(dst[k] + c0) = x[k].w[0];
-        *reinterpret_cast<Word *>(dst[k] + c1) = x[k].w[1];
-        if (a.mm && kind[k] == 0) {
-          T *keep = reinterpret_cast<T *>(smem) + ((i - lo) * heads + head[k]) * kHeadDim;
-          *reinterpret_cast<Word *>(keep + c0) = x[k].w[0];
-          *reinterpret_cast<Word *>(keep + c1) = x[k].w[1];
+        for (int k = 0; k < kFlight; ++k) {
+          const int v = v0 + k * a.per_token;
+          if (v >= count || (v < rows_kv && !there)) continue;
+          T *dst = v < keys      ? static_cast<T *>(a.k_out) + out + (long long)v * apart
+                   : v < rows_kv ? static_cast<T *>(a.v_out) + out + (long long)(v - keys) * apart
+                                 : static_cast<T *>(a.q_out) + at + (v - rows_kv) * kHeadDim;
+          if (turns && (v < keys || v >= rows_kv)) turn<T, kInter>(x[k], c, s);
+          *reinterpret_cast<Word *>(dst + c0) = x[k].w[0];
+          *reinterpret_cast<Word *>(dst + c1) = x[k].w[1];
+          if (a.mm && v < keys) {
+            T *keep = reinterpret_cast<T *>(smem) + ((i - lo) * heads + v) * kHeadDim;
+            *reinterpret_cast<Word *>(keep + c0) = x[k].w[0];
+            *reinterpret_cast<Word *>(keep + c1) = x[k].w[1];
+          }
         }
       }
     }
+    __syncthreads();
   }
   if (!a.mm || ph < 0) return;
-  __syncthreads();
   constexpr int kWords = kHeadDim * sizeof(T) / 4;
-  for (int i = tid; i < heads * kWords; i += kLanes * kGroups) {
+  for (int i = tid; i < heads * kWords; i += blockDim.x) {
     const int h = i / kWords, w = i % kWords;
     uint32_t *e = static_cast<uint32_t *>(a.mm) + (((long long)ph * a.Hkv + h0 + h) * 2) * kWords + w;
     uint32_t mn = 0, mx = 0;
@@ -279,7 +281,7 @@ __global__ void __launch_bounds__(kLanes * kGroups) rope_kernel(const RopeArgs a
 template <class K>
 cudaError_t rope_go(K kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t st,
                     const RopeArgs &a) {
-  if (smem > 48 * 1024) {
+  if (smem > 16 * 1024) {  // (beside the angles)
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeyBytes);
     if (e != cudaSuccess) return e;
@@ -333,16 +335,18 @@ cudaError_t launch_rope(const kv_shape *s, const kv_chunk *c, const kv_rope_plan
   }
   a.tile = mm ? a.ps : 16;
   if (!rope_grid(s, c, bt != nullptr, a.tile, &a.blocks)) return cudaErrorInvalidConfiguration;
-  a.per_token = 1;
   const int tokens = std::min({c->max_q_len, c->total_q, a.tile});
-  while (2 * a.per_token * tokens <= kGroups) a.per_token *= 2;
-  a.first_q = (k ? 1 : 0) + (v ? 1 : 0);
-  a.kinds = a.first_q + (q ? a.G : 0);
-  a.by_kinds = Divisor::of(a.kinds);
-  // kv heads of a block: a dozen vectors a half-warp, or as many half-warps as vectors; no
-  // more than whose keys the shared memory takes (a page of 128 tokens in fp32 is 64 KB)
-  a.heads = std::max(1, (a.per_token > 1 ? a.per_token : KVS_ROPE_VECTORS) / a.kinds);
-  const int key_bytes = tokens * kHeadDim * (s->dtype == KV_F32 ? 4 : 2);  // of a kv head's
+  const int groups = tokens > 16 ? kMaxGroups : 16;
+  a.per_token = 1;
+  while (2 * a.per_token * tokens <= groups) a.per_token *= 2;
+  const int kinds = (k ? 1 : 0) + (v ? 1 : 0) + (q ? a.G : 0);
+  const int row_bytes = kHeadDim * (s->dtype == KV_F32 ? 4 : 2), key_bytes = tokens * row_bytes;
+  // kv heads of a block: some KVS_ROPE_BYTES of vectors a token, which share its angles (fewer
+  // where a tile is a large page), or as many half-warps as vectors; no more than whose keys the
+  // shared memory takes (a page of 128 tokens in fp32 is 64 KB).  (us at half / twice as
+  // many: append of 4 x 2048 tokens, 32/8 heads, bf16 24 / 30 against 22; fp32 36 / 53, here 36)
+  a.heads = (a.per_token > 1 ? a.per_token : KVS_ROPE_BYTES / row_bytes * 16 / a.tile) / kinds;
+  a.heads = std::max(1, a.heads);
   if (ctx_out && ctx_out == ctx && a.blocks == 1)
     a.heads = a.Hkv;  // one block per sequence: it can write the lengths that it alone reads
   if (mm) a.heads = std::min(a.heads, kKeyBytes / key_bytes);
@@ -352,7 +356,7 @@ cudaError_t launch_rope(const kv_shape *s, const kv_chunk *c, const kv_rope_plan
   a.by_parts = Divisor::of(a.parts);
   const bool later = ctx_out && ctx_out == ctx && (a.blocks > 1 || a.parts > 1);
   a.write_lens = ctx_out && !later;
-  const dim3 grid((unsigned)(a.blocks * s->batch * a.parts)), block(kLanes * kGroups);
+  const dim3 grid((unsigned)(a.blocks * s->batch * a.parts)), block(kLanes * groups);
   const size_t smem = mm ? (size_t)a.heads * key_bytes : 0;
   const bool inter = rope && rope->interleaved;
   cudaError_t e;
