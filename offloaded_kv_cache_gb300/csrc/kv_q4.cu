@@ -16,6 +16,10 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kLanesPerVec = 16;  // 8 channels a lane, two lanes a scale
 constexpr int kVecs = kThreads / kLanesPerVec;
+constexpr int kSteps = 2;  // vectors of K and of V in flight per half-warp
+#ifndef KVS_APPEND4_BLOCKS
+#define KVS_APPEND4_BLOCKS 2432  // 16 per SM
+#endif
 
 struct AppendArgs {
   const void *src[2];  // K, V
@@ -30,8 +34,13 @@ struct AppendArgs {
   int write_lens;
 };
 
-// Block (b, j) walks the n_b * Hkv (token, head) pairs of its sequence, K and V of each,
-// sixteen lanes a vector.
+// Block (b, j) walks the n_b * Hkv (token, head) pairs of its sequence in steps of kSteps *
+// 16, K and V of each pair, sixteen lanes a vector; the next step's loads are issued before
+// this step's vectors are quantised.
+template <class T> struct AppendStep {
+  uint4 w[kSteps][2][sizeof(T) / 2];
+  int page[kSteps], pos[kSteps];
+};
 template <class T>
 __global__ void __launch_bounds__(kThreads) q4_append_kernel(const AppendArgs a) {
   pdl_wait();
@@ -39,6 +48,25 @@ __global__ void __launch_bounds__(kThreads) q4_append_kernel(const AppendArgs a)
   const RowSpan r = append_span(a, b);
   const int sub = threadIdx.x / kLanesPerVec, l = threadIdx.x % kLanesPerVec;
   const int items = r.n > 0 ? r.n * a.Hkv : 0;  // <= total_q * Hq, an int32
+  const long long row0 = (long long)r.q0 * a.Hkv * kHeadDim + l * 8;
+  const T *src[2] = {static_cast<const T *>(a.src[0]) + row0, static_cast<const T *>(a.src[1]) + row0};
+  auto load = [&](AppendStep<T> &s, long long step) {
+#pragma unroll
+    for (int u = 0; u < kSteps; ++u) {
+      const long long it = step * (kVecs * kSteps) + u * kVecs + sub;
+      s.page[u] = -1;
+      if (it >= items) continue;
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+#pragma unroll
+        for (int c = 0; c < (int)sizeof(T) / 2; ++c)
+          s.w[u][w][c] = reinterpret_cast<const uint4 *>(src[w] + it * kHeadDim)[c];
+      s.pos[u] = r.len + a.by_heads((int)it);
+      s.page[u] = a.bt[(long long)b * a.maxP + (s.pos[u] >> a.ps_log2)];
+    }
+  };
+  AppendStep<T> now;
+  load(now, j);
   if (j == 0) {
     const bool ok = r.n >= 0 && pages_ok(a, b, r);  // ends in a barrier when it asks
     if (threadIdx.x == 0) {
@@ -48,36 +76,57 @@ __global__ void __launch_bounds__(kThreads) q4_append_kernel(const AppendArgs a)
   }
   pdl_trigger();
   const uint32_t mask = 0xFFFFu << (threadIdx.x & 16);
-  for (long long it = (long long)j * kVecs + sub; it < items; it += (long long)a.blocks * kVecs) {
-    const int tok = a.by_heads((int)it), h = (int)it - tok * a.Hkv, pos = r.len + tok;
-    const int ph = a.bt[(long long)b * a.maxP + (pos >> a.ps_log2)];
-    if (ph < 0 || ph >= a.nphys) continue;  // recorded by the sequence's first block
-    const long long vec = ((long long)ph * a.Hkv + h) * a.ps + (pos & (a.ps - 1));
+  for (long long step = j; step * (kVecs * kSteps) < items; step += a.blocks) {
+    AppendStep<T> next;
+    load(next, step + a.blocks);
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      float x[8];
-      load8(static_cast<const T *>(a.src[w]) + ((long long)r.q0 * a.Hkv + it) * kHeadDim + 8 * l, x);
-      uint32_t top = 0;
+    for (int u = 0; u < kSteps; ++u) {
+      // (a page out of range was recorded by the sequence's first block)
+      if (now.page[u] < 0 || now.page[u] >= a.nphys) continue;
+      const int it = (int)step * (kVecs * kSteps) + u * kVecs + sub;
+      const int h = it - (now.pos[u] - r.len) * a.Hkv;
+      const long long vec = ((long long)now.page[u] * a.Hkv + h) * a.ps + (now.pos[u] & (a.ps - 1));
+      // the largest magnitude of the 16 channels of a scale, of the vector
+      uint32_t group[2] = {q8_top(now.w[u][0]), q8_top(now.w[u][1])}, top[2];
+      if constexpr (sizeof(T) == 2) {  // K's and V's go through the lanes together
+        uint32_t both = group[0] | (group[1] << 16);
+        both = __vmaxu2(both, __shfl_xor_sync(mask, both, 1, kLanesPerVec));
+        group[0] = both & 0xFFFFu;
+        group[1] = both >> 16;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-      const uint32_t group = max(top, __shfl_xor_sync(mask, top, 1, kLanesPerVec));
-      top = group;
+        for (int off = 2; off < kLanesPerVec; off <<= 1)
+          both = __vmaxu2(both, __shfl_xor_sync(mask, both, off, kLanesPerVec));
+        top[0] = both & 0xFFFFu;
+        top[1] = both >> 16;
+      } else {
 #pragma unroll
-      for (int off = 2; off < kLanesPerVec; off <<= 1)
-        top = max(top, __shfl_xor_sync(mask, top, off, kLanesPerVec));
-      uint32_t code = 0x88888888u, scale = 0;
-      int byte = kQ4NanPower;
-      if (top < 0x7F800000u) {
-        const int e = q4_exponent(top, q8_min_exp<T>());
-        float s;
-        scale = q4_scale_code(__uint_as_float(group) * pow2f(-e), s);
-        code = q4_codes8(x, s, e, T{});
-        byte = e + 127;
+        for (int w = 0; w < 2; ++w) {
+          top[w] = group[w] = max(group[w], __shfl_xor_sync(mask, group[w], 1, kLanesPerVec));
+#pragma unroll
+          for (int off = 2; off < kLanesPerVec; off <<= 1)
+            top[w] = max(top[w], __shfl_xor_sync(mask, top[w], off, kLanesPerVec));
+        }
       }
-      *reinterpret_cast<uint32_t *>(a.codes[w] + vec * kQ4Bytes + 4 * l) = code;
-      if (!(l & 1)) a.scale[w][vec * kQ4Scales + l / 2] = (uint8_t)scale;
-      if (l == 0) a.power[w][vec] = (uint8_t)byte;
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const uint32_t most = q8_top_f32(top[w], T{});
+        uint32_t code = 0x88888888u, scale = 0;
+        int byte = kQ4NanPower;
+        if (most < 0x7F800000u) {
+          const int e = q4_exponent(most, q8_min_exp<T>());
+          float s, x[8];
+          load8(reinterpret_cast<const T *>(&now.w[u][w]), x);
+          const float y = __uint_as_float(q8_top_f32(group[w], T{})) * pow2f(-e);
+          scale = q4_scale_code(y, s);
+          code = q4_codes8(x, y, s, e, T{});
+          byte = e + 127;
+        }
+        *reinterpret_cast<uint32_t *>(a.codes[w] + vec * kQ4Bytes + 4 * l) = code;
+        if (!(l & 1)) a.scale[w][vec * kQ4Scales + l / 2] = (uint8_t)scale;
+        if (l == 0) a.power[w][vec] = (uint8_t)byte;
+      }
     }
+    now = next;
   }
 }
 
@@ -175,8 +224,8 @@ cudaError_t launch_q4_append(int dtype, const void *k_new, const void *v_new,
   a.total_q = total_q;
   a.max_q_len = max_q_len;
   const long long items = (long long)std::min(max_q_len, total_q) * Hkv;
-  const long long steps = (items + kVecs - 1) / kVecs;
-  a.blocks = (int)std::max(1LL, std::min(steps, (2432 + B - 1LL) / B));
+  const long long steps = (items + kVecs * kSteps - 1) / (kVecs * kSteps);
+  a.blocks = (int)std::max(1LL, std::min(steps, (KVS_APPEND4_BLOCKS + B - 1LL) / B));
   a.by_blocks = Divisor::of(a.blocks);
   a.by_heads = Divisor::of(Hkv);
   const bool later = ctx_out == ctx && a.blocks > 1;

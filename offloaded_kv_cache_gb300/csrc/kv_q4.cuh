@@ -38,31 +38,36 @@ __device__ __forceinline__ uint32_t q4_scale_code(float top, float &s) {
   if (7.f * s < top && code < 0x7Eu) s = e4m3_pair(++code).x;
   return code;
 }
-// Eight channels as nibbles c + 8, x0 in the lowest.  t = x / (s 2^e) + 1/2 + 8 + 2^-13 +
-// 2^10 has its integer part in bits 13 .. 16.  The quotient by a rounded reciprocal is off by
-// 2^-21 at most, and t is rounded to 2^-13: a tie stays at or above it, and 16-bit data,
-// which differ from a tie (8 significant bits) by 2^-11 of it at least, 2^-12 here, stay below.
-// fp32 data may differ by less: the integer found is compared with its two borders, which
-// are exact.
+// Eight channels as nibbles c + 8, x0 in the lowest; top: the largest magnitude of the scale's
+// channels times 2^-e.  t = x / (s 2^e) + 1/2 + 8 + 2^-13 + 2^10 has its integer part in
+// bits 13 .. 16.  The quotient by a rounded reciprocal is off by 2^-21 at most, and t is
+// rounded to 2^-13: a tie stays at or above it, and 16-bit data, which differ from a tie (8
+// significant bits) by 2^-11 of it at least, 2^-12 here, stay below.  fp32 data may differ by
+// less: the integer found is compared with its two borders, which are exact.
 template <class T>
-__device__ __forceinline__ uint32_t q4_codes8(const float (&x)[8], float s, int e, T) {
+__device__ __forceinline__ uint32_t q4_codes8(const float (&x)[8], float top, float s, int e, T) {
   const float down = pow2f(-e), f = s == 0.f ? 0.f : __frcp_rn(s) * down;
-  uint32_t w = 0;
+  float t[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    float t = fmaf(x[i], f, 1032.5f + 0x1p-13f);
-    t = fminf(fmaxf(t, 1025.5f), 1039.5f);  // (a vector whose power is at its limit)
+    t[i] = fmaf(x[i], f, 1032.5f + 0x1p-13f);
     if constexpr (sizeof(T) == 4) {
-      const float c = (float)((__float_as_uint(t) >> 13) & 15u) - 8.f, y = x[i] * down;
-      if (fmaf(c, s, -0.5f * s) > y) t -= 1.f;
-      else if (s != 0.f && fmaf(c, s, 0.5f * s) <= y) t += 1.f;
-      t = fminf(fmaxf(t, 1025.5f), 1039.5f);
+      t[i] = fminf(fmaxf(t[i], 1025.5f), 1039.5f);
+      const float c = (float)((__float_as_uint(t[i]) >> 13) & 15u) - 8.f, y = x[i] * down;
+      if (fmaf(c, s, -0.5f * s) > y) t[i] -= 1.f;
+      else if (s != 0.f && fmaf(c, s, 0.5f * s) <= y) t[i] += 1.f;
     }
-    const uint32_t u = __float_as_uint(t);
-    w |= (4 * i <= 13 ? u >> (13 - 4 * i < 0 ? 0 : 13 - 4 * i) : u << (4 * i - 13 < 0 ? 0 : 4 * i - 13)) &
-         (15u << (4 * i));
   }
-  return w;
+  if (sizeof(T) == 4 || 7.f * s < top) {  // (a vector whose power is at its limit)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = fminf(fmaxf(t[i], 1025.5f), 1039.5f);
+  }
+  // four nibbles side by side from bit 13 on
+  uint32_t a[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    a[i >> 2] += (__float_as_uint(t[i]) & 0x1E000u) << (4 * (i & 3));
+  return a[0] >> 13 | a[1] << 3;
 }
 // The factor of a vector's power byte; 255 is NaN.
 __device__ __forceinline__ float q4_power(uint32_t byte) { return q8_scale(byte); }
