@@ -55,6 +55,11 @@ __global__ void __launch_bounds__(kThreads) q4_append_kernel(const AppendArgs a)
     for (int u = 0; u < kSteps; ++u) {
       const long long it = step * (kVecs * kSteps) + u * kVecs + sub;
       s.page[u] = -1;
+      s.pos[u] = 0;
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+#pragma unroll
+        for (int c = 0; c < (int)sizeof(T) / 2; ++c) s.w[u][w][c] = make_uint4(0, 0, 0, 0);
       if (it >= items) continue;
 #pragma unroll
       for (int w = 0; w < 2; ++w)
@@ -75,58 +80,63 @@ __global__ void __launch_bounds__(kThreads) q4_append_kernel(const AppendArgs a)
     }
   }
   pdl_trigger();
-  const uint32_t mask = 0xFFFFu << (threadIdx.x & 16);
-  for (long long step = j; step * (kVecs * kSteps) < items; step += a.blocks) {
-    AppendStep<T> next;
-    load(next, step + a.blocks);
+  // (all lanes of a warp take part, those without a vector too)
+  auto quantise = [&](const AppendStep<T> &s, long long step) {
 #pragma unroll
     for (int u = 0; u < kSteps; ++u) {
-      // (a page out of range was recorded by the sequence's first block)
-      if (now.page[u] < 0 || now.page[u] >= a.nphys) continue;
-      const int it = (int)step * (kVecs * kSteps) + u * kVecs + sub;
-      const int h = it - (now.pos[u] - r.len) * a.Hkv;
-      const long long vec = ((long long)now.page[u] * a.Hkv + h) * a.ps + (now.pos[u] & (a.ps - 1));
       // the largest magnitude of the 16 channels of a scale, of the vector
-      uint32_t group[2] = {q8_top(now.w[u][0]), q8_top(now.w[u][1])}, top[2];
+      uint32_t group[2] = {q8_top(s.w[u][0]), q8_top(s.w[u][1])}, top[2];
       if constexpr (sizeof(T) == 2) {  // K's and V's go through the lanes together
         uint32_t both = group[0] | (group[1] << 16);
-        both = __vmaxu2(both, __shfl_xor_sync(mask, both, 1, kLanesPerVec));
+        both = __vmaxu2(both, __shfl_xor_sync(0xFFFFFFFFu, both, 1));
         group[0] = both & 0xFFFFu;
         group[1] = both >> 16;
 #pragma unroll
         for (int off = 2; off < kLanesPerVec; off <<= 1)
-          both = __vmaxu2(both, __shfl_xor_sync(mask, both, off, kLanesPerVec));
+          both = __vmaxu2(both, __shfl_xor_sync(0xFFFFFFFFu, both, off));
         top[0] = both & 0xFFFFu;
         top[1] = both >> 16;
       } else {
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-          top[w] = group[w] = max(group[w], __shfl_xor_sync(mask, group[w], 1, kLanesPerVec));
+          top[w] = group[w] = max(group[w], __shfl_xor_sync(0xFFFFFFFFu, group[w], 1));
 #pragma unroll
           for (int off = 2; off < kLanesPerVec; off <<= 1)
-            top[w] = max(top[w], __shfl_xor_sync(mask, top[w], off, kLanesPerVec));
+            top[w] = max(top[w], __shfl_xor_sync(0xFFFFFFFFu, top[w], off));
         }
       }
+      const int it = (int)step * (kVecs * kSteps) + u * kVecs + sub;
+      const int h = it - (s.pos[u] - r.len) * a.Hkv;
+      // (rows of the cache fit int32)
+      const int vec = (s.page[u] * a.Hkv + h) * a.ps + (s.pos[u] & (a.ps - 1));
+      // (a page out of range was recorded by the sequence's first block)
+      const bool there = s.page[u] >= 0 && s.page[u] < a.nphys;
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         const uint32_t most = q8_top_f32(top[w], T{});
-        uint32_t code = 0x88888888u, scale = 0;
-        int byte = kQ4NanPower;
-        if (most < 0x7F800000u) {
-          const int e = q4_exponent(most, q8_min_exp<T>());
-          float s, x[8];
-          load8(reinterpret_cast<const T *>(&now.w[u][w]), x);
-          const float y = __uint_as_float(q8_top_f32(group[w], T{})) * pow2f(-e);
-          scale = q4_scale_code(y, s);
-          code = q4_codes8(x, y, s, e, T{});
-          byte = e + 127;
-        }
-        *reinterpret_cast<uint32_t *>(a.codes[w] + vec * kQ4Bytes + 4 * l) = code;
-        if (!(l & 1)) a.scale[w][vec * kQ4Scales + l / 2] = (uint8_t)scale;
-        if (l == 0) a.power[w][vec] = (uint8_t)byte;
+        const int e = q4_exponent(most, q8_min_exp<T>());
+        float f, x[8];
+        load8(reinterpret_cast<const T *>(&s.w[u][w]), x);
+        const float y = __uint_as_float(q8_top_f32(group[w], T{})) * pow2f(-e);
+        const uint32_t scale = q4_scale_code(y, f), code = q4_codes8(x, y, f, e, T{});
+        if (!there) continue;
+        const bool nan = most >= 0x7F800000u;
+        *reinterpret_cast<uint32_t *>(a.codes[w] + (long long)vec * kQ4Bytes + 4 * l) =
+            nan ? 0x88888888u : code;
+        if (!(l & 1)) a.scale[w][(long long)vec * kQ4Scales + l / 2] = (uint8_t)(nan ? 0 : scale);
+        if (l == 0) a.power[w][vec] = (uint8_t)(nan ? kQ4NanPower : e + 127);
       }
     }
-    now = next;
+  };
+  for (long long step = j; step * (kVecs * kSteps) < items;) {
+    AppendStep<T> next;
+    load(next, step + a.blocks);
+    quantise(now, step);
+    step += a.blocks;
+    if (step * (kVecs * kSteps) >= items) break;
+    load(now, step + a.blocks);
+    quantise(next, step);
+    step += a.blocks;
   }
 }
 

@@ -38,15 +38,21 @@ __device__ __forceinline__ uint32_t q4_scale_code(float top, float &s) {
   if (7.f * s < top && code < 0x7Eu) s = e4m3_pair(++code).x;
   return code;
 }
+// within 2^-23 of 1 / x
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 // Eight channels as nibbles c + 8, x0 in the lowest; top: the largest magnitude of the scale's
 // channels times 2^-e.  t = x / (s 2^e) + 1/2 + 8 + 2^-13 + 2^10 has its integer part in
-// bits 13 .. 16.  The quotient by a rounded reciprocal is off by 2^-21 at most, and t is
+// bits 13 .. 16.  The quotient by an approximate reciprocal is off by 2^-19 at most, and t is
 // rounded to 2^-13: a tie stays at or above it, and 16-bit data, which differ from a tie (8
 // significant bits) by 2^-11 of it at least, 2^-12 here, stay below.  fp32 data may differ by
-// less: the integer found is compared with its two borders, which are exact.
+// less: the integer found is compared with its two borders, which are exact.  (All lanes call.)
 template <class T>
 __device__ __forceinline__ uint32_t q4_codes8(const float (&x)[8], float top, float s, int e, T) {
-  const float down = pow2f(-e), f = s == 0.f ? 0.f : __frcp_rn(s) * down;
+  const float down = pow2f(-e), f = s == 0.f ? 0.f : rcp(s) * down;
   float t[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -58,7 +64,7 @@ __device__ __forceinline__ uint32_t q4_codes8(const float (&x)[8], float top, fl
       else if (s != 0.f && fmaf(c, s, 0.5f * s) <= y) t[i] += 1.f;
     }
   }
-  if (sizeof(T) == 4 || 7.f * s < top) {  // (a vector whose power is at its limit)
+  if (sizeof(T) == 4 || __any_sync(0xFFFFFFFFu, 7.f * s < top)) {  // (a power at its limit)
 #pragma unroll
     for (int i = 0; i < 8; ++i) t[i] = fminf(fmaxf(t[i], 1025.5f), 1039.5f);
   }
