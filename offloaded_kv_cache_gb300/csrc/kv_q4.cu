@@ -16,7 +16,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kLanesPerVec = 16;  // 8 channels a lane, two lanes a scale
 constexpr int kVecs = kThreads / kLanesPerVec;
-constexpr int kSteps = 2;  // vectors of K and of V in flight per half-warp
+#ifndef KVS_APPEND4_F32_STEPS
+#define KVS_APPEND4_F32_STEPS 1
+#endif
 #ifndef KVS_APPEND4_BLOCKS
 #define KVS_APPEND4_BLOCKS 2432  // 16 per SM
 #endif
@@ -38,11 +40,14 @@ struct AppendArgs {
 // 16, K and V of each pair, sixteen lanes a vector; the next step's loads are issued before
 // this step's vectors are quantised.
 template <class T> struct AppendStep {
+  // vectors of K and of V in flight per half-warp
+  static constexpr int kSteps = sizeof(T) == 2 ? 2 : KVS_APPEND4_F32_STEPS;
   uint4 w[kSteps][2][sizeof(T) / 2];
   int page[kSteps], pos[kSteps];
 };
 template <class T>
 __global__ void __launch_bounds__(kThreads) q4_append_kernel(const AppendArgs a) {
+  constexpr int kSteps = AppendStep<T>::kSteps;
   pdl_wait();
   const int b = a.by_blocks(blockIdx.x), j = (int)blockIdx.x - b * a.blocks;
   const RowSpan r = append_span(a, b);
@@ -147,61 +152,96 @@ struct ReadArgs {
   int *status;
   long long nphys, out_pages;
   int Hkv, ps, ps_log2, maxP;
-  int items;   // of a sequence: (16-token tile, kv head) pairs
   int blocks;  // per sequence
   Divisor by_blocks, by_heads;
 };
 
-// Work item: (b, 16-token tile, kv head), a half-warp per token and lanes as above; a
-// block takes kUnits items, all loads issued before the first store.
+// Work item: (b, 16-token tile, kv head), a half-warp per token and lanes as above.  Block (b,
+// j) walks its sequence's items in steps of kUnits, the next step's codes in flight while this
+// one's are stored, and the pages of the step after that looked up.  (A block for each step
+// paid three dependent round trips by itself: 4 x 32768 tokens, 8 kv heads, bf16 102 us.)
+#ifndef KVS_READ4_BLOCKS
+#define KVS_READ4_BLOCKS 1216  // 8 per SM
+#endif
 constexpr int kUnits = 2;
+struct ReadPages {
+  int src[kUnits], to[kUnits];  // src < 0: nothing to do
+};
+struct ReadStep {
+  uint32_t code[kUnits][2], scale[kUnits][2], byte[kUnits][2];
+  int dst[kUnits];  // (rows of a cache fit int32)
+};
 template <class T>
 __global__ void __launch_bounds__(kThreads) q4_read_kernel(const ReadArgs a) {
   pdl_wait();
   const int t = threadIdx.x / kLanesPerVec, l = threadIdx.x % kLanesPerVec;
   const int b = a.by_blocks(blockIdx.x), j = (int)blockIdx.x - b * a.blocks;
   const int len = a.ctx[b];
-  uint32_t code[kUnits][2], scale[kUnits][2], byte[kUnits][2];
-  int dst[kUnits];  // (rows of a cache fit int32)
-#pragma unroll
-  for (int u = 0; u < kUnits; ++u) {
-    const int it = j * kUnits + u;
-    dst[u] = -1;
-    if (it >= a.items) continue;
-    const int tile = a.by_heads(it), h = it - tile * a.Hkv;
-    const int pos = tile * kTileTokens + t, page = (tile * kTileTokens) >> a.ps_log2;
-    if (len < 0 || (long long)len > (long long)a.maxP * a.ps) {
-      if (threadIdx.x == 0 && tile == 0) flag_error(a.status, KV_ERR_BOUNDS);
-      continue;
-    }
-    if (tile * kTileTokens >= len) continue;
-    const long long row = (long long)b * a.maxP + page;
-    const int src = a.bt[row], to = a.out_table[row];
-    if (to < 0) continue;
-    if (src < 0 || src >= a.nphys || to >= a.out_pages) {
-      if (threadIdx.x == 0) flag_error(a.status, KV_ERR_BOUNDS);
-      continue;
-    }
-    if (pos >= len) continue;
-    const int in = (src * a.Hkv + h) * a.ps + (pos & (a.ps - 1));
-    dst[u] = (to * a.Hkv + h) * a.ps + (pos & (a.ps - 1));
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      code[u][w] = *reinterpret_cast<const uint32_t *>(a.codes[w] + (long long)in * kQ4Bytes + 4 * l);
-      scale[u][w] = a.scale[w][(long long)in * kQ4Scales + l / 2];
-      byte[u][w] = a.power[w][in];
-    }
+  if (len < 0 || (long long)len > (long long)a.maxP * a.ps) {
+    if (threadIdx.x == 0) flag_error(a.status, KV_ERR_BOUNDS);
+    return;
   }
-  pdl_trigger();
+  // (tiles and heads of the block table's width count in int32)
+  const int items = (len + kTileTokens - 1) / kTileTokens * a.Hkv, stride = a.blocks * kUnits;
+  auto look_up = [&](ReadPages &p, long long it0) {
 #pragma unroll
-  for (int u = 0; u < kUnits; ++u) {
-    if (dst[u] < 0) continue;
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      float x[8];
-      q4_unpack8(code[u][w], e4m3_pair(scale[u][w]).x * q4_power(byte[u][w]), x);
-      store8(static_cast<T *>(a.out[w]) + (long long)dst[u] * kHeadDim + l * 8, x);
+    for (int u = 0; u < kUnits; ++u) {
+      p.src[u] = -1;
+      if (it0 + u >= items) continue;
+      const long long row = (long long)b * a.maxP + ((a.by_heads((int)it0 + u) * kTileTokens) >> a.ps_log2);
+      p.src[u] = a.bt[row];
+      p.to[u] = a.out_table[row];
     }
+  };
+  auto load = [&](ReadStep &s, const ReadPages &p, long long it0) {
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      s.dst[u] = -1;
+      if (it0 + u >= items || p.to[u] < 0) continue;
+      if (p.src[u] < 0 || p.src[u] >= a.nphys || p.to[u] >= a.out_pages) {
+        if (threadIdx.x == 0) flag_error(a.status, KV_ERR_BOUNDS);
+        continue;
+      }
+      const int tile = a.by_heads((int)it0 + u), h = (int)it0 + u - tile * a.Hkv;
+      const int pos = tile * kTileTokens + t;
+      if (pos >= len) continue;
+      const int in = (p.src[u] * a.Hkv + h) * a.ps + (pos & (a.ps - 1));
+      s.dst[u] = (p.to[u] * a.Hkv + h) * a.ps + (pos & (a.ps - 1));
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        s.code[u][w] = *reinterpret_cast<const uint32_t *>(a.codes[w] + (long long)in * kQ4Bytes + 4 * l);
+        s.scale[u][w] = a.scale[w][(long long)in * kQ4Scales + l / 2];
+        s.byte[u][w] = a.power[w][in];
+      }
+    }
+  };
+  auto store = [&](const ReadStep &s) {
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      if (s.dst[u] < 0) continue;
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+        q4_store8(static_cast<T *>(a.out[w]) + (long long)s.dst[u] * kHeadDim + l * 8, s.code[u][w],
+                  e4m3_pair(s.scale[u][w]).x * q4_power(s.byte[u][w]));
+    }
+  };
+  ReadPages pages;
+  ReadStep now, next;
+  long long it = (long long)j * kUnits;
+  look_up(pages, it);
+  load(now, pages, it);
+  look_up(pages, it + stride);
+  pdl_trigger();
+  while (it < items) {
+    load(next, pages, it + stride);
+    look_up(pages, it + 2 * stride);
+    store(now);
+    it += stride;
+    if (it >= items) break;
+    load(now, pages, it + stride);
+    look_up(pages, it + 2 * stride);
+    store(next);
+    it += stride;
   }
 }
 
@@ -234,6 +274,7 @@ cudaError_t launch_q4_append(int dtype, const void *k_new, const void *v_new,
   a.total_q = total_q;
   a.max_q_len = max_q_len;
   const long long items = (long long)std::min(max_q_len, total_q) * Hkv;
+  const int kSteps = dtype == KV_F32 ? AppendStep<float>::kSteps : AppendStep<__half>::kSteps;
   const long long steps = (items + kVecs * kSteps - 1) / (kVecs * kSteps);
   a.blocks = (int)std::max(1LL, std::min(steps, (KVS_APPEND4_BLOCKS + B - 1LL) / B));
   a.by_blocks = Divisor::of(a.blocks);
@@ -272,9 +313,9 @@ cudaError_t launch_q4_read(int dtype, const kv_q4_cache &c, const int32_t *bt, c
   a.ps = ps;
   a.ps_log2 = __builtin_ctz(ps);
   a.maxP = maxP;
-  // (the entry point has checked, by q8_grid_fits, that these count in int32)
-  a.items = (int)((long long)maxP * ps / kTileTokens * Hkv);
-  a.blocks = (a.items + kUnits - 1) / kUnits;
+  // (the entry point has checked, by q8_grid_fits, that the items count in int32)
+  const long long steps = ((long long)maxP * ps / kTileTokens * Hkv + kUnits - 1) / kUnits;
+  a.blocks = (int)std::max(1LL, std::min(steps, (KVS_READ4_BLOCKS + B - 1LL) / B));
   a.by_blocks = Divisor::of(a.blocks);
   a.by_heads = Divisor::of(Hkv);
   const dim3 grid((unsigned)((long long)a.blocks * B)), block(kThreads);

@@ -77,10 +77,36 @@ __device__ __forceinline__ uint32_t q4_codes8(const float (&x)[8], float top, fl
 }
 // The factor of a vector's power byte; 255 is NaN.
 __device__ __forceinline__ float q4_power(uint32_t byte) { return q8_scale(byte); }
-// eight nibbles -> the floats c * f
-__device__ __forceinline__ void q4_unpack8(uint32_t w, float f, float (&x)[8]) {
+// Eight nibbles n = c + 8 times f = s 2^e, stored as eight elements.  n is put into the
+// mantissa of 2^23 + n (f16: 1024 + n, bf16: 128 + n, two at a time); what is taken off again
+// leaves c, and c f is exact in every type.
+__device__ __forceinline__ void q4_store8(float *p, uint32_t w, float f) {
+  float x[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = (float)((int)((w >> (4 * i)) & 15u) - 8) * f;
+  for (int i = 0; i < 8; ++i)
+    x[i] = (__uint_as_float(((w >> (4 * i)) & 15u) | 0x4B000000u) - 8388616.f) * f;
+  store8(p, x);
+}
+__device__ __forceinline__ uint32_t q4_pair_of(uint32_t n, uint32_t f, __half) {  // n: at 0, 16
+  uint32_t x;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(x) : "r"(n | 0x64006400u), "r"(0xE408E408u));
+  asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(f));
+  return x;
+}
+__device__ __forceinline__ uint32_t q4_pair_of(uint32_t n, uint32_t f, __nv_bfloat16) {
+  uint32_t x;
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(n | 0x43004300u), "r"(0xC308C308u));
+  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(f));
+  return x;
+}
+template <class T> __device__ __forceinline__ void q4_store8(T *p, uint32_t w, float f) {
+  const uint32_t ff = pack2(f, f, T{});
+  uint32_t x[4];  // channels i and i + 4
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = q4_pair_of((w >> (4 * i)) & 0x000F000Fu, ff, T{});
+  *reinterpret_cast<uint4 *>(p) =
+      make_uint4(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410),
+                 __byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x7632));
 }
 
 }  // namespace kvs
