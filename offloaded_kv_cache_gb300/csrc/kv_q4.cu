@@ -209,8 +209,16 @@ __global__ void __launch_bounds__(kThreads) q4_read_kernel(const ReadArgs a) {
       s.dst[u] = (p.to[u] * a.Hkv + h) * a.ps + (pos & (a.ps - 1));
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
-        s.code[u][w] = *reinterpret_cast<const uint32_t *>(a.codes[w] + (long long)in * kQ4Bytes + 4 * l);
-        s.scale[u][w] = a.scale[w][(long long)in * kQ4Scales + l / 2];
+        const uint8_t *code = a.codes[w] + (long long)in * kQ4Bytes;
+        const uint8_t *scale = a.scale[w] + (long long)in * kQ4Scales;
+        if constexpr (sizeof(T) == 2) {
+          s.code[u][w] = *reinterpret_cast<const uint32_t *>(code + 4 * l);
+          s.scale[u][w] = scale[l / 2];
+        } else {
+          s.code[u][w] = *reinterpret_cast<const uint16_t *>(code + 2 * l) |
+                         *reinterpret_cast<const uint16_t *>(code + 32 + 2 * l) << 16;
+          s.scale[u][w] = scale[l / 4] | scale[4 + l / 4] << 8;
+        }
         s.byte[u][w] = a.power[w][in];
       }
     }
@@ -220,9 +228,17 @@ __global__ void __launch_bounds__(kThreads) q4_read_kernel(const ReadArgs a) {
     for (int u = 0; u < kUnits; ++u) {
       if (s.dst[u] < 0) continue;
 #pragma unroll
-      for (int w = 0; w < 2; ++w)
-        q4_store8(static_cast<T *>(a.out[w]) + (long long)s.dst[u] * kHeadDim + l * 8, s.code[u][w],
-                  e4m3_pair(s.scale[u][w]).x * q4_power(s.byte[u][w]));
+      for (int w = 0; w < 2; ++w) {
+        T *to = static_cast<T *>(a.out[w]) + (long long)s.dst[u] * kHeadDim;
+        const float2 f = e4m3_pair(s.scale[u][w]);
+        const float p = q4_power(s.byte[u][w]);
+        if constexpr (sizeof(T) == 2) {
+          q4_store8(to + l * 8, s.code[u][w], f.x * p);
+        } else {  // four channels of each half: a half-warp's stores have no gaps
+          *reinterpret_cast<float4 *>(to + 4 * l) = q4_values4(s.code[u][w], f.x * p);
+          *reinterpret_cast<float4 *>(to + 64 + 4 * l) = q4_values4(s.code[u][w] >> 16, f.y * p);
+        }
+      }
     }
   };
   ReadPages pages;

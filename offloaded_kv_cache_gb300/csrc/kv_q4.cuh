@@ -58,13 +58,13 @@ __device__ __forceinline__ uint32_t q4_codes8(const float (&x)[8], float top, fl
   for (int i = 0; i < 8; ++i) {
     t[i] = fmaf(x[i], f, 1032.5f + 0x1p-13f);
     if constexpr (sizeof(T) == 4) {
-      t[i] = fminf(fmaxf(t[i], 1025.5f), 1039.5f);
-      const float c = (float)((__float_as_uint(t[i]) >> 13) & 15u) - 8.f, y = x[i] * down;
-      if (fmaf(c, s, -0.5f * s) > y) t[i] -= 1.f;
-      else if (s != 0.f && fmaf(c, s, 0.5f * s) <= y) t[i] += 1.f;
+      const float c = __uint_as_float(__float_as_uint(t[i]) & ~0x1FFFu) - 1032.f;  // floor(t), less
+      const float y = x[i] * down, border = fmaf(c, s, -0.5f * s);
+      if (border > y) t[i] -= 1.f;
+      if (border + s <= y && s != 0.f) t[i] += 1.f;
     }
   }
-  if (sizeof(T) == 4 || __any_sync(0xFFFFFFFFu, 7.f * s < top)) {  // (a power at its limit)
+  if (__any_sync(0xFFFFFFFFu, 7.f * s < top)) {  // (a power at its limit)
 #pragma unroll
     for (int i = 0; i < 8; ++i) t[i] = fminf(fmaxf(t[i], 1025.5f), 1039.5f);
   }
@@ -77,15 +77,16 @@ __device__ __forceinline__ uint32_t q4_codes8(const float (&x)[8], float top, fl
 }
 // The factor of a vector's power byte; 255 is NaN.
 __device__ __forceinline__ float q4_power(uint32_t byte) { return q8_scale(byte); }
-// Eight nibbles n = c + 8 times f = s 2^e, stored as eight elements.  n is put into the
-// mantissa of 2^23 + n (f16: 1024 + n, bf16: 128 + n, two at a time); what is taken off again
-// leaves c, and c f is exact in every type.
-__device__ __forceinline__ void q4_store8(float *p, uint32_t w, float f) {
-  float x[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    x[i] = (__uint_as_float(((w >> (4 * i)) & 15u) | 0x4B000000u) - 8388616.f) * f;
-  store8(p, x);
+// n = c + 8 (below 16) times f = s 2^e: n is put into the mantissa of 2^23 + n (f16: 1024 + n,
+// bf16: 128 + n, two at a time); what is taken off again leaves c, and c f is exact in every
+// type.
+__device__ __forceinline__ float q4_value(uint32_t n, float f) {
+  return (__uint_as_float(n | 0x4B000000u) - 8388616.f) * f;
+}
+// four nibbles -> four floats
+__device__ __forceinline__ float4 q4_values4(uint32_t w, float f) {
+  return make_float4(q4_value(w & 15u, f), q4_value((w >> 4) & 15u, f), q4_value((w >> 8) & 15u, f),
+                     q4_value((w >> 12) & 15u, f));
 }
 __device__ __forceinline__ uint32_t q4_pair_of(uint32_t n, uint32_t f, __half) {  // n: at 0, 16
   uint32_t x;
@@ -98,6 +99,11 @@ __device__ __forceinline__ uint32_t q4_pair_of(uint32_t n, uint32_t f, __nv_bflo
   asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(n | 0x43004300u), "r"(0xC308C308u));
   asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(f));
   return x;
+}
+// eight nibbles, stored as eight elements
+__device__ __forceinline__ void q4_store8(float *p, uint32_t w, float f) {
+  reinterpret_cast<float4 *>(p)[0] = q4_values4(w, f);
+  reinterpret_cast<float4 *>(p)[1] = q4_values4(w >> 16, f);
 }
 template <class T> __device__ __forceinline__ void q4_store8(T *p, uint32_t w, float f) {
   const uint32_t ff = pack2(f, f, T{});
