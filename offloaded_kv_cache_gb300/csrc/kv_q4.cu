@@ -14,11 +14,7 @@ namespace kvs {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kLanesPerVec = 16;  // 8 channels a lane, two lanes a scale
-constexpr int kVecs = kThreads / kLanesPerVec;
-#ifndef KVS_APPEND4_F32_STEPS
-#define KVS_APPEND4_F32_STEPS 1
-#endif
+constexpr int kLanesPerVec = 16;  // of the read back: 8 channels a lane, two lanes a scale
 #ifndef KVS_APPEND4_BLOCKS
 #define KVS_APPEND4_BLOCKS 2432  // 16 per SM
 #endif
@@ -36,46 +32,47 @@ struct AppendArgs {
   int write_lens;
 };
 
-// Block (b, j) walks the n_b * Hkv (token, head) pairs of its sequence in steps of kSteps *
-// 16, K and V of each pair, sixteen lanes a vector; the next step's loads are issued before
-// this step's vectors are quantised.
+// Block (b, j) walks the n_b * Hkv (token, head) pairs of its sequence, K and V of each pair;
+// the next step's loads are issued before this step's vectors are quantised.  16-bit data: a
+// lane has the 16 channels of a scale, eight lanes a vector, so that what is computed per scale
+// and per vector is computed half as often (sixteen lanes a vector: 32 x 513 tokens, 32 kv
+// heads, 36 us).  fp32: 8 channels, sixteen lanes, whose loads lie closer together.
 template <class T> struct AppendStep {
-  // vectors of K and of V in flight per half-warp
-  static constexpr int kSteps = sizeof(T) == 2 ? 2 : KVS_APPEND4_F32_STEPS;
-  uint4 w[kSteps][2][sizeof(T) / 2];
-  int page[kSteps], pos[kSteps];
+  static constexpr int kChannels = sizeof(T) == 2 ? 16 : 8;  // of a lane
+  static constexpr int kLanes = kHeadDim / kChannels, kVecs = kThreads / kLanes;
+  static constexpr int kLoads = kChannels * (int)sizeof(T) / 16;
+  uint4 w[2][kLoads];
+  int page, pos;
 };
 template <class T>
 __global__ void __launch_bounds__(kThreads) q4_append_kernel(const AppendArgs a) {
-  constexpr int kSteps = AppendStep<T>::kSteps;
+  using Step = AppendStep<T>;
+  constexpr int kLanes = Step::kLanes, kVecs = Step::kVecs, kChannels = Step::kChannels;
   pdl_wait();
   const int b = a.by_blocks(blockIdx.x), j = (int)blockIdx.x - b * a.blocks;
   const RowSpan r = append_span(a, b);
-  const int sub = threadIdx.x / kLanesPerVec, l = threadIdx.x % kLanesPerVec;
+  const int sub = threadIdx.x / kLanes, l = threadIdx.x % kLanes;
   const int items = r.n > 0 ? r.n * a.Hkv : 0;  // <= total_q * Hq, an int32
-  const long long row0 = (long long)r.q0 * a.Hkv * kHeadDim + l * 8;
+  const long long row0 = (long long)r.q0 * a.Hkv * kHeadDim + l * kChannels;
   const T *src[2] = {static_cast<const T *>(a.src[0]) + row0, static_cast<const T *>(a.src[1]) + row0};
-  auto load = [&](AppendStep<T> &s, long long step) {
+  auto load = [&](Step &s, long long step) {
+    const long long it = step * kVecs + sub;
+    s.page = -1;
+    s.pos = 0;
 #pragma unroll
-    for (int u = 0; u < kSteps; ++u) {
-      const long long it = step * (kVecs * kSteps) + u * kVecs + sub;
-      s.page[u] = -1;
-      s.pos[u] = 0;
+    for (int w = 0; w < 2; ++w)
 #pragma unroll
-      for (int w = 0; w < 2; ++w)
+      for (int c = 0; c < Step::kLoads; ++c) s.w[w][c] = make_uint4(0, 0, 0, 0);
+    if (it >= items) return;
 #pragma unroll
-        for (int c = 0; c < (int)sizeof(T) / 2; ++c) s.w[u][w][c] = make_uint4(0, 0, 0, 0);
-      if (it >= items) continue;
+    for (int w = 0; w < 2; ++w)
 #pragma unroll
-      for (int w = 0; w < 2; ++w)
-#pragma unroll
-        for (int c = 0; c < (int)sizeof(T) / 2; ++c)
-          s.w[u][w][c] = reinterpret_cast<const uint4 *>(src[w] + it * kHeadDim)[c];
-      s.pos[u] = r.len + a.by_heads((int)it);
-      s.page[u] = a.bt[(long long)b * a.maxP + (s.pos[u] >> a.ps_log2)];
-    }
+      for (int c = 0; c < Step::kLoads; ++c)
+        s.w[w][c] = reinterpret_cast<const uint4 *>(src[w] + it * kHeadDim)[c];
+    s.pos = r.len + a.by_heads((int)it);
+    s.page = a.bt[(long long)b * a.maxP + (s.pos >> a.ps_log2)];
   };
-  AppendStep<T> now;
+  Step now;
   load(now, j);
   if (j == 0) {
     const bool ok = r.n >= 0 && pages_ok(a, b, r);  // ends in a barrier when it asks
@@ -86,59 +83,70 @@ __global__ void __launch_bounds__(kThreads) q4_append_kernel(const AppendArgs a)
   }
   pdl_trigger();
   // (all lanes of a warp take part, those without a vector too)
-  auto quantise = [&](const AppendStep<T> &s, long long step) {
+  auto quantise = [&](const Step &s, long long step) {
+    // the largest magnitude of the 16 channels of a scale, of the vector
+    uint32_t group[2], top[2];
+    if constexpr (sizeof(T) == 2) {  // K's and V's go through the lanes together
 #pragma unroll
-    for (int u = 0; u < kSteps; ++u) {
-      // the largest magnitude of the 16 channels of a scale, of the vector
-      uint32_t group[2] = {q8_top(s.w[u][0]), q8_top(s.w[u][1])}, top[2];
-      if constexpr (sizeof(T) == 2) {  // K's and V's go through the lanes together
-        uint32_t both = group[0] | (group[1] << 16);
-        both = __vmaxu2(both, __shfl_xor_sync(0xFFFFFFFFu, both, 1));
-        group[0] = both & 0xFFFFu;
-        group[1] = both >> 16;
+      for (int w = 0; w < 2; ++w)
+        group[w] = max(q8_top(reinterpret_cast<const uint4(&)[1]>(s.w[w][0])),
+                       q8_top(reinterpret_cast<const uint4(&)[1]>(s.w[w][1])));
+      uint32_t both = group[0] | (group[1] << 16);
 #pragma unroll
-        for (int off = 2; off < kLanesPerVec; off <<= 1)
-          both = __vmaxu2(both, __shfl_xor_sync(0xFFFFFFFFu, both, off));
-        top[0] = both & 0xFFFFu;
-        top[1] = both >> 16;
-      } else {
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          top[w] = group[w] = max(group[w], __shfl_xor_sync(0xFFFFFFFFu, group[w], 1));
-#pragma unroll
-          for (int off = 2; off < kLanesPerVec; off <<= 1)
-            top[w] = max(top[w], __shfl_xor_sync(0xFFFFFFFFu, top[w], off));
-        }
-      }
-      const int it = (int)step * (kVecs * kSteps) + u * kVecs + sub;
-      const int h = it - (s.pos[u] - r.len) * a.Hkv;
-      // (rows of the cache fit int32)
-      const int vec = (s.page[u] * a.Hkv + h) * a.ps + (s.pos[u] & (a.ps - 1));
-      // (a page out of range was recorded by the sequence's first block)
-      const bool there = s.page[u] >= 0 && s.page[u] < a.nphys;
+      for (int off = 1; off < kLanes; off <<= 1)
+        both = __vmaxu2(both, __shfl_xor_sync(0xFFFFFFFFu, both, off));
+      top[0] = both & 0xFFFFu;
+      top[1] = both >> 16;
+    } else {
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
-        const uint32_t most = q8_top_f32(top[w], T{});
-        const int e = q4_exponent(most, q8_min_exp<T>());
-        float f, x[8];
-        load8(reinterpret_cast<const T *>(&s.w[u][w]), x);
-        const float y = __uint_as_float(q8_top_f32(group[w], T{})) * pow2f(-e);
-        const uint32_t scale = q4_scale_code(y, f), code = q4_codes8(x, y, f, e, T{});
-        if (!there) continue;
-        const bool nan = most >= 0x7F800000u;
-        *reinterpret_cast<uint32_t *>(a.codes[w] + (long long)vec * kQ4Bytes + 4 * l) =
-            nan ? 0x88888888u : code;
-        if (!(l & 1)) a.scale[w][(long long)vec * kQ4Scales + l / 2] = (uint8_t)(nan ? 0 : scale);
-        if (l == 0) a.power[w][vec] = (uint8_t)(nan ? kQ4NanPower : e + 127);
+        top[w] = q8_top(s.w[w]);
+        top[w] = group[w] = max(top[w], __shfl_xor_sync(0xFFFFFFFFu, top[w], 1));
+#pragma unroll
+        for (int off = 2; off < kLanes; off <<= 1)
+          top[w] = max(top[w], __shfl_xor_sync(0xFFFFFFFFu, top[w], off));
       }
     }
+    const int it = (int)step * kVecs + sub;
+    const int h = it - (s.pos - r.len) * a.Hkv;
+    // (rows of the cache fit int32)
+    const int vec = (s.page * a.Hkv + h) * a.ps + (s.pos & (a.ps - 1));
+    // (a page out of range was recorded by the sequence's first block)
+    const bool there = s.page >= 0 && s.page < a.nphys;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const uint32_t most = q8_top_f32(top[w], T{});
+      const int e = q4_exponent(most, q8_min_exp<T>());
+      const float y = __uint_as_float(q8_top_f32(group[w], T{})) * pow2f(-e);
+      float f;
+      const uint32_t scale = q4_scale_code(y, f);
+      uint32_t code[kChannels / 8];
+#pragma unroll
+      for (int c = 0; c < kChannels / 8; ++c) {
+        float x[8];
+        load8(reinterpret_cast<const T *>(s.w[w]) + 8 * c, x);
+        code[c] = q4_codes8(x, y, f, e, T{});
+      }
+      if (!there) continue;
+      const bool nan = most >= 0x7F800000u;
+      uint8_t *to = a.codes[w] + (long long)vec * kQ4Bytes;
+      if constexpr (kChannels == 16) {
+        reinterpret_cast<uint2 *>(to)[l] =
+            nan ? make_uint2(0x88888888u, 0x88888888u) : make_uint2(code[0], code[1]);
+        a.scale[w][(long long)vec * kQ4Scales + l] = (uint8_t)(nan ? 0 : scale);
+      } else {
+        reinterpret_cast<uint32_t *>(to)[l] = nan ? 0x88888888u : code[0];
+        if (!(l & 1)) a.scale[w][(long long)vec * kQ4Scales + l / 2] = (uint8_t)(nan ? 0 : scale);
+      }
+      if (l == 0) a.power[w][vec] = (uint8_t)(nan ? kQ4NanPower : e + 127);
+    }
   };
-  for (long long step = j; step * (kVecs * kSteps) < items;) {
-    AppendStep<T> next;
+  for (long long step = j; step * kVecs < items;) {
+    Step next;
     load(next, step + a.blocks);
     quantise(now, step);
     step += a.blocks;
-    if (step * (kVecs * kSteps) >= items) break;
+    if (step * kVecs >= items) break;
     load(now, step + a.blocks);
     quantise(next, step);
     step += a.blocks;
@@ -290,8 +298,8 @@ cudaError_t launch_q4_append(int dtype, const void *k_new, const void *v_new,
   a.total_q = total_q;
   a.max_q_len = max_q_len;
   const long long items = (long long)std::min(max_q_len, total_q) * Hkv;
-  const int kSteps = dtype == KV_F32 ? AppendStep<float>::kSteps : AppendStep<__half>::kSteps;
-  const long long steps = (items + kVecs * kSteps - 1) / (kVecs * kSteps);
+  const int vecs = dtype == KV_F32 ? AppendStep<float>::kVecs : AppendStep<__half>::kVecs;
+  const long long steps = (items + vecs - 1) / vecs;
   a.blocks = (int)std::max(1LL, std::min(steps, (KVS_APPEND4_BLOCKS + B - 1LL) / B));
   a.by_blocks = Divisor::of(a.blocks);
   a.by_heads = Divisor::of(Hkv);
