@@ -60,6 +60,9 @@ int resolve_q4(const kv_shape *s, const kv_q4_cache *c, kv_q4_cache *dev) {
 #ifndef KVS_Q8_DIRECT_ROWS
 #define KVS_Q8_DIRECT_ROWS 768
 #endif
+#ifndef KVS_Q4_DIRECT_ROWS
+#define KVS_Q4_DIRECT_ROWS 768
+#endif
 // What a row may see, as far as the host knows.
 long long seen_tokens(const kv_shape *s, int window) {
   const long long tokens = (long long)s->max_pages_per_seq * s->page_size;
@@ -153,12 +156,14 @@ ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, CacheForm form) 
   } else if (pl.mma) {
     pl.tile = kChunkTile;
     pl.q8 &= packed <= KVS_Q8_DIRECT_ROWS;
-    pl.stage = (q8 && !pl.q8) || !hbm;
+    pl.q4 &= packed <= KVS_Q4_DIRECT_ROWS;
+    pl.stage = (q8 && !pl.q8) || (q4 && !pl.q4) || !hbm;
     // a Q tile holds whole tokens, for the TMA unit, where a token's heads fit
     pl.row_tile = G <= 128 ? 128 / G * G : 128;
     const long long seen = seen_tokens(s, c->window);
     const bool many = packed > pl.row_tile;
     pl.form = pl.q8                                               ? kPair8
+              : pl.q4                                             ? kPair4
               : seen <= (many ? KVS_SOLO_TOKENS : KVS_SOLO_FEW) ? kSolo
               : many                                              ? kWide
                                                                   : kPair;
@@ -166,6 +171,7 @@ ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, CacheForm form) 
     per_sm = pl.form == kSolo ? 2 : 1;
     if (pl.form != kSolo) pl.unit_cost = 2;
   } else {
+    pl.stage = q4;  // (from host memory: fp32 from device memory is for the kernel above)
     // few rows in units of 4 or 8, also while units of 64 would not fill the GPU
     const double units64 = std::min((double)s->batch * ((packed + 63) / 64),
                                     (double)c->total_q * G / 64 + s->batch);
@@ -175,8 +181,6 @@ ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, CacheForm form) 
     pl.rows = packed <= 4 ? 4 : packed <= KVS_F32_FEW_ROWS || !fills ? 8 : 64;
     if (pl.rows == 8) per_sm = 1;  // resident CTAs of its kernel (registers)
   }
-  pl.q4 &= pl.few;
-  if (q4 && !pl.q4) pl.stage = true;
   // units of all sequences: full ones and one more each; no more CTAs than
   // there can be tiles
   const double units = std::min((double)s->batch * ((packed + pl.rows - 1) / pl.rows),
@@ -350,11 +354,11 @@ int chunk_common(const kv_shape *s, const kv_chunk *c, const void *q, const void
     a.nphys = pages = pl.stage_pages;
   }
   CUtensorMap tq = {}, tk = {}, tv = {};
-  if ((pl.few && !pl.q4) || (pl.mma && !pl.few && !pl.q8)) {
+  if ((pl.few && !pl.q4) || (pl.mma && !pl.few && !pl.q8 && !pl.q4)) {
     if ((rc = page_map(s, pl.q8, pl.tile, a.k, pages, &tk)) != KV_OK) return rc;
     if ((rc = page_map(s, pl.q8, pl.tile, a.v, pages, &tv)) != KV_OK) return rc;
   }
-  if (pl.q4) {
+  if (pl.few && pl.q4) {
     e = launch_chunk_q4(s->dtype, a, pl.ctas, st);
   } else if (pl.few) {
     e = launch_chunk_few(s->dtype, pl.q8, a, tk, tv, pl.ctas, st);

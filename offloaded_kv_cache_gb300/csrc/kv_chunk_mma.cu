@@ -7,7 +7,7 @@
 //   1         loads K and V tiles (TMA, one box per page and 64 channels)
 //   1         issues the matrix products (one lane)
 //   2         mend V at the edges (below); the second loads Q
-//   4         (8-bit) expand tiles of codes into the ring's 16-bit tiles
+//   4         (8-bit, 4-bit) expand tiles of codes into the ring's 16-bit tiles
 // Per KV tile of 128 tokens and softmax group: S = Q K^T (128 x 128 x 128)
 // into TMEM; the group takes its maximum and exponentials and writes the
 // weights P in 16 bits over S, the type that the product takes with V's (a second
@@ -22,7 +22,8 @@
 //     product, softmax and product would otherwise be exposed.
 //   * kSolo: a unit is up to 128 rows and a CTA has one group; two CTAs per SM.
 //     For short contexts, where a unit's start and end are much of it.
-//   * kPair8: kPair over the 8-bit cache, up to kv_chunk_api.cu's limit of rows.
+//   * kPair8, kPair4: kPair over the 8-bit and the 4-bit cache, up to kv_chunk_api.cu's
+//     limits of rows.
 //
 // What bounds it, measured on one GB300 (a copy reaches 6.68 TB/s, a large bf16
 // matrix product 1.91 PFLOP/s):
@@ -57,6 +58,7 @@
 
 #include "kv_chunk.cuh"
 #include "kv_launch.h"
+#include "kv_q4.cuh"
 #include "kv_q8.cuh"
 #include "kv_umma.cuh"
 
@@ -66,23 +68,24 @@ namespace {
 constexpr int kTile = kChunkTile;
 constexpr int kTileBytes = kTile * kHeadDim * 2;  // 32 KB
 constexpr int kSlab = kTile * 128;                // 64 channels of a tile
-constexpr int kRawBytes = kTile * kHeadDim;       // a tile of codes
 constexpr float kMoveAt = 8.f;  // log2 of the largest weight before the maximum moves
 
 // How a CTA works: kMode is a ChunkForm.
 template <int kMode> struct Shape {
   static constexpr bool kHalves = kMode == kWide;  // each group has half a unit's rows
-  static constexpr bool kTurns = kMode == kPair || kMode == kPair8;  // the groups take tiles in turn
+  static constexpr bool kQ4 = kMode == kPair4, kQ8 = kMode == kPair8 || kQ4;  // codes; 4 bits
+  static constexpr bool kTurns = kMode == kPair || kQ8;  // the groups take tiles in turn
   static constexpr int kGroups = kMode == kSolo ? 1 : 2;
   static constexpr int kCtas = kMode == kSolo ? 2 : 1;  // per SM
-  static constexpr bool kQ8 = kMode == kPair8;
   static constexpr int kThreads = kMode == kSolo ? 256 : kQ8 ? 512 : 384;
   static constexpr int kQTiles = kMode == kWide ? 2 : 1;
   static constexpr int kQRows = 128;  // of a Q tile
   static constexpr int kRows = kQTiles * kQRows;
   static constexpr int kQBytes = kQRows * kHeadDim * 2;
   static constexpr int kStages = kMode == kWide ? 5 : kMode == kSolo ? 2 : kQ8 ? 4 : 6;  // 16-bit K and V tiles
-  static constexpr int kRaw = kQ8 ? 3 : 0;                           // tiles of codes
+  static constexpr int kRaw = kQ4 ? 5 : kQ8 ? 3 : 0;                 // tiles of codes
+  static constexpr int kCodeBytes = kQ4 ? kQ4Bytes : kHeadDim;       // of a vector
+  static constexpr int kRawBytes = kTile * kCodeBytes;
   static constexpr int kRingAt = kQTiles * kQBytes;
   static constexpr int kRawAt = kRingAt + kStages * kTileBytes;
   static constexpr int kTileArea = kRawAt + kRaw * kRawBytes;
@@ -108,7 +111,8 @@ template <int kMode> struct Control {
     float2 ml[2][Sh::kTurns ? Sh::kRows : 1];  // maximum and sum of each group's rows
   };
   // per tile of codes: its scale bytes, and its rows that hold a token
-  alignas(16) uint8_t scale[Sh::kQ8 ? Sh::kRaw : 1][Sh::kQ8 ? kTile : 16];
+  alignas(16) uint8_t scale[Sh::kQ8 ? Sh::kRaw : 1][Sh::kQ8 ? kTile : 16];  // 4-bit: powers
+  alignas(16) uint8_t group[Sh::kQ4 ? Sh::kRaw : 1][Sh::kQ4 ? kTile * kQ4Scales : 16];
   int raw_rows[Sh::kQ8 ? Sh::kRaw : 1], raw_bad[Sh::kQ8 ? Sh::kRaw : 1];
 };
 template <int kMode> constexpr int smem_bytes() {
@@ -117,6 +121,7 @@ template <int kMode> constexpr int smem_bytes() {
 static_assert(smem_bytes<kWide>() <= 227 * 1024, "shared memory");
 static_assert(smem_bytes<kPair>() <= 227 * 1024, "shared memory");
 static_assert(smem_bytes<kPair8>() <= 227 * 1024, "shared memory");
+static_assert(smem_bytes<kPair4>() <= 227 * 1024, "shared memory");
 static_assert(2 * (smem_bytes<kSolo>() + 1024) <= 228 * 1024, "shared memory");
 
 // What the V of a tile needs before the product reads it.
@@ -361,7 +366,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, Shape<kMode>::kCtas)
                      const __grid_constant__ CUtensorMap tk,
                      const __grid_constant__ CUtensorMap tv) {
   using Sh = Shape<kMode>;
-  constexpr bool kHalves = Sh::kHalves, kTurns = Sh::kTurns, kQ8 = Sh::kQ8;
+  constexpr bool kHalves = Sh::kHalves, kTurns = Sh::kTurns, kQ8 = Sh::kQ8, kQ4 = Sh::kQ4;
   constexpr int kLoad = 4 * Sh::kGroups;  // the loader's warp; the others' follow
   constexpr int kOAt = Sh::kOAt;
   constexpr int kStages = Sh::kStages;
@@ -766,13 +771,17 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, Shape<kMode>::kCtas)
                 if (w == 0) ctl.bad[tiles_loaded & 7] = (uint8_t)bad;
                 ctl.raw_rows[raw.s] = min(kTile, g.len - tile * kTile);
                 ctl.raw_bad[raw.s] = (int)bad;
-                mbar_arrive_expect_tx(bar, bytes * (kHeadDim + 1));
+                mbar_arrive_expect_tx(bar, bytes * (Sh::kCodeBytes + (kQ4 ? kQ4Scales : 0) + 1));
               }
               __syncwarp();
               if (have) {
-                bulk_load(smem_u32(smem) + Sh::kRawAt + raw.s * kRawBytes + lane * a.ps * kHeadDim,
-                          static_cast<const uint8_t *>(w ? a.v : a.k) + (long long)y * kHeadDim,
-                          a.ps * kHeadDim, bar);
+                bulk_load(smem_u32(smem) + Sh::kRawAt + raw.s * Sh::kRawBytes + lane * a.ps * Sh::kCodeBytes,
+                          static_cast<const uint8_t *>(w ? a.v : a.k) + (long long)y * Sh::kCodeBytes,
+                          a.ps * Sh::kCodeBytes, bar);
+                if constexpr (kQ4)
+                  bulk_load(smem_u32(&ctl.group[raw.s][lane * a.ps * kQ4Scales]),
+                            (w ? a.v_group : a.k_group) + (long long)y * kQ4Scales,
+                            a.ps * kQ4Scales, bar);
                 bulk_load(smem_u32(&ctl.scale[raw.s][lane * a.ps]),
                           (w ? a.v_scale : a.k_scale) + y, a.ps, bar);
               }
@@ -948,6 +957,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, Shape<kMode>::kCtas)
     // row's two swizzled slabs.
     if constexpr (kQ8) {
       const int ct = tid - 384, c16 = ct & 7, row0 = ct >> 3;
+      [[maybe_unused]] const Q4Bits<T> bits;
       while (next_list(false)) {
         bool live = true;
         const int nseg = share.nseg;
@@ -960,8 +970,6 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, Shape<kMode>::kCtas)
               break;
             }
             // rows row0 + 16 j: they share their swizzle
-            const uint4 *codes = reinterpret_cast<const uint4 *>(smem + Sh::kRawAt +
-                                                                 raw.s * kRawBytes) + ct;
             const uint8_t *scale = ctl.scale[raw.s] + row0;
             uint8_t *slab = ring + ld.s * kTileBytes + (c16 >> 2) * kSlab;
             uint8_t *to0 = slab + swz(row0, (c16 & 3) * 2), *to1 = slab + swz(row0, (c16 & 3) * 2 + 1);
@@ -969,23 +977,34 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, Shape<kMode>::kCtas)
             // four rows' codes are read ahead of their use (4 x 32k tokens, 32 rows,
             // bf16, 85 -> 74 us; the order that spares the stores' two-way bank
             // conflicts costs more in selections: 74 against 69)
-            uint4 codes_of[4];
-            uint32_t scale_of[4];
+            using Codes = std::conditional_t<kQ4, uint2, uint4>;
+            const Codes *codes = reinterpret_cast<const Codes *>(smem + Sh::kRawAt +
+                                                                 raw.s * Sh::kRawBytes) + ct;
+            Codes codes_of[4];
+            uint32_t scale_of[4], group_of[4];
+            const uint8_t *group = ctl.group[kQ4 ? raw.s : 0] + row0 * kQ4Scales + c16;
+            auto fetch = [&](int r) {
+              codes_of[r & 3] = codes[r * 128];
+              scale_of[r & 3] = scale[16 * r];
+              if constexpr (kQ4) group_of[r & 3] = group[16 * r * kQ4Scales];
+            };
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              codes_of[r] = codes[r * 128];
-              scale_of[r] = scale[16 * r];
-            }
+            for (int r = 0; r < 4; ++r) fetch(r);
 #pragma unroll
             for (int r = 0; r < kTile / 16; ++r) {
-              const uint4 w = codes_of[r & 3];
-              const uint32_t byte = scale_of[r & 3];
-              if (r + 4 < kTile / 16) {
-                codes_of[r & 3] = codes[(r + 4) * 128];
-                scale_of[r & 3] = scale[16 * (r + 4)];
-              }
+              const Codes w = codes_of[r & 3];
+              const uint32_t byte = scale_of[r & 3], factor = group_of[r & 3];
+              if (r + 4 < kTile / 16) fetch(r + 4);
               uint32_t x[8];
-              q8_expand(w, q8_factor<T>(byte), x, T{});
+              if constexpr (kQ4) {
+                const float f = e4m3_pair(factor).x * q4_power(byte);
+                const uint32_t ff = pack2(f, f, T{});
+                const uint4 lo = bits.expand(w.x, ff), hi = bits.expand(w.y, ff);
+                x[0] = lo.x; x[1] = lo.y; x[2] = lo.z; x[3] = lo.w;
+                x[4] = hi.x; x[5] = hi.y; x[6] = hi.z; x[7] = hi.w;
+              } else {
+                q8_expand(w, q8_factor<T>(byte), x, T{});
+              }
               nan |= byte == (uint32_t)kQ8NanScale;
               *reinterpret_cast<uint4 *>(to0 + r * 2048) = make_uint4(x[0], x[1], x[2], x[3]);
               *reinterpret_cast<uint4 *>(to1 + r * 2048) = make_uint4(x[4], x[5], x[6], x[7]);
@@ -1160,6 +1179,7 @@ cudaError_t mma_type(ChunkForm form, const ChunkArgs &a, const CUtensorMap &tq,
   switch (form) {
     case kPair: return mma_go<T, kPair>(a, tq, tk, tv, ctas, st);
     case kPair8: return mma_go<T, kPair8>(a, tq, tk, tv, ctas, st);
+    case kPair4: return mma_go<T, kPair4>(a, tq, tk, tv, ctas, st);
     case kSolo: return mma_go<T, kSolo>(a, tq, tk, tv, ctas, st);
     default: return mma_go<T, kWide>(a, tq, tk, tv, ctas, st);
   }

@@ -83,10 +83,10 @@ enum CacheForm { kOwnForm, kQ8Form, kQ4Form };
 // shares the work is cut into
 struct ChunkArgs;
 cudaError_t launch_chunk_core(const ChunkArgs &a, bool q8, int rows, int ctas, cudaStream_t st);
-// 16-bit q on the tensor cores, in one of four forms (kv_chunk_mma.cu): over 16-bit
+// 16-bit q on the tensor cores, in one of five forms (kv_chunk_mma.cu): over 16-bit
 // K/V in units of two Q tiles (kWide) or of one (kPair, kSolo), or over the 8-bit
-// cache in device memory (kPair8); the maps are of q and 16-bit K/V
-enum ChunkForm { kWide, kPair, kPair8, kSolo };
+// or the 4-bit cache in device memory (kPair8, kPair4); the maps are of q and 16-bit K/V
+enum ChunkForm { kWide, kPair, kPair8, kPair4, kSolo };
 cudaError_t launch_chunk_mma(int dtype, ChunkForm form, const ChunkArgs &a, const CUtensorMap &tq,
                              const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
                              cudaStream_t st);

@@ -231,6 +231,7 @@ __global__ void __launch_bounds__(kThreads) q4_read_kernel(const ReadArgs a) {
       }
     }
   };
+  const Q4Bits<T> bits;
   auto store = [&](const ReadStep &s) {
 #pragma unroll
     for (int u = 0; u < kUnits; ++u) {
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(kThreads) q4_read_kernel(const ReadArgs a) {
         const float2 f = e4m3_pair(s.scale[u][w]);
         const float p = q4_power(s.byte[u][w]);
         if constexpr (sizeof(T) == 2) {
-          q4_store8(to + l * 8, s.code[u][w], f.x * p);
+          q4_store8(to + l * 8, s.code[u][w], f.x * p, bits);
         } else {  // four channels of each half: a half-warp's stores have no gaps
           *reinterpret_cast<float4 *>(to + 4 * l) = q4_values4(s.code[u][w], f.x * p);
           *reinterpret_cast<float4 *>(to + 64 + 4 * l) = q4_values4(s.code[u][w] >> 16, f.y * p);

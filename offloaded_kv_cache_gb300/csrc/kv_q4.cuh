@@ -2,6 +2,8 @@
 // scale s for every 16 channels, one power of two (see the header for the format).
 #pragma once
 
+#include <type_traits>
+
 #include "kv_internal.cuh"
 #include "kv_q8.cuh"
 
@@ -88,31 +90,44 @@ __device__ __forceinline__ float4 q4_values4(uint32_t w, float f) {
   return make_float4(q4_value(w & 15u, f), q4_value((w >> 4) & 15u, f), q4_value((w >> 8) & 15u, f),
                      q4_value((w >> 12) & 15u, f));
 }
-__device__ __forceinline__ uint32_t q4_pair_of(uint32_t n, uint32_t f, __half) {  // n: at 0, 16
-  uint32_t x;
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(x) : "r"(n | 0x64006400u), "r"(0xE408E408u));
-  asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(f));
-  return x;
-}
-__device__ __forceinline__ uint32_t q4_pair_of(uint32_t n, uint32_t f, __nv_bfloat16) {
-  uint32_t x;
-  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(n | 0x43004300u), "r"(0xC308C308u));
-  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(f));
-  return x;
-}
+// The mask of nibbles 0 and 4 of a word, and the exponent of two 16-bit elements, in registers:
+// so that one operation takes both (of two immediates the compiler makes two).
+template <class T> struct Q4Bits {
+  uint32_t mask, one;
+  __device__ __forceinline__ Q4Bits() {
+    constexpr bool f16 = std::is_same<T, __half>::value;
+    asm volatile("mov.b32 %0, 0x000F000F;" : "=r"(mask));
+    asm volatile("mov.b32 %0, %1;" : "=r"(one) : "n"(f16 ? 0x64006400 : 0x43004300));
+  }
+  // c f of nibbles 0 and 4
+  __device__ __forceinline__ uint32_t pair(uint32_t w, uint32_t f) const {
+    uint32_t x;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(x) : "r"(w), "r"(mask), "r"(one));
+    if constexpr (std::is_same<T, __half>::value) {
+      asm("add.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(0xE408E408u));
+      asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(f));
+    } else {
+      asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(0xC308C308u));
+      asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(f));
+    }
+    return x;
+  }
+  // eight nibbles times f, in order
+  __device__ __forceinline__ uint4 expand(uint32_t w, uint32_t f) const {
+    const uint32_t x0 = pair(w, f), x1 = pair(w >> 4, f), x2 = pair(w >> 8, f), x3 = pair(w >> 12, f);
+    return make_uint4(__byte_perm(x0, x1, 0x5410), __byte_perm(x2, x3, 0x5410),
+                      __byte_perm(x0, x1, 0x7632), __byte_perm(x2, x3, 0x7632));
+  }
+};
+template <> struct Q4Bits<float> {};
 // eight nibbles, stored as eight elements
-__device__ __forceinline__ void q4_store8(float *p, uint32_t w, float f) {
+__device__ __forceinline__ void q4_store8(float *p, uint32_t w, float f, const Q4Bits<float> &) {
   reinterpret_cast<float4 *>(p)[0] = q4_values4(w, f);
   reinterpret_cast<float4 *>(p)[1] = q4_values4(w >> 16, f);
 }
-template <class T> __device__ __forceinline__ void q4_store8(T *p, uint32_t w, float f) {
-  const uint32_t ff = pack2(f, f, T{});
-  uint32_t x[4];  // channels i and i + 4
-#pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = q4_pair_of((w >> (4 * i)) & 0x000F000Fu, ff, T{});
-  *reinterpret_cast<uint4 *>(p) =
-      make_uint4(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410),
-                 __byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x7632));
+template <class T>
+__device__ __forceinline__ void q4_store8(T *p, uint32_t w, float f, const Q4Bits<T> &bits) {
+  *reinterpret_cast<uint4 *>(p) = bits.expand(w, pack2(f, f, T{}));
 }
 
 }  // namespace kvs

@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(kThreads) stage_kernel(const StageArgs a) {
     for (int w = 0; w < 2; ++w) {
       T *to = static_cast<T *>(a.out[w]) + (long long)dst[u] * kHeadDim + l * 8;
       if constexpr (kForm == kQ4Form) {
-        q4_store8(to, data[u][w].x, e4m3_pair(data[u][w].y).x * q4_power(byte[u][w]));
+        q4_store8(to, data[u][w].x, e4m3_pair(data[u][w].y).x * q4_power(byte[u][w]), Q4Bits<T>());
       } else if constexpr (kForm == kQ8Form) {
         float lo[4], hi[4], x[8];
         q8_unpack4(data[u][w].x, lo);
