@@ -60,8 +60,11 @@ int resolve_q4(const kv_shape *s, const kv_q4_cache *c, kv_q4_cache *dev) {
 #ifndef KVS_Q8_DIRECT_ROWS
 #define KVS_Q8_DIRECT_ROWS 768
 #endif
+// The 4-bit cache likewise.  (us, direct / expanded, 8 kv heads: 4 x 32k tokens in pages of 16,
+// bf16, 128 rows 82 / 168, 512 rows 203 / 209, 1024 rows 362 / 295; in pages of 64, 512 rows 173 /
+// 205, 1024 rows 309 / 288; 16 x 2k, f16, 512 rows 56 / 66, 1024 rows 89 / 85.)
 #ifndef KVS_Q4_DIRECT_ROWS
-#define KVS_Q4_DIRECT_ROWS 768
+#define KVS_Q4_DIRECT_ROWS 640
 #endif
 // What a row may see, as far as the host knows.
 long long seen_tokens(const kv_shape *s, int window) {
@@ -94,9 +97,13 @@ long long seen_tokens(const kv_shape *s, int window) {
 //     24 rows 29.7 / 26.9; 17 x 456, 32 kv heads: 8 rows 24 / 34, 16 rows 30 / 35
 //   fp32 q, 8-bit, 4 x 32k: 8 rows 70 / 410, 16 rows 106 / 655; 4 x 1.9k: 256 rows
 //     74 / 132; 8448 rows over 528, 2 kv heads: 289 / 112; window 90, 880 rows: 104 / 53
+//   4-bit (kv_chunk_q4.cu), 4 x 32k: 16 rows 50 / 74, 24 rows 58 / 74, 32 rows 80 / 75; 16 x 2k,
+//     f16: 24 rows 26 / 27, 32 rows 28 / 27; 17 x 456, 32 kv heads: 16 rows 25 / 35, 32 rows 36 /
+//     36.  (fp32 q has that kernel alone.)
 int few_rows_limit(const kv_shape *s, int window, CacheForm form) {
   const long long seen = seen_tokens(s, window);
-  if (s->dtype == KV_F32) return form == kOwnForm ? 0 : form == kQ4Form ? INT_MAX : seen <= 1024 ? 64 : INT_MAX;
+  if (form == kQ4Form) return s->dtype == KV_F32 ? INT_MAX : 24;
+  if (s->dtype == KV_F32) return form == kOwnForm ? 0 : seen <= 1024 ? 64 : INT_MAX;
   const bool is_short = seen <= 4096;
   return form != kOwnForm ? (is_short ? 24 : 16) : (is_short ? 16 : 8);
 }

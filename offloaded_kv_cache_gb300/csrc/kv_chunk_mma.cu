@@ -40,6 +40,8 @@
 //   * kPair8, 4 x 32768 tokens, 8 kv heads, bf16: 69 us up to 32 rows, 78 us for
 //     128, 183 us for 512.  The four converting warps (eight, which leave the
 //     others fewer registers, were no faster).
+//   * kPair4, the same: 75 us for 32 rows, 82 us for 128, 203 us for 512 (half the
+//     bytes, but more operations a code); in pages of 64, 173 us for 512.
 //
 // The running maximum is moved only when a row's new maximum exceeds it by
 // more than 2^8 in the weights: until then the weights may be as large as 2^8,
@@ -360,6 +362,25 @@ __device__ __forceinline__ void q8_expand(uint4 w, uint32_t f, uint32_t (&x)[8],
   }
 }
 
+// A warp copies the scales and powers of a tile of 4-bit K (w = 0) or V, from the page rows that
+// lane i has in y (rows_total: no page).  (As bulk copies, three a page with the codes', they bound
+// pages of 16 tokens.)
+__device__ __forceinline__ void copy_q4_scales(const ChunkArgs &a, int w, int y, int rows_total,
+                                               uint32_t groups, uint32_t powers) {
+  const int lane = threadIdx.x & 31, log2 = 31 - __clz(a.ps);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {  // the scales of 64 tokens, 64 more, and the powers
+    const int token = i < 2 ? 64 * i + 2 * lane : 16 * (lane & 7);
+    const int page = __shfl_sync(0xFFFFFFFFu, y, token >> log2);
+    const long long row = page + (token & (a.ps - 1));
+    if (page == rows_total) continue;
+    if (i < 2)
+      cp_async16(groups + token * kQ4Scales, (w ? a.v_group : a.k_group) + row * kQ4Scales);
+    else if (lane < kTile / 16)
+      cp_async16(powers + token, (w ? a.v_scale : a.k_scale) + row);
+  }
+}
+
 template <class T, int kMode>
 __global__ void __launch_bounds__(Shape<kMode>::kThreads, Shape<kMode>::kCtas)
     chunk_mma_kernel(const __grid_constant__ ChunkArgs a, const __grid_constant__ CUtensorMap tq,
@@ -390,7 +411,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, Shape<kMode>::kCtas)
       mbar_init(smem_u32(&ctl.empty[i]), 1);
     }
     for (int i = 0; i < Sh::kRaw; ++i) {
-      mbar_init(smem_u32(&ctl.raw_full[i]), 1);
+      mbar_init(smem_u32(&ctl.raw_full[i]), kQ4 ? 33 : 1);  // (4 bits: a lane's small copies each)
       mbar_init(smem_u32(&ctl.raw_empty[i]), 4);
     }
     for (int x = 0; x < 2; ++x) {
@@ -741,13 +762,22 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, Shape<kMode>::kCtas)
       for (int sg = 0; sg < nseg && live; ++sg) {
         const ChunkSeg g = share.seg[sg];
         const int from = seen_from(a, g);
+        // a tile's pages are read while the tile before it is copied
+        const auto page_of = [&](int tile) {
+          const int page = tile * npg + lane;
+          return lane < npg && tile < g.tile_hi && (long long)page * a.ps < g.len
+                     ? a.bt[(long long)g.b * a.maxP + page]
+                     : -1;
+        };
+        int ph_next = page_of(g.tile_lo);
         for (int tile = g.tile_lo; tile < g.tile_hi; ++tile, ++tiles_loaded) {
           int y = rows_total;  // past the end: the copy fills zeros
           uint32_t bad = 0;
+          const int ph = ph_next;
+          ph_next = page_of(tile + 1);
           if (lane < npg) {
             const int page = tile * npg + lane;
             if ((long long)page * a.ps < g.len) {
-              const int ph = a.bt[(long long)g.b * a.maxP + page];
               if (ph >= 0 && ph < a.nphys) {
                 y = (ph * a.Hkv + g.kvh) * a.ps;
               } else {
@@ -771,19 +801,21 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, Shape<kMode>::kCtas)
                 if (w == 0) ctl.bad[tiles_loaded & 7] = (uint8_t)bad;
                 ctl.raw_rows[raw.s] = min(kTile, g.len - tile * kTile);
                 ctl.raw_bad[raw.s] = (int)bad;
-                mbar_arrive_expect_tx(bar, bytes * (Sh::kCodeBytes + (kQ4 ? kQ4Scales : 0) + 1));
+                mbar_arrive_expect_tx(bar, bytes * (Sh::kCodeBytes + (kQ4 ? 0 : 1)));
               }
               __syncwarp();
               if (have) {
                 bulk_load(smem_u32(smem) + Sh::kRawAt + raw.s * Sh::kRawBytes + lane * a.ps * Sh::kCodeBytes,
                           static_cast<const uint8_t *>(w ? a.v : a.k) + (long long)y * Sh::kCodeBytes,
                           a.ps * Sh::kCodeBytes, bar);
-                if constexpr (kQ4)
-                  bulk_load(smem_u32(&ctl.group[raw.s][lane * a.ps * kQ4Scales]),
-                            (w ? a.v_group : a.k_group) + (long long)y * kQ4Scales,
-                            a.ps * kQ4Scales, bar);
-                bulk_load(smem_u32(&ctl.scale[raw.s][lane * a.ps]),
-                          (w ? a.v_scale : a.k_scale) + y, a.ps, bar);
+                if constexpr (!kQ4)
+                  bulk_load(smem_u32(&ctl.scale[raw.s][lane * a.ps]),
+                            (w ? a.v_scale : a.k_scale) + y, a.ps, bar);
+              }
+              if constexpr (kQ4) {
+                copy_q4_scales(a, w, y, rows_total, smem_u32(ctl.group[raw.s]),
+                               smem_u32(ctl.scale[raw.s]));
+                cp_async_arrive_noinc(bar);
               }
             }
           } else {
