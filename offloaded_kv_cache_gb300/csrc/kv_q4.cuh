@@ -51,15 +51,21 @@ __device__ __forceinline__ float rcp(float x) {
 // bits 13 .. 16.  The quotient by an approximate reciprocal is off by 2^-19 at most, and t is
 // rounded to 2^-13: a tie stays at or above it, and 16-bit data, which differ from a tie (8
 // significant bits) by 2^-11 of it at least, 2^-12 here, stay below.  fp32 data may differ by
-// less: the integer found is compared with its two borders, which are exact.  (All lanes call.)
+// less: with 2^-12 on top, a fraction of 4 * 2^-13 or more shows that no border is near; else
+// the integer found is compared with its two borders, which are exact.  (All lanes call.)
 template <class T>
 __device__ __forceinline__ uint32_t q4_codes8(const float (&x)[8], float top, float s, int e, T) {
   const float down = pow2f(-e), f = s == 0.f ? 0.f : rcp(s) * down;
   float t[8];
+  uint32_t fraction = 0x1FFFu;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    t[i] = fmaf(x[i], f, 1032.5f + 0x1p-13f);
-    if constexpr (sizeof(T) == 4) {
+    t[i] = fmaf(x[i], f, 1032.5f + (sizeof(T) == 4 ? 0x1p-12f : 0x1p-13f));
+    fraction = min(fraction, __float_as_uint(t[i]) & 0x1FFFu);
+  }
+  if (sizeof(T) == 4 && fraction < 4) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
       const float c = __uint_as_float(__float_as_uint(t[i]) & ~0x1FFFu) - 1032.f;  // floor(t), less
       const float y = x[i] * down, border = fmaf(c, s, -0.5f * s);
       if (border > y) t[i] -= 1.f;
