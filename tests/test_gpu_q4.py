@@ -138,6 +138,24 @@ def test_append_difficult_vectors(dtype):
     a.check()
 
 
+def test_append_beside_ties():
+    """fp32: elements at (c + 1/2) s (1 +- 2^-k) for every c, many s and k from 6 to 23."""
+    groups = []
+    for i, s in enumerate(STEPS[1:127]):
+        for k in range(6 + i % 3, 24, 3):
+            tie = torch.arange(-6.5, 7.0).double() * float(s)
+            side = (-1.0) ** torch.arange(14)
+            groups.append(torch.cat([tie * (1 + side * 2.0 ** -k), torch.tensor([7.0, -7.0]).double() * float(s)]))
+    groups = groups[:len(groups) // 7 * 7]
+    x = torch.stack(groups).reshape(-1, 7 * 16)
+    last = torch.zeros(len(x), 16, dtype=torch.float64)
+    last[:, 5] = 3136.0  # the power is 0
+    rows = torch.cat([x, last], 1).float()
+    a = Append("f32", 2, 16, [5], [len(rows)], rows=rows)
+    a.run()
+    a.check()
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 def test_append_every_value(dtype):
     """Every finite value of the type as an element, beside group maxima of many sizes."""
