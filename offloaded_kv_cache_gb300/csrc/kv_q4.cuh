@@ -105,22 +105,26 @@ template <class T> struct Q4Bits {
     asm volatile("mov.b32 %0, 0x000F000F;" : "=r"(mask));
     asm volatile("mov.b32 %0, %1;" : "=r"(one) : "n"(f16 ? 0x64006400 : 0x43004300));
   }
-  // c f of nibbles 0 and 4
-  __device__ __forceinline__ uint32_t pair(uint32_t w, uint32_t f) const {
+  // c f of nibbles 0 and 4.  bf16: (128 + n) f - 136 f in one fma, g = -136 f: f has 4
+  // significant bits and 17 * 15 has 8, so that g is exact.  (f16: 1032 f would be past its range.)
+  __device__ __forceinline__ uint32_t pair(uint32_t w, uint32_t f, [[maybe_unused]] uint32_t g) const {
     uint32_t x;
     asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(x) : "r"(w), "r"(mask), "r"(one));
     if constexpr (std::is_same<T, __half>::value) {
       asm("add.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(0xE408E408u));
       asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(f));
     } else {
-      asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(0xC308C308u));
-      asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(f));
+      asm("fma.rn.bf16x2 %0, %0, %1, %2;" : "+r"(x) : "r"(f), "r"(g));
     }
     return x;
   }
-  // eight nibbles times f, in order
+  // eight nibbles times the factor in both halves of f, in order
   __device__ __forceinline__ uint4 expand(uint32_t w, uint32_t f) const {
-    const uint32_t x0 = pair(w, f), x1 = pair(w >> 4, f), x2 = pair(w >> 8, f), x3 = pair(w >> 12, f);
+    uint32_t g = 0;
+    if constexpr (!std::is_same<T, __half>::value)
+      asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(g) : "r"(f), "r"(0xC308C308u));
+    const uint32_t x0 = pair(w, f, g), x1 = pair(w >> 4, f, g), x2 = pair(w >> 8, f, g),
+                   x3 = pair(w >> 12, f, g);
     return make_uint4(__byte_perm(x0, x1, 0x5410), __byte_perm(x2, x3, 0x5410),
                       __byte_perm(x0, x1, 0x7632), __byte_perm(x2, x3, 0x7632));
   }
