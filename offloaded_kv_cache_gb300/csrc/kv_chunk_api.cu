@@ -97,9 +97,9 @@ long long seen_tokens(const kv_shape *s, int window) {
 //     24 rows 29.7 / 26.9; 17 x 456, 32 kv heads: 8 rows 24 / 34, 16 rows 30 / 35
 //   fp32 q, 8-bit, 4 x 32k: 8 rows 70 / 410, 16 rows 106 / 655; 4 x 1.9k: 256 rows
 //     74 / 132; 8448 rows over 528, 2 kv heads: 289 / 112; window 90, 880 rows: 104 / 53
-//   4-bit (kv_chunk_q4.cu), 4 x 32k: 16 rows 50 / 74, 24 rows 58 / 74, 32 rows 80 / 75; 16 x 2k,
+//   4-bit (kv_chunk_q4.cu), 4 x 32k: 16 rows 48 / 74, 24 rows 56 / 74, 32 rows 80 / 75; 16 x 2k,
 //     f16: 24 rows 26 / 27, 32 rows 28 / 27; 17 x 456, 32 kv heads: 16 rows 25 / 35, 32 rows 36 /
-//     36.  fp32 q (the other kernel reads a copy in fp32): 4 x 32k: 8 rows 42 / 356, 64 rows 164 /
+//     36.  fp32 q (the other kernel reads a copy in fp32): 4 x 32k: 8 rows 40 / 356, 64 rows 164 /
 //     798; 4 x 8k: 2048 rows 1209 / 3307; 16 x 500: 64 rows 23 / 75, 1024 rows 266 / 342
 int few_rows_limit(const kv_shape *s, int window, CacheForm form) {
   const long long seen = seen_tokens(s, window);

@@ -3,16 +3,16 @@
 // work is cut.
 //
 // A CTA is four warps, which take 32 tokens each in turn: a warp copies its own codes, scales
-// and powers (asynchronously, one step ahead, the block table's entries another one), has a
+// and powers (asynchronously, one step ahead, the block table's entries before that), has a
 // softmax of its own, and waits for no other until the end of a segment, where their results
 // are joined.  (A warp that copied for four others by TMA and bulk copies was what bounded
 // small pages: six copies per page of 16 tokens.)
 //
 // What bounds it: 4 bits leave two instructions a byte of the cache.  16 tokens by 8 rows take
-// some 400 of a warp's instructions, 130 of them to expand the nibbles.  One token over 8 x
-// <= 65536, 64/8 heads, bf16: 106 us and 4 to join the parts, 470 MB, 4.3 TB/s; the issue slots
-// are busy for 58% of the time, DRAM for 45%.  Four CTAs per SM at 128 registers (five at 96
-// spill: 139 us).
+// some 390 of a warp's instructions, 130 of them to expand the nibbles.  One token over 8 x
+// <= 65536, 64/8 heads, bf16: 106 us with the joining of parts, 470 MB, 4.4 TB/s; the issue
+// slots are busy for 58% of the time, DRAM for 45%.  Four CTAs per SM at 128 registers (five at
+// 96 spill: 139 us); pages looked up step by step cost 4 us.
 //
 // The products are 16 x 8 x 16, units 8 rows, as in kv_chunk_few.cu:
 //   S^T (16 tokens x 8 rows) = K Q^T: the products sum over the channels, in any order that
@@ -146,48 +146,49 @@ __global__ void __launch_bounds__(kThreads, Shape<T>::kCtas)
     if (nseg == 0) break;
 
     // The warp's steps of the list, in order: of segment sg the steps step0 + warp + 4 i below
-    // step1.  The copies run kSlots - 1 steps ahead, the look-ups of pages one more.
-    struct Walk {
-      int sg, at, end;
-    };
-    auto enter = [&](Walk &w) {  // to the first step from here on; sg = nseg: none
-      while (w.sg < nseg && w.at >= w.end) {
-        if (++w.sg == nseg) break;
-        const ChunkSeg &g = sh.share.seg[w.sg];
-        w.at = g.tile_lo * (kTile / kStep) + warp;
-        w.end = min(g.tile_hi * kTile, g.len + kStep - 1) / kStep;
+    // step1.  The copies run kSlots - 1 steps ahead.  The pages of up to sixteen steps of a
+    // segment are looked up together, while the step before them is copied: lanes 2 i and 2 i + 1
+    // have the rows of the cache where the first, second sixteen tokens of the i-th are; -1: none.
+    int list_sg = -1, list_at = 0, list_end = 0;  // the next step to look up
+    int batch = -1, batch_n = 0, batch_i = 0;
+    auto look_up = [&](int &n) -> int {
+      while (list_sg < nseg && list_at >= list_end) {
+        if (++list_sg == nseg) break;
+        const ChunkSeg &g = sh.share.seg[list_sg];
+        list_at = g.tile_lo * (kTile / kStep) + warp;
+        list_end = min(g.tile_hi * kTile, g.len + kStep - 1) / kStep;
       }
-    };
-    Walk ahead{-1, 0, 0};
-    // lanes 0 and 1: the row of the cache where the step's first, second sixteen tokens are;
-    // -1: none, -2: a page out of range
-    auto look_up = [&]() -> int {
-      enter(ahead);
       int y = -1;
-      if (ahead.sg < nseg && lane < 2) {
-        const ChunkSeg &g = sh.share.seg[ahead.sg];
-        const int tok = ahead.at * kStep + 16 * lane;
-        if (tok < g.len) {
+      n = 16;
+      if (list_sg < nseg) {
+        const ChunkSeg &g = sh.share.seg[list_sg];
+        n = min(16, (list_end - list_at + kWarps - 1) / kWarps);
+        const int tok = (list_at + kWarps * (lane >> 1)) * kStep + 16 * (lane & 1);
+        if ((lane >> 1) < n && tok < g.len) {
           const int ph = a.bt[(long long)g.b * a.maxP + (tok >> ps_log2)];
           if (ph >= 0 && ph < a.nphys) y = (ph * a.Hkv + g.kvh) * a.ps + (tok & (a.ps - 1));
-          else if (tok + 16 > seen_from(a, g)) y = -2;
+          else if (tok + 16 > seen_from(a, g)) flag_error(a.status, KV_ERR_BOUNDS);
         }
+        list_at += kWarps * n;
       }
-      ahead.at += kWarps;
       return y;
     };
-    int next_y = look_up();
+    int next_n, next_batch = look_up(next_n);
     int fill = 0;
-    // starts the copies of the step that was looked up last; bit i: its i-th sixteen tokens
-    // are there
+    // starts the copies of the next step; bit i: its i-th sixteen tokens are there
     auto start = [&]() -> uint32_t {
-      const int y = next_y;
-      next_y = look_up();
-      if (y == -2) flag_error(a.status, KV_ERR_BOUNDS);
-      const uint32_t ok = __ballot_sync(0xFFFFFFFFu, y >= 0);  // (lanes 0 and 1)
+      if (batch_i == batch_n) {
+        batch = next_batch;
+        batch_n = next_n;
+        batch_i = 0;
+        next_batch = look_up(next_n);
+      }
       // (sixteen tokens that are not there are copied from the cache's first, and not used)
-      const int y0 = uniform(__shfl_sync(0xFFFFFFFFu, max(y, 0), 0));
-      const int y1 = uniform(__shfl_sync(0xFFFFFFFFu, max(y, 0), 1));
+      const int at0 = __shfl_sync(0xFFFFFFFFu, batch, 2 * batch_i);
+      const int at1 = __shfl_sync(0xFFFFFFFFu, batch, 2 * batch_i + 1);
+      const int y0 = max(at0, 0), y1 = max(at1, 0);
+      const uint32_t ok = (at0 >= 0 ? 1u : 0u) | (at1 >= 0 ? 2u : 0u);
+      ++batch_i;
       const uint32_t to = smem_u32(slots + fill * kSlot);
       fill = fill + 1 == kSlots ? 0 : fill + 1;
       if (ok) {
