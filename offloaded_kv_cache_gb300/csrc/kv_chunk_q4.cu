@@ -10,7 +10,7 @@
 //
 // What bounds it: 4 bits leave two instructions a byte of the cache.  16 tokens by 8 rows take
 // some 390 of a warp's instructions, 130 of them to expand the nibbles.  One token over 8 x
-// <= 65536, 64/8 heads, bf16: 106 us with the joining of parts, 470 MB, 4.4 TB/s; the issue
+// <= 65536, 64/8 heads, bf16: 105 us with the joining of parts, 470 MB, 4.5 TB/s; the issue
 // slots are busy for 58% of the time, DRAM for 45%.  Four CTAs per SM at 128 registers (five at
 // 96 spill: 139 us); pages looked up step by step cost 4 us.
 //
@@ -18,7 +18,7 @@
 //   S^T (16 tokens x 8 rows) = K Q^T: the products sum over the channels, in any order that
 //     K and Q share.  A thread's 16 bytes of codes are 32 channels of a token; a word's
 //     nibbles i and i + 4 lie in one half each of a register, so that one operation puts
-//     them into the mantissas of two f16, and one fma makes c s / 8 of them, exactly.
+//     them into the mantissas of two f16, and one fma makes c s / 256 of them, exactly.
 //   O^T (128 channels x 8 rows) += V^T P^T: pairs of two tokens' elements, a byte of two
 //     channels at a time.
 // Power bytes stay outside: K's multiplies the scores; V's joins the weight's exponent, weight
@@ -73,25 +73,20 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// two e4m3 codes as two f16
-__device__ __forceinline__ uint32_t e4m3_f16(uint32_t codes) {
-  uint32_t x;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(x) : "h"((uint16_t)codes));
-  return x;
-}
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<__half2 *>(&x); }
 __device__ __forceinline__ uint32_t as_word(__half2 x) { return *reinterpret_cast<uint32_t *>(&x); }
 
 // The integers n = c + 8 of the low (odd: high) nibbles of bytes 0 and 2 of a word, less 8,
-// times an eighth of their scales s.  n is put into the mantissa of 1024 + n (odd: 64 + n),
-// and (1024 + n) s / 8 - 129 s (odd: (64 + n) s / 8 - 9 s), in one fma, is exact: s is an
-// integer of 8 to 15 times a power of two, 129 * 15 has 11 bits, and 129 * 448 = 57792.
+// times a 256th of their scales s: an e4m3 code seven bits up is s / 256 in f16, the least ones
+// included.  n is put into the mantissa of 1024 + n (odd: 64 + n), and (1024 + n) t - 1032 t
+// (odd: (64 + n) t - 72 t), in one fma, is exact: s is an integer of 8 to 15 times a power of
+// two, 1032 * 15 has 11 bits and factors of two.
 struct Factor {
-  __half2 s, even, odd;  // s / 8, -129 s, -9 s of the two
+  __half2 s, even, odd;  // t = s / 256, -1032 t, -72 t of the two
 };
-__device__ __forceinline__ Factor factor_of(uint32_t s) {
-  return Factor{__hmul2(as_half2(s), as_half2(0x30003000u)), __hmul2(as_half2(s), as_half2(0xD808D808u)),
-                __hmul2(as_half2(s), as_half2(0xC880C880u))};
+__device__ __forceinline__ Factor factor_of(uint32_t codes) {  // in bytes 0 and 2
+  const __half2 t = as_half2(codes << 7);
+  return Factor{t, __hmul2(t, as_half2(0xE408E408u)), __hmul2(t, as_half2(0xD480D480u))};
 }
 // (One operation for mask and exponent, as long as both are in registers: of two immediates
 // the compiler makes two.  One token over 8 x 65536: 127 -> 110 us.)
@@ -264,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T>::kCtas)
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          qf[h] = 8.f * __shfl_sync(0xFFFFFFFFu, f, 4 * (2 * t4 + h));  // (K's values are eighths)
+          qf[h] = 256.f * __shfl_sync(0xFFFFFFFFu, f, 4 * (2 * t4 + h));  // (K's values are 256ths)
           tq[h] = g.len - g.n + token_of(a, g.r0 + min(2 * t4 + h, g.nrows - 1));
         }
       }
@@ -307,14 +302,13 @@ __global__ void __launch_bounds__(kThreads, Shape<T>::kCtas)
           const uint4 v = *reinterpret_cast<const uint4 *>(kc + (sub * 16 + 8) * kQ4Bytes);
           const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
           // two scales of token tg, of token tg + 8
-          const uint32_t g0 = e4m3_f16(*reinterpret_cast<const uint16_t *>(kg + sub * 16 * kQ4Scales));
-          const uint32_t g1 =
-              e4m3_f16(*reinterpret_cast<const uint16_t *>(kg + (sub * 16 + 8) * kQ4Scales));
+          const uint32_t g0 = *reinterpret_cast<const uint16_t *>(kg + sub * 16 * kQ4Scales);
+          const uint32_t g1 = *reinterpret_cast<const uint16_t *>(kg + (sub * 16 + 8) * kQ4Scales);
           float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int c = 0; c < 2; ++c) {  // 16 channels, two words
-            const Factor f0 = factor_of(__byte_perm(g0, 0, c ? 0x3232 : 0x1010));
-            const Factor f1 = factor_of(__byte_perm(g1, 0, c ? 0x3232 : 0x1010));
+            const Factor f0 = factor_of(__byte_perm(g0, 0, c ? 0x4141 : 0x4040));
+            const Factor f1 = factor_of(__byte_perm(g1, 0, c ? 0x4141 : 0x4040));
 #pragma unroll
             for (int j = 2 * c; j < 2 * c + 2; ++j) {
               const uint32_t a0 = bits.pair<0>(uu[j], f0), a1 = bits.pair<0>(vv[j], f1);
@@ -446,8 +440,8 @@ __global__ void __launch_bounds__(kThreads, Shape<T>::kCtas)
             for (int i = 0; i < 4; ++i)
               if ((bad >> (4 * (2 * t4 + (i & 1)) + (i >> 1) + 2 * sub)) & 1) sb[i] = 0;
           }
-          const Factor f0 = factor_of(e4m3_f16(sb[0] | (sb[1] << 8)));
-          const Factor f1 = factor_of(e4m3_f16(sb[2] | (sb[3] << 8)));
+          const Factor f0 = factor_of(sb[0] | (sb[1] << 16));
+          const Factor f1 = factor_of(sb[2] | (sb[3] << 16));
 #pragma unroll
           for (int d = 0; d < 8; ++d) {  // a byte of two channels: a block of O^T
             const int byte = 0x0400 + 0x0101 * (d & 3);
@@ -480,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T>::kCtas)
               make_float4(o[d][h], o[d][h + 2], o[d + 1][h], o[d + 1][h + 2]);
         if (g8 == 0) {
           sh.m[warp][n] = m[h];
-          sh.r[warp][n] = r[h] == -INFINITY ? -INFINITY : r[h] - kShift + 3.f;  // (V's are eighths)
+          sh.r[warp][n] = r[h] == -INFINITY ? -INFINITY : r[h] - kShift + 8.f;  // (V's are 256ths)
           sh.l[warp][n] = lt;
         }
       }
