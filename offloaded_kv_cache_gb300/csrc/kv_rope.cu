@@ -9,10 +9,11 @@
 //
 // Each byte is read and written once, and a pair's sine and cosine serve all heads of a
 // kv head's group: memory bounds it, for a few tokens the launch and two round trips.
-// 32 prompts of <= 513 tokens, 32/32 heads, f16: 43 us, 230 MB, 5.4 TB/s; append of 4 x <= 2048,
-// 32/8 heads, bf16, with the index: 22 us, 102 MB, 4.6 TB/s; 32 x 1: 2.4 us, append 3.0.
+// 32 prompts of <= 513 tokens, 32/32 heads, f16: 41 us, 230 MB, 5.6 TB/s; append of 4 x <= 2048,
+// 32/8 heads, bf16, with the index: 21 us, 102 MB, 4.9 TB/s; 32 x 1: 2.4 us, append 3.0.
 #include <algorithm>
 #include <climits>
+#include <type_traits>
 
 #include "kv_append.cuh"
 #include "kv_launch.h"
@@ -24,10 +25,12 @@ namespace {
 #ifndef KVS_ROPE_BYTES
 #define KVS_ROPE_BYTES 6144
 #endif
+#ifndef KVS_ROPE_FLIGHT
+#define KVS_ROPE_FLIGHT 16  // pairs of a lane in flight (32: the prompts below 45 us, not 41)
+#endif
 
-constexpr int kLanes = 16;   // of a vector: two times 4 channels each
-constexpr int kMaxGroups = 32;  // half-warps of a block: 16, or 32 for pages of more tokens
-constexpr int kFlight = 4;   // vectors in flight per half-warp
+constexpr int kThreads = 256;   // or twice as many, for pages of more than 16 tokens
+constexpr int kMaxAtOnce = 32;  // tokens
 constexpr int kPairs = kHeadDim / 2;
 constexpr int kKeyBytes = 64 * 1024;  // of keys that a block keeps for the index
 
@@ -42,10 +45,10 @@ struct RopeArgs {
   int *status;
   long long nphys;
   int Hq, Hkv, G, ps, ps_log2, maxP, total_q, max_q_len;
-  int lanes;                      // lanes whose channels are turned
+  int pairs;                      // that are turned
   float scale;
   int tile;                       // tokens per block: a page, or 16
-  int per_token;                  // half-warps that share a token's vectors, a power of two
+  int per_token;                  // groups that share a token's vectors, a power of two
   int heads;                      // kv heads of a block
   int blocks, parts;              // tiles per sequence, blocks per tile
   Divisor by_blocks, by_parts;
@@ -76,54 +79,69 @@ __device__ __forceinline__ void cos_sin(uint64_t f, int pos, float scale, float 
   s = ((quarter & 2) ? -v : v) * scale;
 }
 
-// A lane's two pieces of a vector, 4 channels each, as they lie in memory.
-template <class T> struct Piece {
-  using Word = uint2;
-  Word w[2];
+// A lane's two pieces of a vector, kCh channels each, as they lie in memory: 16 bytes, or, of 16-bit
+// data whose turned pairs are an odd number of fours, 8 (16 x <= 2000 tokens, 32/8 heads, bf16:
+// 48.3 us with 16 bytes, 53.4 with 8).
+template <class T, int kCh> struct Piece {
+  static constexpr int kWords = kCh * (int)sizeof(T) / 4;
+  using Word = std::conditional_t<kWords == 4, uint4, uint2>;
+  alignas(16) uint32_t w[2][kWords];
+  __device__ __forceinline__ void load(int i, const T *src) {
+    *reinterpret_cast<Word *>(w[i]) = *reinterpret_cast<const Word *>(src);
+  }
+  __device__ __forceinline__ void store(int i, T *dst) const {
+    *reinterpret_cast<Word *>(dst) = *reinterpret_cast<const Word *>(w[i]);
+  }
 };
-template <> struct Piece<float> {
-  using Word = uint4;
-  Word w[2];
-};
-__device__ __forceinline__ void unpack4(const uint4 &w, float (&x)[4], float) {
-  x[0] = __uint_as_float(w.x); x[1] = __uint_as_float(w.y);
-  x[2] = __uint_as_float(w.z); x[3] = __uint_as_float(w.w);
+template <int kCh>
+__device__ __forceinline__ void unpack(const uint32_t (&w)[kCh], float (&x)[kCh], float) {
+#pragma unroll
+  for (int i = 0; i < kCh; ++i) x[i] = __uint_as_float(w[i]);
 }
-__device__ __forceinline__ uint4 pack4(const float (&x)[4], float) {
-  return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
-                    __float_as_uint(x[3]));
+template <int kCh>
+__device__ __forceinline__ void pack(const float (&x)[kCh], uint32_t (&w)[kCh], float) {
+#pragma unroll
+  for (int i = 0; i < kCh; ++i) w[i] = __float_as_uint(x[i]);
 }
-template <class T> __device__ __forceinline__ void unpack4(const uint2 &w, float (&x)[4], T) {
-  const float2 a = unpack2(w.x, T{}), b = unpack2(w.y, T{});
-  x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
+template <class T, int kCh>
+__device__ __forceinline__ void unpack(const uint32_t (&w)[kCh / 2], float (&x)[kCh], T) {
+#pragma unroll
+  for (int i = 0; i < kCh / 2; ++i) {
+    const float2 a = unpack2(w[i], T{});
+    x[2 * i] = a.x;
+    x[2 * i + 1] = a.y;
+  }
 }
-template <class T> __device__ __forceinline__ uint2 pack4(const float (&x)[4], T) {
-  return make_uint2(pack2(x[0], x[1], T{}), pack2(x[2], x[3], T{}));
+template <class T, int kCh>
+__device__ __forceinline__ void pack(const float (&x)[kCh], uint32_t (&w)[kCh / 2], T) {
+#pragma unroll
+  for (int i = 0; i < kCh / 2; ++i) w[i] = pack2(x[2 * i], x[2 * i + 1], T{});
 }
 
-// Turns a lane's four pairs: channel i of both pieces (halves), or neighbours (interleaved).
-template <class T, bool kInter>
-__device__ __forceinline__ void turn(Piece<T> &p, const float (&c)[4], const float (&s)[4]) {
-  float x[4], y[4], u[4], v[4];
-  unpack4(p.w[0], x, T{});
-  unpack4(p.w[1], y, T{});
+// Turns a lane's pairs: channel i of both pieces (halves), or neighbours (interleaved).
+template <class T, int kCh, bool kInter>
+__device__ __forceinline__ void turn(Piece<T, kCh> &p, const float (&c)[kCh], const float (&s)[kCh]) {
+  float x[kCh], y[kCh], u[kCh], v[kCh];
+  unpack(p.w[0], x, T{});
+  unpack(p.w[1], y, T{});
   if constexpr (kInter) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kCh / 2; ++i) {
+      const int k = kCh / 2 + i;
       u[2 * i] = x[2 * i] * c[i] - x[2 * i + 1] * s[i];
       u[2 * i + 1] = x[2 * i] * s[i] + x[2 * i + 1] * c[i];
-      v[2 * i] = y[2 * i] * c[2 + i] - y[2 * i + 1] * s[2 + i];
-      v[2 * i + 1] = y[2 * i] * s[2 + i] + y[2 * i + 1] * c[2 + i];
+      v[2 * i] = y[2 * i] * c[k] - y[2 * i + 1] * s[k];
+      v[2 * i + 1] = y[2 * i] * s[k] + y[2 * i + 1] * c[k];
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kCh; ++i) {
       u[i] = x[i] * c[i] - y[i] * s[i];
       v[i] = x[i] * s[i] + y[i] * c[i];
     }
   }
-  p.w[0] = pack4(u, T{});
-  p.w[1] = pack4(v, T{});
+  pack(u, p.w[0], T{});
+  pack(v, p.w[1], T{});
 }
 
 // The minimum and maximum of one word of the keys of `count` tokens, `stride` words apart, and
@@ -155,24 +173,26 @@ __device__ __forceinline__ void word_bounds(const uint32_t *at, int stride, int 
 }
 
 // Block (sequence, tile of tokens, kv heads), 16 or 32 tokens of the tile at a time: first a
-// thread a pair takes the tokens' sines and cosines into shared memory, then a half-warp
-// a vector turns and stores, kFlight vectors loaded before the first is stored; per_token
-// half-warps share a token.  A tile is a page where the index is kept, so that its keys meet
+// thread a pair takes the tokens' sines and cosines into shared memory, then a group of 8 or 16
+// lanes a vector turns and stores, kFlight vectors loaded before the first is stored; per_token
+// groups share a token.  A tile is a page where the index is kept, so that its keys meet
 // in one block: they are left in shared memory too, and looked over there, in totalOrder, at
 // the end.
-template <class T, bool kInter>
-__global__ void __launch_bounds__(kLanes * kMaxGroups, sizeof(T) == 2 ? 2 : 1) rope_kernel(const RopeArgs a) {
+template <class T, int kCh, bool kInter>
+__global__ void __launch_bounds__(2 * kThreads, sizeof(T) == 2 ? 2 : 1) rope_kernel(const RopeArgs a) {
+  constexpr int kLanes = kHeadDim / 2 / kCh, kFlight = KVS_ROPE_FLIGHT / kCh;
   extern __shared__ __align__(16) uint8_t smem[];  // [token][kv head][128] keys, with an index only
-  __shared__ __align__(16) float cosine[kMaxGroups][kPairs], sine[kMaxGroups][kPairs];
+  __shared__ __align__(16) float cosine[kMaxAtOnce][kPairs], sine[kMaxAtOnce][kPairs];
   pdl_wait();
   const int tid = threadIdx.x, l = tid % kLanes, grp = tid / kLanes;
   const int groups = blockDim.x / kLanes, at_once = groups / a.per_token;  // tokens at a time
   const int seq_tile = a.by_parts(blockIdx.x), part = (int)blockIdx.x - seq_tile * a.parts;
   const int b = a.by_blocks(seq_tile), j = seq_tile - b * a.blocks;
-  const bool turns = l < a.lanes;
+  const int lanes = a.pairs / kCh;  // that turn
+  const bool turns = l < lanes;
   const int pair = tid % kPairs;
   double freq = 0.0;
-  if (pair < 4 * a.lanes) freq = a.freq[pair];
+  if (pair < a.pairs) freq = a.freq[pair];
   RowSpan r{a.q_start[b], a.q_start[b + 1] - a.q_start[b], 0};
   if (a.bt) {
     r = append_span(a, b);
@@ -201,10 +221,9 @@ __global__ void __launch_bounds__(kLanes * kMaxGroups, sizeof(T) == 2 ? 2 : 1) r
     if (ph < 0 || ph >= a.nphys) ph = -1;  // recorded by the sequence's first block
     slot0 = (r.len + lo) & (a.ps - 1);
   }
-  const int c0 = turns && !kInter ? 4 * l : 8 * l;
-  const int c1 = turns && !kInter ? 4 * (a.lanes + l) : 8 * l + 4;
+  const int c0 = turns && !kInter ? kCh * l : 2 * kCh * l;
+  const int c1 = turns && !kInter ? kCh * (lanes + l) : 2 * kCh * l + kCh;
   const int h0 = part * a.heads, heads = min(a.heads, a.Hkv - h0), sub = grp & (a.per_token - 1);
-  using Word = typename Piece<T>::Word;
   // A token's vectors: its keys, its values, q heads; K's and V's heads lie a page's tokens
   // apart in the cache.
   const int keys = a.k ? heads : 0, rows_kv = keys + (a.v ? heads : 0);
@@ -212,7 +231,7 @@ __global__ void __launch_bounds__(kLanes * kMaxGroups, sizeof(T) == 2 ? 2 : 1) r
   const uint64_t f = turns_of(freq);
   for (int i0 = lo; i0 < hi; i0 += at_once) {
     const int tokens = min(at_once, hi - i0);
-    if (pair < 4 * a.lanes) {
+    if (pair < a.pairs) {
       for (int k = tid / kPairs; k < tokens; k += blockDim.x / kPairs)
         cos_sin(f, a.at ? a.at[r.q0 + i0 + k] : r.len + i0 + k, a.scale, cosine[k][pair], sine[k][pair]);
     }
@@ -226,16 +245,19 @@ __global__ void __launch_bounds__(kLanes * kMaxGroups, sizeof(T) == 2 ? 2 : 1) r
       const long long out =
           a.bt ? (((long long)ph * a.Hkv + h0) * a.ps + slot0 + (i - lo)) * kHeadDim : in;
       const bool there = !a.bt || ph >= 0;
-      float c[4], s[4];
+      float c[kCh], s[kCh];
       if (turns) {
-        const float4 u = *reinterpret_cast<const float4 *>(&cosine[mine][4 * l]);
-        const float4 v = *reinterpret_cast<const float4 *>(&sine[mine][4 * l]);
-        c[0] = u.x; c[1] = u.y; c[2] = u.z; c[3] = u.w;
-        s[0] = v.x; s[1] = v.y; s[2] = v.z; s[3] = v.w;
+#pragma unroll
+        for (int k = 0; k < kCh; k += 4) {
+          const float4 u = *reinterpret_cast<const float4 *>(&cosine[mine][kCh * l + k]);
+          const float4 v = *reinterpret_cast<const float4 *>(&sine[mine][kCh * l + k]);
+          c[k] = u.x; c[k + 1] = u.y; c[k + 2] = u.z; c[k + 3] = u.w;
+          s[k] = v.x; s[k + 1] = v.y; s[k + 2] = v.z; s[k + 3] = v.w;
+        }
       }
 #pragma unroll 1
       for (int v0 = sub; v0 < count; v0 += kFlight * a.per_token) {
-        Piece<T> x[kFlight];
+        Piece<T, kCh> x[kFlight];
 #pragma unroll
         for (int k = 0; k < kFlight; ++k) {
           const int v = v0 + k * a.per_token;
@@ -243,8 +265,8 @@ __global__ void __launch_bounds__(kLanes * kMaxGroups, sizeof(T) == 2 ? 2 : 1) r
           const T *src = v < keys      ? static_cast<const T *>(a.k) + in + v * kHeadDim
                          : v < rows_kv ? static_cast<const T *>(a.v) + in + (v - keys) * kHeadDim
                                        : static_cast<const T *>(a.q) + at + (v - rows_kv) * kHeadDim;
-          x[k].w[0] = *reinterpret_cast<const Word *>(src + c0);
-          x[k].w[1] = *reinterpret_cast<const Word *>(src + c1);
+          x[k].load(0, src + c0);
+          x[k].load(1, src + c1);
         }
 #pragma unroll
         for (int k = 0; k < kFlight; ++k) {
@@ -253,13 +275,13 @@ __global__ void __launch_bounds__(kLanes * kMaxGroups, sizeof(T) == 2 ? 2 : 1) r
           T *dst = v < keys      ? static_cast<T *>(a.k_out) + out + (long long)v * apart
                    : v < rows_kv ? static_cast<T *>(a.v_out) + out + (long long)(v - keys) * apart
                                  : static_cast<T *>(a.q_out) + at + (v - rows_kv) * kHeadDim;
-          if (turns && (v < keys || v >= rows_kv)) turn<T, kInter>(x[k], c, s);
-          *reinterpret_cast<Word *>(dst + c0) = x[k].w[0];
-          *reinterpret_cast<Word *>(dst + c1) = x[k].w[1];
+          if (turns && (v < keys || v >= rows_kv)) turn<T, kCh, kInter>(x[k], c, s);
+          x[k].store(0, dst + c0);
+          x[k].store(1, dst + c1);
           if (a.mm && v < keys) {
             T *keep = reinterpret_cast<T *>(smem) + ((i - lo) * heads + v) * kHeadDim;
-            *reinterpret_cast<Word *>(keep + c0) = x[k].w[0];
-            *reinterpret_cast<Word *>(keep + c1) = x[k].w[1];
+            x[k].store(0, keep + c0);
+            x[k].store(1, keep + c1);
           }
         }
       }
@@ -332,23 +354,29 @@ cudaError_t launch_rope(const kv_shape *s, const kv_chunk *c, const kv_rope_plan
   if (rope) {
     a.freq = rope->freq;
     a.at = rope->positions;
-    a.lanes = rope->rotary_dim / 8;
+    a.pairs = rope->rotary_dim / 2;
     a.scale = rope->scale;
   }
   a.tile = mm ? a.ps : 16;
   if (!rope_grid(s, c, bt != nullptr, a.tile, &a.blocks)) return cudaErrorInvalidConfiguration;
   const int tokens = std::min({c->max_q_len, c->total_q, a.tile});
-  const int groups = tokens > 16 ? kMaxGroups : 16;
+  const int threads = tokens > 16 ? 2 * kThreads : kThreads;
+  const bool wide = s->dtype != KV_F32 && a.pairs % 8 == 0;
+  const int groups = threads / (kHeadDim / 2 / (wide ? 8 : 4));
   a.per_token = 1;
-  while (2 * a.per_token * tokens <= groups) a.per_token *= 2;
+  while (2 * a.per_token * tokens <= groups || a.per_token * kMaxAtOnce < groups) a.per_token *= 2;
   const int kinds = (k ? 1 : 0) + (v ? 1 : 0) + (q ? a.G : 0);
   const int row_bytes = kHeadDim * (s->dtype == KV_F32 ? 4 : 2), key_bytes = tokens * row_bytes;
   // kv heads of a block: some KVS_ROPE_BYTES of vectors a token, which share its angles (fewer
-  // where a tile is a large page), or as many half-warps as vectors; no more than whose keys the
+  // where a tile is a large page), or, of a few tokens, as many groups as vectors and a thread
+  // for a word of the index (256 x 1 token, 32/8 heads, f16: 4 heads 4.7 us, 5 heads 5.4, 2 heads
+  // 6.9); no more than whose keys the
   // shared memory takes (a page of 128 tokens in fp32 is 64 KB).  (us at half / twice as
-  // many: append of 4 x 2048 tokens, 32/8 heads, bf16 24 / 30 against 22; fp32 36 / 53, here 36)
-  a.heads = (a.per_token > 1 ? a.per_token : KVS_ROPE_BYTES / row_bytes * 16 / a.tile) / kinds;
+  // many bytes: append of 4 x 2048 tokens, 32/8 heads, bf16 22.4 / 25.5 against 20.7; fp32 46 /
+  // 37, here 39; 32 prompts of <= 513, 32/32 heads, f16 42.6 / 43.1 against 41.3)
+  a.heads = (tokens <= 8 ? a.per_token : KVS_ROPE_BYTES / row_bytes * 16 / a.tile) / kinds;
   a.heads = std::max(1, a.heads);
+  if (mm && tokens <= 8) a.heads = std::min(a.heads, threads * 4 / row_bytes);
   if (ctx_out && ctx_out == ctx && a.blocks == 1)
     a.heads = a.Hkv;  // one block per sequence: it can write the lengths that it alone reads
   if (mm) a.heads = std::min(a.heads, kKeyBytes / key_bytes);
@@ -358,23 +386,23 @@ cudaError_t launch_rope(const kv_shape *s, const kv_chunk *c, const kv_rope_plan
   a.by_parts = Divisor::of(a.parts);
   const bool later = ctx_out && ctx_out == ctx && (a.blocks > 1 || a.parts > 1);
   a.write_lens = ctx_out && !later;
-  const dim3 grid((unsigned)(a.blocks * s->batch * a.parts)), block(kLanes * groups);
+  const dim3 grid((unsigned)(a.blocks * s->batch * a.parts)), block(threads);
   const size_t smem = mm ? (size_t)a.heads * key_bytes : 0;
   const bool inter = rope && rope->interleaved;
-  cudaError_t e;
-  switch (s->dtype) {
-    case KV_F32:
-      e = inter ? rope_go(rope_kernel<float, true>, grid, block, smem, st, a)
-                : rope_go(rope_kernel<float, false>, grid, block, smem, st, a);
-      break;
-    case KV_F16:
-      e = inter ? rope_go(rope_kernel<__half, true>, grid, block, smem, st, a)
-                : rope_go(rope_kernel<__half, false>, grid, block, smem, st, a);
-      break;
-    default:
-      e = inter ? rope_go(rope_kernel<__nv_bfloat16, true>, grid, block, smem, st, a)
-                : rope_go(rope_kernel<__nv_bfloat16, false>, grid, block, smem, st, a);
-  }
+  const auto go = [&](auto t) {
+    using T = decltype(t);
+    constexpr int kCh = 16 / sizeof(T);
+    if constexpr (kCh == 8) {
+      if (!wide)
+        return inter ? rope_go(rope_kernel<T, 4, true>, grid, block, smem, st, a)
+                     : rope_go(rope_kernel<T, 4, false>, grid, block, smem, st, a);
+    }
+    return inter ? rope_go(rope_kernel<T, kCh, true>, grid, block, smem, st, a)
+                 : rope_go(rope_kernel<T, kCh, false>, grid, block, smem, st, a);
+  };
+  cudaError_t e = s->dtype == KV_F32   ? go(float{})
+                  : s->dtype == KV_F16 ? go(__half{})
+                                       : go(__nv_bfloat16{});
   if (e == cudaSuccess && later)
     e = launch_pdl(advance_kernel<RopeArgs>, dim3(s->batch), dim3(256), 0, st, a);
   return e;
