@@ -22,11 +22,14 @@
 namespace kvs {
 namespace {
 
-#ifndef KVS_ROPE_BYTES
-#define KVS_ROPE_BYTES 6144
+#ifndef KVS_ROPE_VECTORS
+#define KVS_ROPE_VECTORS 24
+#endif
+#ifndef KVS_ROPE_FILL
+#define KVS_ROPE_FILL (152 * 1024 * 3 / 2)  // threads
 #endif
 #ifndef KVS_ROPE_FLIGHT
-#define KVS_ROPE_FLIGHT 16  // pairs of a lane in flight (32: the prompts below 45 us, not 41)
+#define KVS_ROPE_FLIGHT 16  // pairs of a lane in flight (32: the prompts above 45 us)
 #endif
 
 constexpr int kThreads = 256;   // or twice as many, for pages of more than 16 tokens
@@ -367,16 +370,25 @@ cudaError_t launch_rope(const kv_shape *s, const kv_chunk *c, const kv_rope_plan
   while (2 * a.per_token * tokens <= groups || a.per_token * kMaxAtOnce < groups) a.per_token *= 2;
   const int kinds = (k ? 1 : 0) + (v ? 1 : 0) + (q ? a.G : 0);
   const int row_bytes = kHeadDim * (s->dtype == KV_F32 ? 4 : 2), key_bytes = tokens * row_bytes;
-  // kv heads of a block: some KVS_ROPE_BYTES of vectors a token, which share its angles (fewer
-  // where a tile is a large page), or, of a few tokens, as many groups as vectors and a thread
-  // for a word of the index (256 x 1 token, 32/8 heads, f16: 4 heads 4.7 us, 5 heads 5.4, 2 heads
-  // 6.9); no more than whose keys the
-  // shared memory takes (a page of 128 tokens in fp32 is 64 KB).  (us at half / twice as
-  // many bytes: append of 4 x 2048 tokens, 32/8 heads, bf16 22.4 / 25.5 against 20.7; fp32 46 /
-  // 37, here 39; 32 prompts of <= 513, 32/32 heads, f16 42.6 / 43.1 against 41.3)
-  a.heads = (tokens <= 8 ? a.per_token : KVS_ROPE_BYTES / row_bytes * 16 / a.tile) / kinds;
+  // kv heads of a block: up to KVS_ROPE_VECTORS of a token's vectors, which share its angles, but
+  // blocks enough to fill the GPU one and a half times; of a few tokens, as many groups as vectors
+  // and a thread for a word of the index; no more than whose keys the shared memory takes (a page
+  // of 128 tokens in fp32 is 64 KB).  Append, us:
+  //   4 x 2048 tokens, 32/8 heads, bf16: pages of 16, 2 / 4 / 8 heads 22.2 / 20.6 / 25.2; of 64,
+  //     1 / 2 / 4 heads 28.7 / 22.2 / 30.6; of 128, 1 / 2 heads 27.8 / 35.5; fp32, pages of 16,
+  //     2 / 4 / 8 heads 38.9 / 37.0 / 36.1
+  //   16 x 2000, 64/8 heads, f16, pages of 64: 1 / 2 heads 114 / 99; 1 x 513, 32/8: 10.4 / 13.1
+  //   256 x 1, 32/8 heads, f16: 2 / 4 / 5 heads 6.9 / 4.7 / 5.4
+  if (tokens <= 8) {
+    a.heads = a.per_token / kinds;
+    if (mm) a.heads = std::min(a.heads, threads * 4 / row_bytes);
+  } else {
+    a.heads = std::min(KVS_ROPE_VECTORS / kinds, a.Hkv);
+    while (a.heads > 1 &&
+           (long long)a.blocks * s->batch * ((a.Hkv + a.heads - 1) / a.heads) * threads < KVS_ROPE_FILL)
+      --a.heads;
+  }
   a.heads = std::max(1, a.heads);
-  if (mm && tokens <= 8) a.heads = std::min(a.heads, threads * 4 / row_bytes);
   if (ctx_out && ctx_out == ctx && a.blocks == 1)
     a.heads = a.Hkv;  // one block per sequence: it can write the lengths that it alone reads
   if (mm) a.heads = std::min(a.heads, kKeyBytes / key_bytes);
