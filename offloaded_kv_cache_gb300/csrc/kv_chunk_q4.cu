@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T>::kCtas)
         if (++list_sg == nseg) break;
         const ChunkSeg &g = sh.share.seg[list_sg];
         list_at = g.tile_lo * (kTile / kStep) + warp;
-        list_end = min(g.tile_hi * kTile, g.len + kStep - 1) / kStep;
+        list_end = min(g.tile_hi * (kTile / kStep), (g.len - 1) / kStep + 1);
       }
       int y = -1;
       n = 16;
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T>::kCtas)
         for (int i = 0; i < 4; ++i) o[d][i] = 0.f;
       float bm[2] = {0.f, 0.f}, br[2] = {0.f, 0.f};  // the maxima that the weights refer to
       bool begun = false;                            // every row has seen a token
-      const int end = min(g.tile_hi * kTile, g.len + kStep - 1) / kStep;
+      const int end = min(g.tile_hi * (kTile / kStep), (g.len - 1) / kStep + 1);
       for (int step = g.tile_lo * (kTile / kStep) + warp; step < end; step += kWarps) {
         __syncwarp();  // the slot that is filled next has been read
         there[kSlots - 1] = start();

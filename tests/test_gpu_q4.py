@@ -498,6 +498,29 @@ def test_offsets_past_32_bits(dtype, n):
     check(p.d_out, *p.expected())
 
 
+@pytest.mark.parametrize("heads", [8, 32])
+def test_as_many_tokens_as_an_int_counts(heads):
+    """One page, 2^27 - 1 times in the table: the attention over its 16 tokens.
+
+    8 rows: a warp takes 2^31 / 32 / 2432 = 27594 steps of two products (cut by 2^-23 of the sum
+    at most) and eight weights a lane (2^-24): 2 * 27594 * 2^-23 + 8 * 27594 * 2^-24 = 2%.  32
+    rows: a CTA takes 2^31 / 128 / 152 = 110377 tiles of eight products, cut by half of that on
+    average and of a sum half as large on average: 8 * 110377 * 2^-25 = 2.6%, and as much at most
+    for the weights.  A twentieth of the largest value."""
+    p = Problem4("bf16", heads, 1, 16, [16], [1], seed=5).upload()
+    want, tol = p.expected()
+    pages = 2 ** 27 - 1
+    p.shape.max_pages_per_seq = pages
+    p.d_table = torch.full((1, pages), int(p.table[0, 0]), dtype=torch.int32, device="cuda")
+    p.d_lens = torch.tensor([16 * pages], dtype=torch.int32, device="cuda")
+    p.use(p.d_four)
+    p.attend()
+    torch.cuda.synchronize()
+    top = float(p.tokens("v", 0, 0)[0].abs().max())
+    off = (p.d_out.cpu().double() - want).abs()
+    assert bool((off <= tol + top / 20).all())
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_no_rows_at_all(dtype):
     p = Problem4(dtype, 4, 2, 16, [30, 0], [0, 0]).upload()
