@@ -61,7 +61,7 @@ int resolve_q4(const kv_shape *s, const kv_q4_cache *c, kv_q4_cache *dev) {
 #define KVS_Q8_DIRECT_ROWS 768
 #endif
 // The 4-bit cache likewise.  (us, direct / expanded, 8 kv heads: 4 x 32k tokens in pages of 16,
-// bf16, 128 rows 82 / 168, 512 rows 203 / 209, 1024 rows 362 / 295; in pages of 64, 512 rows 173 /
+// bf16, 128 rows 81 / 168, 512 rows 201 / 209, 1024 rows 362 / 289; in pages of 64, 512 rows 170 /
 // 205, 1024 rows 309 / 288; 16 x 2k, f16, 512 rows 56 / 66, 1024 rows 89 / 85.)
 #ifndef KVS_Q4_DIRECT_ROWS
 #define KVS_Q4_DIRECT_ROWS 640

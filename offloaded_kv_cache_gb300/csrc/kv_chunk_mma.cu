@@ -40,8 +40,10 @@
 //   * kPair8, 4 x 32768 tokens, 8 kv heads, bf16: 69 us up to 32 rows, 78 us for
 //     128, 183 us for 512.  The four converting warps (eight, which leave the
 //     others fewer registers, were no faster).
-//   * kPair4, the same: 75 us for 32 rows, 82 us for 128, 203 us for 512 (half the
-//     bytes, but more operations a code); in pages of 64, 173 us for 512.
+//   * kPair4, the same in pages of 16 / of 64: 64 rows 76 / 64 us, 512 rows 201 /
+//     170 us.  Its converters, with half the bytes but more operations a code; stores
+//     that meet no bank twice, for two selections a row, were no faster (f16 2 us
+//     slower, bf16 up to 5 us faster).
 //
 // The running maximum is moved only when a row's new maximum exceeds it by
 // more than 2^8 in the weights: until then the weights may be as large as 2^8,

@@ -4,8 +4,8 @@
 //
 // 73 bytes a vector where 16-bit data takes 256: memory bounds the read back (4 x <= 32768
 // tokens, 8 kv heads, bf16: 92 us, 568 MB, 6.2 TB/s), the append nearly: its issue slots are
-// busy for 79% of the time (32 x <= 513 tokens, 32 kv heads: f16 28 us, 148 MB, 5.2 TB/s; fp32
-// 50 us, 5.3 TB/s).  A decode step's append (2.2 us) is the launch and two round trips.
+// busy for some 70% of the time (32 x <= 513 tokens, 32 kv heads: f16 27 us, 148 MB, 5.4 TB/s;
+// fp32 48 us, 5.5 TB/s).  A decode step's append (2.2 us) is the launch and two round trips.
 #include <algorithm>
 
 #include "kv_append.cuh"

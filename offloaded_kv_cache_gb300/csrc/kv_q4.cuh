@@ -47,26 +47,26 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 // Eight channels as nibbles c + 8, x0 in the lowest; top: the largest magnitude of the scale's
-// channels times 2^-e.  t = x / (s 2^e) + 1/2 + 8 + 2^-13 + 2^10 has its integer part in
-// bits 13 .. 16.  The quotient by an approximate reciprocal is off by 2^-19 at most, and t is
-// rounded to 2^-13: a tie stays at or above it, and 16-bit data, which differ from a tie (8
-// significant bits) by 2^-11 of it at least, 2^-12 here, stay below.  fp32 data may differ by
-// less: with 2^-12 on top, a fraction of 4 * 2^-13 or more shows that no border is near; else
-// the integer found is compared with its two borders, which are exact.  (All lanes call.)
+// channels times 2^-e.  t = x / (s 2^e) + 1/2 + 8 + 2^-15 + 2^7 has its integer part, less 2^7,
+// in its third byte alone.  The quotient by an approximate reciprocal is off by 2^-19 at most,
+// and t is rounded to 2^-16: a tie stays at or above it, and 16-bit data, which differ from a tie
+// (8 significant bits) by 2^-11 of it at least, 2^-12 here, stay below.  fp32 data may differ by
+// less: a fraction of 4 * 2^-16 or more shows that no border is near; else the integer found is
+// compared with its two borders, which are exact.  (All lanes call.)
 template <class T>
 __device__ __forceinline__ uint32_t q4_codes8(const float (&x)[8], float top, float s, int e, T) {
   const float down = pow2f(-e), f = s == 0.f ? 0.f : rcp(s) * down;
   float t[8];
-  uint32_t fraction = 0x1FFFu;
+  uint32_t fraction = 0xFFFFu;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    t[i] = fmaf(x[i], f, 1032.5f + (sizeof(T) == 4 ? 0x1p-12f : 0x1p-13f));
-    fraction = min(fraction, __float_as_uint(t[i]) & 0x1FFFu);
+    t[i] = fmaf(x[i], f, 136.5f + 0x1p-15f);
+    fraction = min(fraction, __float_as_uint(t[i]) & 0xFFFFu);
   }
   if (sizeof(T) == 4 && fraction < 4) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float c = __uint_as_float(__float_as_uint(t[i]) & ~0x1FFFu) - 1032.f;  // floor(t), less
+      const float c = __uint_as_float(__float_as_uint(t[i]) & ~0xFFFFu) - 136.f;  // floor(t), less
       const float y = x[i] * down, border = fmaf(c, s, -0.5f * s);
       if (border > y) t[i] -= 1.f;
       if (border + s <= y && s != 0.f) t[i] += 1.f;
@@ -74,14 +74,15 @@ __device__ __forceinline__ uint32_t q4_codes8(const float (&x)[8], float top, fl
   }
   if (__any_sync(0xFFFFFFFFu, 7.f * s < top)) {  // (a power at its limit)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = fminf(fmaxf(t[i], 1025.5f), 1039.5f);
+    for (int i = 0; i < 8; ++i) t[i] = fminf(fmaxf(t[i], 129.5f), 143.5f);
   }
-  // four nibbles side by side from bit 13 on
-  uint32_t a[2] = {0, 0};
+  // the third bytes, four even and four odd ones side by side
+  uint32_t half[2];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    a[i >> 2] += (__float_as_uint(t[i]) & 0x1E000u) << (4 * (i & 3));
-  return a[0] >> 13 | a[1] << 3;
+  for (int i = 0; i < 2; ++i)
+    half[i] = __byte_perm(__byte_perm(__float_as_uint(t[i]), __float_as_uint(t[i + 2]), 0x0062),
+                          __byte_perm(__float_as_uint(t[i + 4]), __float_as_uint(t[i + 6]), 0x0062), 0x5410);
+  return half[1] * 16u + half[0];
 }
 // The factor of a vector's power byte; 255 is NaN.
 __device__ __forceinline__ float q4_power(uint32_t byte) { return q8_scale(byte); }
