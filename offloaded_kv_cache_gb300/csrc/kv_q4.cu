@@ -4,8 +4,8 @@
 //
 // 73 bytes a vector where 16-bit data takes 256: memory bounds the read back (4 x <= 32768
 // tokens, 8 kv heads, bf16: 92 us, 568 MB, 6.2 TB/s), the append nearly: its issue slots are
-// busy for some 70% of the time (32 x <= 513 tokens, 32 kv heads: f16 27 us, 148 MB, 5.4 TB/s;
-// fp32 48 us, 5.5 TB/s).  A decode step's append (2.2 us) is the launch and two round trips.
+// busy for some 70% of the time (32 x <= 513 tokens, 32 kv heads: f16 26 us, 148 MB, 5.6 TB/s;
+// fp32 47 us, 5.6 TB/s).  A decode step's append (2.2 us) is the launch and two round trips.
 #include <algorithm>
 #include <type_traits>
 
@@ -59,6 +59,17 @@ template <class T> __device__ __forceinline__ uint32_t q4_top16(const uint4 (&w)
   const Two top = __hmax2_nan(__hmax2_nan(m[0], m[1]), __hmax2_nan(m[2], m[3]));
   const uint32_t t = reinterpret_cast<const uint32_t &>(top);
   return max(t & 0xFFFFu, t >> 16);
+}
+__device__ __forceinline__ uint32_t q4_top32(const uint4 (&w)[2]) {  // of eight fp32 elements
+  const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+  float m[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m[i] = fabsf(__uint_as_float(u[i]));
+#pragma unroll
+  for (int n = 4; n > 0; n >>= 1)
+#pragma unroll
+    for (int i = 0; i < n; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m[i]) : "f"(m[i + n]));
+  return __float_as_uint(m[0]);
 }
 template <class T>
 __global__ void __launch_bounds__(kThreads) q4_append_kernel(const AppendArgs a) {
@@ -115,7 +126,7 @@ __global__ void __launch_bounds__(kThreads) q4_append_kernel(const AppendArgs a)
     } else {
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
-        top[w] = q8_top(s.w[w]);
+        top[w] = q4_top32(s.w[w]);
         top[w] = group[w] = max(top[w], __shfl_xor_sync(0xFFFFFFFFu, top[w], 1));
 #pragma unroll
         for (int off = 2; off < kLanes; off <<= 1)
