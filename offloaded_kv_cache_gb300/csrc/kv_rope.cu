@@ -9,8 +9,8 @@
 //
 // Each byte is read and written once, and a pair's sine and cosine serve all heads of a
 // kv head's group: memory bounds it, for a few tokens the launch and two round trips.
-// 32 prompts of <= 513 tokens, 32/32 heads, f16: 41 us, 230 MB, 5.6 TB/s; append of 4 x <= 2048,
-// 32/8 heads, bf16, with the index: 21 us, 102 MB, 4.9 TB/s; 32 x 1: 2.4 us, append 3.0.
+// 32 prompts of <= 513 tokens, 32/32 heads, f16: 40 us, 230 MB, 5.8 TB/s; append of 4 x <= 2048,
+// 32/8 heads, bf16, with the index: 20 us, 102 MB, 5.2 TB/s; 32 x 1: 2.4 us, append 3.0.
 #include <algorithm>
 #include <climits>
 #include <type_traits>
@@ -177,7 +177,8 @@ __device__ __forceinline__ void word_bounds(const uint32_t *at, int stride, int 
 
 // Block (sequence, tile of tokens, kv heads), 16 or 32 tokens of the tile at a time: first a
 // thread a pair takes the tokens' sines and cosines into shared memory, then a group of 8 or 16
-// lanes a vector turns and stores, kFlight vectors loaded before the first is stored; per_token
+// lanes a vector turns and stores, kFlight vectors loaded before the first is stored, the first of
+// them before the angles are taken (after: the prompts above 41 us, the append 20.4); per_token
 // groups share a token.  A tile is a page where the index is kept, so that its keys meet
 // in one block: they are left in shared memory too, and looked over there, in totalOrder, at
 // the end.
@@ -234,16 +235,30 @@ __global__ void __launch_bounds__(2 * kThreads, sizeof(T) == 2 ? 2 : 1) rope_ker
   const uint64_t f = turns_of(freq);
   for (int i0 = lo; i0 < hi; i0 += at_once) {
     const int tokens = min(at_once, hi - i0);
+    const int mine = grp / a.per_token, i = i0 + mine;
+    const long long row = r.q0 + i;
+    const long long in = (row * a.Hkv + h0) * kHeadDim;
+    const long long at = (row * a.Hq + (long long)h0 * a.G) * kHeadDim;
+    Piece<T, kCh> x[kFlight];
+    const auto load = [&](int v0) {
+#pragma unroll
+      for (int k = 0; k < kFlight; ++k) {
+        const int v = v0 + k * a.per_token;
+        if (v >= count) continue;
+        const T *src = v < keys      ? static_cast<const T *>(a.k) + in + v * kHeadDim
+                       : v < rows_kv ? static_cast<const T *>(a.v) + in + (v - keys) * kHeadDim
+                                     : static_cast<const T *>(a.q) + at + (v - rows_kv) * kHeadDim;
+        x[k].load(0, src + c0);
+        x[k].load(1, src + c1);
+      }
+    };
+    if (mine < tokens) load(sub);
     if (pair < a.pairs) {
       for (int k = tid / kPairs; k < tokens; k += blockDim.x / kPairs)
         cos_sin(f, a.at ? a.at[r.q0 + i0 + k] : r.len + i0 + k, a.scale, cosine[k][pair], sine[k][pair]);
     }
     __syncthreads();
-    const int mine = grp / a.per_token, i = i0 + mine;
     if (mine < tokens) {
-      const long long row = r.q0 + i;
-      const long long in = (row * a.Hkv + h0) * kHeadDim;
-      const long long at = (row * a.Hq + (long long)h0 * a.G) * kHeadDim;
       // (rows of the cache fit int32)
       const long long out =
           a.bt ? (((long long)ph * a.Hkv + h0) * a.ps + slot0 + (i - lo)) * kHeadDim : in;
@@ -259,18 +274,7 @@ __global__ void __launch_bounds__(2 * kThreads, sizeof(T) == 2 ? 2 : 1) rope_ker
         }
       }
 #pragma unroll 1
-      for (int v0 = sub; v0 < count; v0 += kFlight * a.per_token) {
-        Piece<T, kCh> x[kFlight];
-#pragma unroll
-        for (int k = 0; k < kFlight; ++k) {
-          const int v = v0 + k * a.per_token;
-          if (v >= count) continue;
-          const T *src = v < keys      ? static_cast<const T *>(a.k) + in + v * kHeadDim
-                         : v < rows_kv ? static_cast<const T *>(a.v) + in + (v - keys) * kHeadDim
-                                       : static_cast<const T *>(a.q) + at + (v - rows_kv) * kHeadDim;
-          x[k].load(0, src + c0);
-          x[k].load(1, src + c1);
-        }
+      for (int v0 = sub; v0 < count;) {
 #pragma unroll
         for (int k = 0; k < kFlight; ++k) {
           const int v = v0 + k * a.per_token;
@@ -287,6 +291,8 @@ __global__ void __launch_bounds__(2 * kThreads, sizeof(T) == 2 ? 2 : 1) rope_ker
             x[k].store(1, keep + c1);
           }
         }
+        v0 += kFlight * a.per_token;
+        if (v0 < count) load(v0);
       }
     }
     __syncthreads();
