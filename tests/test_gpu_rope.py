@@ -272,6 +272,36 @@ def test_index(dtype):
             assert torch.equal(mm.view(bits), untouched.view(bits))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("hq,hkv,ps,rot,inter", [(32, 8, 16, 128, False), (14, 7, 32, 64, True), (32, 8, 64, 72, False),
+                                                 (24, 12, 128, 128, True), (8, 8, 16, 8, False)])
+def test_many_sequences(dtype, hq, hkv, ps, rot, inter):
+    """Enough blocks for several kv heads to share one: rows, the append, its index."""
+    bits = torch.int32 if dtype == "f32" else torch.int16
+    g = torch.Generator().manual_seed(hq + ps)
+    before = torch.randint(0, 140, (270,), generator=g).tolist()
+    news = torch.randint(0, 41, (270,), generator=g).tolist()
+    c = Chunk(dtype, hq, hkv, ps, before, news, rot, inter, max_new=40)
+    mm = c.index()
+    anew = mm.clone()
+    out = torch.zeros(len(news), dtype=torch.int32, device="cuda")
+    c.put(out, mm)
+    c.check_cache()
+    near(c.q_out, *c.rows(c.q))
+    c.build(anew, out)
+    torch.cuda.synchronize()
+    assert torch.equal(mm.view(bits), anew.view(bits)) and out.tolist() == c.p.lens
+    q = c.q_out.clone()
+    c.q_out.fill_(7.0)
+    c.put(out)  # without an index the tiles are of 16 tokens
+    assert torch.equal(q, c.q_out)
+    c.check_cache()
+    c.turn()
+    torch.cuda.synchronize()
+    near(c.k_out, *c.rows(c.k))
+    assert torch.equal(q, c.q_out)
+
+
 @pytest.mark.parametrize("news", [[1, 1, 1], [40, 0, 7], [1000, 3, 64], [0, 0, 0]])
 @pytest.mark.parametrize("index", [False, True])
 @pytest.mark.parametrize("hq,hkv", [(8, 4), (10, 5), (3, 1)])
