@@ -10,7 +10,7 @@
 // Each byte is read and written once, and a pair's sine and cosine serve all heads of a
 // kv head's group: memory bounds it, for a few tokens the launch and two round trips.
 // 32 prompts of <= 513 tokens, 32/32 heads, f16: 40 us, 230 MB, 5.8 TB/s; append of 4 x <= 2048,
-// 32/8 heads, bf16, with the index: 20 us, 102 MB, 5.2 TB/s; 32 x 1: 2.4 us, append 3.0.
+// 32/8 heads, bf16, with the index: 20 us, 102 MB, 5.2 TB/s; 32 x 1: 2.4 us, append 3.1.
 #include <algorithm>
 #include <climits>
 #include <type_traits>
