@@ -97,7 +97,7 @@ long long seen_tokens(const kv_shape *s, int window) {
 //     24 rows 29.7 / 26.9; 17 x 456, 32 kv heads: 8 rows 24 / 34, 16 rows 30 / 35
 //   fp32 q, 8-bit, 4 x 32k: 8 rows 70 / 410, 16 rows 106 / 655; 4 x 1.9k: 256 rows
 //     74 / 132; 8448 rows over 528, 2 kv heads: 289 / 112; window 90, 880 rows: 104 / 53
-//   4-bit (kv_chunk_q4.cu), 4 x 32k: 16 rows 48 / 74, 24 rows 56 / 74, 32 rows 80 / 75; 16 x 2k,
+//   4-bit (kv_chunk_q4.cu), 4 x 32k: 16 rows 47 / 74, 24 rows 54 / 74, 32 rows 80 / 75; 16 x 2k,
 //     f16: 24 rows 26 / 27, 32 rows 28 / 27; 17 x 456, 32 kv heads: 16 rows 25 / 35, 32 rows 36 /
 //     36.  fp32 q (the other kernel reads a copy in fp32): 4 x 32k: 8 rows 40 / 356, 64 rows 164 /
 //     798; 4 x 8k: 2048 rows 1209 / 3307; 16 x 500: 64 rows 23 / 75, 1024 rows 266 / 342
@@ -108,6 +108,14 @@ int few_rows_limit(const kv_shape *s, int window, CacheForm form) {
   const bool is_short = seen <= 4096;
   return form != kOwnForm ? (is_short ? 24 : 16) : (is_short ? 16 : 8);
 }
+// The 4-bit cache's kernel for few rows: above so many tokens that a row may see, eight
+// warps a CTA, which leaves half as many parts to join; up to it four, between which short
+// units divide better.  (us, four / eight, 8 kv heads, 8 rows: 8 x 64k 105 / 102, 4 x 32k 38 /
+// 34, 16 x 8k 33 / 33, 4 x 8k 24 / 20, 32 x 4k 32 / 32, 4 x 4k 21 / 16, 64 x 2k 32 / 35, 16 x 2k
+// 18.3 / 18.9, 4 x 700 9.4 / 10; 32 kv heads, one row, 64 x 2k 107 / 128, 8 x 16k 102 / 102.)
+#ifndef KVS_Q4_EIGHT_WARPS
+#define KVS_Q4_EIGHT_WARPS 4000
+#endif
 // fp32: up to this many packed rows K and V go straight to registers, in units of
 // 4 or 8 rows; above, through shared memory in units of 64.  (4 x 8k tokens, 8 kv
 // heads, us, units of 8 / of 64: 12 rows 73 / 175, 24 rows 111 / 176, 32 rows 131 /
@@ -120,6 +128,7 @@ struct ChunkPlan {
   bool q8 = false;    // the kernel reads the 8-bit cache itself
   bool q4 = false;    // the kernel reads the 4-bit cache itself
   bool few = false;   // the kernel for few rows
+  bool eight = false; // whose CTAs have eight warps, not four (4-bit cache)
   bool stage = false; // K/V pass through the workspace in 16 bits
   bool renumber = false;  // the staged pages have a block table of their own
   long long stage_pages = 0;
@@ -157,7 +166,8 @@ ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, CacheForm form) 
   pl.few = packed <= few_rows_limit(s, c->window, pl.q8 ? kQ8Form : pl.q4 ? kQ4Form : kOwnForm);
   if (pl.few) {
     pl.stage = !hbm;
-    const FewShape sh = pl.q4 ? chunk_q4_shape(s->dtype) : chunk_few_shape(s->dtype, pl.q8);
+    pl.eight = pl.q4 && s->dtype != KV_F32 && seen_tokens(s, c->window) > KVS_Q4_EIGHT_WARPS;
+    const FewShape sh = pl.q4 ? chunk_q4_shape(s->dtype, pl.eight) : chunk_few_shape(s->dtype, pl.q8);
     pl.rows = sh.rows;
     pl.tile = sh.tile;
     per_sm = sh.per_sm;
@@ -367,7 +377,7 @@ int chunk_common(const kv_shape *s, const kv_chunk *c, const void *q, const void
     if ((rc = page_map(s, pl.q8, pl.tile, a.v, pages, &tv)) != KV_OK) return rc;
   }
   if (pl.few && pl.q4) {
-    e = launch_chunk_q4(s->dtype, a, pl.ctas, st);
+    e = launch_chunk_q4(s->dtype, pl.eight, a, pl.ctas, st);
   } else if (pl.few) {
     e = launch_chunk_few(s->dtype, pl.q8, a, tk, tv, pl.ctas, st);
   } else if (pl.mma) {

@@ -2,17 +2,17 @@
 // step, a few proposed tokens), and for fp32 q.  kv_chunk.cuh has the formula and how the
 // work is cut.
 //
-// A CTA is four warps, which take 32 tokens each in turn: a warp copies its own codes, scales
-// and powers (asynchronously, one step ahead, the block table's entries before that), has a
-// softmax of its own, and waits for no other until the end of a segment, where their results
-// are joined.  (A warp that copied for four others by TMA and bulk copies was what bounded
+// A CTA is four warps, or eight for long contexts, which take 32 tokens each in turn: a warp
+// copies its own codes, scales and powers (asynchronously, one step ahead, the block table's
+// entries before that), has a softmax of its own, and waits for no other until the end of a
+// segment, where their results are joined.  (A warp that copied for four others by TMA and bulk copies was what bounded
 // small pages: six copies per page of 16 tokens.)
 //
 // What bounds it: 4 bits leave two instructions a byte of the cache.  16 tokens by 8 rows take
 // some 390 of a warp's instructions, 130 of them to expand the nibbles.  One token over 8 x
-// <= 65536, 64/8 heads, bf16: 105 us with the joining of parts, 470 MB, 4.5 TB/s; the issue
-// slots are busy for 58% of the time, DRAM for 48%.  Four CTAs per SM at 128 registers (five at
-// 96 spill: 139 us); pages looked up step by step cost 4 us.
+// <= 65536, 64/8 heads, bf16: 102 us with the joining of parts, 470 MB, 4.6 TB/s; the issue
+// slots are busy for 58% of the time, DRAM for 48%.  Sixteen warps an SM at 128 registers (twenty
+// at 96 spill: 139 us); pages looked up step by step cost 4 us.
 //
 // The products are 16 x 8 x 16, units 8 rows, as in kv_chunk_few.cu:
 //   S^T (16 tokens x 8 rows) = K Q^T: the products sum over the channels, in any order that
@@ -38,8 +38,6 @@ namespace {
 constexpr float kMoveAt = 8.f;  // the maxima move when a weight would exceed 2^8 ...
 constexpr float kShift = 7.f;   // ... times 2^7, so that small weights keep their f16 bits
 constexpr int kRows = 8;        // rows of a unit
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kStep = 32;       // tokens of a warp's step
 constexpr int kTile = 64;       // tokens per KV tile: what the work is cut by
 
@@ -48,12 +46,13 @@ constexpr int kTile = 64;       // tokens per KV tile: what the work is cut by
 constexpr int kVAt = kStep * kQ4Bytes, kGroupAt = 2 * kVAt, kPowerAt = kGroupAt + 2 * kStep * kQ4Scales;
 constexpr int kSlot = (kPowerAt + 2 * kStep + 127) / 128 * 128;
 
-template <class T> struct Shape {
-  static constexpr int kCtas = sizeof(T) == 2 ? 4 : 2;  // per SM
+// A CTA has kWarps warps, 4 or (16-bit data) 8; an SM sixteen, of fp32 q eight.
+template <class T, int kWarps> struct Shape {
+  static constexpr int kCtas = (sizeof(T) == 2 ? 16 : 8) / kWarps;  // per SM
   static constexpr int kSlots = sizeof(T) == 2 ? 2 : 3;
 };
-template <class T> struct Shared {
-  alignas(128) uint8_t slot[kWarps][Shape<T>::kSlots][kSlot];
+template <class T, int kWarps> struct Shared {
+  alignas(128) uint8_t slot[kWarps][Shape<T, kWarps>::kSlots][kSlot];
   float o[kWarps][kRows][kHeadDim];  // per warp, at the end of a segment
   float m[kWarps][kRows], r[kWarps][kRows], l[kWarps][kRows];
   ChunkShare<8> share;
@@ -116,13 +115,14 @@ template <int n> __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
 }
 
-template <class T>
-__global__ void __launch_bounds__(kThreads, Shape<T>::kCtas)
+template <class T, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, Shape<T, kWarps>::kCtas)
     chunk_q4_kernel(const __grid_constant__ ChunkArgs a) {
   constexpr bool kTwo = sizeof(T) == 4;  // q and the weights in two terms
-  constexpr int kTerms = kTwo ? 2 : 1, kSlots = Shape<T>::kSlots;
+  constexpr int kTerms = kTwo ? 2 : 1, kSlots = Shape<T, kWarps>::kSlots;
   extern __shared__ __align__(128) uint8_t smem[];
-  Shared<T> &sh = *reinterpret_cast<Shared<T> *>(smem);
+  using Sh = Shared<T, kWarps>;
+  Sh &sh = *reinterpret_cast<Sh *>(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g8 = lane >> 2, t4 = lane & 3;  // row and column group of the fragments
   const int tg = token_of_row(g8);          // the token of row g8 (and + 8)
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T>::kCtas)
       }
       __syncthreads();
       const bool whole = g.whole();
-      for (int n = tid >> 4; n < min(kRows, g.nrows); n += kThreads / 16) {
+      for (int n = tid >> 4; n < min(kRows, g.nrows); n += 2 * kWarps) {
         const int c = (tid & 15) * 8;
         float top = -INFINITY;
 #pragma unroll
@@ -520,25 +520,27 @@ __global__ void __launch_bounds__(kThreads, Shape<T>::kCtas)
   }
 }
 
-template <class T> cudaError_t q4_go(const ChunkArgs &a, int ctas, cudaStream_t st) {
-  constexpr int bytes = (int)sizeof(Shared<T>);
-  static_assert(bytes <= (228 / Shape<T>::kCtas - 1) * 1024, "shared memory");
+template <class T, int kWarps> cudaError_t q4_go(const ChunkArgs &a, int ctas, cudaStream_t st) {
+  constexpr int bytes = (int)sizeof(Shared<T, kWarps>);
+  static_assert(bytes <= (228 / Shape<T, kWarps>::kCtas - 1) * 1024, "shared memory");
   const cudaError_t e = cudaFuncSetAttribute(
-      chunk_q4_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+      chunk_q4_kernel<T, kWarps>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  return launch_pdl(chunk_q4_kernel<T>, dim3(ctas), dim3(kThreads), bytes, st, a);
+  return launch_pdl(chunk_q4_kernel<T, kWarps>, dim3(ctas), dim3(32 * kWarps), bytes, st, a);
 }
 
 }  // namespace
 
-FewShape chunk_q4_shape(int dtype) {
-  return FewShape{kRows, kTile, dtype == KV_F32 ? Shape<float>::kCtas : Shape<__half>::kCtas};
+FewShape chunk_q4_shape(int dtype, bool eight) {
+  return FewShape{kRows, kTile, dtype == KV_F32 ? Shape<float, 4>::kCtas
+                                : eight         ? Shape<__half, 8>::kCtas
+                                                : Shape<__half, 4>::kCtas};
 }
 
-cudaError_t launch_chunk_q4(int dtype, const ChunkArgs &a, int ctas, cudaStream_t st) {
-  return dtype == KV_F32   ? q4_go<float>(a, ctas, st)
-         : dtype == KV_F16 ? q4_go<__half>(a, ctas, st)
-                           : q4_go<__nv_bfloat16>(a, ctas, st);
+cudaError_t launch_chunk_q4(int dtype, bool eight, const ChunkArgs &a, int ctas, cudaStream_t st) {
+  if (dtype == KV_F32) return q4_go<float, 4>(a, ctas, st);
+  if (dtype == KV_F16) return eight ? q4_go<__half, 8>(a, ctas, st) : q4_go<__half, 4>(a, ctas, st);
+  return eight ? q4_go<__nv_bfloat16, 8>(a, ctas, st) : q4_go<__nv_bfloat16, 4>(a, ctas, st);
 }
 
 }  // namespace kvs

@@ -101,8 +101,8 @@ FewShape chunk_few_shape(int dtype, bool q8);
 cudaError_t launch_chunk_few(int dtype, bool q8, const ChunkArgs &a, const CUtensorMap &tk,
                              const CUtensorMap &tv, int ctas, cudaStream_t st);
 // few rows, and fp32 q, over the 4-bit cache
-FewShape chunk_q4_shape(int dtype);
-cudaError_t launch_chunk_q4(int dtype, const ChunkArgs &a, int ctas, cudaStream_t st);
+FewShape chunk_q4_shape(int dtype, bool eight);  // (eight warps a CTA, or four)
+cudaError_t launch_chunk_q4(int dtype, bool eight, const ChunkArgs &a, int ctas, cudaStream_t st);
 // the pages it needs into device memory in the shape's type (table: their new block table,
 // or null); 32 bits from the 4-bit cache only
 cudaError_t launch_chunk_stage(int dtype, CacheForm form, const ChunkArgs &c, void *k_out, void *v_out,

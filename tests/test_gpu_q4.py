@@ -345,6 +345,39 @@ def test_few_rows(dtype, hq, hkv, n, window, ps):
     run(Problem4(dtype, hq, hkv, ps, [n + 120, n, 390, 5], [n, n, 1, 0], window, seed=n))
 
 
+# A table for long contexts takes the form of twice as many warps.
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("hq,hkv,n", FEW)
+@pytest.mark.parametrize("window", [0, 40])
+@pytest.mark.parametrize("ps", [16, 128])
+def test_few_rows_of_a_wide_table(dtype, hq, hkv, n, window, ps):
+    run(Problem4(dtype, hq, hkv, ps, [n + 120, n, 390, 5, 1100], [n, n, 1, 0, 1], window, seed=n,
+                 extra_pages=6000 // ps))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("n", [1, 9])
+def test_odd_values_under_a_wide_table(dtype, n):
+    """Scores that rise from tile to tile, vectors of all sizes, one of NaN, and bad pages."""
+    p = Problem4(dtype, 2, 1, 16, [700, 1300, 600], [n, n, 1], scale=1.0, extra_pages=400)
+    p.q = torch.zeros_like(p.q)
+    p.q[:, :, 0] = 1
+    for j in range(700):
+        p.k[p.table[0, j // 16], :, j % 16, 0] = -100 + j / 3.5
+    x = p.k.double().nan_to_num(nan=0.0).numpy()
+    p.four["k"] = [torch.from_numpy(t) for t in quantise4(x, dtype)]
+    c, s, w = p.four["v"]
+    g = torch.Generator().manual_seed(6)
+    p.four["v"][2] = torch.where(w == 255, w, torch.randint(112, 124, w.shape, generator=g).to(torch.uint8))
+    p.set_nan("v", p.table[1, 1290 // 16], slice(None), 1290 % 16)
+    p.table[1, 7] = p.pages
+    p.table[2, 30] = -1
+    p.upload()
+    p.attend()
+    assert kv.kv_device_status() == kv.KV_ERR_BOUNDS
+    check(p.d_out, *p.expected())
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("n", [2, 20, 150])
 def test_vectors_of_very_different_size(dtype, n):
