@@ -11,7 +11,7 @@
 // What bounds it: 4 bits leave two instructions a byte of the cache.  16 tokens by 8 rows take
 // some 390 of a warp's instructions, 130 of them to expand the nibbles.  One token over 8 x
 // <= 65536, 64/8 heads, bf16: 102 us with the joining of parts, 470 MB, 4.6 TB/s; the issue
-// slots are busy for 58% of the time, DRAM for 48%.  Sixteen warps an SM at 128 registers (twenty
+// slots are busy for 58% of the time, DRAM for 46%.  Sixteen warps an SM at 128 registers (twenty
 // at 96 spill: 139 us); pages looked up step by step cost 4 us.
 //
 // The products are 16 x 8 x 16, units 8 rows, as in kv_chunk_few.cu:
