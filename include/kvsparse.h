@@ -141,7 +141,8 @@ int kv_page_minmax_build(const kv_shape *shape, const void *k_cache, const int32
  * min/max keeps the overwritten key too (a looser, still valid bound).
  * context_lens_out (may be NULL, may equal context_lens): receives len_b + 1.
  * A row whose len_b or block-table entry is out of range is skipped, keeps
- * its length and sets KV_ERR_BOUNDS in the device status word. */
+ * its length and sets KV_ERR_BOUNDS in the device status word.  Where a page
+ * window is in use, kv_window_trim comes first. */
 int kv_append_token(const kv_shape *shape, const void *k_new, const void *v_new, void *k_cache,
                     void *v_cache, const int32_t *block_table, const int32_t *context_lens,
                     int32_t *context_lens_out, void *minmax, void *stream);
@@ -390,6 +391,20 @@ size_t kv_window_workspace_bytes(const kv_shape *shape, int32_t k, int32_t cache
 
 int kv_window_reset(const kv_shape *shape, const kv_window *win, void *stream);
 
+/* Drops from the window every page that does not lie wholly below its row's
+ * length: pages p with (p + 1) * ps > context_lens[b] leave both maps, their
+ * slots become free.  To be called, with the lengths BEFORE, ahead of every call
+ * that stores tokens behind them (kv_append_token, kv_rope_append, a caller's own
+ * kernel), and after lengths were taken back: a slot does not say how many of its
+ * page's tokens its copy holds, and of the hits only the row's last page is
+ * fetched again, so that a page copied while it was partly filled would keep the
+ * slots behind that fill as they are once later pages follow it.  (The last page
+ * is fetched at every step anyway: nothing else crosses the link for it.)
+ * 0 <= context_lens[b] <= maxP * ps; a row out of that range keeps its pages and
+ * sets KV_ERR_BOUNDS in the device status word. */
+int kv_window_trim(const kv_shape *shape, const kv_window *win, const int32_t *context_lens,
+                   void *stream);
+
 /* One decode step of sparse attention through the window.  Inputs as
  * kv_sparse_decode_attn (k_cache / v_cache where kv_loc says, typically
  * pinned host memory), plus this step's page scores [B][Hq][maxP] (the
@@ -403,7 +418,8 @@ int kv_window_reset(const kv_shape *shape, const kv_window *win, void *stream);
  *             ascending slot order;
  *   fetch   = the misses, and the row's last page when it is a hit (tokens
  *             may have been appended since it was copied);
- * then attention runs exactly as kv_sparse_decode_attn -- same out -- reading
+ * then attention runs exactly as kv_sparse_decode_attn -- same out, given that
+ * kv_window_trim preceded what was stored since the last step -- reading
  * the hits from the window (HBM) and the fetched pages from k_cache /
  * v_cache, whose valid tokens it also stores into their window slots.  When
  * G exceeds the heads one attention CTA covers (G > 8; G > 4 for fp32), a
@@ -527,7 +543,7 @@ int kv_rope(const kv_shape *shape, const kv_chunk *chunk, const kv_rope_plan *ro
  * A token whose block-table entry is out of range is dropped; its sequence keeps its
  * length, and KV_ERR_BOUNDS is recorded (the same for a sequence that is skipped whole,
  * whose rows of q_out are not written).  The pages written must not be shared with
- * another row. */
+ * another row.  Where a page window is in use, kv_window_trim comes first. */
 int kv_rope_append(const kv_shape *shape, const kv_chunk *chunk, const kv_rope_plan *rope,
                    const void *q, void *q_out, const void *k_new, const void *v_new, void *k_cache,
                    void *v_cache, const int32_t *block_table, const int32_t *context_lens,

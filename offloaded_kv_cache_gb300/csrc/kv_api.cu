@@ -1106,6 +1106,25 @@ int kv_window_reset(const kv_shape *shape, const kv_window *win, void *stream) {
   return KV_OK;
 }
 
+int kv_window_trim(const kv_shape *shape, const kv_window *win, const int32_t *context_lens,
+                   void *stream) {
+  KV_API_RANGE();
+  int rc = check_shape(shape);
+  if (rc) return rc;
+  if (!win || win->cache_pages < 1 || !al4(win->slot_page) || !al4(win->page_slot) ||
+      !al4(context_lens))
+    return KV_ERR_INVALID_ARG;
+  if ((long long)shape->batch * shape->num_kv_heads > INT_MAX) return KV_ERR_UNSUPPORTED;
+  const int dev = current_device();
+  if (dev < 0) return KV_ERR_CUDA;
+  int *status = status_ptr(dev);
+  if (!status) return KV_ERR_CUDA;
+  const cudaError_t e = launch_window_trim(
+      context_lens, shape->batch, shape->num_kv_heads, shape->page_size, shape->max_pages_per_seq,
+      win->cache_pages, win->slot_page, win->page_slot, status, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+}
+
 int kv_sparse_decode_attn_window(const kv_shape *shape, const void *q, const void *k_cache,
                                  const void *v_cache, const int32_t *block_table,
                                  const int32_t *context_lens, const int32_t *indices, int32_t k,

@@ -34,6 +34,9 @@ cudaError_t launch_window_step(const int32_t *indices, const float *scores, cons
                                int32_t *slot_page, int32_t *page_slot, uint32_t *fetch_bits,
                                int32_t *stats, int gc, int umax, int32_t *upages,
                                uint32_t *umasks, int32_t *ucount, int *status, cudaStream_t st);
+cudaError_t launch_window_trim(const int32_t *ctx, int B, int Hkv, int ps, int maxP, int C,
+                               int32_t *slot_page, int32_t *page_slot, int *status,
+                               cudaStream_t st);
 cudaError_t launch_fill(int32_t *p, long long n, int32_t v, cudaStream_t st);
 // one decode step's q and context lengths, mapped host -> device buffers
 cudaError_t launch_stage_inputs(const void *q_src, void *q_dst, size_t q_bytes,

@@ -18,6 +18,10 @@
 // then the window instantiation of the sparse attention reads the hits from
 // the window and the fetched pages from the (host) cache, and stores each
 // fetched page's valid tokens into its slot as it goes.
+// A slot does not say how many tokens its copy holds, so a page that is about to
+// grow leaves the window first:
+//   window_trim_kernel  one CTA per group: the pages that do not lie wholly below
+//                       the length before an append are dropped.
 #include <algorithm>
 
 #include "kv_select.cuh"
@@ -291,6 +295,29 @@ __global__ void __launch_bounds__(kWinThreads)
   }
 }
 
+// Drops from group (b, kv head)'s window the pages that do not lie wholly below the row's
+// length.  Tens of slots a thread at most, read once: the launch and two round trips.
+__global__ void __launch_bounds__(256)
+    window_trim_kernel(const int32_t *ctx, int Hkv, int ps, int maxP, int C, int32_t *slot_page,
+                       int32_t *page_slot, int *status) {
+  pdl_wait();
+  const long long g = blockIdx.x;
+  const int len = ctx[g / Hkv];
+  pdl_trigger();
+  if (len < 0 || len > (long long)maxP * ps) {
+    if (threadIdx.x == 0) flag_error(status, KV_ERR_BOUNDS);
+    return;
+  }
+  const int whole = len / ps;  // pages below the length
+  int32_t *sp = slot_page + g * C, *pslot = page_slot + g * maxP;
+  for (int s = threadIdx.x; s < C; s += blockDim.x) {
+    const int p = sp[s];
+    if (p < whole || p >= maxP) continue;
+    sp[s] = -1;
+    pslot[p] = -1;
+  }
+}
+
 __global__ void fill_kernel(int32_t *p, long long n, int32_t v) {
   pdl_wait();
   for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n;
@@ -326,6 +353,13 @@ cudaError_t launch_window_step(const int32_t *indices, const float *scores, cons
   return launch_pdl(window_step_kernel, dim3(blocks), dim3(kWinThreads), smem, st, indices,
                     scores, ctx, Hq, Hkv, ps, maxP, K, C, slot_page, page_slot, fetch_bits, stats,
                     status, n_update, G, gc, umax, groups, upages, umasks, ucount);
+}
+
+cudaError_t launch_window_trim(const int32_t *ctx, int B, int Hkv, int ps, int maxP, int C,
+                               int32_t *slot_page, int32_t *page_slot, int *status,
+                               cudaStream_t st) {
+  return launch_pdl(window_trim_kernel, dim3((unsigned)(B * Hkv)), dim3(256), 0, st, ctx, Hkv, ps,
+                    maxP, C, slot_page, page_slot, status);
 }
 
 cudaError_t launch_fill(int32_t *p, long long n, int32_t v, cudaStream_t st) {

@@ -120,6 +120,7 @@ def load(path: str = LIB_PATH):
         "kv_dense_decode_attn": (ctypes.c_int, [S, P, P, P, P, P, f32, P, P, sz, P]),
         "kv_window_workspace_bytes": (sz, [S, i32, i32]),
         "kv_window_reset": (ctypes.c_int, [S, ctypes.POINTER(kv_window), P]),
+        "kv_window_trim": (ctypes.c_int, [S, ctypes.POINTER(kv_window), P, P]),
         "kv_sparse_decode_attn_window": (ctypes.c_int, [S, P, P, P, P, P, P, i32, P, f32, P,
                                                         ctypes.POINTER(kv_window), P, sz, P]),
         "kv_decode_step": (ctypes.c_int, [S, ctypes.POINTER(kv_step_io), P]),
@@ -184,6 +185,12 @@ def kv_window_workspace_bytes(shape, k, cache_pages) -> int:
 def kv_window_reset(shape, win, stream=None, check=True):
     rc = load().kv_window_reset(ctypes.byref(shape), ctypes.byref(win), _stream(stream))
     return _ret(rc, "kv_window_reset", check)
+
+
+def kv_window_trim(shape, win, context_lens, stream=None, check=True):
+    rc = load().kv_window_trim(ctypes.byref(shape), ctypes.byref(win), _ptr(context_lens),
+                               _stream(stream))
+    return _ret(rc, "kv_window_trim", check)
 
 
 def kv_sparse_decode_attn_window(shape, q, k_cache, v_cache, block_table, context_lens, indices,

@@ -10,6 +10,7 @@ binding:
     sparse_step()  -> kv_page_score, kv_topk_select, kv_sparse_decode_attn
     sparse_step_fused() -> kv_select_pages, kv_sparse_decode_attn_selected
     enable_window(C), window_attn() -> kv_window_reset, kv_sparse_decode_attn_window
+                      (kv_window_trim before every append)
     dense_step()   -> kv_dense_decode_attn
     host_step()    -> kv_decode_step (host q / lengths in, out back)
     append_chunk() -> kv_rope_append (a chunk of new tokens, q and keys turned)
@@ -187,6 +188,7 @@ class DecodeLayer:
         self.out = torch.empty((spec.batch, spec.num_q_heads, spec.head_dim),
                                dtype=torch.float32, device=dev)
         self.mean = None  # the mean-key index, allocated by build_mean_index()
+        self.window = None  # the page window, allocated by enable_window()
         self.ws_dense_bytes = kv.kv_attn_workspace_bytes(self.shape, 0)
         self.ws_sparse_bytes = kv.kv_attn_workspace_bytes(self.shape, k) if self.topk else 0
         self.ws_topk_bytes = kv.kv_topk_workspace_bytes(self.shape, k)
@@ -216,6 +218,13 @@ class DecodeLayer:
         if nbytes > self.workspace.numel():
             self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         kv.kv_window_reset(self.shape, self.window, self._st(stream))
+
+    def trim_window(self, stream=None):
+        """Drop the window's pages that do not lie wholly below the rows' lengths: what
+        append() and append_chunk() do first, and a program that stores tokens or takes
+        lengths back itself (a captured graph holds it if the window was there then)."""
+        if self.window is not None:
+            kv.kv_window_trim(self.shape, self.window, self.context_lens, self._st(stream))
 
     def window_attn(self, indices=None, scores=None, stream=None):
         stream = self._st(stream)
@@ -254,6 +263,7 @@ class DecodeLayer:
         repeated call rewrites the same slot.
         """
         stream = self._st(stream)
+        self.trim_window(stream)
         kv.kv_append_token(self.shape, k_new, v_new, self.k_cache, self.v_cache, self.block_table,
                            self.context_lens, self.context_lens if advance else None,
                            self.minmax if update_index else None, stream)
@@ -379,6 +389,7 @@ class DecodeLayer:
                 out = torch.empty_like(q)
         chunk = kv.make_chunk(q_start, total, max_q_len)
         plan = rotary.plan(total, positions) if rotary is not None else None
+        self.trim_window(stream)
         kv.kv_rope_append(self.shape, chunk, plan, q, out, k_new, v_new, self.k_cache, self.v_cache,
                           self.block_table, self.context_lens,
                           self.context_lens if advance else None,
