@@ -171,7 +171,9 @@ int kv_page_score(const kv_shape *shape, const void *q, const void *minmax,
  * values span few binades), the division in fp64.  Entries of unreferenced
  * pages are not written.
  * kv_page_mean_refresh: the same for the page holding each row's last token
- * only (B x Hkv entries) -- what an append changes.
+ * only (B x Hkv entries) -- what one kv_append_token changes.  A chunk
+ * (kv_rope_append), or several appends, may have filled pages before it:
+ * kv_page_mean_build then.
  * kv_page_score_mean: scores[b][h][p] = sum_c q_c * mean_c of page
  * block_table[b][p], kv head h / G (an estimate of q . k, not a bound), fp32
  * accumulation; p >= P_b -> -inf.  Same layouts and errors as kv_page_score;
@@ -537,7 +539,8 @@ int kv_rope(const kv_shape *shape, const kv_chunk *chunk, const kv_rope_plan *ro
  *   minmax        may be NULL (no index update): the entry of every page that receives
  *                 tokens becomes the channel-wise min/max of its tokens, bit-identical to
  *                 kv_page_minmax_build on the new lengths; preconditions as in
- *                 kv_append_token
+ *                 kv_append_token.  (A mean-key index: kv_page_mean_build, not
+ *                 kv_page_mean_refresh, after a chunk.)
  *   context_lens_out  may be NULL, may equal context_lens, may not overlap it in part:
  *                 receives context_lens[b] + n_b
  * A token whose block-table entry is out of range is dropped; its sequence keeps its

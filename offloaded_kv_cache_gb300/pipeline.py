@@ -188,6 +188,8 @@ class DecodeLayer:
         self.out = torch.empty((spec.batch, spec.num_q_heads, spec.head_dim),
                                dtype=torch.float32, device=dev)
         self.mean = None  # the mean-key index, allocated by build_mean_index()
+        self._unmeant = 0  # appends since it was last brought up to date (2: or a chunk)
+        self._replayed = False  # a graph holds an append whose replays are not seen here
         self.window = None  # the page window, allocated by enable_window()
         self.ws_dense_bytes = kv.kv_attn_workspace_bytes(self.shape, 0)
         self.ws_sparse_bytes = kv.kv_attn_workspace_bytes(self.shape, k) if self.topk else 0
@@ -267,15 +269,22 @@ class DecodeLayer:
         kv.kv_append_token(self.shape, k_new, v_new, self.k_cache, self.v_cache, self.block_table,
                            self.context_lens, self.context_lens if advance else None,
                            self.minmax if update_index else None, stream)
+        self._unmeant += 1
 
     def build_mean_index(self, stream=None, last_only=False):
+        """The mean-key index of every page, or, last_only, of the pages that an append()
+        changed: those of the rows' last tokens.  A chunk, or several appends, change other
+        pages too, and the index is built whole then.  (Replays of a graph that holds an
+        append_chunk() do not pass here: from its capture on every call builds it whole.)"""
         stream = self._st(stream)
+        last_only = last_only and self.mean is not None and self._unmeant <= 1
         if self.mean is None:
             spec = self.spec
             self.mean = torch.zeros((spec.num_phys_pages, spec.num_kv_heads, spec.head_dim),
                                     dtype=TORCH_DTYPE[spec.dtype], device=self.device)
         fn = kv.kv_page_mean_refresh if last_only else kv.kv_page_mean_build
         fn(self.shape, self.k_cache, self.block_table, self.context_lens, self.mean, stream)
+        self._unmeant = 2 if self._replayed else 0
 
     def score_mean(self, stream=None):
         stream = self._st(stream)
@@ -394,6 +403,8 @@ class DecodeLayer:
                           self.block_table, self.context_lens,
                           self.context_lens if advance else None,
                           self.minmax if update_index else None, stream)
+        self._unmeant += 2
+        self._replayed |= torch.cuda.is_current_stream_capturing()
         return out
 
     # --- host views --------------------------------------------------------

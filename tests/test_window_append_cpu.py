@@ -50,8 +50,9 @@ def layer(calls, window, monkeypatch):
     for name in ("kv_window_trim", "kv_append_token", "kv_rope_append"):
         monkeypatch.setattr(kv, name, lambda *a, _n=name, **k: calls.append((_n, a)))
     monkeypatch.setattr(pipeline, "_chunk_inputs", lambda *a, **k: None)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     x = types.SimpleNamespace(shape=SHAPE, window=window, context_lens="lens", k_cache=None,
-                              v_cache=None, block_table=None, minmax=None, _st=lambda s: s)
+                              v_cache=None, block_table=None, minmax=None, _st=lambda s: s, _unmeant=0, _replayed=False)
     x.trim_window = lambda stream=None: pipeline.DecodeLayer.trim_window(x, stream)
     return x
 
