@@ -129,7 +129,7 @@ struct ChunkPlan {
   bool q4 = false;    // the kernel reads the 4-bit cache itself
   bool few = false;   // the kernel for few rows
   bool eight = false; // whose CTAs have eight warps, not four (4-bit cache)
-  bool stage = false; // K/V pass through the workspace in 16 bits
+  bool stage = false; // K/V pass through the workspace, in the shape's type
   bool renumber = false;  // the staged pages have a block table of their own
   long long stage_pages = 0;
   int rows = 64;      // packed rows per unit
@@ -150,8 +150,9 @@ struct ChunkPlan {
 };
 
 // Everything here follows from the shape and the host's bounds; the lengths
-// are known on the device only.
-ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, CacheForm form) {
+// are known on the device only.  coarse: the kernels with the largest units, whatever
+// they cost.
+ChunkPlan chunk_plan(const kv_shape *s, const kv_chunk *c, CacheForm form, bool coarse) {
   ChunkPlan pl;
   const bool q8 = form == kQ8Form, q4 = form == kQ4Form;
   const int dev = current_device();
@@ -163,7 +164,8 @@ ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, CacheForm form) 
   int per_sm = 2;
   pl.q8 = q8 && hbm;
   pl.q4 = q4 && hbm;
-  pl.few = packed <= few_rows_limit(s, c->window, pl.q8 ? kQ8Form : pl.q4 ? kQ4Form : kOwnForm);
+  pl.few = !coarse &&
+           packed <= few_rows_limit(s, c->window, pl.q8 ? kQ8Form : pl.q4 ? kQ4Form : kOwnForm);
   if (pl.few) {
     pl.stage = !hbm;
     pl.eight = pl.q4 && s->dtype != KV_F32 && seen_tokens(s, c->window) > KVS_Q4_EIGHT_WARPS;
@@ -173,30 +175,30 @@ ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, CacheForm form) 
     per_sm = sh.per_sm;
   } else if (pl.mma) {
     pl.tile = kChunkTile;
-    pl.q8 &= packed <= KVS_Q8_DIRECT_ROWS;
-    pl.q4 &= packed <= KVS_Q4_DIRECT_ROWS;
-    pl.stage = (q8 && !pl.q8) || (q4 && !pl.q4) || !hbm;
     // a Q tile holds whole tokens, for the TMA unit, where a token's heads fit
     pl.row_tile = G <= 128 ? 128 / G * G : 128;
     const long long seen = seen_tokens(s, c->window);
-    const bool many = packed > pl.row_tile;
-    pl.form = pl.q8                                               ? kPair8
-              : pl.q4                                             ? kPair4
-              : seen <= (many ? KVS_SOLO_TOKENS : KVS_SOLO_FEW) ? kSolo
-              : many                                              ? kWide
-                                                                  : kPair;
+    const bool many = packed > pl.row_tile, wide = coarse && many;
+    pl.q8 &= packed <= KVS_Q8_DIRECT_ROWS && !wide;
+    pl.q4 &= packed <= KVS_Q4_DIRECT_ROWS && !wide;
+    pl.stage = (q8 && !pl.q8) || (q4 && !pl.q4) || !hbm;
+    pl.form = pl.q8                                                        ? kPair8
+              : pl.q4                                                      ? kPair4
+              : seen <= (many ? KVS_SOLO_TOKENS : KVS_SOLO_FEW) && !wide ? kSolo
+              : many                                                       ? kWide
+                                                                           : kPair;
     pl.rows = pl.row_tile * (pl.form == kWide ? 2 : 1);
     per_sm = pl.form == kSolo ? 2 : 1;
     if (pl.form != kSolo) pl.unit_cost = 2;
   } else {
-    pl.stage = q4;  // (from host memory: fp32 from device memory is for the kernel above)
+    pl.stage = q4;  // (from host memory, or coarse: else it is for the kernel above)
     // few rows in units of 4 or 8, also while units of 64 would not fill the GPU
     const double units64 = std::min((double)s->batch * ((packed + 63) / 64),
                                     (double)c->total_q * G / 64 + s->batch);
     const bool fills = units64 * s->num_kv_heads *
                            (((double)s->max_pages_per_seq * s->page_size + pl.tile - 1) / pl.tile) >=
                        per_sm * (double)sms;
-    pl.rows = packed <= 4 ? 4 : packed <= KVS_F32_FEW_ROWS || !fills ? 8 : 64;
+    pl.rows = coarse ? 64 : packed <= 4 ? 4 : packed <= KVS_F32_FEW_ROWS || !fills ? 8 : 64;
     if (pl.rows == 8) per_sm = 1;  // resident CTAs of its kernel (registers)
   }
   // units of all sequences: full ones and one more each; no more CTAs than
@@ -229,6 +231,24 @@ ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, CacheForm form) 
   }
   pl.total = off;
   return pl;
+}
+
+// The kernels count tiles and the staging's blocks in int32, and index the staged
+// cache's rows as a cache's own.
+bool plan_fits(const kv_shape *s, const ChunkPlan &pl) {
+  if (pl.most_tiles > INT_MAX) return false;
+  return !pl.stage ||
+         (pl.stage_pages <= INT_MAX / ((long long)s->num_kv_heads * s->page_size) &&
+          q8_grid_fits(s->batch, s->max_pages_per_seq, s->page_size, s->num_kv_heads));
+}
+
+// The plan of a call: the fastest, or, where its units and tiles do not count in int32 (units
+// of 8 rows: fp32 over the 4-bit cache, one prompt of 131072 tokens with 64/8 heads), the
+// coarsest.
+ChunkPlan make_chunk_plan(const kv_shape *s, const kv_chunk *c, CacheForm form) {
+  const ChunkPlan pl = chunk_plan(s, c, form, false);
+  if (plan_fits(s, pl)) return pl;
+  return chunk_plan(s, c, form, true);
 }
 
 // A tensor map of rows of 128 channels under the 128-byte swizzle.
@@ -277,15 +297,6 @@ int q_map(const kv_shape *s, const kv_chunk *c, const void *q, int row_tile,
           CUtensorMap *map) {
   const int G = s->num_q_heads / s->num_kv_heads;
   return encode_map(MapShape{type16(s), q, c->total_q, s->num_q_heads, G, row_tile / G}, map);
-}
-
-// The kernels count tiles and the staging's blocks in int32, and index the staged
-// cache's rows as a cache's own.
-bool plan_fits(const kv_shape *s, const ChunkPlan &pl) {
-  if (pl.most_tiles > INT_MAX) return false;
-  return !pl.stage ||
-         (pl.stage_pages <= INT_MAX / ((long long)s->num_kv_heads * s->page_size) &&
-          q8_grid_fits(s->batch, s->max_pages_per_seq, s->page_size, s->num_kv_heads));
 }
 
 size_t chunk_bytes(const kv_shape *s, const kv_chunk *c, CacheForm form) {
