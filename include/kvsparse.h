@@ -543,6 +543,8 @@ int kv_rope(const kv_shape *shape, const kv_chunk *chunk, const kv_rope_plan *ro
  *                 kv_page_mean_refresh, after a chunk.)
  *   context_lens_out  may be NULL, may equal context_lens, may not overlap it in part:
  *                 receives context_lens[b] + n_b
+ * The caches, the index and the row arrays do not overlap (KV_ERR_INVALID_ARG), q and
+ * q_out, and the three arrays that are only read, apart.
  * A token whose block-table entry is out of range is dropped; its sequence keeps its
  * length, and KV_ERR_BOUNDS is recorded (the same for a sequence that is skipped whole,
  * whose rows of q_out are not written).  The pages written must not be shared with

@@ -473,6 +473,26 @@ bool rows_apart(const Rows *r, int n, int in_out) {
   return true;
 }
 
+// Whether what an append writes, the cache and its index (may be null), meets neither its rows
+// nor itself.  (k, v: as the device sees them, like the rows.)
+bool cache_apart(const kv_shape *s, const void *k, const void *v, const void *mm, const Rows *rows,
+                 int n) {
+  const size_t head = (size_t)s->num_phys_pages * s->num_kv_heads * kHeadDim * elem_bytes(s->dtype);
+  const Rows out[3] = {{static_cast<const uint8_t *>(k), head * s->page_size},
+                       {static_cast<const uint8_t *>(v), head * s->page_size},
+                       {static_cast<const uint8_t *>(mm), head * 2}};
+  const auto meet = [](const Rows &x, const Rows &y) {
+    return x.at && y.at && x.at < y.at + y.bytes && y.at < x.at + x.bytes;
+  };
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (meet(out[i], out[j])) return false;
+    for (int j = 0; j < n; ++j)
+      if (meet(out[i], rows[j])) return false;
+  }
+  return true;
+}
+
 }  // namespace
 
 extern "C" {
@@ -642,6 +662,7 @@ int kv_rope_append(const kv_shape *shape, const kv_chunk *chunk, const kv_rope_p
   const void *k = nullptr, *v = nullptr;
   if ((rc = resolve_kv(shape, k_cache, &k)) != KV_OK) return rc;
   if ((rc = resolve_kv(shape, v_cache, &v)) != KV_OK) return rc;
+  if (!cache_apart(shape, k, v, minmax, rows, 4)) return KV_ERR_INVALID_ARG;
   int *status = status_ptr(dev);
   if (!status) return KV_ERR_CUDA;
   const cudaError_t e = launch_rope(shape, chunk, rope, q, q_out, k_new, const_cast<void *>(k), v_new,
