@@ -503,7 +503,9 @@ int kv_chunk_attn(const kv_shape *shape, const kv_chunk *chunk, const void *q,
  * the other channels stay as they are, bit for bit.  Frequencies changed for longer
  * contexts are the caller's: they are in freq, and scale takes the factor that some
  * such schemes put on the turned channels (else 1).
- *   freq       [rotary_dim / 2] double, device memory: radians per position, below 2^54
+ *   freq       [rotary_dim / 2] double, device memory: radians per position, of either
+ *              sign, below 2^54 in magnitude.  A pair whose frequency is not (infinities,
+ *              NaN) is multiplied by scale alone, and KV_ERR_BOUNDS is recorded
  *   positions  [total_q] int32, device memory, or NULL: row i of sequence b's chunk is
  *              at position context_lens[b] + i
  * The angle is kept as a fraction of a turn in 64 bits, so that far positions (int32, of

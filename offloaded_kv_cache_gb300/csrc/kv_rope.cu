@@ -70,6 +70,10 @@ __device__ __forceinline__ uint64_t turns_of(double freq) {
   if (s > 0 && s < 64) f = (lo >> s) | (hi << (64 - s));
   return (u >> 63) ? 0ull - f : f;
 }
+// (others, infinities and NaN among them, give 0 above: they turn nothing)
+__device__ __forceinline__ bool turnable(double freq) {
+  return ((uint64_t)__double_as_longlong(freq) >> 52 & 0x7FF) < 1023 + 54;
+}
 // cosine and sine of f * pos turns: the nearest quarter and the rest, within an eighth
 __device__ __forceinline__ void cos_sin(uint64_t f, int pos, float scale, float &c, float &s) {
   const uint64_t a = f * (uint64_t)(long long)pos;
@@ -212,6 +216,7 @@ __global__ void __launch_bounds__(2 * kThreads, sizeof(T) == 2 ? 2 : 1) rope_ker
       if (!ok) flag_error(a.status, KV_ERR_BOUNDS);
       if (a.write_lens) a.ctx_out[b] = ok ? r.len + r.n : r.len;
     }
+    if (tid < kPairs && !turnable(freq)) flag_error(a.status, KV_ERR_BOUNDS);
   }
   pdl_trigger();
   // the block's tokens, counted from the chunk's start

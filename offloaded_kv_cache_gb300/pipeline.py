@@ -112,7 +112,10 @@ class Rotary:
     `fast` times or more over the trained length keep their speed, those that turn `slow`
     times or fewer are slowed by the stretch, those between in proportion (fast = slow:
     all are slowed); the turned channels are multiplied by `scale` (None: 0.1 ln(stretch) + 1).
-    Frequencies of any other kind: freq, a tensor [rotary_dim / 2] of radians per position."""
+    The proportion is in the number of turns.  Models whose frequencies were blended otherwise
+    (in proportion to the pair's index, with ramps rounded to whole pairs), or slowed by a
+    scheme of another kind: freq, a tensor [rotary_dim / 2] of radians per position, below 2^54
+    in magnitude."""
 
     def __init__(self, rotary_dim: int = 128, base: float = 10000.0, interleaved: bool = False,
                  stretch: float = 1.0, trained: int = 8192, fast: float = 32.0, slow: float = 1.0,
@@ -131,6 +134,8 @@ class Rotary:
                 freq = freq * (keep + (1 - keep) / stretch)
         if tuple(freq.shape) != (rotary_dim // 2,):
             raise ValueError(f"freq: [{rotary_dim // 2}] is needed, not {list(freq.shape)}")
+        if not bool((freq.abs() < 2.0 ** 54).all()):
+            raise ValueError("freq: numbers below 2^54 in magnitude are needed")
         self.rotary_dim, self.interleaved = rotary_dim, bool(interleaved)
         self.freq = freq.to(device=device, dtype=torch.float64).contiguous()
         self.scale = scale if scale is not None else 0.1 * math.log(stretch) + 1
