@@ -508,10 +508,12 @@ int kv_chunk_attn(const kv_shape *shape, const kv_chunk *chunk, const void *q,
  *              NaN) is multiplied by scale alone, and KV_ERR_BOUNDS is recorded
  *   positions  [total_q] int32, device memory, or NULL: row i of sequence b's chunk is
  *              at position context_lens[b] + i
- * The angle is kept as a fraction of a turn in 64 bits, so that far positions (int32, of
- * either sign: -t turns back what t turned) lose nothing; sines, cosines and the turning
- * itself are fp32, and a result is rounded once, to dtype.  rotary_dim is a multiple of
- * 8 in 8 .. 128 (else KV_ERR_UNSUPPORTED). */
+ * The angle is kept as a fraction of a turn, off by at most |t| (2^-64 + |freq| 2^-66) +
+ * 2^-33 turns: by less than 2^-29 radians, finer than an fp32 sine, at every int32 position
+ * (of either sign: -t turns back what t turned) while |t freq| <= 2^32 radians.  Sines,
+ * cosines, their products with scale and the turning itself are fp32, and a result is
+ * rounded once, to dtype.  rotary_dim is a multiple of 8 in 8 .. 128 (else
+ * KV_ERR_UNSUPPORTED). */
 typedef struct {
   const double *freq;
   const int32_t *positions;

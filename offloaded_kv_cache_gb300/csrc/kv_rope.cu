@@ -4,8 +4,9 @@
 // A pair (a, b) at position t becomes (a cos - b sin, a sin + b cos), angle t * freq.  In
 // fp32 t * freq loses the angle's fraction of a turn at far positions (2^20 * 1 is known
 // to 2^-4 radians), and fp64 runs at a few percent of fp32's rate here.  So freq / 2 pi is
-// taken as a fraction of a turn in units of 2^-64, and the product with t modulo 2^64 is
-// the angle's fraction, exact but for t times the last bit of freq.
+// taken as a fraction of a turn in units of 2^-64, rounded down, and its product with t modulo
+// 2^64 is the angle's fraction.  It is off by t times what freq / 2 pi is: 2^-64 for the unit,
+// freq * 2^-66 for 1 / 2 pi's last bit; and 2^-33 for the 32 bits that sine and cosine take.
 //
 // Each byte is read and written once, and a pair's sine and cosine serve all heads of a
 // kv head's group: memory bounds it, for a few tokens the launch and two round trips.
