@@ -612,7 +612,9 @@ int kv_q8_read(const kv_shape *shape, const kv_q8_cache *cache, const int32_t *b
  * may enter the products as two f16 terms each (22 bits); a row of q is scaled by
  * a power of two for it, 2^100 at most, so its own size does not matter (rows below
  * 2^-86 lose bits, of scores below 2^-62 * scale).  16-bit q: the weights enter the
- * value product in 16 bits, f16 or dtype. */
+ * value product in 16 bits, f16 or dtype.  kv_q8_chunk_workspace_bytes: 16-bit q over a cache
+ * in host memory, or of more than 768 rows of a kv head, needs room for min(N, B * maxP)
+ * pages in dtype, twice their bytes in 8 bits. */
 size_t kv_q8_chunk_workspace_bytes(const kv_shape *shape, const kv_chunk *chunk);
 int kv_q8_chunk_attn(const kv_shape *shape, const kv_chunk *chunk, const void *q,
                      const kv_q8_cache *cache, const int32_t *block_table,
@@ -647,8 +649,21 @@ typedef struct {
 } kv_q4_cache;
 
 /* kv_q8_append, kv_q8_read and kv_q8_chunk_attn for the 4-bit cache: the same arguments,
- * checks and errors.  KV_F32 queries and weights enter the products as two f16 terms
- * each, as there. */
+ * checks and errors.  What the attention's products take, its scores, softmax and sums being
+ * fp32 and the softmax's sum of weights that are not rounded:
+ *  - few rows (16-bit q: max_q_len * Hq / Hkv up to 24; KV_F32: any number).  q in f16 after
+ *    a power of two per row: f16 as it is, bf16 exactly down to 2^-31 of the row's largest
+ *    element (nothing below 2^-39), KV_F32 as two terms (22 bits, to 2^-39 of the largest).
+ *    A weight times its V's power 2^e, relative to the row's largest such product, in f16
+ *    (KV_F32: as two terms): 11 bits down to 2^-21 of the largest, nothing below 2^-32 of
+ *    it, not even to a channel that is 0 in every larger vector.
+ *  - more rows: as kv_chunk_attn over the values in dtype, the weights in dtype too.
+ * kv_q4_chunk_workspace_bytes: few rows, and up to 640 rows of 16-bit q, over a cache in
+ * device memory need room for partial results only.  For more rows, and for a cache in host
+ * memory whatever the rows, the pages that the rows see pass through the workspace in
+ * dtype, which has room for min(N, B * maxP) pages whatever the lengths and the window: 3.5
+ * times their bytes in 4 bits (KV_F32: 7 times).  Where that does not fit, calls of fewer
+ * sequences take less. */
 int kv_q4_append(const kv_shape *shape, const kv_chunk *chunk, const void *k_new,
                  const void *v_new, const kv_q4_cache *cache, const int32_t *block_table,
                  const int32_t *context_lens, int32_t *context_lens_out, void *stream);

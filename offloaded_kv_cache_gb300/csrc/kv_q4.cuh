@@ -86,6 +86,9 @@ __device__ __forceinline__ uint32_t q4_codes8(const float (&x)[8], float top, fl
 }
 // The factor of a vector's power byte; 255 is NaN.
 __device__ __forceinline__ float q4_power(uint32_t byte) { return q8_scale(byte); }
+// (Integers put into the mantissa of a float of known exponent: a published method, for 4 bits
+// and f16 in Kim, Henry, Fahim and Hassan Awadalla, "Who Says Elephants Can't Run: Bringing
+// Large Scale MoE Models into Cloud Scale Production", 2022.)
 // n = c + 8 (below 16) times f = s 2^e: n is put into the mantissa of 2^23 + n (f16: 1024 + n,
 // bf16: 128 + n, two at a time); what is taken off again leaves c, and c f is exact in every
 // type.
