@@ -402,6 +402,9 @@ int kv_window_reset(const kv_shape *shape, const kv_window *win, void *stream);
  * fetched again, so that a page copied while it was partly filled would keep the
  * slots behind that fill as they are once later pages follow it.  (The last page
  * is fetched at every step anyway: nothing else crosses the link for it.)
+ * Tokens below the lengths are taken not to change while their page is in the
+ * window: kv_window_reset where they do (a row given to another sequence, a cache
+ * read back from 8 or 4 bits).
  * 0 <= context_lens[b] <= maxP * ps; a row out of that range keeps its pages and
  * sets KV_ERR_BOUNDS in the device status word. */
 int kv_window_trim(const kv_shape *shape, const kv_window *win, const int32_t *context_lens,
